@@ -366,6 +366,134 @@ fp8q_status_t fp8q_pack_plan(const fp8q_pack_item_t* items, int count, uint64_t 
                              uint64_t* batch_bytes, int* num_batches);
 fp8q_status_t fp8q_copy_segments(const fp8q_copy_t* segs, int count, fp8q_stream_t stream);
 
+/* ------------------------------------------------ expert-block operators ----
+ * What stands next to MXFP8 expert weights in a mixture-of-experts block: the
+ * norm in front of it with an 8-bit output, the way of the tokens to their
+ * experts and back, and the experts' products themselves.  The first two have
+ * their gradients; the products read weights that a refit has sent to an
+ * inference engine and have none.
+ *
+ * Arrays are row-major and dense; all arithmetic is binary32 and is rounded
+ * once, where an output is stored, unless said otherwise.  No result depends
+ * on timing: no sum is formed by atomics.  NaN and infinities are not looked
+ * for: a row that holds one gives what the formula gives (a NaN code where
+ * the value is NaN, the largest code where it is infinite). */
+
+/* Residual addition, root-mean-square norm and quantization of `rows` rows:
+ *     h = x + residual;  rstd = 1 / sqrt(mean(h^2) + eps);  y = (h * rstd) * weight
+ * with the norm taken of the unrounded h, and y quantized from binary32: by
+ * the rules of (a) with a scale per 128 columns (fp8q_), or by those of (d)
+ * (mxfp8_).
+ *   residual_bf16 : rows * k bf16, or NULL for h = x
+ *   weight_bf16   : k bf16
+ *   sum_bf16      : RNE_bf16(h), or NULL; needs a residual (FP8Q_ERR_NULL), and
+ *                   may be the same pointer as x_bf16 or as residual_bf16
+ *   y_bf16        : RNE_bf16(y), or NULL
+ *   codes         : rows * k bytes
+ *   scales        : fp8q_: rows * k / 128 floats; mxfp8_: E8M0 bytes, row-major
+ *                   [rows, k / 32] (swizzled == 0, what the products below
+ *                   read) or the layout of (d) for one [rows, k] matrix
+ *                   (swizzled == 1, what a block-scaled GEMM reads)
+ *   rstd          : rows floats, or NULL (the gradient needs them)
+ * k: a positive multiple of 128 (fp8q_) or 32 (mxfp8_), at most 16384
+ * (FP8Q_ERR_K).  eps: finite, not negative (FP8Q_ERR_SIZE).  rows == 0 is a
+ * no-op. */
+fp8q_status_t fp8q_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* weight_bf16,
+                                    int64_t rows, int64_t k, float eps, fp8q_format_t fmt, void* sum_bf16,
+                                    void* y_bf16, uint8_t* codes, float* scales, float* rstd, fp8q_stream_t stream);
+fp8q_status_t mxfp8_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* weight_bf16,
+                                     int64_t rows, int64_t k, float eps, int swizzled, void* sum_bf16, void* y_bf16,
+                                     uint8_t* codes, uint8_t* scales, float* rstd, fp8q_stream_t stream);
+
+/* Gradient of the norm, the rounding to 8 bits taken as the identity:
+ *     xhat = h * rstd;  g = dy * weight
+ *     dx = rstd * (g - xhat * mean(g * xhat)) + dsum;   dweight = sum over rows of dy * xhat
+ * dx is the gradient of x and of the residual alike.
+ *   h_bf16  : the rows the norm was taken of (sum_bf16, or x without residual)
+ *   rstd    : as the forward pass wrote them
+ *   dsum_bf16 : gradient that reaches sum_bf16 from elsewhere, or NULL
+ *   dx_bf16 : rows * k bf16; may be the same pointer as dy_bf16 or dsum_bf16
+ *   dweight : k floats (all zero when rows == 0)
+ *   workspace : fp8q_rmsnorm_backward_workspace_bytes(rows, k) bytes, caller-owned
+ * k: a positive multiple of 32, at most 16384. */
+size_t fp8q_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t k);
+fp8q_status_t fp8q_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* weight_bf16,
+                                    const float* rstd, const void* dsum_bf16, int64_t rows, int64_t k, void* dx_bf16,
+                                    float* dweight, void* workspace, size_t workspace_bytes, fp8q_stream_t stream);
+
+/* Tokens sorted by expert.  Token t's choice j, number i = t * topk + j, goes
+ * to expert ids[i]; an id outside [0, experts) is a choice that no expert
+ * takes (dropped, or another rank's).  A stable sort by expert, dropped
+ * choices last, gives
+ *     offsets[e] : choices of experts before e; offsets[experts] = choices of all
+ *     slots[i]   : choice i's place in the sorted order
+ *     order[s]   : the choice at place s
+ *   ids : tokens * topk integers of id_bytes 4 or 8 (FP8Q_ERR_FORMAT)
+ *   offsets: experts + 1, order and slots: tokens * topk 32-bit integers
+ *   workspace : fp8q_moe_sort_workspace_bytes(tokens, topk, experts) bytes,
+ *               caller-owned (0 bytes for few choices: may be NULL then)
+ * experts: 1 .. FP8Q_MOE_MAX_EXPERTS, tokens * topk < 2^31 (FP8Q_ERR_SIZE);
+ * topk: 1 .. FP8Q_MOE_MAX_TOPK (FP8Q_ERR_K).  tokens == 0 zeroes offsets. */
+#define FP8Q_MOE_MAX_EXPERTS 1024
+#define FP8Q_MOE_MAX_TOPK 32
+size_t fp8q_moe_sort_workspace_bytes(int64_t tokens, int topk, int experts);
+fp8q_status_t fp8q_moe_sort(const void* ids, int id_bytes, int64_t tokens, int topk, int experts, int32_t* offsets,
+                            int32_t* order, int32_t* slots, void* workspace, size_t workspace_bytes,
+                            fp8q_stream_t stream);
+
+/* The tokens' rows carried to their experts: rows[slots[t, j]] = x[t], and
+ * zero rows at the places of dropped choices.  bf16 rows, or MXFP8 rows with
+ * their row-major scales.  The gradient of fp8q_moe_gather is
+ * fp8q_moe_combine without weights.
+ *   slots, offsets : as fp8q_moe_sort wrote them; a slot outside
+ *                    [0, tokens * topk) is skipped
+ *   k : a positive multiple of 8 (bf16) or 32 (MXFP8) (FP8Q_ERR_K)
+ * tokens == 0 is a no-op. */
+fp8q_status_t fp8q_moe_gather(const void* x_bf16, const int32_t* slots, const int32_t* offsets, int64_t tokens,
+                              int topk, int experts, int64_t k, void* rows_bf16, fp8q_stream_t stream);
+fp8q_status_t mxfp8_moe_gather(const uint8_t* codes, const uint8_t* scales, const int32_t* slots,
+                               const int32_t* offsets, int64_t tokens, int topk, int experts, int64_t k,
+                               uint8_t* row_codes, uint8_t* row_scales, fp8q_stream_t stream);
+
+/* The experts' rows summed back, over a token's choices in their order:
+ *     out[t] = sum over j of weights[t, j] * y[slots[t, j]]
+ * Dropped choices are left out, whatever their rows hold; a token without
+ * any gives zeros.
+ *   y_bf16  : tokens * topk rows of k bf16;  out_bf16 : tokens rows
+ *   weights : tokens * topk floats, or NULL for all 1
+ *   k       : a positive multiple of 8 (FP8Q_ERR_K)
+ * Its gradient:
+ *     dy[slots[t, j]] = weights[t, j] * dout[t];   dweights[t, j] = sum of dout[t] * y[slots[t, j]]
+ * both zero for dropped choices. */
+fp8q_status_t fp8q_moe_combine(const void* y_bf16, const int32_t* slots, const int32_t* offsets, const float* weights,
+                               int64_t tokens, int topk, int experts, int64_t k, void* out_bf16, fp8q_stream_t stream);
+fp8q_status_t fp8q_moe_combine_backward(const void* dout_bf16, const void* y_bf16, const int32_t* slots,
+                                        const int32_t* offsets, const float* weights, int64_t tokens, int topk,
+                                        int experts, int64_t k, void* dy_bf16, float* dweights, fp8q_stream_t stream);
+
+/* The experts' products.  Row r belongs to the expert e with offsets[e] <= r <
+ * offsets[e + 1]; rows from offsets[experts] on belong to none.  Values are
+ * decode_e4m3(code) * 2^(scale - 127), sums binary32 (tensor core):
+ *     matmul: out[r, f] = RNE_bf16(sum over c of W[e, f, c] * a[r, c])
+ *     swiglu: g, u the sums with the gate and the up weights,
+ *             h = g / (1 + exp(-g)) * u, quantized from binary32 by the rules
+ *             of (d), scales row-major [rows, n / 32]
+ * Rows of no expert give zeros (codes and scales 0).
+ *   codes, scales : rows * k codes and row-major [rows, k / 32] E8M0 bytes
+ *   *_codes, *_scales (weights) : [experts, n, k] as mxfp8_quantize_swizzled
+ *                   writes them for batch = experts, m = n
+ *   offsets       : experts + 1 integers on the device, not decreasing; values
+ *                   outside [0, rows] count as the nearer end
+ * k: a positive multiple of 32; swiglu: n too (FP8Q_ERR_K).  experts: 1 ..
+ * FP8Q_MOE_MAX_EXPERTS.  rows == 0 or n == 0 is a no-op. */
+fp8q_status_t mxfp8_moe_matmul(const uint8_t* codes, const uint8_t* scales, int64_t rows, const uint8_t* w_codes,
+                               const uint8_t* w_scales, const int32_t* offsets, int experts, int64_t n, int64_t k,
+                               void* out_bf16, fp8q_stream_t stream);
+fp8q_status_t mxfp8_moe_swiglu(const uint8_t* codes, const uint8_t* scales, int64_t rows, const uint8_t* gate_codes,
+                               const uint8_t* gate_scales, const uint8_t* up_codes, const uint8_t* up_scales,
+                               const int32_t* offsets, int experts, int64_t n, int64_t k, uint8_t* out_codes,
+                               uint8_t* out_scales, fp8q_stream_t stream);
+
 /* ------------------------------------------------------------- helpers ---- */
 
 /* ceil(n / 128): the number of fp32 scales of an n-element blockwise array. */
@@ -394,9 +522,11 @@ int fp8q_set_launch_overlap(int enable);
 /* Diagnostic, and the one call that synchronizes: waits for the current
  * device, then returns in *flags the error bits the kernels raised since the
  * last clear (0 = none; bit 0 = an input copy into shared memory did not land
- * within 2 s, after which the kernel stopped and its outputs are invalid).
+ * within 2 s, bit 1 = a step of the expert products did not finish within 2 s,
+ * after which the kernel stopped and its outputs are invalid).
  * Clears the bits when `clear` is non-zero. */
 #define FP8Q_DEVICE_ERR_COPY_TIMEOUT 1u
+#define FP8Q_DEVICE_ERR_PRODUCT_TIMEOUT 2u
 fp8q_status_t fp8q_device_errors(unsigned int* flags, int clear);
 
 /* Self-test of the bounded copy wait (a test hook, not a step of the codec).

@@ -29,7 +29,7 @@ FP8Q_BLOCK = 128
 MXFP8_BLOCK = 32
 
 STATUS = {0: "FP8Q_OK", 1: "FP8Q_ERR_NULL", 2: "FP8Q_ERR_SIZE", 3: "FP8Q_ERR_ALIGN", 4: "FP8Q_ERR_FORMAT",
-          5: "FP8Q_ERR_K", 6: "FP8Q_ERR_CUDA", 7: "FP8Q_ERR_ALIAS"}
+          5: "FP8Q_ERR_K", 6: "FP8Q_ERR_CUDA", 7: "FP8Q_ERR_ALIAS", 8: "FP8Q_ERR_FLAGS"}
 
 
 class Fp8qError(RuntimeError):
@@ -44,6 +44,7 @@ _vp = ctypes.c_void_p
 _sz = ctypes.c_size_t
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
+_f32 = ctypes.c_float
 
 
 class fp8q_hop_t(ctypes.Structure):
@@ -67,6 +68,9 @@ FP8Q_HOP_LOCAL_READY = 1
 FP8Q_INPUTS_READY = 1
 FP8Q_ALLREDUCE_MEAN = 1
 FP8Q_DEVICE_ERR_COPY_TIMEOUT = 1
+FP8Q_DEVICE_ERR_PRODUCT_TIMEOUT = 2
+FP8Q_MOE_MAX_EXPERTS = 1024
+FP8Q_MOE_MAX_TOPK = 32
 
 
 class mxfp8_tensor_t(ctypes.Structure):
@@ -119,6 +123,18 @@ _SIGNATURES = {
                                  ctypes.POINTER(ctypes.c_uint64), _vp], _int),
     "fp8q_ring_allreduce_sim_ex": ([ctypes.POINTER(_vp), ctypes.POINTER(_vp), _int, _sz, _int, _vp, _sz,
                                     ctypes.POINTER(ctypes.c_uint64), ctypes.c_uint, _vp], _int),
+    "fp8q_rmsnorm_quantize": ([_vp, _vp, _vp, _i64, _i64, _f32, _int, _vp, _vp, _vp, _vp, _vp, _vp], _int),
+    "mxfp8_rmsnorm_quantize": ([_vp, _vp, _vp, _i64, _i64, _f32, _int, _vp, _vp, _vp, _vp, _vp, _vp], _int),
+    "fp8q_rmsnorm_backward_workspace_bytes": ([_i64, _i64], _sz),
+    "fp8q_rmsnorm_backward": ([_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp], _int),
+    "fp8q_moe_sort_workspace_bytes": ([_i64, _int, _int], _sz),
+    "fp8q_moe_sort": ([_vp, _int, _i64, _int, _int, _vp, _vp, _vp, _vp, _sz, _vp], _int),
+    "fp8q_moe_gather": ([_vp, _vp, _vp, _i64, _int, _int, _i64, _vp, _vp], _int),
+    "mxfp8_moe_gather": ([_vp, _vp, _vp, _vp, _i64, _int, _int, _i64, _vp, _vp, _vp], _int),
+    "fp8q_moe_combine": ([_vp, _vp, _vp, _vp, _i64, _int, _int, _i64, _vp, _vp], _int),
+    "fp8q_moe_combine_backward": ([_vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _i64, _vp, _vp, _vp], _int),
+    "mxfp8_moe_matmul": ([_vp, _vp, _i64, _vp, _vp, _vp, _int, _i64, _i64, _vp, _vp], _int),
+    "mxfp8_moe_swiglu": ([_vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _int, _i64, _i64, _vp, _vp, _vp], _int),
     "fp8q_num_scales": ([_sz], _sz),
     "mxfp8_swizzled_scale_bytes": ([_i64, _i64, _i64], _sz),
     "fp8q_status_string": ([_int], ctypes.c_char_p),
@@ -649,3 +665,260 @@ def fp8q_dequant_reduce_unfused_static(codes: Sequence[torch.Tensor], scales: Se
                                                   _dev(out_fp32, "out_fp32", torch.float32, n), _stream(stream))
     _check("fp8q_dequant_reduce_unfused_static", st)
     return out_bf16, out_fp32
+
+
+# ------------------------------------------------- expert-block operators ----
+def _rows_of(t: torch.Tensor, what: str, k: Optional[int] = None):
+    """(rows, k) of a 2D [rows, k] tensor."""
+    if t.dim() != 2 or (k is not None and t.shape[1] != k):
+        raise ValueError(f"{what} must be [rows, {'k' if k is None else k}], got {list(t.shape)}")
+    return t.shape
+
+
+def _shaped(t: torch.Tensor, what: str, shape) -> torch.Tensor:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _rmsnorm(name: str, scale_dtype, scale_shape, scale_numel, code_or_flag, x, weight, eps, residual, want_bf16, want_rstd, codes,
+             scales, out_sum, out_bf16, rstd, stream):
+    rows, k = x.shape
+    dev = x.device
+    _shaped(weight, "weight", (k,))
+    if residual is not None:
+        _shaped(residual, "residual", (rows, k))
+        if out_sum is None:
+            out_sum = torch.empty((rows, k), dtype=torch.bfloat16, device=dev)
+    if codes is None:
+        codes = torch.empty((rows, k), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty(scale_shape, dtype=scale_dtype, device=dev)
+    if out_bf16 is None and want_bf16:
+        out_bf16 = torch.empty((rows, k), dtype=torch.bfloat16, device=dev)
+    if rstd is None and want_rstd:
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    n = rows * k
+    st = getattr(lib(), name)(_dev(x, "x", torch.bfloat16), _dev(residual, "residual", torch.bfloat16),
+                              _dev(weight, "weight", torch.bfloat16), rows, k, eps, code_or_flag,
+                              _dev(out_sum, "out_sum", torch.bfloat16, n), _dev(out_bf16, "out_bf16", torch.bfloat16, n),
+                              _dev(codes, "codes", torch.uint8, n), _dev(scales, "scales", scale_dtype, scale_numel),
+                              _dev(rstd, "rstd", torch.float32, rows), _stream(stream))
+    _check(name, st)
+    return codes, scales, out_sum, out_bf16, rstd
+
+
+def fp8q_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, fmt="e4m3",
+                          residual: Optional[torch.Tensor] = None, want_bf16: bool = False, want_rstd: bool = False,
+                          codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                          out_sum: Optional[torch.Tensor] = None, out_bf16: Optional[torch.Tensor] = None,
+                          rstd: Optional[torch.Tensor] = None, stream=None):
+    """Norm of x + residual (bf16 [rows, k]) with a blockwise FP8 output ->
+    (codes uint8 [rows, k], scales float32 [rows, k/128], sum bf16 or None,
+    y bf16 or None, rstd float32 [rows] or None).  The sum is written when a
+    residual is given; out_sum may be `x` or `residual` (in place)."""
+    rows, k = _rows_of(x, "x")
+    cols = k // FP8Q_BLOCK
+    return _rmsnorm("fp8q_rmsnorm_quantize", torch.float32, (rows, cols), rows * cols, _fmt(fmt), x, weight, eps,
+                    residual, want_bf16, want_rstd, codes, scales, out_sum, out_bf16, rstd, stream)
+
+
+def mxfp8_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                           residual: Optional[torch.Tensor] = None, swizzled: bool = False, want_bf16: bool = False,
+                           want_rstd: bool = False, codes: Optional[torch.Tensor] = None,
+                           scales: Optional[torch.Tensor] = None, out_sum: Optional[torch.Tensor] = None,
+                           out_bf16: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None, stream=None):
+    """As fp8q_rmsnorm_quantize with an MXFP8 output: scales are E8M0 bytes,
+    row-major [rows, k/32], or flat in the 128x4-tiled layout (swizzled)."""
+    rows, k = _rows_of(x, "x")
+    sb = mxfp8_swizzled_scale_bytes(1, rows, k) if swizzled else rows * (k // MXFP8_BLOCK)
+    return _rmsnorm("mxfp8_rmsnorm_quantize", torch.uint8, (sb,) if swizzled else (rows, k // MXFP8_BLOCK), sb,
+                    int(bool(swizzled)), x, weight, eps, residual, want_bf16, want_rstd, codes, scales, out_sum,
+                    out_bf16, rstd, stream)
+
+
+def fp8q_rmsnorm_backward_workspace_bytes(rows: int, k: int) -> int:
+    return int(lib().fp8q_rmsnorm_backward_workspace_bytes(rows, k))
+
+
+def fp8q_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                          dsum: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                          dweight: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of the norm -> (dx bf16 [rows, k], dweight float32 [k]).  dx
+    may be `dy` or `dsum` (in place)."""
+    rows, k = _rows_of(h, "h")
+    _shaped(dy, "dy", (rows, k))
+    _shaped(weight, "weight", (k,))
+    if dsum is not None:
+        _shaped(dsum, "dsum", (rows, k))
+    if dx is None:
+        dx = torch.empty((rows, k), dtype=torch.bfloat16, device=h.device)
+    if dweight is None:
+        dweight = torch.empty(k, dtype=torch.float32, device=h.device)
+    need = fp8q_rmsnorm_backward_workspace_bytes(rows, k)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=h.device)
+    st = lib().fp8q_rmsnorm_backward(_dev(dy, "dy", torch.bfloat16), _dev(h, "h", torch.bfloat16),
+                                     _dev(weight, "weight", torch.bfloat16), _dev(rstd, "rstd", torch.float32, rows),
+                                     _dev(dsum, "dsum", torch.bfloat16), rows, k,
+                                     _dev(dx, "dx", torch.bfloat16, rows * k), _dev(dweight, "dweight", torch.float32, k),
+                                     _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                                     _stream(stream))
+    _check("fp8q_rmsnorm_backward", st)
+    return dx, dweight
+
+
+def fp8q_moe_sort_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
+    return int(lib().fp8q_moe_sort_workspace_bytes(tokens, topk, experts))
+
+
+def fp8q_moe_sort(ids: torch.Tensor, experts: int, offsets: Optional[torch.Tensor] = None,
+                  order: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None):
+    """ids int32 or int64 [tokens, topk] (an id outside [0, experts) is dropped)
+    -> (offsets int32 [experts + 1], order int32 [tokens * topk], slots int32
+    [tokens, topk])."""
+    tokens, topk = _rows_of(ids, "ids")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
+    n, dev = tokens * topk, ids.device
+    if offsets is None:
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
+    if order is None:
+        order = torch.empty(n, dtype=torch.int32, device=dev)
+    if slots is None:
+        slots = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
+    if workspace is None:
+        need = fp8q_moe_sort_workspace_bytes(tokens, topk, experts)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    st = lib().fp8q_moe_sort(_dev(ids, "ids"), ids.element_size(), tokens, topk, experts,
+                             _dev(offsets, "offsets", torch.int32, experts + 1), _dev(order, "order", torch.int32, n),
+                             _dev(slots, "slots", torch.int32, n), _dev(workspace, "workspace"),
+                             0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("fp8q_moe_sort", st)
+    return offsets, order, slots
+
+
+def _routes(slots: torch.Tensor, offsets: torch.Tensor):
+    """(tokens, topk, experts, slots pointer, offsets pointer) of a sort's results."""
+    tokens, topk = _rows_of(slots, "slots")
+    return tokens, topk, offsets.numel() - 1, _dev(slots, "slots", torch.int32), _dev(offsets, "offsets", torch.int32)
+
+
+def fp8q_moe_gather(x: torch.Tensor, slots: torch.Tensor, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                    stream=None):
+    """bf16 x [tokens, k] -> the experts' rows bf16 [tokens * topk, k]."""
+    tokens, topk, experts, sp, op = _routes(slots, offsets)
+    _, k = _shaped(x, "x", (tokens, x.shape[-1])).shape
+    if rows is None:
+        rows = torch.empty((tokens * topk, k), dtype=torch.bfloat16, device=x.device)
+    st = lib().fp8q_moe_gather(_dev(x, "x", torch.bfloat16), sp, op, tokens, topk, experts, k,
+                               _dev(rows, "rows", torch.bfloat16, tokens * topk * k), _stream(stream))
+    _check("fp8q_moe_gather", st)
+    return rows
+
+
+def mxfp8_moe_gather(codes: torch.Tensor, scales: torch.Tensor, slots: torch.Tensor, offsets: torch.Tensor,
+                     row_codes: Optional[torch.Tensor] = None, row_scales: Optional[torch.Tensor] = None, stream=None):
+    """MXFP8 rows (codes uint8 [tokens, k], scales uint8 [tokens, k/32]) -> the
+    experts' rows (codes [tokens * topk, k], scales [tokens * topk, k/32])."""
+    tokens, topk, experts, sp, op = _routes(slots, offsets)
+    _, k = _shaped(codes, "codes", (tokens, codes.shape[-1])).shape
+    cols = k // MXFP8_BLOCK
+    n = tokens * topk
+    if row_codes is None:
+        row_codes = torch.empty((n, k), dtype=torch.uint8, device=codes.device)
+    if row_scales is None:
+        row_scales = torch.empty((n, cols), dtype=torch.uint8, device=codes.device)
+    st = lib().mxfp8_moe_gather(_dev(codes, "codes", torch.uint8), _dev(scales, "scales", torch.uint8, tokens * cols), sp, op,
+                                tokens, topk, experts, k, _dev(row_codes, "row_codes", torch.uint8, n * k),
+                                _dev(row_scales, "row_scales", torch.uint8, n * cols), _stream(stream))
+    _check("mxfp8_moe_gather", st)
+    return row_codes, row_scales
+
+
+def fp8q_moe_combine(y: torch.Tensor, slots: torch.Tensor, offsets: torch.Tensor,
+                     weights: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None):
+    """The experts' rows bf16 [tokens * topk, k] summed back (with float32
+    weights [tokens, topk], or all 1) -> bf16 [tokens, k].  Without weights it
+    is also the gradient of fp8q_moe_gather."""
+    tokens, topk, experts, sp, op = _routes(slots, offsets)
+    _, k = _shaped(y, "y", (tokens * topk, y.shape[-1])).shape
+    if weights is not None:
+        _shaped(weights, "weights", (tokens, topk))
+    if out is None:
+        out = torch.empty((tokens, k), dtype=torch.bfloat16, device=y.device)
+    st = lib().fp8q_moe_combine(_dev(y, "y", torch.bfloat16), sp, op, _dev(weights, "weights", torch.float32), tokens, topk,
+                                experts, k, _dev(out, "out", torch.bfloat16, tokens * k), _stream(stream))
+    _check("fp8q_moe_combine", st)
+    return out
+
+
+def fp8q_moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, slots: torch.Tensor, offsets: torch.Tensor,
+                              weights: torch.Tensor, dy: Optional[torch.Tensor] = None,
+                              dweights: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of fp8q_moe_combine -> (dy bf16 [tokens * topk, k], dweights float32 [tokens, topk])."""
+    tokens, topk, experts, sp, op = _routes(slots, offsets)
+    _, k = _shaped(dout, "dout", (tokens, dout.shape[-1])).shape
+    n = tokens * topk
+    _shaped(y, "y", (n, k))
+    _shaped(weights, "weights", (tokens, topk))
+    if dy is None:
+        dy = torch.empty((n, k), dtype=torch.bfloat16, device=y.device)
+    if dweights is None:
+        dweights = torch.empty((tokens, topk), dtype=torch.float32, device=y.device)
+    st = lib().fp8q_moe_combine_backward(_dev(dout, "dout", torch.bfloat16), _dev(y, "y", torch.bfloat16), sp, op,
+                                         _dev(weights, "weights", torch.float32), tokens, topk, experts, k,
+                                         _dev(dy, "dy", torch.bfloat16, n * k),
+                                         _dev(dweights, "dweights", torch.float32, n), _stream(stream))
+    _check("fp8q_moe_combine_backward", st)
+    return dy, dweights
+
+
+def _expert_weights(codes: torch.Tensor, scales: torch.Tensor, what: str, experts: int, k: int):
+    """n of weights [experts, n, k] (codes) with their swizzled scales, and both pointers."""
+    if codes.dim() != 3 or codes.shape[0] != experts or codes.shape[2] != k:
+        raise ValueError(f"{what} must be [{experts}, n, {k}], got {list(codes.shape)}")
+    n = codes.shape[1]
+    return n, _dev(codes, what, torch.uint8), _dev(scales, f"{what} scales", torch.uint8, mxfp8_swizzled_scale_bytes(experts, n, k))
+
+
+def mxfp8_moe_matmul(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                     offsets: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None):
+    """MXFP8 rows sorted by expert (codes [rows, k], scales [rows, k/32]) times
+    their experts' weights (w_codes [experts, n, k] and their swizzled scales,
+    as mxfp8_quantize_swizzled gives them) -> bf16 [rows, n]."""
+    rows, k = _rows_of(codes, "codes")
+    experts = offsets.numel() - 1
+    n, wp, wsp = _expert_weights(w_codes, w_scales, "w_codes", experts, k)
+    if out is None:
+        out = torch.empty((rows, n), dtype=torch.bfloat16, device=codes.device)
+    st = lib().mxfp8_moe_matmul(_dev(codes, "codes", torch.uint8), _dev(scales, "scales", torch.uint8, rows * (k // MXFP8_BLOCK)),
+                                rows, wp, wsp, _dev(offsets, "offsets", torch.int32), experts, n, k,
+                                _dev(out, "out", torch.bfloat16, rows * n), _stream(stream))
+    _check("mxfp8_moe_matmul", st)
+    return out
+
+
+def mxfp8_moe_swiglu(codes: torch.Tensor, scales: torch.Tensor, gate_codes: torch.Tensor, gate_scales: torch.Tensor,
+                     up_codes: torch.Tensor, up_scales: torch.Tensor, offsets: torch.Tensor,
+                     out_codes: Optional[torch.Tensor] = None, out_scales: Optional[torch.Tensor] = None, stream=None):
+    """silu(rows x gate) * (rows x up), quantized to MXFP8 rows -> (codes uint8
+    [rows, n], scales uint8 [rows, n/32]), the input of the down product."""
+    rows, k = _rows_of(codes, "codes")
+    experts = offsets.numel() - 1
+    n, gp, gsp = _expert_weights(gate_codes, gate_scales, "gate_codes", experts, k)
+    nu, up, usp = _expert_weights(up_codes, up_scales, "up_codes", experts, k)
+    if nu != n:
+        raise ValueError(f"gate has {n} rows and up {nu}")
+    cols = n // MXFP8_BLOCK
+    if out_codes is None:
+        out_codes = torch.empty((rows, n), dtype=torch.uint8, device=codes.device)
+    if out_scales is None:
+        out_scales = torch.empty((rows, cols), dtype=torch.uint8, device=codes.device)
+    st = lib().mxfp8_moe_swiglu(_dev(codes, "codes", torch.uint8), _dev(scales, "scales", torch.uint8, rows * (k // MXFP8_BLOCK)),
+                                rows, gp, gsp, up, usp, _dev(offsets, "offsets", torch.int32), experts, n, k,
+                                _dev(out_codes, "out_codes", torch.uint8, rows * n),
+                                _dev(out_scales, "out_scales", torch.uint8, rows * cols), _stream(stream))
+    _check("mxfp8_moe_swiglu", st)
+    return out_codes, out_scales

@@ -44,6 +44,23 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// A byte range of an argument.
+struct Range {
+    const void* p;
+    size_t bytes;
+};
+
+// An output overlaps an input or another output.
+inline bool any_alias(const Range* outs, int nout, const Range* ins, int nin) {
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j)
+            if (overlaps(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return true;
+        for (int j = i + 1; j < nout; ++j)
+            if (overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return true;
+    }
+    return false;
+}
+
 inline bool valid_fmt(fp8q_format_t f) { return f == FP8Q_E4M3 || f == FP8Q_E5M2; }
 
 // Records and maps a CUDA error (thread-local, see fp8q_last_cuda_error).
@@ -60,6 +77,11 @@ unsigned unit_errors_ring_hop(bool clear);
 unsigned unit_errors_mxfp8(bool clear);
 unsigned unit_errors_selftest(bool clear);
 unsigned unit_errors_tensorwise(bool clear);
+unsigned unit_errors_moe_product(bool clear);
+
+// The driver's cuTensorMapEncodeTiled (PFN_cuTensorMapEncodeTiled_v12000), or
+// NULL where the driver has none.
+void* tensor_map_encode_fn();
 
 // Devices whose per-device state is cached; others are set up on every call.
 constexpr int kMaxDevices = 64;

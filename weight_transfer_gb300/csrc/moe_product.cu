@@ -1,0 +1,466 @@
+// The experts' products with MXFP8 weights, on the tensor cores.
+//
+// Rows of activations are sorted by expert (expert e owns rows offsets[e] ..
+// offsets[e + 1]); expert e's weights are a row-major [n, k] matrix, codes and
+// swizzled scales as mxfp8_quantize_swizzled writes them for a batch of
+// experts.  With a = sum over blocks of 32 of 2^(s - 127) * code on both sides
+//     matmul   out[r, f]  = sum over k of W[e(r), f, k] * a[r, k]
+//     swiglu   g, u the same products with two weight tensors,
+//              h[r, f] = g / (1 + exp(-g)) * u, quantized to MXFP8 rows
+// Products of 8-bit codes and their scales are exact, sums are binary32 in the
+// tensor core's accumulators.
+//
+// The weights are the M side of the product (128 features a tile) and the
+// rows its N side (16 .. 224 a tile, as many as the expert has): an expert
+// with one row costs a 16-wide product, not a 128-wide one, and each feature
+// is a TMEM lane, so that a block of 32 features is one warp and its largest
+// magnitude one warp reduction.
+//
+// One CTA per SM walks over the tiles.  Warp 0 copies weights, rows and
+// weight scales by TMA, warp 2 brings the rows' scales into the tensor core's
+// tile order (rows of an expert start anywhere, so their scales cannot lie
+// pre-tiled), warp 1 issues the products, warps 4 to 7 read the accumulators
+// of one tile while the products of the next fill the other half of TMEM.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "fp8q_host.cuh"
+#include "tcgen05.cuh"
+
+namespace fp8q {
+
+constexpr int kMpThreads = 256;
+constexpr int kMpStages = 4;
+constexpr int kMpMaxExperts = 1024;
+constexpr int kMpRowBoxes = 4;                  // row boxes of 128, 64, 32 and 16 rows
+constexpr uint32_t kMpTmemColumns = 512;
+constexpr uint32_t kMpAccColumns = 224;         // per accumulator half
+constexpr uint32_t kMpScaleColumns = 448;       // scales: 12 columns per stage from here
+constexpr unsigned kErrProductTimeout = 2u;
+
+// WT weight tensors (1: matmul, 2: gate and up), up to kRows rows per tile.
+template <int WT> struct MpShape {
+    static constexpr int kRows = WT == 1 ? 224 : 112;
+    static constexpr int kStageBytes = WT * 16384 + kRows * 128;
+    static constexpr int kScaleBytes = WT * 512 + 1024;
+    static constexpr int kBars = 2 * kMpStages + 4;
+    static constexpr size_t kSmem = (size_t)kMpStages * (kStageBytes + kScaleBytes) + kBars * 8 + 16 +
+                                    (kMpMaxExperts + 2) * 4 + 1024;
+};
+
+struct MpArgs {
+    CUtensorMap w[2];                           // [experts][n][k] codes, 128 x 128 boxes
+    CUtensorMap rows[kMpRowBoxes];              // [rows][k] codes
+    const uint8_t* w_scales[2];
+    const uint8_t* row_scales;                  // [rows][k / 32]
+    const int* offsets;
+    uint16_t* out_bf16;                         // matmul
+    uint8_t* out_codes;                         // swiglu
+    uint8_t* out_scales;
+    int64_t rows_total;
+    int experts, n, k;
+    int feature_tiles, k_steps;                 // ceil(n / 128), ceil(k / 128)
+};
+
+struct MpTile {
+    int e;                                      // expert, or `experts` for rows of no expert (written as zeros)
+    int f;                                      // first feature
+    int64_t r0;                                 // first row
+    int rows;                                   // valid rows, 0 if none
+};
+
+__device__ __forceinline__ int64_t mp_offset(const MpArgs& a, int e) {
+    const int64_t o = a.offsets[e];
+    return o < 0 ? 0 : o > a.rows_total ? a.rows_total : o;
+}
+__device__ __forceinline__ void mp_span(const MpArgs& a, int e, int64_t* lo, int64_t* hi) {
+    *lo = mp_offset(a, e);
+    *hi = e < a.experts ? mp_offset(a, e + 1) : a.rows_total;
+    if (*hi < *lo) *hi = *lo;
+}
+
+// prefix[e] = row tiles of the experts before e; prefix[experts + 1] = all of them.
+__device__ __forceinline__ MpTile mp_tile(const MpArgs& a, const int* prefix, int max_rows, int t) {
+    MpTile d;
+    const int rt = t / a.feature_tiles;
+    d.f = (t - rt * a.feature_tiles) * 128;
+    int lo = 0, hi = a.experts;                 // the last e with prefix[e] <= rt
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= rt) lo = mid; else hi = mid - 1;
+    }
+    d.e = lo;
+    int64_t begin, end;
+    mp_span(a, lo, &begin, &end);
+    const int64_t count = end - begin;
+    const int64_t tiles = (count + max_rows - 1) / max_rows;
+    // equal tiles, in steps of 16 rows: fewer, fuller columns than full tiles and a rest
+    const int64_t per = tiles > 0 ? ((count + tiles - 1) / tiles + 15) / 16 * 16 : 0;
+    const int64_t i = rt - prefix[lo];
+    d.r0 = begin + i * per;
+    const int64_t left = i < 0 ? 0 : count - i * per;
+    d.rows = (int)(left < 0 ? 0 : left < per ? left : per);
+    return d;
+}
+
+// The four E8M0 bytes of one row for K step kb (128 columns); bytes past k are 0.
+__device__ __forceinline__ uint32_t row_scale_word(const uint8_t* row, int kb, int cols) {
+    if ((cols & 3) == 0) return *reinterpret_cast<const uint32_t*>(row + kb * 4);
+    uint32_t w = 0;
+    for (int j = 0; j < 4; ++j)
+        if (kb * 4 + j < cols) w |= (uint32_t)row[kb * 4 + j] << (8 * j);
+    return w;
+}
+
+__device__ __forceinline__ bool mp_wait(uint64_t* bar, uint32_t parity) {
+    if (mbar_wait(bar, parity)) return true;
+    raise_error(kErrProductTimeout);
+    return false;
+}
+
+template <int WT>
+__global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid_constant__ MpArgs a) {
+    using S = MpShape<WT>;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t* sscale = smem + kMpStages * S::kStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sscale + kMpStages * S::kScaleBytes);
+    uint64_t* empty = full + kMpStages;
+    uint64_t* acc_full = empty + kMpStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    int* prefix = reinterpret_cast<int*>(tmem_slot + 4);
+    const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int s = 0; s < kMpStages; ++s) {
+            mbar_init(&full[s], 2);             // the copying thread and the scale warp
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 4);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 3) tmem_alloc(tmem_slot, kMpTmemColumns);
+    dependency_wait();
+    allow_dependents();
+    if (warp == 0) {
+        int run = 0;
+        for (int e0 = 0; e0 <= a.experts; e0 += 32) {
+            const int e = e0 + lane;
+            int tiles = 0;
+            if (e <= a.experts) {
+                int64_t lo, hi;
+                mp_span(a, e, &lo, &hi);
+                tiles = (int)((hi - lo + S::kRows - 1) / S::kRows);
+            }
+            int incl = tiles;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                if (lane >= d) incl += o;
+            }
+            if (e <= a.experts) prefix[e + 1] = run + incl;
+            run += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        }
+        if (lane == 0) prefix[0] = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int total = prefix[a.experts + 1] * a.feature_tiles;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // copies: weights, rows and weight scales
+            int it = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+                const MpTile d = mp_tile(a, prefix, S::kRows, t);
+                if (d.e >= a.experts || d.rows <= 0) continue;
+                const int n16 = (d.rows + 15) >> 4;
+                const uint32_t bytes = WT * (16384 + 512) + n16 * 2048;
+                const int64_t scale_tile = ((int64_t)d.e * a.feature_tiles + (d.f >> 7)) * a.k_steps;
+                for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
+                    const int s = it % kMpStages;
+                    if (!mp_wait(&empty[s], (uint32_t)((it / kMpStages) & 1) ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* st = smem + s * S::kStageBytes;
+                    mbar_arrive_expect_tx(&full[s], bytes);
+#pragma unroll
+                    for (int i = 0; i < WT; ++i) {
+                        tma_3d_g2s(st + i * 16384, &a.w[i], kb * 128, d.f, d.e, &full[s]);
+                        bulk_g2s(sscale + s * S::kScaleBytes + i * 512, a.w_scales[i] + (scale_tile + kb) * 512, 512, &full[s]);
+                    }
+                    int at = 0;
+#pragma unroll
+                    for (int b = 0; b < kMpRowBoxes; ++b) {
+                        const int h = 128 >> b;
+                        if (n16 & (h >> 4)) {
+                            tma_2d_g2s(st + WT * 16384 + at * 128, &a.rows[b], kb * 128, (int)(d.r0 + at), &full[s]);
+                            at += h;
+                        }
+                    }
+                }
+            }
+            if (!ok) {
+                // let the copies in flight land before the shared memory is given up
+                for (int s = 0; s < kMpStages && s < it; ++s) {
+                    const int last = (it - 1 - s);
+                    mbar_wait(&full[last % kMpStages], (uint32_t)((last / kMpStages) & 1));
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int it = 0, tile = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+                const MpTile d = mp_tile(a, prefix, S::kRows, t);
+                if (d.e >= a.experts || d.rows <= 0) continue;
+                const int b = tile & 1;
+                const uint32_t idesc = mx_instr_desc((d.rows + 15) & ~15);
+                const uint32_t acc = tmem + (uint32_t)b * kMpAccColumns;
+                if (!mp_wait(&acc_empty[b], (uint32_t)((tile >> 1) & 1) ^ 1u)) break;
+                tc_fence_after();
+                for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
+                    const int s = it % kMpStages;
+                    if (!mp_wait(&full[s], (uint32_t)((it / kMpStages) & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = smem_addr(smem + s * S::kStageBytes);
+                    const uint32_t sc = smem_addr(sscale + s * S::kScaleBytes);
+                    const uint32_t tsc = tmem + kMpScaleColumns + (uint32_t)s * 12;
+#pragma unroll
+                    for (int i = 0; i < WT; ++i) tc_copy_scales(tsc + 4 * i, scale_desc(sc + 512 * i));
+                    tc_copy_scales(tsc + 4 * WT, scale_desc(sc + 512 * WT));
+                    if (WT == 1 && d.rows > 128) tc_copy_scales(tsc + 8, scale_desc(sc + 1024));
+#pragma unroll
+                    for (int i = 0; i < WT; ++i)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            tc_mma_mx(acc + (uint32_t)(i * S::kRows), operand_desc(st + i * 16384 + q * 32),
+                                      operand_desc(st + WT * 16384 + q * 32), mx_instr_step(idesc, q), tsc + 4 * i,
+                                      tsc + 4 * WT, kb > 0 || q > 0);
+                    tc_commit(&empty[s]);
+                }
+                tc_commit(&acc_full[b]);
+                ++tile;
+            }
+        }
+    } else if (warp == 2) {
+        // the rows' scales: lane l takes rows l, l + 32, ... of the tile, whose words for one K step are
+        // 16 consecutive bytes of the tensor core's scale tile
+        const int cols = a.k >> 5;
+        int it = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+            const MpTile d = mp_tile(a, prefix, S::kRows, t);
+            if (d.e >= a.experts || d.rows <= 0) continue;
+            const uint8_t* base = a.row_scales + (d.r0 + lane) * cols;
+            constexpr int kWords = (S::kRows + 31) / 32;
+            uint32_t next[kWords];
+            auto fetch = [&](int kb) {
+#pragma unroll
+                for (int c = 0; c < kWords; ++c)
+                    next[c] = lane + 32 * c < d.rows ? row_scale_word(base + (int64_t)32 * c * cols, kb, cols) : 0u;
+            };
+            fetch(0);
+            for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
+                const int s = it % kMpStages;
+                uint32_t now[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                for (int c = 0; c < kWords; ++c) now[c] = next[c];
+                if (kb + 1 < a.k_steps) fetch(kb + 1);
+                if (!__all_sync(0xFFFFFFFFu, mp_wait(&empty[s], (uint32_t)((it / kMpStages) & 1) ^ 1u))) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* sc = sscale + s * S::kScaleBytes + WT * 512 + lane * 16;
+                *reinterpret_cast<uint4*>(sc) = make_uint4(now[0], now[1], now[2], now[3]);
+                if (kWords > 4) *reinterpret_cast<uint4*>(sc + 512) = make_uint4(now[4], now[5], now[6], now[7]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[s]);
+            }
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp & 3;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        int tile = 0;
+        for (int t = blockIdx.x; t < total; t += gridDim.x) {
+            const MpTile d = mp_tile(a, prefix, S::kRows, t);
+            const int f = d.f + quarter * 32 + lane;
+            const bool zero = d.e >= a.experts;
+            if (d.rows <= 0) continue;
+            const int b = tile & 1;
+            if (!zero) {
+                if (!__all_sync(0xFFFFFFFFu, mp_wait(&acc_full[b], (uint32_t)((tile >> 1) & 1)))) break;
+                tc_fence_after();
+            }
+            const uint32_t acc = tmem + (uint32_t)b * kMpAccColumns + lanes;
+            for (int c0 = 0; c0 < d.rows; c0 += 16) {
+                uint32_t v[16], u[16];
+                if (!zero) {
+                    tmem_load16(acc + c0, v);
+                    if (WT == 2) tmem_load16(acc + S::kRows + c0, u);
+                    tmem_load_wait();
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) v[c] = u[c] = 0u;
+                }
+                if (WT == 1) {
+                    if (f < a.n) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            if (c0 + c < d.rows)
+                                a.out_bf16[(d.r0 + c0 + c) * a.n + f] =
+                                    (uint16_t)pack_bf16x2(__uint_as_float(v[c]), 0.0f);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float g = __uint_as_float(v[c]);
+                        const float h = g / (1.0f + expf(-g)) * __uint_as_float(u[c]);
+                        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h)));
+                        const int E = (int)(top >> 23);
+                        const int e8 = E > 8 ? E - 8 : 0;
+                        const float q = __fmul_rn(h, __uint_as_float((uint32_t)(254 - e8) << 23));
+                        if (f < a.n && c0 + c < d.rows) {
+                            const int64_t r = d.r0 + c0 + c;
+                            a.out_codes[r * a.n + f] = (uint8_t)cvt_fp8x2<kE4M3>(q, 0.0f);
+                            if (lane == 0) a.out_scales[r * (a.n >> 5) + (f >> 5)] = (uint8_t)e8;
+                        }
+                    }
+                }
+            }
+            if (!zero) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[b]);
+                ++tile;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 3) tmem_free(tmem, kMpTmemColumns);
+}
+
+unsigned unit_errors_moe_product(bool clear) { return read_unit_errors(clear); }
+
+}  // namespace fp8q
+
+using namespace fp8q;
+
+namespace fp8q {
+
+static bool mp_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const void* base, int rank,
+                   const cuuint64_t* dims, const cuuint64_t* strides, int box_rows) {
+    const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estride,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct MpCall {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    const uint8_t* w[2];
+    const uint8_t* ws[2];
+    const int32_t* offsets;
+    int64_t rows, n, k;
+    int experts;
+    void* out;
+    uint8_t* out_scales;
+};
+
+template <int WT>
+static fp8q_status_t mp_launch(const MpCall& c, cudaStream_t stream) {
+    if (c.rows < 0 || c.rows >= (int64_t)1 << 31 || c.experts < 1 || c.experts > kMpMaxExperts || c.n < 0)
+        return FP8Q_ERR_SIZE;
+    if (c.k <= 0 || c.k % MXFP8_BLOCK != 0 || (WT == 2 && c.n % MXFP8_BLOCK != 0)) return FP8Q_ERR_K;
+    if (c.n >= (int64_t)1 << 31 || c.k >= (int64_t)1 << 31) return FP8Q_ERR_SIZE;
+    if (c.n > 0 && (uint64_t)c.k > FP8Q_MAX_ELEMENTS / (uint64_t)c.n / (uint64_t)c.experts) return FP8Q_ERR_SIZE;
+    const int64_t wide = c.n > c.k ? c.n : c.k;
+    if (c.rows > 0 && (uint64_t)wide > FP8Q_MAX_ELEMENTS / (uint64_t)c.rows) return FP8Q_ERR_SIZE;
+    if (c.rows == 0 || c.n == 0) return FP8Q_OK;
+    const void* need[] = {c.codes, c.scales, c.w[0], c.ws[0], c.offsets, c.out, WT == 2 ? c.w[1] : c.w[0],
+                          WT == 2 ? c.ws[1] : c.ws[0], WT == 2 ? c.out_scales : c.out};
+    for (const void* p : need)
+        if (!p) return FP8Q_ERR_NULL;
+    for (const void* p : need)
+        if (!aligned16(p)) return FP8Q_ERR_ALIGN;
+    const size_t wn = (size_t)c.experts * (size_t)c.n * (size_t)c.k;
+    const size_t wsn = mxfp8_swizzled_scale_bytes(c.experts, c.n, c.k);
+    const size_t on = (size_t)c.rows * (size_t)c.n;
+    const Range ins[] = {{c.codes, (size_t)(c.rows * c.k)}, {c.scales, (size_t)(c.rows * (c.k / 32))}, {c.w[0], wn},
+                         {c.ws[0], wsn}, {c.w[1], wn}, {c.ws[1], wsn}, {c.offsets, 4 * (size_t)(c.experts + 1)}};
+    const Range outs[] = {{c.out, WT == 1 ? 2 * on : on}, {c.out_scales, on / 32}};
+    if (any_alias(outs, 2, ins, 7)) return FP8Q_ERR_ALIAS;
+
+    using S = MpShape<WT>;
+    const int64_t feature_tiles = (c.n + 127) / 128;
+    const int64_t row_tiles = c.rows / S::kRows + (c.rows < c.experts ? c.rows : c.experts) + 1;
+    if (feature_tiles * row_tiles >= (int64_t)1 << 31) return FP8Q_ERR_SIZE;
+    const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
+    if (!encode) return cuda_status(cudaErrorNotSupported);
+    MpArgs a;
+    const cuuint64_t wd[3] = {(cuuint64_t)c.k, (cuuint64_t)c.n, (cuuint64_t)c.experts};
+    const cuuint64_t wst[2] = {(cuuint64_t)c.k, (cuuint64_t)c.k * (cuuint64_t)c.n};
+    const cuuint64_t rd[2] = {(cuuint64_t)c.k, (cuuint64_t)c.rows};
+    const cuuint64_t rst[1] = {(cuuint64_t)c.k};
+    for (int i = 0; i < WT; ++i)
+        if (!mp_map(encode, &a.w[i], c.w[i], 3, wd, wst, 128)) return cuda_status(cudaErrorInvalidValue);
+    if (WT == 1) a.w[1] = a.w[0];
+    for (int b = 0; b < kMpRowBoxes; ++b)
+        if (!mp_map(encode, &a.rows[b], c.codes, 2, rd, rst, 128 >> b)) return cuda_status(cudaErrorInvalidValue);
+    a.w_scales[0] = c.ws[0];
+    a.w_scales[1] = c.ws[1];
+    a.row_scales = c.scales;
+    a.offsets = c.offsets;
+    a.out_bf16 = static_cast<uint16_t*>(WT == 1 ? c.out : nullptr);
+    a.out_codes = static_cast<uint8_t*>(WT == 2 ? c.out : nullptr);
+    a.out_scales = c.out_scales;
+    a.rows_total = c.rows;
+    a.experts = c.experts;
+    a.n = (int)c.n;
+    a.k = (int)c.k;
+    a.feature_tiles = (int)feature_tiles;
+    a.k_steps = (int)((c.k + 127) / 128);
+    static KernelCache kc;
+    int resident = 0;
+    const fp8q_status_t st = prepare_kernel(kc, moe_product_kernel<WT>, kMpThreads, S::kSmem, S::kSmem, &resident);
+    if (st != FP8Q_OK) return st;
+    return launch(moe_product_kernel<WT>, grid_for((size_t)(feature_tiles * row_tiles), 1), kMpThreads, S::kSmem, stream, a);
+}
+
+}  // namespace fp8q
+
+extern "C" fp8q_status_t mxfp8_moe_matmul(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                          const uint8_t* w_codes, const uint8_t* w_scales, const int32_t* offsets,
+                                          int experts, int64_t n, int64_t k, void* out_bf16, fp8q_stream_t stream) {
+    FP8Q_NVTX_RANGE("mxfp8_moe_matmul");
+    const MpCall c = {codes, scales, {w_codes, nullptr}, {w_scales, nullptr}, offsets, rows, n, k, experts, out_bf16, nullptr};
+    return mp_launch<1>(c, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" fp8q_status_t mxfp8_moe_swiglu(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                          const uint8_t* gate_codes, const uint8_t* gate_scales,
+                                          const uint8_t* up_codes, const uint8_t* up_scales, const int32_t* offsets,
+                                          int experts, int64_t n, int64_t k, uint8_t* out_codes, uint8_t* out_scales,
+                                          fp8q_stream_t stream) {
+    FP8Q_NVTX_RANGE("mxfp8_moe_swiglu");
+    const MpCall c = {codes, scales, {gate_codes, up_codes}, {gate_scales, up_scales}, offsets, rows, n, k, experts,
+                      out_codes, out_scales};
+    return mp_launch<2>(c, reinterpret_cast<cudaStream_t>(stream));
+}

@@ -1,0 +1,525 @@
+// Tokens to their experts and back.
+//
+// A token t has topk choices; choice i = t * topk + j names expert ids[i].  A
+// stable counting sort by expert gives every choice a slot, the experts' rows
+// lying one after the other (offsets[e] .. offsets[e + 1]) and the choices of
+// no expert (an id outside [0, experts)) last, from offsets[experts] on.
+// Everything after the sort is done from the token's side, so that no sum
+// needs atomics and every result is the same on every run:
+//     gather            rows[slots[t, j]] = x[t]                 (zero rows for dropped choices)
+//     combine           out[t] = sum over j of w[t, j] * y[slots[t, j]]
+//     combine, backward dy[slots[t, j]] = w[t, j] * dout[t],  dw[t, j] = <dout[t], y[slots[t, j]]>
+// and the gradient of gather is combine without weights.
+//
+// The sort is bound by latency, the row movement by HBM.
+#include "fp8q_device.cuh"
+#include "fp8q_host.cuh"
+
+namespace fp8q {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopk = 32;
+
+// ------------------------------------------------------------------ sort ----
+// Blocks of kSortWarps warps own consecutive chunks of choices, and each warp
+// a consecutive segment of its block's chunk, taken 32 choices at a time.  A
+// choice's rank among equal keys is the number of equal keys in earlier
+// blocks, in earlier warps of its block, in earlier steps of its warp and in
+// lower lanes: a sum of counts, so the order is stable without any atomics.
+constexpr int kSortWarps = 16;
+constexpr int kSortThreads = kSortWarps * 32;
+constexpr int kSortMaxBlocks = 128;
+
+struct SortArgs {
+    const void* ids;
+    int id64;
+    int64_t n;
+    int64_t chunk;              // choices per block, a multiple of kSortThreads
+    int experts;
+    int* counts;                // [blocks][experts + 1], unused with one block
+    int* offsets;               // [experts + 1]
+    int* order;                 // [n]
+    int* slots;                 // [n]
+};
+
+__device__ __forceinline__ int sort_key(const SortArgs& a, int64_t i) {
+    const int64_t id = a.id64 ? static_cast<const int64_t*>(a.ids)[i] : (int64_t)static_cast<const int*>(a.ids)[i];
+    return id >= 0 && id < a.experts ? (int)id : a.experts;
+}
+
+// hist[warp][key] = number of this warp's choices with that key.
+__device__ __forceinline__ void warp_histogram(const SortArgs& a, int* hist, int64_t lo, int64_t hi) {
+    const int lane = (int)(threadIdx.x & 31u);
+    for (int64_t i = lo; i < hi; i += 32) {
+        const bool ok = i + lane < hi;
+        const int key = ok ? sort_key(a, i + lane) : -1;
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
+        if (ok && (same & ((1u << lane) - 1u)) == 0) hist[key] += __popc(same);
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ void segment_of(const SortArgs& a, int64_t* lo, int64_t* hi) {
+    const int64_t seg = a.chunk / kSortWarps;
+    const int64_t begin = (int64_t)blockIdx.x * a.chunk + (int64_t)(threadIdx.x >> 5) * seg;
+    *lo = begin < a.n ? begin : a.n;
+    *hi = begin + seg < a.n ? begin + seg : a.n;
+}
+
+__global__ void __launch_bounds__(kSortThreads) moe_sort_count_kernel(const SortArgs a) {
+    extern __shared__ int hist_all[];
+    const int keys = a.experts + 1;
+    const int t = (int)threadIdx.x;
+    for (int i = t; i < kSortWarps * keys; i += kSortThreads) hist_all[i] = 0;
+    dependency_wait();
+    allow_dependents();
+    __syncthreads();
+    int64_t lo, hi;
+    segment_of(a, &lo, &hi);
+    warp_histogram(a, hist_all + (t >> 5) * keys, lo, hi);
+    __syncthreads();
+    for (int e = t; e < keys; e += kSortThreads) {
+        int s = 0;
+        for (int w = 0; w < kSortWarps; ++w) s += hist_all[w * keys + e];
+        a.counts[(int64_t)blockIdx.x * keys + e] = s;
+    }
+}
+
+__global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const SortArgs a) {
+    extern __shared__ int hist_all[];                       // [kSortWarps][keys], then first[keys]
+    __shared__ int warp_total[kSortWarps];
+    const int keys = a.experts + 1;
+    int* first = hist_all + kSortWarps * keys;              // total of each key, then its first slot
+    const int t = (int)threadIdx.x, lane = t & 31, warp = t >> 5;
+    for (int i = t; i < kSortWarps * keys; i += kSortThreads) hist_all[i] = 0;
+    dependency_wait();
+    allow_dependents();
+    __syncthreads();
+    int64_t lo, hi;
+    segment_of(a, &lo, &hi);
+    int* hist = hist_all + warp * keys;
+    warp_histogram(a, hist, lo, hi);
+    __syncthreads();
+    // per key: the counts of this block's warps become their offsets inside
+    // the key's run (behind the earlier blocks); `first` gets the key's total
+    for (int e = t; e < keys; e += kSortThreads) {
+        int before = 0, total = 0;
+        if (gridDim.x > 1) {
+            for (int b = 0; b < (int)gridDim.x; ++b) {
+                const int c = a.counts[(int64_t)b * keys + e];
+                if (b < (int)blockIdx.x) before += c;
+                total += c;
+            }
+        }
+        int run = before;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int c = hist_all[w * keys + e];
+            hist_all[w * keys + e] = run;
+            run += c;
+        }
+        first[e] = gridDim.x > 1 ? total : run;
+    }
+    __syncthreads();
+    // exclusive scan of the totals: each thread a run of consecutive keys
+    const int per = (keys + kSortThreads - 1) / kSortThreads;
+    const int e0 = t * per, e1 = e0 + per < keys ? e0 + per : keys;
+    int mine = 0;
+    for (int e = e0; e < e1; ++e) mine += first[e];
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) warp_total[warp] = incl;
+    __syncthreads();
+    int at = incl - mine;
+    for (int w = 0; w < warp; ++w) at += warp_total[w];
+    for (int e = e0; e < e1; ++e) {
+        const int c = first[e];
+        first[e] = at;
+        if (blockIdx.x == 0) a.offsets[e] = at;
+        at += c;
+    }
+    __syncthreads();
+    for (int64_t i = lo; i < hi; i += 32) {
+        const bool ok = i + lane < hi;
+        const int key = ok ? sort_key(a, i + lane) : -1;
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
+        const unsigned below = same & ((1u << lane) - 1u);
+        const int run = ok ? hist[key] : 0;
+        __syncwarp();
+        if (ok) {
+            const int s = first[key] + run + __popc(below);
+            a.slots[i + lane] = s;
+            a.order[s] = (int)(i + lane);
+            if (below == 0) hist[key] = run + __popc(same);
+        }
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------- gather ----
+// A warp copies one 2 KB segment of one token's row to the slots of all its
+// choices: the row is read once however many experts take it.
+struct RowCopy {
+    const uint8_t* src;
+    uint8_t* dst;
+    int64_t bytes;              // per row
+};
+struct GatherArgs {
+    RowCopy main, extra;        // extra: the scale rows, or bytes == 0
+    const int* slots;
+    const int* routed;          // &offsets[experts]
+    int64_t tokens;
+    int topk;
+    int segments;               // of 2 KB in a main row
+};
+constexpr int kSegBytes = 2048;
+constexpr int kRowWarps = 8;
+
+template <class T>
+__device__ __forceinline__ void copy_to_slots(const RowCopy& r, int64_t t, int64_t lo, int64_t hi, int slot, int topk,
+                                              int routed, int64_t n) {
+    const int lane = (int)(threadIdx.x & 31u);
+    const T* src = reinterpret_cast<const T*>(r.src + t * r.bytes);
+    constexpr int U = 4;
+    const int64_t e0 = lo / (int64_t)sizeof(T), e1 = hi / (int64_t)sizeof(T);
+    for (int64_t b = e0; b < e1; b += 32 * U) {
+        T v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (b + u * 32 + lane < e1) v[u] = src[b + u * 32 + lane];
+        for (int j = 0; j < topk; ++j) {
+            const int s = __shfl_sync(0xFFFFFFFFu, slot, j);
+            if (s < 0 || s >= n) continue;
+            T* dst = reinterpret_cast<T*>(r.dst + (int64_t)s * r.bytes);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (b + u * 32 + lane < e1) dst[b + u * 32 + lane] = s < routed ? v[u] : T{};
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kRowWarps * 32) moe_gather_kernel(const GatherArgs a) {
+    const int lane = (int)(threadIdx.x & 31u);
+    const int64_t unit = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    const int64_t t = unit / a.segments;
+    const int seg = (int)(unit - t * a.segments);
+    dependency_wait();
+    allow_dependents();
+    if (t >= a.tokens) return;
+    const int64_t n = a.tokens * a.topk;
+    const int routed = *a.routed;
+    const int slot = lane < a.topk ? a.slots[t * a.topk + lane] : -1;
+    const int64_t lo = (int64_t)seg * kSegBytes;
+    const int64_t hi = lo + kSegBytes < a.main.bytes ? lo + kSegBytes : a.main.bytes;
+    copy_to_slots<uint4>(a.main, t, lo, hi, slot, a.topk, routed, n);
+    if (seg == 0 && a.extra.bytes > 0) {
+        if (a.extra.bytes % 16 == 0)
+            copy_to_slots<uint4>(a.extra, t, 0, a.extra.bytes, slot, a.topk, routed, n);
+        else if (a.extra.bytes % 4 == 0)
+            copy_to_slots<uint32_t>(a.extra, t, 0, a.extra.bytes, slot, a.topk, routed, n);
+        else
+            copy_to_slots<uint8_t>(a.extra, t, 0, a.extra.bytes, slot, a.topk, routed, n);
+    }
+}
+
+// --------------------------------------------------------------- combine ----
+struct CombineArgs {
+    const uint16_t* y;
+    const int* slots;
+    const int* routed;
+    const float* weights;       // or NULL: all 1
+    uint16_t* out;
+    int64_t tokens;
+    int topk;
+    int k;
+    int segments;               // of 256 columns
+};
+
+__global__ void __launch_bounds__(kRowWarps * 32) moe_combine_kernel(const CombineArgs a) {
+    const int lane = (int)(threadIdx.x & 31u);
+    const int64_t unit = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    const int64_t t = unit / a.segments;
+    const int col = (int)(unit - t * a.segments) * 256 + lane * 8;
+    dependency_wait();
+    allow_dependents();
+    if (t >= a.tokens) return;
+    const int64_t n = a.tokens * a.topk;
+    const int64_t routed = *a.routed < n ? *a.routed : n;
+    int slot = -1;
+    float w = 1.0f;
+    if (lane < a.topk) {
+        slot = a.slots[t * a.topk + lane];
+        if (a.weights) w = a.weights[t * a.topk + lane];
+    }
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    constexpr int U = 4;
+    for (int j0 = 0; j0 < a.topk; j0 += U) {
+        uint4 v[U];
+        float wj[U];
+        bool live[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = __shfl_sync(0xFFFFFFFFu, slot, (j0 + u) & 31);
+            wj[u] = __shfl_sync(0xFFFFFFFFu, w, (j0 + u) & 31);
+            live[u] = j0 + u < a.topk && s >= 0 && s < routed && col < a.k;
+            if (live[u]) v[u] = ld_stream(a.y + (int64_t)s * a.k + col);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (live[u]) {
+                float f[8];
+                unpack8(v[u], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] = __fmaf_rn(wj[u], f[i], acc[i]);
+            }
+    }
+    if (col < a.k)
+        st_stream(a.out + t * a.k + col, make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                                                    pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7])));
+}
+
+struct CombineGradArgs {
+    const uint16_t* dout;
+    const uint16_t* y;
+    const int* slots;
+    const int* routed;
+    const float* weights;
+    uint16_t* dy;
+    float* dweights;
+    int64_t tokens;
+    int topk;
+    int k;
+};
+
+// One token per warp: the dot products are summed in the lanes and joined by
+// shuffles, dy leaves as the row of y passes by.
+__global__ void __launch_bounds__(kRowWarps * 32) moe_combine_backward_kernel(const CombineGradArgs a) {
+    const int lane = (int)(threadIdx.x & 31u);
+    const int64_t t = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    dependency_wait();
+    allow_dependents();
+    if (t >= a.tokens) return;
+    const int64_t n = a.tokens * a.topk;
+    const int routed = *a.routed;
+    int slot = -1;
+    float w = 0.0f;
+    if (lane < a.topk) {
+        slot = a.slots[t * a.topk + lane];
+        w = a.weights[t * a.topk + lane];
+    }
+    const uint16_t* drow = a.dout + t * a.k;
+    for (int j = 0; j < a.topk; ++j) {
+        const int s = __shfl_sync(0xFFFFFFFFu, slot, j);
+        const float wj = __shfl_sync(0xFFFFFFFFu, w, j);
+        float dot = 0.0f;
+        if (s >= 0 && s < n) {
+            const bool live = s < routed;
+            const int64_t base = (int64_t)s * a.k;
+            for (int col = lane * 8; col < a.k; col += 256) {
+                uint4 o = make_uint4(0, 0, 0, 0);
+                if (live) {
+                    float d[8], f[8];
+                    unpack8(*reinterpret_cast<const uint4*>(drow + col), d);
+                    unpack8(ld_stream(a.y + base + col), f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        dot = __fmaf_rn(d[i], f[i], dot);
+                        d[i] = __fmul_rn(d[i], wj);
+                    }
+                    o = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[4], d[5]),
+                                   pack_bf16x2(d[6], d[7]));
+                }
+                st_stream(a.dy + base + col, o);
+            }
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, m);
+        if (lane == 0) a.dweights[t * a.topk + j] = dot;
+    }
+}
+
+// Choices per sort block, and the number of blocks.
+static int64_t sort_chunk(int64_t n, int64_t* blocks) {
+    // one block up to 4 choices per thread; then blocks of 2 per thread while kSortMaxBlocks of them are enough
+    int64_t chunk = n <= 4 * kSortThreads ? 4 * kSortThreads : 2 * kSortThreads;
+    while ((n + chunk - 1) / chunk > kSortMaxBlocks) chunk *= 2;
+    *blocks = (n + chunk - 1) / chunk;
+    return chunk;
+}
+
+// The checks that all the routed operators share.
+static fp8q_status_t route_sizes(int64_t tokens, int topk, int experts) {
+    if (tokens < 0 || experts < 1 || experts > kMaxExperts) return FP8Q_ERR_SIZE;
+    if (topk < 1 || topk > kMaxTopk) return FP8Q_ERR_K;
+    if (tokens > ((int64_t)1 << 31) / topk - 1) return FP8Q_ERR_SIZE;
+    return FP8Q_OK;
+}
+
+static fp8q_status_t row_sizes(int64_t tokens, int topk, int experts, int64_t k, int64_t multiple) {
+    const fp8q_status_t st = route_sizes(tokens, topk, experts);
+    if (st != FP8Q_OK) return st;
+    if (k <= 0 || k % multiple != 0) return FP8Q_ERR_K;
+    if (k > ((int64_t)1 << 30) || (tokens > 0 && (uint64_t)k > FP8Q_MAX_ELEMENTS / (uint64_t)(tokens * topk)))
+        return FP8Q_ERR_SIZE;
+    return FP8Q_OK;
+}
+
+template <int N>
+static bool all_aligned(const void* const (&p)[N]) {
+    for (const void* q : p)
+        if (!aligned16(q)) return false;
+    return true;
+}
+
+static fp8q_status_t units_grid(int64_t units, unsigned* grid) {
+    const int64_t g = (units + kRowWarps - 1) / kRowWarps;
+    if (g > 0x7FFFFFFF) return FP8Q_ERR_SIZE;
+    *grid = (unsigned)g;
+    return FP8Q_OK;
+}
+
+}  // namespace fp8q
+
+using namespace fp8q;
+
+extern "C" size_t fp8q_moe_sort_workspace_bytes(int64_t tokens, int topk, int experts) {
+    if (route_sizes(tokens, topk, experts) != FP8Q_OK) return 0;
+    int64_t blocks;
+    sort_chunk(tokens * topk, &blocks);
+    return blocks > 1 ? (size_t)blocks * (size_t)(experts + 1) * sizeof(int) : 0;
+}
+
+extern "C" fp8q_status_t fp8q_moe_sort(const void* ids, int id_bytes, int64_t tokens, int topk, int experts,
+                                       int32_t* offsets, int32_t* order, int32_t* slots, void* workspace,
+                                       size_t workspace_bytes, fp8q_stream_t stream) {
+    FP8Q_NVTX_RANGE("fp8q_moe_sort");
+    if (id_bytes != 4 && id_bytes != 8) return FP8Q_ERR_FORMAT;
+    const fp8q_status_t st = route_sizes(tokens, topk, experts);
+    if (st != FP8Q_OK) return st;
+    const int64_t n = tokens * topk;
+    const size_t need = fp8q_moe_sort_workspace_bytes(tokens, topk, experts);
+    if (!offsets || (n > 0 && (!ids || !order || !slots)) || (need > 0 && !workspace)) return FP8Q_ERR_NULL;
+    if (workspace_bytes < need) return FP8Q_ERR_SIZE;
+    const void* const all[] = {ids, offsets, order, slots, workspace};
+    if (!all_aligned(all)) return FP8Q_ERR_ALIGN;
+    const Range in = {ids, (size_t)n * id_bytes};
+    const Range outs[] = {{offsets, 4 * (size_t)(experts + 1)}, {order, 4 * (size_t)n}, {slots, 4 * (size_t)n}, {workspace, need}};
+    if (any_alias(outs, 4, &in, 1)) return FP8Q_ERR_ALIAS;
+    int64_t blocks;
+    const int64_t chunk = sort_chunk(n, &blocks);
+    const SortArgs a = {ids, id_bytes == 8, n, chunk, experts, static_cast<int*>(workspace), offsets, order, slots};
+    const size_t most = (size_t)(kSortWarps + 1) * (kMaxExperts + 1) * sizeof(int);
+    const size_t smem = (size_t)(kSortWarps + 1) * (experts + 1) * sizeof(int);
+    static KernelCache kc1, kc2;
+    int resident = 0;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (blocks > 1) {
+        fp8q_status_t s = prepare_kernel(kc1, moe_sort_count_kernel, kSortThreads, most, most, &resident);
+        if (s == FP8Q_OK) s = launch(moe_sort_count_kernel, (unsigned)blocks, kSortThreads, smem, cs, a);
+        if (s != FP8Q_OK) return s;
+    }
+    const fp8q_status_t s = prepare_kernel(kc2, moe_sort_place_kernel, kSortThreads, most, most, &resident);
+    if (s != FP8Q_OK) return s;
+    return launch(moe_sort_place_kernel, (unsigned)(blocks > 0 ? blocks : 1), kSortThreads, smem, cs, a);
+}
+
+namespace fp8q {
+
+static fp8q_status_t gather_launch(GatherArgs a, int experts, cudaStream_t stream) {
+    const int64_t n = a.tokens * a.topk;
+    if (!a.main.src || !a.main.dst || !a.slots || !a.routed || (a.extra.bytes > 0 && (!a.extra.src || !a.extra.dst)))
+        return FP8Q_ERR_NULL;
+    const void* const all[] = {a.main.src, a.main.dst, a.extra.src, a.extra.dst, a.slots, a.routed};
+    if (!all_aligned(all)) return FP8Q_ERR_ALIGN;
+    const Range ins[] = {{a.main.src, (size_t)(a.tokens * a.main.bytes)}, {a.extra.src, (size_t)(a.tokens * a.extra.bytes)},
+                         {a.slots, 4 * (size_t)n}, {a.routed, 4 * (size_t)(experts + 1)}};
+    const Range outs[] = {{a.main.dst, (size_t)(n * a.main.bytes)}, {a.extra.dst, (size_t)(n * a.extra.bytes)}};
+    if (any_alias(outs, 2, ins, 4)) return FP8Q_ERR_ALIAS;
+    a.routed += experts;
+    a.segments = (int)((a.main.bytes + kSegBytes - 1) / kSegBytes);
+    unsigned grid;
+    const fp8q_status_t st = units_grid(a.tokens * a.segments, &grid);
+    if (st != FP8Q_OK) return st;
+    return launch(moe_gather_kernel, grid, kRowWarps * 32, 0, stream, a);
+}
+
+}  // namespace fp8q
+
+extern "C" fp8q_status_t fp8q_moe_gather(const void* x_bf16, const int32_t* slots, const int32_t* offsets,
+                                         int64_t tokens, int topk, int experts, int64_t k, void* rows_bf16,
+                                         fp8q_stream_t stream) {
+    FP8Q_NVTX_RANGE("fp8q_moe_gather");
+    const fp8q_status_t st = row_sizes(tokens, topk, experts, k, 8);
+    if (st != FP8Q_OK || tokens == 0) return st;
+    GatherArgs a = {};
+    a.main = {static_cast<const uint8_t*>(x_bf16), static_cast<uint8_t*>(rows_bf16), 2 * k};
+    a.slots = slots;
+    a.routed = offsets;
+    a.tokens = tokens;
+    a.topk = topk;
+    return gather_launch(a, experts, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" fp8q_status_t mxfp8_moe_gather(const uint8_t* codes, const uint8_t* scales, const int32_t* slots,
+                                          const int32_t* offsets, int64_t tokens, int topk, int experts, int64_t k,
+                                          uint8_t* row_codes, uint8_t* row_scales, fp8q_stream_t stream) {
+    FP8Q_NVTX_RANGE("mxfp8_moe_gather");
+    const fp8q_status_t st = row_sizes(tokens, topk, experts, k, MXFP8_BLOCK);
+    if (st != FP8Q_OK || tokens == 0) return st;
+    GatherArgs a = {};
+    a.main = {codes, row_codes, k};
+    a.extra = {scales, row_scales, k / MXFP8_BLOCK};
+    a.slots = slots;
+    a.routed = offsets;
+    a.tokens = tokens;
+    a.topk = topk;
+    return gather_launch(a, experts, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" fp8q_status_t fp8q_moe_combine(const void* y_bf16, const int32_t* slots, const int32_t* offsets,
+                                          const float* weights, int64_t tokens, int topk, int experts, int64_t k,
+                                          void* out_bf16, fp8q_stream_t stream) {
+    FP8Q_NVTX_RANGE("fp8q_moe_combine");
+    const fp8q_status_t st = row_sizes(tokens, topk, experts, k, 8);
+    if (st != FP8Q_OK || tokens == 0) return st;
+    if (!y_bf16 || !slots || !offsets || !out_bf16) return FP8Q_ERR_NULL;
+    const void* const all[] = {y_bf16, slots, offsets, weights, out_bf16};
+    if (!all_aligned(all)) return FP8Q_ERR_ALIGN;
+    const size_t n = (size_t)(tokens * topk);
+    const Range ins[] = {{y_bf16, 2 * n * (size_t)k}, {slots, 4 * n}, {offsets, 4 * (size_t)(experts + 1)}, {weights, 4 * n}};
+    const Range out = {out_bf16, 2 * (size_t)(tokens * k)};
+    if (any_alias(&out, 1, ins, 4)) return FP8Q_ERR_ALIAS;
+    const int segments = (int)((k + 255) / 256);
+    unsigned grid;
+    const fp8q_status_t sg = units_grid(tokens * segments, &grid);
+    if (sg != FP8Q_OK) return sg;
+    const CombineArgs a = {static_cast<const uint16_t*>(y_bf16), slots, offsets + experts, weights,
+                           static_cast<uint16_t*>(out_bf16), tokens, topk, (int)k, segments};
+    return launch(moe_combine_kernel, grid, kRowWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream), a);
+}
+
+extern "C" fp8q_status_t fp8q_moe_combine_backward(const void* dout_bf16, const void* y_bf16, const int32_t* slots,
+                                                   const int32_t* offsets, const float* weights, int64_t tokens,
+                                                   int topk, int experts, int64_t k, void* dy_bf16, float* dweights,
+                                                   fp8q_stream_t stream) {
+    FP8Q_NVTX_RANGE("fp8q_moe_combine_backward");
+    const fp8q_status_t st = row_sizes(tokens, topk, experts, k, 8);
+    if (st != FP8Q_OK || tokens == 0) return st;
+    if (!dout_bf16 || !y_bf16 || !slots || !offsets || !weights || !dy_bf16 || !dweights) return FP8Q_ERR_NULL;
+    const void* const all[] = {dout_bf16, y_bf16, slots, offsets, weights, dy_bf16, dweights};
+    if (!all_aligned(all)) return FP8Q_ERR_ALIGN;
+    const size_t n = (size_t)(tokens * topk);
+    const Range ins[] = {{dout_bf16, 2 * (size_t)(tokens * k)}, {y_bf16, 2 * n * (size_t)k}, {slots, 4 * n},
+                         {offsets, 4 * (size_t)(experts + 1)}, {weights, 4 * n}};
+    const Range outs[] = {{dy_bf16, 2 * n * (size_t)k}, {dweights, 4 * n}};
+    if (any_alias(outs, 2, ins, 5)) return FP8Q_ERR_ALIAS;
+    unsigned grid;
+    const fp8q_status_t sg = units_grid(tokens, &grid);
+    if (sg != FP8Q_OK) return sg;
+    const CombineGradArgs a = {static_cast<const uint16_t*>(dout_bf16), static_cast<const uint16_t*>(y_bf16), slots,
+                               offsets + experts, weights, static_cast<uint16_t*>(dy_bf16), dweights, tokens, topk, (int)k};
+    return launch(moe_combine_backward_kernel, grid, kRowWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream), a);
+}

@@ -214,6 +214,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
+void* tensor_map_encode_fn() { return reinterpret_cast<void*>(tensor_map_encoder()); }
+
 }  // namespace fp8q
 
 namespace fp8q {

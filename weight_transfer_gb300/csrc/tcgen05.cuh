@@ -1,0 +1,99 @@
+// The fifth-generation tensor core's instructions that the expert products
+// use, one inline function each (sm_103a).
+//
+// Operands lie in shared memory in the K-major layout with a 128-byte swizzle
+// that a tensor-map copy writes; their E8M0 scales and the binary32
+// accumulators lie in tensor memory (TMEM, 128 lanes of 512 32-bit columns).
+#pragma once
+
+#include "fp8q_device.cuh"
+
+namespace fp8q {
+
+// Tensor memory of one CTA: `columns` (a power of two, at least 32) are
+// allocated by one whole warp, which also frees them; the address is written
+// to shared memory.
+__device__ __forceinline__ void tmem_alloc(uint32_t* smem_addr_out, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(smem_addr_out)),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns) : "memory");
+}
+
+// Order tcgen05 work around barriers that other threads wait on.
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory descriptor of a K-major operand: rows of 128 bytes, groups of
+// 8 rows 1024 bytes apart, 128-byte swizzle (code 2 in bits 61..63).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Descriptor of a 512-byte scale tile: 32 rows of 16 bytes, groups of 8 rows
+// 128 bytes apart, no swizzle.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+// A scale tile of 128 rows x 4 scales: shared memory -> 4 TMEM columns, to
+// the 32 lanes of each of the four warps' quarters.
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Instruction descriptor of an e4m3 x e4m3 product with E8M0 scales: M = 128,
+// N = n (a multiple of 16), and which byte of the scale words this K step of
+// 32 uses.
+__device__ __forceinline__ uint32_t mx_instr_desc(int n) {
+    return ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t mx_instr_step(uint32_t idesc, uint32_t step) {
+    return idesc | (step << 4) | (step << 29);
+}
+
+// D[128, n] (+)= A[128, 32] * B[n, 32]^T with one scale per row and 32 columns.
+__device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                          bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// Arrives on `bar` once everything this thread issued to the tensor core is done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+// 16 columns of this warp's 32 lanes: r[c] = TMEM[lane, taddr + c].
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// 3D tiled bulk copy of the box at (x, y, z); x * element size must be a
+// multiple of 16 bytes, out-of-range elements read as zero.
+__device__ __forceinline__ void tma_3d_g2s(void* smem_dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(smem_dst)),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+}  // namespace fp8q
