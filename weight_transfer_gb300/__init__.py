@@ -200,8 +200,15 @@ def _dev(t: Optional[torch.Tensor], what: str, dtype=None, numel: Optional[int] 
     return t.data_ptr()
 
 
+# torch.cuda.current_stream() builds a stream object on every call (2.9 us on
+# a Grace core, as long as a launch); the handle alone takes 0.1 us
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -668,6 +675,9 @@ def fp8q_dequant_reduce_unfused_static(codes: Sequence[torch.Tensor], scales: Se
 
 
 # ------------------------------------------------- expert-block operators ----
+# Their small calls are bound by the host, so that the binding spends on each
+# tensor what it must: inputs are checked once, and outputs that it makes itself
+# are not checked at all.
 def _rows_of(t: torch.Tensor, what: str, k: Optional[int] = None):
     """(rows, k) of a 2D [rows, k] tensor."""
     if t.dim() != 2 or (k is not None and t.shape[1] != k):
@@ -675,36 +685,43 @@ def _rows_of(t: torch.Tensor, what: str, k: Optional[int] = None):
     return t.shape
 
 
-def _shaped(t: torch.Tensor, what: str, shape) -> torch.Tensor:
-    if tuple(t.shape) != tuple(shape):
+def _in(t: Optional[torch.Tensor], what: str, dtype, shape) -> Optional[int]:
+    """Pointer of an input of exactly this shape and type."""
+    if t is None:
+        return None
+    if t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
-    return t
+    return _dev(t, what, dtype)
 
 
-def _rmsnorm(name: str, scale_dtype, scale_shape, scale_numel, code_or_flag, x, weight, eps, residual, want_bf16, want_rstd, codes,
-             scales, out_sum, out_bf16, rstd, stream):
-    rows, k = x.shape
-    dev = x.device
-    _shaped(weight, "weight", (k,))
-    if residual is not None:
-        _shaped(residual, "residual", (rows, k))
-        if out_sum is None:
-            out_sum = torch.empty((rows, k), dtype=torch.bfloat16, device=dev)
-    if codes is None:
-        codes = torch.empty((rows, k), dtype=torch.uint8, device=dev)
-    if scales is None:
-        scales = torch.empty(scale_shape, dtype=scale_dtype, device=dev)
-    if out_bf16 is None and want_bf16:
-        out_bf16 = torch.empty((rows, k), dtype=torch.bfloat16, device=dev)
-    if rstd is None and want_rstd:
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+def _out(t: Optional[torch.Tensor], what: str, dtype, shape, device, numel: int):
+    """(tensor, pointer) of an output: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _dev(t, what, dtype, numel)
+
+
+def _rmsnorm(name: str, fmt_or_flag: int, x, k, weight, eps, residual, want_bf16, want_rstd, codes, scales, scale_dtype,
+             scale_shape, scale_numel, out_sum, out_bf16, rstd, stream):
+    shape = x.shape
+    rows, dev = shape[0], x.device
     n = rows * k
-    st = getattr(lib(), name)(_dev(x, "x", torch.bfloat16), _dev(residual, "residual", torch.bfloat16),
-                              _dev(weight, "weight", torch.bfloat16), rows, k, eps, code_or_flag,
-                              _dev(out_sum, "out_sum", torch.bfloat16, n), _dev(out_bf16, "out_bf16", torch.bfloat16, n),
-                              _dev(codes, "codes", torch.uint8, n), _dev(scales, "scales", scale_dtype, scale_numel),
-                              _dev(rstd, "rstd", torch.float32, rows), _stream(stream))
-    _check(name, st)
+    rp = _in(residual, "residual", torch.bfloat16, shape)
+    wp = _in(weight, "weight", torch.bfloat16, (k,))
+    xp = _dev(x, "x", torch.bfloat16)
+    sp = yp = dp = None
+    if residual is not None or out_sum is not None:
+        out_sum, sp = _out(out_sum, "out_sum", torch.bfloat16, shape, dev, n)
+    codes, cp = _out(codes, "codes", torch.uint8, shape, dev, n)
+    scales, ap = _out(scales, "scales", scale_dtype, scale_shape, dev, scale_numel)
+    if want_bf16 or out_bf16 is not None:
+        out_bf16, yp = _out(out_bf16, "out_bf16", torch.bfloat16, shape, dev, n)
+    if want_rstd or rstd is not None:
+        rstd, dp = _out(rstd, "rstd", torch.float32, (rows,), dev, rows)
+    st = getattr(_lib, name)(xp, rp, wp, rows, k, eps, fmt_or_flag, sp, yp, cp, ap, dp, _stream(stream))
+    if st:
+        _check(name, st)
     return codes, scales, out_sum, out_bf16, rstd
 
 
@@ -719,8 +736,8 @@ def fp8q_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e
     residual is given; out_sum may be `x` or `residual` (in place)."""
     rows, k = _rows_of(x, "x")
     cols = k // FP8Q_BLOCK
-    return _rmsnorm("fp8q_rmsnorm_quantize", torch.float32, (rows, cols), rows * cols, _fmt(fmt), x, weight, eps,
-                    residual, want_bf16, want_rstd, codes, scales, out_sum, out_bf16, rstd, stream)
+    return _rmsnorm("fp8q_rmsnorm_quantize", _fmt(fmt), x, k, weight, eps, residual, want_bf16, want_rstd, codes, scales,
+                    torch.float32, (rows, cols), rows * cols, out_sum, out_bf16, rstd, stream)
 
 
 def mxfp8_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -731,14 +748,18 @@ def mxfp8_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1
     """As fp8q_rmsnorm_quantize with an MXFP8 output: scales are E8M0 bytes,
     row-major [rows, k/32], or flat in the 128x4-tiled layout (swizzled)."""
     rows, k = _rows_of(x, "x")
-    sb = mxfp8_swizzled_scale_bytes(1, rows, k) if swizzled else rows * (k // MXFP8_BLOCK)
-    return _rmsnorm("mxfp8_rmsnorm_quantize", torch.uint8, (sb,) if swizzled else (rows, k // MXFP8_BLOCK), sb,
-                    int(bool(swizzled)), x, weight, eps, residual, want_bf16, want_rstd, codes, scales, out_sum,
-                    out_bf16, rstd, stream)
+    if swizzled:
+        sb = mxfp8_swizzled_scale_bytes(1, rows, k)
+        shape = (sb,)
+    else:
+        sb = rows * (k // MXFP8_BLOCK)
+        shape = (rows, k // MXFP8_BLOCK)
+    return _rmsnorm("mxfp8_rmsnorm_quantize", 1 if swizzled else 0, x, k, weight, eps, residual, want_bf16, want_rstd,
+                    codes, scales, torch.uint8, shape, sb, out_sum, out_bf16, rstd, stream)
 
 
 def fp8q_rmsnorm_backward_workspace_bytes(rows: int, k: int) -> int:
-    return int(lib().fp8q_rmsnorm_backward_workspace_bytes(rows, k))
+    return int(_lib.fp8q_rmsnorm_backward_workspace_bytes(rows, k))
 
 
 def fp8q_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -747,29 +768,27 @@ def fp8q_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
     """Gradient of the norm -> (dx bf16 [rows, k], dweight float32 [k]).  dx
     may be `dy` or `dsum` (in place)."""
     rows, k = _rows_of(h, "h")
-    _shaped(dy, "dy", (rows, k))
-    _shaped(weight, "weight", (k,))
-    if dsum is not None:
-        _shaped(dsum, "dsum", (rows, k))
-    if dx is None:
-        dx = torch.empty((rows, k), dtype=torch.bfloat16, device=h.device)
-    if dweight is None:
-        dweight = torch.empty(k, dtype=torch.float32, device=h.device)
-    need = fp8q_rmsnorm_backward_workspace_bytes(rows, k)
+    shape, dev = h.shape, h.device
+    hp = _dev(h, "h", torch.bfloat16)
+    gp = _in(dy, "dy", torch.bfloat16, shape)
+    wp = _in(weight, "weight", torch.bfloat16, (k,))
+    rp = _in(rstd, "rstd", torch.float32, (rows,))
+    sp = _in(dsum, "dsum", torch.bfloat16, shape)
+    need = _lib.fp8q_rmsnorm_backward_workspace_bytes(rows, k)
+    dx, xp = _out(dx, "dx", torch.bfloat16, shape, dev, rows * k)
+    dweight, dp = _out(dweight, "dweight", torch.float32, (k,), dev, k)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=h.device)
-    st = lib().fp8q_rmsnorm_backward(_dev(dy, "dy", torch.bfloat16), _dev(h, "h", torch.bfloat16),
-                                     _dev(weight, "weight", torch.bfloat16), _dev(rstd, "rstd", torch.float32, rows),
-                                     _dev(dsum, "dsum", torch.bfloat16), rows, k,
-                                     _dev(dx, "dx", torch.bfloat16, rows * k), _dev(dweight, "dweight", torch.float32, k),
-                                     _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-                                     _stream(stream))
-    _check("fp8q_rmsnorm_backward", st)
+        workspace, have = torch.empty(need, dtype=torch.uint8, device=dev), need
+    else:
+        have = workspace.numel() * workspace.element_size()
+    st = _lib.fp8q_rmsnorm_backward(gp, hp, wp, rp, sp, rows, k, xp, dp, _dev(workspace, "workspace"), have, _stream(stream))
+    if st:
+        _check("fp8q_rmsnorm_backward", st)
     return dx, dweight
 
 
 def fp8q_moe_sort_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
-    return int(lib().fp8q_moe_sort_workspace_bytes(tokens, topk, experts))
+    return int(_lib.fp8q_moe_sort_workspace_bytes(tokens, topk, experts))
 
 
 def fp8q_moe_sort(ids: torch.Tensor, experts: int, offsets: Optional[torch.Tensor] = None,
@@ -779,42 +798,39 @@ def fp8q_moe_sort(ids: torch.Tensor, experts: int, offsets: Optional[torch.Tenso
     -> (offsets int32 [experts + 1], order int32 [tokens * topk], slots int32
     [tokens, topk])."""
     tokens, topk = _rows_of(ids, "ids")
-    if ids.dtype not in (torch.int32, torch.int64):
-        raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
+    dtype = ids.dtype
+    if dtype is not torch.int32 and dtype is not torch.int64:
+        raise ValueError(f"ids must be int32 or int64, got {dtype}")
     n, dev = tokens * topk, ids.device
-    if offsets is None:
-        offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
-    if order is None:
-        order = torch.empty(n, dtype=torch.int32, device=dev)
-    if slots is None:
-        slots = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
+    ip = _dev(ids, "ids")
+    offsets, op = _out(offsets, "offsets", torch.int32, (experts + 1,), dev, experts + 1)
+    order, rp = _out(order, "order", torch.int32, (n,), dev, n)
+    slots, sp = _out(slots, "slots", torch.int32, (tokens, topk), dev, n)
+    have = 0
     if workspace is None:
-        need = fp8q_moe_sort_workspace_bytes(tokens, topk, experts)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    st = lib().fp8q_moe_sort(_dev(ids, "ids"), ids.element_size(), tokens, topk, experts,
-                             _dev(offsets, "offsets", torch.int32, experts + 1), _dev(order, "order", torch.int32, n),
-                             _dev(slots, "slots", torch.int32, n), _dev(workspace, "workspace"),
-                             0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
-    _check("fp8q_moe_sort", st)
+        have = _lib.fp8q_moe_sort_workspace_bytes(tokens, topk, experts)
+        if have:
+            workspace = torch.empty(have, dtype=torch.uint8, device=dev)
+    else:
+        have = workspace.numel() * workspace.element_size()
+    st = _lib.fp8q_moe_sort(ip, 4 if dtype is torch.int32 else 8, tokens, topk, experts, op, rp, sp,
+                            _dev(workspace, "workspace"), have, _stream(stream))
+    if st:
+        _check("fp8q_moe_sort", st)
     return offsets, order, slots
-
-
-def _routes(slots: torch.Tensor, offsets: torch.Tensor):
-    """(tokens, topk, experts, slots pointer, offsets pointer) of a sort's results."""
-    tokens, topk = _rows_of(slots, "slots")
-    return tokens, topk, offsets.numel() - 1, _dev(slots, "slots", torch.int32), _dev(offsets, "offsets", torch.int32)
 
 
 def fp8q_moe_gather(x: torch.Tensor, slots: torch.Tensor, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
                     stream=None):
     """bf16 x [tokens, k] -> the experts' rows bf16 [tokens * topk, k]."""
-    tokens, topk, experts, sp, op = _routes(slots, offsets)
-    _, k = _shaped(x, "x", (tokens, x.shape[-1])).shape
-    if rows is None:
-        rows = torch.empty((tokens * topk, k), dtype=torch.bfloat16, device=x.device)
-    st = lib().fp8q_moe_gather(_dev(x, "x", torch.bfloat16), sp, op, tokens, topk, experts, k,
-                               _dev(rows, "rows", torch.bfloat16, tokens * topk * k), _stream(stream))
-    _check("fp8q_moe_gather", st)
+    tokens, topk = _rows_of(slots, "slots")
+    k, n = x.shape[-1], tokens * topk
+    xp = _in(x, "x", torch.bfloat16, (tokens, k))
+    rows, rp = _out(rows, "rows", torch.bfloat16, (n, k), x.device, n * k)
+    st = _lib.fp8q_moe_gather(xp, _dev(slots, "slots", torch.int32), _dev(offsets, "offsets", torch.int32), tokens, topk,
+                              offsets.numel() - 1, k, rp, _stream(stream))
+    if st:
+        _check("fp8q_moe_gather", st)
     return rows
 
 
@@ -822,18 +838,17 @@ def mxfp8_moe_gather(codes: torch.Tensor, scales: torch.Tensor, slots: torch.Ten
                      row_codes: Optional[torch.Tensor] = None, row_scales: Optional[torch.Tensor] = None, stream=None):
     """MXFP8 rows (codes uint8 [tokens, k], scales uint8 [tokens, k/32]) -> the
     experts' rows (codes [tokens * topk, k], scales [tokens * topk, k/32])."""
-    tokens, topk, experts, sp, op = _routes(slots, offsets)
-    _, k = _shaped(codes, "codes", (tokens, codes.shape[-1])).shape
+    tokens, topk = _rows_of(slots, "slots")
+    k, n, dev = codes.shape[-1], tokens * topk, codes.device
     cols = k // MXFP8_BLOCK
-    n = tokens * topk
-    if row_codes is None:
-        row_codes = torch.empty((n, k), dtype=torch.uint8, device=codes.device)
-    if row_scales is None:
-        row_scales = torch.empty((n, cols), dtype=torch.uint8, device=codes.device)
-    st = lib().mxfp8_moe_gather(_dev(codes, "codes", torch.uint8), _dev(scales, "scales", torch.uint8, tokens * cols), sp, op,
-                                tokens, topk, experts, k, _dev(row_codes, "row_codes", torch.uint8, n * k),
-                                _dev(row_scales, "row_scales", torch.uint8, n * cols), _stream(stream))
-    _check("mxfp8_moe_gather", st)
+    cp = _in(codes, "codes", torch.uint8, (tokens, k))
+    sp = _in(scales, "scales", torch.uint8, (tokens, cols))
+    row_codes, rcp = _out(row_codes, "row_codes", torch.uint8, (n, k), dev, n * k)
+    row_scales, rsp = _out(row_scales, "row_scales", torch.uint8, (n, cols), dev, n * cols)
+    st = _lib.mxfp8_moe_gather(cp, sp, _dev(slots, "slots", torch.int32), _dev(offsets, "offsets", torch.int32), tokens, topk,
+                               offsets.numel() - 1, k, rcp, rsp, _stream(stream))
+    if st:
+        _check("mxfp8_moe_gather", st)
     return row_codes, row_scales
 
 
@@ -842,15 +857,15 @@ def fp8q_moe_combine(y: torch.Tensor, slots: torch.Tensor, offsets: torch.Tensor
     """The experts' rows bf16 [tokens * topk, k] summed back (with float32
     weights [tokens, topk], or all 1) -> bf16 [tokens, k].  Without weights it
     is also the gradient of fp8q_moe_gather."""
-    tokens, topk, experts, sp, op = _routes(slots, offsets)
-    _, k = _shaped(y, "y", (tokens * topk, y.shape[-1])).shape
-    if weights is not None:
-        _shaped(weights, "weights", (tokens, topk))
-    if out is None:
-        out = torch.empty((tokens, k), dtype=torch.bfloat16, device=y.device)
-    st = lib().fp8q_moe_combine(_dev(y, "y", torch.bfloat16), sp, op, _dev(weights, "weights", torch.float32), tokens, topk,
-                                experts, k, _dev(out, "out", torch.bfloat16, tokens * k), _stream(stream))
-    _check("fp8q_moe_combine", st)
+    tokens, topk = _rows_of(slots, "slots")
+    k = y.shape[-1]
+    yp = _in(y, "y", torch.bfloat16, (tokens * topk, k))
+    wp = _in(weights, "weights", torch.float32, (tokens, topk))
+    out, op = _out(out, "out", torch.bfloat16, (tokens, k), y.device, tokens * k)
+    st = _lib.fp8q_moe_combine(yp, _dev(slots, "slots", torch.int32), _dev(offsets, "offsets", torch.int32), wp, tokens, topk,
+                               offsets.numel() - 1, k, op, _stream(stream))
+    if st:
+        _check("fp8q_moe_combine", st)
     return out
 
 
@@ -858,29 +873,24 @@ def fp8q_moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, slots: torch.
                               weights: torch.Tensor, dy: Optional[torch.Tensor] = None,
                               dweights: Optional[torch.Tensor] = None, stream=None):
     """Gradient of fp8q_moe_combine -> (dy bf16 [tokens * topk, k], dweights float32 [tokens, topk])."""
-    tokens, topk, experts, sp, op = _routes(slots, offsets)
-    _, k = _shaped(dout, "dout", (tokens, dout.shape[-1])).shape
-    n = tokens * topk
-    _shaped(y, "y", (n, k))
-    _shaped(weights, "weights", (tokens, topk))
-    if dy is None:
-        dy = torch.empty((n, k), dtype=torch.bfloat16, device=y.device)
-    if dweights is None:
-        dweights = torch.empty((tokens, topk), dtype=torch.float32, device=y.device)
-    st = lib().fp8q_moe_combine_backward(_dev(dout, "dout", torch.bfloat16), _dev(y, "y", torch.bfloat16), sp, op,
-                                         _dev(weights, "weights", torch.float32), tokens, topk, experts, k,
-                                         _dev(dy, "dy", torch.bfloat16, n * k),
-                                         _dev(dweights, "dweights", torch.float32, n), _stream(stream))
-    _check("fp8q_moe_combine_backward", st)
+    tokens, topk = _rows_of(slots, "slots")
+    k, n, dev = dout.shape[-1], tokens * topk, dout.device
+    gp = _in(dout, "dout", torch.bfloat16, (tokens, k))
+    yp = _in(y, "y", torch.bfloat16, (n, k))
+    wp = _in(weights, "weights", torch.float32, (tokens, topk))
+    dy, dp = _out(dy, "dy", torch.bfloat16, (n, k), dev, n * k)
+    dweights, dwp = _out(dweights, "dweights", torch.float32, (tokens, topk), dev, n)
+    st = _lib.fp8q_moe_combine_backward(gp, yp, _dev(slots, "slots", torch.int32), _dev(offsets, "offsets", torch.int32), wp,
+                                        tokens, topk, offsets.numel() - 1, k, dp, dwp, _stream(stream))
+    if st:
+        _check("fp8q_moe_combine_backward", st)
     return dy, dweights
 
 
-def _expert_weights(codes: torch.Tensor, scales: torch.Tensor, what: str, experts: int, k: int):
-    """n of weights [experts, n, k] (codes) with their swizzled scales, and both pointers."""
-    if codes.dim() != 3 or codes.shape[0] != experts or codes.shape[2] != k:
-        raise ValueError(f"{what} must be [{experts}, n, {k}], got {list(codes.shape)}")
-    n = codes.shape[1]
-    return n, _dev(codes, what, torch.uint8), _dev(scales, f"{what} scales", torch.uint8, mxfp8_swizzled_scale_bytes(experts, n, k))
+def _expert_weights(codes: torch.Tensor, scales: torch.Tensor, what: str, experts: int, n: int, k: int):
+    """Pointers of weights [experts, n, k] (codes) and of their swizzled scales."""
+    need = experts * ((n + 127) // 128) * ((k + 127) // 128) * 512
+    return _in(codes, what, torch.uint8, (experts, n, k)), _dev(scales, f"{what}' scales", torch.uint8, need)
 
 
 def mxfp8_moe_matmul(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
@@ -889,14 +899,15 @@ def mxfp8_moe_matmul(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.T
     their experts' weights (w_codes [experts, n, k] and their swizzled scales,
     as mxfp8_quantize_swizzled gives them) -> bf16 [rows, n]."""
     rows, k = _rows_of(codes, "codes")
-    experts = offsets.numel() - 1
-    n, wp, wsp = _expert_weights(w_codes, w_scales, "w_codes", experts, k)
-    if out is None:
-        out = torch.empty((rows, n), dtype=torch.bfloat16, device=codes.device)
-    st = lib().mxfp8_moe_matmul(_dev(codes, "codes", torch.uint8), _dev(scales, "scales", torch.uint8, rows * (k // MXFP8_BLOCK)),
-                                rows, wp, wsp, _dev(offsets, "offsets", torch.int32), experts, n, k,
-                                _dev(out, "out", torch.bfloat16, rows * n), _stream(stream))
-    _check("mxfp8_moe_matmul", st)
+    experts, n = offsets.numel() - 1, w_codes.shape[-2]
+    cp = _dev(codes, "codes", torch.uint8)
+    sp = _in(scales, "scales", torch.uint8, (rows, k // MXFP8_BLOCK))
+    wp, wsp = _expert_weights(w_codes, w_scales, "w_codes", experts, n, k)
+    out, op = _out(out, "out", torch.bfloat16, (rows, n), codes.device, rows * n)
+    st = _lib.mxfp8_moe_matmul(cp, sp, rows, wp, wsp, _dev(offsets, "offsets", torch.int32), experts, n, k, op,
+                               _stream(stream))
+    if st:
+        _check("mxfp8_moe_matmul", st)
     return out
 
 
@@ -906,19 +917,16 @@ def mxfp8_moe_swiglu(codes: torch.Tensor, scales: torch.Tensor, gate_codes: torc
     """silu(rows x gate) * (rows x up), quantized to MXFP8 rows -> (codes uint8
     [rows, n], scales uint8 [rows, n/32]), the input of the down product."""
     rows, k = _rows_of(codes, "codes")
-    experts = offsets.numel() - 1
-    n, gp, gsp = _expert_weights(gate_codes, gate_scales, "gate_codes", experts, k)
-    nu, up, usp = _expert_weights(up_codes, up_scales, "up_codes", experts, k)
-    if nu != n:
-        raise ValueError(f"gate has {n} rows and up {nu}")
+    experts, n, dev = offsets.numel() - 1, gate_codes.shape[-2], codes.device
+    cp = _dev(codes, "codes", torch.uint8)
+    sp = _in(scales, "scales", torch.uint8, (rows, k // MXFP8_BLOCK))
+    gp, gsp = _expert_weights(gate_codes, gate_scales, "gate_codes", experts, n, k)
+    up, usp = _expert_weights(up_codes, up_scales, "up_codes", experts, n, k)
     cols = n // MXFP8_BLOCK
-    if out_codes is None:
-        out_codes = torch.empty((rows, n), dtype=torch.uint8, device=codes.device)
-    if out_scales is None:
-        out_scales = torch.empty((rows, cols), dtype=torch.uint8, device=codes.device)
-    st = lib().mxfp8_moe_swiglu(_dev(codes, "codes", torch.uint8), _dev(scales, "scales", torch.uint8, rows * (k // MXFP8_BLOCK)),
-                                rows, gp, gsp, up, usp, _dev(offsets, "offsets", torch.int32), experts, n, k,
-                                _dev(out_codes, "out_codes", torch.uint8, rows * n),
-                                _dev(out_scales, "out_scales", torch.uint8, rows * cols), _stream(stream))
-    _check("mxfp8_moe_swiglu", st)
+    out_codes, op = _out(out_codes, "out_codes", torch.uint8, (rows, n), dev, rows * n)
+    out_scales, osp = _out(out_scales, "out_scales", torch.uint8, (rows, cols), dev, rows * cols)
+    st = _lib.mxfp8_moe_swiglu(cp, sp, rows, gp, gsp, up, usp, _dev(offsets, "offsets", torch.int32), experts, n, k, op, osp,
+                               _stream(stream))
+    if st:
+        _check("mxfp8_moe_swiglu", st)
     return out_codes, out_scales
