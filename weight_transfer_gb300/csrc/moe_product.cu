@@ -45,7 +45,7 @@ template <int WT> struct MpShape {
     static constexpr int kScaleBytes = WT * 512 + 1024;
     static constexpr int kBars = 2 * kMpStages + 4;
     static constexpr size_t kSmem = (size_t)kMpStages * (kStageBytes + kScaleBytes) + kBars * 8 + 16 +
-                                    (kMpMaxExperts + 2) * 4 + 1024;
+                                    (kMpMaxExperts + 2) * 4 + 1024 + 4 * 1024;
 };
 
 struct MpArgs {
@@ -105,11 +105,39 @@ __device__ __forceinline__ MpTile mp_tile(const MpArgs& a, const int* prefix, in
 
 // The four E8M0 bytes of one row for K step kb (128 columns); bytes past k are 0.
 __device__ __forceinline__ uint32_t row_scale_word(const uint8_t* row, int kb, int cols) {
-    if ((cols & 3) == 0) return *reinterpret_cast<const uint32_t*>(row + kb * 4);
     uint32_t w = 0;
     for (int j = 0; j < 4; ++j)
         if (kb * 4 + j < cols) w |= (uint32_t)row[kb * 4 + j] << (8 * j);
     return w;
+}
+
+// Byte of 16-byte chunk `chunk` (8 features) of row r in a reading warp's
+// 16 x 64-byte staging area; the exclusive or spreads 8 rows over all banks.
+__device__ __forceinline__ int out_stage_at(int r, int chunk) { return r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4); }
+
+// g / (1 + exp(-g)) * u.  The reciprocal is the hardware's (1 ulp, with
+// subnormal results); the result is about to be rounded to 8 bits.
+__device__ __forceinline__ float silu_times(float g, float u) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, expf(-g))));
+    return __fmul_rn(__fmul_rn(g, r), u);
+}
+
+// One step of the 4 x 4 byte transpose of the words x and y over four lanes:
+// with the lane at distance `mask`, a lane exchanges the bytes whose index
+// differs from its own in bit BIT (0: odd and even bytes, 1: halves).  Each
+// word gives away two bytes, so that one shuffle serves both words.
+template <int BIT>
+__device__ __forceinline__ void transpose_step(uint32_t& x, uint32_t& y, int mask, bool upper) {
+    const uint32_t send = BIT == 0 ? __byte_perm(x, y, upper ? 0x6420u : 0x7531u) : __byte_perm(x, y, upper ? 0x5410u : 0x7632u);
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, send, mask);      // two bytes for x, two for y
+    if (BIT == 0) {
+        x = __byte_perm(x, got, upper ? 0x3514u : 0x5240u);
+        y = __byte_perm(y, got, upper ? 0x3716u : 0x7260u);
+    } else {
+        x = __byte_perm(x, got, upper ? 0x3254u : 0x5410u);
+        y = __byte_perm(y, got, upper ? 0x3276u : 0x7610u);
+    }
 }
 
 __device__ __forceinline__ bool mp_wait(uint64_t* bar, uint32_t parity) {
@@ -124,7 +152,8 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
     extern __shared__ __align__(128) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* sscale = smem + kMpStages * S::kStageBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sscale + kMpStages * S::kScaleBytes);
+    uint8_t* sout = sscale + kMpStages * S::kScaleBytes;            // 1 KB per reading warp
+    uint64_t* full = reinterpret_cast<uint64_t*>(sout + 4 * 1024);
     uint64_t* empty = full + kMpStages;
     uint64_t* acc_full = empty + kMpStages;
     uint64_t* acc_empty = acc_full + 2;
@@ -134,7 +163,7 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
 
     if (tid == 0) {
         for (int s = 0; s < kMpStages; ++s) {
-            mbar_init(&full[s], 2);             // the copying thread and the scale warp
+            mbar_init(&full[s], 33);            // the copying thread and the scale warp's lanes
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -235,6 +264,7 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                         break;
                     }
                     tc_fence_after();
+                    fence_proxy_async_smem();   // the scale warp's stores, before the tensor core reads them
                     const uint32_t st = smem_addr(smem + s * S::kStageBytes);
                     const uint32_t sc = smem_addr(sscale + s * S::kScaleBytes);
                     const uint32_t tsc = tmem + kMpScaleColumns + (uint32_t)s * 12;
@@ -259,45 +289,48 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
         // the rows' scales: lane l takes rows l, l + 32, ... of the tile, whose words for one K step are
         // 16 consecutive bytes of the tensor core's scale tile
         const int cols = a.k >> 5;
+        const bool words = (cols & 3) == 0;
         int it = 0;
         bool ok = true;
         for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
             const MpTile d = mp_tile(a, prefix, S::kRows, t);
             if (d.e >= a.experts || d.rows <= 0) continue;
-            const uint8_t* base = a.row_scales + (d.r0 + lane) * cols;
+            const uint8_t* base = a.row_scales + d.r0 * cols;
             constexpr int kWords = (S::kRows + 31) / 32;
-            uint32_t next[kWords];
-            auto fetch = [&](int kb) {
-#pragma unroll
-                for (int c = 0; c < kWords; ++c)
-                    next[c] = lane + 32 * c < d.rows ? row_scale_word(base + (int64_t)32 * c * cols, kb, cols) : 0u;
-            };
-            fetch(0);
             for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
                 const int s = it % kMpStages;
-                uint32_t now[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-                for (int c = 0; c < kWords; ++c) now[c] = next[c];
-                if (kb + 1 < a.k_steps) fetch(kb + 1);
                 if (!__all_sync(0xFFFFFFFFu, mp_wait(&empty[s], (uint32_t)((it / kMpStages) & 1) ^ 1u))) {
                     ok = false;
                     break;
                 }
                 uint8_t* sc = sscale + s * S::kScaleBytes + WT * 512 + lane * 16;
-                *reinterpret_cast<uint4*>(sc) = make_uint4(now[0], now[1], now[2], now[3]);
-                if (kWords > 4) *reinterpret_cast<uint4*>(sc + 512) = make_uint4(now[4], now[5], now[6], now[7]);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[s]);
+                if (words) {
+                    // asynchronous 4-byte copies: this warp never waits for memory, only for a free stage
+#pragma unroll
+                    for (int c = 0; c < kWords; ++c) {
+                        const int r = lane + 32 * c;
+                        cp_async4(sc + (c >> 2) * 512 + (c & 3) * 4, base + (r < d.rows ? (int64_t)r * cols + kb * 4 : 0),
+                                  r < d.rows ? 4 : 0);
+                    }
+                    cp_async_arrive(&full[s]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kWords; ++c) {
+                        const int r = lane + 32 * c;
+                        *reinterpret_cast<uint32_t*>(sc + (c >> 2) * 512 + (c & 3) * 4) =
+                            r < d.rows ? row_scale_word(base + (int64_t)r * cols, kb, cols) : 0u;
+                    }
+                    mbar_arrive(&full[s]);
+                }
             }
         }
+        cp_async_wait_all();                    // none of this warp's copies outlives the block, whatever stopped it
     } else if (warp >= 4) {
         const int quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         int tile = 0;
         for (int t = blockIdx.x; t < total; t += gridDim.x) {
             const MpTile d = mp_tile(a, prefix, S::kRows, t);
-            const int f = d.f + quarter * 32 + lane;
             const bool zero = d.e >= a.experts;
             if (d.rows <= 0) continue;
             const int b = tile & 1;
@@ -306,38 +339,115 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                 tc_fence_after();
             }
             const uint32_t acc = tmem + (uint32_t)b * kMpAccColumns + lanes;
-            for (int c0 = 0; c0 < d.rows; c0 += 16) {
-                uint32_t v[16], u[16];
-                if (!zero) {
-                    tmem_load16(acc + c0, v);
-                    if (WT == 2) tmem_load16(acc + S::kRows + c0, u);
-                    tmem_load_wait();
-                } else {
+            if (WT == 1) {
+                uint8_t* stage = sout + quarter * 1024;             // [16 rows][32 features] bf16
+                const int f0 = d.f + quarter * 32;
+                for (int c0 = 0; c0 < d.rows; c0 += 16) {
+                    uint32_t lo[8], hi[8];                          // features 0..15 and 16..31 of the warp
+                    if (!zero) {
+                        tmem_load_16x256b_x2(acc + c0, lo);
+                        tmem_load_16x256b_x2(acc + (16u << 16) + c0, hi);
+                        tmem_load_wait();
+                    } else {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) v[c] = u[c] = 0u;
-                }
-                if (WT == 1) {
-                    if (f < a.n) {
-#pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            if (c0 + c < d.rows)
-                                a.out_bf16[(d.r0 + c0 + c) * a.n + f] =
-                                    (uint16_t)pack_bf16x2(__uint_as_float(v[c]), 0.0f);
+                        for (int i = 0; i < 8; ++i) lo[i] = hi[i] = 0u;
                     }
-                } else {
+                    // register pair i of `lo` holds rows c0 + 8 * (i / 2) + 2 * (lane % 4) + {0, 1} of feature
+                    // lane / 4 + 8 * (i % 2); stored transposed, 8 features are 16 bytes of an output row
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const float g = __uint_as_float(v[c]);
-                        const float h = g / (1.0f + expf(-g)) * __uint_as_float(u[c]);
-                        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h)));
-                        const int E = (int)(top >> 23);
-                        const int e8 = E > 8 ? E - 8 : 0;
-                        const float q = __fmul_rn(h, __uint_as_float((uint32_t)(254 - e8) << 23));
-                        if (f < a.n && c0 + c < d.rows) {
-                            const int64_t r = d.r0 + c0 + c;
-                            a.out_codes[r * a.n + f] = (uint8_t)cvt_fp8x2<kE4M3>(q, 0.0f);
-                            if (lane == 0) a.out_scales[r * (a.n >> 5) + (f >> 5)] = (uint8_t)e8;
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t m[4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            m[i] = pack_bf16x2(__uint_as_float(lo[4 * h + 2 * i]), __uint_as_float(lo[4 * h + 2 * i + 1]));
+                            m[2 + i] = pack_bf16x2(__uint_as_float(hi[4 * h + 2 * i]), __uint_as_float(hi[4 * h + 2 * i + 1]));
                         }
+                        const int r = 8 * h + (lane & 7), chunk = lane >> 3;
+                        stmatrix_x4_trans(stage + out_stage_at(r, chunk), m);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = 8 * h + (lane >> 2), chunk = lane & 3;
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + out_stage_at(r, chunk));
+                        const int ff = f0 + chunk * 8;
+                        if (c0 + r < d.rows && ff < a.n) {
+                            uint16_t* o = a.out_bf16 + (d.r0 + c0 + r) * a.n + ff;
+                            if ((a.n & 7) == 0)
+                                *reinterpret_cast<uint4*>(o) = v;
+                            else
+                                st_u16_tail(o, &v.x, 4, a.n - ff);
+                        }
+                    }
+                    __syncwarp();
+                }
+            } else {
+                // fragment order (see tmem_load_16x256b_x2): this lane holds rows c0 + 8 h + 2 q + j of features
+                // p + 8 i, q = lane % 4, p = lane / 4; the 8 lanes of one q hold the 32 features of their rows
+                const int q4 = lane & 3, p = lane >> 2;
+                const int f0 = d.f + quarter * 32;
+                const int64_t scale_cols = a.n >> 5;
+                for (int c0 = 0; c0 < d.rows; c0 += 16) {
+                    uint32_t g[2][8], u[2][8];
+                    if (!zero) {
+                        tmem_load_16x256b_x2(acc + c0, g[0]);
+                        tmem_load_16x256b_x2(acc + (16u << 16) + c0, g[1]);
+                        tmem_load_16x256b_x2(acc + S::kRows + c0, u[0]);
+                        tmem_load_16x256b_x2(acc + (16u << 16) + S::kRows + c0, u[1]);
+                        tmem_load_wait();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) g[0][i] = g[1][i] = u[0][i] = u[1][i] = 0u;
+                    }
+                    // v[r][i]: row r = 2 h + j of this lane's four, feature p + 8 i
+                    float v[4][4];
+                    uint32_t top[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        top[r] = 0u;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int at = 4 * (r >> 1) + 2 * (i & 1) + (r & 1);
+                            v[r][i] = silu_times(__uint_as_float(g[i >> 1][at]), __uint_as_float(u[i >> 1][at]));
+                            top[r] = max(top[r], __float_as_uint(fabsf(v[r][i])));
+                        }
+                    }
+                    // the scale needs the exponent of the block's largest magnitude only: two rows' exponents per word
+                    uint32_t ex[2] = {(top[0] >> 23) | (top[1] >> 23 << 16), (top[2] >> 23) | (top[3] >> 23 << 16)};
+#pragma unroll
+                    for (int m = 4; m < 32; m <<= 1) {
+                        ex[0] = __vmaxu2(ex[0], __shfl_xor_sync(0xFFFFFFFFu, ex[0], m));
+                        ex[1] = __vmaxu2(ex[1], __shfl_xor_sync(0xFFFFFFFFu, ex[1], m));
+                    }
+                    int e8[4];
+                    uint32_t w[4];                                  // byte i: feature p + 8 i
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int E = (int)((ex[r >> 1] >> (16 * (r & 1))) & 0xFFFFu);
+                        e8[r] = E > 8 ? E - 8 : 0;
+                        const float factor = __uint_as_float((uint32_t)(254 - e8[r]) << 23);
+                        w[r] = cvt_fp8x4<kE4M3>(__fmul_rn(v[r][0], factor), __fmul_rn(v[r][1], factor),
+                                                __fmul_rn(v[r][2], factor), __fmul_rn(v[r][3], factor));
+                    }
+                    // 4 x 4 byte transposes over the lanes p, p ^ 1, p ^ 2, p ^ 3: byte b of the result is feature
+                    // 8 (p % 4) + 4 (p / 4) + b, so that a word is four neighbours
+                    transpose_step<0>(w[0], w[1], 4, (p & 1) != 0);
+                    transpose_step<0>(w[2], w[3], 4, (p & 1) != 0);
+                    transpose_step<1>(w[0], w[1], 8, (p & 2) != 0);
+                    transpose_step<1>(w[2], w[3], 8, (p & 2) != 0);
+                    if (f0 < a.n) {
+                        const int64_t row0 = d.r0 + c0 + 2 * q4;
+                        const int fo = f0 + 8 * (p & 3) + 4 * (p >> 2);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int c = 8 * (r >> 1) + (r & 1);
+                            if (c0 + 2 * q4 + c < d.rows)
+                                *reinterpret_cast<uint32_t*>(a.out_codes + (row0 + c) * a.n + fo) = w[r];
+                        }
+                        const int c = 8 * ((p >> 1) & 1) + (p & 1);   // lane p < 4 writes the scale of row r = p
+                        const int e = p == 0 ? e8[0] : p == 1 ? e8[1] : p == 2 ? e8[2] : e8[3];
+                        if (p < 4 && c0 + 2 * q4 + c < d.rows)
+                            a.out_scales[(row0 + c) * scale_cols + (f0 >> 5)] = (uint8_t)e;
                     }
                 }
             }
