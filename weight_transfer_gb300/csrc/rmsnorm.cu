@@ -9,7 +9,7 @@
 // the unrounded sum h; only the stored sum is rounded to bf16.
 //
 // The work is bound by HBM: a row is read once and stays in registers between
-// the sum of squares and the output.
+// the sum of squares and the output, and the next row is read meanwhile.
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 
@@ -40,127 +40,166 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sum over the block's threads, the same value in every thread and the same
-// order on every run.  `slot` alternates between two shared arrays so that one
-// barrier per call is enough.
-__device__ __forceinline__ float block_sum(float v, float (*red)[32], int slot) {
-    v = warp_sum(v);
-    const int warps = (int)(blockDim.x + 31u) >> 5;
-    if (warps == 1) return v;
-    if ((threadIdx.x & 31u) == 0) red[slot][threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.0f;
-    for (int i = 0; i < warps; ++i) s += red[slot][i];
-    return s;
-}
+constexpr int kNormWarps = 4;   // warps of a block whose warps have a row each
+
+// How the threads of a block share the rows: a warp per row (short rows, no
+// barrier at all) or the whole block per row.  Blocks walk over the rows with
+// a fixed stride; the weights stay in registers and the next row is on its way
+// while this one is summed up and written.
+template <bool WARP_ROWS> struct RowGroup {
+    int t;                      // thread inside the group
+    int size;                   // threads of the group
+    int64_t first, stride;      // rows of this group
+    __device__ __forceinline__ RowGroup() {
+        if (WARP_ROWS) {
+            const int groups = (int)blockDim.x >> 5;
+            t = (int)(threadIdx.x & 31u);
+            size = 32;
+            first = (int64_t)blockIdx.x * groups + (threadIdx.x >> 5);
+            stride = (int64_t)gridDim.x * groups;
+        } else {
+            t = (int)threadIdx.x;
+            size = (int)blockDim.x;
+            first = blockIdx.x;
+            stride = gridDim.x;
+        }
+    }
+    // Sum over the group, the same value in every thread and the same order on
+    // every run.  `slot` alternates between two shared arrays, so that one
+    // barrier per row is enough.
+    __device__ __forceinline__ float sum(float v, float (*red)[32], int slot) const {
+        v = warp_sum(v);
+        if (WARP_ROWS) return v;
+        const int warps = size >> 5;
+        if ((t & 31) == 0) red[slot][t >> 5] = v;
+        __syncthreads();
+        float s = 0.0f;
+        for (int i = 0; i < warps; ++i) s += red[slot][i];
+        return s;
+    }
+};
 
 // Position of scale column j of row r in the 128x4-tiled layout (`tiles` column tiles).
 __device__ __forceinline__ int64_t tiled_scale_at(int64_t r, int j, int tiles) {
     return ((r >> 7) * tiles + (j >> 2)) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (j & 3);
 }
 
-// One row per block; thread t holds the 8-element chunks t, t + B, ... (V of them).
-template <int OUT, int V>
-__global__ void rmsnorm_kernel(const NormArgs a) {
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+// Thread t of a group holds the 8-element chunks t, t + size, ... (V of them).
+template <int OUT, int V, bool WARP_ROWS>
+__global__ void __launch_bounds__(512) rmsnorm_kernel(const NormArgs a) {
     __shared__ float red[2][32];
-    const int B = (int)blockDim.x;
-    const int t = (int)threadIdx.x;
+    const RowGroup<WARP_ROWS> g;
     const int chunks = a.k >> 3;
-    const int64_t row = blockIdx.x;
-    dependency_wait();
-    allow_dependents();
     constexpr bool kMx = OUT == kNormMxRows || OUT == kNormMxTiled;
     const int scale_cols = kMx ? a.k >> 5 : a.k >> 7;
     const int tiles = (scale_cols + 3) >> 2;
-    if (OUT == kNormMxTiled) {
-        // padding of the tiled layout is zero: whole rows past the last one, and the columns that fill up a tile
-        uint8_t* s8 = static_cast<uint8_t*>(a.scales);
-        const int first = row < a.rows ? scale_cols : 0;
-        for (int j = first + t; j < tiles * 4; j += B) s8[tiled_scale_at(row, j, tiles)] = 0;
-        if (row >= a.rows) return;
-    }
-    const int64_t base = row * a.k;
-    float h[V][8];
-    float ss = 0.0f;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    dependency_wait();
+    allow_dependents();
+    uint4 w[V], x[V], r[V];
+    auto fetch = [&](int64_t row) {
+        const int64_t base = row * a.k;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = g.t + v * g.size;
+            const bool ok = row < a.rows && c < chunks;
+            x[v] = ok ? ld_once(a.x + base + c * 8) : zero;
+            r[v] = ok && a.residual ? ld_once(a.residual + base + c * 8) : zero;
+        }
+    };
+    fetch(g.first);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int c = t + v * B;
-        if (c < chunks) {
-            unpack8(ld_once(a.x + base + c * 8), h[v]);
-            if (a.residual) {
-                float r[8];
-                unpack8(ld_once(a.residual + base + c * 8), r);
+        const int c = g.t + v * g.size;
+        w[v] = c < chunks ? *reinterpret_cast<const uint4*>(a.weight + c * 8) : zero;
+    }
+    int slot = 0;
+    for (int64_t row = g.first; row < a.padded_rows; row += g.stride, slot ^= 1) {
+        if (OUT == kNormMxTiled) {
+            // padding of the tiled layout is zero: whole rows past the last one, and the columns that fill up a tile
+            uint8_t* s8 = static_cast<uint8_t*>(a.scales);
+            const int first = row < a.rows ? scale_cols : 0;
+            for (int j = first + g.t; j < tiles * 4; j += g.size) s8[tiled_scale_at(row, j, tiles)] = 0;
+            if (row >= a.rows) continue;
+        }
+        const int64_t base = row * a.k;
+        float h[V][8];
+        float ss = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) h[v][i] = __fadd_rn(h[v][i], r[i]);
-                if (a.sum)
-                    st_stream(a.sum + base + c * 8,
-                              make_uint4(pack_bf16x2(h[v][0], h[v][1]), pack_bf16x2(h[v][2], h[v][3]),
-                                         pack_bf16x2(h[v][4], h[v][5]), pack_bf16x2(h[v][6], h[v][7])));
+        for (int v = 0; v < V; ++v) {
+            unpack8(x[v], h[v]);
+            if (a.residual) {
+                float f[8];
+                unpack8(r[v], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[v][i] = __fadd_rn(h[v][i], f[i]);
+                const int c = g.t + v * g.size;
+                if (a.sum && c < chunks) st_stream(a.sum + base + c * 8, pack8(h[v]));
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = __fmaf_rn(h[v][i], h[v][i], ss);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[v][i] = 0.0f;
         }
-    }
-    const float mean = block_sum(ss, red, 0) / (float)a.k;
-    const float rstd = 1.0f / sqrtf(mean + a.eps);
-    if (t == 0 && a.rstd) a.rstd[row] = rstd;
+        fetch(row + g.stride);
+        const float mean = g.sum(ss, red, slot) / (float)a.k;
+        const float rstd = 1.0f / sqrtf(mean + a.eps);
+        if (g.t == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = t + v * B;
-        const bool ok = c < chunks;
-        float y[8], w[8];
-        unpack8(ok ? *reinterpret_cast<const uint4*>(a.weight + c * 8) : make_uint4(0, 0, 0, 0), w);
-        float m = 0.0f;
+        for (int v = 0; v < V; ++v) {
+            const int c = g.t + v * g.size;
+            const bool ok = c < chunks;
+            float y[8], f[8];
+            unpack8(w[v], f);
+            float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            y[i] = __fmul_rn(__fmul_rn(h[v][i], rstd), w[i]);
-            m = fmaxf(m, fabsf(y[i]));
-        }
-        if (ok && a.y)
-            st_stream(a.y + base + c * 8, make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                     pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])));
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        float q[8];
-        if (kMx) {
-            const int E = (int)(__float_as_uint(m) >> 23);
-            const int e8 = E > 8 ? E - 8 : 0;
-            const float factor = __uint_as_float((uint32_t)(254 - e8) << 23);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(y[i], factor);
-            if (ok && (c & 3) == 0) {
-                uint8_t* s8 = static_cast<uint8_t*>(a.scales);
-                const int j = c >> 2;
-                if (OUT == kNormMxRows)
-                    s8[row * scale_cols + j] = (uint8_t)e8;
-                else
-                    s8[tiled_scale_at(row, j, tiles)] = (uint8_t)e8;
+            for (int i = 0; i < 8; ++i) {
+                y[i] = __fmul_rn(__fmul_rn(h[v][i], rstd), f[i]);
+                m = fmaxf(m, fabsf(y[i]));
             }
-            if (ok)
-                st_stream(a.codes + base + c * 8, make_uint2(cvt_fp8x4<kE4M3>(q[0], q[1], q[2], q[3]),
-                                                             cvt_fp8x4<kE4M3>(q[4], q[5], q[6], q[7])));
-        } else {
-            constexpr int FMT = OUT == kNormE5M2 ? kE5M2 : kE4M3;
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
-            const float s = block_scale<FMT>(m);
-            block_quotients<2, 8>(y, s, q);
-            if (ok && (c & 15) == 0) static_cast<float*>(a.scales)[row * scale_cols + (c >> 4)] = s;
-            if (ok)
-                st_stream(a.codes + base + c * 8, make_uint2(cvt_fp8x4<FMT>(q[0], q[1], q[2], q[3]),
-                                                             cvt_fp8x4<FMT>(q[4], q[5], q[6], q[7])));
+            if (ok && a.y) st_stream(a.y + base + c * 8, pack8(y));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            float q[8];
+            if (kMx) {
+                const int E = (int)(__float_as_uint(m) >> 23);
+                const int e8 = E > 8 ? E - 8 : 0;
+                const float factor = __uint_as_float((uint32_t)(254 - e8) << 23);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(y[i], factor);
+                if (ok && (c & 3) == 0) {
+                    uint8_t* s8 = static_cast<uint8_t*>(a.scales);
+                    const int j = c >> 2;
+                    if (OUT == kNormMxRows)
+                        s8[row * scale_cols + j] = (uint8_t)e8;
+                    else
+                        s8[tiled_scale_at(row, j, tiles)] = (uint8_t)e8;
+                }
+                if (ok)
+                    st_stream(a.codes + base + c * 8, make_uint2(cvt_fp8x4<kE4M3>(q[0], q[1], q[2], q[3]),
+                                                                 cvt_fp8x4<kE4M3>(q[4], q[5], q[6], q[7])));
+            } else {
+                constexpr int FMT = OUT == kNormE5M2 ? kE5M2 : kE4M3;
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+                const float s = block_scale<FMT>(m);
+                block_quotients<2, 8>(y, s, q);
+                if (ok && (c & 15) == 0) static_cast<float*>(a.scales)[row * scale_cols + (c >> 4)] = s;
+                if (ok)
+                    st_stream(a.codes + base + c * 8, make_uint2(cvt_fp8x4<FMT>(q[0], q[1], q[2], q[3]),
+                                                                 cvt_fp8x4<FMT>(q[4], q[5], q[6], q[7])));
+            }
         }
     }
 }
 
 // ------------------------------------------------------------- gradient ----
 //   g = dy * w;  xhat = h * rstd;  dx = rstd * (g - xhat * mean(g * xhat)) + dsum;  dw = sum over rows of dy * xhat
-// Blocks walk over the rows with a fixed stride, each thread keeps dw of its
-// own columns in registers; the blocks' partial sums are joined in block order
-// by a second kernel, so the result does not depend on timing.
+// Each thread keeps dw of its own columns in registers over all its rows; the
+// blocks' partial sums are joined in a fixed order by a second kernel, so the
+// result does not depend on timing.
 struct NormGradArgs {
     const uint16_t* dy;
     const uint16_t* h;
@@ -168,107 +207,166 @@ struct NormGradArgs {
     const float* rstd;
     const uint16_t* dsum;       // or NULL
     uint16_t* dx;
-    float* partial;             // [gridDim.x][k]
+    float* partial;             // [blocks][k]
     int64_t rows;
     int k;
 };
 
-template <int V>
-__global__ void rmsnorm_backward_kernel(const NormGradArgs a) {
+template <int V, bool WARP_ROWS>
+__global__ void __launch_bounds__(512) rmsnorm_backward_kernel(const NormGradArgs a) {
+    // four chunks per thread leave no registers for the next row
+    constexpr bool kAhead = V < 4;
     __shared__ float red[2][32];
-    const int B = (int)blockDim.x;
-    const int t = (int)threadIdx.x;
+    __shared__ float joined[WARP_ROWS ? kNormWarps * V * 256 : 1];
+    const RowGroup<WARP_ROWS> g;
     const int chunks = a.k >> 3;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
     dependency_wait();
     allow_dependents();
+    uint4 w[V], dy_next[V], h_next[V], ds_next[V];
+    float rstd_next = 0.0f;
+    auto fetch = [&](int64_t row) {
+        const int64_t base = row * a.k;
+        rstd_next = row < a.rows ? a.rstd[row] : 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = g.t + v * g.size;
+            const bool ok = row < a.rows && c < chunks;
+            dy_next[v] = ok ? ld_once(a.dy + base + c * 8) : zero;
+            h_next[v] = ok ? ld_once(a.h + base + c * 8) : zero;
+            ds_next[v] = ok && a.dsum ? ld_once(a.dsum + base + c * 8) : zero;
+        }
+    };
+    if (kAhead) fetch(g.first);
     float dw[V][8];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+        const int c = g.t + v * g.size;
+        w[v] = c < chunks ? *reinterpret_cast<const uint4*>(a.weight + c * 8) : zero;
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[v][i] = 0.0f;
+    }
     int slot = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, slot ^= 1) {
+    for (int64_t row = g.first; row < a.rows; row += g.stride, slot ^= 1) {
         const int64_t base = row * a.k;
-        const float rstd = a.rstd[row];
-        float g[V][8], xh[V][8];
+        if (!kAhead) fetch(row);
+        // the row stays packed; xhat and g are formed again after the sum (cheaper than 16 registers per chunk)
+        const float rstd = rstd_next;
+        uint4 dy[V], h[V], ds[V];
         float dot = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = t + v * B;
-            if (c < chunks) {
-                float dy[8], w[8];
-                unpack8(ld_once(a.dy + base + c * 8), dy);
-                unpack8(ld_once(a.h + base + c * 8), xh[v]);
-                unpack8(*reinterpret_cast<const uint4*>(a.weight + c * 8), w);
+            dy[v] = dy_next[v];
+            h[v] = h_next[v];
+            ds[v] = ds_next[v];
+            float d[8], x[8], f[8];
+            unpack8(dy[v], d);
+            unpack8(h[v], x);
+            unpack8(w[v], f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    xh[v][i] = __fmul_rn(xh[v][i], rstd);
-                    dw[v][i] = __fmaf_rn(dy[i], xh[v][i], dw[v][i]);
-                    g[v][i] = __fmul_rn(dy[i], w[i]);
-                    dot = __fmaf_rn(g[v][i], xh[v][i], dot);
-                }
+            for (int i = 0; i < 8; ++i) {
+                x[i] = __fmul_rn(x[i], rstd);
+                dw[v][i] = __fmaf_rn(d[i], x[i], dw[v][i]);
+                dot = __fmaf_rn(__fmul_rn(d[i], f[i]), x[i], dot);
             }
         }
-        const float mean = block_sum(dot, red, slot) / (float)a.k;
+        if (kAhead) fetch(row + g.stride);
+        const float mean = g.sum(dot, red, slot) / (float)a.k;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = t + v * B;
-            if (c < chunks) {
-                float d[8];
+            const int c = g.t + v * g.size;
+            float d[8], x[8], f[8], add[8];
+            unpack8(dy[v], d);
+            unpack8(h[v], x);
+            unpack8(w[v], f);
+            unpack8(ds[v], add);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] = __fmul_rn(rstd, __fmaf_rn(-xh[v][i], mean, g[v][i]));
-                if (a.dsum) {
-                    float r[8];
-                    unpack8(ld_once(a.dsum + base + c * 8), r);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) d[i] = __fadd_rn(d[i], r[i]);
-                }
-                st_stream(a.dx + base + c * 8, make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]),
-                                                          pack_bf16x2(d[4], d[5]), pack_bf16x2(d[6], d[7])));
+            for (int i = 0; i < 8; ++i) {
+                d[i] = __fmul_rn(rstd, __fmaf_rn(-__fmul_rn(x[i], rstd), mean, __fmul_rn(d[i], f[i])));
+                if (a.dsum) d[i] = __fadd_rn(d[i], add[i]);
             }
+            if (c < chunks) st_stream(a.dx + base + c * 8, pack8(d));
         }
     }
+    float* out = a.partial + (int64_t)blockIdx.x * a.k;
+    if (WARP_ROWS) {
+        // the block's warps hold the same columns: joined here, in warp order
+        float* mine = joined + (threadIdx.x >> 5) * (V * 256);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = t + v * B;
-        if (c < chunks) {
-            float4* p = reinterpret_cast<float4*>(a.partial + (int64_t)blockIdx.x * a.k + c * 8);
-            p[0] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
-            p[1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mine[(g.t + v * 32) * 8 + i] = dw[v][i];
+        __syncthreads();
+        for (int c = (int)threadIdx.x; c < a.k; c += (int)blockDim.x) {
+            float sum = joined[c];
+#pragma unroll
+            for (int i = 1; i < kNormWarps; ++i) sum += joined[i * (V * 256) + c];
+            out[c] = sum;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = g.t + v * g.size;
+            if (c < chunks) {
+                float4* p = reinterpret_cast<float4*>(out + c * 8);
+                p[0] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
+                p[1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+            }
         }
     }
 }
 
-// dweight[c] = sum over b of partial[b][c]: 32 columns per block, the warps
-// take every 8th partial row and are joined in warp order.
-constexpr int kJoinWarps = 8;
+// dweight[c] = sum over b of partial[b][c]: 32 columns per block, warp i takes
+// the partial rows i, i + 32, ... and the warps are joined in warp order.
+constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(kJoinWarps * 32)
 rmsnorm_join_kernel(const float* __restrict__ partial, int parts, int k, float* __restrict__ dweight) {
-    __shared__ float red[kJoinWarps][32];
+    __shared__ float red[kJoinWarps][33];
     const int lane = (int)(threadIdx.x & 31u), warp = (int)(threadIdx.x >> 5);
     const int c = (int)blockIdx.x * 32 + lane;
     dependency_wait();
     allow_dependents();
     float s = 0.0f;
-    if (c < k)
-        for (int b = warp; b < parts; b += kJoinWarps) s += partial[(int64_t)b * k + c];
+#pragma unroll 4
+    for (int b = warp; b < parts; b += kJoinWarps) s += partial[(int64_t)b * k + c];
     red[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && c < k) {
-        s = red[0][lane];
-#pragma unroll
-        for (int i = 1; i < kJoinWarps; ++i) s += red[i][lane];
-        dweight[c] = s;
-    }
+    s = warp_sum(red[lane][warp]);          // column `warp` of the block, lane = warp that summed it
+    if (lane == 0) dweight[(int64_t)blockIdx.x * 32 + warp] = s;
 }
 
 constexpr int kNormMaxK = 16384;          // 512 threads of 4 chunks: what their registers allow
 
-// Threads and chunks per thread for a row of `chunks` 8-element chunks.
-static void norm_shape(int chunks, int* threads, int* v) {
-    *v = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4;
-    const int t = (chunks + *v - 1) / *v;
-    *threads = (t + 31) / 32 * 32;
+// How a call's rows are shared out (see RowGroup).
+struct NormShape {
+    bool warp_rows;
+    int v;                      // chunks per thread
+    int threads;                // of a block
+    int groups;                 // row groups per block
+};
+// Rows of up to 128 chunks (k <= 1024) go to single warps.  Longer ones take a
+// block of as many threads as `v` chunks per thread need; with few rows a
+// block has one chunk per thread, as latency counts and nothing else runs.
+static NormShape norm_shape(int chunks, int64_t rows, int most_v) {
+    if (chunks <= 32) return {true, 1, kNormWarps * 32, kNormWarps};
+    if (chunks <= 32 * most_v) return {true, most_v, kNormWarps * 32, kNormWarps};
+    const bool few = rows <= 2 * (int64_t)sm_count() && chunks <= 512;
+    const int v = few ? 1 : chunks <= 512 * most_v ? most_v : 4;
+    const int per = (chunks + v - 1) / v;
+    return {false, v, (per + 31) / 32 * 32, 1};
+}
+
+// Blocks that are resident on the device at once, for each block size of a kernel.
+struct ShapeCache {
+    KernelCache by_warps[16];
+};
+template <class K>
+static fp8q_status_t resident_grid(ShapeCache& sc, K kernel, const NormShape& sh, int64_t rows, unsigned* grid) {
+    int resident = 0;
+    const fp8q_status_t st = prepare_kernel(sc.by_warps[sh.threads / 32 - 1], kernel, sh.threads, 0, 0, &resident);
+    if (st != FP8Q_OK) return st;
+    *grid = grid_for((size_t)((rows + sh.groups - 1) / sh.groups), resident);
+    return FP8Q_OK;
 }
 
 }  // namespace fp8q
@@ -276,6 +374,20 @@ static void norm_shape(int chunks, int* threads, int* v) {
 using namespace fp8q;
 
 namespace fp8q {
+
+template <int OUT, int V, bool WARP_ROWS>
+static fp8q_status_t norm_go(const NormShape& sh, const NormArgs& a, cudaStream_t stream) {
+    static ShapeCache sc;
+    unsigned grid;
+    const fp8q_status_t st = resident_grid(sc, rmsnorm_kernel<OUT, V, WARP_ROWS>, sh, a.padded_rows, &grid);
+    if (st != FP8Q_OK) return st;
+    return launch(rmsnorm_kernel<OUT, V, WARP_ROWS>, grid, (unsigned)sh.threads, 0, stream, a);
+}
+template <int OUT>
+static fp8q_status_t norm_go(const NormShape& sh, const NormArgs& a, cudaStream_t stream) {
+    if (sh.warp_rows) return sh.v == 1 ? norm_go<OUT, 1, true>(sh, a, stream) : norm_go<OUT, 4, true>(sh, a, stream);
+    return sh.v == 1 ? norm_go<OUT, 1, false>(sh, a, stream) : norm_go<OUT, 4, false>(sh, a, stream);
+}
 
 static fp8q_status_t norm_launch(int out, const NormArgs& a, size_t scale_bytes, cudaStream_t stream) {
     const size_t n = (size_t)a.rows * (size_t)a.k;
@@ -295,17 +407,12 @@ static fp8q_status_t norm_launch(int out, const NormArgs& a, size_t scale_bytes,
             any_alias(&s, 1, outs, 4) || overlaps(s.p, s.bytes, a.weight, 2 * (size_t)a.k))
             return FP8Q_ERR_ALIAS;
     }
-    int threads, v;
-    norm_shape(a.k >> 3, &threads, &v);
-    const unsigned grid = (unsigned)a.padded_rows;
-    auto go = [&](auto k1, auto k2, auto k4) {
-        return launch(v == 1 ? k1 : v == 2 ? k2 : k4, grid, (unsigned)threads, 0, stream, a);
-    };
+    const NormShape sh = norm_shape(a.k >> 3, a.rows, 4);
     switch (out) {
-        case kNormE4M3: return go(rmsnorm_kernel<kNormE4M3, 1>, rmsnorm_kernel<kNormE4M3, 2>, rmsnorm_kernel<kNormE4M3, 4>);
-        case kNormE5M2: return go(rmsnorm_kernel<kNormE5M2, 1>, rmsnorm_kernel<kNormE5M2, 2>, rmsnorm_kernel<kNormE5M2, 4>);
-        case kNormMxRows: return go(rmsnorm_kernel<kNormMxRows, 1>, rmsnorm_kernel<kNormMxRows, 2>, rmsnorm_kernel<kNormMxRows, 4>);
-        default: return go(rmsnorm_kernel<kNormMxTiled, 1>, rmsnorm_kernel<kNormMxTiled, 2>, rmsnorm_kernel<kNormMxTiled, 4>);
+        case kNormE4M3: return norm_go<kNormE4M3>(sh, a, stream);
+        case kNormE5M2: return norm_go<kNormE5M2>(sh, a, stream);
+        case kNormMxRows: return norm_go<kNormMxRows>(sh, a, stream);
+        default: return norm_go<kNormMxTiled>(sh, a, stream);
     }
 }
 
@@ -350,15 +457,25 @@ extern "C" fp8q_status_t mxfp8_rmsnorm_quantize(const void* x_bf16, const void* 
                        reinterpret_cast<cudaStream_t>(stream));
 }
 
-// Blocks of the gradient kernel, and so rows of its workspace.
-static int64_t norm_backward_blocks(int64_t rows) {
-    const int64_t most = (int64_t)sm_count() * 4;
-    return rows < most ? rows : most;
+namespace fp8q {
+
+// The gradient's shape: at most 2 chunks per thread while 512 threads are
+// enough (a chunk needs 40 registers there), and blocks for 1024 threads per SM.
+static NormShape norm_backward_shape(int64_t rows, int64_t k, int64_t* blocks) {
+    const NormShape sh = norm_shape((int)(k >> 3), rows, 2);
+    const int64_t most = (int64_t)sm_count() * (1024 / sh.threads > 0 ? 1024 / sh.threads : 1);
+    const int64_t want = (rows + sh.groups - 1) / sh.groups;
+    *blocks = want < most ? want : most;
+    return sh;
 }
+
+}  // namespace fp8q
 
 extern "C" size_t fp8q_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t k) {
     if (norm_sizes(rows, k, MXFP8_BLOCK, 0.0f) != FP8Q_OK) return 0;
-    return (size_t)norm_backward_blocks(rows) * (size_t)k * sizeof(float);
+    int64_t blocks;
+    norm_backward_shape(rows, k, &blocks);
+    return (size_t)blocks * (size_t)k * sizeof(float);
 }
 
 extern "C" fp8q_status_t fp8q_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* weight_bf16,
@@ -387,17 +504,18 @@ extern "C" fp8q_status_t fp8q_rmsnorm_backward(const void* dy_bf16, const void* 
                            {dsum_bf16, 2 * n}, {dx_bf16, 2 * n}};
     const Range rest[] = {{dweight, 4 * (size_t)k}, {workspace, need}};
     if (any_alias(rest, 2, whole, 6)) return FP8Q_ERR_ALIAS;
-    const int parts = (int)norm_backward_blocks(rows);
+    int64_t blocks;
+    const NormShape sh = norm_backward_shape(rows, k, &blocks);
+    const int parts = (int)blocks;
     if (rows > 0) {
         const NormGradArgs a = {static_cast<const uint16_t*>(dy_bf16), static_cast<const uint16_t*>(h_bf16),
                                 static_cast<const uint16_t*>(weight_bf16), rstd, static_cast<const uint16_t*>(dsum_bf16),
                                 static_cast<uint16_t*>(dx_bf16), static_cast<float*>(workspace), rows, (int)k};
-        int threads, v;
-        norm_shape((int)(k >> 3), &threads, &v);
-        const fp8q_status_t s1 = launch(v == 1   ? rmsnorm_backward_kernel<1>
-                                        : v == 2 ? rmsnorm_backward_kernel<2>
-                                                 : rmsnorm_backward_kernel<4>,
-                                        (unsigned)parts, (unsigned)threads, 0, cs, a);
+        const auto kernel = sh.warp_rows ? (sh.v == 1 ? rmsnorm_backward_kernel<1, true> : rmsnorm_backward_kernel<2, true>)
+                            : sh.v == 1  ? rmsnorm_backward_kernel<1, false>
+                            : sh.v == 2  ? rmsnorm_backward_kernel<2, false>
+                                         : rmsnorm_backward_kernel<4, false>;
+        const fp8q_status_t s1 = launch(kernel, (unsigned)blocks, (unsigned)sh.threads, 0, cs, a);
         if (s1 != FP8Q_OK) return s1;
     }
     return launch(rmsnorm_join_kernel, (unsigned)((k + 31) / 32), kJoinWarps * 32, 0, cs,
