@@ -199,11 +199,13 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const int total = prefix[a.experts + 1] * a.feature_tiles;
+    // all 512 columns are allocated, so they begin at column 0: a constant that keeps the products' operands uniform
+    constexpr uint32_t tmem = 0;
+    if (tid == 0 && *tmem_slot != tmem) raise_error(kErrProductTimeout);
+    const int total = *tmem_slot == tmem ? prefix[a.experts + 1] * a.feature_tiles : 0;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             // copies: weights, rows and weight scales
             int it = 0;
             bool ok = true;
@@ -246,7 +248,8 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
+            const uint32_t st0 = operand_desc(smem_addr(smem)), sc0 = scale_desc(smem_addr(sscale));
             int it = 0, tile = 0;
             bool ok = true;
             for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
@@ -265,20 +268,20 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                     }
                     tc_fence_after();
                     fence_proxy_async_smem();   // the scale warp's stores, before the tensor core reads them
-                    const uint32_t st = smem_addr(smem + s * S::kStageBytes);
-                    const uint32_t sc = smem_addr(sscale + s * S::kScaleBytes);
+                    const uint32_t st = st0 + (uint32_t)s * (S::kStageBytes >> 4);
+                    const uint32_t sc = sc0 + (uint32_t)s * (S::kScaleBytes >> 4);
                     const uint32_t tsc = tmem + kMpScaleColumns + (uint32_t)s * 12;
 #pragma unroll
-                    for (int i = 0; i < WT; ++i) tc_copy_scales(tsc + 4 * i, scale_desc(sc + 512 * i));
-                    tc_copy_scales(tsc + 4 * WT, scale_desc(sc + 512 * WT));
-                    if (WT == 1 && d.rows > 128) tc_copy_scales(tsc + 8, scale_desc(sc + 1024));
+                    for (int i = 0; i < WT; ++i) tc_copy_scales(tsc + 4 * i, sc + (512 >> 4) * i);
+                    tc_copy_scales(tsc + 4 * WT, sc + (512 >> 4) * WT);
+                    if (WT == 1 && d.rows > 128) tc_copy_scales(tsc + 8, sc + (1024 >> 4));
 #pragma unroll
                     for (int i = 0; i < WT; ++i)
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            tc_mma_mx(acc + (uint32_t)(i * S::kRows), operand_desc(st + i * 16384 + q * 32),
-                                      operand_desc(st + WT * 16384 + q * 32), mx_instr_step(idesc, q), tsc + 4 * i,
-                                      tsc + 4 * WT, kb > 0 || q > 0);
+                            tc_mma_mx(acc + (uint32_t)(i * S::kRows), st + i * (16384 >> 4) + q * 2,
+                                      st + WT * (16384 >> 4) + q * 2, mx_instr_step(idesc, q), tsc + 4 * i, tsc + 4 * WT,
+                                      kb > 0 || q > 0);
                     tc_commit(&empty[s]);
                 }
                 tc_commit(&acc_full[b]);
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 3) tmem_free(tmem, kMpTmemColumns);
+    if (warp == 3) tmem_free(*tmem_slot, kMpTmemColumns);
 }
 
 unsigned unit_errors_moe_product(bool clear) { return read_unit_errors(clear); }
