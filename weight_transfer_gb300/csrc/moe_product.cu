@@ -19,8 +19,9 @@
 // One CTA per SM walks over the tiles.  Warp 0 copies weights, rows and
 // weight scales by TMA, warp 2 brings the rows' scales into the tensor core's
 // tile order (rows of an expert start anywhere, so their scales cannot lie
-// pre-tiled), warp 1 issues the products, warps 4 to 7 read the accumulators
-// of one tile while the products of the next fill the other half of TMEM.
+// pre-tiled), warp 1 issues the products, warps 4 to 11 read the accumulators
+// of one tile while the products of the next fill the other half of TMEM (two
+// warps for each quarter of the lanes, every other 16 rows each).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -29,7 +30,8 @@
 
 namespace fp8q {
 
-constexpr int kMpThreads = 256;
+constexpr int kMpReaders = 8;                   // warps that read the accumulators
+constexpr int kMpThreads = 128 + 32 * kMpReaders;
 constexpr int kMpStages = 4;
 constexpr int kMpMaxExperts = 1024;
 constexpr int kMpRowBoxes = 4;                  // row boxes of 128, 64, 32 and 16 rows
@@ -44,8 +46,9 @@ template <int WT> struct MpShape {
     static constexpr int kStageBytes = WT * 16384 + kRows * 128;
     static constexpr int kScaleBytes = WT * 512 + 1024;
     static constexpr int kBars = 2 * kMpStages + 4;
-    static constexpr size_t kSmem = (size_t)kMpStages * (kStageBytes + kScaleBytes) + kBars * 8 + 16 +
-                                    (kMpMaxExperts + 2) * 4 + 1024 + 4 * 1024;
+    static constexpr int kOutBytes = WT == 1 ? kMpReaders * 2048 : 0;    // two 16-row staging areas per reading warp
+    static constexpr size_t kSmem = (size_t)kMpStages * (kStageBytes + kScaleBytes) + kOutBytes + kBars * 8 + 16 +
+                                    2 * (kMpMaxExperts + 2) * 4 + 1024;
 };
 
 struct MpArgs {
@@ -57,51 +60,64 @@ struct MpArgs {
     uint16_t* out_bf16;                         // matmul
     uint8_t* out_codes;                         // swiglu
     uint8_t* out_scales;
-    int64_t rows_total;
+    int rows_total;
     int experts, n, k;
     int feature_tiles, k_steps;                 // ceil(n / 128), ceil(k / 128)
 };
 
-struct MpTile {
-    int e;                                      // expert, or `experts` for rows of no expert (written as zeros)
-    int f;                                      // first feature
-    int64_t r0;                                 // first row
-    int rows;                                   // valid rows, 0 if none
-};
+// The tiles of one CTA, in the order in which every warp of it walks over
+// them.  Both tables are in shared memory: row_start[e] is the first row of
+// expert e (row_start[experts] the first row of no expert, row_start[experts +
+// 1] = rows), prefix[e] the number of row tiles before it.
+struct MpTiles {
+    const int* prefix;
+    const int* row_start;
+    int experts, feature_tiles;
+    int step_rt, step_f;                        // one grid further
+    int rt, ft;                                 // row tile and feature tile
+    int e, end;                                 // expert (`experts`: rows of none, written as zeros), its last row tile + 1
+    int per;                                    // rows of its full tiles
+    int r0, rows;                               // first row and number of rows of the tile
 
-__device__ __forceinline__ int64_t mp_offset(const MpArgs& a, int e) {
-    const int64_t o = a.offsets[e];
-    return o < 0 ? 0 : o > a.rows_total ? a.rows_total : o;
-}
-__device__ __forceinline__ void mp_span(const MpArgs& a, int e, int64_t* lo, int64_t* hi) {
-    *lo = mp_offset(a, e);
-    *hi = e < a.experts ? mp_offset(a, e + 1) : a.rows_total;
-    if (*hi < *lo) *hi = *lo;
-}
-
-// prefix[e] = row tiles of the experts before e; prefix[experts + 1] = all of them.
-__device__ __forceinline__ MpTile mp_tile(const MpArgs& a, const int* prefix, int max_rows, int t) {
-    MpTile d;
-    const int rt = t / a.feature_tiles;
-    d.f = (t - rt * a.feature_tiles) * 128;
-    int lo = 0, hi = a.experts;                 // the last e with prefix[e] <= rt
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] <= rt) lo = mid; else hi = mid - 1;
+    __device__ __forceinline__ MpTiles(const MpArgs& a, const int* prefix_, const int* row_start_)
+        : prefix(prefix_), row_start(row_start_), experts(a.experts), feature_tiles(a.feature_tiles) {
+        rt = (int)blockIdx.x / feature_tiles;
+        ft = (int)blockIdx.x - rt * feature_tiles;
+        step_rt = (int)gridDim.x / feature_tiles;
+        step_f = (int)gridDim.x - step_rt * feature_tiles;
+        e = -1;
+        end = 0;
     }
-    d.e = lo;
-    int64_t begin, end;
-    mp_span(a, lo, &begin, &end);
-    const int64_t count = end - begin;
-    const int64_t tiles = (count + max_rows - 1) / max_rows;
-    // equal tiles, in steps of 16 rows: fewer, fuller columns than full tiles and a rest
-    const int64_t per = tiles > 0 ? ((count + tiles - 1) / tiles + 15) / 16 * 16 : 0;
-    const int64_t i = rt - prefix[lo];
-    d.r0 = begin + i * per;
-    const int64_t left = i < 0 ? 0 : count - i * per;
-    d.rows = (int)(left < 0 ? 0 : left < per ? left : per);
-    return d;
-}
+    // Resolves the current tile; false if there is none left.
+    __device__ __forceinline__ bool here() {
+        if (rt >= prefix[experts + 1]) return false;
+        if (rt >= end) {
+            int lo = e + 1, hi = experts;       // the last expert with prefix[.] <= rt
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (prefix[mid] <= rt) lo = mid; else hi = mid - 1;
+            }
+            e = lo;
+            end = prefix[e + 1];
+            const int tiles = end - prefix[e];
+            // equal tiles, in steps of 16 rows: fewer, fuller columns than full tiles and a rest
+            per = ((row_start[e + 1] - row_start[e] + tiles - 1) / tiles + 15) & ~15;
+        }
+        r0 = row_start[e] + (rt - prefix[e]) * per;
+        const int left = row_start[e + 1] - r0;
+        rows = left < per ? left : per;
+        return true;
+    }
+    __device__ __forceinline__ void next() {
+        rt += step_rt;
+        ft += step_f;
+        if (ft >= feature_tiles) {
+            ft -= feature_tiles;
+            ++rt;
+        }
+    }
+    __device__ __forceinline__ bool none() const { return e >= experts; }
+};
 
 // The four E8M0 bytes of one row for K step kb (128 columns); bytes past k are 0.
 __device__ __forceinline__ uint32_t row_scale_word(const uint8_t* row, int kb, int cols) {
@@ -152,13 +168,14 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
     extern __shared__ __align__(128) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* sscale = smem + kMpStages * S::kStageBytes;
-    uint8_t* sout = sscale + kMpStages * S::kScaleBytes;            // 1 KB per reading warp
-    uint64_t* full = reinterpret_cast<uint64_t*>(sout + 4 * 1024);
+    uint8_t* sout = sscale + kMpStages * S::kScaleBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sout + S::kOutBytes);
     uint64_t* empty = full + kMpStages;
     uint64_t* acc_full = empty + kMpStages;
     uint64_t* acc_empty = acc_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     int* prefix = reinterpret_cast<int*>(tmem_slot + 4);
+    int* row_start = prefix + kMpMaxExperts + 2;
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -168,7 +185,7 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 4);
+            mbar_init(&acc_empty[b], kMpReaders);
         }
         fence_barrier_init();
     }
@@ -176,25 +193,33 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
     dependency_wait();
     allow_dependents();
     if (warp == 0) {
-        int run = 0;
-        for (int e0 = 0; e0 <= a.experts; e0 += 32) {
+        // the offsets, taken into 0 .. rows and not decreasing, whatever they hold; then the tiles before each expert
+        int top = 0, run = 0;
+        for (int e0 = 0; e0 <= a.experts + 1; e0 += 32) {
             const int e = e0 + lane;
-            int tiles = 0;
-            if (e <= a.experts) {
-                int64_t lo, hi;
-                mp_span(a, e, &lo, &hi);
-                tiles = (int)((hi - lo + S::kRows - 1) / S::kRows);
-            }
-            int incl = tiles;
+            int o = e == 0 ? 0 : e <= a.experts ? a.offsets[e] : a.rows_total;
+            o = max(0, min(o, a.rows_total));
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-                if (lane >= d) incl += o;
+                const int q = __shfl_up_sync(0xFFFFFFFFu, o, d);
+                if (lane >= d) o = max(o, q);
             }
-            if (e <= a.experts) prefix[e + 1] = run + incl;
+            o = max(o, top);
+            int before = __shfl_up_sync(0xFFFFFFFFu, o, 1);
+            if (lane == 0) before = top;
+            top = __shfl_sync(0xFFFFFFFFu, o, 31);
+            int incl = (o - before + S::kRows - 1) / S::kRows;      // row tiles of expert e - 1
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int q = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                if (lane >= d) incl += q;
+            }
+            if (e <= a.experts + 1) {
+                row_start[e] = o;
+                prefix[e] = run + incl;
+            }
             run += __shfl_sync(0xFFFFFFFFu, incl, 31);
         }
-        if (lane == 0) prefix[0] = 0;
     }
     tc_fence_before();
     __syncthreads();
@@ -202,19 +227,19 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
     // all 512 columns are allocated, so they begin at column 0: a constant that keeps the products' operands uniform
     constexpr uint32_t tmem = 0;
     if (tid == 0 && *tmem_slot != tmem) raise_error(kErrProductTimeout);
-    const int total = *tmem_slot == tmem ? prefix[a.experts + 1] * a.feature_tiles : 0;
+    if (*tmem_slot != tmem) prefix[a.experts + 1] = 0;         // no tiles
+    MpTiles d(a, prefix, row_start);
 
     if (warp == 0) {
         if (elect_one()) {
             // copies: weights, rows and weight scales
             int it = 0;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-                const MpTile d = mp_tile(a, prefix, S::kRows, t);
-                if (d.e >= a.experts || d.rows <= 0) continue;
+            for (; ok && d.here(); d.next()) {
+                if (d.none()) continue;
                 const int n16 = (d.rows + 15) >> 4;
                 const uint32_t bytes = WT * (16384 + 512) + n16 * 2048;
-                const int64_t scale_tile = ((int64_t)d.e * a.feature_tiles + (d.f >> 7)) * a.k_steps;
+                const int64_t scale_tile = ((int64_t)d.e * a.feature_tiles + d.ft) * a.k_steps;
                 for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
                     const int s = it % kMpStages;
                     if (!mp_wait(&empty[s], (uint32_t)((it / kMpStages) & 1) ^ 1u)) {
@@ -225,7 +250,7 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                     mbar_arrive_expect_tx(&full[s], bytes);
 #pragma unroll
                     for (int i = 0; i < WT; ++i) {
-                        tma_3d_g2s(st + i * 16384, &a.w[i], kb * 128, d.f, d.e, &full[s]);
+                        tma_3d_g2s(st + i * 16384, &a.w[i], kb * 128, d.ft * 128, d.e, &full[s]);
                         bulk_g2s(sscale + s * S::kScaleBytes + i * 512, a.w_scales[i] + (scale_tile + kb) * 512, 512, &full[s]);
                     }
                     int at = 0;
@@ -233,7 +258,7 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                     for (int b = 0; b < kMpRowBoxes; ++b) {
                         const int h = 128 >> b;
                         if (n16 & (h >> 4)) {
-                            tma_2d_g2s(st + WT * 16384 + at * 128, &a.rows[b], kb * 128, (int)(d.r0 + at), &full[s]);
+                            tma_2d_g2s(st + WT * 16384 + at * 128, &a.rows[b], kb * 128, d.r0 + at, &full[s]);
                             at += h;
                         }
                     }
@@ -252,9 +277,8 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
             const uint32_t st0 = operand_desc(smem_addr(smem)), sc0 = scale_desc(smem_addr(sscale));
             int it = 0, tile = 0;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-                const MpTile d = mp_tile(a, prefix, S::kRows, t);
-                if (d.e >= a.experts || d.rows <= 0) continue;
+            for (; ok && d.here(); d.next()) {
+                if (d.none()) continue;
                 const int b = tile & 1;
                 const uint32_t idesc = mx_instr_desc((d.rows + 15) & ~15);
                 const uint32_t acc = tmem + (uint32_t)b * kMpAccColumns;
@@ -295,10 +319,9 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
         const bool words = (cols & 3) == 0;
         int it = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-            const MpTile d = mp_tile(a, prefix, S::kRows, t);
-            if (d.e >= a.experts || d.rows <= 0) continue;
-            const uint8_t* base = a.row_scales + d.r0 * cols;
+        for (; ok && d.here(); d.next()) {
+            if (d.none()) continue;
+            const uint8_t* base = a.row_scales + (int64_t)d.r0 * cols;
             constexpr int kWords = (S::kRows + 31) / 32;
             for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
                 const int s = it % kMpStages;
@@ -329,45 +352,47 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
         }
         cp_async_wait_all();                    // none of this warp's copies outlives the block, whatever stopped it
     } else if (warp >= 4) {
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         int tile = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x) {
-            const MpTile d = mp_tile(a, prefix, S::kRows, t);
-            const bool zero = d.e >= a.experts;
-            if (d.rows <= 0) continue;
+        for (; d.here(); d.next()) {
+            const bool zero = d.none();
             const int b = tile & 1;
             if (!zero) {
                 if (!__all_sync(0xFFFFFFFFu, mp_wait(&acc_full[b], (uint32_t)((tile >> 1) & 1)))) break;
                 tc_fence_after();
             }
             const uint32_t acc = tmem + (uint32_t)b * kMpAccColumns + lanes;
+            const int f0 = d.ft * 128 + quarter * 32;
+            const int64_t r0 = d.r0;
             if (WT == 1) {
-                uint8_t* stage = sout + quarter * 1024;             // [16 rows][32 features] bf16
-                const int f0 = d.f + quarter * 32;
-                for (int c0 = 0; c0 < d.rows; c0 += 16) {
-                    uint32_t lo[8], hi[8];                          // features 0..15 and 16..31 of the warp
-                    if (!zero) {
-                        tmem_load_16x256b_x2(acc + c0, lo);
-                        tmem_load_16x256b_x2(acc + (16u << 16) + c0, hi);
-                        tmem_load_wait();
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) lo[i] = hi[i] = 0u;
+                int area = 0;
+                uint32_t lo[8], hi[8];                              // features 0..15 and 16..31 of the warp
+                const auto fetch = [&](int c) {
+                    if (!zero && c < d.rows) {
+                        tmem_load_16x256b_x2(acc + c, lo);
+                        tmem_load_16x256b_x2(acc + (16u << 16) + c, hi);
                     }
+                };
+#pragma unroll
+                for (int i = 0; i < 8; ++i) lo[i] = hi[i] = 0u;
+                fetch(half * 16);
+                for (int c0 = half * 16; c0 < d.rows; c0 += 32, area ^= 1024) {
+                    uint8_t* stage = sout + (warp - 4) * 2048 + area;   // [16 rows][32 features] bf16
                     // register pair i of `lo` holds rows c0 + 8 * (i / 2) + 2 * (lane % 4) + {0, 1} of feature
                     // lane / 4 + 8 * (i % 2); stored transposed, 8 features are 16 bytes of an output row
+                    tmem_load_wait(lo, hi);
+                    uint32_t m[2][4];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t m[4];
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            m[i] = pack_bf16x2(__uint_as_float(lo[4 * h + 2 * i]), __uint_as_float(lo[4 * h + 2 * i + 1]));
-                            m[2 + i] = pack_bf16x2(__uint_as_float(hi[4 * h + 2 * i]), __uint_as_float(hi[4 * h + 2 * i + 1]));
+                            m[h][i] = pack_bf16x2(__uint_as_float(lo[4 * h + 2 * i]), __uint_as_float(lo[4 * h + 2 * i + 1]));
+                            m[h][2 + i] = pack_bf16x2(__uint_as_float(hi[4 * h + 2 * i]), __uint_as_float(hi[4 * h + 2 * i + 1]));
                         }
-                        const int r = 8 * h + (lane & 7), chunk = lane >> 3;
-                        stmatrix_x4_trans(stage + out_stage_at(r, chunk), m);
-                    }
+                    fetch(c0 + 32);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) stmatrix_x4_trans(stage + out_stage_at(8 * h + (lane & 7), lane >> 3), m[h]);
                     __syncwarp();
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -375,33 +400,35 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                         const uint4 v = *reinterpret_cast<const uint4*>(stage + out_stage_at(r, chunk));
                         const int ff = f0 + chunk * 8;
                         if (c0 + r < d.rows && ff < a.n) {
-                            uint16_t* o = a.out_bf16 + (d.r0 + c0 + r) * a.n + ff;
+                            uint16_t* o = a.out_bf16 + (r0 + c0 + r) * a.n + ff;
                             if ((a.n & 7) == 0)
                                 *reinterpret_cast<uint4*>(o) = v;
                             else
                                 st_u16_tail(o, &v.x, 4, a.n - ff);
                         }
                     }
-                    __syncwarp();
                 }
+                __syncwarp();                                       // both areas free for the next tile
             } else {
                 // fragment order (see tmem_load_16x256b_x2): this lane holds rows c0 + 8 h + 2 q + j of features
                 // p + 8 i, q = lane % 4, p = lane / 4; the 8 lanes of one q hold the 32 features of their rows
                 const int q4 = lane & 3, p = lane >> 2;
-                const int f0 = d.f + quarter * 32;
                 const int64_t scale_cols = a.n >> 5;
-                for (int c0 = 0; c0 < d.rows; c0 += 16) {
-                    uint32_t g[2][8], u[2][8];
-                    if (!zero) {
-                        tmem_load_16x256b_x2(acc + c0, g[0]);
-                        tmem_load_16x256b_x2(acc + (16u << 16) + c0, g[1]);
-                        tmem_load_16x256b_x2(acc + S::kRows + c0, u[0]);
-                        tmem_load_16x256b_x2(acc + (16u << 16) + S::kRows + c0, u[1]);
-                        tmem_load_wait();
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) g[0][i] = g[1][i] = u[0][i] = u[1][i] = 0u;
+                uint32_t g[2][8], u[2][8];
+                const auto fetch = [&](int c) {
+                    if (!zero && c < d.rows) {
+                        tmem_load_16x256b_x2(acc + c, g[0]);
+                        tmem_load_16x256b_x2(acc + (16u << 16) + c, g[1]);
+                        tmem_load_16x256b_x2(acc + S::kRows + c, u[0]);
+                        tmem_load_16x256b_x2(acc + (16u << 16) + S::kRows + c, u[1]);
                     }
+                };
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[0][i] = g[1][i] = u[0][i] = u[1][i] = 0u;
+                fetch(half * 16);
+                for (int c0 = half * 16; c0 < d.rows; c0 += 32) {
+                    tmem_load_wait(g[0], g[1]);
+                    tmem_load_wait(u[0], u[1]);
                     // v[r][i]: row r = 2 h + j of this lane's four, feature p + 8 i
                     float v[4][4];
                     uint32_t top[4];
@@ -415,6 +442,7 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                             top[r] = max(top[r], __float_as_uint(fabsf(v[r][i])));
                         }
                     }
+                    fetch(c0 + 32);
                     // the scale needs the exponent of the block's largest magnitude only: two rows' exponents per word
                     uint32_t ex[2] = {(top[0] >> 23) | (top[1] >> 23 << 16), (top[2] >> 23) | (top[3] >> 23 << 16)};
 #pragma unroll
@@ -439,7 +467,7 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                     transpose_step<1>(w[0], w[1], 8, (p & 2) != 0);
                     transpose_step<1>(w[2], w[3], 8, (p & 2) != 0);
                     if (f0 < a.n) {
-                        const int64_t row0 = d.r0 + c0 + 2 * q4;
+                        const int64_t row0 = r0 + c0 + 2 * q4;
                         const int fo = f0 + 8 * (p & 3) + 4 * (p >> 2);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
@@ -544,7 +572,7 @@ static fp8q_status_t mp_launch(const MpCall& c, cudaStream_t stream) {
     a.out_bf16 = static_cast<uint16_t*>(WT == 1 ? c.out : nullptr);
     a.out_codes = static_cast<uint8_t*>(WT == 2 ? c.out : nullptr);
     a.out_scales = c.out_scales;
-    a.rows_total = c.rows;
+    a.rows_total = (int)c.rows;
     a.experts = c.experts;
     a.n = (int)c.n;
     a.k = (int)c.k;
