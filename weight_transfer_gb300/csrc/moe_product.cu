@@ -16,6 +16,9 @@
 // is a TMEM lane, so that a block of 32 features is one warp and its largest
 // magnitude one warp reduction.
 //
+// With many rows per expert two CTAs work as a pair on 256 features: each
+// holds its own 128 features' weights and half of the rows.
+//
 // One CTA per SM walks over the tiles.  Warp 0 copies weights, rows and
 // weight scales by TMA, warp 2 brings the rows' scales into the tensor core's
 // tile order (rows of an expert start anywhere, so their scales cannot lie
@@ -30,25 +33,31 @@
 
 namespace fp8q {
 
-constexpr int kMpReaders = 8;                   // warps that read the accumulators
-constexpr int kMpThreads = 128 + 32 * kMpReaders;
-constexpr int kMpStages = 4;
 constexpr int kMpMaxExperts = 1024;
-constexpr int kMpRowBoxes = 4;                  // row boxes of 128, 64, 32 and 16 rows
+constexpr int kMpListed = 128;                  // tiles of a CTA that are found ahead (see MpTiles)
+constexpr int kMpRowBoxes = 4;                  // row boxes of 128, 64, 32 and 16 rows, or half of that for pairs
 constexpr uint32_t kMpTmemColumns = 512;
-constexpr uint32_t kMpAccColumns = 224;         // per accumulator half
-constexpr uint32_t kMpScaleColumns = 448;       // scales: 12 columns per stage from here
 constexpr unsigned kErrProductTimeout = 2u;
 
-// WT weight tensors (1: matmul, 2: gate and up), up to kRows rows per tile.
-template <int WT> struct MpShape {
-    static constexpr int kRows = WT == 1 ? 224 : 112;
-    static constexpr int kStageBytes = WT * 16384 + kRows * 128;
+// WT weight tensors (1: matmul, 2: gate and up); PAIR: the work of two CTAs.
+template <int WT, bool PAIR> struct MpShape {
+    static constexpr int kReaders = 8;                                      // warps that read the accumulators
+    static constexpr int kThreads = 128 + 32 * kReaders;
+    static constexpr int kRows = WT == 2 ? 112 : PAIR ? 208 : 224;          // most rows of a tile
+    static constexpr int kHeld = PAIR ? kRows / 2 : kRows;                  // rows of it in this CTA's shared memory
+    static constexpr int kStages = !PAIR ? 4 : WT == 1 ? 6 : 5;
+    static constexpr int kHalves = 2;                                       // tiles whose accumulators fit TMEM
+    static constexpr uint32_t kAccColumns = WT * kRows;                     // of one tile
+    static constexpr uint32_t kScaleBase = kHalves * kAccColumns;           // scales behind them:
+    static constexpr uint32_t kScaleColumns = 4 * WT + (kRows > 128 ? 8 : 4);   // of one stage
+    static_assert(kScaleBase + kStages * kScaleColumns <= kMpTmemColumns, "tensor memory");
+    static constexpr int kStageBytes = WT * 16384 + kHeld * 128;
     static constexpr int kScaleBytes = WT * 512 + 1024;
-    static constexpr int kBars = 2 * kMpStages + 4;
-    static constexpr int kOutBytes = WT == 1 ? kMpReaders * 2048 : 0;    // two 16-row staging areas per reading warp
-    static constexpr size_t kSmem = (size_t)kMpStages * (kStageBytes + kScaleBytes) + kOutBytes + kBars * 8 + 16 +
-                                    2 * (kMpMaxExperts + 2) * 4 + 1024;
+    static constexpr int kOutBytes = WT == 1 ? kReaders * 2048 : 0;       // two 16-row staging areas per reading warp
+    static constexpr int kBars = 2 * kStages + 4;
+    static constexpr size_t kSmem = (size_t)kStages * (kStageBytes + kScaleBytes) + kOutBytes + kBars * 8 + 16 +
+                                    kMpListed * 16 + 2 * (kMpMaxExperts + 2) * 4 + 1024;
+    static_assert(kStageBytes % 1024 == 0 && kSmem <= 232448, "shared memory");
 };
 
 struct MpArgs {
@@ -65,58 +74,60 @@ struct MpArgs {
     int feature_tiles, k_steps;                 // ceil(n / 128), ceil(k / 128)
 };
 
+// A tile: rows r0 .. r0 + rows of expert e (`experts`: rows of no expert, which
+// are written as zeros) and 128 features; rows < 0 behind the last tile.
+struct MpTile {
+    int e, ft, r0, rows;
+};
+
+// Tile number j of this CTA.  Both tables are in shared memory: row_start[e]
+// is the first row of expert e (row_start[experts] the first row of no expert,
+// row_start[experts + 1] = rows), prefix[e] the number of row tiles before it.
+template <bool PAIR>
+__device__ __forceinline__ MpTile mp_find(const MpArgs& a, const int* prefix, const int* row_start, int j) {
+    const int units = PAIR ? (a.feature_tiles + 1) >> 1 : a.feature_tiles;      // feature tiles, or pairs of them
+    const int me = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x, all = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
+    const int64_t t = me + (int64_t)j * all;
+    MpTile d = {0, 0, 0, -1};
+    if (t >= (int64_t)prefix[a.experts + 1] * units) return d;
+    const int rt = (int)(t / units), unit = (int)(t - (int64_t)rt * units);
+    int lo = 0, hi = a.experts;                 // the last expert with prefix[.] <= rt
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= rt) lo = mid; else hi = mid - 1;
+    }
+    const int tiles = prefix[lo + 1] - prefix[lo];
+    // equal tiles, in steps of 16 rows: fewer, fuller columns than full tiles and a rest
+    const int per = ((row_start[lo + 1] - row_start[lo] + tiles - 1) / tiles + 15) & ~15;
+    d.e = lo;
+    d.ft = PAIR ? 2 * unit + (int)cluster_rank() : unit;
+    d.r0 = row_start[lo] + (rt - prefix[lo]) * per;
+    d.rows = min(row_start[lo + 1] - d.r0, per);
+    return d;
+}
+
 // The tiles of one CTA, in the order in which every warp of it walks over
-// them.  Both tables are in shared memory: row_start[e] is the first row of
-// expert e (row_start[experts] the first row of no expert, row_start[experts +
-// 1] = rows), prefix[e] the number of row tiles before it.
+// them.  Finding one takes a search and two divisions, some 700 cycles that a
+// single thread cannot hide (matmul, 65,533 rows: 22 us of 130); so the first
+// kMpListed are found by all threads at once and kept in shared memory.
+template <bool PAIR>
 struct MpTiles {
+    const MpArgs& a;
+    const MpTile* listed;
     const int* prefix;
     const int* row_start;
-    int experts, feature_tiles;
-    int step_rt, step_f;                        // one grid further
-    int rt, ft;                                 // row tile and feature tile
-    int e, end;                                 // expert (`experts`: rows of none, written as zeros), its last row tile + 1
-    int per;                                    // rows of its full tiles
-    int r0, rows;                               // first row and number of rows of the tile
-
-    __device__ __forceinline__ MpTiles(const MpArgs& a, const int* prefix_, const int* row_start_)
-        : prefix(prefix_), row_start(row_start_), experts(a.experts), feature_tiles(a.feature_tiles) {
-        rt = (int)blockIdx.x / feature_tiles;
-        ft = (int)blockIdx.x - rt * feature_tiles;
-        step_rt = (int)gridDim.x / feature_tiles;
-        step_f = (int)gridDim.x - step_rt * feature_tiles;
-        e = -1;
-        end = 0;
-    }
-    // Resolves the current tile; false if there is none left.
+    int j = 0;
+    MpTile d;
     __device__ __forceinline__ bool here() {
-        if (rt >= prefix[experts + 1]) return false;
-        if (rt >= end) {
-            int lo = e + 1, hi = experts;       // the last expert with prefix[.] <= rt
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (prefix[mid] <= rt) lo = mid; else hi = mid - 1;
-            }
-            e = lo;
-            end = prefix[e + 1];
-            const int tiles = end - prefix[e];
-            // equal tiles, in steps of 16 rows: fewer, fuller columns than full tiles and a rest
-            per = ((row_start[e + 1] - row_start[e] + tiles - 1) / tiles + 15) & ~15;
+        if (j < kMpListed) {
+            const int4 v = *reinterpret_cast<const int4*>(listed + j);
+            d = {v.x, v.y, v.z, v.w};
+        } else {
+            d = mp_find<PAIR>(a, prefix, row_start, j);
         }
-        r0 = row_start[e] + (rt - prefix[e]) * per;
-        const int left = row_start[e + 1] - r0;
-        rows = left < per ? left : per;
-        return true;
+        return d.rows >= 0;
     }
-    __device__ __forceinline__ void next() {
-        rt += step_rt;
-        ft += step_f;
-        if (ft >= feature_tiles) {
-            ft -= feature_tiles;
-            ++rt;
-        }
-    }
-    __device__ __forceinline__ bool none() const { return e >= experts; }
+    __device__ __forceinline__ bool none() const { return d.e >= a.experts; }
 };
 
 // The four E8M0 bytes of one row for K step kb (128 columns); bytes past k are 0.
@@ -162,34 +173,38 @@ __device__ __forceinline__ bool mp_wait(uint64_t* bar, uint32_t parity) {
     return false;
 }
 
-template <int WT>
-__global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid_constant__ MpArgs a) {
-    using S = MpShape<WT>;
+template <int WT, bool PAIR>
+__global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_kernel(const __grid_constant__ MpArgs a) {
+    using S = MpShape<WT, PAIR>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    uint8_t* sscale = smem + kMpStages * S::kStageBytes;
-    uint8_t* sout = sscale + kMpStages * S::kScaleBytes;
+    uint8_t* sscale = smem + S::kStages * S::kStageBytes;
+    uint8_t* sout = sscale + S::kStages * S::kScaleBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(sout + S::kOutBytes);
-    uint64_t* empty = full + kMpStages;
-    uint64_t* acc_full = empty + kMpStages;
+    uint64_t* empty = full + S::kStages;
+    uint64_t* acc_full = empty + S::kStages;
     uint64_t* acc_empty = acc_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
-    int* prefix = reinterpret_cast<int*>(tmem_slot + 4);
+    MpTile* listed = reinterpret_cast<MpTile*>(tmem_slot + 4);
+    int* prefix = reinterpret_cast<int*>(listed + kMpListed);
     int* row_start = prefix + kMpMaxExperts + 2;
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int s = 0; s < kMpStages; ++s) {
-            mbar_init(&full[s], 33);            // the copying thread and the scale warp's lanes
+        for (int s = 0; s < S::kStages; ++s) {
+            // the copying thread and the scale warp's lanes; for the first of a pair the second one's full stage, too
+            mbar_init(&full[s], PAIR && cluster_rank() == 0 ? 34 : 33);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], kMpReaders);
+            mbar_init(&acc_empty[b], PAIR ? 2 * S::kReaders : S::kReaders);
         }
         fence_barrier_init();
     }
-    if (warp == 3) tmem_alloc(tmem_slot, kMpTmemColumns);
+    if (warp == 3) {
+        if (PAIR) tmem_alloc_pair(tmem_slot, kMpTmemColumns); else tmem_alloc(tmem_slot, kMpTmemColumns);
+    }
     dependency_wait();
     allow_dependents();
     if (warp == 0) {
@@ -221,28 +236,36 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
             run += __shfl_sync(0xFFFFFFFFu, incl, 31);
         }
     }
-    tc_fence_before();
     __syncthreads();
+    if (tid < kMpListed) listed[tid] = mp_find<PAIR>(a, prefix, row_start, tid);
+    tc_fence_before();
+    if (PAIR) cluster_sync(); else __syncthreads();     // the other CTA's barriers are ready too
     tc_fence_after();
     // all 512 columns are allocated, so they begin at column 0: a constant that keeps the products' operands uniform
     constexpr uint32_t tmem = 0;
     if (tid == 0 && *tmem_slot != tmem) raise_error(kErrProductTimeout);
-    if (*tmem_slot != tmem) prefix[a.experts + 1] = 0;         // no tiles
-    MpTiles d(a, prefix, row_start);
+    const bool usable = *tmem_slot == tmem;
+    const int rank = PAIR ? (int)cluster_rank() : 0;
+    MpTiles<PAIR> tiles = {a, listed, prefix, row_start};
 
     if (warp == 0) {
         if (elect_one()) {
             // copies: weights, rows and weight scales
             int it = 0;
-            bool ok = true;
-            for (; ok && d.here(); d.next()) {
-                if (d.none()) continue;
-                const int n16 = (d.rows + 15) >> 4;
-                const uint32_t bytes = WT * (16384 + 512) + n16 * 2048;
-                const int64_t scale_tile = ((int64_t)d.e * a.feature_tiles + d.ft) * a.k_steps;
+            bool ok = usable;
+            for (; ok && tiles.here(); ++tiles.j) {
+                if (tiles.none()) continue;
+                const MpTile d = tiles.d;
+                const int sft = d.ft < a.feature_tiles ? d.ft : a.feature_tiles - 1;    // an odd one out has no scales
+                const int64_t scale_tile = ((int64_t)d.e * a.feature_tiles + sft) * a.k_steps;
+                // rows in units of the smallest box: all of them, or this CTA's half
+                constexpr int kUnit = PAIR ? 8 : 16;
+                const int units = (d.rows + 15) >> 4;
+                const int first = PAIR ? d.r0 + rank * units * kUnit : d.r0;
+                const uint32_t bytes = WT * (16384 + 512) + units * kUnit * 128;
                 for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
-                    const int s = it % kMpStages;
-                    if (!mp_wait(&empty[s], (uint32_t)((it / kMpStages) & 1) ^ 1u)) {
+                    const int s = it % S::kStages;
+                    if (!mp_wait(&empty[s], (uint32_t)((it / S::kStages) & 1) ^ 1u)) {
                         ok = false;
                         break;
                     }
@@ -256,19 +279,40 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                     int at = 0;
 #pragma unroll
                     for (int b = 0; b < kMpRowBoxes; ++b) {
-                        const int h = 128 >> b;
-                        if (n16 & (h >> 4)) {
-                            tma_2d_g2s(st + WT * 16384 + at * 128, &a.rows[b], kb * 128, d.r0 + at, &full[s]);
+                        const int h = 8 * kUnit >> b;
+                        if (units & (8 >> b)) {
+                            tma_2d_g2s(st + WT * 16384 + at * 128, &a.rows[b], kb * 128, first + at, &full[s]);
                             at += h;
                         }
                     }
                 }
             }
+            // every stage given back: no commit of the pair's other CTA is on its way to this one any more
+            for (int s = 0; PAIR && ok && s < S::kStages && s < it; ++s) {
+                const int last = it - 1 - s;
+                ok = mp_wait(&empty[last % S::kStages], (uint32_t)((last / S::kStages) & 1));
+            }
             if (!ok) {
                 // let the copies in flight land before the shared memory is given up
-                for (int s = 0; s < kMpStages && s < it; ++s) {
+                for (int s = 0; s < S::kStages && s < it; ++s) {
                     const int last = (it - 1 - s);
-                    mbar_wait(&full[last % kMpStages], (uint32_t)((last / kMpStages) & 1));
+                    mbar_wait(&full[last % S::kStages], (uint32_t)((last / S::kStages) & 1));
+                }
+            }
+        }
+    } else if (warp == 1 && PAIR && rank == 1) {
+        if (elect_one()) {
+            // the pair's first CTA issues the products; it learns here that this one's stage is full
+            int it = 0;
+            bool ok = usable;
+            for (; ok && tiles.here(); ++tiles.j) {
+                if (tiles.none()) continue;
+                const MpTile d = tiles.d;
+                for (int kb = 0; ok && kb < a.k_steps; ++kb, ++it) {
+                    const int s = it % S::kStages;
+                    ok = mp_wait(&full[s], (uint32_t)((it / S::kStages) & 1));
+                    fence_proxy_async_smem();   // the scale warp's stores, before the tensor core reads them
+                    if (ok) mbar_arrive_first(&full[s]);
                 }
             }
         }
@@ -276,17 +320,18 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
         if (elect_one()) {
             const uint32_t st0 = operand_desc(smem_addr(smem)), sc0 = scale_desc(smem_addr(sscale));
             int it = 0, tile = 0;
-            bool ok = true;
-            for (; ok && d.here(); d.next()) {
-                if (d.none()) continue;
-                const int b = tile & 1;
-                const uint32_t idesc = mx_instr_desc((d.rows + 15) & ~15);
-                const uint32_t acc = tmem + (uint32_t)b * kMpAccColumns;
-                if (!mp_wait(&acc_empty[b], (uint32_t)((tile >> 1) & 1) ^ 1u)) break;
+            bool ok = usable;
+            for (; ok && tiles.here(); ++tiles.j) {
+                if (tiles.none()) continue;
+                const MpTile d = tiles.d;
+                const int b = tile % S::kHalves;
+                const uint32_t idesc = mx_instr_desc(PAIR ? 256 : 128, (d.rows + 15) & ~15);
+                const uint32_t acc = tmem + (uint32_t)b * S::kAccColumns;
+                if (!mp_wait(&acc_empty[b], (uint32_t)((tile / S::kHalves) & 1) ^ 1u)) break;
                 tc_fence_after();
                 for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
-                    const int s = it % kMpStages;
-                    if (!mp_wait(&full[s], (uint32_t)((it / kMpStages) & 1))) {
+                    const int s = it % S::kStages;
+                    if (!mp_wait(&full[s], (uint32_t)((it / S::kStages) & 1))) {
                         ok = false;
                         break;
                     }
@@ -294,21 +339,25 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                     fence_proxy_async_smem();   // the scale warp's stores, before the tensor core reads them
                     const uint32_t st = st0 + (uint32_t)s * (S::kStageBytes >> 4);
                     const uint32_t sc = sc0 + (uint32_t)s * (S::kScaleBytes >> 4);
-                    const uint32_t tsc = tmem + kMpScaleColumns + (uint32_t)s * 12;
+                    const uint32_t tsc = tmem + S::kScaleBase + (uint32_t)s * S::kScaleColumns;
 #pragma unroll
-                    for (int i = 0; i < WT; ++i) tc_copy_scales(tsc + 4 * i, sc + (512 >> 4) * i);
-                    tc_copy_scales(tsc + 4 * WT, sc + (512 >> 4) * WT);
-                    if (WT == 1 && d.rows > 128) tc_copy_scales(tsc + 8, sc + (1024 >> 4));
+                    for (int i = 0; i < WT + (S::kRows > 128 ? 2 : 1); ++i)
+                        if (i <= WT || d.rows > 128) {
+                            if (PAIR) tc_copy_scales_pair(tsc + 4 * i, sc + (512 >> 4) * i);
+                            else tc_copy_scales(tsc + 4 * i, sc + (512 >> 4) * i);
+                        }
 #pragma unroll
                     for (int i = 0; i < WT; ++i)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            tc_mma_mx(acc + (uint32_t)(i * S::kRows), st + i * (16384 >> 4) + q * 2,
-                                      st + WT * (16384 >> 4) + q * 2, mx_instr_step(idesc, q), tsc + 4 * i, tsc + 4 * WT,
-                                      kb > 0 || q > 0);
-                    tc_commit(&empty[s]);
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t dst = acc + (uint32_t)(i * S::kRows);
+                            const uint32_t wd = st + i * (16384 >> 4) + q * 2, rd = st + WT * (16384 >> 4) + q * 2;
+                            if (PAIR) tc_mma_mx_pair(dst, wd, rd, mx_instr_step(idesc, q), tsc + 4 * i, tsc + 4 * WT, kb > 0 || q > 0);
+                            else tc_mma_mx(dst, wd, rd, mx_instr_step(idesc, q), tsc + 4 * i, tsc + 4 * WT, kb > 0 || q > 0);
+                        }
+                    if (PAIR) tc_commit_pair(&empty[s]); else tc_commit(&empty[s]);
                 }
-                tc_commit(&acc_full[b]);
+                if (PAIR) tc_commit_pair(&acc_full[b]); else tc_commit(&acc_full[b]);
                 ++tile;
             }
         }
@@ -318,14 +367,15 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
         const int cols = a.k >> 5;
         const bool words = (cols & 3) == 0;
         int it = 0;
-        bool ok = true;
-        for (; ok && d.here(); d.next()) {
-            if (d.none()) continue;
+        bool ok = usable;
+        for (; ok && tiles.here(); ++tiles.j) {
+            if (tiles.none()) continue;
+            const MpTile d = tiles.d;
             const uint8_t* base = a.row_scales + (int64_t)d.r0 * cols;
             constexpr int kWords = (S::kRows + 31) / 32;
             for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
-                const int s = it % kMpStages;
-                if (!__all_sync(0xFFFFFFFFu, mp_wait(&empty[s], (uint32_t)((it / kMpStages) & 1) ^ 1u))) {
+                const int s = it % S::kStages;
+                if (!__all_sync(0xFFFFFFFFu, mp_wait(&empty[s], (uint32_t)((it / S::kStages) & 1) ^ 1u))) {
                     ok = false;
                     break;
                 }
@@ -352,17 +402,19 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
         }
         cp_async_wait_all();                    // none of this warp's copies outlives the block, whatever stopped it
     } else if (warp >= 4) {
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const int quarter = warp & 3, share = (warp - 4) >> 2;     // lanes, and which 16 rows out of every kStep
+        constexpr int kStep = 16 * (S::kReaders / 4);
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         int tile = 0;
-        for (; d.here(); d.next()) {
-            const bool zero = d.none();
-            const int b = tile & 1;
+        for (; usable && tiles.here(); ++tiles.j) {
+            const MpTile d = tiles.d;
+            const bool zero = tiles.none();
+            const int b = tile % S::kHalves;
             if (!zero) {
-                if (!__all_sync(0xFFFFFFFFu, mp_wait(&acc_full[b], (uint32_t)((tile >> 1) & 1)))) break;
+                if (!__all_sync(0xFFFFFFFFu, mp_wait(&acc_full[b], (uint32_t)((tile / S::kHalves) & 1)))) break;
                 tc_fence_after();
             }
-            const uint32_t acc = tmem + (uint32_t)b * kMpAccColumns + lanes;
+            const uint32_t acc = tmem + (uint32_t)b * S::kAccColumns + lanes;
             const int f0 = d.ft * 128 + quarter * 32;
             const int64_t r0 = d.r0;
             if (WT == 1) {
@@ -376,8 +428,8 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                 };
 #pragma unroll
                 for (int i = 0; i < 8; ++i) lo[i] = hi[i] = 0u;
-                fetch(half * 16);
-                for (int c0 = half * 16; c0 < d.rows; c0 += 32, area ^= 1024) {
+                fetch(share * 16);
+                for (int c0 = share * 16; c0 < d.rows; c0 += kStep, area ^= 1024) {
                     uint8_t* stage = sout + (warp - 4) * 2048 + area;   // [16 rows][32 features] bf16
                     // register pair i of `lo` holds rows c0 + 8 * (i / 2) + 2 * (lane % 4) + {0, 1} of feature
                     // lane / 4 + 8 * (i % 2); stored transposed, 8 features are 16 bytes of an output row
@@ -390,7 +442,7 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                             m[h][i] = pack_bf16x2(__uint_as_float(lo[4 * h + 2 * i]), __uint_as_float(lo[4 * h + 2 * i + 1]));
                             m[h][2 + i] = pack_bf16x2(__uint_as_float(hi[4 * h + 2 * i]), __uint_as_float(hi[4 * h + 2 * i + 1]));
                         }
-                    fetch(c0 + 32);
+                    fetch(c0 + kStep);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) stmatrix_x4_trans(stage + out_stage_at(8 * h + (lane & 7), lane >> 3), m[h]);
                     __syncwarp();
@@ -425,8 +477,8 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                 };
 #pragma unroll
                 for (int i = 0; i < 8; ++i) g[0][i] = g[1][i] = u[0][i] = u[1][i] = 0u;
-                fetch(half * 16);
-                for (int c0 = half * 16; c0 < d.rows; c0 += 32) {
+                fetch(share * 16);
+                for (int c0 = share * 16; c0 < d.rows; c0 += kStep) {
                     tmem_load_wait(g[0], g[1]);
                     tmem_load_wait(u[0], u[1]);
                     // v[r][i]: row r = 2 h + j of this lane's four, feature p + 8 i
@@ -442,7 +494,7 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
                             top[r] = max(top[r], __float_as_uint(fabsf(v[r][i])));
                         }
                     }
-                    fetch(c0 + 32);
+                    fetch(c0 + kStep);
                     // the scale needs the exponent of the block's largest magnitude only: two rows' exponents per word
                     uint32_t ex[2] = {(top[0] >> 23) | (top[1] >> 23 << 16), (top[2] >> 23) | (top[3] >> 23 << 16)};
 #pragma unroll
@@ -485,15 +537,19 @@ __global__ void __launch_bounds__(kMpThreads, 1) moe_product_kernel(const __grid
             if (!zero) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_empty[b]);
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_first(&acc_empty[b]); else mbar_arrive(&acc_empty[b]);
+                }
                 ++tile;
             }
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if (PAIR) cluster_sync(); else __syncthreads();
     tc_fence_after();
-    if (warp == 3) tmem_free(*tmem_slot, kMpTmemColumns);
+    if (warp == 3) {
+        if (PAIR) tmem_free_pair(*tmem_slot, kMpTmemColumns); else tmem_free(*tmem_slot, kMpTmemColumns);
+    }
 }
 
 unsigned unit_errors_moe_product(bool clear) { return read_unit_errors(clear); }
@@ -513,6 +569,11 @@ static bool mp_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, con
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether the call's CTAs work in pairs (see the head of this file).
+static bool mp_pair(int64_t rows, int experts, int64_t feature_tiles) {
+    return rows / experts >= 64 && (feature_tiles % 2 == 0 || feature_tiles >= 8);
+}
+
 struct MpCall {
     const uint8_t* codes;
     const uint8_t* scales;
@@ -524,6 +585,9 @@ struct MpCall {
     void* out;
     uint8_t* out_scales;
 };
+
+template <int WT, bool PAIR>
+static fp8q_status_t mp_start(const MpArgs& a, int64_t tiles, cudaStream_t stream);
 
 template <int WT>
 static fp8q_status_t mp_launch(const MpCall& c, cudaStream_t stream) {
@@ -549,9 +613,10 @@ static fp8q_status_t mp_launch(const MpCall& c, cudaStream_t stream) {
     const Range outs[] = {{c.out, WT == 1 ? 2 * on : on}, {c.out_scales, on / 32}};
     if (any_alias(outs, 2, ins, 7)) return FP8Q_ERR_ALIAS;
 
-    using S = MpShape<WT>;
     const int64_t feature_tiles = (c.n + 127) / 128;
-    const int64_t row_tiles = c.rows / S::kRows + (c.rows < c.experts ? c.rows : c.experts) + 1;
+    const bool pair = mp_pair(c.rows, c.experts, feature_tiles);
+    const int most = pair ? MpShape<WT, true>::kRows : MpShape<WT, false>::kRows;
+    const int64_t row_tiles = c.rows / most + (c.rows < c.experts ? c.rows : c.experts) + 1;
     if (feature_tiles * row_tiles >= (int64_t)1 << 31) return FP8Q_ERR_SIZE;
     const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
     if (!encode) return cuda_status(cudaErrorNotSupported);
@@ -564,7 +629,7 @@ static fp8q_status_t mp_launch(const MpCall& c, cudaStream_t stream) {
         if (!mp_map(encode, &a.w[i], c.w[i], 3, wd, wst, 128)) return cuda_status(cudaErrorInvalidValue);
     if (WT == 1) a.w[1] = a.w[0];
     for (int b = 0; b < kMpRowBoxes; ++b)
-        if (!mp_map(encode, &a.rows[b], c.codes, 2, rd, rst, 128 >> b)) return cuda_status(cudaErrorInvalidValue);
+        if (!mp_map(encode, &a.rows[b], c.codes, 2, rd, rst, (pair ? 64 : 128) >> b)) return cuda_status(cudaErrorInvalidValue);
     a.w_scales[0] = c.ws[0];
     a.w_scales[1] = c.ws[1];
     a.row_scales = c.scales;
@@ -578,11 +643,46 @@ static fp8q_status_t mp_launch(const MpCall& c, cudaStream_t stream) {
     a.k = (int)c.k;
     a.feature_tiles = (int)feature_tiles;
     a.k_steps = (int)((c.k + 127) / 128);
+    const int64_t tiles = feature_tiles * row_tiles;
+    return pair ? mp_start<WT, true>(a, tiles, stream) : mp_start<WT, false>(a, tiles, stream);
+}
+
+template <int WT, bool PAIR>
+static fp8q_status_t mp_start(const MpArgs& a, int64_t tiles, cudaStream_t stream) {
     static KernelCache kc;
     int resident = 0;
-    const fp8q_status_t st = prepare_kernel(kc, moe_product_kernel<WT>, kMpThreads, S::kSmem, S::kSmem, &resident);
+    constexpr size_t kSmem = MpShape<WT, PAIR>::kSmem;
+    const fp8q_status_t st = prepare_kernel(kc, moe_product_kernel<WT, PAIR>, MpShape<WT, PAIR>::kThreads, kSmem, kSmem, &resident);
     if (st != FP8Q_OK) return st;
-    return launch(moe_product_kernel<WT>, grid_for((size_t)(feature_tiles * row_tiles), 1), kMpThreads, S::kSmem, stream, a);
+    if (!PAIR) return launch(moe_product_kernel<WT, PAIR>, grid_for((size_t)tiles, 1), MpShape<WT, PAIR>::kThreads, kSmem, stream, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sm_count() / 2 * 2);           // as asked of the occupancy query; set below
+    cfg.blockDim = dim3(MpShape<WT, PAIR>::kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = launch_overlap() ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {2, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    // a pair needs two neighbouring SMs: as many pairs as fit at once, since each walks over its own share of the tiles
+    static std::atomic<int> cached[kMaxDevices];
+    const int dev = current_device();
+    const bool cache = dev >= 0 && dev < kMaxDevices;
+    int pairs = cache ? cached[dev].load(std::memory_order_relaxed) : 0;
+    if (pairs < 1) {
+        if (cudaOccupancyMaxActiveClusters(&pairs, moe_product_kernel<WT, PAIR>, &cfg) != cudaSuccess || pairs < 1) {
+            (void)cudaGetLastError();
+            pairs = 1;
+        }
+        if (cache) cached[dev].store(pairs, std::memory_order_relaxed);
+    }
+    cfg.gridDim = dim3(2u * (unsigned)pairs);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_product_kernel<WT, PAIR>, a);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return cuda_status(e);
 }
 
 }  // namespace fp8q

@@ -64,11 +64,11 @@ __device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint32_t desc) {
         : "memory");
 }
 
-// Instruction descriptor of an e4m3 x e4m3 product with E8M0 scales: M = 128,
-// N = n (a multiple of 16), and which byte of the scale words this K step of
-// 32 uses.
-__device__ __forceinline__ uint32_t mx_instr_desc(int n) {
-    return ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
+// Instruction descriptor of an e4m3 x e4m3 product with E8M0 scales: M = m
+// (128, or 256 for a pair of CTAs), N = n (a multiple of 16), and which byte of
+// the scale words this K step of 32 uses.
+__device__ __forceinline__ uint32_t mx_instr_desc(uint32_t m, int n) {
+    return ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24);
 }
 __device__ __forceinline__ uint32_t mx_instr_step(uint32_t idesc, uint32_t step) {
     return idesc | (step << 4) | (step << 29);
@@ -130,6 +130,61 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// ------------------------------------------------------- pairs of CTAs ----
+// Two CTAs of a cluster may work on one product of M = 256 (cta_group::2): each
+// holds 128 rows of A, half of the rows of B and the accumulators of its own
+// 128 rows.  One thread of the CTA of rank 0 issues for both; descriptors and
+// TMEM addresses name the same places in both.
+constexpr uint16_t kPairMask = 3;
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_addr_out, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(smem_addr_out)),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t addr, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns) : "memory");
+}
+__device__ __forceinline__ void tc_copy_scales_pair(uint32_t taddr, uint32_t desc) {
+    asm volatile(
+        "{\n\t.reg .b64 s;\n\tmov.b64 s, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], s;\n\t}" ::"r"(taddr),
+        "r"(desc), "n"(kScaleLayout)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_mx_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                               bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)accumulate), "n"(kOperandLayout)
+        : "memory");
+}
+// Arrives on the barriers at this offset of both CTAs.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"(kPairMask)
+        : "memory");
+}
+// Arrives on the barrier at this offset of the CTA of rank 0.
+__device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
+        "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_addr(bar))
+        : "memory");
+}
 
 // 3D tiled bulk copy of the box at (x, y, z); x * element size must be a
 // multiple of 16 bytes, out-of-range elements read as zero.
