@@ -96,6 +96,30 @@ __device__ __forceinline__ void decode_fp8x4(uint32_t w, float* f) {
     f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
 }
 
+// ------------------------------------------------------------- clusters ----
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
+}
+// The word at this shared-memory place of the cluster's block `rank`.
+__device__ __forceinline__ int peer_smem(const int* p, int rank) {
+    int v;
+    asm volatile(
+        "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\t"
+        "ld.shared::cluster.s32 %0, [r];\n\t}"
+        : "=r"(v)
+        : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank)
+        : "memory");
+    return v;
+}
+
 // -------------------------------------------- programmatic dependent launch ----
 // Every kernel of the library is launched so that it may be dispatched while
 // the previous kernel on its stream is still finishing.  A kernel calls

@@ -655,34 +655,16 @@ static fp8q_status_t mp_start(const MpArgs& a, int64_t tiles, cudaStream_t strea
     const fp8q_status_t st = prepare_kernel(kc, moe_product_kernel<WT, PAIR>, MpShape<WT, PAIR>::kThreads, kSmem, kSmem, &resident);
     if (st != FP8Q_OK) return st;
     if (!PAIR) return launch(moe_product_kernel<WT, PAIR>, grid_for((size_t)tiles, 1), MpShape<WT, PAIR>::kThreads, kSmem, stream, a);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)sm_count() / 2 * 2);           // as asked of the occupancy query; set below
-    cfg.blockDim = dim3(MpShape<WT, PAIR>::kThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = launch_overlap() ? 1 : 0;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {2, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    // a pair needs two neighbouring SMs: as many pairs as fit at once, since each walks over its own share of the tiles
+    // as many pairs as are resident at once, since each walks over its own share of the tiles
     static std::atomic<int> cached[kMaxDevices];
     const int dev = current_device();
     const bool cache = dev >= 0 && dev < kMaxDevices;
     int pairs = cache ? cached[dev].load(std::memory_order_relaxed) : 0;
     if (pairs < 1) {
-        if (cudaOccupancyMaxActiveClusters(&pairs, moe_product_kernel<WT, PAIR>, &cfg) != cudaSuccess || pairs < 1) {
-            (void)cudaGetLastError();
-            pairs = 1;
-        }
+        pairs = resident_clusters(moe_product_kernel<WT, PAIR>, 2, MpShape<WT, PAIR>::kThreads, kSmem);
         if (cache) cached[dev].store(pairs, std::memory_order_relaxed);
     }
-    cfg.gridDim = dim3(2u * (unsigned)pairs);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_product_kernel<WT, PAIR>, a);
-    if (e != cudaSuccess) (void)cudaGetLastError();
-    return cuda_status(e);
+    return launch_clusters(moe_product_kernel<WT, PAIR>, 2u * (unsigned)pairs, 2, MpShape<WT, PAIR>::kThreads, kSmem, stream, a);
 }
 
 }  // namespace fp8q

@@ -85,15 +85,18 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_count_kernel(const Sort
     }
 }
 
+template <bool COUNTED>
 __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const SortArgs a) {
-    extern __shared__ int hist_all[];                       // [kSortWarps][keys], then first[keys]
+    extern __shared__ int hist_all[];                       // [kSortWarps][keys], then first[keys], behind[keys]
     __shared__ int warp_total[kSortWarps];
     const int keys = a.experts + 1;
-    int* first = hist_all + kSortWarps * keys;              // total of each key, then its first slot
+    int* first = hist_all + kSortWarps * keys;              // total of each key, then its first slot in this block
+    int* behind = first + keys;                             // the earlier blocks' choices of each key
     const int t = (int)threadIdx.x, lane = t & 31, warp = t >> 5;
     for (int i = t; i < kSortWarps * keys; i += kSortThreads) hist_all[i] = 0;
-    dependency_wait();
-    allow_dependents();
+    // Behind the counting launch the ids may be read at once: its blocks let
+    // this launch start only when whatever wrote the ids had completed.
+    if (!COUNTED) dependency_wait();
     __syncthreads();
     int64_t lo, hi;
     segment_of(a, &lo, &hi);
@@ -101,25 +104,46 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const Sort
     warp_histogram(a, hist, lo, hi);
     __syncthreads();
     // per key: the counts of this block's warps become their offsets inside
-    // the key's run (behind the earlier blocks); `first` gets the key's total
+    // the key's run; `first` gets the key's total
     for (int e = t; e < keys; e += kSortThreads) {
-        int before = 0, total = 0;
-        if (gridDim.x > 1) {
-#pragma unroll 16
-            for (int b = 0; b < (int)gridDim.x; ++b) {
-                const int c = a.counts[(int64_t)b * keys + e];
-                if (b < (int)blockIdx.x) before += c;
-                total += c;
-            }
-        }
-        int run = before;
+        int run = 0;
+#pragma unroll
         for (int w = 0; w < kSortWarps; ++w) {
             const int c = hist_all[w * keys + e];
             hist_all[w * keys + e] = run;
             run += c;
         }
-        first[e] = gridDim.x > 1 ? total : run;
+        first[e] = run;
+        behind[e] = 0;
     }
+    if (COUNTED) {
+        dependency_wait();
+        // four threads a key: each a quarter of the blocks' counts
+        const int blocks = (int)gridDim.x, q = t & 3;
+        __syncthreads();
+        for (int e0 = 0; e0 < keys; e0 += kSortThreads / 4) {
+            const int e = e0 + (t >> 2);
+            int before = 0, total = 0;
+            if (e < keys) {
+#pragma unroll 8
+                for (int b = q; b < blocks; b += 4) {
+                    const int c = a.counts[(int64_t)b * keys + e];
+                    before += b < (int)blockIdx.x ? c : 0;
+                    total += c;
+                }
+            }
+#pragma unroll
+            for (int m = 1; m < 4; m <<= 1) {
+                before += __shfl_xor_sync(0xFFFFFFFFu, before, m);
+                total += __shfl_xor_sync(0xFFFFFFFFu, total, m);
+            }
+            if (e < keys && q == 0) {
+                first[e] = total;
+                behind[e] = before;
+            }
+        }
+    }
+    allow_dependents();
     __syncthreads();
     // exclusive scan of the totals: each thread a run of consecutive keys
     const int per = (keys + kSortThreads - 1) / kSortThreads;
@@ -135,10 +159,10 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const Sort
     if (lane == 31) warp_total[warp] = incl;
     __syncthreads();
     int at = incl - mine;
-    for (int w = 0; w < warp; ++w) at += warp_total[w];
+    at += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warp_total[lane] : 0);
     for (int e = e0; e < e1; ++e) {
         const int c = first[e];
-        first[e] = at;
+        first[e] = at + behind[e];
         if (blockIdx.x == 0) a.offsets[e] = at;
         at += c;
     }
@@ -432,19 +456,20 @@ extern "C" fp8q_status_t fp8q_moe_sort(const void* ids, int id_bytes, int64_t to
     int64_t blocks;
     const int64_t chunk = sort_chunk(n, &blocks);
     const SortArgs a = {ids, id_bytes == 8, n, chunk, experts, static_cast<int*>(workspace), offsets, order, slots};
-    const size_t most = (size_t)(kSortWarps + 1) * (kMaxExperts + 1) * sizeof(int);
-    const size_t smem = (size_t)(kSortWarps + 1) * (experts + 1) * sizeof(int);
-    static KernelCache kc1, kc2;
+    const size_t most = (size_t)(kSortWarps + 2) * (kMaxExperts + 1) * sizeof(int);
+    const size_t smem = (size_t)(kSortWarps + 2) * (experts + 1) * sizeof(int);
+    static KernelCache kc1, kc2, kc3;
     int resident = 0;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (blocks > 1) {
-        fp8q_status_t s = prepare_kernel(kc1, moe_sort_count_kernel, kSortThreads, most, most, &resident);
-        if (s == FP8Q_OK) s = launch(moe_sort_count_kernel, (unsigned)blocks, kSortThreads, smem, cs, a);
-        if (s != FP8Q_OK) return s;
+    fp8q_status_t s;
+    if (blocks <= 1) {
+        s = prepare_kernel(kc1, moe_sort_place_kernel<false>, kSortThreads, most, most, &resident);
+        return s != FP8Q_OK ? s : launch(moe_sort_place_kernel<false>, 1, kSortThreads, smem, cs, a);
     }
-    const fp8q_status_t s = prepare_kernel(kc2, moe_sort_place_kernel, kSortThreads, most, most, &resident);
-    if (s != FP8Q_OK) return s;
-    return launch(moe_sort_place_kernel, (unsigned)(blocks > 0 ? blocks : 1), kSortThreads, smem, cs, a);
+    s = prepare_kernel(kc2, moe_sort_count_kernel, kSortThreads, most, most, &resident);
+    if (s == FP8Q_OK) s = launch(moe_sort_count_kernel, (unsigned)blocks, kSortThreads, smem, cs, a);
+    if (s == FP8Q_OK) s = prepare_kernel(kc3, moe_sort_place_kernel<true>, kSortThreads, most, most, &resident);
+    return s != FP8Q_OK ? s : launch(moe_sort_place_kernel<true>, (unsigned)blocks, kSortThreads, smem, cs, a);
 }
 
 namespace fp8q {
