@@ -185,7 +185,14 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormArgs a) {
                 m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
                 const float s = block_scale<FMT>(m);
-                block_quotients<2, 8>(y, s, q);
+                // y itself carries some ulps, so that the quotient is y * RN(1 / s), within 1.5 ulp of y / s
+                if (s >= 0x1p-100f || s == 0.0f) {
+                    const float inv = s > 0.0f ? __frcp_rn(s) : 1.0f;   // an all-zero block keeps its zeros
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(y[i], inv);
+                } else {
+                    block_quotients<2, 8>(y, s, q);
+                }
                 if (ok && (c & 15) == 0) static_cast<float*>(a.scales)[row * scale_cols + (c >> 4)] = s;
                 if (ok)
                     st_stream(a.codes + base + c * 8, make_uint2(cvt_fp8x4<FMT>(q[0], q[1], q[2], q[3]),
@@ -348,8 +355,8 @@ struct NormShape {
 // block of as many threads as `v` chunks per thread need; with few rows a
 // block has one chunk per thread, as latency counts and nothing else runs.
 static NormShape norm_shape(int chunks, int64_t rows, int most_v) {
-    if (chunks <= 32) return {true, 1, kNormWarps * 32, kNormWarps};
-    if (chunks <= 32 * most_v) return {true, most_v, kNormWarps * 32, kNormWarps};
+    for (int v = 1; v <= most_v; v *= 2)
+        if (chunks <= 32 * v) return {true, v, kNormWarps * 32, kNormWarps};
     const bool few = rows <= 2 * (int64_t)sm_count() && chunks <= 512;
     const int v = few ? 1 : chunks <= 512 * most_v ? most_v : 4;
     const int per = (chunks + v - 1) / v;
@@ -385,7 +392,10 @@ static fp8q_status_t norm_go(const NormShape& sh, const NormArgs& a, cudaStream_
 }
 template <int OUT>
 static fp8q_status_t norm_go(const NormShape& sh, const NormArgs& a, cudaStream_t stream) {
-    if (sh.warp_rows) return sh.v == 1 ? norm_go<OUT, 1, true>(sh, a, stream) : norm_go<OUT, 4, true>(sh, a, stream);
+    if (sh.warp_rows)
+        return sh.v == 1   ? norm_go<OUT, 1, true>(sh, a, stream)
+               : sh.v == 2 ? norm_go<OUT, 2, true>(sh, a, stream)
+                           : norm_go<OUT, 4, true>(sh, a, stream);
     return sh.v == 1 ? norm_go<OUT, 1, false>(sh, a, stream) : norm_go<OUT, 4, false>(sh, a, stream);
 }
 
