@@ -19,10 +19,11 @@
 // With many rows per expert two CTAs work as a pair on 256 features: each
 // holds its own 128 features' weights and half of the rows.
 //
-// One CTA per SM walks over the tiles.  Warp 0 copies weights, rows and
-// weight scales by TMA, warp 2 brings the rows' scales into the tensor core's
-// tile order (rows of an expert start anywhere, so their scales cannot lie
-// pre-tiled), warp 1 issues the products, warps 4 to 11 read the accumulators
+// One CTA per SM walks over the tiles.  Warp 0 copies weights and rows by TMA,
+// as few copies a K step as possible (its one thread's instructions bound the
+// pipeline), warp 2 copies the scales and brings the rows' into the tensor
+// core's tile order (rows of an expert start anywhere, so their scales cannot
+// lie pre-tiled), warp 1 issues the products, warps 4 to 11 read the accumulators
 // of one tile while the products of the next fill the other half of TMEM (two
 // warps for each quarter of the lanes, every other 16 rows each).
 #include <cuda.h>
@@ -35,7 +36,7 @@ namespace fp8q {
 
 constexpr int kMpMaxExperts = 1024;
 constexpr int kMpListed = 128;                  // tiles of a CTA that are found ahead (see MpTiles)
-constexpr int kMpRowBoxes = 4;                  // row boxes of 128, 64, 32 and 16 rows, or half of that for pairs
+constexpr int kMpRowBoxes = 6;
 constexpr uint32_t kMpTmemColumns = 512;
 constexpr unsigned kErrProductTimeout = 2u;
 
@@ -45,6 +46,11 @@ template <int WT, bool PAIR> struct MpShape {
     static constexpr int kThreads = 128 + 32 * kReaders;
     static constexpr int kRows = WT == 2 ? 112 : PAIR ? 208 : 224;          // most rows of a tile
     static constexpr int kHeld = PAIR ? kRows / 2 : kRows;                  // rows of it in this CTA's shared memory
+    // Rows are copied by one box a K step, the lowest of these that holds the tile's, in units of 16 (8 for a pair's half).
+    static constexpr int kUnits = kRows / 16;
+    static __host__ __device__ constexpr int box(int b) {
+        return b == 0 ? kUnits : b == 1 ? kUnits - 2 : b == 2 ? kUnits - 4 : b == 3 ? (kUnits + 1) / 2 : b == 4 ? (kUnits + 3) / 4 : 1;
+    }
     static constexpr int kStages = !PAIR ? 4 : WT == 1 ? 6 : 5;
     static constexpr int kHalves = 2;                                       // tiles whose accumulators fit TMEM
     static constexpr uint32_t kAccColumns = WT * kRows;                     // of one tile
@@ -256,13 +262,18 @@ __global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_
             for (; ok && tiles.here(); ++tiles.j) {
                 if (tiles.none()) continue;
                 const MpTile d = tiles.d;
-                const int sft = d.ft < a.feature_tiles ? d.ft : a.feature_tiles - 1;    // an odd one out has no scales
-                const int64_t scale_tile = ((int64_t)d.e * a.feature_tiles + sft) * a.k_steps;
-                // rows in units of the smallest box: all of them, or this CTA's half
-                constexpr int kUnit = PAIR ? 8 : 16;
                 const int units = (d.rows + 15) >> 4;
+                int box = 0;
+#pragma unroll
+                for (int b = 1; b < kMpRowBoxes; ++b)
+                    if (S::box(b) >= units) box = b;
+                constexpr int kUnit = PAIR ? 8 : 16;
                 const int first = PAIR ? d.r0 + rank * units * kUnit : d.r0;
-                const uint32_t bytes = WT * (16384 + 512) + units * kUnit * 128;
+                uint32_t bytes = S::kUnits;
+#pragma unroll
+                for (int b = 1; b < kMpRowBoxes; ++b)
+                    if (box == b) bytes = S::box(b);
+                bytes = WT * 16384 + bytes * kUnit * 128;
                 for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
                     const int s = it % S::kStages;
                     if (!mp_wait(&empty[s], (uint32_t)((it / S::kStages) & 1) ^ 1u)) {
@@ -272,19 +283,8 @@ __global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_
                     uint8_t* st = smem + s * S::kStageBytes;
                     mbar_arrive_expect_tx(&full[s], bytes);
 #pragma unroll
-                    for (int i = 0; i < WT; ++i) {
-                        tma_3d_g2s(st + i * 16384, &a.w[i], kb * 128, d.ft * 128, d.e, &full[s]);
-                        bulk_g2s(sscale + s * S::kScaleBytes + i * 512, a.w_scales[i] + (scale_tile + kb) * 512, 512, &full[s]);
-                    }
-                    int at = 0;
-#pragma unroll
-                    for (int b = 0; b < kMpRowBoxes; ++b) {
-                        const int h = 8 * kUnit >> b;
-                        if (units & (8 >> b)) {
-                            tma_2d_g2s(st + WT * 16384 + at * 128, &a.rows[b], kb * 128, first + at, &full[s]);
-                            at += h;
-                        }
-                    }
+                    for (int i = 0; i < WT; ++i) tma_3d_g2s(st + i * 16384, &a.w[i], kb * 128, d.ft * 128, d.e, &full[s]);
+                    tma_2d_g2s(st + WT * 16384, &a.rows[box], kb * 128, first, &full[s]);
                 }
             }
             // every stage given back: no commit of the pair's other CTA is on its way to this one any more
@@ -362,8 +362,8 @@ __global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_
             }
         }
     } else if (warp == 2) {
-        // the rows' scales: lane l takes rows l, l + 32, ... of the tile, whose words for one K step are
-        // 16 consecutive bytes of the tensor core's scale tile
+        // the scales: the weights' lie tiled, 16 bytes a lane; of the rows' lane l takes rows l, l + 32, ... of the
+        // tile, whose words for one K step are 16 consecutive bytes of the tensor core's scale tile
         const int cols = a.k >> 5;
         const bool words = (cols & 3) == 0;
         int it = 0;
@@ -372,6 +372,8 @@ __global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_
             if (tiles.none()) continue;
             const MpTile d = tiles.d;
             const uint8_t* base = a.row_scales + (int64_t)d.r0 * cols;
+            const int sft = d.ft < a.feature_tiles ? d.ft : a.feature_tiles - 1;    // an odd one out has no scales
+            const int64_t wsc = ((int64_t)d.e * a.feature_tiles + sft) * a.k_steps * 512 + lane * 16;
             constexpr int kWords = (S::kRows + 31) / 32;
             for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
                 const int s = it % S::kStages;
@@ -379,13 +381,16 @@ __global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_
                     ok = false;
                     break;
                 }
-                uint8_t* sc = sscale + s * S::kScaleBytes + WT * 512 + lane * 16;
+                uint8_t* sc = sscale + s * S::kScaleBytes + lane * 16;
+#pragma unroll
+                for (int i = 0; i < WT; ++i) cp_async16(sc + i * 512, a.w_scales[i] + wsc + kb * 512);
+                sc += WT * 512;
                 if (words) {
                     // asynchronous 4-byte copies: this warp never waits for memory, only for a free stage
 #pragma unroll
                     for (int c = 0; c < kWords; ++c) {
                         const int r = lane + 32 * c;
-                        cp_async4(sc + (c >> 2) * 512 + (c & 3) * 4, base + (r < d.rows ? (int64_t)r * cols + kb * 4 : 0),
+                        cp_async4(sc + (c >> 2) * 512 + (c & 3) * 4, r < d.rows ? base + ((int64_t)r * cols + kb * 4) : a.row_scales,
                                   r < d.rows ? 4 : 0);
                     }
                     cp_async_arrive(&full[s]);
@@ -396,6 +401,7 @@ __global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_
                         *reinterpret_cast<uint32_t*>(sc + (c >> 2) * 512 + (c & 3) * 4) =
                             r < d.rows ? row_scale_word(base + (int64_t)r * cols, kb, cols) : 0u;
                     }
+                    cp_async_wait_all();
                     mbar_arrive(&full[s]);
                 }
             }
@@ -629,7 +635,7 @@ static fp8q_status_t mp_launch(const MpCall& c, cudaStream_t stream) {
         if (!mp_map(encode, &a.w[i], c.w[i], 3, wd, wst, 128)) return cuda_status(cudaErrorInvalidValue);
     if (WT == 1) a.w[1] = a.w[0];
     for (int b = 0; b < kMpRowBoxes; ++b)
-        if (!mp_map(encode, &a.rows[b], c.codes, 2, rd, rst, (pair ? 64 : 128) >> b)) return cuda_status(cudaErrorInvalidValue);
+        if (!mp_map(encode, &a.rows[b], c.codes, 2, rd, rst, pair ? MpShape<WT, true>::box(b) * 8 : MpShape<WT, false>::box(b) * 16)) return cuda_status(cudaErrorInvalidValue);
     a.w_scales[0] = c.ws[0];
     a.w_scales[1] = c.ws[1];
     a.row_scales = c.scales;
