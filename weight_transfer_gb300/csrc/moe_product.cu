@@ -136,11 +136,12 @@ struct MpTiles {
     __device__ __forceinline__ bool none() const { return d.e >= a.experts; }
 };
 
-// The four E8M0 bytes of one row for K step kb (128 columns); bytes past k are 0.
-__device__ __forceinline__ uint32_t row_scale_word(const uint8_t* row, int kb, int cols) {
+// The aligned word at byte `at` (a multiple of 4) of an array of `left` bytes; bytes past its end are 0.
+__device__ __forceinline__ uint32_t word_within(const uint8_t* p, int64_t at, int64_t left) {
+    if (at + 4 <= left) return *reinterpret_cast<const uint32_t*>(p + at);
     uint32_t w = 0;
     for (int j = 0; j < 4; ++j)
-        if (kb * 4 + j < cols) w |= (uint32_t)row[kb * 4 + j] << (8 * j);
+        if (at + j < left) w |= (uint32_t)p[at + j] << (8 * j);
     return w;
 }
 
@@ -198,8 +199,9 @@ __global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_
 
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
-            // the copying thread and the scale warp's lanes; for the first of a pair the second one's full stage, too
-            mbar_init(&full[s], PAIR && cluster_rank() == 0 ? 34 : 33);
+            // the copying thread and the scale warp's lanes (twice, where they also store); for the first of a pair the
+            // second one's full stage, too
+            mbar_init(&full[s], 33 + ((a.k & 127) != 0 ? 32 : 0) + (PAIR && cluster_rank() == 0 ? 1 : 0));
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -375,6 +377,23 @@ __global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_
             const int sft = d.ft < a.feature_tiles ? d.ft : a.feature_tiles - 1;    // an odd one out has no scales
             const int64_t wsc = ((int64_t)d.e * a.feature_tiles + sft) * a.k_steps * 512 + lane * 16;
             constexpr int kWords = (S::kRows + 31) / 32;
+            // Rows that are no multiple of 4 bytes long go through registers: K step kb's four bytes lie across the
+            // aligned words kb and kb + 1 behind the row's start; `low` is the former, `high` the latter, on its way
+            // since the step before.
+            uint32_t low[kWords], high[kWords];
+            const int64_t at0 = (int64_t)d.r0 * cols, start = at0 & ~(int64_t)3;
+            const int64_t left = (int64_t)a.rows_total * cols - start;
+            const auto word = [&](int c, int i) {
+                const int r = lane + 32 * c;
+                return r < d.rows ? word_within(a.row_scales + start, (((at0 - start) + (int64_t)r * cols) & ~(int64_t)3) + 4 * i, left) : 0u;
+            };
+            if (!words) {
+#pragma unroll
+                for (int c = 0; c < kWords; ++c) {
+                    low[c] = word(c, 0);
+                    high[c] = word(c, 1);
+                }
+            }
             for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
                 const int s = it % S::kStages;
                 if (!__all_sync(0xFFFFFFFFu, mp_wait(&empty[s], (uint32_t)((it / S::kStages) & 1) ^ 1u))) {
@@ -397,12 +416,15 @@ __global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_
                 } else {
 #pragma unroll
                     for (int c = 0; c < kWords; ++c) {
-                        const int r = lane + 32 * c;
-                        *reinterpret_cast<uint32_t*>(sc + (c >> 2) * 512 + (c & 3) * 4) =
-                            r < d.rows ? row_scale_word(base + (int64_t)r * cols, kb, cols) : 0u;
+                        const int shift = (int)((at0 - start) + (int64_t)(lane + 32 * c) * cols) & 3;
+                        uint32_t w = __funnelshift_r(low[c], high[c], 8 * shift);
+                        if (cols - kb * 4 < 4) w &= (1u << (8 * (cols - kb * 4))) - 1u;
+                        *reinterpret_cast<uint32_t*>(sc + (c >> 2) * 512 + (c & 3) * 4) = w;
+                        low[c] = high[c];
+                        high[c] = word(c, kb + 2);
                     }
-                    cp_async_wait_all();
-                    mbar_arrive(&full[s]);
+                    cp_async_arrive(&full[s]);  // the weights' scales
+                    mbar_arrive(&full[s]);      // the stores above
                 }
             }
         }

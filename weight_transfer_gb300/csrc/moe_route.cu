@@ -332,58 +332,75 @@ struct CombineGradArgs {
     int k;
 };
 
-// One choice per warp: the dot product is summed in the lanes and joined by
-// shuffles, dy leaves as the row of y passes by.  The choices of a token are
-// neighbouring warps, so that its row of dout comes from the first-level cache
-// for all but one of them.
+// A warp takes NC choices at once: as many as it can hold whole rows of, for
+// short rows, so that it always has four 16-byte pieces per lane on their way.
+// A dot product is summed in the lanes and joined by shuffles, dy leaves as the
+// row of y passes by.  The choices of a token are neighbours, so that its row
+// of dout comes from the first-level cache for all but one of them.
+template <int NC>
 __global__ void __launch_bounds__(kRowWarps * 32) moe_combine_backward_kernel(const CombineGradArgs a) {
+    constexpr int U = 4 / NC;                   // pieces of a row per lane and step
     const int lane = (int)(threadIdx.x & 31u);
-    const int64_t i = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    const int64_t i0 = ((int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5)) * NC;
     const int64_t n = a.tokens * a.topk;
     dependency_wait();
     allow_dependents();
-    if (i >= n) return;
-    const int64_t t = i / a.topk;
-    const int s = a.slots[i];
-    const bool inside = s >= 0 && s < n;
-    const bool live = inside && s < *a.routed;
-    const float w = a.weights[i];
-    const uint16_t* drow = a.dout + t * a.k;
-    const uint16_t* yrow = a.y + (int64_t)(live ? s : 0) * a.k;
-    uint16_t* orow = a.dy + (int64_t)(inside ? s : 0) * a.k;
-    float dot = 0.0f;
-    constexpr int U = 4;
+    if (i0 >= n) return;
+    const int routed = *a.routed;
+    const uint16_t *drow[NC], *yrow[NC];
+    uint16_t* orow[NC];
+    bool inside[NC], live[NC];
+    float w[NC], dot[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int64_t i = i0 + c < n ? i0 + c : n - 1;
+        const int s = a.slots[i];
+        inside[c] = i0 + c < n && s >= 0 && s < n;
+        live[c] = inside[c] && s < routed;
+        w[c] = a.weights[i];
+        drow[c] = a.dout + i / a.topk * a.k;
+        yrow[c] = a.y + (int64_t)(live[c] ? s : 0) * a.k;
+        orow[c] = a.dy + (int64_t)(inside[c] ? s : 0) * a.k;
+        dot[c] = 0.0f;
+    }
     for (int c0 = lane * 8; c0 < a.k; c0 += 256 * U) {
-        uint4 d[U], y[U];
+        uint4 d[NC][U], y[NC][U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = c0 + u * 256;
-            d[u] = y[u] = make_uint4(0, 0, 0, 0);
-            if (live && c < a.k) {
-                d[u] = *reinterpret_cast<const uint4*>(drow + c);
-                y[u] = ld_stream(yrow + c);
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int col = c0 + u * 256;
+                d[c][u] = y[c][u] = make_uint4(0, 0, 0, 0);
+                if (live[c] && col < a.k) {
+                    d[c][u] = *reinterpret_cast<const uint4*>(drow[c] + col);
+                    y[c][u] = ld_stream(yrow[c] + col);
+                }
             }
-        }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = c0 + u * 256;
-            float fd[8], fy[8];
-            unpack8(d[u], fd);
-            unpack8(y[u], fy);
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                dot = __fmaf_rn(fd[e], fy[e], dot);
-                fd[e] = __fmul_rn(fd[e], w);
+            for (int u = 0; u < U; ++u) {
+                const int col = c0 + u * 256;
+                float fd[8], fy[8];
+                unpack8(d[c][u], fd);
+                unpack8(y[c][u], fy);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dot[c] = __fmaf_rn(fd[e], fy[e], dot[c]);
+                    fd[e] = __fmul_rn(fd[e], w[c]);
+                }
+                if (inside[c] && col < a.k)
+                    st_stream(orow[c] + col, live[c] ? make_uint4(pack_bf16x2(fd[0], fd[1]), pack_bf16x2(fd[2], fd[3]),
+                                                                  pack_bf16x2(fd[4], fd[5]), pack_bf16x2(fd[6], fd[7]))
+                                                     : make_uint4(0, 0, 0, 0));
             }
-            if (inside && c < a.k)
-                st_stream(orow + c, live ? make_uint4(pack_bf16x2(fd[0], fd[1]), pack_bf16x2(fd[2], fd[3]),
-                                                      pack_bf16x2(fd[4], fd[5]), pack_bf16x2(fd[6], fd[7]))
-                                         : make_uint4(0, 0, 0, 0));
-        }
     }
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, m);
-    if (lane == 0) a.dweights[i] = dot;
+    for (int c = 0; c < NC; ++c) {
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) dot[c] += __shfl_xor_sync(0xFFFFFFFFu, dot[c], m);
+        if (lane == 0 && i0 + c < n) a.dweights[i0 + c] = dot[c];
+    }
 }
 
 // Choices per sort block, and the number of blocks.
@@ -563,9 +580,12 @@ extern "C" fp8q_status_t fp8q_moe_combine_backward(const void* dout_bf16, const 
     const Range outs[] = {{dy_bf16, 2 * n * (size_t)k}, {dweights, 4 * n}};
     if (any_alias(outs, 2, ins, 5)) return FP8Q_ERR_ALIAS;
     unsigned grid;
-    const fp8q_status_t sg = units_grid(tokens * topk, &grid);
+    const int per = k <= 256 ? 4 : k <= 512 ? 2 : 1;
+    const fp8q_status_t sg = units_grid((tokens * topk + per - 1) / per, &grid);
     if (sg != FP8Q_OK) return sg;
     const CombineGradArgs a = {static_cast<const uint16_t*>(dout_bf16), static_cast<const uint16_t*>(y_bf16), slots,
                                offsets + experts, weights, static_cast<uint16_t*>(dy_bf16), dweights, tokens, topk, (int)k};
-    return launch(moe_combine_backward_kernel, grid, kRowWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream), a);
+    return launch(per == 4   ? moe_combine_backward_kernel<4>
+                  : per == 2 ? moe_combine_backward_kernel<2>
+                             : moe_combine_backward_kernel<1>, grid, kRowWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream), a);
 }

@@ -473,8 +473,11 @@ namespace fp8q {
 // enough (a chunk needs 40 registers there), and blocks for 1024 threads per SM.
 static NormShape norm_backward_shape(int64_t rows, int64_t k, int64_t* blocks) {
     const NormShape sh = norm_shape((int)(k >> 3), rows, 2);
-    const int64_t most = (int64_t)sm_count() * (1024 / sh.threads > 0 ? 1024 / sh.threads : 1);
-    const int64_t want = (rows + sh.groups - 1) / sh.groups;
+    const int64_t sms = sm_count();
+    const int64_t most = sms * (1024 / sh.threads > 0 ? 1024 / sh.threads : 1);
+    // a block's partial sums cost 8 bytes per column, a row 6 to 8: at least four rows per group beyond one block per SM
+    int64_t want = (rows + 4 * sh.groups - 1) / (4 * sh.groups);
+    if (want < sms) want = (rows + sh.groups - 1) / sh.groups < sms ? (rows + sh.groups - 1) / sh.groups : sms;
     *blocks = want < most ? want : most;
     return sh;
 }
