@@ -482,10 +482,12 @@ fp8q_status_t fp8q_moe_combine_backward(const void* dout_bf16, const void* y_bf1
  *   codes, scales : rows * k codes and row-major [rows, k / 32] E8M0 bytes
  *   *_codes, *_scales (weights) : [experts, n, k] as mxfp8_quantize_swizzled
  *                   writes them for batch = experts, m = n
- *   offsets       : experts + 1 integers on the device, not decreasing; values
- *                   outside [0, rows] count as the nearer end
+ *   offsets       : experts + 1 integers on the device, the first 0, not
+ *                   decreasing; values outside [0, rows] count as the nearer
+ *                   end, one below its predecessor as the predecessor
  * k: a positive multiple of 32; swiglu: n too (FP8Q_ERR_K).  experts: 1 ..
- * FP8Q_MOE_MAX_EXPERTS.  rows == 0 or n == 0 is a no-op. */
+ * FP8Q_MOE_MAX_EXPERTS, rows < 2^30 (FP8Q_ERR_SIZE).  rows == 0 or n == 0 is a
+ * no-op. */
 fp8q_status_t mxfp8_moe_matmul(const uint8_t* codes, const uint8_t* scales, int64_t rows, const uint8_t* w_codes,
                                const uint8_t* w_scales, const int32_t* offsets, int experts, int64_t n, int64_t k,
                                void* out_bf16, fp8q_stream_t stream);

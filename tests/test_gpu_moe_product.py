@@ -173,3 +173,66 @@ def test_empty(w):
     off = torch.zeros(3, dtype=torch.int32, device="cuda")
     out = w.mxfp8_moe_matmul(e(0, 64), e(0, 2), e(2, 96, 64), e(2 * 512), off)
     assert out.shape == (0, 96)
+
+
+@pytest.mark.parametrize("counts,rows", [([60, 300, 0, 209, 70], 640), ([49], 49), ([417, 415], 840), ([1, 1, 700, 2, 0], 704),
+                                         ([64] * 12, 768), ([49, 51], 100)])
+@pytest.mark.parametrize("n,k", [(256, 160), (384, 128), (1100, 96), (130, 288), (512, 1024)])
+def test_matmul_many_rows_per_expert(w, counts, rows, n, k):
+    """Pairs of blocks (an even number of feature tiles, or at least 8), an odd tile out, and single blocks."""
+    off, e_of = groups(counts, rows)
+    ac, ae, av = whole_mx((rows, k), 6)
+    wc, we, wv = whole_mx((len(counts), n, k), 7)
+    got = w.mxfp8_moe_matmul(ac.cuda(), ae.cuda(), wc.cuda(), swizzle(we).cuda(), off)
+    assert torch.equal(got.cpu(), product(av, wv, e_of).float().bfloat16())
+
+
+@pytest.mark.parametrize("counts,rows", [([60, 300, 0, 209, 70], 640), ([113, 225], 350), ([1, 1, 700, 2, 0], 704)])
+@pytest.mark.parametrize("n,k", [(256, 160), (1120, 96), (384, 1024), (288, 64)])
+def test_swiglu_many_rows_per_expert(w, counts, rows, n, k):
+    off, e_of = groups(counts, rows)
+    ac, ae, av = whole_mx((rows, k), 8)
+    gc, ge, gv = whole_mx((len(counts), n, k), 9)
+    uc, ue, uv = whole_mx((len(counts), n, k), 10)
+    ge, gv = ge - 10, gv * 2.0 ** -10
+    codes, scales = w.mxfp8_moe_swiglu(ac.cuda(), ae.cuda(), gc.cuda(), swizzle(ge).cuda(), uc.cuda(), swizzle(ue).cuda(), off)
+    g, u = product(av, gv, e_of), product(av, uv, e_of)
+    check_mx(g / (1 + torch.exp(-g)) * u, codes, scales.cpu().long(), 2.0 ** -20)
+
+
+@pytest.mark.parametrize("experts,rows,n", [(1024, 1300, 4096), (1, 150_000, 4096)])
+def test_more_tiles_than_are_listed_ahead(w, experts, rows, n):
+    """Over 128 tiles per block: those behind are found one by one."""
+    k = 32
+    g = torch.Generator().manual_seed(1)
+    cuts = torch.sort(torch.randint(0, rows + 1, (experts - 1,), generator=g)).values.tolist()
+    counts = [b - a for a, b in zip([0] + cuts, cuts + [rows])]
+    off, e_of = groups(counts, rows)
+    ac, ae, av = whole_mx((rows, k), 3)
+    v = torch.randint(-4, 5, (experts, n, k), generator=g, dtype=torch.int8).cuda()
+    wc = v.float().to(torch.float8_e4m3fn).view(torch.uint8)
+    ws = torch.zeros(experts, n // 128, 512, dtype=torch.uint8, device="cuda")
+    ws.view(experts, n // 128, 32, 4, 4)[..., 0] = 127               # one scale column of 1
+    got = w.mxfp8_moe_matmul(ac.cuda(), ae.cuda(), wc, ws.reshape(-1), off)
+    av, e_of = av.float().cuda(), e_of.cuda()
+    for r0 in range(0, rows, 10_000):
+        r = slice(r0, min(rows, r0 + 10_000))
+        if experts == 1:
+            want = av[r] @ v[0].float().T
+        else:
+            want = torch.einsum("rk,rnk->rn", av[r], v[e_of[r]].float())
+        assert torch.equal(got[r], want.bfloat16())
+
+
+def test_repeatable(w):
+    rows, n, k = 3000, 768, 1056
+    off, _ = groups([1000, 0, 1500, 100], rows)
+    g = torch.Generator().manual_seed(2)
+    wt = (torch.randn(4, n, k, generator=g) * 0.02).bfloat16().cuda()
+    wc, ws = w.mxfp8_quantize_swizzled(wt)
+    ac, ae, *_ = w.mxfp8_rmsnorm_quantize(torch.randn(rows, k, generator=g).bfloat16().cuda(),
+                                          torch.ones(k, dtype=torch.bfloat16, device="cuda"))
+    first = w.mxfp8_moe_matmul(ac, ae, wc, ws, off), *w.mxfp8_moe_swiglu(ac, ae, wc, ws, wc, ws, off)
+    for _ in range(5):
+        again = w.mxfp8_moe_matmul(ac, ae, wc, ws, off), *w.mxfp8_moe_swiglu(ac, ae, wc, ws, wc, ws, off)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))

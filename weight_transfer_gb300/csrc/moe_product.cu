@@ -40,25 +40,31 @@ constexpr int kMpRowBoxes = 6;
 constexpr uint32_t kMpTmemColumns = 512;
 constexpr unsigned kErrProductTimeout = 2u;
 
-// WT weight tensors (1: matmul, 2: gate and up); PAIR: the work of two CTAs.
-template <int WT, bool PAIR> struct MpShape {
+// How a call's CTAs work: singly with tiles of up to 32 rows (more and smaller
+// stages: the weights' latency counts), singly, or in pairs.
+enum MpKind { kMpFew, kMpSingle, kMpPair };
+
+// WT weight tensors (1: matmul, 2: gate and up).
+template <int WT, int KIND> struct MpShape {
+    static constexpr bool PAIR = KIND == kMpPair;
     static constexpr int kReaders = 8;                                      // warps that read the accumulators
     static constexpr int kThreads = 128 + 32 * kReaders;
-    static constexpr int kRows = WT == 2 ? 112 : PAIR ? 208 : 224;          // most rows of a tile
+    static constexpr int kRows = KIND == kMpFew ? 32 : WT == 2 ? 112 : PAIR ? 208 : 224;    // most rows of a tile
     static constexpr int kHeld = PAIR ? kRows / 2 : kRows;                  // rows of it in this CTA's shared memory
     // Rows are copied by one box a K step, the lowest of these that holds the tile's, in units of 16 (8 for a pair's half).
     static constexpr int kUnits = kRows / 16;
     static __host__ __device__ constexpr int box(int b) {
-        return b == 0 ? kUnits : b == 1 ? kUnits - 2 : b == 2 ? kUnits - 4 : b == 3 ? (kUnits + 1) / 2 : b == 4 ? (kUnits + 3) / 4 : 1;
+        const int u = b == 0 ? kUnits : b == 1 ? kUnits - 2 : b == 2 ? kUnits - 4 : b == 3 ? (kUnits + 1) / 2 : b == 4 ? (kUnits + 3) / 4 : 1;
+        return u > 1 ? u : 1;
     }
-    static constexpr int kStages = !PAIR ? 4 : WT == 1 ? 6 : 5;
+    static constexpr int kStages = KIND == kMpFew ? (WT == 1 ? 9 : 5) : KIND == kMpSingle ? 4 : WT == 1 ? 6 : 5;
     static constexpr int kHalves = 2;                                       // tiles whose accumulators fit TMEM
     static constexpr uint32_t kAccColumns = WT * kRows;                     // of one tile
     static constexpr uint32_t kScaleBase = kHalves * kAccColumns;           // scales behind them:
     static constexpr uint32_t kScaleColumns = 4 * WT + (kRows > 128 ? 8 : 4);   // of one stage
     static_assert(kScaleBase + kStages * kScaleColumns <= kMpTmemColumns, "tensor memory");
     static constexpr int kStageBytes = WT * 16384 + kHeld * 128;
-    static constexpr int kScaleBytes = WT * 512 + 1024;
+    static constexpr int kScaleBytes = WT * 512 + (kRows > 128 ? 1024 : 512);
     static constexpr int kOutBytes = WT == 1 ? kReaders * 2048 : 0;       // two 16-row staging areas per reading warp
     static constexpr int kBars = 2 * kStages + 4;
     static constexpr size_t kSmem = (size_t)kStages * (kStageBytes + kScaleBytes) + kOutBytes + kBars * 8 + 16 +
@@ -180,9 +186,10 @@ __device__ __forceinline__ bool mp_wait(uint64_t* bar, uint32_t parity) {
     return false;
 }
 
-template <int WT, bool PAIR>
-__global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_kernel(const __grid_constant__ MpArgs a) {
-    using S = MpShape<WT, PAIR>;
+template <int WT, int KIND>
+__global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_kernel(const __grid_constant__ MpArgs a) {
+    using S = MpShape<WT, KIND>;
+    constexpr bool PAIR = S::PAIR;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* sscale = smem + S::kStages * S::kStageBytes;
@@ -210,6 +217,7 @@ __global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_
         }
         fence_barrier_init();
     }
+    if (warp == 2 && lane < WT + kMpRowBoxes) prefetch_tmap(lane < WT ? &a.w[lane] : &a.rows[lane - WT]);
     if (warp == 3) {
         if (PAIR) tmem_alloc_pair(tmem_slot, kMpTmemColumns); else tmem_alloc(tmem_slot, kMpTmemColumns);
     }
@@ -378,9 +386,9 @@ __global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_
             const int64_t wsc = ((int64_t)d.e * a.feature_tiles + sft) * a.k_steps * 512 + lane * 16;
             constexpr int kWords = (S::kRows + 31) / 32;
             // Rows that are no multiple of 4 bytes long go through registers: K step kb's four bytes lie across the
-            // aligned words kb and kb + 1 behind the row's start; `low` is the former, `high` the latter, on its way
-            // since the step before.
-            uint32_t low[kWords], high[kWords];
+            // aligned words kb and kb + 1 behind the row's start; queue[c] holds the words kb .. kb + 3, so that a
+            // word is on its way for three steps.
+            uint32_t queue[kWords][4];
             const int64_t at0 = (int64_t)d.r0 * cols, start = at0 & ~(int64_t)3;
             const int64_t left = (int64_t)a.rows_total * cols - start;
             const auto word = [&](int c, int i) {
@@ -390,8 +398,8 @@ __global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_
             if (!words) {
 #pragma unroll
                 for (int c = 0; c < kWords; ++c) {
-                    low[c] = word(c, 0);
-                    high[c] = word(c, 1);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) queue[c][i] = word(c, i);
                 }
             }
             for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
@@ -417,11 +425,12 @@ __global__ void __launch_bounds__((MpShape<WT, PAIR>::kThreads), 1) moe_product_
 #pragma unroll
                     for (int c = 0; c < kWords; ++c) {
                         const int shift = (int)((at0 - start) + (int64_t)(lane + 32 * c) * cols) & 3;
-                        uint32_t w = __funnelshift_r(low[c], high[c], 8 * shift);
+                        uint32_t w = __funnelshift_r(queue[c][0], queue[c][1], 8 * shift);
                         if (cols - kb * 4 < 4) w &= (1u << (8 * (cols - kb * 4))) - 1u;
                         *reinterpret_cast<uint32_t*>(sc + (c >> 2) * 512 + (c & 3) * 4) = w;
-                        low[c] = high[c];
-                        high[c] = word(c, kb + 2);
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) queue[c][i] = queue[c][i + 1];
+                        queue[c][3] = word(c, kb + 4);
                     }
                     cp_async_arrive(&full[s]);  // the weights' scales
                     mbar_arrive(&full[s]);      // the stores above
@@ -597,9 +606,15 @@ static bool mp_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, con
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether the call's CTAs work in pairs (see the head of this file).
-static bool mp_pair(int64_t rows, int experts, int64_t feature_tiles) {
-    return rows / experts >= 64 && (feature_tiles % 2 == 0 || feature_tiles >= 8);
+// The kind for a call (see MpKind), by the mean number of rows per expert.
+// Measured with 78 experts (matmul 1760 x 768 / swiglu 768 x 2048): at 30 rows
+// 30.7 / 59.4 us in small tiles, 32.8 / 61.5 in pairs, 34.8 / 61.4 singly; at
+// 59 rows 36.9 / 63.4, 32.8 / 62.1 and 36.9 / 63.5.  A pair with an odd feature
+// tile out computes it for nothing, which only many tiles make up for.
+static MpKind mp_kind(int64_t rows, int experts, int64_t feature_tiles) {
+    const int64_t each = rows / experts;
+    if (each <= 48) return kMpFew;
+    return feature_tiles % 2 == 0 || feature_tiles >= 8 ? kMpPair : kMpSingle;
 }
 
 struct MpCall {
@@ -614,12 +629,12 @@ struct MpCall {
     uint8_t* out_scales;
 };
 
-template <int WT, bool PAIR>
+template <int WT, int KIND>
 static fp8q_status_t mp_start(const MpArgs& a, int64_t tiles, cudaStream_t stream);
 
 template <int WT>
 static fp8q_status_t mp_launch(const MpCall& c, cudaStream_t stream) {
-    if (c.rows < 0 || c.rows >= (int64_t)1 << 31 || c.experts < 1 || c.experts > kMpMaxExperts || c.n < 0)
+    if (c.rows < 0 || c.rows >= (int64_t)1 << 30 || c.experts < 1 || c.experts > kMpMaxExperts || c.n < 0)
         return FP8Q_ERR_SIZE;
     if (c.k <= 0 || c.k % MXFP8_BLOCK != 0 || (WT == 2 && c.n % MXFP8_BLOCK != 0)) return FP8Q_ERR_K;
     if (c.n >= (int64_t)1 << 31 || c.k >= (int64_t)1 << 31) return FP8Q_ERR_SIZE;
@@ -642,8 +657,8 @@ static fp8q_status_t mp_launch(const MpCall& c, cudaStream_t stream) {
     if (any_alias(outs, 2, ins, 7)) return FP8Q_ERR_ALIAS;
 
     const int64_t feature_tiles = (c.n + 127) / 128;
-    const bool pair = mp_pair(c.rows, c.experts, feature_tiles);
-    const int most = pair ? MpShape<WT, true>::kRows : MpShape<WT, false>::kRows;
+    const MpKind kind = mp_kind(c.rows, c.experts, feature_tiles);
+    const int most = kind == kMpFew ? MpShape<WT, kMpFew>::kRows : kind == kMpSingle ? MpShape<WT, kMpSingle>::kRows : MpShape<WT, kMpPair>::kRows;
     const int64_t row_tiles = c.rows / most + (c.rows < c.experts ? c.rows : c.experts) + 1;
     if (feature_tiles * row_tiles >= (int64_t)1 << 31) return FP8Q_ERR_SIZE;
     const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
@@ -656,8 +671,17 @@ static fp8q_status_t mp_launch(const MpCall& c, cudaStream_t stream) {
     for (int i = 0; i < WT; ++i)
         if (!mp_map(encode, &a.w[i], c.w[i], 3, wd, wst, 128)) return cuda_status(cudaErrorInvalidValue);
     if (WT == 1) a.w[1] = a.w[0];
-    for (int b = 0; b < kMpRowBoxes; ++b)
-        if (!mp_map(encode, &a.rows[b], c.codes, 2, rd, rst, pair ? MpShape<WT, true>::box(b) * 8 : MpShape<WT, false>::box(b) * 16)) return cuda_status(cudaErrorInvalidValue);
+    int height = 0;
+    for (int b = 0; b < kMpRowBoxes; ++b) {
+        const int h = kind == kMpFew      ? MpShape<WT, kMpFew>::box(b) * 16
+                      : kind == kMpSingle ? MpShape<WT, kMpSingle>::box(b) * 16
+                                          : MpShape<WT, kMpPair>::box(b) * 8;
+        if (h == height)
+            a.rows[b] = a.rows[b - 1];
+        else if (!mp_map(encode, &a.rows[b], c.codes, 2, rd, rst, h))
+            return cuda_status(cudaErrorInvalidValue);
+        height = h;
+    }
     a.w_scales[0] = c.ws[0];
     a.w_scales[1] = c.ws[1];
     a.row_scales = c.scales;
@@ -672,27 +696,31 @@ static fp8q_status_t mp_launch(const MpCall& c, cudaStream_t stream) {
     a.feature_tiles = (int)feature_tiles;
     a.k_steps = (int)((c.k + 127) / 128);
     const int64_t tiles = feature_tiles * row_tiles;
-    return pair ? mp_start<WT, true>(a, tiles, stream) : mp_start<WT, false>(a, tiles, stream);
+    switch (kind) {
+        case kMpFew: return mp_start<WT, kMpFew>(a, tiles, stream);
+        case kMpSingle: return mp_start<WT, kMpSingle>(a, tiles, stream);
+        default: return mp_start<WT, kMpPair>(a, tiles, stream);
+    }
 }
 
-template <int WT, bool PAIR>
+template <int WT, int KIND>
 static fp8q_status_t mp_start(const MpArgs& a, int64_t tiles, cudaStream_t stream) {
     static KernelCache kc;
     int resident = 0;
-    constexpr size_t kSmem = MpShape<WT, PAIR>::kSmem;
-    const fp8q_status_t st = prepare_kernel(kc, moe_product_kernel<WT, PAIR>, MpShape<WT, PAIR>::kThreads, kSmem, kSmem, &resident);
+    constexpr size_t kSmem = MpShape<WT, KIND>::kSmem;
+    const fp8q_status_t st = prepare_kernel(kc, moe_product_kernel<WT, KIND>, MpShape<WT, KIND>::kThreads, kSmem, kSmem, &resident);
     if (st != FP8Q_OK) return st;
-    if (!PAIR) return launch(moe_product_kernel<WT, PAIR>, grid_for((size_t)tiles, 1), MpShape<WT, PAIR>::kThreads, kSmem, stream, a);
+    if (KIND != kMpPair) return launch(moe_product_kernel<WT, KIND>, grid_for((size_t)tiles, 1), MpShape<WT, KIND>::kThreads, kSmem, stream, a);
     // as many pairs as are resident at once, since each walks over its own share of the tiles
     static std::atomic<int> cached[kMaxDevices];
     const int dev = current_device();
     const bool cache = dev >= 0 && dev < kMaxDevices;
     int pairs = cache ? cached[dev].load(std::memory_order_relaxed) : 0;
     if (pairs < 1) {
-        pairs = resident_clusters(moe_product_kernel<WT, PAIR>, 2, MpShape<WT, PAIR>::kThreads, kSmem);
+        pairs = resident_clusters(moe_product_kernel<WT, KIND>, 2, MpShape<WT, KIND>::kThreads, kSmem);
         if (cache) cached[dev].store(pairs, std::memory_order_relaxed);
     }
-    return launch_clusters(moe_product_kernel<WT, PAIR>, 2u * (unsigned)pairs, 2, MpShape<WT, PAIR>::kThreads, kSmem, stream, a);
+    return launch_clusters(moe_product_kernel<WT, KIND>, 2u * (unsigned)pairs, 2, MpShape<WT, KIND>::kThreads, kSmem, stream, a);
 }
 
 }  // namespace fp8q

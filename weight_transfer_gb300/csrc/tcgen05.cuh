@@ -181,6 +181,11 @@ __device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
         : "memory");
 }
 
+// Fetches a tensor map (a kernel parameter) ahead of its first copy.
+__device__ __forceinline__ void prefetch_tmap(const void* tmap) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
+}
+
 // 3D tiled bulk copy of the box at (x, y, z); x * element size must be a
 // multiple of 16 bytes, out-of-range elements read as zero.
 __device__ __forceinline__ void tma_3d_g2s(void* smem_dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
