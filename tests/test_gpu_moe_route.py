@@ -193,3 +193,30 @@ def test_other_stream(w):
         got = w.fp8q_moe_combine(y, slots2, off2)
     s.synchronize()
     assert torch.equal(got, want) and torch.equal(slots, slots2)
+
+
+def test_stream_argument(w):
+    """A stream passed to the calls, with outputs and workspaces made by them: nothing is reused while in use there."""
+    tokens, topk, experts = 20011, 8, 256
+    ids = ids_of(tokens, topk, experts, 1, "drop").cuda()
+    want = sort_ref(ids, experts)
+    x = torch.randn(1500, 1408, device="cuda").bfloat16()
+    rstd, wt = torch.rsqrt(x.float().square().mean(1)), torch.ones(1408, device="cuda").bfloat16()
+    ref = w.fp8q_rmsnorm_backward(x, x, wt, rstd)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for handle in (s, s.cuda_stream):
+        got, grads = [], []
+        for _ in range(4):
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(1_000_000)
+            got.append(w.fp8q_moe_sort(ids, experts, stream=handle))
+            grads.append(w.fp8q_rmsnorm_backward(x, x, wt, rstd, stream=handle))
+            for _ in range(8):                          # would take a workspace that is free too early
+                torch.full((tokens * 32,), -1, dtype=torch.int32, device="cuda")
+        s.synchronize()
+        for g in got:
+            for a, b in zip(g, want):
+                assert np.array_equal(a.cpu().numpy(), b)
+        for g in grads:
+            assert torch.equal(g[0], ref[0]) and torch.equal(g[1], ref[1])

@@ -694,10 +694,18 @@ def _in(t: Optional[torch.Tensor], what: str, dtype, shape) -> Optional[int]:
     return _dev(t, what, dtype)
 
 
-def _out(t: Optional[torch.Tensor], what: str, dtype, shape, device, numel: int):
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor from torch's allocator, which is told where the stream of use is not the current one."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None and t.numel():
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    return t
+
+
+def _out(t: Optional[torch.Tensor], what: str, dtype, shape, device, numel: int, stream):
     """(tensor, pointer) of an output: the caller's, checked, or a new one."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty(shape, dtype=dtype, device=device) if stream is None else _new(shape, dtype, device, stream)
         return t, t.data_ptr()
     return t, _dev(t, what, dtype, numel)
 
@@ -712,13 +720,13 @@ def _rmsnorm(name: str, fmt_or_flag: int, x, k, weight, eps, residual, want_bf16
     xp = _dev(x, "x", torch.bfloat16)
     sp = yp = dp = None
     if residual is not None or out_sum is not None:
-        out_sum, sp = _out(out_sum, "out_sum", torch.bfloat16, shape, dev, n)
-    codes, cp = _out(codes, "codes", torch.uint8, shape, dev, n)
-    scales, ap = _out(scales, "scales", scale_dtype, scale_shape, dev, scale_numel)
+        out_sum, sp = _out(out_sum, "out_sum", torch.bfloat16, shape, dev, n, stream)
+    codes, cp = _out(codes, "codes", torch.uint8, shape, dev, n, stream)
+    scales, ap = _out(scales, "scales", scale_dtype, scale_shape, dev, scale_numel, stream)
     if want_bf16 or out_bf16 is not None:
-        out_bf16, yp = _out(out_bf16, "out_bf16", torch.bfloat16, shape, dev, n)
+        out_bf16, yp = _out(out_bf16, "out_bf16", torch.bfloat16, shape, dev, n, stream)
     if want_rstd or rstd is not None:
-        rstd, dp = _out(rstd, "rstd", torch.float32, (rows,), dev, rows)
+        rstd, dp = _out(rstd, "rstd", torch.float32, (rows,), dev, rows, stream)
     st = getattr(_lib, name)(xp, rp, wp, rows, k, eps, fmt_or_flag, sp, yp, cp, ap, dp, _stream(stream))
     if st:
         _check(name, st)
@@ -775,10 +783,10 @@ def fp8q_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
     rp = _in(rstd, "rstd", torch.float32, (rows,))
     sp = _in(dsum, "dsum", torch.bfloat16, shape)
     need = _lib.fp8q_rmsnorm_backward_workspace_bytes(rows, k)
-    dx, xp = _out(dx, "dx", torch.bfloat16, shape, dev, rows * k)
-    dweight, dp = _out(dweight, "dweight", torch.float32, (k,), dev, k)
+    dx, xp = _out(dx, "dx", torch.bfloat16, shape, dev, rows * k, stream)
+    dweight, dp = _out(dweight, "dweight", torch.float32, (k,), dev, k, stream)
     if workspace is None:
-        workspace, have = torch.empty(need, dtype=torch.uint8, device=dev), need
+        workspace, have = _new(need, torch.uint8, dev, stream), need
     else:
         have = workspace.numel() * workspace.element_size()
     st = _lib.fp8q_rmsnorm_backward(gp, hp, wp, rp, sp, rows, k, xp, dp, _dev(workspace, "workspace"), have, _stream(stream))
@@ -803,14 +811,14 @@ def fp8q_moe_sort(ids: torch.Tensor, experts: int, offsets: Optional[torch.Tenso
         raise ValueError(f"ids must be int32 or int64, got {dtype}")
     n, dev = tokens * topk, ids.device
     ip = _dev(ids, "ids")
-    offsets, op = _out(offsets, "offsets", torch.int32, (experts + 1,), dev, experts + 1)
-    order, rp = _out(order, "order", torch.int32, (n,), dev, n)
-    slots, sp = _out(slots, "slots", torch.int32, (tokens, topk), dev, n)
+    offsets, op = _out(offsets, "offsets", torch.int32, (experts + 1,), dev, experts + 1, stream)
+    order, rp = _out(order, "order", torch.int32, (n,), dev, n, stream)
+    slots, sp = _out(slots, "slots", torch.int32, (tokens, topk), dev, n, stream)
     have = 0
     if workspace is None:
         have = _lib.fp8q_moe_sort_workspace_bytes(tokens, topk, experts)
         if have:
-            workspace = torch.empty(have, dtype=torch.uint8, device=dev)
+            workspace = _new(have, torch.uint8, dev, stream)
     else:
         have = workspace.numel() * workspace.element_size()
     st = _lib.fp8q_moe_sort(ip, 4 if dtype is torch.int32 else 8, tokens, topk, experts, op, rp, sp,
@@ -826,7 +834,7 @@ def fp8q_moe_gather(x: torch.Tensor, slots: torch.Tensor, offsets: torch.Tensor,
     tokens, topk = _rows_of(slots, "slots")
     k, n = x.shape[-1], tokens * topk
     xp = _in(x, "x", torch.bfloat16, (tokens, k))
-    rows, rp = _out(rows, "rows", torch.bfloat16, (n, k), x.device, n * k)
+    rows, rp = _out(rows, "rows", torch.bfloat16, (n, k), x.device, n * k, stream)
     st = _lib.fp8q_moe_gather(xp, _dev(slots, "slots", torch.int32), _dev(offsets, "offsets", torch.int32), tokens, topk,
                               offsets.numel() - 1, k, rp, _stream(stream))
     if st:
@@ -843,8 +851,8 @@ def mxfp8_moe_gather(codes: torch.Tensor, scales: torch.Tensor, slots: torch.Ten
     cols = k // MXFP8_BLOCK
     cp = _in(codes, "codes", torch.uint8, (tokens, k))
     sp = _in(scales, "scales", torch.uint8, (tokens, cols))
-    row_codes, rcp = _out(row_codes, "row_codes", torch.uint8, (n, k), dev, n * k)
-    row_scales, rsp = _out(row_scales, "row_scales", torch.uint8, (n, cols), dev, n * cols)
+    row_codes, rcp = _out(row_codes, "row_codes", torch.uint8, (n, k), dev, n * k, stream)
+    row_scales, rsp = _out(row_scales, "row_scales", torch.uint8, (n, cols), dev, n * cols, stream)
     st = _lib.mxfp8_moe_gather(cp, sp, _dev(slots, "slots", torch.int32), _dev(offsets, "offsets", torch.int32), tokens, topk,
                                offsets.numel() - 1, k, rcp, rsp, _stream(stream))
     if st:
@@ -861,7 +869,7 @@ def fp8q_moe_combine(y: torch.Tensor, slots: torch.Tensor, offsets: torch.Tensor
     k = y.shape[-1]
     yp = _in(y, "y", torch.bfloat16, (tokens * topk, k))
     wp = _in(weights, "weights", torch.float32, (tokens, topk))
-    out, op = _out(out, "out", torch.bfloat16, (tokens, k), y.device, tokens * k)
+    out, op = _out(out, "out", torch.bfloat16, (tokens, k), y.device, tokens * k, stream)
     st = _lib.fp8q_moe_combine(yp, _dev(slots, "slots", torch.int32), _dev(offsets, "offsets", torch.int32), wp, tokens, topk,
                                offsets.numel() - 1, k, op, _stream(stream))
     if st:
@@ -878,8 +886,8 @@ def fp8q_moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, slots: torch.
     gp = _in(dout, "dout", torch.bfloat16, (tokens, k))
     yp = _in(y, "y", torch.bfloat16, (n, k))
     wp = _in(weights, "weights", torch.float32, (tokens, topk))
-    dy, dp = _out(dy, "dy", torch.bfloat16, (n, k), dev, n * k)
-    dweights, dwp = _out(dweights, "dweights", torch.float32, (tokens, topk), dev, n)
+    dy, dp = _out(dy, "dy", torch.bfloat16, (n, k), dev, n * k, stream)
+    dweights, dwp = _out(dweights, "dweights", torch.float32, (tokens, topk), dev, n, stream)
     st = _lib.fp8q_moe_combine_backward(gp, yp, _dev(slots, "slots", torch.int32), _dev(offsets, "offsets", torch.int32), wp,
                                         tokens, topk, offsets.numel() - 1, k, dp, dwp, _stream(stream))
     if st:
@@ -903,7 +911,7 @@ def mxfp8_moe_matmul(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.T
     cp = _dev(codes, "codes", torch.uint8)
     sp = _in(scales, "scales", torch.uint8, (rows, k // MXFP8_BLOCK))
     wp, wsp = _expert_weights(w_codes, w_scales, "w_codes", experts, n, k)
-    out, op = _out(out, "out", torch.bfloat16, (rows, n), codes.device, rows * n)
+    out, op = _out(out, "out", torch.bfloat16, (rows, n), codes.device, rows * n, stream)
     st = _lib.mxfp8_moe_matmul(cp, sp, rows, wp, wsp, _dev(offsets, "offsets", torch.int32), experts, n, k, op,
                                _stream(stream))
     if st:
@@ -923,8 +931,8 @@ def mxfp8_moe_swiglu(codes: torch.Tensor, scales: torch.Tensor, gate_codes: torc
     gp, gsp = _expert_weights(gate_codes, gate_scales, "gate_codes", experts, n, k)
     up, usp = _expert_weights(up_codes, up_scales, "up_codes", experts, n, k)
     cols = n // MXFP8_BLOCK
-    out_codes, op = _out(out_codes, "out_codes", torch.uint8, (rows, n), dev, rows * n)
-    out_scales, osp = _out(out_scales, "out_scales", torch.uint8, (rows, cols), dev, rows * cols)
+    out_codes, op = _out(out_codes, "out_codes", torch.uint8, (rows, n), dev, rows * n, stream)
+    out_scales, osp = _out(out_scales, "out_scales", torch.uint8, (rows, cols), dev, rows * cols, stream)
     st = _lib.mxfp8_moe_swiglu(cp, sp, rows, gp, gsp, up, usp, _dev(offsets, "offsets", torch.int32), experts, n, k, op, osp,
                                _stream(stream))
     if st:

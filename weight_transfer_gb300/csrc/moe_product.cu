@@ -155,12 +155,20 @@ __device__ __forceinline__ uint32_t word_within(const uint8_t* p, int64_t at, in
 // 16 x 64-byte staging area; the exclusive or spreads 8 rows over all banks.
 __device__ __forceinline__ int out_stage_at(int r, int chunk) { return r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4); }
 
-// g / (1 + exp(-g)) * u.  The reciprocal is the hardware's (1 ulp, with
-// subnormal results); the result is about to be rounded to 8 bits.
-__device__ __forceinline__ float silu_times(float g, float u) {
-    float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, expf(-g))));
-    return __fmul_rn(__fmul_rn(g, r), u);
+// g / (1 + exp(-g)) * u of two values.  exp and the reciprocal are the
+// hardware's (2 ulp and 1 ulp, subnormal results kept); rounding the exponent's
+// product costs |g| * 2^-24 more, relative to exp(-g).  The result is about to
+// be rounded to 8 bits.
+__device__ __forceinline__ uint64_t silu_times2(uint64_t g, uint64_t u) {
+    constexpr float kLog2E = 1.44269504088896340736f;
+    float a, b;
+    f2_unpack(f2_mul(g, f2_pack(-kLog2E, -kLog2E)), a, b);
+    asm("ex2.approx.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.f32 %0, %0;" : "+f"(b));
+    f2_unpack(f2_add(f2_pack(a, b), f2_pack(1.0f, 1.0f)), a, b);
+    asm("rcp.approx.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.f32 %0, %0;" : "+f"(b));
+    return f2_mul(f2_mul(g, f2_pack(a, b)), u);
 }
 
 // One step of the 4 x 4 byte transpose of the words x and y over four lanes:
@@ -518,18 +526,25 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
                 for (int c0 = share * 16; c0 < d.rows; c0 += kStep) {
                     tmem_load_wait(g[0], g[1]);
                     tmem_load_wait(u[0], u[1]);
-                    // v[r][i]: row r = 2 h + j of this lane's four, feature p + 8 i
-                    float v[4][4];
-                    uint32_t top[4];
+                    // v[h][i]: rows c0 + 8 h + 2 q + {0, 1} (a register pair) of feature p + 8 i
+                    uint64_t v[2][4];
+                    uint32_t top[4];                                // of row r = 2 h + j of this lane's four
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        top[r] = 0u;
+                    for (int h = 0; h < 2; ++h) {
+                        float big[2] = {0.0f, 0.0f};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int at = 4 * (r >> 1) + 2 * (i & 1) + (r & 1);
-                            v[r][i] = silu_times(__uint_as_float(g[i >> 1][at]), __uint_as_float(u[i >> 1][at]));
-                            top[r] = max(top[r], __float_as_uint(fabsf(v[r][i])));
+                            const int at = 4 * h + 2 * (i & 1);
+                            v[h][i] = silu_times2(
+                                f2_pack(__uint_as_float(g[i >> 1][at]), __uint_as_float(g[i >> 1][at + 1])),
+                                f2_pack(__uint_as_float(u[i >> 1][at]), __uint_as_float(u[i >> 1][at + 1])));
+                            float x, y;
+                            f2_unpack(v[h][i], x, y);
+                            big[0] = fmaxf(big[0], fabsf(x));
+                            big[1] = fmaxf(big[1], fabsf(y));
                         }
+                        top[2 * h] = __float_as_uint(big[0]);
+                        top[2 * h + 1] = __float_as_uint(big[1]);
                     }
                     fetch(c0 + kStep);
                     // the scale needs the exponent of the block's largest magnitude only: two rows' exponents per word
@@ -542,12 +557,19 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
                     int e8[4];
                     uint32_t w[4];                                  // byte i: feature p + 8 i
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int E = (int)((ex[r >> 1] >> (16 * (r & 1))) & 0xFFFFu);
-                        e8[r] = E > 8 ? E - 8 : 0;
-                        const float factor = __uint_as_float((uint32_t)(254 - e8[r]) << 23);
-                        w[r] = cvt_fp8x4<kE4M3>(__fmul_rn(v[r][0], factor), __fmul_rn(v[r][1], factor),
-                                                __fmul_rn(v[r][2], factor), __fmul_rn(v[r][3], factor));
+                    for (int h = 0; h < 2; ++h) {
+                        float factor[2], f[2][4];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int E = (int)((ex[h] >> (16 * j)) & 0xFFFFu);
+                            e8[2 * h + j] = E > 8 ? E - 8 : 0;
+                            factor[j] = __uint_as_float((uint32_t)(254 - e8[2 * h + j]) << 23);
+                        }
+                        const uint64_t both = f2_pack(factor[0], factor[1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f2_unpack(f2_mul(v[h][i], both), f[0][i], f[1][i]);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) w[2 * h + j] = cvt_fp8x4<kE4M3>(f[j][0], f[j][1], f[j][2], f[j][3]);
                     }
                     // 4 x 4 byte transposes over the lanes p, p ^ 1, p ^ 2, p ^ 3: byte b of the result is feature
                     // 8 (p % 4) + 4 (p / 4) + b, so that a word is four neighbours

@@ -42,8 +42,11 @@ struct SortArgs {
     int* slots;                 // [n]
 };
 
+// Past the first-level cache: the placing launch may read the ids before its
+// own dependency wait, which is what would make that cache's lines current.
 __device__ __forceinline__ int sort_key(const SortArgs& a, int64_t i) {
-    const int64_t id = a.id64 ? static_cast<const int64_t*>(a.ids)[i] : (int64_t)static_cast<const int*>(a.ids)[i];
+    const int64_t id = a.id64 ? (int64_t)__ldcg(static_cast<const long long*>(a.ids) + i)
+                              : (int64_t)__ldcg(static_cast<const int*>(a.ids) + i);
     return id >= 0 && id < a.experts ? (int)id : a.experts;
 }
 

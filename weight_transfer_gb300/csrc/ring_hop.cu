@@ -64,28 +64,9 @@ struct HopGroup {
     float nzero;           // -0.0f
 };
 
-// Packed two-lane binary32 arithmetic (PTX f32x2: one instruction for two
-// values, each lane rounded exactly as the scalar instruction would round it),
-// the widening add of a bf16 and a binary32, and the three-input maximum.
-// They take the hop from about 20.5 to 17 thread-instructions per element.
-__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
+// Packed two-lane arithmetic (f2_*), the widening add of a bf16 and a binary32,
+// and the three-input maximum take the hop from about 20.5 to 17
+// thread-instructions per element.
 // RN(bf16 + x): the bf16 widened exactly, then one rounded add.
 __device__ __forceinline__ float add_bf16_f32(uint16_t h, float x) {
     float r;
