@@ -11,7 +11,14 @@
 //     combine, backward dy[slots[t, j]] = w[t, j] * dout[t],  dw[t, j] = <dout[t], y[slots[t, j]]>
 // and the gradient of gather is combine without weights.
 //
-// The sort is bound by latency, the row movement by HBM.
+// The sort is bound by latency (65,536 choices in two launches: 12.3 us with
+// the launches' own time), the row movement by HBM.  8192 tokens to 8 of 128
+// experts, rows of 2048:
+//     gather   MXFP8 28 us: 138 MB written at 5.1 TB/s, what plain writes reach
+//              here (eleven shapes, bulk copies among them, 26.7 to 29.4 us)
+//     combine  50.3 us, 6.0 TB/s: 4 KB rows in random order (fourteen shapes of
+//              warps, columns and rows in flight, 50.3 to 53.4 us)
+//     backward 84 us, 6.8 TB/s
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 
@@ -21,6 +28,8 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopk = 32;
 
 // ------------------------------------------------------------------ sort ----
+// (One cluster of eight blocks instead of the two launches took 26.6 us against
+// 16.4 then: all its scattered stores leave through eight SMs.)
 // Blocks of kSortWarps warps own consecutive chunks of choices, and each warp
 // a consecutive segment of its block's chunk, taken 32 choices at a time.  A
 // choice's rank among equal keys is the number of equal keys in earlier

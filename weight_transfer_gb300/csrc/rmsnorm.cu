@@ -9,7 +9,12 @@
 // the unrounded sum h; only the stored sum is rounded to bf16.
 //
 // The work is bound by HBM: a row is read once and stays in registers between
-// the sum of squares and the output, and the next row is read meanwhile.
+// the sum of squares and the output, and the next row is read meanwhile (one
+// row per block without that took 110.6 us where this takes 100.4: 16,384 rows
+// of 4096 with residual, MXFP8 and bf16 outputs).  Back to back that case runs
+// at 6.3 TB/s (95.9 us, 93% of the measured copy rate); ncu counts 22
+// thread-instructions per element and 40% of the issue slots.  Few rows are
+// bound by latency, and below about 20 us by the caller's launches.
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 
@@ -204,6 +209,8 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormArgs a) {
 
 // ------------------------------------------------------------- gradient ----
 //   g = dy * w;  xhat = h * rstd;  dx = rstd * (g - xhat * mean(g * xhat)) + dsum;  dw = sum over rows of dy * xhat
+// 16,384 rows of 4096 with dsum take 88.3 us back to back (6.1 TB/s, 90% of the
+// copy rate), of which the second kernel has about 5.
 // Each thread keeps dw of its own columns in registers over all its rows; the
 // blocks' partial sums are joined in a fixed order by a second kernel, so the
 // result does not depend on timing.
