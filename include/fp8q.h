@@ -486,7 +486,7 @@ fp8q_status_t fp8q_moe_combine_backward(const void* dout_bf16, const void* y_bf1
  *                   decreasing; values outside [0, rows] count as the nearer
  *                   end, one below its predecessor as the predecessor
  * k: a positive multiple of 32; swiglu: n too (FP8Q_ERR_K).  experts: 1 ..
- * FP8Q_MOE_MAX_EXPERTS, rows < 2^30 (FP8Q_ERR_SIZE).  rows == 0 or n == 0 is a
+ * FP8Q_MOE_MAX_EXPERTS, rows < 2^30, k < 2^28 (FP8Q_ERR_SIZE).  rows == 0 or n == 0 is a
  * no-op. */
 fp8q_status_t mxfp8_moe_matmul(const uint8_t* codes, const uint8_t* scales, int64_t rows, const uint8_t* w_codes,
                                const uint8_t* w_scales, const int32_t* offsets, int experts, int64_t n, int64_t k,

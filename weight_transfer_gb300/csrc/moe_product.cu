@@ -153,14 +153,40 @@ struct MpTiles {
     __device__ __forceinline__ bool none() const { return d.e >= a.experts; }
 };
 
-// The aligned word at byte `at` (a multiple of 4) of an array of `left` bytes; bytes past its end are 0.
-__device__ __forceinline__ uint32_t word_within(const uint8_t* p, int64_t at, int64_t left) {
-    if (at + 4 <= left) return *reinterpret_cast<const uint32_t*>(p + at);
-    uint32_t w = 0;
-    for (int j = 0; j < 4; ++j)
-        if (at + j < left) w |= (uint32_t)p[at + j] << (8 * j);
-    return w;
-}
+// The scales of a tile's rows whose length is no multiple of 4 bytes: lane l
+// holds rows l, l + 32, ... (C of them).  K step kb's four bytes of a row lie
+// across the aligned words kb and kb + 1 behind the row's start.
+template <int C>
+struct MpScaleRows {
+    const uint8_t* base;                        // the aligned word where the tile's first row begins
+    uint32_t end;                               // bytes from there to the end of the array (as far as 32 bits reach)
+    uint32_t at[C];                             // of each row's start from there; ~0 for no row
+
+    __device__ __forceinline__ void open(const MpArgs& a, const MpTile& t, int lane) {
+        const int64_t cols = a.k >> 5, first = t.r0 * cols, left = a.rows_total * cols - (first & ~(int64_t)3);
+        base = a.row_scales + (first & ~(int64_t)3);
+        end = left < 0xFFFFFFF0ll ? (uint32_t)left : 0xFFFFFFF0u;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            at[c] = lane + 32 * c < t.rows ? (uint32_t)(first & 3) + (uint32_t)(lane + 32 * c) * (uint32_t)cols : ~0u;
+    }
+    __device__ __forceinline__ int shift(int c) const { return 8 * (int)(at[c] & 3u); }
+    // Words i .. i + N - 1 of row c; bytes past the array's end and rows that are none give 0.
+    template <int N> __device__ __forceinline__ void words(int c, int i, uint32_t* w) const {
+        const uint32_t o = (at[c] & ~3u) + 4u * (uint32_t)i;
+        if (at[c] != ~0u && o + 4u * N <= end) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) w[n] = *reinterpret_cast<const uint32_t*>(base + o + 4 * n);
+            return;
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            w[n] = 0u;
+            for (uint32_t j = 0; at[c] != ~0u && j < 4; ++j)
+                if (o + 4 * n + j < end) w[n] |= (uint32_t)base[o + 4 * n + j] << (8 * j);
+        }
+    }
+};
 
 // Byte of 16-byte chunk `chunk` (8 features) of row r in a reading warp's
 // 16 x 64-byte staging area; the exclusive or spreads 8 rows over all banks.
@@ -225,9 +251,9 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
 
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
-            // the copying thread and the scale warp's lanes (twice, where they also store); for the first of a pair the
-            // second one's full stage, too
-            mbar_init(&full[s], 33 + ((a.k & 127) != 0 ? 32 : 0) + (PAIR && cluster_rank() == 0 ? 1 : 0));
+            // the copying thread and the scale warp's lanes (and the warp once more, where it also stores); for the first
+            // of a pair the second one's full stage, too
+            mbar_init(&full[s], 33 + ((a.k & 127) != 0 ? 1 : 0) + (PAIR && cluster_rank() == 0 ? 1 : 0));
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -394,65 +420,97 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
         // the scales: the weights' lie tiled, 16 bytes a lane; of the rows' lane l takes rows l, l + 32, ... of the
         // tile, whose words for one K step are 16 consecutive bytes of the tensor core's scale tile
         const int cols = a.k >> 5;
-        const bool words = (cols & 3) == 0;
+        constexpr int kWords = (S::kRows + 31) / 32;
         int it = 0;
         bool ok = usable;
-        for (; ok && tiles.here(); ++tiles.j) {
-            if (tiles.none()) continue;
-            const MpTile d = tiles.d;
-            const uint8_t* base = a.row_scales + (int64_t)d.r0 * cols;
+        // waits for the stage of this step, sends for its weight scales and gives the place of the rows'
+        const auto stage = [&](int64_t weights_at) -> uint8_t* {
+            const int s = it % S::kStages;
+            ok = __all_sync(0xFFFFFFFFu, mp_wait(&empty[s], (uint32_t)((it / S::kStages) & 1) ^ 1u));
+            uint8_t* sc = sscale + s * S::kScaleBytes + lane * 16;
+#pragma unroll
+            for (int i = 0; i < WT; ++i)
+                if (ok) cp_async16(sc + i * 512, a.w_scales[i] + weights_at);
+            return sc + WT * 512;
+        };
+        const auto weights_of = [&](const MpTile& d) {
             const int sft = d.ft < a.feature_tiles ? d.ft : a.feature_tiles - 1;    // an odd one out has no scales
-            const int64_t wsc = ((int64_t)d.e * a.feature_tiles + sft) * a.k_steps * 512 + lane * 16;
-            constexpr int kWords = (S::kRows + 31) / 32;
-            // Rows that are no multiple of 4 bytes long go through registers: K step kb's four bytes lie across the
-            // aligned words kb and kb + 1 behind the row's start; queue[c] holds the words kb .. kb + 3, so that a
-            // word is on its way for three steps.
-            uint32_t queue[kWords][4];
-            const int64_t at0 = (int64_t)d.r0 * cols, start = at0 & ~(int64_t)3;
-            const int64_t left = (int64_t)a.rows_total * cols - start;
-            const auto word = [&](int c, int i) {
-                const int r = lane + 32 * c;
-                return r < d.rows ? word_within(a.row_scales + start, (((at0 - start) + (int64_t)r * cols) & ~(int64_t)3) + 4 * i, left) : 0u;
-            };
-            if (!words) {
-#pragma unroll
-                for (int c = 0; c < kWords; ++c) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) queue[c][i] = word(c, i);
-                }
-            }
-            for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
-                const int s = it % S::kStages;
-                if (!__all_sync(0xFFFFFFFFu, mp_wait(&empty[s], (uint32_t)((it / S::kStages) & 1) ^ 1u))) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* sc = sscale + s * S::kScaleBytes + lane * 16;
-#pragma unroll
-                for (int i = 0; i < WT; ++i) cp_async16(sc + i * 512, a.w_scales[i] + wsc + kb * 512);
-                sc += WT * 512;
-                if (words) {
-                    // asynchronous 4-byte copies: this warp never waits for memory, only for a free stage
+            return ((int64_t)d.e * a.feature_tiles + sft) * a.k_steps * 512 + lane * 16;
+        };
+        if ((cols & 3) == 0) {
+            // asynchronous 4-byte copies: this warp never waits for memory, only for a free stage
+            for (; ok && tiles.here(); ++tiles.j) {
+                if (tiles.none()) continue;
+                const MpTile d = tiles.d;
+                const uint8_t* base = a.row_scales + (int64_t)d.r0 * cols;
+                const int64_t wsc = weights_of(d);
+                for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
+                    uint8_t* sc = stage(wsc + kb * 512);
+                    if (!ok) break;
 #pragma unroll
                     for (int c = 0; c < kWords; ++c) {
                         const int r = lane + 32 * c;
                         cp_async4(sc + (c >> 2) * 512 + (c & 3) * 4, r < d.rows ? base + ((int64_t)r * cols + kb * 4) : a.row_scales,
                                   r < d.rows ? 4 : 0);
                     }
-                    cp_async_arrive(&full[s]);
-                } else {
+                    cp_async_arrive(&full[it % S::kStages]);
+                }
+            }
+        } else {
+            // through registers, four K steps' words at a time, the next four (of this tile or the next) on their way
+            MpScaleRows<kWords> rows;
+            uint32_t now[kWords][5], then[kWords][5];
+            bool opened = false;
+            for (; ok && tiles.here(); ++tiles.j) {
+                if (tiles.none()) continue;
+                const MpTile d = tiles.d;
+                const int64_t wsc = weights_of(d);
+                if (!opened) {
+                    rows.open(a, d, lane);
 #pragma unroll
-                    for (int c = 0; c < kWords; ++c) {
-                        const int shift = (int)((at0 - start) + (int64_t)(lane + 32 * c) * cols) & 3;
-                        uint32_t w = __funnelshift_r(queue[c][0], queue[c][1], 8 * shift);
-                        if (cols - kb * 4 < 4) w &= (1u << (8 * (cols - kb * 4))) - 1u;
-                        *reinterpret_cast<uint32_t*>(sc + (c >> 2) * 512 + (c & 3) * 4) = w;
+                    for (int c = 0; c < kWords; ++c) rows.template words<5>(c, 0, now[c]);
+                    opened = true;
+                }
+                for (int kb0 = 0; ok && kb0 < a.k_steps; kb0 += 4) {
+                    int shift[kWords];
 #pragma unroll
-                        for (int i = 0; i < 3; ++i) queue[c][i] = queue[c][i + 1];
-                        queue[c][3] = word(c, kb + 4);
+                    for (int c = 0; c < kWords; ++c) shift[c] = rows.shift(c);
+                    if (kb0 + 4 < a.k_steps) {
+#pragma unroll
+                        for (int c = 0; c < kWords; ++c) {
+                            then[c][0] = now[c][4];
+                            rows.template words<4>(c, kb0 + 5, then[c] + 1);
+                        }
+                    } else {
+                        MpTiles<PAIR> behind = tiles;
+                        ++behind.j;
+                        if (behind.here() && !behind.none()) {
+                            rows.open(a, behind.d, lane);
+#pragma unroll
+                            for (int c = 0; c < kWords; ++c) rows.template words<5>(c, 0, then[c]);
+                        }
                     }
-                    cp_async_arrive(&full[s]);  // the weights' scales
-                    mbar_arrive(&full[s]);      // the stores above
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int kb = kb0 + q, left = cols - 4 * kb;
+                        if (left <= 0) break;
+                        uint8_t* sc = stage(wsc + kb * 512);
+                        if (!ok) break;
+                        const uint32_t mask = left < 4 ? (1u << (8 * left)) - 1u : ~0u;
+                        uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+                        for (int c = 0; c < kWords; ++c) w[c] = __funnelshift_r(now[c][q], now[c][q + 1], shift[c]) & mask;
+                        *reinterpret_cast<uint4*>(sc) = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (kWords > 4) *reinterpret_cast<uint4*>(sc + 512) = make_uint4(w[4], w[5], w[6], w[7]);
+                        cp_async_arrive(&full[it % S::kStages]);        // the weights' scales
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&full[it % S::kStages]);     // the stores above, of all lanes
+                        ++it;
+                    }
+#pragma unroll
+                    for (int c = 0; c < kWords; ++c)
+#pragma unroll
+                        for (int i = 0; i < 5; ++i) now[c][i] = then[c][i];
                 }
             }
         }
@@ -670,7 +728,7 @@ static fp8q_status_t mp_launch(const MpCall& c, cudaStream_t stream) {
     if (c.rows < 0 || c.rows >= (int64_t)1 << 30 || c.experts < 1 || c.experts > kMpMaxExperts || c.n < 0)
         return FP8Q_ERR_SIZE;
     if (c.k <= 0 || c.k % MXFP8_BLOCK != 0 || (WT == 2 && c.n % MXFP8_BLOCK != 0)) return FP8Q_ERR_K;
-    if (c.n >= (int64_t)1 << 31 || c.k >= (int64_t)1 << 31) return FP8Q_ERR_SIZE;
+    if (c.n >= (int64_t)1 << 31 || c.k >= (int64_t)1 << 28) return FP8Q_ERR_SIZE;
     if (c.n > 0 && (uint64_t)c.k > FP8Q_MAX_ELEMENTS / (uint64_t)c.n / (uint64_t)c.experts) return FP8Q_ERR_SIZE;
     const int64_t wide = c.n > c.k ? c.n : c.k;
     if (c.rows > 0 && (uint64_t)wide > FP8Q_MAX_ELEMENTS / (uint64_t)c.rows) return FP8Q_ERR_SIZE;
