@@ -268,13 +268,18 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
     }
     dependency_wait();
     allow_dependents();
+    // the offsets, taken into 0 .. rows: fetched by all threads at once, as one warp would wait for each 32 of them
+    for (int e = tid; e <= a.experts + 1; e += S::kThreads) {
+        const int o = e == 0 ? 0 : e <= a.experts ? a.offsets[e] : a.rows_total;
+        row_start[e] = max(0, min(o, a.rows_total));
+    }
+    __syncthreads();
     if (warp == 0) {
-        // the offsets, taken into 0 .. rows and not decreasing, whatever they hold; then the tiles before each expert
+        // ... and made not to decrease, whatever they hold; then the tiles before each expert
         int top = 0, run = 0;
         for (int e0 = 0; e0 <= a.experts + 1; e0 += 32) {
             const int e = e0 + lane;
-            int o = e == 0 ? 0 : e <= a.experts ? a.offsets[e] : a.rows_total;
-            o = max(0, min(o, a.rows_total));
+            int o = e <= a.experts + 1 ? row_start[e] : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int q = __shfl_up_sync(0xFFFFFFFFu, o, d);
