@@ -110,10 +110,10 @@ template <bool PAIR>
 __device__ __forceinline__ MpTile mp_find(const MpArgs& a, const int* prefix, const int* row_start, int j) {
     const int units = PAIR ? (a.feature_tiles + 1) >> 1 : a.feature_tiles;      // feature tiles, or pairs of them
     const int me = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x, all = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
-    const int64_t t = me + (int64_t)j * all;
+    const uint32_t t = (uint32_t)me + (uint32_t)j * (uint32_t)all;     // the host allows for fewer than 2^31 tiles
     MpTile d = {0, 0, 0, -1};
-    if (t >= (int64_t)prefix[a.experts + 1] * units) return d;
-    const int rt = (int)(t / units), unit = (int)(t - (int64_t)rt * units);
+    if (t >= (uint32_t)prefix[a.experts + 1] * (uint32_t)units) return d;
+    const int rt = (int)(t / (uint32_t)units), unit = (int)(t - (uint32_t)rt * (uint32_t)units);
     int lo = 0, hi = a.experts;                 // the last expert with prefix[.] <= rt
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -275,32 +275,33 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
     }
     __syncthreads();
     if (warp == 0) {
-        // ... and made not to decrease, whatever they hold; then the tiles before each expert
-        int top = 0, run = 0;
-        for (int e0 = 0; e0 <= a.experts + 1; e0 += 32) {
-            const int e = e0 + lane;
-            int o = e <= a.experts + 1 ? row_start[e] : 0;
+        // ... and made not to decrease, whatever they hold; then the tiles before each expert.  Each lane takes a run
+        // of neighbours, so that two scans over the warp are enough.
+        const int per = (a.experts + 2 + 31) >> 5, e0 = lane * per, e1 = min(e0 + per, a.experts + 2);
+        int top = 0;
+        for (int e = e0; e < e1; ++e) top = max(top, row_start[e]);
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int q = __shfl_up_sync(0xFFFFFFFFu, o, d);
-                if (lane >= d) o = max(o, q);
-            }
-            o = max(o, top);
-            int before = __shfl_up_sync(0xFFFFFFFFu, o, 1);
-            if (lane == 0) before = top;
-            top = __shfl_sync(0xFFFFFFFFu, o, 31);
-            int incl = (o - before + S::kRows - 1) / S::kRows;      // row tiles of expert e - 1
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int q = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-                if (lane >= d) incl += q;
-            }
-            if (e <= a.experts + 1) {
-                row_start[e] = o;
-                prefix[e] = run + incl;
-            }
-            run += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        for (int d = 1; d < 32; d <<= 1) {
+            const int q = __shfl_up_sync(0xFFFFFFFFu, top, d);
+            if (lane >= d) top = max(top, q);
         }
+        top = __shfl_up_sync(0xFFFFFFFFu, top, 1);
+        if (lane == 0) top = 0;
+        int run = 0;
+        for (int e = e0; e < e1; ++e) {
+            const int o = max(top, row_start[e]);
+            run += (o - top + S::kRows - 1) / S::kRows;             // row tiles of expert e - 1
+            row_start[e] = top = o;
+            prefix[e] = run;
+        }
+        int before = run;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int q = __shfl_up_sync(0xFFFFFFFFu, before, d);
+            if (lane >= d) before += q;
+        }
+        before -= run;
+        for (int e = e0; e < e1; ++e) prefix[e] += before;
     }
     __syncthreads();
     if (tid < kMpListed) listed[tid] = mp_find<PAIR>(a, prefix, row_start, tid);
