@@ -1,9 +1,10 @@
 """The expert-block operators together, through examples/moe_block.py.
 
-Serving: against the same block in 64 bits on the dequantized weights, where the only other errors are the roundings of
-activations to MXFP8 (e4m3, 3 mantissa bits: a uniform relative error of at most 2^-4, rms 2^-4 / sqrt(3) = 0.036 per
-rounding for values spread over a binade) at two places and bf16 at three: each output is a sum of many independent
-terms, so the relative error of the whole (2-norms) stays near sqrt(0.036^2 + 0.036^2) = 0.05, and 0.06 is asked.
+Serving: the block is the composition of its calls, bit for bit, and each stage is checked in 64 bits against the codes
+that the stage before it left, so that no bound has to allow for a rounding to 8 bits: gate/up codes are roundings of
+h64 within the products' accumulation error (k/32 + 1 steps of 2^-22 of the sum of magnitudes, on g and on u, carried
+through silu(g) * u with |silu'| <= 1.1) plus 2^-19 relative; the output is within half a bf16 step (2^-8) of each
+expert row and of itself.
 Training: the gradients against torch's own in 32 bits; bf16 roundings (2^-9) at about ten places in a row:
 10 * 2^-9 = 0.02."""
 import os
@@ -35,19 +36,37 @@ def test_serving(ex, tokens, experts, k, f, topk):
     x, res = (torch.randn(tokens, k, device="cuda").bfloat16() for _ in range(2))
     out, stream = block.forward(x, res)
     assert torch.equal(stream, (x.float() + res.float()).bfloat16())
-    h = x.double() + res.double()
-    y = h / torch.sqrt((h * h).mean(1, keepdim=True) + 1e-6) * norm_w.double()
-    _, _, _, y16, _ = w.mxfp8_rmsnorm_quantize(x, norm_w, residual=res, want_bf16=True)
+    codes, scales, stream2, y16, _ = w.mxfp8_rmsnorm_quantize(x, norm_w, residual=res, want_bf16=True)
     score, ids = torch.topk((y16 @ router.T).float(), topk, dim=1)       # the router's own choice
-    p = torch.softmax(score.double(), 1)
-    deq = [w.mxfp8_dequantize_swizzled(c, s).double() for c, s in (block.gate, block.up, block.down)]
-    want = torch.zeros(tokens, k, dtype=torch.float64, device="cuda")
-    for t in range(tokens):
-        for j in range(topk):
-            e = int(ids[t, j])
-            g, u = deq[0][e] @ y[t], deq[1][e] @ y[t]
-            want[t] += p[t, j] * (deq[2][e] @ (g * torch.sigmoid(g) * u))
-    assert rel(out, want) < 0.06
+    p = torch.softmax(score, 1)
+    off, order, slots = w.fp8q_moe_sort(ids, experts)
+    rows, row_scales = w.mxfp8_moe_gather(codes, scales, slots, off)
+    h, hs = w.mxfp8_moe_swiglu(rows, row_scales, *block.gate, *block.up, off)
+    y = w.mxfp8_moe_matmul(h, hs, *block.down, off)
+    assert torch.equal(stream, stream2) and torch.equal(out, w.fp8q_moe_combine(y, slots, off, p))
+
+    value = lambda c, e: c.view(torch.float8_e4m3fn).double() * (2.0 ** (e.double() - 127)).repeat_interleave(32, 1)  # noqa: E731
+    src = order.long() // topk
+    assert torch.equal(rows, codes[src]) and torch.equal(row_scales, scales[src])
+    e_of = ids.reshape(-1)[order.long()]
+    gate64, up64, down64 = (w.mxfp8_dequantize_swizzled(c, s).double() for c, s in (block.gate, block.up, block.down))
+    a, hv = value(rows, row_scales), value(h, hs)
+    h64, slack, y64, y_slack = (torch.zeros(len(src), n, dtype=torch.float64, device="cuda") for n in (f, f, k, k))
+    for e in range(experts):
+        m = e_of == e
+        g, u = a[m] @ gate64[e].T, a[m] @ up64[e].T
+        eps = (k / 32 + 1) * 2.0 ** -22
+        dg, du = eps * (a[m].abs() @ gate64[e].abs().T), eps * (a[m].abs() @ up64[e].abs().T)
+        h64[m] = g * torch.sigmoid(g) * u
+        slack[m] = 1.1 * dg * (u.abs() + du) + (g.abs() + dg) * du + 2.0 ** -19 * h64[m].abs()
+        y64[m] = hv[m] @ down64[e].T
+        y_slack[m] = (f / 32 + 1) * 2.0 ** -22 * (hv[m].abs() @ down64[e].abs().T)
+    step = 2.0 ** (hs.double() - 127).repeat_interleave(32, 1)           # value of code 1: codes are steps of 2^-3 of their
+    half = torch.maximum(hv.abs() * 2.0 ** -3, step * 2.0 ** -8) / 2      # power of two, at least 2^-9; half of one either way
+    assert ((hv - h64).abs() <= half + slack + (h64.abs() - 448 * step).clamp(min=0)).all()
+    assert ((y.double() - y64).abs() <= 2.0 ** -8 * y64.abs() + 2 * y_slack).all()
+    terms = y.double()[slots.long()] * p.double()[..., None]
+    assert ((out.double() - terms.sum(1)).abs() <= 2.0 ** -8 * terms.sum(1).abs() + topk * 2.0 ** -24 * terms.abs().sum(1)).all()
 
 
 def test_training(ex):
