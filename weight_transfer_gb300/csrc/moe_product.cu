@@ -28,9 +28,9 @@
 // warps for each quarter of the lanes, every other 16 rows each).
 //
 // Measured back to back, 128 experts: 65,533 rows through 2048 x 768 weights
-// 108 us (HBM alone needs 78; of 528 MB half are writes), 65,536 rows through
-// two 768 x 2048 weights 189 us, 2.2 PFLOP/s (169 us with pauses between, at a
-// higher clock), 512 rows through the same 63 us, 6.5 TB/s of weights.  The
+// 104 us (HBM alone needs 78; of 528 MB half are writes), 65,536 rows through
+// two 768 x 2048 weights 184 us, 2.2 PFLOP/s (166 us with pauses between, at a
+// higher clock), 512 rows through the same 60 us, 6.8 TB/s of weights.  The
 // prefill cases wait for a stage's round trip: five stages of 39 KB are on
 // their way, the tensor pipe is busy about half the time (profiled at 32
 // experts).  Tried and slower: weights multicast to two pairs (186 us against
