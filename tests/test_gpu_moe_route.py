@@ -96,7 +96,12 @@ def test_gather_mxfp8(w, tokens, topk, experts, k, how):
         assert torch.equal(g, want)
 
 
-@pytest.mark.parametrize("tokens,topk,experts,k,how", CASES)
+# few choices: a warp sums several 256-column pieces of a row, the last of them partly or wholly outside
+FEW = [(37, 1, 9, 4104, "drop"), (3, 1, 2, 1800, "any"), (50, 1, 4, 256, "drop"), (41, 2, 7, 2056, "drop"),
+       (19, 2, 3, 768, "any"), (29, 4, 11, 1032, "drop"), (23, 3, 5, 264, "any")]
+
+
+@pytest.mark.parametrize("tokens,topk,experts,k,how", CASES + FEW)
 @pytest.mark.parametrize("weighted", [False, True])
 def test_combine(w, tokens, topk, experts, k, how, weighted):
     ids, off, order, slots, n = routed(w, tokens, topk, experts, how)

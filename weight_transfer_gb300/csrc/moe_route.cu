@@ -285,14 +285,21 @@ struct CombineArgs {
     int64_t tokens;
     int topk;
     int k;
-    int segments;               // of 256 columns
+    int segments;               // of 256 * C columns (see moe_combine_kernel)
 };
 
+// A warp sums 256 * C columns of one token, 8 / C choices at a time: eight
+// 16-byte pieces per lane on their way, however few choices there are (us, with
+// C = 1 always -> with the C of fp8q_moe_combine: 22,255 tokens of 1600 columns,
+// one choice 79.8 -> 34.8; 12,000 of 2048, two choices 57.2 -> 32.8; 8,000 of
+// 2048, four 45.0 -> 32.8; 8,192 of 2048, six or eight 51.2 and 55.3 either way).
+template <int C>
 __global__ void __launch_bounds__(kRowWarps * 32) moe_combine_kernel(const CombineArgs a) {
+    constexpr int U = 8 / C;
     const int lane = (int)(threadIdx.x & 31u);
     const int64_t unit = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
     const int64_t t = unit / a.segments;
-    const int col = (int)(unit - t * a.segments) * 256 + lane * 8;
+    const int col0 = (int)(unit - t * a.segments) * (256 * C) + lane * 8;
     dependency_wait();
     allow_dependents();
     if (t >= a.tokens) return;
@@ -304,31 +311,42 @@ __global__ void __launch_bounds__(kRowWarps * 32) moe_combine_kernel(const Combi
         slot = a.slots[t * a.topk + lane];
         if (a.weights) w = a.weights[t * a.topk + lane];
     }
-    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    constexpr int U = 8;
+    float acc[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[c][i] = 0.0f;
     for (int j0 = 0; j0 < a.topk; j0 += U) {
-        uint4 v[U];
+        uint4 v[U][C];
         float wj[U];
-        bool live[U];
+        bool live[U][C];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = __shfl_sync(0xFFFFFFFFu, slot, (j0 + u) & 31);
             wj[u] = __shfl_sync(0xFFFFFFFFu, w, (j0 + u) & 31);
-            live[u] = j0 + u < a.topk && s >= 0 && s < routed && col < a.k;
-            if (live[u]) v[u] = ld_stream(a.y + (int64_t)s * a.k + col);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                live[u][c] = j0 + u < a.topk && s >= 0 && s < routed && col0 + c * 256 < a.k;
+                if (live[u][c]) v[u][c] = ld_stream(a.y + (int64_t)s * a.k + col0 + c * 256);
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (live[u]) {
-                float f[8];
-                unpack8(v[u], f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = __fmaf_rn(wj[u], f[i], acc[i]);
-            }
+            for (int c = 0; c < C; ++c)
+                if (live[u][c]) {
+                    float f[8];
+                    unpack8(v[u][c], f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[c][i] = __fmaf_rn(wj[u], f[i], acc[c][i]);
+                }
     }
-    if (col < a.k)
-        st_stream(a.out + t * a.k + col, make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
-                                                    pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7])));
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (col0 + c * 256 < a.k)
+            st_stream(a.out + t * a.k + col0 + c * 256,
+                      make_uint4(pack_bf16x2(acc[c][0], acc[c][1]), pack_bf16x2(acc[c][2], acc[c][3]),
+                                 pack_bf16x2(acc[c][4], acc[c][5]), pack_bf16x2(acc[c][6], acc[c][7])));
 }
 
 struct CombineGradArgs {
@@ -567,13 +585,18 @@ extern "C" fp8q_status_t fp8q_moe_combine(const void* y_bf16, const int32_t* slo
     const Range ins[] = {{y_bf16, 2 * n * (size_t)k}, {slots, 4 * n}, {offsets, 4 * (size_t)(experts + 1)}, {weights, 4 * n}};
     const Range out = {out_bf16, 2 * (size_t)(tokens * k)};
     if (any_alias(&out, 1, ins, 4)) return FP8Q_ERR_ALIAS;
-    const int segments = (int)((k + 255) / 256);
+    int wide = topk <= 1 ? 8 : topk <= 2 ? 4 : topk <= 4 ? 2 : 1;
+    while (wide > 1 && (wide / 2) * 256 >= k) wide /= 2;
+    const int segments = (int)((k + 256 * wide - 1) / (256 * wide));
     unsigned grid;
     const fp8q_status_t sg = units_grid(tokens * segments, &grid);
     if (sg != FP8Q_OK) return sg;
     const CombineArgs a = {static_cast<const uint16_t*>(y_bf16), slots, offsets + experts, weights,
                            static_cast<uint16_t*>(out_bf16), tokens, topk, (int)k, segments};
-    return launch(moe_combine_kernel, grid, kRowWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream), a);
+    return launch(wide == 8   ? moe_combine_kernel<8>
+                  : wide == 4 ? moe_combine_kernel<4>
+                  : wide == 2 ? moe_combine_kernel<2>
+                              : moe_combine_kernel<1>, grid, kRowWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream), a);
 }
 
 extern "C" fp8q_status_t fp8q_moe_combine_backward(const void* dout_bf16, const void* y_bf16, const int32_t* slots,
