@@ -76,9 +76,11 @@ template <int WT, int KIND> struct MpShape {
     static_assert(kScaleBase + kStages * kScaleColumns <= kMpTmemColumns, "tensor memory");
     static constexpr int kStageBytes = WT * 16384 + kHeld * 128;
     static constexpr int kScaleBytes = WT * 512 + (kRows > 128 ? 1024 : 512);
-    static constexpr int kOutBytes = WT == 1 ? kReaders * 2048 : 0;       // two 16-row staging areas per reading warp
+    // Staging of the outputs: two areas of 16 bf16 rows per reading warp (matmul), or one area of 16 code rows per reading
+    // warp and two of a tile's scale words (swiglu).
+    static constexpr int kOutBytes = WT == 1 ? kReaders * 2048 : kReaders * 608 + 2 * kRows * 4;
     static constexpr int kBars = 2 * kStages + 4;
-    static constexpr size_t kSmem = (size_t)kStages * (kStageBytes + kScaleBytes) + kOutBytes + kBars * 8 + 16 +
+    static constexpr size_t kSmem = (size_t)kStages * (kStageBytes + kScaleBytes) + (kOutBytes + 15) / 16 * 16 + kBars * 8 + 16 +
                                     kMpListed * 16 + 2 * (kMpMaxExperts + 2) * 4 + 1024;
     static_assert(kStageBytes % 1024 == 0 && kSmem <= 232448, "shared memory");
 };
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* sscale = smem + S::kStages * S::kStageBytes;
     uint8_t* sout = sscale + S::kStages * S::kScaleBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sout + S::kOutBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sout + (S::kOutBytes + 15) / 16 * 16);
     uint64_t* empty = full + S::kStages;
     uint64_t* acc_full = empty + S::kStages;
     uint64_t* acc_empty = acc_full + 2;
@@ -525,15 +527,16 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
         const int quarter = warp & 3, share = (warp - 4) >> 2;     // lanes, and which 16 rows out of every kStep
         constexpr int kStep = 16 * (S::kReaders / 4);
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        int tile = 0;
+        int tile = 0, scale_area = 0;
+        bool dead = false;
         for (; usable && tiles.here(); ++tiles.j) {
             const MpTile d = tiles.d;
             const bool zero = tiles.none();
             const int b = tile % S::kHalves;
-            if (!zero) {
-                if (!__all_sync(0xFFFFFFFFu, mp_wait(&acc_full[b], (uint32_t)((tile / S::kHalves) & 1)))) break;
-                tc_fence_after();
-            }
+            // a wait that ran out ends the output, not the walk: the reading warps meet at a barrier for every tile
+            if (!zero && !dead) dead = !__all_sync(0xFFFFFFFFu, mp_wait(&acc_full[b], (uint32_t)((tile / S::kHalves) & 1)));
+            if (!zero) tc_fence_after();
+            const int rows_here = dead ? 0 : d.rows;
             const uint32_t acc = tmem + (uint32_t)b * S::kAccColumns + lanes;
             const int f0 = d.ft * 128 + quarter * 32;
             const int64_t r0 = d.r0;
@@ -541,7 +544,7 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
                 int area = 0;
                 uint32_t lo[8], hi[8];                              // features 0..15 and 16..31 of the warp
                 const auto fetch = [&](int c) {
-                    if (!zero && c < d.rows) {
+                    if (!zero && c < rows_here) {
                         tmem_load_16x256b_x2(acc + c, lo);
                         tmem_load_16x256b_x2(acc + (16u << 16) + c, hi);
                     }
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
 #pragma unroll
                 for (int i = 0; i < 8; ++i) lo[i] = hi[i] = 0u;
                 fetch(share * 16);
-                for (int c0 = share * 16; c0 < d.rows; c0 += kStep, area ^= 1024) {
+                for (int c0 = share * 16; c0 < rows_here; c0 += kStep, area ^= 1024) {
                     uint8_t* stage = sout + (warp - 4) * 2048 + area;   // [16 rows][32 features] bf16
                     // register pair i of `lo` holds rows c0 + 8 * (i / 2) + 2 * (lane % 4) + {0, 1} of feature
                     // lane / 4 + 8 * (i % 2); stored transposed, 8 features are 16 bytes of an output row
@@ -571,7 +574,7 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
                         const int r = 8 * h + (lane >> 2), chunk = lane & 3;
                         const uint4 v = *reinterpret_cast<const uint4*>(stage + out_stage_at(r, chunk));
                         const int ff = f0 + chunk * 8;
-                        if (c0 + r < d.rows && ff < a.n) {
+                        if (c0 + r < rows_here && ff < a.n) {
                             uint16_t* o = a.out_bf16 + (r0 + c0 + r) * a.n + ff;
                             if ((a.n & 7) == 0)
                                 *reinterpret_cast<uint4*>(o) = v;
@@ -585,10 +588,10 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
                 // fragment order (see tmem_load_16x256b_x2): this lane holds rows c0 + 8 h + 2 q + j of features
                 // p + 8 i, q = lane % 4, p = lane / 4; the 8 lanes of one q hold the 32 features of their rows
                 const int q4 = lane & 3, p = lane >> 2;
-                const int64_t scale_cols = a.n >> 5;
+                uint8_t* tile_scales = sout + S::kReaders * 608 + scale_area * S::kRows * 4;
                 uint32_t g[2][8], u[2][8];
                 const auto fetch = [&](int c) {
-                    if (!zero && c < d.rows) {
+                    if (!zero && c < rows_here) {
                         tmem_load_16x256b_x2(acc + c, g[0]);
                         tmem_load_16x256b_x2(acc + (16u << 16) + c, g[1]);
                         tmem_load_16x256b_x2(acc + S::kRows + c, u[0]);
@@ -598,7 +601,7 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
 #pragma unroll
                 for (int i = 0; i < 8; ++i) g[0][i] = g[1][i] = u[0][i] = u[1][i] = 0u;
                 fetch(share * 16);
-                for (int c0 = share * 16; c0 < d.rows; c0 += kStep) {
+                for (int c0 = share * 16; c0 < rows_here; c0 += kStep) {
                     tmem_load_wait(g[0], g[1]);
                     tmem_load_wait(u[0], u[1]);
                     // v[h][i]: rows c0 + 8 h + 2 q + {0, 1} (a register pair) of feature p + 8 i
@@ -652,26 +655,43 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
                     transpose_step<0>(w[2], w[3], 4, (p & 1) != 0);
                     transpose_step<1>(w[0], w[1], 8, (p & 2) != 0);
                     transpose_step<1>(w[2], w[3], 8, (p & 2) != 0);
-                    if (f0 < a.n) {
-                        const int64_t row0 = r0 + c0 + 2 * q4;
-                        const int fo = f0 + 8 * (p & 3) + 4 * (p >> 2);
+                    // 16 rows of 32 bytes leave as one store of 16 bytes per lane, the scales below as words: with 4-byte
+                    // stores of codes and single bytes of scales the stores bounded short sums (22,529 rows, n 1856,
+                    // k 256: 86.0 -> 79.9 us; 65,536 rows, n 768: k 512 96.3 -> 90.1, k 2048 166.0 -> 164.0).  The row
+                    // pitch (8 words, and 8 more behind every fourth row) keeps both sides free of bank conflicts
+                    uint32_t* words = reinterpret_cast<uint32_t*>(sout + (warp - 4) * 608);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int c = 8 * (r >> 1) + (r & 1);
-                            if (c0 + 2 * q4 + c < d.rows)
-                                *reinterpret_cast<uint32_t*>(a.out_codes + (row0 + c) * a.n + fo) = w[r];
-                        }
-                        const int c = 8 * ((p >> 1) & 1) + (p & 1);   // lane p < 4 writes the scale of row r = p
-                        const int e = p == 0 ? e8[0] : p == 1 ? e8[1] : p == 2 ? e8[2] : e8[3];
-                        if (p < 4 && c0 + 2 * q4 + c < d.rows)
-                            a.out_scales[(row0 + c) * scale_cols + (f0 >> 5)] = (uint8_t)e;
+                    for (int r = 0; r < 4; ++r) {
+                        const int c = 8 * (r >> 1) + 2 * q4 + (r & 1);
+                        words[c * 8 + (c >> 2) * 8 + 2 * (p & 3) + (p >> 2)] = w[r];
                     }
+                    const int sr = 8 * ((p >> 1) & 1) + 2 * q4 + (p & 1);     // lane p < 4 has the scale of row r = p
+                    const int e = p == 0 ? e8[0] : p == 1 ? e8[1] : p == 2 ? e8[2] : e8[3];
+                    if (p < 4 && c0 + sr < rows_here) tile_scales[(c0 + sr) * 4 + quarter] = (uint8_t)e;
+                    __syncwarp();
+                    const int c = lane >> 1;
+                    if (f0 < a.n && c0 + c < rows_here)
+                        *reinterpret_cast<uint4*>(a.out_codes + (r0 + c0 + c) * a.n + f0 + 16 * (lane & 1)) =
+                            *reinterpret_cast<const uint4*>(words + c * 8 + (c >> 2) * 8 + 4 * (lane & 1));
+                    __syncwarp();
                 }
+                // the tile's scales, four neighbouring blocks' bytes a row at once: behind a barrier of the reading warps
+                // (the next tile's go to the other area, and are not read before the next barrier)
+                named_barrier(1, 32 * S::kReaders);
+                const int blocks = min(4, (a.n - d.ft * 128 + 31) >> 5);
+                for (int r = tid - 128; r < rows_here && blocks > 0; r += 32 * S::kReaders) {
+                    uint8_t* o = a.out_scales + (r0 + r) * (int64_t)(a.n >> 5) + d.ft * 4;
+                    if (blocks == 4 && (a.n & 127) == 0)
+                        *reinterpret_cast<uint32_t*>(o) = *reinterpret_cast<const uint32_t*>(tile_scales + r * 4);
+                    else
+                        for (int i = 0; i < blocks; ++i) o[i] = tile_scales[r * 4 + i];
+                }
+                scale_area ^= 1;
             }
             if (!zero) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
+                if (lane == 0 && !dead) {
                     if (PAIR) mbar_arrive_first(&acc_empty[b]); else mbar_arrive(&acc_empty[b]);
                 }
                 ++tile;

@@ -112,6 +112,11 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// Barrier `id` (1 to 15) of the block's `threads` threads that call it.
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // Four 8 x 8 matrices of 16-bit elements, stored transposed: lane l gives the
 // address of row l % 8 of matrix l / 8.
 __device__ __forceinline__ void stmatrix_x4_trans(void* smem_row, const uint32_t (&m)[4]) {
