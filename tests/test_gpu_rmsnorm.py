@@ -188,3 +188,38 @@ def test_other_stream(w):
         got = w.mxfp8_rmsnorm_quantize(x, wt, EPS, residual=r)
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want[:3], got[:3]))
+
+
+# rows of up to 128 elements share a warp, two to eight of them; here the last warp has some without a row
+SHORT = [(37, 32), (1001, 64), (515, 128), (9, 96), (5000, 32)]
+
+
+@pytest.mark.parametrize("rows,k", SHORT)
+@pytest.mark.parametrize("residual", [False, True])
+def test_short_rows(w, rows, k, residual):
+    test_mxfp8(w, rows, k, residual, False)
+    test_mxfp8(w, rows, k, residual, True)
+    test_gradient(w, rows, k, residual)
+    if k % 128 == 0:
+        test_blockwise(w, rows, k, "e4m3")
+
+
+@pytest.mark.parametrize("rows,k", [(37, 32), (51, 128), (9, 384), (5, 2048)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_do_not_meet(w, rows, k, bad):
+    """A row that holds NaN or an infinity leaves the others as they are, in both directions."""
+    x, r, wt = make(rows, k, rows + 5 * k)
+    dy = torch.randn_like(x)
+    x2 = x.clone()
+    x2[rows // 2, k // 3] = bad
+    keep = torch.arange(rows, device="cuda") != rows // 2
+    calls = [lambda t: w.mxfp8_rmsnorm_quantize(t, wt, EPS, residual=r, want_bf16=True, want_rstd=True)]
+    if k % 128 == 0:
+        calls.append(lambda t: w.fp8q_rmsnorm_quantize(t, wt, EPS, residual=r, want_bf16=True, want_rstd=True))
+    for call in calls:
+        for a, b in zip(call(x), call(x2)):
+            a, b = (t.view(torch.uint8).reshape(rows, -1) for t in (a, b))
+            assert torch.equal(a[keep], b[keep])
+    rstd = torch.rsqrt(x.float().square().mean(1) + EPS)
+    a, b = w.fp8q_rmsnorm_backward(dy, x, wt, rstd)[0], w.fp8q_rmsnorm_backward(dy, x2, wt, rstd)[0]
+    assert torch.equal(a[keep], b[keep])
