@@ -71,7 +71,12 @@ def routed(w, tokens, topk, experts, how):
     return ids, off, order, slots, int(off[-1])
 
 
-@pytest.mark.parametrize("tokens,topk,experts,k,how", CASES)
+# short rows, few choices: a warp has several tokens, the last one fewer
+SHORT = [(5, 1, 3, 256, "any"), (203, 1, 7, 64, "drop"), (77, 2, 9, 128, "drop"), (131, 2, 5, 480, "any"), (33, 2, 6, 512, "drop"),
+         (67, 1, 4, 672, "drop"), (45, 4, 8, 96, "drop")]
+
+
+@pytest.mark.parametrize("tokens,topk,experts,k,how", CASES + SHORT)
 def test_gather(w, tokens, topk, experts, k, how):
     ids, off, order, slots, n = routed(w, tokens, topk, experts, how)
     x = torch.randn(tokens, k, device="cuda").bfloat16()
@@ -82,7 +87,7 @@ def test_gather(w, tokens, topk, experts, k, how):
     assert torch.equal(got, want)
 
 
-@pytest.mark.parametrize("tokens,topk,experts,k,how", [(c[0], c[1], c[2], -(-c[3] // 32) * 32, c[4]) for c in CASES])
+@pytest.mark.parametrize("tokens,topk,experts,k,how", [(c[0], c[1], c[2], -(-c[3] // 32) * 32, c[4]) for c in CASES + SHORT])
 def test_gather_mxfp8(w, tokens, topk, experts, k, how):
     ids, off, order, slots, n = routed(w, tokens, topk, experts, how)
     codes = torch.randint(0, 256, (tokens, k), dtype=torch.uint8, device="cuda")
@@ -101,7 +106,7 @@ FEW = [(37, 1, 9, 4104, "drop"), (3, 1, 2, 1800, "any"), (50, 1, 4, 256, "drop")
        (19, 2, 3, 768, "any"), (29, 4, 11, 1032, "drop"), (23, 3, 5, 264, "any")]
 
 
-@pytest.mark.parametrize("tokens,topk,experts,k,how", CASES + FEW)
+@pytest.mark.parametrize("tokens,topk,experts,k,how", CASES + FEW + SHORT)
 @pytest.mark.parametrize("weighted", [False, True])
 def test_combine(w, tokens, topk, experts, k, how, weighted):
     ids, off, order, slots, n = routed(w, tokens, topk, experts, how)

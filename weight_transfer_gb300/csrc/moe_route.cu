@@ -196,9 +196,31 @@ __global__ void __launch_bounds__(kSortThreads) moe_sort_place_kernel(const Sort
     }
 }
 
+// Blocks of 4 warps: their turnover hides better than that of 8 (us back to back: combine of 8192 x 8 rows of 2048
+// 49.2 and 47.9, of 200,000 x 1 of 256 50.3 and 38.1).
+constexpr int kRowWarps = 4;
+
+// The work of this warp where `segments` warps in a row share one token (or
+// group of tokens): divisions in 32 bits, as the blocks fit into them.
+struct WarpUnit {
+    int64_t t;
+    int segment;
+    __device__ __forceinline__ explicit WarpUnit(int segments) {
+        const uint32_t s = (uint32_t)segments, warp = threadIdx.x >> 5;
+        const uint32_t q = blockIdx.x / s, r = (blockIdx.x - q * s) * kRowWarps + warp;
+        t = (int64_t)q * kRowWarps + r / s;
+        segment = (int)(r % s);
+    }
+};
+
 // ---------------------------------------------------------------- gather ----
 // A warp copies one 2 KB segment of one token's row to the slots of all its
-// choices: the row is read once however many experts take it.
+// choices: the row is read once however many experts take it.  Of short rows
+// with one or two choices it copies two or four at once (us back to back, MXFP8:
+// 200,000 x 1 rows of 256 71.9 -> 25.6, 65,536 x 2 of 512 30.5 -> 17.8; with
+// four choices or more it makes no difference).  The second launch bound lets
+// the compiler have the registers to keep all the loads ahead of the stores
+// (8192 x 8 rows of 2048: 25.4 -> 24.8; 5329 x 8 of 928: 13.3 -> 10.8).
 struct RowCopy {
     const uint8_t* src;
     uint8_t* dst;
@@ -213,65 +235,65 @@ struct GatherArgs {
     int segments;               // of 2 KB in a main row
 };
 constexpr int kSegBytes = 2048;
-constexpr int kRowWarps = 8;
 
-template <class T>
-__device__ __forceinline__ void copy_to_slots(const RowCopy& r, int64_t t, int64_t lo, int64_t hi, int slot, int topk,
-                                              int routed, int64_t n) {
-    const int lane = (int)(threadIdx.x & 31u);
-    const T* src = reinterpret_cast<const T*>(r.src + t * r.bytes);
-    constexpr int U = 4;
-    const int64_t e0 = lo / (int64_t)sizeof(T), e1 = hi / (int64_t)sizeof(T);
-    for (int64_t b = e0; b < e1; b += 32 * U) {
-        T v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (b + u * 32 + lane < e1) v[u] = src[b + u * 32 + lane];
-        for (int j = 0; j < topk; ++j) {
-            const int s = __shfl_sync(0xFFFFFFFFu, slot, j);
-            if (s < 0 || s >= n) continue;
-            T* dst = reinterpret_cast<T*>(r.dst + (int64_t)s * r.bytes);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (b + u * 32 + lane < e1) dst[b + u * 32 + lane] = s < routed ? v[u] : T{};
-        }
-    }
-}
-
-// Short rows (scales): the lanes share out all of the choices' pieces at once.
-template <class T>
-__device__ __forceinline__ void copy_short(const RowCopy& r, int64_t t, const int* slots, int topk, int routed, int64_t n) {
+// Short rows (scales) of `tokens` tokens from t0 on: the lanes share out all their choices' pieces at once.
+template <class T, bool ONE>
+__device__ __forceinline__ void copy_short(const RowCopy& r, int64_t t0, int tokens, const int* slots, int topk, int routed,
+                                           int64_t n) {
     const int lane = (int)(threadIdx.x & 31u);
     const int pieces = (int)(r.bytes / (int64_t)sizeof(T));
-    const T* src = reinterpret_cast<const T*>(r.src + t * r.bytes);
-    for (int u = lane; u < pieces * topk; u += 32) {
-        const int j = u / pieces, i = u - j * pieces;
-        const int s = slots[t * topk + j];
-        if (s >= 0 && s < n) reinterpret_cast<T*>(r.dst + (int64_t)s * r.bytes)[i] = s < routed ? src[i] : T{};
+    for (int u = lane; u < pieces * tokens * topk; u += 32) {
+        const int c = u / pieces, i = u - c * pieces;
+        const int s = slots[t0 * topk + c];
+        const int64_t t = t0 + (ONE ? 0 : c / topk);
+        if (s >= 0 && s < n)
+            reinterpret_cast<T*>(r.dst + (int64_t)s * r.bytes)[i] =
+                s < routed ? reinterpret_cast<const T*>(r.src + t * r.bytes)[i] : T{};
     }
 }
 
-__global__ void __launch_bounds__(kRowWarps * 32) moe_gather_kernel(const GatherArgs a) {
+template <int G>
+__global__ void __launch_bounds__(kRowWarps * 32, 1) moe_gather_kernel(const GatherArgs a) {
+    constexpr int U = 4, P = U / G;             // 512-byte pieces of a warp, and of a token
     const int lane = (int)(threadIdx.x & 31u);
-    const int64_t unit = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-    const int64_t t = unit / a.segments;
-    const int seg = (int)(unit - t * a.segments);
+    const WarpUnit unit(a.segments);
+    const int64_t t0 = unit.t * G;
     dependency_wait();
     allow_dependents();
-    if (t >= a.tokens) return;
+    if (t0 >= a.tokens) return;
     const int64_t n = a.tokens * a.topk;
     const int routed = *a.routed;
-    const int slot = lane < a.topk ? a.slots[t * a.topk + lane] : -1;
-    const int64_t lo = (int64_t)seg * kSegBytes;
-    const int64_t hi = lo + kSegBytes < a.main.bytes ? lo + kSegBytes : a.main.bytes;
-    copy_to_slots<uint4>(a.main, t, lo, hi, slot, a.topk, routed, n);
-    if (seg == 0 && a.extra.bytes > 0) {
+    const int tokens = a.tokens - t0 < G ? (int)(a.tokens - t0) : G;
+    const int slot = lane < tokens * a.topk ? a.slots[t0 * a.topk + lane] : -1;
+    const int64_t col = (int64_t)unit.segment * kSegBytes + lane * 16;
+    const uint8_t* src = a.main.src + t0 * a.main.bytes + col;
+    uint4 v[U];
+    bool ok[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        ok[u] = u / P < tokens && col + (u % P) * 512 < a.main.bytes;
+        if (ok[u]) v[u] = *reinterpret_cast<const uint4*>(src + (u / P) * a.main.bytes + (u % P) * 512);
+    }
+#pragma unroll 1
+    for (int j = 0; j < a.topk; ++j) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int s = __shfl_sync(0xFFFFFFFFu, slot, (g * a.topk + j) & 31);
+            if (g < tokens && s >= 0 && s < n) {
+                uint8_t* dst = a.main.dst + (int64_t)s * a.main.bytes + col;
+#pragma unroll
+                for (int u = g * P; u < (g + 1) * P; ++u)
+                    if (ok[u]) *reinterpret_cast<uint4*>(dst + (u % P) * 512) = s < routed ? v[u] : make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+    if (unit.segment == 0 && a.extra.bytes > 0) {
         if (a.extra.bytes % 16 == 0)
-            copy_short<uint4>(a.extra, t, a.slots, a.topk, routed, n);
+            copy_short<uint4, G == 1>(a.extra, t0, tokens, a.slots, a.topk, routed, n);
         else if (a.extra.bytes % 4 == 0)
-            copy_short<uint32_t>(a.extra, t, a.slots, a.topk, routed, n);
+            copy_short<uint32_t, G == 1>(a.extra, t0, tokens, a.slots, a.topk, routed, n);
         else
-            copy_short<uint8_t>(a.extra, t, a.slots, a.topk, routed, n);
+            copy_short<uint8_t, G == 1>(a.extra, t0, tokens, a.slots, a.topk, routed, n);
     }
 }
 
@@ -293,60 +315,72 @@ struct CombineArgs {
 // C = 1 always -> with the C of fp8q_moe_combine: 22,255 tokens of 1600 columns,
 // one choice 79.8 -> 34.8; 12,000 of 2048, two choices 57.2 -> 32.8; 8,000 of
 // 2048, four 45.0 -> 32.8; 8,192 of 2048, six or eight 51.2 and 55.3 either way).
-template <int C>
+// Of rows shorter than that it sums those of G tokens (200,000 x 1 of 256, back
+// to back: 89.1 -> 38.5; 65,536 x 2 of 512 38.9 and 38.0).
+template <int C, int G>
 __global__ void __launch_bounds__(kRowWarps * 32) moe_combine_kernel(const CombineArgs a) {
-    constexpr int U = 8 / C;
+    constexpr int U = 8 / (C * G);
     const int lane = (int)(threadIdx.x & 31u);
-    const int64_t unit = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-    const int64_t t = unit / a.segments;
-    const int col0 = (int)(unit - t * a.segments) * (256 * C) + lane * 8;
+    const WarpUnit unit(a.segments);
+    const int64_t t0 = unit.t * G;
+    const int col0 = unit.segment * (256 * C) + lane * 8;
     dependency_wait();
     allow_dependents();
-    if (t >= a.tokens) return;
+    if (t0 >= a.tokens) return;
     const int64_t n = a.tokens * a.topk;
     const int64_t routed = *a.routed < n ? *a.routed : n;
     int slot = -1;
     float w = 1.0f;
-    if (lane < a.topk) {
-        slot = a.slots[t * a.topk + lane];
-        if (a.weights) w = a.weights[t * a.topk + lane];
+    if (lane < G * a.topk && t0 * a.topk + lane < n) {
+        slot = a.slots[t0 * a.topk + lane];
+        if (a.weights) w = a.weights[t0 * a.topk + lane];
     }
-    float acc[C][8];
+    float acc[G][C][8];
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[c][i] = 0.0f;
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[g][c][i] = 0.0f;
     for (int j0 = 0; j0 < a.topk; j0 += U) {
-        uint4 v[U][C];
-        float wj[U];
-        bool live[U][C];
+        uint4 v[G][U][C];
+        float wj[G][U];
+        bool live[G][U][C];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = __shfl_sync(0xFFFFFFFFu, slot, (j0 + u) & 31);
-            wj[u] = __shfl_sync(0xFFFFFFFFu, w, (j0 + u) & 31);
+        for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                live[u][c] = j0 + u < a.topk && s >= 0 && s < routed && col0 + c * 256 < a.k;
-                if (live[u][c]) v[u][c] = ld_stream(a.y + (int64_t)s * a.k + col0 + c * 256);
-            }
-        }
+            for (int u = 0; u < U; ++u) {
+                const int s = __shfl_sync(0xFFFFFFFFu, slot, (g * a.topk + j0 + u) & 31);
+                wj[g][u] = __shfl_sync(0xFFFFFFFFu, w, (g * a.topk + j0 + u) & 31);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (live[u][c]) {
-                    float f[8];
-                    unpack8(v[u][c], f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[c][i] = __fmaf_rn(wj[u], f[i], acc[c][i]);
+                for (int c = 0; c < C; ++c) {
+                    live[g][u][c] = j0 + u < a.topk && s >= 0 && s < routed && col0 + c * 256 < a.k;
+                    if (live[g][u][c]) v[g][u][c] = ld_stream(a.y + (int64_t)s * a.k + col0 + c * 256);
                 }
+            }
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (live[g][u][c]) {
+                        float f[8];
+                        unpack8(v[g][u][c], f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) acc[g][c][i] = __fmaf_rn(wj[g][u], f[i], acc[g][c][i]);
+                    }
     }
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-        if (col0 + c * 256 < a.k)
-            st_stream(a.out + t * a.k + col0 + c * 256,
-                      make_uint4(pack_bf16x2(acc[c][0], acc[c][1]), pack_bf16x2(acc[c][2], acc[c][3]),
-                                 pack_bf16x2(acc[c][4], acc[c][5]), pack_bf16x2(acc[c][6], acc[c][7])));
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (t0 + g < a.tokens && col0 + c * 256 < a.k) {
+                const float(&f)[8] = acc[g][c];
+                st_stream(a.out + (t0 + g) * a.k + col0 + c * 256,
+                          make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                     pack_bf16x2(f[6], f[7])));
+            }
 }
 
 struct CombineGradArgs {
@@ -533,10 +567,13 @@ static fp8q_status_t gather_launch(GatherArgs a, int experts, cudaStream_t strea
     if (any_alias(outs, 2, ins, 4)) return FP8Q_ERR_ALIAS;
     a.routed += experts;
     a.segments = (int)((a.main.bytes + kSegBytes - 1) / kSegBytes);
+    // as many tokens per warp as its lanes hold rows and slots of
+    const int group = a.topk > 2 ? 1 : a.main.bytes <= kSegBytes / 4 ? 4 : a.main.bytes <= kSegBytes / 2 ? 2 : 1;
     unsigned grid;
-    const fp8q_status_t st = units_grid(a.tokens * a.segments, &grid);
+    const fp8q_status_t st = units_grid((a.tokens + group - 1) / group * a.segments, &grid);
     if (st != FP8Q_OK) return st;
-    return launch(moe_gather_kernel, grid, kRowWarps * 32, 0, stream, a);
+    return launch(group == 4 ? moe_gather_kernel<4> : group == 2 ? moe_gather_kernel<2> : moe_gather_kernel<1>, grid,
+                  kRowWarps * 32, 0, stream, a);
 }
 
 }  // namespace fp8q
@@ -585,18 +622,29 @@ extern "C" fp8q_status_t fp8q_moe_combine(const void* y_bf16, const int32_t* slo
     const Range ins[] = {{y_bf16, 2 * n * (size_t)k}, {slots, 4 * n}, {offsets, 4 * (size_t)(experts + 1)}, {weights, 4 * n}};
     const Range out = {out_bf16, 2 * (size_t)(tokens * k)};
     if (any_alias(&out, 1, ins, 4)) return FP8Q_ERR_ALIAS;
-    int wide = topk <= 1 ? 8 : topk <= 2 ? 4 : topk <= 4 ? 2 : 1;
+    const int pieces = topk <= 1 ? 8 : topk <= 2 ? 4 : topk <= 4 ? 2 : 1;      // C * G: all choices at once if topk <= 8
+    int wide = pieces;
     while (wide > 1 && (wide / 2) * 256 >= k) wide /= 2;
+    const int group = pieces / wide;
     const int segments = (int)((k + 256 * wide - 1) / (256 * wide));
     unsigned grid;
-    const fp8q_status_t sg = units_grid(tokens * segments, &grid);
+    const fp8q_status_t sg = units_grid((tokens + group - 1) / group * segments, &grid);
     if (sg != FP8Q_OK) return sg;
     const CombineArgs a = {static_cast<const uint16_t*>(y_bf16), slots, offsets + experts, weights,
                            static_cast<uint16_t*>(out_bf16), tokens, topk, (int)k, segments};
-    return launch(wide == 8   ? moe_combine_kernel<8>
-                  : wide == 4 ? moe_combine_kernel<4>
-                  : wide == 2 ? moe_combine_kernel<2>
-                              : moe_combine_kernel<1>, grid, kRowWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream), a);
+    void (*kernel)(const CombineArgs) = moe_combine_kernel<1, 1>;
+    switch (pieces * 16 + wide) {
+        case 8 * 16 + 8: kernel = moe_combine_kernel<8, 1>; break;
+        case 8 * 16 + 4: kernel = moe_combine_kernel<4, 2>; break;
+        case 8 * 16 + 2: kernel = moe_combine_kernel<2, 4>; break;
+        case 8 * 16 + 1: kernel = moe_combine_kernel<1, 8>; break;
+        case 4 * 16 + 4: kernel = moe_combine_kernel<4, 1>; break;
+        case 4 * 16 + 2: kernel = moe_combine_kernel<2, 2>; break;
+        case 4 * 16 + 1: kernel = moe_combine_kernel<1, 4>; break;
+        case 2 * 16 + 2: kernel = moe_combine_kernel<2, 1>; break;
+        case 2 * 16 + 1: kernel = moe_combine_kernel<1, 2>; break;
+    }
+    return launch(kernel, grid, kRowWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream), a);
 }
 
 extern "C" fp8q_status_t fp8q_moe_combine_backward(const void* dout_bf16, const void* y_bf16, const int32_t* slots,
