@@ -200,6 +200,14 @@ def test_swiglu_many_rows_per_expert(w, counts, rows, n, k):
     check_mx(g / (1 + torch.exp(-g)) * u, codes, scales.cpu().long(), 2.0 ** -20)
 
 
+@pytest.mark.parametrize("counts,rows", [([60, 300, 0, 209, 70], 640), ([49], 49), ([1, 1, 700, 2, 0], 704)])
+@pytest.mark.parametrize("n,k", [(256, 1056), (384, 1248), (1120, 1056), (96, 1952)])
+def test_long_odd_scale_rows(w, counts, rows, n, k):
+    """Scale rows of 33, 39 and 61 bytes, shared by two warps: pairs and single blocks, up to the arrays' last byte."""
+    test_matmul_many_rows_per_expert(w, counts, rows, n, k)
+    test_swiglu_many_rows_per_expert(w, counts, rows, n, k)
+
+
 @pytest.mark.parametrize("experts,rows,n", [(1024, 1300, 4096), (1, 150_000, 4096)])
 def test_more_tiles_than_are_listed_ahead(w, experts, rows, n):
     """Over 128 tiles per block: those behind are found one by one."""
