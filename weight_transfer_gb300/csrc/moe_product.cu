@@ -28,15 +28,16 @@
 // warps for each quarter of the lanes, every other 16 rows each).
 //
 // Measured back to back, 128 experts: 65,533 rows through 2048 x 768 weights
-// 104 us (HBM alone needs 78; of 528 MB half are writes), 65,536 rows through
-// two 768 x 2048 weights 184 us, 2.2 PFLOP/s (166 us with pauses between, at a
-// higher clock), 512 rows through the same 60 us, 6.8 TB/s of weights.  The
+// 107 us (97 from a graph; HBM alone needs 78; of 528 MB half are writes),
+// 65,536 rows through two 768 x 2048 weights 184 us, 2.2 PFLOP/s (164 us with
+// pauses between, at a higher clock), 512 rows through the same 60 us, 6.8 TB/s of weights.  The
 // prefill cases wait for a stage's round trip: five stages of 39 KB are on
 // their way, the tensor pipe is busy about half the time (profiled at 32
 // experts).  Tried and slower: weights multicast to two pairs (186 us against
 // 176 then), 208 rows per tile with one set of accumulators (211 against 173),
 // weights brought into L2 ahead (170 to 205 against 168), 16 reading warps
-// (matmul 114.7 against 108.5).
+// (matmul 114.7 against 108.5; gate/up 164.0 against 160.1, though 16.5 against
+// 18.6 for 6244 rows of k 320, whose epilogue they share).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -14,11 +14,11 @@
 // The sort is bound by latency (65,536 choices in two launches: 12.3 us with
 // the launches' own time), the row movement by HBM.  8192 tokens to 8 of 128
 // experts, rows of 2048:
-//     gather   MXFP8 28 us: 138 MB written at 5.1 TB/s, what plain writes reach
-//              here (eleven shapes, bulk copies among them, 26.7 to 29.4 us)
-//     combine  50.3 us, 6.0 TB/s: 4 KB rows in random order (fourteen shapes of
-//              warps, columns and rows in flight, 50.3 to 53.4 us)
-//     backward 84 us, 6.8 TB/s
+//     gather   MXFP8 24.8 us back to back: 138 MB written at 5.6 TB/s (bulk
+//              copies through shared memory and wider segments 26.7 to 29.4)
+//     combine  47.9 us, 6.3 TB/s: 4 KB rows in random order (fourteen shapes of
+//              warps, columns and rows in flight 50.3 to 53.4)
+//     backward 86 us, 6.7 TB/s
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 
