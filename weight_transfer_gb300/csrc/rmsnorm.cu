@@ -459,7 +459,9 @@ struct NormShape {
 // rows of 128, e4m3: 28.7 us; a warp each 55.4), rows of up to 128 chunks
 // (k <= 1024) to single warps.  Longer ones take a block of as many threads as
 // `v` chunks per thread need; with few rows a block has one chunk per thread, as
-// latency counts and nothing else runs.
+// latency counts and nothing else runs (us from a graph, one chunk and four:
+// 4 x 2048 1.5 and 1.8, 304 x 2048 1.8 and 2.0, 304 x 4096 2.4 and 2.4,
+// 450 x 4096 3.8 and 3.1).
 static NormShape norm_shape(int chunks, int64_t rows, int most_v) {
     int lanes = 4;
     while (lanes < 32 && lanes < chunks) lanes *= 2;
