@@ -215,6 +215,27 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _new(shape, dtype, device, stream, kept: bool = True) -> torch.Tensor:
+    """A tensor that a call on `stream` makes.  Where that is not the current
+    stream it comes from the passed stream's own memory: a block that was freed
+    on the current stream may still be in use by work queued there, which the
+    passed stream does not wait for.  What is `kept`, and not a workspace that
+    ends with the call, is recorded on the current stream, where the caller is
+    likely to read it: freed early, it is not reused before that has happened."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    current, handle = torch.cuda.current_stream(device), _stream(stream)
+    if handle == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):       # 0 and 1 are CUDA's names of the legacy default stream
+        stream = torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if kept and t.numel():
+        t.record_stream(current)
+    return t
+
+
 def fp8q_device_errors(clear: bool = True) -> int:
     """Synchronizes the device and returns the kernels' error bits (0 = none)."""
     v = ctypes.c_uint(0)
@@ -694,14 +715,6 @@ def _in(t: Optional[torch.Tensor], what: str, dtype, shape) -> Optional[int]:
     return _dev(t, what, dtype)
 
 
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """A tensor from torch's allocator, which is told where the stream of use is not the current one."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and t.numel():
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
-    return t
-
-
 def _out(t: Optional[torch.Tensor], what: str, dtype, shape, device, numel: int, stream):
     """(tensor, pointer) of an output: the caller's, checked, or a new one."""
     if t is None:
@@ -786,7 +799,7 @@ def fp8q_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
     dx, xp = _out(dx, "dx", torch.bfloat16, shape, dev, rows * k, stream)
     dweight, dp = _out(dweight, "dweight", torch.float32, (k,), dev, k, stream)
     if workspace is None:
-        workspace, have = _new(need, torch.uint8, dev, stream), need
+        workspace, have = _new(need, torch.uint8, dev, stream, kept=False), need
     else:
         have = workspace.numel() * workspace.element_size()
     st = _lib.fp8q_rmsnorm_backward(gp, hp, wp, rp, sp, rows, k, xp, dp, _dev(workspace, "workspace"), have, _stream(stream))
@@ -818,7 +831,7 @@ def fp8q_moe_sort(ids: torch.Tensor, experts: int, offsets: Optional[torch.Tenso
     if workspace is None:
         have = _lib.fp8q_moe_sort_workspace_bytes(tokens, topk, experts)
         if have:
-            workspace = _new(have, torch.uint8, dev, stream)
+            workspace = _new(have, torch.uint8, dev, stream, kept=False)
     else:
         have = workspace.numel() * workspace.element_size()
     st = _lib.fp8q_moe_sort(ip, 4 if dtype is torch.int32 else 8, tokens, topk, experts, op, rp, sp,
