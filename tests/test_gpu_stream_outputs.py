@@ -84,3 +84,46 @@ def check(call):
 @pytest.mark.parametrize("name", EXPERT)
 def test_expert_block(w, name):
     check(expert_calls(w)[name])
+
+
+def codec_calls(w):
+    g = torch.Generator().manual_seed(6)
+    n = 1 << 21
+    xs = [torch.randn(n, generator=g).bfloat16().cuda() for _ in range(2)]
+    q = [w.fp8q_quantize_blockwise(x) for x in xs]
+    codes, scales = [c for c, _ in q], [s for _, s in q]
+    hop = lambda: {"in_codes": codes[0], "in_scales": scales[0], "local": xs[1], "want_bf16": True}  # noqa: E731
+    wt = xs[0].view(4, 512, 1024)
+    wc, ws = w.mxfp8_quantize_swizzled(wt)
+    f32 = xs[0].float()
+    return {
+        "quantize": lambda **s: w.fp8q_quantize_blockwise(xs[0], **s),
+        "quantize_group": lambda **s: sum(w.fp8q_quantize_blockwise_group(xs, **s), []),
+        "quantize_tensorwise": lambda **s: w.fp8q_quantize_tensorwise(xs[0], **s),
+        "encode": lambda **s: (w.fp8q_encode_f32(f32, **s),),
+        "dequantize": lambda **s: w.fp8q_dequantize(codes[0], scales[0], want_bf16=True, **s),
+        "dequant_reduce": lambda **s: w.fp8q_dequant_reduce(codes, scales, **s),
+        "dequant_reduce_unfused": lambda **s: w.fp8q_dequant_reduce_unfused(codes, scales, **s),
+        "dequant_reduce_unfused_static": lambda **s: w.fp8q_dequant_reduce_unfused_static(
+            [c[:1 << 20] for c in codes], [t[:1 << 13] for t in scales], **s),
+        "ring_hop": lambda **s: w.fp8q_ring_hop(codes[0], scales[0], xs[1], want_bf16=True, **s),
+        "ring_hop_group": lambda **s: w.fp8q_ring_hop_group([hop()], **s)[0],
+        "ring_hop_bf16_requant": lambda **s: w.fp8q_ring_hop_bf16_requant(codes[0], scales[0], xs[1], want_bf16=True, **s),
+        "gather_decode": lambda **s: w.fp8q_gather_decode(codes[0], scales[0], 2, **s),
+        "ring_allreduce": lambda **s: w.fp8q_ring_allreduce_sim(xs, **s)[0],
+        "mx_quantize": lambda **s: w.mxfp8_quantize_swizzled(wt, **s),
+        "mx_quantize_group": lambda **s: sum(w.mxfp8_quantize_swizzled_group([wt, wt], **s), []),
+        "mx_dequantize": lambda **s: (w.mxfp8_dequantize_swizzled(wc, ws, **s),),
+        "mx_unswizzle": lambda **s: (w.mxfp8_unswizzle_scales(ws, 4, 512, 1024, **s),),
+        "mismatches": lambda **s: (w.fp8q_count_mismatches(xs[0], xs[1], **s),),
+    }
+
+
+CODEC = ["quantize", "quantize_group", "quantize_tensorwise", "encode", "dequantize", "dequant_reduce", "dequant_reduce_unfused",
+         "dequant_reduce_unfused_static", "ring_hop", "ring_hop_group", "ring_hop_bf16_requant", "gather_decode",
+         "ring_allreduce", "mx_quantize", "mx_quantize_group", "mx_dequantize", "mx_unswizzle", "mismatches"]
+
+
+@pytest.mark.parametrize("name", CODEC)
+def test_codec(w, name):
+    check(codec_calls(w)[name])

@@ -1,6 +1,7 @@
 """Where the calls take the memory of the outputs and workspaces that they make
 when a stream is passed: from that stream's own pool, whatever the current
 stream is.  Runs without a GPU, on stand-ins for torch's streams and allocator."""
+import ast
 import contextlib
 
 import pytest
@@ -68,3 +69,17 @@ def test_memory_of_the_current_stream(w, s):
 def test_legacy_default_stream(w, s):
     """Handles 0 and 1 both name the legacy default stream, whose memory is that of torch's default stream."""
     assert w._new((4, 5), torch.uint8, torch.device("cuda"), s).on == 0
+
+
+def test_every_call_takes_its_memory_there():
+    """No function of the binding that takes a stream asks torch for memory by itself."""
+    build_lib()
+    import weight_transfer_gb300 as m
+    with open(m.__file__) as f:
+        tree = ast.parse(f.read())
+    bad = []
+    for fn in tree.body:
+        if isinstance(fn, ast.FunctionDef) and fn.name not in ("_new", "_out") and "stream" in [a.arg for a in fn.args.args]:
+            bad += [f"{fn.name}: {ast.unparse(c)}" for c in ast.walk(fn) if isinstance(c, ast.Call)
+                    and isinstance(c.func, ast.Attribute) and isinstance(c.func.value, ast.Name) and c.func.value.id == "torch"]
+    assert not bad, bad

@@ -215,22 +215,23 @@ def _stream(stream) -> int:
     return int(stream)
 
 
-def _new(shape, dtype, device, stream, kept: bool = True) -> torch.Tensor:
+def _new(shape, dtype, device, stream, kept: bool = True, zero: bool = False) -> torch.Tensor:
     """A tensor that a call on `stream` makes.  Where that is not the current
     stream it comes from the passed stream's own memory: a block that was freed
     on the current stream may still be in use by work queued there, which the
     passed stream does not wait for.  What is `kept`, and not a workspace that
     ends with the call, is recorded on the current stream, where the caller is
     likely to read it: freed early, it is not reused before that has happened."""
+    make = torch.zeros if zero else torch.empty
     if stream is None or device.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
     current, handle = torch.cuda.current_stream(device), _stream(stream)
     if handle == current.cuda_stream:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):       # 0 and 1 are CUDA's names of the legacy default stream
         stream = torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = make(shape, dtype=dtype, device=device)
     if kept and t.numel():
         t.record_stream(current)
     return t
@@ -273,9 +274,9 @@ def fp8q_quantize_blockwise(x: torch.Tensor, fmt="e4m3", codes: Optional[torch.T
     """bf16 x -> (codes uint8 [n], scales float32 [ceil(n/128)])."""
     n = x.numel()
     if codes is None:
-        codes = torch.empty(n, dtype=torch.uint8, device=x.device)
+        codes = _new(n, torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty(max(fp8q_num_scales(n), 1), dtype=torch.float32, device=x.device)
+        scales = _new(max(fp8q_num_scales(n), 1), torch.float32, x.device, stream)
     st = lib().fp8q_quantize_blockwise_ex(_dev(x, "x", torch.bfloat16), n, _fmt(fmt),
                                           _dev(codes, "codes", torch.uint8, n),
                                           _dev(scales, "scales", torch.float32, fp8q_num_scales(n)), flags,
@@ -300,9 +301,8 @@ def fp8q_quantize_blockwise_group(xs: Sequence[torch.Tensor], fmt="e4m3", flags:
     outc, outs = [], []
     for i, x in enumerate(xs):
         n = x.numel()
-        c = codes[i] if codes is not None else torch.empty(n, dtype=torch.uint8, device=x.device)
-        sc = scales[i] if scales is not None else torch.empty(max(fp8q_num_scales(n), 1), dtype=torch.float32,
-                                                              device=x.device)
+        c = codes[i] if codes is not None else _new(n, torch.uint8, x.device, stream)
+        sc = scales[i] if scales is not None else _new(max(fp8q_num_scales(n), 1), torch.float32, x.device, stream)
         arr[i] = fp8q_quant_t(_dev(x, f"xs[{i}]", torch.bfloat16), n, _dev(c, f"codes[{i}]", torch.uint8, n),
                               _dev(sc, f"scales[{i}]", torch.float32, fp8q_num_scales(n)))
         outc.append(c)
@@ -331,9 +331,9 @@ def fp8q_dequant_reduce(codes: Sequence[torch.Tensor], scales: Sequence[torch.Te
         n = codes[0].numel()
     dev = codes[0].device
     if out_bf16 is None and want_bf16:
-        out_bf16 = torch.empty(n, dtype=torch.bfloat16, device=dev)
+        out_bf16 = _new(n, torch.bfloat16, dev, stream)
     if out_fp32 is None and want_fp32:
-        out_fp32 = torch.empty(n, dtype=torch.float32, device=dev)
+        out_fp32 = _new(n, torch.float32, dev, stream)
     cp = _ptr_array(codes, "codes", torch.uint8, n)
     sp = _ptr_array(scales, "scales", torch.float32, fp8q_num_scales(n))
     st = lib().fp8q_dequant_reduce_ex(cp, sp, k, n, _fmt(fmt), _dev(out_bf16, "out_bf16", torch.bfloat16, n),
@@ -355,11 +355,11 @@ def fp8q_ring_hop(in_codes: torch.Tensor, in_scales: torch.Tensor, local: torch.
     n = local.numel()
     dev = local.device
     if out_codes is None:
-        out_codes = torch.empty(n, dtype=torch.uint8, device=dev)
+        out_codes = _new(n, torch.uint8, dev, stream)
     if out_scales is None:
-        out_scales = torch.empty(max(fp8q_num_scales(n), 1), dtype=torch.float32, device=dev)
+        out_scales = _new(max(fp8q_num_scales(n), 1), torch.float32, dev, stream)
     if out_bf16 is None and want_bf16:
-        out_bf16 = torch.empty(n, dtype=torch.bfloat16, device=dev)
+        out_bf16 = _new(n, torch.bfloat16, dev, stream)
     nb = fp8q_num_scales(n)
     st = lib().fp8q_ring_hop(_dev(in_codes, "in_codes", torch.uint8, n), _dev(in_scales, "in_scales", torch.float32, nb),
                              _dev(local, "local", torch.bfloat16), n, _fmt(fmt),
@@ -382,9 +382,9 @@ def mxfp8_quantize_swizzled(w: torch.Tensor, codes: Optional[torch.Tensor] = Non
     dev = w.device
     sb = mxfp8_swizzled_scale_bytes(batch, m, k)
     if codes is None:
-        codes = torch.empty(w.shape, dtype=torch.uint8, device=dev)
+        codes = _new(w.shape, torch.uint8, dev, stream)
     if scales_swizzled is None:
-        scales_swizzled = torch.empty(max(sb, 16), dtype=torch.uint8, device=dev)
+        scales_swizzled = _new(max(sb, 16), torch.uint8, dev, stream)
     st = lib().mxfp8_quantize_swizzled(_dev(w, "w", torch.bfloat16), batch, m, k,
                                        _dev(codes, "codes", torch.uint8, batch * m * k),
                                        _dev(scales_swizzled, "scales_swizzled", torch.uint8, sb), _stream(stream))
@@ -410,14 +410,11 @@ def fp8q_ring_hop_group_ex(hops: Sequence[dict], fmt="e4m3", flags: int = 0, str
         loc = hp["local"]
         n = loc.numel()
         nb = fp8q_num_scales(n)
-        oc = hp.get("out_codes") if hp.get("out_codes") is not None else torch.empty(n, dtype=torch.uint8,
-                                                                                      device=loc.device)
-        os_ = hp.get("out_scales") if hp.get("out_scales") is not None else torch.empty(max(nb, 1),
-                                                                                        dtype=torch.float32,
-                                                                                        device=loc.device)
+        oc = hp.get("out_codes") if hp.get("out_codes") is not None else _new(n, torch.uint8, loc.device, stream)
+        os_ = hp.get("out_scales") if hp.get("out_scales") is not None else _new(max(nb, 1), torch.float32, loc.device, stream)
         ob = hp.get("out_bf16")
         if ob is None and hp.get("want_bf16"):
-            ob = torch.empty(n, dtype=torch.bfloat16, device=loc.device)
+            ob = _new(n, torch.bfloat16, loc.device, stream)
         arr[i] = fp8q_hop_t(_dev(hp["in_codes"], f"hops[{i}].in_codes", torch.uint8, n),
                             _dev(hp["in_scales"], f"hops[{i}].in_scales", torch.float32, nb),
                             _dev(loc, f"hops[{i}].local", torch.bfloat16), n,
@@ -443,10 +440,10 @@ def fp8q_ring_allreduce_sim(partials: Sequence[torch.Tensor], fmt="e4m3", result
     n = partials[0].numel()
     dev = partials[0].device
     if results is None:
-        results = [torch.empty(n, dtype=torch.bfloat16, device=dev) for _ in range(P)]
+        results = [_new(n, torch.bfloat16, dev, stream) for _ in range(P)]
     wb = int(lib().fp8q_ring_allreduce_workspace_bytes(P, n))
     if workspace is None:
-        workspace = torch.empty(max(wb, 16), dtype=torch.uint8, device=dev)
+        workspace = _new(max(wb, 16), torch.uint8, dev, stream, kept=False)
     pp = (_vp * P)(*[_dev(t, f"partials[{i}]", torch.bfloat16, n) for i, t in enumerate(partials)])
     rp = (_vp * P)(*[_dev(t, f"results[{i}]", torch.bfloat16, n) for i, t in enumerate(results)])
     wire = ctypes.c_uint64(0)
@@ -463,7 +460,7 @@ def fp8q_gather_decode(codes: torch.Tensor, scales: torch.Tensor, count: int, fm
     step of the ring AllReduce); mean=True divides by `count` first."""
     n = codes.numel()
     if outs is None:
-        outs = [torch.empty(n, dtype=torch.bfloat16, device=codes.device) for _ in range(count)]
+        outs = [_new(n, torch.bfloat16, codes.device, stream) for _ in range(count)]
     op = (_vp * count)(*[_dev(t, f"outs[{i}]", torch.bfloat16, n) for i, t in enumerate(outs)])
     st = lib().fp8q_gather_decode(_dev(codes, "codes", torch.uint8), _dev(scales, "scales", torch.float32,
                                                                            fp8q_num_scales(n)),
@@ -490,8 +487,8 @@ def mxfp8_quantize_swizzled_group(weights: Sequence[torch.Tensor], codes: Option
         else:
             raise ValueError("each weight must be 2D or 3D")
         sb = mxfp8_swizzled_scale_bytes(b, m, k)
-        c = codes[i] if codes is not None else torch.empty(w.shape, dtype=torch.uint8, device=w.device)
-        sc = scales[i] if scales is not None else torch.empty(max(sb, 16), dtype=torch.uint8, device=w.device)
+        c = codes[i] if codes is not None else _new(w.shape, torch.uint8, w.device, stream)
+        sc = scales[i] if scales is not None else _new(max(sb, 16), torch.uint8, w.device, stream)
         arr[i] = mxfp8_tensor_t(_dev(w, f"weights[{i}]", torch.bfloat16), b, m, k,
                                 _dev(c, f"codes[{i}]", torch.uint8, b * m * k),
                                 _dev(sc, f"scales[{i}]", torch.uint8, sb))
@@ -521,7 +518,7 @@ def mxfp8_dequantize_swizzled(codes: torch.Tensor, scales_swizzled: torch.Tensor
     """E4M3 codes [m, k] / [batch, m, k] + swizzled E8M0 bytes -> bf16 weights."""
     b, m, k = _mx_shape(codes)
     if out is None:
-        out = torch.empty(codes.shape, dtype=torch.bfloat16, device=codes.device)
+        out = _new(codes.shape, torch.bfloat16, codes.device, stream)
     st = lib().mxfp8_dequantize_swizzled(_dev(codes, "codes", torch.uint8),
                                          _dev(scales_swizzled, "scales_swizzled", torch.uint8,
                                               mxfp8_swizzled_scale_bytes(b, m, k)),
@@ -534,7 +531,7 @@ def mxfp8_unswizzle_scales(scales_swizzled: torch.Tensor, batch: int, m: int, k:
                            out: Optional[torch.Tensor] = None, stream=None):
     """Swizzled E8M0 bytes -> row-major uint8 [batch, m, k // 32]."""
     if out is None:
-        out = torch.empty((batch, m, k // 32), dtype=torch.uint8, device=scales_swizzled.device)
+        out = _new((batch, m, k // 32), torch.uint8, scales_swizzled.device, stream)
     st = lib().mxfp8_unswizzle_scales(_dev(scales_swizzled, "scales_swizzled", torch.uint8,
                                            mxfp8_swizzled_scale_bytes(batch, m, k)),
                                       batch, m, k, _dev(out, "out", torch.uint8, batch * m * (k // 32)),
@@ -550,7 +547,7 @@ def fp8q_count_mismatches(a: torch.Tensor, b: torch.Tensor, count: Optional[torc
     if b.numel() * b.element_size() != nbytes:
         raise ValueError("a and b must have the same byte size")
     if count is None:
-        count = torch.zeros(1, dtype=torch.int64, device=a.device)
+        count = _new(1, torch.int64, a.device, stream, zero=True)
     st = lib().fp8q_count_mismatches(_dev(a, "a"), _dev(b, "b"), nbytes, _dev(count, "count", torch.int64, 1),
                                      _stream(stream))
     _check("fp8q_count_mismatches", st)
@@ -562,9 +559,9 @@ def fp8q_quantize_tensorwise(x: torch.Tensor, fmt="e4m3", codes: Optional[torch.
     """bf16 x -> (codes uint8 [n], float32 [2] device tensor holding (scale, amax))."""
     n = x.numel()
     if codes is None:
-        codes = torch.empty(n, dtype=torch.uint8, device=x.device)
+        codes = _new(n, torch.uint8, x.device, stream)
     if scale_amax is None:
-        scale_amax = torch.empty(4, dtype=torch.float32, device=x.device)
+        scale_amax = _new(4, torch.float32, x.device, stream)
     st = lib().fp8q_quantize_tensorwise(_dev(x, "x", torch.bfloat16), n, _fmt(fmt),
                                         _dev(codes, "codes", torch.uint8, n),
                                         _dev(scale_amax, "scale_amax", torch.float32, 2), _stream(stream))
@@ -578,9 +575,9 @@ def fp8q_ring_hop_bf16_requant(in_codes: torch.Tensor, in_scales: torch.Tensor, 
     n = local.numel()
     dev = local.device
     nb = fp8q_num_scales(n)
-    oc = torch.empty(n, dtype=torch.uint8, device=dev)
-    os_ = torch.empty(max(nb, 1), dtype=torch.float32, device=dev)
-    ob = torch.empty(n, dtype=torch.bfloat16, device=dev) if want_bf16 else None
+    oc = _new(n, torch.uint8, dev, stream)
+    os_ = _new(max(nb, 1), torch.float32, dev, stream)
+    ob = _new(n, torch.bfloat16, dev, stream) if want_bf16 else None
     st = lib().fp8q_ring_hop_bf16_requant(_dev(in_codes, "in_codes", torch.uint8, n),
                                           _dev(in_scales, "in_scales", torch.float32, nb),
                                           _dev(local, "local", torch.bfloat16), n, _fmt(fmt), _dev(oc, "out_codes"),
@@ -617,7 +614,7 @@ def fp8q_copy_segments(segments: Sequence[tuple], stream=None):
 def fp8q_encode_f32(x: torch.Tensor, fmt="e4m3", codes: Optional[torch.Tensor] = None, stream=None):
     n = x.numel()
     if codes is None:
-        codes = torch.empty(n, dtype=torch.uint8, device=x.device)
+        codes = _new(n, torch.uint8, x.device, stream)
     st = lib().fp8q_encode_f32(_dev(x, "x", torch.float32), n, _fmt(fmt), _dev(codes, "codes", torch.uint8, n),
                                _stream(stream))
     _check("fp8q_encode_f32", st)
@@ -630,9 +627,9 @@ def fp8q_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt="e4m3", out_b
     n = codes.numel()
     dev = codes.device
     if out_bf16 is None and want_bf16:
-        out_bf16 = torch.empty(n, dtype=torch.bfloat16, device=dev)
+        out_bf16 = _new(n, torch.bfloat16, dev, stream)
     if out_fp32 is None and want_fp32:
-        out_fp32 = torch.empty(n, dtype=torch.float32, device=dev)
+        out_fp32 = _new(n, torch.float32, dev, stream)
     st = lib().fp8q_dequantize(_dev(codes, "codes", torch.uint8, n),
                                _dev(scales, "scales", torch.float32, fp8q_num_scales(n)), n, _fmt(fmt),
                                _dev(out_bf16, "out_bf16", torch.bfloat16, n), _dev(out_fp32, "out_fp32", torch.float32, n),
@@ -653,11 +650,11 @@ def fp8q_dequant_reduce_unfused(codes: Sequence[torch.Tensor], scales: Sequence[
     dev = codes[0].device
     stride = int(lib().fp8q_unfused_stride(n))
     if workspace is None:
-        workspace = torch.empty(max(k * stride, 1), dtype=torch.float32, device=dev)
+        workspace = _new(max(k * stride, 1), torch.float32, dev, stream, kept=False)
     if out_bf16 is None and want_bf16:
-        out_bf16 = torch.empty(n, dtype=torch.bfloat16, device=dev)
+        out_bf16 = _new(n, torch.bfloat16, dev, stream)
     if out_fp32 is None and want_fp32:
-        out_fp32 = torch.empty(n, dtype=torch.float32, device=dev)
+        out_fp32 = _new(n, torch.float32, dev, stream)
     cp = _ptr_array(codes, "codes", torch.uint8, n)
     sp = _ptr_array(scales, "scales", torch.float32, fp8q_num_scales(n))
     st = lib().fp8q_dequant_reduce_unfused(cp, sp, k, n, _fmt(fmt), _dev(workspace, "workspace", torch.float32, k * stride),
@@ -683,9 +680,9 @@ def fp8q_dequant_reduce_unfused_static(codes: Sequence[torch.Tensor], scales: Se
         n = codes[0].numel()
     dev = codes[0].device
     if out_bf16 is None and want_bf16:
-        out_bf16 = torch.empty(n, dtype=torch.bfloat16, device=dev)
+        out_bf16 = _new(n, torch.bfloat16, dev, stream)
     if out_fp32 is None and want_fp32:
-        out_fp32 = torch.empty(n, dtype=torch.float32, device=dev)
+        out_fp32 = _new(n, torch.float32, dev, stream)
     cp = _ptr_array(codes, "codes", torch.uint8, n)
     sp = _ptr_array(scales, "scales", torch.float32, fp8q_num_scales(n))
     st = lib().fp8q_dequant_reduce_unfused_static(cp, sp, k, n, _fmt(fmt),
