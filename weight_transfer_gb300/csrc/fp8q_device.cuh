@@ -265,15 +265,26 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
                  : "memory");
 }
 
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+// CLUSTER: some of the barrier's arrivals come from another block of the
+// cluster, whose writes before them the wait has to acquire.
+template <bool CLUSTER = false> __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
+    if (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
     return done != 0;
 }
 
@@ -290,13 +301,14 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // Waits until phase `parity` of the barrier has completed; false if that did
 // not happen within `limit_ns` (kWaitLimitNs for every kernel of the library;
 // the bounded-wait self-test passes a shorter limit).
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
-    if (mbar_test(bar, parity)) return true;
+    if (mbar_test<CLUSTER>(bar, parity)) return true;
     const uint64_t t0 = global_ns();
     for (;;) {
 #pragma unroll 1
         for (int i = 0; i < 256; ++i)
-            if (mbar_test(bar, parity)) return true;
+            if (mbar_test<CLUSTER>(bar, parity)) return true;
         if (global_ns() - t0 > limit_ns) return false;
     }
 }

@@ -228,8 +228,8 @@ __device__ __forceinline__ void transpose_step(uint32_t& x, uint32_t& y, int mas
     }
 }
 
-__device__ __forceinline__ bool mp_wait(uint64_t* bar, uint32_t parity) {
-    if (mbar_wait(bar, parity)) return true;
+template <bool CLUSTER = false> __device__ __forceinline__ bool mp_wait(uint64_t* bar, uint32_t parity) {
+    if (mbar_wait<CLUSTER>(bar, parity)) return true;
     raise_error(kErrProductTimeout);
     return false;
 }
@@ -366,7 +366,8 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
         }
     } else if (warp == 1 && PAIR && rank == 1) {
         if (elect_one()) {
-            // the pair's first CTA issues the products; it learns here that this one's stage is full
+            // the pair's first CTA issues the products; it learns here that this one's stage is full, and acquires
+            // what this one's scale warp stored
             int it = 0;
             bool ok = usable;
             for (; ok && tiles.here(); ++tiles.j) {
@@ -391,11 +392,11 @@ __global__ void __launch_bounds__((MpShape<WT, KIND>::kThreads), 1) moe_product_
                 const int b = tile % S::kHalves;
                 const uint32_t idesc = mx_instr_desc(PAIR ? 256 : 128, (d.rows + 15) & ~15);
                 const uint32_t acc = tmem + (uint32_t)b * S::kAccColumns;
-                if (!mp_wait(&acc_empty[b], (uint32_t)((tile / S::kHalves) & 1) ^ 1u)) break;
+                if (!mp_wait<PAIR>(&acc_empty[b], (uint32_t)((tile / S::kHalves) & 1) ^ 1u)) break;
                 tc_fence_after();
                 for (int kb = 0; kb < a.k_steps; ++kb, ++it) {
                     const int s = it % S::kStages;
-                    if (!mp_wait(&full[s], (uint32_t)((it / S::kStages) & 1))) {
+                    if (!mp_wait<PAIR>(&full[s], (uint32_t)((it / S::kStages) & 1))) {
                         ok = false;
                         break;
                     }

@@ -178,11 +178,16 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
         "h"(kPairMask)
         : "memory");
 }
-// Arrives on the barrier at this offset of the CTA of rank 0.
+// Arrives on the barrier at this offset of the CTA of rank 0, and releases to
+// the cluster what this CTA has stored in its shared memory, for a wait that
+// acquires it (an arrival without a scope orders its own CTA only).  The fence
+// is for shared memory alone: with mbarrier.arrive.release.cluster, which
+// releases global memory too, gate/up of 65,536 rows takes 419 us instead of 160.
 __device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
-        "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_addr(bar))
+        "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_addr(bar))
         : "memory");
 }
 
