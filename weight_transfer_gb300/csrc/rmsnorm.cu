@@ -192,10 +192,11 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormArgs a) {
         const float mean = __fmul_rn(g.sum(even + odd, red, slot), a.inv_k);
         const float rstd = __frsqrt_rn(mean + a.eps);
         if (g.t == 0 && a.rstd && live) a.rstd[row] = rstd;
-        const uint64_t rstd2 = f2_pack(rstd, rstd);
+        // h becomes y, or -y for the blockwise quotients, which then need no other negation
+        const uint64_t rstd2 = kMx ? f2_pack(rstd, rstd) : f2_pack(-rstd, -rstd);
         float m[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {           // h becomes y
+        for (int v = 0; v < V; ++v) {
             uint64_t f[4];
             unpack8(w[v], f);
             m[v] = 0.0f;
@@ -206,7 +207,11 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormArgs a) {
                 f2_unpack(h[v][i], y0, y1);
                 m[v] = fmaxf(m[v], fmaxf(fabsf(y0), fabsf(y1)));
             }
-            if (a.y && live && g.c0 + v * 32 < chunks) st_stream(a.y + base + v * 256, pack8(h[v]));
+            if (a.y && live && g.c0 + v * 32 < chunks) {
+                uint4 y = pack8(h[v]);
+                if (!kMx) y = make_uint4(y.x ^ 0x80008000u, y.y ^ 0x80008000u, y.z ^ 0x80008000u, y.w ^ 0x80008000u);
+                st_stream(a.y + base + v * 256, y);
+            }
         }
         uint8_t* codes = a.codes + base;
         const auto put = [&](int v, const float (&q)[8]) {
@@ -263,21 +268,37 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormArgs a) {
             const float s = block_scale<FMT>(top);
             const int own = lane & 15, c = g.c0 - own + own * 32;
             if (live && own < V && c < chunks) static_cast<float*>(a.scales)[row * scale_cols + (c >> 4)] = s;
-            // y itself carries some ulps, so that the quotient is y * RN(1 / s), within 1.5 ulp of y / s; a scale too
-            // small for that travels as -s
-            const float inv = s >= 0x1p-100f ? __frcp_rn(s) : s == 0.0f ? 1.0f : -s;    // an all-zero block keeps its zeros
+            // The code of the correctly rounded quotient y / s by one step of markstein_div in packed form, h holding
+            // -y.  For a binary32 y one step rounds a value within 2^-21 half-ulps of y / s, which can show in a code
+            // only beside a value between two codes; all such y and s are tried in tests/test_norm_quotient.py.
+            // y * RN(1 / s) alone misses ties (16,384 x 4096, e4m3 alone, back to back: 41.5 us without the step, 44.7
+            // with it, 48.1 with a second one; with residual 73.5 and 73.7).  An all-zero block keeps its zeros,
+            // divided by 1.
+            const float by = s == 0.0f ? 1.0f : s, inv = __frcp_rn(by);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float f = V == 1 ? inv : __shfl_sync(0xFFFFFFFFu, inv, (lane & 16) | v);
-                if (f >= 0.0f) {
-                    put_scaled(v, f);
-                } else {
-                    float y[8], q[8];
+                const float sv = V == 1 ? by : __shfl_sync(0xFFFFFFFFu, by, (lane & 16) | v);
+                const float yr = V == 1 ? inv : __shfl_sync(0xFFFFFFFFu, inv, (lane & 16) | v);
+                float q[8];
+                if (sv >= 0x1p-58f) {
+                    const uint64_t s2 = f2_pack(sv, sv), nyr2 = f2_pack(-yr, -yr);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) f2_unpack(h[v][i], y[2 * i], y[2 * i + 1]);
-                    block_quotients<2, 8>(y, -f, q);
-                    put(v, q);
+                    for (int i = 0; i < 4; ++i) {
+                        uint64_t q2 = f2_mul(h[v][i], nyr2);
+                        q2 = f2_fma(f2_fma(q2, s2, h[v][i]), nyr2, q2);
+                        f2_unpack(q2, q[2 * i], q[2 * i + 1]);
+                    }
+                } else {                        // too small for the steps (see block_quotients), or NaN
+                    float y[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f2_unpack(h[v][i], y[2 * i], y[2 * i + 1]);
+                        y[2 * i] = -y[2 * i];
+                        y[2 * i + 1] = -y[2 * i + 1];
+                    }
+                    block_quotients<2, 8>(y, sv, q);
                 }
+                put(v, q);
             }
         }
     }
