@@ -376,8 +376,10 @@ fp8q_status_t fp8q_copy_segments(const fp8q_copy_t* segs, int count, fp8q_stream
  * Arrays are row-major and dense; all arithmetic is binary32 and is rounded
  * once, where an output is stored, unless said otherwise.  No result depends
  * on timing: no sum is formed by atomics.  NaN and infinities are not looked
- * for: a row that holds one gives what the formula gives (a NaN code where
- * the value is NaN, the largest code where it is infinite). */
+ * for: a row that holds one gives what the formula gives.  In 8 bits a NaN has
+ * a NaN code.  An infinite value has the largest code under the largest scale
+ * in MXFP8; blockwise, the scale and all codes of its block are NaN, as the
+ * quotients by an infinite scale are. */
 
 /* Residual addition, root-mean-square norm and quantization of `rows` rows:
  *     h = x + residual;  rstd = 1 / sqrt(mean(h^2) + eps);  y = (h * rstd) * weight

@@ -57,3 +57,36 @@ def test_codes_are_the_quantizers(w, rows, k, fmt, residual):
         ec, es = w.fp8q_quantize_blockwise(want.bfloat16(), fmt)
         assert torch.equal(scales.reshape(-1).view(torch.int32), es.view(torch.int32))
         assert torch.equal(codes.reshape(-1), ec)
+
+
+@pytest.mark.parametrize("rows,k", [(3, 128), (5, 512), (2, 2048), (400, 2048)])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_infinite_weight(w, rows, k, fmt):
+    """An infinite y makes its block's scale and codes NaN; the other blocks are as they are without it."""
+    sign = torch.where(torch.rand(rows, k, generator=torch.Generator().manual_seed(1)) < 0.5, -2.0, 2.0).bfloat16().cuda()
+    wt = torch.randn(k, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    bad = wt.clone()
+    bad[k - 5] = float("inf")
+    good_c, good_s, *_ = w.fp8q_rmsnorm_quantize(sign, wt, 0.0, fmt)
+    codes, scales, *_ = w.fp8q_rmsnorm_quantize(sign, bad, 0.0, fmt)
+    assert torch.equal(codes[:, :k - 128], good_c[:, :k - 128]) and torch.equal(scales[:, :-1], good_s[:, :-1])
+    assert scales[:, -1].isnan().all()
+    dtype = torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2
+    assert codes[:, k - 128:].view(dtype).float().isnan().all()
+
+
+@pytest.mark.parametrize("rows,k", [(3, 128), (5, 512), (2, 2048), (400, 2048)])
+def test_infinite_weight_mxfp8(w, rows, k):
+    """An infinite y is the largest code under the largest scale; the other blocks are as they are without it."""
+    sign = torch.where(torch.rand(rows, k, generator=torch.Generator().manual_seed(1)) < 0.5, -2.0, 2.0).bfloat16().cuda()
+    wt = torch.randn(k, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    bad = wt.clone()
+    bad[k - 5] = float("inf")
+    good_c, good_s, *_ = w.mxfp8_rmsnorm_quantize(sign, wt, 0.0)
+    codes, scales, *_ = w.mxfp8_rmsnorm_quantize(sign, bad, 0.0)
+    assert torch.equal(codes[:, :k - 32], good_c[:, :k - 32]) and torch.equal(scales[:, :-1], good_s[:, :-1])
+    assert (scales[:, -1] == 247).all()
+    top = codes[:, k - 5].view(torch.float8_e4m3fn).float()
+    assert torch.equal(top, 448 * sign[:, k - 5].float().sign())
+    rest = torch.cat([codes[:, k - 32:k - 5], codes[:, k - 4:]], 1).view(torch.float8_e4m3fn).float()
+    assert (rest == 0).all()
