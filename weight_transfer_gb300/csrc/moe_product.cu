@@ -197,7 +197,8 @@ __device__ __forceinline__ int out_stage_at(int r, int chunk) { return r * 64 + 
 
 // g / (1 + exp(-g)) * u of two values.  exp and the reciprocal are the
 // hardware's (2 ulp and 1 ulp, subnormal results kept); rounding the exponent's
-// product costs |g| * 2^-24 more, relative to exp(-g).  The result is about to
+// product and its constant costs |g| * 2^-23.7 more, relative to exp(-g).  With
+// g below -88.72 exp(-g) is infinite and the result -0.  The result is about to
 // be rounded to 8 bits.
 __device__ __forceinline__ uint64_t silu_times2(uint64_t g, uint64_t u) {
     constexpr float kLog2E = 1.44269504088896340736f;
