@@ -66,7 +66,8 @@ template <int WT, int KIND> struct MpShape {
     // Rows are copied by one box a K step, the lowest of these that holds the tile's, in units of 16 (8 for a pair's half).
     static constexpr int kUnits = kRows / 16;
     static __host__ __device__ constexpr int box(int b) {
-        const int u = b == 0 ? kUnits : b == 1 ? kUnits - 2 : b == 2 ? kUnits - 4 : b == 3 ? (kUnits + 1) / 2 : b == 4 ? (kUnits + 3) / 4 : 1;
+        constexpr int big = kUnits > 8;         // 14: 14 12 10 7 4 1, 13: 13 11 9 7 4 1, 7: 7 5 4 3 2 1
+        const int u = b == 0 ? kUnits : b == 1 ? kUnits - 2 : b == 2 ? kUnits - 3 - big : b == 3 ? (kUnits + big) / 2 : b == 4 ? (kUnits + 3) / 4 : 1;
         return u > 1 ? u : 1;
     }
     static constexpr int kStages = KIND == kMpFew ? (WT == 1 ? 9 : 5) : KIND == kMpSingle ? 4 : WT == 1 ? 6 : 5;
@@ -84,6 +85,12 @@ template <int WT, int KIND> struct MpShape {
     static constexpr size_t kSmem = (size_t)kStages * (kStageBytes + kScaleBytes) + (kOutBytes + 15) / 16 * 16 + kBars * 8 + 16 +
                                     kMpListed * 16 + 2 * (kMpMaxExperts + 2) * 4 + 1024;
     static_assert(kStageBytes % 1024 == 0 && kSmem <= 232448, "shared memory");
+    static constexpr bool boxes_fall() {
+        for (int b = 1; b < kMpRowBoxes; ++b)
+            if (box(b) > box(b - 1) || (box(b) == box(b - 1) && box(b) > 1)) return false;
+        return box(0) == kUnits && box(kMpRowBoxes - 1) == 1;
+    }
+    static_assert(boxes_fall(), "the lowest box that holds a tile is the last one that does");
 };
 
 struct MpArgs {
