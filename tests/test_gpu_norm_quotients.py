@@ -59,6 +59,21 @@ def test_codes_are_the_quantizers(w, rows, k, fmt, residual):
         assert torch.equal(codes.reshape(-1), ec)
 
 
+@pytest.mark.parametrize("rows,k", [(1, 128), (333, 128), (3, 256), (41, 512), (600, 1024), (3, 2048), (400, 2048), (2, 16384)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_mxfp8_codes_are_the_weight_quantizers(w, rows, k, residual):
+    """The same rows with an MXFP8 output, against mxfp8_quantize_swizzled of y."""
+    for seed in range(8 if k < 1024 else 1):
+        sign = torch.where(torch.rand(rows, k, generator=torch.Generator().manual_seed(seed)) < 0.5, -1.0, 1.0)
+        wt = weights(k, seed).cuda()
+        x = (sign if residual else 2 * sign).bfloat16().cuda()
+        ec, es = w.mxfp8_quantize_swizzled((sign.cuda() * wt.float()).bfloat16())
+        codes, scales, *_ = w.mxfp8_rmsnorm_quantize(x, wt, 0.0, residual=x if residual else None, swizzled=True)
+        assert torch.equal(codes, ec) and torch.equal(scales, es)
+        codes, scales, *_ = w.mxfp8_rmsnorm_quantize(x, wt, 0.0, residual=x if residual else None)
+        assert torch.equal(codes, ec) and torch.equal(scales, w.mxfp8_unswizzle_scales(es, 1, rows, k)[0])
+
+
 @pytest.mark.parametrize("rows,k", [(3, 128), (5, 512), (2, 2048), (400, 2048)])
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 def test_infinite_weight(w, rows, k, fmt):
