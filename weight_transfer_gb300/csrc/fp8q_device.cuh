@@ -134,17 +134,6 @@ __device__ __forceinline__ void cluster_sync() {
     cluster_arrive();
     cluster_wait();
 }
-// The word at this shared-memory place of the cluster's block `rank`.
-__device__ __forceinline__ int peer_smem(const int* p, int rank) {
-    int v;
-    asm volatile(
-        "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\t"
-        "ld.shared::cluster.s32 %0, [r];\n\t}"
-        : "=r"(v)
-        : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank)
-        : "memory");
-    return v;
-}
 
 // -------------------------------------------- programmatic dependent launch ----
 // Every kernel of the library is launched so that it may be dispatched while
