@@ -475,14 +475,14 @@ fp8q_status_t fp8q_moe_combine_backward(const void* dout_bf16, const void* y_bf1
 
 /* The experts' products.  Row r belongs to the expert e with offsets[e] <= r <
  * offsets[e + 1]; rows from offsets[experts] on belong to none.  Values are
- * decode_e4m3(code) * 2^(scale - 127).  The products are exact, the sums the
- * tensor core's binary32 accumulators, which may cut off what a step of 32
- * products has below 2^-22 of its largest term:
+ * decode_e4m3(code) * 2^(scale - 127).  Each product is exact; the sums are the
+ * tensor core's, which adds 32 products at a time to a binary32 accumulator and
+ * cuts the result off towards zero instead of rounding it:
  *     matmul: out[r, f] = RNE_bf16(sum over c of W[e, f, c] * a[r, c])
  *     swiglu: g, u the sums with the gate and the up weights,
  *             h = g / (1 + exp(-g)) * u, quantized from binary32 by the rules
- *             of (d), scales row-major [rows, n / 32]; h carries 2^-20.9 and
- *             |g| * 2^-23.7 relative, and is 0 where exp(-g) is infinite
+ *             of (d), scales row-major [rows, n / 32]; h itself carries 2^-20.8
+ *             and |g| * 2^-23.7 relative, and is 0 where exp(-g) is infinite
  *             (g < -88.72)
  * Rows of no expert give zeros (codes and scales 0).
  *   codes, scales : rows * k codes and row-major [rows, k / 32] E8M0 bytes
