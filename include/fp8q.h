@@ -54,9 +54,12 @@ typedef enum {
     FP8Q_ERR_NULL = 1,   /* a required pointer is NULL                        */
     FP8Q_ERR_SIZE = 2,   /* a size is negative or beyond FP8Q_MAX_ELEMENTS    */
     FP8Q_ERR_ALIGN = 3,  /* a pointer is not 16-byte aligned                  */
-    FP8Q_ERR_FORMAT = 4, /* unknown fp8q_format_t                             */
-    FP8Q_ERR_K = 5,      /* shard count outside [1, FP8Q_MAX_SHARDS], or an
-                            MXFP8 K that is not a positive multiple of 32     */
+    FP8Q_ERR_FORMAT = 4, /* unknown fp8q_format_t, or expert ids of a width
+                            other than 4 or 8 bytes                           */
+    FP8Q_ERR_K = 5,      /* a count outside its limits (shards, ranks, choices
+                            per token), or a row length that is no positive
+                            multiple of what the entry point asks for, or
+                            beyond its limit                                  */
     FP8Q_ERR_CUDA = 6,   /* the CUDA runtime rejected a launch                */
     FP8Q_ERR_ALIAS = 7,  /* an output overlaps an input or another output     */
     FP8Q_ERR_FLAGS = 8   /* unknown bits in a flags argument                  */

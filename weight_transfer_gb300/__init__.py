@@ -5,7 +5,9 @@ The functions carry the C names; each one only marshals torch CUDA tensors
 into device pointers, sizes and the current CUDA stream, calls the library,
 and raises ``Fp8qError`` on a non-zero status.  All arithmetic runs in the
 library's CUDA kernels; there is no CPU path.  Outputs may be passed in
-(reused, caller-owned buffers) or are allocated with torch when omitted.
+(reused, caller-owned buffers) or are allocated with torch when omitted; with
+`stream` given, from that stream's own pool.  Inputs have to be ready on the
+stream of the call, as with any work queued there.
 
 Importing the package loads the library and fails loudly if it has not been
 built (``python weight_transfer_gb300/build.py`` or ``__graft_entry__.build()``).

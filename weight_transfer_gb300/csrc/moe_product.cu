@@ -28,7 +28,7 @@
 // warps for each quarter of the lanes, every other 16 rows each).
 //
 // Measured back to back, 128 experts: 65,533 rows through 2048 x 768 weights
-// 107 us (97 from a graph; HBM alone needs 78; of 528 MB half are writes),
+// 107 us (98 from a graph; HBM alone needs 78; of 528 MB half are writes),
 // 65,536 rows through two 768 x 2048 weights 184 us, 2.2 PFLOP/s (164 us with
 // pauses between, at a higher clock), 512 rows through the same 60 us, 6.8 TB/s of weights.  The
 // prefill cases wait for a stage's round trip: five stages of 39 KB are on

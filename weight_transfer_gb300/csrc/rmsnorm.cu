@@ -12,12 +12,15 @@
 // in registers between the sum of squares and the output, and the next row is
 // read meanwhile (one row per block without that took 110.6 us where this takes
 // 100.4: 16,384 rows of 4096 with residual, MXFP8 and bf16 outputs; 96.7 back to
-// back, 92% of the measured copy rate).  With codes alone it is bound by
-// instructions, 12 to 16 per element: hence the packed arithmetic on pairs,
-// scales worked out once for each block and lane, and a form without residual
-// (16,384 x 4096, e4m3 alone: 65.5 us without these, 47.1 with; MXFP8 47.1 and
-// 41.0).  Few rows are bound by latency, and below about 20 us by the caller's
-// launches.
+// back, 92% of the measured copy rate).  With codes alone it is bound by the
+// latency of its arithmetic, 12 (MXFP8) to 15 (e4m3) instructions per element:
+// the 15 warps an SM has registers for issue in 59 to 64% of the cycles and wait
+// for earlier instructions and shuffles, hardly ever for memory.  Hence the
+// packed arithmetic on pairs, scales worked out once for each block and lane,
+// and a form without residual (16,384 x 4096, one call at a time, MXFP8 alone:
+// 47.1 us without these, 41.0 with; e4m3 65.5 and 49.2, exact quotients
+// included).  Few rows are bound by latency, and below about 20 us by the
+// caller's launches.
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 
