@@ -505,6 +505,132 @@ fp8q_status_t mxfp8_moe_swiglu(const uint8_t* codes, const uint8_t* scales, int6
                                const int32_t* offsets, int experts, int64_t n, int64_t k, uint8_t* out_codes,
                                uint8_t* out_scales, fp8q_stream_t stream);
 
+/* The whole layer for a few tokens: gate, up and down products and the sum
+ * over a token's choices, e = ids[t, j], without sorting or carrying rows:
+ *     h[t, j] = g / (1 + exp(-g)) * u,   g, u = the gate's and the up weights' products with x[t]
+ *     out[t]  = RNE_bf16(sum over j of weights[t, j] * (down weights' product with h[t, j]))
+ * x in MXFP8 rows as for the products above.  h is not quantized, so that the
+ * result lies nearer to the formula than swiglu, matmul and combine together.
+ * Choices whose id lies outside [0, experts) are left out; a token without any
+ * gives zeros.  The same id may stand twice in a token.
+ *   codes, scales : tokens * k codes, row-major [tokens, k / 32] E8M0 bytes
+ *   ids           : tokens * topk integers of id_bytes 4 or 8 (FP8Q_ERR_FORMAT)
+ *   weights       : tokens * topk floats
+ *   gate, up      : [experts, n, k], down: [experts, k, n], codes and scales as
+ *                   mxfp8_quantize_swizzled writes them
+ *   workspace     : mxfp8_moe_decode_workspace_bytes(tokens, topk, n) bytes,
+ *                   caller-owned
+ * tokens: at most FP8Q_MOE_DECODE_MAX_TOKENS, experts 1 .. FP8Q_MOE_MAX_EXPERTS
+ * (FP8Q_ERR_SIZE); topk 1 .. FP8Q_MOE_MAX_TOPK, n and k positive multiples of
+ * 32 up to FP8Q_MOE_DECODE_MAX_ROW (FP8Q_ERR_K).  tokens == 0 is a no-op. */
+#define FP8Q_MOE_DECODE_MAX_TOKENS 32
+#define FP8Q_MOE_DECODE_MAX_ROW 16384
+size_t mxfp8_moe_decode_workspace_bytes(int64_t tokens, int topk, int64_t n);
+fp8q_status_t mxfp8_moe_decode(const uint8_t* codes, const uint8_t* scales, const void* ids, int id_bytes,
+                               const float* weights, int64_t tokens, int topk, const uint8_t* gate_codes,
+                               const uint8_t* gate_scales, const uint8_t* up_codes, const uint8_t* up_scales,
+                               const uint8_t* down_codes, const uint8_t* down_scales, int experts, int64_t n, int64_t k,
+                               void* out_bf16, void* workspace, size_t workspace_bytes, fp8q_stream_t stream);
+
+/* ---------------------------------------------- scores of given tokens ----
+ * What a trainer and an inference engine compare across a weight transfer: the
+ * log probability of each sampled token, the entropy of its distribution and
+ * the best alternatives; and for the trainer the gradient.
+ *
+ * For `rows` rows of `vocab` logits x, `stride` elements apart, m = max x_j:
+ *     S = sum over j of exp((x_j - m) / T),   log p_j = (x_j - m) / T - log S
+ *     logprobs[r] = log p_target;  0 where the target lies outside [0, vocab)
+ *     entropy[r]  = - sum of p_j log p_j
+ *     top_ids[r, i], top_logprobs[r, i] : the `top` largest logits in falling
+ *                   order, equal ones (+0 and -0 too) by rising index
+ *     stats[r]    = (m, log S), what the gradient reads
+ *   logits   : bf16 (logit_bytes 2) or binary32 (4) (FP8Q_ERR_FORMAT); aligned
+ *              to their own size, not to 16 bytes
+ *   targets  : rows integers of id_bytes 4 or 8, or NULL together with logprobs
+ *   entropy, stats : rows and rows * 2 floats, or NULL
+ *   top_logprobs, top_ids : rows * top, or NULL when top == 0
+ * At least one output has to be asked for (FP8Q_ERR_NULL).  All arithmetic is
+ * binary32; exponentials carry 2^-22 relative and are 0 below 2^-126.  A logit
+ * of -inf is a masked one; in a row of nothing else the scores are -inf, the
+ * entropy 0 and stats (-inf, 0).  A row that holds +inf or NaN has NaN scores; among its
+ * alternatives +inf counts as the largest, NaN as -inf.
+ * vocab: 1 .. FP8Q_MAX_VOCAB, top: 0 .. min(vocab, FP8Q_MAX_TOP) (FP8Q_ERR_K).
+ * rows < 2^27, stride >= vocab, T from 2^-20 to 2^20 (FP8Q_ERR_SIZE).
+ * rows == 0 is a no-op. */
+#define FP8Q_MAX_VOCAB (1 << 30)
+#define FP8Q_MAX_TOP 32
+fp8q_status_t fp8q_token_logprobs(const void* logits, int logit_bytes, int64_t rows, int64_t vocab, int64_t stride,
+                                  const void* targets, int id_bytes, float temperature, int top, float* logprobs,
+                                  float* entropy, float* top_logprobs, int32_t* top_ids, float* stats,
+                                  fp8q_stream_t stream);
+
+/* Gradient of logprobs and entropy (the alternatives have none):
+ *     dlogits[r, j] = ([j = target] g - p_j (g + dH (log p_j + entropy))) / T
+ * with g = dlogprobs[r] (0 where the target lies outside [0, vocab)) and dH =
+ * dentropy[r].  A row with g = dH = 0, or of -inf alone, gets zeros.
+ *   stats, entropy : as the forward pass wrote them
+ *   targets and dlogprobs : both or neither;  entropy and dentropy : likewise;
+ *              one pair at least (FP8Q_ERR_NULL)
+ *   dlogits  : of the logits' type, `dstride` elements apart, aligned to their
+ *              own size; may be the logits themselves (same pointer and stride)
+ * Elements between vocab and the stride are left as they are. */
+fp8q_status_t fp8q_token_logprobs_backward(const void* logits, int logit_bytes, int64_t rows, int64_t vocab, int64_t stride,
+                                           const void* targets, int id_bytes, float temperature, const float* stats,
+                                           const float* dlogprobs, const float* entropy, const float* dentropy,
+                                           void* dlogits, int64_t dstride, fp8q_stream_t stream);
+
+/* ------------------------------------------- norm and clipping of gradients ----
+ * The global norm of many gradient tensors, and the gradients clipped by it:
+ *     norm[0] = scale * sqrt(sum of x^2 over all tensors)
+ *     norm[1] = min(1, max_norm / (norm[0] + 1e-6))
+ *     each[i] = scale * sqrt(sum of x^2 over tensor i)
+ *     out_i   = RN(x_i * RN(scale * norm[1])), rounded to the output's type
+ * `scale` is what the gradients are to be multiplied by anyway: 1 / ranks
+ * where they are the ranks' sum (fp8q_dequant_reduce).  Squares are summed in
+ * binary32 by 64 and in binary64 above, over any magnitude and in a fixed
+ * order.  NaN and infinities are not looked for: a NaN anywhere makes the norm
+ * and all clipped gradients NaN; an infinite norm makes norm[1] 0.
+ *
+ * fp8q_grad_plan (host only, no GPU) checks a list of tensors and lays it out
+ * for the calls below, in caller-owned HOST memory of fp8q_grad_plan_bytes(count)
+ * bytes, 16-byte aligned.  The plan holds the tensors' addresses, types and
+ * sizes, no values, and serves any number of calls while they stay valid, from
+ * several threads at once.
+ *   grads : HOST array of `count` tensors, count <= FP8Q_MAX_GRADS
+ *           (FP8Q_ERR_SIZE); a tensor is aligned to its element's size.
+ *           out == NULL, or equal to grad with the same type: in place.
+ *   *workspace_bytes : what the calls need as workspace
+ * Inputs may overlap one another.  Where an output overlaps anything but its
+ * own input, fp8q_grad_clip on the plan gives FP8Q_ERR_ALIAS. */
+typedef enum {
+    FP8Q_BF16 = 0,
+    FP8Q_F32 = 1
+} fp8q_float_t;
+
+typedef struct {
+    const void* grad;          /* n elements (in)                              */
+    void* out;                 /* n elements (out), or NULL for in place       */
+    uint64_t n;
+    int32_t grad_type;         /* fp8q_float_t of grad (FP8Q_ERR_FORMAT)       */
+    int32_t out_type;          /* fp8q_float_t of out; not read without one    */
+} fp8q_grad_t;
+
+#define FP8Q_MAX_GRADS 16384
+size_t fp8q_grad_plan_bytes(int count);
+fp8q_status_t fp8q_grad_plan(const fp8q_grad_t* grads, int count, void* plan, size_t plan_bytes, size_t* workspace_bytes);
+
+/* The norm alone, and the norm and the clipped gradients (an in-place tensor
+ * whose factor is 1 is not written).
+ *   plan      : HOST memory as fp8q_grad_plan left it (FP8Q_ERR_FORMAT)
+ *   scale     : positive and finite;  max_norm : positive, may be infinite
+ *               (FP8Q_ERR_SIZE)
+ *   norm      : 2 floats;  each : one float per tensor of the plan, or NULL
+ *   workspace : device memory, caller-owned; may be NULL when it needs 0 bytes */
+fp8q_status_t fp8q_grad_norm(const void* plan, double scale, double max_norm, float* norm, float* each, void* workspace,
+                             size_t workspace_bytes, fp8q_stream_t stream);
+fp8q_status_t fp8q_grad_clip(const void* plan, double scale, double max_norm, float* norm, float* each, void* workspace,
+                             size_t workspace_bytes, fp8q_stream_t stream);
+
 /* ------------------------------------------------------------- helpers ---- */
 
 /* ceil(n / 128): the number of fp32 scales of an n-element blockwise array. */

@@ -47,6 +47,7 @@ _sz = ctypes.c_size_t
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 
 
 class fp8q_hop_t(ctypes.Structure):
@@ -73,6 +74,13 @@ FP8Q_DEVICE_ERR_COPY_TIMEOUT = 1
 FP8Q_DEVICE_ERR_PRODUCT_TIMEOUT = 2
 FP8Q_MOE_MAX_EXPERTS = 1024
 FP8Q_MOE_MAX_TOPK = 32
+FP8Q_MOE_DECODE_MAX_TOKENS = 32
+FP8Q_MOE_DECODE_MAX_ROW = 16384
+FP8Q_MAX_VOCAB = 1 << 30
+FP8Q_MAX_TOP = 32
+FP8Q_BF16 = 0
+FP8Q_F32 = 1
+FP8Q_MAX_GRADS = 16384
 
 
 class mxfp8_tensor_t(ctypes.Structure):
@@ -97,6 +105,13 @@ class fp8q_copy_t(ctypes.Structure):
 
 
 FP8Q_MAX_COPY_SEGMENTS = 96
+
+
+class fp8q_grad_t(ctypes.Structure):
+    """One tensor of fp8q_grad_plan (same layout as the C struct)."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_uint64),
+                ("grad_type", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+
 
 # name -> (argtypes, restype)
 _SIGNATURES = {
@@ -137,6 +152,15 @@ _SIGNATURES = {
     "fp8q_moe_combine_backward": ([_vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _i64, _vp, _vp, _vp], _int),
     "mxfp8_moe_matmul": ([_vp, _vp, _i64, _vp, _vp, _vp, _int, _i64, _i64, _vp, _vp], _int),
     "mxfp8_moe_swiglu": ([_vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _int, _i64, _i64, _vp, _vp, _vp], _int),
+    "mxfp8_moe_decode_workspace_bytes": ([_i64, _int, _i64], _sz),
+    "mxfp8_moe_decode": ([_vp, _vp, _vp, _int, _vp, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _int, _i64, _i64, _vp, _vp, _sz,
+                          _vp], _int),
+    "fp8q_token_logprobs": ([_vp, _int, _i64, _i64, _i64, _vp, _int, _f32, _int, _vp, _vp, _vp, _vp, _vp, _vp], _int),
+    "fp8q_token_logprobs_backward": ([_vp, _int, _i64, _i64, _i64, _vp, _int, _f32, _vp, _vp, _vp, _vp, _vp, _i64, _vp], _int),
+    "fp8q_grad_plan_bytes": ([_int], _sz),
+    "fp8q_grad_plan": ([ctypes.POINTER(fp8q_grad_t), _int, _vp, _sz, ctypes.POINTER(_sz)], _int),
+    "fp8q_grad_norm": ([_vp, _f64, _f64, _vp, _vp, _vp, _sz, _vp], _int),
+    "fp8q_grad_clip": ([_vp, _f64, _f64, _vp, _vp, _vp, _sz, _vp], _int),
     "fp8q_num_scales": ([_sz], _sz),
     "mxfp8_swizzled_scale_bytes": ([_i64, _i64, _i64], _sz),
     "fp8q_status_string": ([_int], ctypes.c_char_p),
@@ -950,3 +974,229 @@ def mxfp8_moe_swiglu(codes: torch.Tensor, scales: torch.Tensor, gate_codes: torc
     if st:
         _check("mxfp8_moe_swiglu", st)
     return out_codes, out_scales
+
+
+def _one_device(tensors) -> None:
+    """Refuses tensors of different devices, or of another device than the current one, on which the call would run."""
+    at = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("every tensor must be a CUDA tensor")
+            if at is None:
+                at = d
+                if d != torch.cuda.current_device():
+                    raise ValueError(f"the tensors are on cuda:{d}, which is not the current device")
+            elif d != at:
+                raise ValueError(f"tensors on cuda:{at} and on cuda:{d} in one call")
+
+
+def _ids(t: torch.Tensor, what: str, shape) -> tuple:
+    """(pointer, bytes per element) of integers of exactly this shape."""
+    if t.dtype is not torch.int64 and t.dtype is not torch.int32:
+        raise ValueError(f"{what} must be int32 or int64, got {t.dtype}")
+    return _in(t, what, t.dtype, shape), 8 if t.dtype is torch.int64 else 4
+
+
+def mxfp8_moe_decode_workspace_bytes(tokens: int, topk: int, n: int) -> int:
+    return int(_lib.mxfp8_moe_decode_workspace_bytes(tokens, topk, n))
+
+
+def mxfp8_moe_decode(codes: torch.Tensor, scales: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                     gate_codes: torch.Tensor, gate_scales: torch.Tensor, up_codes: torch.Tensor, up_scales: torch.Tensor,
+                     down_codes: torch.Tensor, down_scales: torch.Tensor, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """The whole expert layer for a few tokens: MXFP8 rows (codes uint8 [tokens,
+    k], scales uint8 [tokens, k/32]), their experts (ids int32 or int64 [tokens,
+    topk], an id outside [0, experts) is dropped) and weights float32 [tokens,
+    topk]; gate and up [experts, n, k] and down [experts, k, n] with their
+    swizzled scales -> bf16 [tokens, k]."""
+    tokens, k = _rows_of(codes, "codes")
+    topk = _rows_of(ids, "ids")[1]
+    experts, n = gate_codes.shape[0], gate_codes.shape[-2]
+    _one_device((codes, scales, ids, weights, gate_codes, gate_scales, up_codes, up_scales, down_codes, down_scales, out, workspace))
+    cp = _dev(codes, "codes", torch.uint8)
+    sp = _in(scales, "scales", torch.uint8, (tokens, k // MXFP8_BLOCK))
+    ip, id_bytes = _ids(ids, "ids", (tokens, topk))
+    wp = _in(weights, "weights", torch.float32, (tokens, topk))
+    gp, gsp = _expert_weights(gate_codes, gate_scales, "gate_codes", experts, n, k)
+    up, usp = _expert_weights(up_codes, up_scales, "up_codes", experts, n, k)
+    dp, dsp = _expert_weights(down_codes, down_scales, "down_codes", experts, k, n)
+    out, op = _out(out, "out", torch.bfloat16, (tokens, k), codes.device, tokens * k, stream)
+    if workspace is None:
+        have = _lib.mxfp8_moe_decode_workspace_bytes(tokens, topk, n)
+        workspace = _new(have, torch.uint8, codes.device, stream, kept=False)
+    else:
+        have = workspace.numel() * workspace.element_size()
+    st = _lib.mxfp8_moe_decode(cp, sp, ip, id_bytes, wp, tokens, topk, gp, gsp, up, usp, dp, dsp, experts, n, k, op,
+                               _dev(workspace, "workspace"), have, _stream(stream))
+    if st:
+        _check("mxfp8_moe_decode", st)
+    return out
+
+
+# ------------------------------------------------- scores of given tokens ----
+def _logits(t: torch.Tensor, what: str):
+    """(pointer, bytes per element, rows, columns, row stride) of a matrix whose rows may lie apart."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be [rows, vocab], got {list(t.shape)}")
+    size = 2 if t.dtype is torch.bfloat16 else 4 if t.dtype is torch.float32 else 0
+    if not size:
+        raise ValueError(f"{what} must be bfloat16 or float32, got {t.dtype}")
+    rows, vocab = t.shape
+    if vocab > 1 and t.stride(1) != 1:
+        raise ValueError(f"the elements of a row of {what} must lie next to each other")
+    return t.data_ptr(), size, rows, vocab, t.stride(0) if rows > 1 else vocab
+
+
+def fp8q_token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None, temperature: float = 1.0, top: int = 0,
+                        want_entropy: bool = False, want_stats: bool = False, logprobs: Optional[torch.Tensor] = None,
+                        entropy: Optional[torch.Tensor] = None, top_logprobs: Optional[torch.Tensor] = None,
+                        top_ids: Optional[torch.Tensor] = None, stats: Optional[torch.Tensor] = None, stream=None):
+    """Logits bf16 or float32 [rows, vocab] (rows may lie apart) and targets
+    int32 or int64 [rows] (one outside [0, vocab) scores 0) -> (logprobs float32
+    [rows] or None, entropy float32 [rows] or None, top_logprobs float32 [rows,
+    top] or None, top_ids int32 [rows, top] or None, stats float32 [rows, 2] or
+    None), of softmax(logits / temperature).  stats is what the gradient reads."""
+    _one_device((logits, targets, logprobs, entropy, top_logprobs, top_ids, stats))
+    xp, size, rows, vocab, stride = _logits(logits, "logits")
+    dev = logits.device
+    tp = lp = ep = vp = ip = sp = None
+    id_bytes = 8
+    if targets is not None:
+        tp, id_bytes = _ids(targets, "targets", (rows,))
+        logprobs, lp = _out(logprobs, "logprobs", torch.float32, (rows,), dev, rows, stream)
+    elif logprobs is not None:
+        raise ValueError("logprobs without targets")
+    if want_entropy or entropy is not None:
+        entropy, ep = _out(entropy, "entropy", torch.float32, (rows,), dev, rows, stream)
+    if top > 0:
+        top_logprobs, vp = _out(top_logprobs, "top_logprobs", torch.float32, (rows, top), dev, rows * top, stream)
+        top_ids, ip = _out(top_ids, "top_ids", torch.int32, (rows, top), dev, rows * top, stream)
+    elif top_logprobs is not None or top_ids is not None:
+        raise ValueError("top_logprobs or top_ids without top")
+    if want_stats or stats is not None:
+        stats, sp = _out(stats, "stats", torch.float32, (rows, 2), dev, rows * 2, stream)
+    st = _lib.fp8q_token_logprobs(xp, size, rows, vocab, stride, tp, id_bytes, temperature, top, lp, ep, vp, ip, sp,
+                                  _stream(stream))
+    if st:
+        _check("fp8q_token_logprobs", st)
+    return logprobs, entropy, top_logprobs, top_ids, stats
+
+
+def _like_rows(logits: torch.Tensor, ptr: int, size: int, rows: int, vocab: int, stride: int, stream) -> torch.Tensor:
+    """A matrix like `logits` whose rows lie relative to 16-byte boundaries as
+    its do, which lets the gradient move whole vectors: dense where the logits
+    are, and otherwise up to 15 bytes apart."""
+    per = 16 // size
+    apart = vocab + (stride - vocab) % per
+    shift = ptr % 16 // size
+    flat = _new(rows * apart + shift, logits.dtype, logits.device, stream)
+    return flat[shift:].as_strided((rows, vocab), (apart, 1))
+
+
+def fp8q_token_logprobs_backward(logits: torch.Tensor, targets: Optional[torch.Tensor], stats: torch.Tensor,
+                                 dlogprobs: Optional[torch.Tensor] = None, entropy: Optional[torch.Tensor] = None,
+                                 dentropy: Optional[torch.Tensor] = None, temperature: float = 1.0,
+                                 dlogits: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of fp8q_token_logprobs' logprobs (dlogprobs float32 [rows], with
+    the targets) and entropy (dentropy float32 [rows], with the entropy) ->
+    dlogits of the logits' shape and type; may be `logits` (in place)."""
+    _one_device((logits, targets, stats, dlogprobs, entropy, dentropy, dlogits))
+    xp, size, rows, vocab, stride = _logits(logits, "logits")
+    sp = _in(stats, "stats", torch.float32, (rows, 2))
+    tp, id_bytes, gp = None, 8, None
+    if dlogprobs is not None:
+        if targets is None:
+            raise ValueError("dlogprobs without targets")
+        tp, id_bytes = _ids(targets, "targets", (rows,))
+        gp = _in(dlogprobs, "dlogprobs", torch.float32, (rows,))
+    ep = _in(entropy, "entropy", torch.float32, (rows,)) if dentropy is not None else None
+    hp = _in(dentropy, "dentropy", torch.float32, (rows,))
+    if dlogits is None:
+        dlogits = _like_rows(logits, xp, size, rows, vocab, stride, stream)
+    elif dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
+        raise ValueError(f"dlogits must be {logits.dtype} {list(logits.shape)}, got {dlogits.dtype} {list(dlogits.shape)}")
+    dp, _, _, _, dstride = _logits(dlogits, "dlogits")
+    st = _lib.fp8q_token_logprobs_backward(xp, size, rows, vocab, stride, tp, id_bytes, temperature, sp, gp, ep, hp, dp, dstride,
+                                           _stream(stream))
+    if st:
+        _check("fp8q_token_logprobs_backward", st)
+    return dlogits
+
+
+# ----------------------------------------------- norm and clipping of gradients ----
+_GRAD_TYPES = {torch.bfloat16: FP8Q_BF16, torch.float32: FP8Q_F32}
+
+
+class fp8q_grad_list:
+    """Gradient tensors (bf16 or float32, contiguous, any alignment), checked and
+    laid out once for fp8q_grad_norm and fp8q_grad_clip, as a training loop with
+    lasting gradient buffers keeps them.  `outs`: where the clipped gradients go
+    (bf16 or float32, the same number of elements each); in place without."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
+        grads = list(grads)
+        outs = None if outs is None else list(outs)
+        if outs is not None and len(outs) != len(grads):
+            raise ValueError(f"{len(grads)} gradients and {len(outs)} outputs")
+        _one_device(grads + (outs or []))
+        self.grads, self.outs, self.count = grads, outs, len(grads)
+        self.device = grads[0].device if grads else torch.device("cuda")
+        arr = (fp8q_grad_t * max(self.count, 1))()
+        for i, g in enumerate(grads):
+            o = g if outs is None else outs[i]
+            for t, what in ((g, "grads"), (o, "outs")):
+                if t.dtype not in _GRAD_TYPES:
+                    raise ValueError(f"{what}[{i}] must be bfloat16 or float32, got {t.dtype}")
+            if o.numel() != g.numel():
+                raise ValueError(f"outs[{i}] holds {o.numel()} elements, grads[{i}] {g.numel()}")
+            arr[i] = fp8q_grad_t(_dev(g, f"grads[{i}]"), _dev(o, f"outs[{i}]"), g.numel(), _GRAD_TYPES[g.dtype],
+                                 _GRAD_TYPES[o.dtype])
+        need = _lib.fp8q_grad_plan_bytes(self.count)
+        self._memory = ctypes.create_string_buffer(need + 16)
+        self.plan = (ctypes.addressof(self._memory) + 15) & ~15
+        workspace = _sz(0)
+        _check("fp8q_grad_plan", _lib.fp8q_grad_plan(arr, self.count, self.plan, need, ctypes.byref(workspace)))
+        self.workspace_bytes = int(workspace.value)
+
+
+def _grad_call(name: str, grads, max_norm, scale, want_each, norm, each, workspace, stream):
+    _one_device((norm, each, workspace) if not grads.grads else (grads.grads[0], norm, each, workspace))
+    norm, np_ = _out(norm, "norm", torch.float32, (2,), grads.device, 2, stream)
+    ep = None
+    if want_each or each is not None:
+        each, ep = _out(each, "each", torch.float32, (grads.count,), grads.device, grads.count, stream)
+    have = grads.workspace_bytes
+    if workspace is None:
+        workspace = _new(have, torch.uint8, grads.device, stream, kept=False)
+    else:
+        have = workspace.numel() * workspace.element_size()
+    st = getattr(_lib, name)(grads.plan, scale, max_norm, np_, ep, _dev(workspace, "workspace"), have, _stream(stream))
+    if st:
+        _check(name, st)
+    return norm, each
+
+
+def fp8q_grad_norm(grads, max_norm: float = float("inf"), scale: float = 1.0, want_each: bool = False,
+                   norm: Optional[torch.Tensor] = None, each: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """The global norm of gradients (a sequence of tensors or a fp8q_grad_list),
+    times `scale` -> (float32 [2]: the norm and min(1, max_norm / (norm + 1e-6)),
+    each tensor's norm float32 [count] or None)."""
+    if not isinstance(grads, fp8q_grad_list):
+        grads = fp8q_grad_list(grads)
+    return _grad_call("fp8q_grad_norm", grads, max_norm, scale, want_each, norm, each, workspace, stream)
+
+
+def fp8q_grad_clip(grads, max_norm: float, scale: float = 1.0, outs: Optional[Sequence[torch.Tensor]] = None,
+                   want_each: bool = False, norm: Optional[torch.Tensor] = None, each: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """As fp8q_grad_norm, and the gradients times `scale` and that coefficient,
+    in place or into the list's outputs (`outs`, where grads is a sequence)."""
+    if not isinstance(grads, fp8q_grad_list):
+        grads = fp8q_grad_list(grads, outs)
+    elif outs is not None:
+        raise ValueError("a fp8q_grad_list has its outputs")
+    return _grad_call("fp8q_grad_clip", grads, max_norm, scale, want_each, norm, each, workspace, stream)

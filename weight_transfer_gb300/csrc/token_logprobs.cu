@@ -1,0 +1,637 @@
+// Log probabilities of given tokens, with entropy and the best alternatives,
+// and their gradient.
+//
+// For a row x of logits and z = x / T, m = max x:
+//     S = sum of exp((x_j - m) / T),   log p_j = (x_j - m) / T - log S
+//     entropy = - sum of p_j log p_j = log S - (sum of e_j (x_j - m) / T) / S
+// One pass: every thread keeps the running maximum of what it has read, the
+// sum S relative to it and the sum E of 2^t * t with t = (x - m) * log2(e) / T,
+// so that a larger maximum m' turns them into
+//     S' = S * 2^d,   E' = 2^d * (E + d * S),   d = (m - m') * log2(e) / T
+// and the same step joins threads, warps and the blocks of a cluster, in a
+// fixed order.  The difference x - m is taken before the product with
+// log2(e) / T, so that rows of the type's lowest value stay finite.
+//
+// Gradient, from the statistics that the forward pass wrote:
+//     dx_j = ([j = t] g - p_j (g + dH (log p_j + entropy))) / T
+#include "fp8q_device.cuh"
+#include "fp8q_host.cuh"
+
+#include <math.h>
+
+namespace fp8q {
+
+constexpr int kLpMaxTop = FP8Q_MAX_TOP;
+constexpr int kLpCap = 2048;            // candidates held in shared memory
+constexpr int kLpMaxCluster = 8;
+constexpr int kLpUnroll = 4;            // 16-byte vectors per thread and step
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLowest = -3.402823466e38f;
+
+struct LpArgs {
+    const void* logits;
+    const void* targets;        // or NULL
+    int id64;
+    int64_t vocab, stride;
+    float temperature, c;       // c = log2(e) / temperature
+    int top;
+    float* logprobs;            // each NULL when not wanted
+    float* entropy;
+    float* top_logprobs;
+    int32_t* top_ids;
+    float* stats;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+template <int BYTES> struct Logit;
+template <> struct Logit<2> {
+    using type = uint16_t;
+    static constexpr int kPerVec = 8;
+    static constexpr uint32_t kNothing = 0xFF80FF80u;       // two -inf
+    static __device__ __forceinline__ float load(const void* p, int64_t i) {
+        return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
+    }
+    static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) { unpack8(v, f); }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+        return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    }
+    static __device__ __forceinline__ void store(void* p, int64_t i, float f) {
+        static_cast<uint16_t*>(p)[i] = (uint16_t)pack_bf16x2(f, 0.0f);
+    }
+};
+template <> struct Logit<4> {
+    using type = float;
+    static constexpr int kPerVec = 4;
+    static constexpr uint32_t kNothing = 0xFF800000u;
+    static __device__ __forceinline__ float load(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+    static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
+        f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+    static __device__ __forceinline__ void store(void* p, int64_t i, float f) { static_cast<float*>(p)[i] = f; }
+};
+
+// Elements in front of the first 16-byte boundary of a row, its whole vectors
+// and the elements behind them.
+struct RowCut {
+    int head, tail;
+    int64_t vecs;
+};
+template <int BYTES> __device__ __forceinline__ RowCut cut_row(const void* p, int64_t n) {
+    constexpr int per = 16 / BYTES;
+    RowCut r;
+    const int64_t to = (int64_t)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / BYTES;
+    r.head = (int)(to < n ? to : n);
+    r.vecs = (n - r.head) / per;
+    r.tail = (int)(n - r.head - r.vecs * per);
+    return r;
+}
+
+__device__ __forceinline__ int64_t load_id(const void* p, int id64, int64_t i) {
+    return id64 ? (int64_t)static_cast<const long long*>(p)[i] : (int64_t)static_cast<const int*>(p)[i];
+}
+
+// The running maximum, sum and weighted sum of a set of logits.
+struct Soft {
+    float m, s, e;
+};
+__device__ __forceinline__ void raise(Soft& a, float m, float c) {
+    const float d = fmaxf((a.m - m) * c, -1000.0f);         // a.m <= m; 2^-1000 is 0
+    const float f = ex2(d);
+    a.e = f * (a.e + d * a.s);
+    a.s *= f;
+    a.m = m;
+}
+__device__ __forceinline__ Soft join(Soft a, Soft b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    raise(a, m, c);
+    raise(b, m, c);
+    return {m, a.s + b.s, a.e + b.e};
+}
+
+// Candidates are ordered by one 64-bit key, larger logits first and among
+// equal ones the lower index; +0 and -0 are equal.  No key is 0.
+__device__ __forceinline__ uint64_t key_of(float x, int64_t i) {
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    const uint32_t o = b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+    return ((uint64_t)o << 32) | (0xFFFFFFFFu - (uint32_t)i);
+}
+__device__ __forceinline__ float key_value(uint64_t k) {
+    const uint32_t o = (uint32_t)(k >> 32);
+    return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ int32_t key_index(uint64_t k) { return (int32_t)(0xFFFFFFFFu - (uint32_t)k); }
+
+__device__ __forceinline__ uint32_t map_rank0(const void* p) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
+    return r;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t a, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u64(uint32_t a, uint64_t v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+
+template <int NT> struct LpShared {
+    Soft warp[NT / 32];
+    Soft part[kLpMaxCluster];
+};
+struct LpTopShared {
+    uint64_t keys[kLpCap];
+    uint64_t sorted[kLpMaxTop];
+    uint64_t gather[kLpMaxCluster * kLpMaxTop];
+    uint64_t best[kLpMaxTop];
+    uint64_t threshold;
+    float group[64];
+    int count, kept, sum[3];
+};
+
+// Leaves the `top` largest of keys[0 .. n) and of the elements marked in
+// `open` as keys[0 .. top), and the smallest of them as the threshold: the
+// top-th largest key is found bit by bit.  Taken where the candidates do not
+// fit, which many equal logits or rising ones bring about.  n or open > top.
+template <int BYTES, int NT>
+__device__ __noinline__ void narrow(LpTopShared& t, int top, int n, uint64_t open, const uint4* v, float extra, int64_t at,
+                                    int64_t extra_at) {
+    constexpr int per = 16 / BYTES;
+    const int tid = (int)threadIdx.x;
+    if (tid == 0) { t.sum[0] = 0; t.kept = 0; }
+    __syncthreads();
+    uint64_t lo = 0;
+    for (int i = 0; i < 64; ++i) {
+        const uint64_t mid = lo | (1ull << (63 - i));
+        int c = 0;
+        for (int j = tid; j < n; j += NT) c += t.keys[j] >= mid;
+        for (int u = 0; u < kLpUnroll; ++u) {
+            float f[per];
+            Logit<BYTES>::unpack(v[u], f);
+#pragma unroll
+            for (int j = 0; j < per; ++j)
+                if (open >> (u * per + j) & 1) c += key_of(f[j], at + (int64_t)u * NT * per + j) >= mid;
+        }
+        if (open >> 63) c += key_of(extra, extra_at) >= mid;
+        c = __reduce_add_sync(0xFFFFFFFFu, c);
+        if (tid == 0) t.sum[(i + 1) % 3] = 0;
+        if ((tid & 31) == 0 && c) atomicAdd(&t.sum[i % 3], c);
+        __syncthreads();
+        if (t.sum[i % 3] >= top) lo = mid;
+    }
+    for (int j = tid; j < n; j += NT)
+        if (t.keys[j] >= lo) t.best[atomicAdd(&t.kept, 1)] = t.keys[j];
+    for (int u = 0; u < kLpUnroll; ++u) {
+        float f[per];
+        Logit<BYTES>::unpack(v[u], f);
+#pragma unroll
+        for (int j = 0; j < per; ++j) {
+            const uint64_t k = key_of(f[j], at + (int64_t)u * NT * per + j);
+            if ((open >> (u * per + j) & 1) && k >= lo) t.best[atomicAdd(&t.kept, 1)] = k;
+        }
+    }
+    if ((open >> 63) && key_of(extra, extra_at) >= lo) t.best[atomicAdd(&t.kept, 1)] = key_of(extra, extra_at);
+    __syncthreads();
+    if (tid < top) t.keys[tid] = t.best[tid];
+    if (tid == 0) { t.count = top; t.threshold = lo; }
+    __syncthreads();
+}
+
+// The top-th largest keys of keys[0 .. n) in falling order (keys are unique;
+// n of them where there are fewer), 0 behind.
+template <int NT> __device__ __forceinline__ void sort_top(const uint64_t* keys, int n, int top, uint64_t* sorted) {
+    const int tid = (int)threadIdx.x;
+    if (tid < top) sorted[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += NT) {
+        const uint64_t k = keys[i];
+        if (k == 0) continue;
+        int above = 0;
+        for (int j = 0; j < n; ++j) above += keys[j] > k;
+        if (above < top) sorted[above] = k;
+    }
+    __syncthreads();
+}
+
+template <int BYTES, bool TOP, bool ENT, int NT>
+__global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
+    using L = Logit<BYTES>;
+    constexpr int per = L::kPerVec;
+    __shared__ LpShared<NT> sh;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    LpTopShared& t = *reinterpret_cast<LpTopShared*>(dyn);
+    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t ranks;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
+    const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
+    const int64_t row = blockIdx.x / ranks;
+    const unsigned char* x = static_cast<const unsigned char*>(a.logits) + row * a.stride * BYTES;
+    const RowCut cut = cut_row<BYTES>(x, a.vocab);
+    const int64_t v0 = cut.vecs * rank / ranks, v1 = cut.vecs * (rank + 1) / ranks;
+    const unsigned char* body = x + (int64_t)cut.head * BYTES;
+    if (ranks > 1) cluster_arrive();
+    if (TOP && tid == 0) t.count = 0;
+    dependency_wait();
+    allow_dependents();
+
+    // the elements outside the row's vectors, one for a thread
+    float extra = -INFINITY;
+    int64_t extra_at = 0;
+    if (rank == 0 && tid < cut.head) extra_at = tid, extra = L::load(x, extra_at);
+    if (rank == ranks - 1 && tid >= 32 && tid - 32 < cut.tail)
+        extra_at = cut.head + cut.vecs * per + (tid - 32), extra = L::load(x, extra_at);
+    int64_t target = -1;
+    float target_logit = 0.0f;
+    if (rank == 0 && tid == 0 && a.targets) {
+        target = load_id(a.targets, a.id64, row);
+        if (target < 0 || target >= a.vocab) target = -1;
+        else target_logit = L::load(x, target);
+    }
+
+    Soft acc = {kLowest, 0.0f, 0.0f};
+    float floor_value = -INFINITY;                   // candidates are not below it
+    bool first = true;
+    for (int64_t base = v0; base < v1 || first; base += (int64_t)NT * kLpUnroll) {
+        uint4 v[kLpUnroll];
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) {
+            const int64_t i = base + u * NT + tid;
+            v[u] = i < v1 ? ld_stream(body + 16 * i) : make_uint4(L::kNothing, L::kNothing, L::kNothing, L::kNothing);
+        }
+        float most = first ? extra : -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) {
+            float f[per];
+            L::unpack(v[u], f);
+#pragma unroll
+            for (int j = 0; j < per; ++j) most = fmaxf(most, f[j]);
+        }
+        if (most > acc.m) raise(acc, most, a.c);
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) {
+            float f[per];
+            L::unpack(v[u], f);
+#pragma unroll
+            for (int j = 0; j < per; ++j) {
+                float d = (f[j] - acc.m) * a.c;
+                if (ENT) d = max_nan(d, -126.0f);    // 2^-126 stands for 0, so that 0 * -inf does not arise
+                const float p = ex2(d);
+                acc.s += p;
+                if (ENT) acc.e = __fmaf_rn(p, d, acc.e);
+            }
+        }
+        if (first) {
+            float d = (extra - acc.m) * a.c;
+            if (ENT) d = max_nan(d, -126.0f);
+            const float p = ex2(d);
+            acc.s += p;
+            if (ENT) acc.e = __fmaf_rn(p, d, acc.e);
+        }
+        if (TOP) {
+            const int64_t at = cut.head + (base + tid) * per;
+            if (first) {
+                // the top-th largest of 64 groups' maxima: as many elements are not below it
+                float g = most;
+#pragma unroll
+                for (int o = 1; o < NT / 64; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
+                if (tid % (NT / 64) == 0) t.group[tid / (NT / 64)] = g;
+                __syncthreads();
+                if (tid < 64) {
+                    const float mine = t.group[tid];
+                    int above = 0;
+                    for (int j = 0; j < 64; ++j) {
+                        const float o = t.group[j];
+                        above += o > mine || (o == mine && j < tid);
+                    }
+                    if (above == a.top - 1) t.threshold = key_of(mine, 0xFFFFFFFFll);
+                }
+                __syncthreads();
+                floor_value = key_value(t.threshold);
+            }
+            uint64_t open = 0;                       // candidates that found no place
+            if (most >= floor_value) {
+                const uint64_t threshold = t.threshold;
+                for (int u = 0; u < kLpUnroll; ++u) {
+                    float f[per];
+                    L::unpack(v[u], f);
+#pragma unroll
+                    for (int j = 0; j < per; ++j) {
+                        if (f[j] > -INFINITY && f[j] >= floor_value) {
+                            const uint64_t k = key_of(f[j], at + (int64_t)u * NT * per + j);
+                            if (k >= threshold) {
+                                const int pos = atomicAdd(&t.count, 1);
+                                if (pos < kLpCap) t.keys[pos] = k;
+                                else open |= 1ull << (u * per + j);
+                            }
+                        }
+                    }
+                }
+                if (first && extra > -INFINITY && extra >= floor_value) {
+                    const uint64_t k = key_of(extra, extra_at);
+                    const int pos = atomicAdd(&t.count, 1);
+                    if (pos < kLpCap) t.keys[pos] = k;
+                    else open |= 1ull << 63;
+                }
+            }
+            if (__syncthreads_or(open != 0)) {
+                narrow<BYTES, NT>(t, a.top, kLpCap, open, v, extra, at, extra_at);
+                floor_value = key_value(t.threshold);
+            }
+        }
+        first = false;
+    }
+
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Soft b;
+        b.m = __shfl_xor_sync(0xFFFFFFFFu, acc.m, o);
+        b.s = __shfl_xor_sync(0xFFFFFFFFu, acc.s, o);
+        b.e = __shfl_xor_sync(0xFFFFFFFFu, acc.e, o);
+        acc = (lane & o) ? join(b, acc, a.c) : join(acc, b, a.c);
+    }
+    if (lane == 0) sh.warp[warp] = acc;
+    if (TOP) {
+        __syncthreads();
+        int n = t.count;
+        if (n > 256) {
+            const uint4 none[kLpUnroll] = {};
+            __syncthreads();
+            narrow<BYTES, NT>(t, a.top, n, 0, none, 0.0f, 0, 0);
+            n = a.top;
+        }
+        sort_top<NT>(t.keys, n, a.top, t.sorted);
+    } else {
+        __syncthreads();
+    }
+    if (tid == 0) {
+        acc = sh.warp[0];
+        for (int w = 1; w < NT / 32; ++w) acc = join(acc, sh.warp[w], a.c);
+    }
+    if (ranks > 1) {
+        cluster_wait();                              // the first block has started
+        if (tid == 0) {
+            const uint32_t to = map_rank0(&sh.part[rank]);
+            st_cluster_f32(to, acc.m);
+            st_cluster_f32(to + 4, acc.s);
+            st_cluster_f32(to + 8, acc.e);
+        }
+        if (TOP && tid < a.top) st_cluster_u64(map_rank0(&t.gather[rank * a.top + tid]), t.sorted[tid]);
+        cluster_sync();
+        if (rank != 0) return;
+        if (tid == 0) {
+            acc = sh.part[0];
+            for (uint32_t r = 1; r < ranks; ++r) acc = join(acc, sh.part[r], a.c);
+        }
+        if (TOP) sort_top<NT>(t.gather, (int)ranks * a.top, a.top, t.sorted);
+    }
+    if (tid == 0) {
+        // a row of -inf alone has no distribution: its scores are -inf, its entropy 0
+        const bool none = acc.m == kLowest && acc.s < 0.5f;
+        const float log_s = none ? 0.0f : logf(acc.s);
+        const float m = none ? -INFINITY : acc.m;
+        if (a.logprobs)
+            a.logprobs[row] = target < 0 ? 0.0f : none ? -INFINITY : __fdiv_rn(target_logit - m, a.temperature) - log_s;
+        if (ENT) a.entropy[row] = none ? 0.0f : log_s - __fdiv_rn(acc.e, acc.s) * kLn2;
+        if (a.stats) {
+            a.stats[2 * row] = m;
+            a.stats[2 * row + 1] = log_s;
+        }
+        if (TOP) {
+            sh.part[0] = {m, log_s, none ? 1.0f : 0.0f};
+            // fewer candidates than asked for: the first logits that are -inf (or NaN) fill the list; fewer than `top`
+            // are neither, so that they lie among the first 2 * top
+            int n = 0;
+            while (n < a.top && t.sorted[n] != 0) ++n;
+            for (int64_t i = 0; n < a.top; ++i)
+                if (!(L::load(x, i) > -INFINITY)) t.sorted[n++] = key_of(-INFINITY, i);
+        }
+    }
+    if (TOP) {
+        __syncthreads();
+        if (tid < a.top) {
+            const uint64_t k = t.sorted[tid];
+            const float value = key_value(k), m = sh.part[0].m, log_s = sh.part[0].s;
+            a.top_ids[row * a.top + tid] = key_index(k);
+            a.top_logprobs[row * a.top + tid] =
+                sh.part[0].e != 0.0f ? -INFINITY : __fdiv_rn(value - m, a.temperature) - log_s;
+        }
+    }
+}
+
+// ------------------------------------------------------------- gradient ----
+struct LpGradArgs {
+    const void* logits;
+    const void* targets;
+    int id64;
+    int64_t rows, vocab, stride, dstride;
+    float temperature, c;
+    const float* stats;
+    const float* dlogprobs;     // or NULL
+    const float* entropy;       // with dentropy
+    const float* dentropy;      // or NULL
+    void* dlogits;
+    unsigned parts;             // blocks per row
+};
+
+constexpr int kLpGradThreads = 256;
+
+// A block takes one part of one row.  VEC: the rows of logits and dlogits lie
+// alike relative to 16-byte boundaries.
+template <int BYTES, bool ENT, bool VEC>
+__global__ void __launch_bounds__(kLpGradThreads) token_logprobs_backward_kernel(const LpGradArgs a) {
+    using L = Logit<BYTES>;
+    constexpr int per = L::kPerVec;
+    constexpr int NT = kLpGradThreads;
+    const int tid = (int)threadIdx.x;
+    const int64_t row = blockIdx.x / a.parts;
+    const unsigned part = blockIdx.x % a.parts;
+    const unsigned char* x = static_cast<const unsigned char*>(a.logits) + row * a.stride * BYTES;
+    unsigned char* dx = static_cast<unsigned char*>(a.dlogits) + row * a.dstride * BYTES;
+    dependency_wait();
+    allow_dependents();
+    int64_t target = a.targets ? load_id(a.targets, a.id64, row) : -1;
+    if (target < 0 || target >= a.vocab) target = -1;
+    const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
+    const bool none = m == -INFINITY;
+    const float inv_t = __fdiv_rn(1.0f, a.temperature);
+    const float g = target >= 0 && a.dlogprobs ? a.dlogprobs[row] * inv_t : 0.0f;
+    const float dh = ENT ? a.dentropy[row] * inv_t : 0.0f;
+    const float base = ENT ? -(g + dh * a.entropy[row]) : -g;       // dx_j = p_j * (base + slope * log2 p_j)
+    const float slope = ENT ? -dh * kLn2 : 0.0f;
+    const float shift = -log_s * kLog2e;
+    const bool zero = none || (g == 0.0f && dh == 0.0f);            // nothing reaches this row: zeros, whatever it holds
+    auto grad = [&](float v, int64_t i) {
+        if (zero) return 0.0f;
+        float d = __fmaf_rn(v - m, a.c, shift);
+        if (ENT) d = max_nan(d, -200.0f);            // 2^-200 is 0 here, and 0 * -inf does not arise
+        float r = ex2(d) * (ENT ? __fmaf_rn(slope, d, base) : base);
+        if (i == target) r += g;
+        return r;
+    };
+    if (!VEC) {
+        const int64_t lo = a.vocab * part / a.parts, hi = a.vocab * (part + 1) / a.parts;
+        for (int64_t i = lo + tid; i < hi; i += NT) L::store(dx, i, grad(L::load(x, i), i));
+        return;
+    }
+    const RowCut cut = cut_row<BYTES>(x, a.vocab);
+    if (part == 0 && tid < cut.head) L::store(dx, tid, grad(L::load(x, tid), tid));
+    if (part == a.parts - 1 && tid < cut.tail) {
+        const int64_t i = cut.head + cut.vecs * per + tid;
+        L::store(dx, i, grad(L::load(x, i), i));
+    }
+    const int64_t v0 = cut.vecs * part / a.parts, v1 = cut.vecs * (part + 1) / a.parts;
+    const unsigned char* body = x + (int64_t)cut.head * BYTES;
+    unsigned char* dbody = dx + (int64_t)cut.head * BYTES;
+    for (int64_t b = v0; b < v1; b += (int64_t)NT * kLpUnroll) {
+        uint4 v[kLpUnroll];
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) {
+            const int64_t i = b + u * NT + tid;
+            if (i < v1 && !zero) v[u] = ld_once(body + 16 * i);     // dlogits may be the logits themselves
+        }
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) {
+            const int64_t i = b + u * NT + tid;
+            if (i >= v1) break;
+            float f[per];
+            L::unpack(v[u], f);
+#pragma unroll
+            for (int j = 0; j < per; ++j) f[j] = grad(f[j], cut.head + i * per + j);
+            st_stream(dbody + 16 * i, L::pack(f));
+        }
+    }
+}
+
+}  // namespace fp8q
+
+using namespace fp8q;
+
+namespace {
+
+bool valid_temperature(float t) { return t >= 0x1p-20f && t <= 0x1p20f; }
+
+// Bytes from the first row's first element to the last one's last.
+size_t span(int64_t rows, int64_t cols, int64_t stride, int bytes) {
+    return rows ? ((size_t)(rows - 1) * (size_t)stride + (size_t)cols) * (size_t)bytes : 0;
+}
+
+fp8q_status_t check_logits(int64_t rows, int64_t vocab, int64_t stride, int logit_bytes, int id_bytes, float temperature) {
+    if (logit_bytes != 2 && logit_bytes != 4) return FP8Q_ERR_FORMAT;
+    if (id_bytes != 4 && id_bytes != 8) return FP8Q_ERR_FORMAT;
+    if (vocab < 1 || vocab > FP8Q_MAX_VOCAB) return FP8Q_ERR_K;
+    if (rows < 0 || rows >= (1ll << 27)) return FP8Q_ERR_SIZE;
+    if (stride < vocab || (uint64_t)stride > FP8Q_MAX_ELEMENTS) return FP8Q_ERR_SIZE;
+    if (rows > 0 && (uint64_t)stride > FP8Q_MAX_ELEMENTS / (uint64_t)rows) return FP8Q_ERR_SIZE;
+    if (!valid_temperature(temperature)) return FP8Q_ERR_SIZE;
+    return FP8Q_OK;
+}
+
+template <int BYTES, bool TOP, bool ENT, int NT>
+fp8q_status_t launch_logprobs(const LpArgs& a, int64_t rows, cudaStream_t stream) {
+    // blocks of a cluster share a row while there are fewer rows than SMs to fill twice
+    unsigned ranks = 1;
+    const int64_t steps = (a.vocab * BYTES + NT * kLpUnroll * 16 - 1) / (NT * kLpUnroll * 16);
+    while (ranks < kLpMaxCluster && rows * ranks * 2 <= 2 * sm_count() && (int64_t)ranks * 2 <= steps) ranks *= 2;
+    return launch_clusters(token_logprobs_kernel<BYTES, TOP, ENT, NT>, (unsigned)rows * ranks, ranks, NT,
+                           TOP ? sizeof(LpTopShared) : 0, stream, a);
+}
+
+template <int BYTES, bool TOP, bool ENT>
+fp8q_status_t launch_logprobs_size(const LpArgs& a, int64_t rows, cudaStream_t stream) {
+    return a.vocab * BYTES <= 16384 ? launch_logprobs<BYTES, TOP, ENT, 128>(a, rows, stream)
+                                    : launch_logprobs<BYTES, TOP, ENT, 512>(a, rows, stream);
+}
+
+template <int BYTES> fp8q_status_t launch_logprobs_kind(const LpArgs& a, int64_t rows, cudaStream_t stream) {
+    if (a.top) return a.entropy ? launch_logprobs_size<BYTES, true, true>(a, rows, stream)
+                                : launch_logprobs_size<BYTES, true, false>(a, rows, stream);
+    return a.entropy ? launch_logprobs_size<BYTES, false, true>(a, rows, stream)
+                     : launch_logprobs_size<BYTES, false, false>(a, rows, stream);
+}
+
+template <int BYTES> fp8q_status_t launch_backward(LpGradArgs a, bool vec, cudaStream_t stream) {
+    const int64_t per_block = (int64_t)kLpGradThreads * kLpUnroll * 16 / BYTES;
+    int64_t parts = (a.vocab + per_block - 1) / per_block;
+    const int64_t most = 0x7FFFFFFFll / a.rows;
+    a.parts = (unsigned)(parts < most ? parts : most);
+    const unsigned grid = (unsigned)a.rows * a.parts;
+    const bool ent = a.dentropy != nullptr;
+    if (vec)
+        return ent ? launch(token_logprobs_backward_kernel<BYTES, true, true>, grid, kLpGradThreads, 0, stream, a)
+                   : launch(token_logprobs_backward_kernel<BYTES, false, true>, grid, kLpGradThreads, 0, stream, a);
+    return ent ? launch(token_logprobs_backward_kernel<BYTES, true, false>, grid, kLpGradThreads, 0, stream, a)
+               : launch(token_logprobs_backward_kernel<BYTES, false, false>, grid, kLpGradThreads, 0, stream, a);
+}
+
+}  // namespace
+
+extern "C" fp8q_status_t fp8q_token_logprobs(const void* logits, int logit_bytes, int64_t rows, int64_t vocab, int64_t stride,
+                                             const void* targets, int id_bytes, float temperature, int top,
+                                             float* logprobs, float* entropy, float* top_logprobs, int32_t* top_ids,
+                                             float* stats, fp8q_stream_t stream) {
+    FP8Q_NVTX_RANGE("fp8q_token_logprobs");
+    const fp8q_status_t st = check_logits(rows, vocab, stride, logit_bytes, id_bytes, temperature);
+    if (st != FP8Q_OK) return st;
+    if (top < 0 || top > FP8Q_MAX_TOP || top > vocab) return FP8Q_ERR_K;
+    if (rows == 0) return FP8Q_OK;
+    if (!logits || (targets == nullptr) != (logprobs == nullptr)) return FP8Q_ERR_NULL;
+    if ((top > 0) != (top_logprobs != nullptr) || (top > 0) != (top_ids != nullptr)) return FP8Q_ERR_NULL;
+    if (!logprobs && !entropy && !top && !stats) return FP8Q_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(logits) % (unsigned)logit_bytes) return FP8Q_ERR_ALIGN;
+    if (!aligned16(targets) || !aligned16(logprobs) || !aligned16(entropy) || !aligned16(top_logprobs) ||
+        !aligned16(top_ids) || !aligned16(stats))
+        return FP8Q_ERR_ALIGN;
+    const size_t r = (size_t)rows;
+    const Range outs[] = {{logprobs, 4 * r}, {entropy, 4 * r}, {top_logprobs, 4 * r * top}, {top_ids, 4 * r * top},
+                          {stats, 8 * r}};
+    const Range ins[] = {{logits, span(rows, vocab, stride, logit_bytes)}, {targets, r * id_bytes}};
+    if (any_alias(outs, 5, ins, 2)) return FP8Q_ERR_ALIAS;
+    const LpArgs a = {logits, targets, id_bytes == 8, vocab, stride, temperature,
+                      (float)(1.44269504088896340736 / (double)temperature), top, logprobs, entropy, top_logprobs, top_ids, stats};
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return logit_bytes == 2 ? launch_logprobs_kind<2>(a, rows, s) : launch_logprobs_kind<4>(a, rows, s);
+}
+
+extern "C" fp8q_status_t fp8q_token_logprobs_backward(const void* logits, int logit_bytes, int64_t rows, int64_t vocab,
+                                                      int64_t stride, const void* targets, int id_bytes, float temperature,
+                                                      const float* stats, const float* dlogprobs, const float* entropy,
+                                                      const float* dentropy, void* dlogits, int64_t dstride,
+                                                      fp8q_stream_t stream) {
+    FP8Q_NVTX_RANGE("fp8q_token_logprobs_backward");
+    fp8q_status_t st = check_logits(rows, vocab, stride, logit_bytes, id_bytes, temperature);
+    if (st == FP8Q_OK) st = check_logits(rows, vocab, dstride, logit_bytes, id_bytes, temperature);
+    if (st != FP8Q_OK) return st;
+    if (rows == 0) return FP8Q_OK;
+    if (!logits || !stats || !dlogits) return FP8Q_ERR_NULL;
+    if ((targets == nullptr) != (dlogprobs == nullptr) || (entropy == nullptr) != (dentropy == nullptr)) return FP8Q_ERR_NULL;
+    if (!dlogprobs && !dentropy) return FP8Q_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(logits) % (unsigned)logit_bytes || reinterpret_cast<uintptr_t>(dlogits) % (unsigned)logit_bytes)
+        return FP8Q_ERR_ALIGN;
+    if (!aligned16(targets) || !aligned16(stats) || !aligned16(dlogprobs) || !aligned16(entropy) || !aligned16(dentropy))
+        return FP8Q_ERR_ALIGN;
+    const size_t r = (size_t)rows;
+    const Range out[] = {{dlogits, span(rows, vocab, dstride, logit_bytes)}};
+    const bool in_place = dlogits == logits && dstride == stride;
+    const Range ins[] = {{in_place ? nullptr : logits, span(rows, vocab, stride, logit_bytes)}, {targets, r * id_bytes},
+                         {stats, 8 * r}, {dlogprobs, 4 * r}, {entropy, 4 * r}, {dentropy, 4 * r}};
+    if (any_alias(out, 1, ins, 6)) return FP8Q_ERR_ALIAS;
+    const LpGradArgs a = {logits, targets, id_bytes == 8, rows, vocab, stride, dstride, temperature,
+                          (float)(1.44269504088896340736 / (double)temperature), stats, dlogprobs, entropy, dentropy, dlogits, 1};
+    const uintptr_t apart = reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(dlogits);
+    const bool vec = apart % 16 == 0 && (rows == 1 || (uint64_t)(stride - dstride) * (unsigned)logit_bytes % 16 == 0);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return logit_bytes == 2 ? launch_backward<2>(a, vec, s) : launch_backward<4>(a, vec, s);
+}
