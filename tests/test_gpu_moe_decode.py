@@ -225,6 +225,27 @@ def test_ids_and_weights_made_just_before():
         assert torch.equal(call(s).clone(), want)
 
 
+def test_weights_made_just_before():
+    """Weights that the launch right before the call writes over those of the call before it."""
+    s, r = layer(3, 2, 4, 256, 512, seed=14), layer(3, 2, 4, 256, 512, seed=15)
+    for name in ("xc", "xs", "ids", "p"):
+        r[name] = s[name]
+    g = torch.Generator(device="cuda").manual_seed(16)
+    raw = [torch.randn(4, 512, 256, generator=g, device="cuda").bfloat16() * 0.06 for _ in range(2)]
+    live = w.mxfp8_quantize_swizzled(raw[0])
+    want = []
+    for v in raw:
+        s["down"] = w.mxfp8_quantize_swizzled(v)
+        want.append(call(s).clone())
+    s["down"] = live
+    torch.cuda.synchronize()
+    got = []
+    for i in range(30):
+        w.mxfp8_quantize_swizzled(raw[i % 2], codes=live[0], scales_swizzled=live[1])
+        got.append(call(s))
+    assert all(torch.equal(v, want[i % 2]) for i, v in enumerate(got))
+
+
 def test_refusals_of_the_binding():
     s = layer(4, 2, 3, 64, 96, seed=13)
     with pytest.raises(ValueError, match="ids"):
