@@ -17,8 +17,8 @@ namespace fp8q {
 constexpr int kMdThreads = 256;
 constexpr int kMdWarps = kMdThreads / 32;
 constexpr int kMdMaxChoices = FP8Q_MOE_DECODE_MAX_TOKENS * FP8Q_MOE_MAX_TOPK;
-constexpr int kMdTiles = 4;                 // tiles of 8 rows that one pass over an expert's weights takes
-constexpr int kMdMaxCluster = 8;
+constexpr int kMdTiles = 2;                 // tiles of 8 columns that one pass over an expert's weights takes
+constexpr int kMdRow = 160;                 // bytes from row to row of a stage: 128, and 32 that keep rows off each other's banks
 
 struct MdArgs {
     const uint8_t *codes, *scales;                  // [tokens, k], [tokens, k / 32]
@@ -28,11 +28,13 @@ struct MdArgs {
     int tokens, topk, experts;
     int64_t n, k;
     const uint8_t *gate, *gate_scales, *up, *up_scales, *down, *down_scales;
-    uint16_t *hi, *lo;                              // [tokens * topk, n], h's halves
-    uint8_t* hs;                                    // [tokens * topk, hgroups * 4], their scales
+    uint8_t* h;                                     // [tokens * topk, 4, n], h's four terms
+    uint8_t* hs;                                    // [tokens * topk, hgroups * 4], the first one's scales
     int hgroups;                                    // groups of four blocks of 32
+    float* y;                                       // [tokens * topk, k], the down products
+    int* done;                                      // [ceil(k / 64)], blocks of a tile of features that have stored theirs
     uint16_t* out;                                  // [tokens, k]
-    int tiles;                                      // tiles of 8 rows that the buffer of partial sums holds
+    int tiles;                                      // column tiles that a pass takes, at most kMdTiles
 };
 
 // ------------------------------------------------------------ building blocks ----
@@ -44,18 +46,6 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint2 a0, uint2 a1, uint
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0.x), "r"(a1.x), "r"(a0.y), "r"(a1.y), "r"(b.x), "r"(b.y), "f"(0.0f));
 }
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Two e4m3 codes -> two f16, exactly.
-__device__ __forceinline__ uint32_t e4m3_f16(uint32_t two) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
-    return r;
-}
 // Four E8M0 bytes -> 2^(byte - 127) each, NaN for 255.
 __device__ __forceinline__ void e8m0x4(uint32_t w, float (&f)[4]) {
     uint32_t a, b;
@@ -63,85 +53,87 @@ __device__ __forceinline__ void e8m0x4(uint32_t w, float (&f)[4]) {
     asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(w >> 16)));
     f[0] = bf16_lo(a); f[1] = bf16_hi(a); f[2] = bf16_lo(b); f[3] = bf16_hi(b);
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
+// 16 bytes global -> shared, past the first-level cache.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint32_t ld_nc32(const void* p) {
-    uint32_t r;
-    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(p));
-    return r;
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ uint2 ld_nc64(const void* p) {
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 r;
-    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+// acc += (d * row) * column for a tile's sums over one block of 32: rows' scales a and b, columns' c.
+__device__ __forceinline__ void scaled_add(uint64_t (&acc)[2], const float (&d)[4], float a, float b, uint64_t c) {
+    acc[0] = f2_fma(f2_mul(f2_pack(d[0], d[1]), f2_pack(a, a)), c, acc[0]);
+    acc[1] = f2_fma(f2_mul(f2_pack(d[2], d[3]), f2_pack(b, b)), c, acc[1]);
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
     return r;
 }
 
-// Past the first-level cache, for what may be read before a kernel's dependency wait.
-__device__ __forceinline__ uint32_t ld_l2_32(const void* p) {
-    uint32_t r;
-    asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(r) : "l"(p));
-    return r;
-}
-__device__ __forceinline__ uint2 ld_l2_64(const void* p) {
-    uint2 r;
-    asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-    return r;
-}
-
-// The four scales of blocks 4 j .. 4 j + 3 of row r in the 128 x 4 tiled layout.
-__device__ __forceinline__ const uint8_t* scale_word(const uint8_t* s, int64_t r, int64_t j, int64_t tiles) {
-    return s + ((r >> 7) * tiles + j) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
+// The 16 bytes of the 128 x 4 tiled layout that hold the scales of blocks 4 j ..
+// 4 j + 3 of row r, as their word (r / 32) % 4.
+__device__ __forceinline__ const uint8_t* scale_line(const uint8_t* s, int64_t r, int64_t j, int64_t tiles) {
+    return s + ((r >> 7) * tiles + j) * 512 + (r & 31) * 16;
 }
 
 // ------------------------------------------------------- choices by expert ----
 // Every block sorts the choices by expert for itself.
-struct MdList {
-    int16_t expert[kMdMaxChoices];          // the experts that are chosen, rising
-    int16_t start[kMdMaxChoices + 1];       // where their choices start in `order`
-    int16_t order[kMdMaxChoices];           // choices by expert, and in their order
+struct MdList {                             // arrays in shared memory, list_stride(choices) long
+    int16_t* expert;                        // the experts that are chosen, rising
+    int16_t* start;                         // where their choices start in `order`
+    int16_t* order;                         // choices by expert, and in their order
+    int16_t* token;                         // their tokens
     int active;
-    int twice;                              // some token names an expert twice
 };
+__host__ __device__ __forceinline__ int list_stride(int choices) { return (choices + 8) & ~7; }
+
 struct MdScratch {
     int count[FP8Q_MOE_MAX_EXPERTS];
-    int16_t key[kMdMaxChoices], rank[kMdMaxChoices];
+    int16_t key[kMdMaxChoices + 8], rank[kMdMaxChoices];
     int warp[kMdWarps];
+    int active;
 };
 
-// The ids are read past the first-level cache: the down kernel reads them
-// before its own dependency wait.
+// The ids are read past the first-level cache: the down products' kernel reads
+// them before its own dependency wait.
 __device__ __forceinline__ void sort_choices(const MdArgs& a, MdList& s, MdScratch& w) {
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int choices = a.tokens * a.topk;
     for (int i = tid; i < a.experts; i += kMdThreads) w.count[i] = 0;
-    for (int i = tid; i < choices; i += kMdThreads) {
-        const int64_t id = a.id64 ? (int64_t)__ldcg(static_cast<const long long*>(a.ids) + i)
-                                  : (int64_t)__ldcg(static_cast<const int*>(a.ids) + i);
+    for (int i = tid; i < ((choices + 7) & ~7); i += kMdThreads) {
+        int64_t id = -1;
+        if (i < choices)
+            id = a.id64 ? (int64_t)__ldcg(static_cast<const long long*>(a.ids) + i) : (int64_t)__ldcg(static_cast<const int*>(a.ids) + i);
         w.key[i] = id >= 0 && id < a.experts ? (int16_t)id : (int16_t)-1;
     }
-    if (tid == 0) s.twice = 0;
     __syncthreads();
-    if (warp == 0) {
-        for (int base = 0; base < choices; base += 32) {
-            const int i = base + lane;
-            const int key = i < choices ? w.key[i] : -1;
-            const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
-            const int below = __popc(same & ((1u << lane) - 1u));
-            const int had = key >= 0 ? w.count[key] : 0;
-            if (key >= 0) w.rank[i] = (int16_t)(had + below);
-            __syncwarp();
-            if (key >= 0 && below == 0) w.count[key] = had + __popc(same);
-            __syncwarp();
+    // a choice's rank: the earlier ones of its expert, counted eight at a time
+    for (int i = tid; i < choices; i += kMdThreads) {
+        const int key = w.key[i];
+        if (key < 0) continue;
+        atomicAdd(&w.count[key], 1);
+        const uint32_t both = (uint32_t)key * 0x10001u;
+        int below = 0;
+        for (int j = 0; j < i; j += 8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(&w.key[j]);
+            const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const uint32_t d = h[m] ^ both;
+                below += (j + 2 * m < i && (d & 0xFFFFu) == 0) + (j + 2 * m + 1 < i && (d >> 16) == 0);
+            }
         }
-    } else {
-        for (int i = tid - 32; i < choices; i += kMdThreads - 32) {
-            const int key = w.key[i];
-            for (int j = i - i % a.topk; key >= 0 && j < i; ++j)
-                if (w.key[j] == key) s.twice = 1;
-        }
+        w.rank[i] = (int16_t)below;
     }
     __syncthreads();
     // chosen experts and choices in front of each expert, in one scan: both stay below 2^16
@@ -177,304 +169,320 @@ __device__ __forceinline__ void sort_choices(const MdArgs& a, MdList& s, MdScrat
         w.count[e] = (int)(at & 0xFFFFu);
     }
     if (tid == kMdThreads - 1) {
-        s.active = (int)((before + sum) >> 16);
-        s.start[s.active] = (int16_t)((before + sum) & 0xFFFFu);
+        w.active = (int)((before + sum) >> 16);
+        s.start[w.active] = (int16_t)((before + sum) & 0xFFFFu);
     }
     __syncthreads();
     for (int i = tid; i < choices; i += kMdThreads) {
         const int key = w.key[i];
-        if (key >= 0) s.order[w.count[key] + w.rank[i]] = (int16_t)i;
+        if (key >= 0) {
+            const int at = w.count[key] + w.rank[i];
+            s.order[at] = (int16_t)i;
+            s.token[at] = (int16_t)(i / a.topk);
+        }
     }
+    s.active = w.active;
     __syncthreads();
 }
 
-// ------------------------------------------------------ gate and up products ----
-// A block takes 32 features of one expert, in four passes of 8 whose gate rows
-// are the upper and whose up rows the lower half of a tensor-core tile, so that
-// a lane gets both sums of a feature.  Its warps share K.
-struct UpTile {
-    uint2 w[2][4][2];           // two groups of four blocks of 32; gate, up
-    uint32_t s[2][2];
-};
-
-__device__ __forceinline__ void load_up(UpTile& t, const MdArgs& a, int e, int64_t f0, int step, int chunks) {
-    const int lane = (int)(threadIdx.x & 31u), warp = (int)(threadIdx.x >> 5);
-    const int kb = (int)(a.k / 32), groups = (kb + 3) / 4;
-    const int64_t f = f0 + (step / chunks) * 8 + (lane >> 2);
-    const int first = (step % chunks) * 2 * kMdWarps + warp;
-    const int64_t row = ((int64_t)e * a.n + f) * a.k + (lane & 3) * 8;
-    const int64_t per = (a.n + 127) / 128 * groups * 512;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int g = first + q * kMdWarps;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const bool in = g * 4 + b < kb;
-            const int64_t at = row + (g * 4 + b) * 32;
-            t.w[q][b][0] = in ? ld_stream8(a.gate + at) : make_uint2(0u, 0u);
-            t.w[q][b][1] = in ? ld_stream8(a.up + at) : make_uint2(0u, 0u);
+// out for 64 features from f0 on: the choices' products, weighted, in their order.
+__device__ __forceinline__ void sum_choices(const MdArgs& a, int64_t f0) {
+    for (int i = (int)threadIdx.x; i < a.tokens * 16; i += kMdThreads) {
+        const int token = i >> 4;
+        const int64_t f = f0 + (i & 15) * 4;
+        if (f >= a.k) continue;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int j = 0; j < a.topk; ++j) {
+            const int64_t choice = token * a.topk + j;
+            const int64_t id = a.id64 ? (int64_t)__ldcg(static_cast<const long long*>(a.ids) + choice)
+                                      : (int64_t)__ldcg(static_cast<const int*>(a.ids) + choice);
+            if (id < 0 || id >= a.experts) continue;
+            const float p = __ldcg(a.weights + choice);
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(a.y + choice * a.k + f));
+            v.x = __fmaf_rn(p, y.x, v.x);
+            v.y = __fmaf_rn(p, y.y, v.y);
+            v.z = __fmaf_rn(p, y.z, v.z);
+            v.w = __fmaf_rn(p, y.w, v.w);
         }
-        const bool in = g < groups;
-        t.s[q][0] = in ? ld_nc32(scale_word(a.gate_scales + e * per, f, g, groups)) : 0u;
-        t.s[q][1] = in ? ld_nc32(scale_word(a.up_scales + e * per, f, g, groups)) : 0u;
+        *reinterpret_cast<uint2*>(a.out + token * a.k + f) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
 }
 
-// Scales of blocks 4 g .. 4 g + 3 of a row-major row.
-__device__ __forceinline__ uint32_t row_scales(const uint8_t* s, int g, int kb) {
-    if ((kb & 3) == 0) return ld_nc32(s + 4 * g);
-    uint32_t w = 0;
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-        if (4 * g + b < kb) w |= (uint32_t)s[4 * g + b] << (8 * b);
-    return w;
-}
+// ------------------------------------------------------------- the products ----
+// A block takes 32 features of an expert's gate and up weights, or 64 of its
+// down weights.  Two of its warps share 16 rows of weights, one taking the even,
+// one the odd groups of 128 columns of K: eight features' gate rows above their
+// up rows, so that a lane gets both sums of a feature, or 16 features' down
+// rows.  Such a unit of 16 rows of 128 bytes and their scales comes into a ring
+// of the warp's own by asynchronous copies that run kMdDepth - 1 units ahead,
+// across items, so that no barrier stops them.
+//   The columns of a tensor-core tile are 8 rows of x, or the four terms of two
+// rows of h.  Columns without a row repeat the first one's data; their sums are
+// not read.
+//   Down products wait for h in front of their first tile only; their weights
+// are on the way by then.  The last block to store a tile of 64 features sums
+// the choices for it, in their order.
+constexpr int kMdDepth = 4;
+constexpr int kMdScales = 16 * kMdRow;                  // where a stage's 16 scale lines lie
+constexpr int kMdStage = kMdScales + 16 * 16;
+constexpr int kMdRing = kMdWarps * kMdDepth * kMdStage;
+constexpr int kMdSums = 2 * kMdWarps * 4 * 33 * 4;      // bytes of partial sums for each column tile
 
-__global__ void __launch_bounds__(kMdThreads, 2) moe_decode_up_kernel(const MdArgs a) {
-    __shared__ MdList list;
+template <bool DOWN> __global__ void __launch_bounds__(kMdThreads, 2) moe_decode_kernel(const MdArgs a) {
+    __shared__ int last_one;
     extern __shared__ __align__(16) unsigned char dyn[];
-    float* red = reinterpret_cast<float*>(dyn);         // [4 passes][warps][tiles][4][32], a pass one word further
+    float* red = reinterpret_cast<float*>(dyn + kMdRing);           // [2][warps][tiles][4][33]
+    const int stride = list_stride(a.tokens * a.topk);
+    int16_t* lists = reinterpret_cast<int16_t*>(dyn + kMdRing + a.tiles * kMdSums);
+    MdList list = {lists, lists + stride, lists + 2 * stride, lists + 3 * stride, 0};
+    uint32_t* xscales = reinterpret_cast<uint32_t*>(lists + 4 * stride);                    // [tokens][groups], of x
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    dependency_wait();
-    allow_dependents();
+    const int64_t features = DOWN ? a.k : a.n, cols = DOWN ? a.n : a.k;
+    const int kb = (int)(cols / 32), groups = (kb + 3) / 4;
+    constexpr int kWidth = DOWN ? 64 : 32, kTile = DOWN ? 16 : 8, kRows = DOWN ? 2 : 8;
+    const int blocks = (int)((features + kWidth - 1) / kWidth);
+    // Ids and weights may be read by the second launch at once: the blocks of the first let it start only when
+    // whatever wrote them had completed.
+    if (!DOWN) {
+        dependency_wait();
+        allow_dependents();
+        if (blockIdx.x == 0)
+            for (int i = tid; i < (int)((a.k + 63) / 64); i += kMdThreads) a.done[i] = 0;
+    }
     sort_choices(a, list, *reinterpret_cast<MdScratch*>(dyn));
-    const int kb = (int)(a.k / 32), groups = (kb + 3) / 4;
-    const int chunks = (groups + 2 * kMdWarps - 1) / (2 * kMdWarps), steps = 4 * chunks;
-    const int blocks = (int)(a.n / 32);
-    const int pass_words = kMdWarps * a.tiles * 128 + 1;
+    if (!DOWN)
+        for (int i = tid; i < a.tokens * groups; i += kMdThreads) {
+            const uint8_t* s = a.scales + (int64_t)(i / groups) * kb + i % groups * 4;
+            uint32_t w = 0;
+            for (int b = 0; b < 4; ++b)
+                if (i % groups * 4 + b < kb) w |= (uint32_t)s[b] << (8 * b);
+            xscales[i] = w;
+        }
+    const int pass_rows = kRows * a.tiles;
+    const uint32_t ring = smem_addr(dyn) + warp * kMdDepth * kMdStage;
+    const int q = lane >> 2, t = lane & 3;
+    const int offset = (warp >> 1) * kTile, odd = warp & 1;
+    const int warp_words = a.tiles * 4 * 33;
     const int items = list.active * blocks;
+
+    // ---- the copies, ahead of the products
+    // Gate and up go through all features of an expert before the next; down through all experts of a tile of
+    // features, so that its sum over the choices can be formed while other tiles are on their way.
+    int a_item = (int)blockIdx.x, a_ai = 0, a_r0 = 0, a_col = 0;
+    const int c = (lane & 7) * 16;                      // eight lanes bring a row's 128 bytes
+    const int64_t four = 4 * cols;
+    const uint32_t to = ring + (lane >> 3) * kMdRow + c;
+    const uint8_t *upper = nullptr, *lower = nullptr, *line = nullptr;
+    auto aim = [&] {                                    // at the first group of an item
+        a_col = odd * 128;
+        int64_t f = 0;
+        for (;; a_item += (int)gridDim.x) {             // the last tile of features may have none for this warp
+            if (a_item >= items) return;
+            f = (int64_t)(DOWN ? a_item / list.active : a_item % blocks) * kWidth + offset;
+            if (f < features) break;
+        }
+        a_ai = DOWN ? a_item % list.active : a_item / blocks;
+        const int64_t e = list.expert[a_ai];
+        const int64_t at = (e * features + f + (lane >> 3)) * cols + a_col + c;
+        const int64_t matrix = (features + 127) / 128 * groups * 512 * e + odd * 512;
+        if (DOWN) {
+            upper = a.down + at;
+            lower = upper + 8 * cols;
+            line = scale_line(a.down_scales, f + (lane & 15), 0, groups) + matrix;
+        } else {
+            upper = a.gate + at;
+            lower = a.up + at;
+            line = scale_line(lane < 8 ? a.gate_scales : a.up_scales, f + (lane & 7), 0, groups) + matrix;
+        }
+    };
+    auto issue = [&](uint32_t stage) {
+        if (a_item < items && odd < groups) {
+            const uint32_t d = to + stage;
+            if (a_col + 128 <= (int)cols) {
+                copy16(d, upper);
+                copy16(d + 4 * kMdRow, upper + four);
+                copy16(d + 8 * kMdRow, lower);
+                copy16(d + 12 * kMdRow, lower + four);
+            } else {
+                const bool in = a_col + c < (int)cols;
+                const int64_t back = in ? 0 : -c;       // to a column that exists, of which nothing is read
+                copy16_or_zero(d, upper + back, in);
+                copy16_or_zero(d + 4 * kMdRow, upper + back + four, in);
+                copy16_or_zero(d + 8 * kMdRow, lower + back, in);
+                copy16_or_zero(d + 12 * kMdRow, lower + back + four, in);
+            }
+            if (lane < 16) copy16(ring + stage + kMdScales + lane * 16, line);
+            upper += 256;
+            lower += 256;
+            line += 1024;
+            a_col += 256;
+            if (a_col >= (int)cols) {
+                a_r0 += pass_rows;
+                if (a_r0 >= list.start[a_ai + 1] - list.start[a_ai]) {
+                    a_r0 = 0;
+                    a_item += (int)gridDim.x;
+                }
+                aim();
+            }
+        }
+        copy_commit();
+    };
+    aim();
+#pragma unroll
+    for (int i = 0; i < kMdDepth - 1; ++i) issue(i * kMdStage);
+    if (DOWN) {
+        dependency_wait();
+        allow_dependents();
+    } else {
+        __syncthreads();                                // x's scales
+    }
+
+    uint32_t stage = 0;
+    int flip = 0;
     for (int item = (int)blockIdx.x; item < items; item += (int)gridDim.x) {
-        const int ai = item / blocks;
-        const int block = item % blocks;
-        const int64_t f0 = (int64_t)block * 32;
-        const int e = list.expert[ai], first = list.start[ai], rows = list.start[ai + 1] - first;
-        for (int r0 = 0; r0 < rows; r0 += 8 * a.tiles) {
-            const int left = rows - r0, nt = (left + 7) / 8 < a.tiles ? (left + 7) / 8 : a.tiles;
-            UpTile next;
-            load_up(next, a, e, f0, 0, chunks);
-            float acc[kMdTiles][4];
-            for (int step = 0; step < steps; ++step) {
-                const UpTile t = next;
-                if (step + 1 < steps) load_up(next, a, e, f0, step + 1, chunks);
-                const int chunk = step % chunks;
-                if (chunk == 0) {
+        const int ai = DOWN ? item % list.active : item / blocks, block = DOWN ? item / list.active : item % blocks;
+        const int first = list.start[ai], rows = list.start[ai + 1] - first;
+        const int64_t f0 = (int64_t)block * kWidth;
+        const uint32_t word = kMdScales + (uint32_t)((f0 + offset) >> 5 & 3) * 4 + q * 16;
+        const bool idle = DOWN && f0 + offset >= features;
+        for (int r0 = 0; r0 < rows; r0 += pass_rows) {
+            const int left = rows - r0, nt = left > kRows && a.tiles > 1 ? 2 : 1;
+            // this lane's column of B, and the scales of its sums' two columns
+            const uint8_t* xb[kMdTiles];
+            const uint32_t* cs[kMdTiles];
+            uint32_t s0[kMdTiles], s1[kMdTiles];
 #pragma unroll
-                    for (int i = 0; i < kMdTiles; ++i)
+            for (int i = 0; i < kMdTiles; ++i) {
+                if (DOWN) {
+                    const int rb = r0 + i * 2 + (q >> 2), rd = r0 + i * 2 + (t >> 1);
+                    const int64_t cb = list.order[rb < rows ? first + rb : first], cd = list.order[rd < rows ? first + rd : first];
+                    xb[i] = a.h + (cb * 4 + (q & 3)) * a.n + odd * 128 + t * 8;
+                    cs[i] = reinterpret_cast<const uint32_t*>(a.hs) + cd * groups;
+                } else {
+                    const int rb = r0 + i * 8 + q, rd = r0 + i * 8 + t * 2;
+                    xb[i] = a.codes + list.token[rb < rows ? first + rb : first] * a.k + odd * 128 + t * 8;
+                    s0[i] = smem_addr(xscales + list.token[rd < rows ? first + rd : first] * groups);
+                    s1[i] = smem_addr(xscales + list.token[rd + 1 < rows ? first + rd + 1 : first] * groups);
+                }
+            }
+            uint64_t acc[kMdTiles][2];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+            for (int i = 0; i < kMdTiles; ++i) acc[i][0] = acc[i][1] = 0;
+            for (int g = idle ? groups : odd; g < groups; g += 2) {
+                uint2 x[kMdTiles][4];
+                uint32_t w0[kMdTiles], w1[kMdTiles];
+                const bool whole = g * 4 + 4 <= kb;
+#pragma unroll
+                for (int i = 0; i < kMdTiles; ++i) {
+                    if (i >= nt) break;
+                    const uint8_t* from = xb[i] + (g - odd) * 128;
+                    if (whole) {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) x[i][b] = *reinterpret_cast<const uint2*>(from + b * 32);
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < 3; ++b)
+                            x[i][b] = g * 4 + b < kb ? *reinterpret_cast<const uint2*>(from + b * 32) : make_uint2(0u, 0u);
+                    }
+                    if (DOWN) {
+                        // a term's scale is 2^-4 of the one's before it; the first is at least 2^(13 - 127)
+                        w0[i] = cs[i][g] - (t & 1) * 0x08080808u;
+                        w1[i] = w0[i] - 0x04040404u;
+                    } else {
+                        w0[i] = lds32(s0[i] + g * 4);
+                        w1[i] = lds32(s1[i] + g * 4);
+                    }
+                }
+                copy_wait<kMdDepth - 2>();
+                __syncwarp();
+                issue(stage == 0 ? (kMdDepth - 1) * kMdStage : stage - kMdStage);
+                const uint32_t from = ring + stage;
+                stage = stage + kMdStage < kMdDepth * kMdStage ? stage + kMdStage : 0;
+                float su[4], sl[4];
+                e8m0x4(lds32(from + word), su);
+                e8m0x4(lds32(from + word + 128), sl);
+                uint2 wu[4], wl[4];
+                const uint32_t row = from + q * kMdRow + t * 8;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    wu[b] = lds64(row + b * 32);
+                    wl[b] = lds64(row + 8 * kMdRow + b * 32);
                 }
 #pragma unroll
                 for (int i = 0; i < kMdTiles; ++i) {
                     if (i >= nt) break;
-                    // this lane's column of B, and the two columns of its sums
-                    const int rb = r0 + i * 8 + (lane >> 2), rd = r0 + i * 8 + (lane & 3) * 2;
-                    const bool inb = rb < rows;
-                    const int64_t tb = inb ? list.order[first + rb] / a.topk : 0;
-                    const int64_t t0 = rd < rows ? list.order[first + rd] / a.topk : 0;
-                    const int64_t t1 = rd + 1 < rows ? list.order[first + rd + 1] / a.topk : 0;
+                    float x0[4], x1[4];
+                    e8m0x4(w0[i], x0);
+                    e8m0x4(w1[i], x1);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int g = (chunk * 2 + q) * kMdWarps + warp;
-                        if (g >= groups) break;
-                        uint2 x[4];
-#pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            x[b] = inb && g * 4 + b < kb ? ld_nc64(a.codes + tb * a.k + (g * 4 + b) * 32 + (lane & 3) * 8)
-                                                         : make_uint2(0u, 0u);
-                        float s0[4], s1[4], sg[4], su[4];
-                        e8m0x4(row_scales(a.scales + t0 * kb, g, kb), s0);
-                        e8m0x4(row_scales(a.scales + t1 * kb, g, kb), s1);
-                        e8m0x4(t.s[q][0], sg);
-                        e8m0x4(t.s[q][1], su);
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            float d[4];
-                            mma_e4m3(d, t.w[q][b][0], t.w[q][b][1], x[b]);
-                            acc[i][0] = __fmaf_rn(d[0] * sg[b], s0[b], acc[i][0]);
-                            acc[i][1] = __fmaf_rn(d[1] * sg[b], s1[b], acc[i][1]);
-                            acc[i][2] = __fmaf_rn(d[2] * su[b], s0[b], acc[i][2]);
-                            acc[i][3] = __fmaf_rn(d[3] * su[b], s1[b], acc[i][3]);
-                        }
+                    for (int b = 0; b < 4; ++b) {
+                        if (!whole && g * 4 + b >= kb) break;       // scales of no block may be anything
+                        float d[4];
+                        mma_e4m3(d, wu[b], wl[b], x[i][b]);
+                        scaled_add(acc[i], d, su[b], sl[b], f2_pack(x0[b], x1[b]));
                     }
                 }
-                if (chunk == chunks - 1) {
-                    float* p = red + (step / chunks) * pass_words + warp * a.tiles * 128 + lane;
+            }
+            float* p = red + (flip * kMdWarps + warp) * warp_words + lane;
 #pragma unroll
-                    for (int i = 0; i < kMdTiles; ++i)
-                        if (i < nt)
+            for (int i = 0; i < kMdTiles; ++i)
+                if (i < nt) {
+                    float v[4];
+                    f2_unpack(acc[i][0], v[0], v[1]);
+                    f2_unpack(acc[i][1], v[2], v[3]);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) p[(i * 4 + j) * 32] = acc[i][j];
+                    for (int j = 0; j < 4; ++j) p[(i * 4 + j) * 33] = v[j];
                 }
+            __syncthreads();
+            if (DOWN) {
+                // 64 features of up to four rows: the sums of a feature's two warps over the four terms
+                const int f = tid & 63, r = tid >> 6;
+                if (r < left && r < nt * 2 && f0 + f < features) {
+                    const float* s = red + (flip * kMdWarps + (f >> 4) * 2) * warp_words + ((r >> 1) * 4 + (f >> 3 & 1) * 2) * 33 +
+                                     (f & 7) * 4 + (r & 1) * 2;
+                    const float* z = s + warp_words;
+                    a.y[(int64_t)list.order[first + r0 + r] * a.k + f0 + f] =
+                        ((s[34] + z[34]) + (s[1] + z[1])) + ((s[33] + z[33]) + (s[0] + z[0]));
+                }
+            } else {
+                // a warp takes a row, a lane a feature: the sums of its two warps, the activation, and the terms of h
+                for (int r = warp; r < nt * 8 && r < left; r += kMdWarps) {
+                    const float* s = red + (flip * kMdWarps + (lane >> 3) * 2) * warp_words + ((r >> 3) * 4 + (r & 1)) * 33 +
+                                     (lane & 7) * 4 + ((r & 7) >> 1);
+                    const float g = s[0] + s[warp_words], u = s[66] + s[warp_words + 66];
+                    const float h = g / (1.0f + expf(-g)) * u;
+                    // the block's largest value goes to [2^7, 2^8), and each term leaves at most 2^-4 of what it rounds
+                    uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu) >> 23;
+                    top = top < 20u ? 20u : top > 254u ? 254u : top;
+                    float v = h * __uint_as_float((261u - top) << 23);
+                    if (isinf(v)) v = __uint_as_float(0x7FFFFFFFu);     // the codes have no infinity
+                    const int64_t choice = list.order[first + r0 + r];
+                    uint8_t* out = a.h + choice * 4 * a.n + f0 + lane;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t code = cvt_fp8x2<kE4M3>(v, 0.0f) & 0xFFu;
+                        out[j * a.n] = (uint8_t)code;
+                        v = (v - decode_fp8x2<kE4M3>(code).x) * 16.0f;
+                    }
+                    if (lane == 0) a.hs[choice * a.hgroups * 4 + block] = (uint8_t)(top - 7u);
+                }
+            }
+            flip ^= 1;                                  // the other half is free: its readers have met the barrier above
+        }
+        if (DOWN) {
+            __syncthreads();
+            if (tid == 0) {
+                __threadfence();
+                last_one = atomicAdd(a.done + block, 1) == list.active - 1;
+                __threadfence();
             }
             __syncthreads();
-            // a warp takes a row, a lane a feature
-            for (int r = warp; r < nt * 8 && r < left; r += kMdWarps) {
-                const float* p = red + (lane >> 3) * pass_words + ((r >> 3) * 4 + (r & 1)) * 32 + (lane & 7) * 4 + ((r & 7) >> 1);
-                float g = 0.0f, u = 0.0f;
-#pragma unroll
-                for (int v = 0; v < kMdWarps; ++v) {
-                    g += p[v * a.tiles * 128];
-                    u += p[v * a.tiles * 128 + 64];
-                }
-                const float h = g / (1.0f + expf(-g)) * u;
-                // the block's largest value goes to [2^14, 2^15): h = (hi + lo) * 2^(byte - 127)
-                uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu) >> 23;
-                top = top < 16u ? 16u : top > 254u ? 254u : top;
-                const float v = h * __uint_as_float((268u - top) << 23);
-                const uint32_t hi = pack_f16x2(v, 0.0f) & 0xFFFFu;
-                const float back = __half2float(__ushort_as_half((unsigned short)hi));
-                const uint32_t lo = (hi & 0x7C00u) == 0x7C00u ? 0u : pack_f16x2(v - back, 0.0f) & 0xFFFFu;
-                const int64_t choice = list.order[first + r0 + r];
-                a.hi[choice * a.n + f0 + lane] = (uint16_t)hi;
-                a.lo[choice * a.n + f0 + lane] = (uint16_t)lo;
-                if (lane == 0) a.hs[choice * a.hgroups * 4 + block] = (uint8_t)(top - 14u);
-            }
-            __syncthreads();
+            if (last_one) sum_choices(a, f0);
         }
     }
-}
-
-// -------------------------------------------- down product, sum over choices ----
-// A cluster takes 32 output features of all tokens.  The pairs of a chosen
-// expert and a group of 128 columns of n are cut evenly over its warps; a warp
-// adds its products, times the choices' weights, to sums of its own, which are
-// joined over the warps and over the cluster's blocks in a fixed order.
-struct DownTile {
-    uint2 w[2][4][2];           // two tiles of 16 features, four blocks of 32; features r, r + 8
-    uint32_t s[2][2];
-};
-
-__device__ __forceinline__ void load_down(DownTile& t, const MdArgs& a, int e, int64_t f0, int g) {
-    const int lane = (int)(threadIdx.x & 31u);
-    const int nb = (int)(a.n / 32), groups = a.hgroups;
-    const int64_t per = (a.k + 127) / 128 * groups * 512;
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int64_t f = f0 + m * 16 + r * 8 + (lane >> 2);
-            const uint8_t* row = a.down + ((int64_t)e * a.k + f) * a.n + (lane & 3) * 8;
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                t.w[m][b][r] = g * 4 + b < nb ? ld_l2_64(row + (g * 4 + b) * 32) : make_uint2(0u, 0u);
-            t.s[m][r] = ld_l2_32(scale_word(a.down_scales + e * per, f, g, groups));
-        }
-}
-
-__global__ void __launch_bounds__(kMdThreads, 2) moe_decode_down_kernel(const MdArgs a) {
-    __shared__ MdList list;
-    extern __shared__ __align__(16) unsigned char dyn[];
-    float* part = reinterpret_cast<float*>(dyn);        // [warps][tokens][33]
-    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t ranks;
-    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
-    const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
-    if (ranks > 1) cluster_arrive();
-    const int sums = a.tokens * 33;
-    float* gather = part + kMdWarps * sums;             // [ranks][tokens][32], in the first block
-    // Ids and weights may be read at once: the blocks of the launch before this one let it start only when whatever
-    // wrote them had completed.
-    sort_choices(a, list, *reinterpret_cast<MdScratch*>(dyn));
-    for (int i = tid; i < kMdWarps * sums; i += kMdThreads) part[i] = 0.0f;
-    const int64_t f0 = (int64_t)(blockIdx.x / ranks) * 32;
-    const int groups = a.hgroups, nb = (int)(a.n / 32);
-    const int units = list.active * groups, shares = (int)ranks * kMdWarps, share = (int)rank * kMdWarps + warp;
-    const int lo = (int)((int64_t)units * share / shares), hi = (int)((int64_t)units * (share + 1) / shares);
-    DownTile next;
-    if (lo < hi) load_down(next, a, list.expert[lo / groups], f0, lo % groups);
-    dependency_wait();
-    allow_dependents();
-    __syncthreads();
-    float* mine = part + warp * sums;
-    for (int u = lo; u < hi; ++u) {
-        const DownTile t = next;
-        if (u + 1 < hi) load_down(next, a, list.expert[(u + 1) / groups], f0, (u + 1) % groups);
-        const int ai = u / groups, g = u % groups;
-        const int first = list.start[ai], rows = list.start[ai + 1] - first;
-        for (int r0 = 0; r0 < rows; r0 += 8) {
-            const int rb = r0 + (lane >> 2), rd = r0 + (lane & 3) * 2;
-            const int64_t cb = rb < rows ? list.order[first + rb] : -1;
-            const int c0 = rd < rows ? list.order[first + rd] : -1, c1 = rd + 1 < rows ? list.order[first + rd + 1] : -1;
-            uint4 xh[4], xl[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const bool in = cb >= 0 && g * 4 + b < nb;
-                const int64_t at = cb * a.n + (g * 4 + b) * 32 + (lane & 3) * 8;
-                xh[b] = in ? __ldcg(reinterpret_cast<const uint4*>(a.hi + at)) : make_uint4(0u, 0u, 0u, 0u);
-                xl[b] = in ? __ldcg(reinterpret_cast<const uint4*>(a.lo + at)) : make_uint4(0u, 0u, 0u, 0u);
-            }
-            float s0[4], s1[4];
-            e8m0x4(c0 >= 0 ? __ldcg(reinterpret_cast<const uint32_t*>(a.hs) + (int64_t)c0 * groups + g) : 0u, s0);
-            e8m0x4(c1 >= 0 ? __ldcg(reinterpret_cast<const uint32_t*>(a.hs) + (int64_t)c1 * groups + g) : 0u, s1);
-            const float p0 = c0 >= 0 ? __ldcg(a.weights + c0) : 0.0f, p1 = c1 >= 0 ? __ldcg(a.weights + c1) : 0.0f;
-            float acc[2][4];
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                float sa[4], sb[4];
-                e8m0x4(t.s[m][0], sa);
-                e8m0x4(t.s[m][1], sb);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[m][j] = 0.0f;
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (g * 4 + b >= nb) break;
-                    const uint2 w0 = t.w[m][b][0], w1 = t.w[m][b][1];
-                    const uint32_t a0 = e4m3_f16(w0.x), a1 = e4m3_f16(w1.x), a2 = e4m3_f16(w0.x >> 16), a3 = e4m3_f16(w1.x >> 16);
-                    const uint32_t a4 = e4m3_f16(w0.y), a5 = e4m3_f16(w1.y), a6 = e4m3_f16(w0.y >> 16), a7 = e4m3_f16(w1.y >> 16);
-                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma_f16(d, a0, a1, a2, a3, xl[b].x, xl[b].y);
-                    mma_f16(d, a4, a5, a6, a7, xl[b].z, xl[b].w);
-                    mma_f16(d, a0, a1, a2, a3, xh[b].x, xh[b].y);
-                    mma_f16(d, a4, a5, a6, a7, xh[b].z, xh[b].w);
-                    acc[m][0] = __fmaf_rn(d[0] * sa[b], s0[b], acc[m][0]);
-                    acc[m][1] = __fmaf_rn(d[1] * sa[b], s1[b], acc[m][1]);
-                    acc[m][2] = __fmaf_rn(d[2] * sb[b], s0[b], acc[m][2]);
-                    acc[m][3] = __fmaf_rn(d[3] * sb[b], s1[b], acc[m][3]);
-                }
-            }
-            // columns of one tile are different tokens unless a token names an expert twice: then one column at a time
-            const int turns = list.twice ? 4 : 1;
-            for (int turn = 0; turn < turns; ++turn) {
-                if (turns == 1 || (lane & 3) == turn) {
-#pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const int f = m * 16 + r * 8 + (lane >> 2);
-                            if (c0 >= 0) {
-                                float* o = mine + c0 / a.topk * 33 + f;
-                                *o = __fmaf_rn(p0, acc[m][2 * r], *o);
-                            }
-                            if (c1 >= 0) {
-                                float* o = mine + c1 / a.topk * 33 + f;
-                                *o = __fmaf_rn(p1, acc[m][2 * r + 1], *o);
-                            }
-                        }
-                }
-                __syncwarp();
-            }
-        }
-    }
-    __syncthreads();
-    if (ranks > 1) cluster_wait();                      // the first block has started
-    uint32_t to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_addr(gather + rank * a.tokens * 32)));
-    for (int i = tid; i < a.tokens * 32; i += kMdThreads) {
-        const float* p = part + (i >> 5) * 33 + (i & 31);
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kMdWarps; ++w) v += p[w * sums];
-        if (ranks > 1) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * i), "f"(v) : "memory");
-        else a.out[(int64_t)(i >> 5) * a.k + f0 + (i & 31)] = (uint16_t)pack_bf16x2(v, 0.0f);
-    }
-    if (ranks == 1) return;
-    cluster_sync();
-    if (rank != 0) return;
-    for (int i = tid; i < a.tokens * 32; i += kMdThreads) {
-        float v = 0.0f;
-        for (uint32_t r = 0; r < ranks; ++r) v += gather[r * a.tokens * 32 + i];
-        a.out[(int64_t)(i >> 5) * a.k + f0 + (i & 31)] = (uint16_t)pack_bf16x2(v, 0.0f);
-    }
+    if (DOWN && list.active == 0)
+        for (int block = (int)blockIdx.x; block < blocks; block += (int)gridDim.x) sum_choices(a, (int64_t)block * 64);
+    copy_wait<0>();
 }
 
 }  // namespace fp8q
@@ -483,19 +491,21 @@ using namespace fp8q;
 
 namespace {
 
-// The two halves of h and a byte for every 32 values, rows of them filled up to words.
-size_t workspace_of(int64_t tokens, int topk, int64_t n) {
+// The down products, the four terms of h and a byte for every 32 of its values
+// (rows of them filled up to words), and a counter for every 64 features.
+size_t workspace_of(int64_t tokens, int topk, int64_t n, int64_t k) {
     const size_t choices = (size_t)tokens * (size_t)topk;
-    return choices * (size_t)n * 4 + choices * (size_t)((n + 127) / 128) * 4;
+    return choices * (size_t)k * 4 + choices * (size_t)n * 4 + choices * (size_t)((n + 127) / 128) * 4 + (size_t)((k + 63) / 64) * 4;
 }
 
 bool valid_row(int64_t k) { return k > 0 && k % MXFP8_BLOCK == 0 && k <= FP8Q_MOE_DECODE_MAX_ROW; }
 
 }  // namespace
 
-extern "C" size_t mxfp8_moe_decode_workspace_bytes(int64_t tokens, int topk, int64_t n) {
-    if (tokens < 0 || tokens > FP8Q_MOE_DECODE_MAX_TOKENS || topk < 1 || topk > FP8Q_MOE_MAX_TOPK || !valid_row(n)) return 0;
-    return workspace_of(tokens, topk, n);
+extern "C" size_t mxfp8_moe_decode_workspace_bytes(int64_t tokens, int topk, int64_t n, int64_t k) {
+    if (tokens < 0 || tokens > FP8Q_MOE_DECODE_MAX_TOKENS || topk < 1 || topk > FP8Q_MOE_MAX_TOPK || !valid_row(n) || !valid_row(k))
+        return 0;
+    return workspace_of(tokens, topk, n, k);
 }
 
 extern "C" fp8q_status_t mxfp8_moe_decode(const uint8_t* codes, const uint8_t* scales, const void* ids, int id_bytes,
@@ -516,7 +526,7 @@ extern "C" fp8q_status_t mxfp8_moe_decode(const uint8_t* codes, const uint8_t* s
     for (const void* p : in)
         if (!aligned16(p)) return FP8Q_ERR_ALIGN;
     if (!aligned16(out_bf16) || !aligned16(workspace)) return FP8Q_ERR_ALIGN;
-    const size_t need = workspace_of(tokens, topk, n);
+    const size_t need = workspace_of(tokens, topk, n, k);
     if (workspace_bytes < need) return FP8Q_ERR_SIZE;
     const size_t t = (size_t)tokens, w = (size_t)experts * (size_t)n * (size_t)k;
     const Range outs[] = {{out_bf16, t * (size_t)k * 2}, {workspace, need}};
@@ -528,30 +538,27 @@ extern "C" fp8q_status_t mxfp8_moe_decode(const uint8_t* codes, const uint8_t* s
     const int choices = (int)tokens * topk;
     MdArgs a = {codes, scales, ids, id_bytes == 8, weights, (int)tokens, topk, experts, n, k, gate_codes, gate_scales,
                 up_codes, up_scales, down_codes, down_scales};
-    a.hi = static_cast<uint16_t*>(workspace);
-    a.lo = a.hi + (size_t)choices * n;
-    a.hs = reinterpret_cast<uint8_t*>(a.lo + (size_t)choices * n);
     a.hgroups = (int)((n + 127) / 128);
+    a.y = static_cast<float*>(workspace);
+    a.h = reinterpret_cast<uint8_t*>(a.y + (size_t)choices * k);
+    a.hs = a.h + (size_t)choices * n * 4;
+    a.done = reinterpret_cast<int*>(a.hs + (size_t)choices * a.hgroups * 4);
     a.out = static_cast<uint16_t*>(out_bf16);
     a.tiles = (choices + 7) / 8 < kMdTiles ? (choices + 7) / 8 : kMdTiles;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    constexpr size_t kMaxUp = 4 * (kMdWarps * kMdTiles * 128 + 1) * sizeof(float);
-    constexpr size_t kMaxDown = (kMdWarps * 33 + kMdMaxCluster * 32) * FP8Q_MOE_DECODE_MAX_TOKENS * sizeof(float);
+    static_assert(kMdRing >= sizeof(MdScratch), "the sort works where the rings lie");
+    constexpr size_t kMaxScales = FP8Q_MOE_DECODE_MAX_TOKENS * (FP8Q_MOE_DECODE_MAX_ROW / 128) * 4;
+    constexpr size_t kMaxSmem = kMdRing + kMdTiles * kMdSums + 8 * (kMdMaxChoices + 8);
+    const size_t smem = kMdRing + (size_t)a.tiles * kMdSums + 8 * (size_t)list_stride(choices);
     static KernelCache up_cache, down_cache;
     int resident = 0;
-    const size_t up_smem = std::max(sizeof(MdScratch), 4 * (size_t)(kMdWarps * a.tiles * 128 + 1) * sizeof(float));
-    fp8q_status_t st = prepare_kernel(up_cache, moe_decode_up_kernel, kMdThreads, kMaxUp, kMaxUp, &resident);
-    if (st != FP8Q_OK) return st;
     const int most = choices < experts ? choices : experts;         // chosen experts
-    const unsigned up_blocks = grid_for((size_t)most * (size_t)(n / 32), 2);
-    st = launch(moe_decode_up_kernel, up_blocks, kMdThreads, up_smem, s, a);
+    fp8q_status_t st = prepare_kernel(up_cache, moe_decode_kernel<false>, kMdThreads, kMaxSmem, kMaxSmem + kMaxScales, &resident);
     if (st != FP8Q_OK) return st;
-    unsigned ranks = 1;
-    while (ranks < kMdMaxCluster && (int64_t)(k / 32) * ranks < 2 * sm_count() &&
-           (int64_t)ranks * kMdWarps < (int64_t)most * a.hgroups)
-        ranks *= 2;
-    const size_t down_smem = std::max(sizeof(MdScratch), (size_t)(kMdWarps * 33 + ranks * 32) * tokens * sizeof(float));
-    st = prepare_kernel(down_cache, moe_decode_down_kernel, kMdThreads, kMaxDown, kMaxDown, &resident);
+    st = launch(moe_decode_kernel<false>, grid_for((size_t)most * (size_t)(n / 32), 2), kMdThreads,
+                smem + (size_t)tokens * (size_t)((k + 127) / 128) * 4, s, a);
     if (st != FP8Q_OK) return st;
-    return launch_clusters(moe_decode_down_kernel, (unsigned)(k / 32) * ranks, ranks, kMdThreads, down_smem, s, a);
+    st = prepare_kernel(down_cache, moe_decode_kernel<true>, kMdThreads, kMaxSmem, kMaxSmem, &resident);
+    if (st != FP8Q_OK) return st;
+    return launch(moe_decode_kernel<true>, grid_for((size_t)most * (size_t)((k + 63) / 64), 2), kMdThreads, smem, s, a);
 }
