@@ -518,14 +518,14 @@ fp8q_status_t mxfp8_moe_swiglu(const uint8_t* codes, const uint8_t* scales, int6
  *   weights       : tokens * topk floats
  *   gate, up      : [experts, n, k], down: [experts, k, n], codes and scales as
  *                   mxfp8_quantize_swizzled writes them
- *   workspace     : mxfp8_moe_decode_workspace_bytes(tokens, topk, n, k)
- *                   bytes, caller-owned
+ *   workspace     : mxfp8_moe_decode_workspace_bytes(tokens, topk, n) bytes,
+ *                   caller-owned
  * tokens: at most FP8Q_MOE_DECODE_MAX_TOKENS, experts 1 .. FP8Q_MOE_MAX_EXPERTS
  * (FP8Q_ERR_SIZE); topk 1 .. FP8Q_MOE_MAX_TOPK, n and k positive multiples of
  * 32 up to FP8Q_MOE_DECODE_MAX_ROW (FP8Q_ERR_K).  tokens == 0 is a no-op. */
 #define FP8Q_MOE_DECODE_MAX_TOKENS 32
 #define FP8Q_MOE_DECODE_MAX_ROW 16384
-size_t mxfp8_moe_decode_workspace_bytes(int64_t tokens, int topk, int64_t n, int64_t k);
+size_t mxfp8_moe_decode_workspace_bytes(int64_t tokens, int topk, int64_t n);
 fp8q_status_t mxfp8_moe_decode(const uint8_t* codes, const uint8_t* scales, const void* ids, int id_bytes,
                                const float* weights, int64_t tokens, int topk, const uint8_t* gate_codes,
                                const uint8_t* gate_scales, const uint8_t* up_codes, const uint8_t* up_scales,

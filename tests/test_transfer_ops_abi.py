@@ -136,10 +136,10 @@ def test_grad_clip_refuses_overlapping_outputs(L):
 
 
 def test_moe_decode(L):
-    need = L.mxfp8_moe_decode_workspace_bytes(4, 2, 64, 96)
+    need = L.mxfp8_moe_decode_workspace_bytes(4, 2, 64)
     assert need >= 4 * 2 * 64 * 4
-    assert L.mxfp8_moe_decode_workspace_bytes(33, 2, 64, 96) == 0 and L.mxfp8_moe_decode_workspace_bytes(4, 2, 48, 96) == 0
-    assert L.mxfp8_moe_decode_workspace_bytes(4, 33, 64, 96) == 0 and L.mxfp8_moe_decode_workspace_bytes(4, 2, 64, 80) == 0
+    assert L.mxfp8_moe_decode_workspace_bytes(33, 2, 64) == 0 and L.mxfp8_moe_decode_workspace_bytes(4, 2, 48) == 0
+    assert L.mxfp8_moe_decode_workspace_bytes(4, 33, 64) == 0
 
     def call(c=P[0], s=P[1], ids=P[2], ib=8, w=P[3], tokens=4, topk=2, g=P[4], gs=P[5], u=P[6], us=P[7], d=P[8], ds=P[9],
              experts=3, n=64, k=96, out=P[10], ws=P[11], wb=need):

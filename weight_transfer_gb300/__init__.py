@@ -152,7 +152,7 @@ _SIGNATURES = {
     "fp8q_moe_combine_backward": ([_vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _i64, _vp, _vp, _vp], _int),
     "mxfp8_moe_matmul": ([_vp, _vp, _i64, _vp, _vp, _vp, _int, _i64, _i64, _vp, _vp], _int),
     "mxfp8_moe_swiglu": ([_vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _int, _i64, _i64, _vp, _vp, _vp], _int),
-    "mxfp8_moe_decode_workspace_bytes": ([_i64, _int, _i64, _i64], _sz),
+    "mxfp8_moe_decode_workspace_bytes": ([_i64, _int, _i64], _sz),
     "mxfp8_moe_decode": ([_vp, _vp, _vp, _int, _vp, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _int, _i64, _i64, _vp, _vp, _sz,
                           _vp], _int),
     "fp8q_token_logprobs": ([_vp, _int, _i64, _i64, _i64, _vp, _int, _f32, _int, _vp, _vp, _vp, _vp, _vp, _vp], _int),
@@ -999,8 +999,8 @@ def _ids(t: torch.Tensor, what: str, shape) -> tuple:
     return _in(t, what, t.dtype, shape), 8 if t.dtype is torch.int64 else 4
 
 
-def mxfp8_moe_decode_workspace_bytes(tokens: int, topk: int, n: int, k: int) -> int:
-    return int(_lib.mxfp8_moe_decode_workspace_bytes(tokens, topk, n, k))
+def mxfp8_moe_decode_workspace_bytes(tokens: int, topk: int, n: int) -> int:
+    return int(_lib.mxfp8_moe_decode_workspace_bytes(tokens, topk, n))
 
 
 def mxfp8_moe_decode(codes: torch.Tensor, scales: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
@@ -1025,7 +1025,7 @@ def mxfp8_moe_decode(codes: torch.Tensor, scales: torch.Tensor, ids: torch.Tenso
     dp, dsp = _expert_weights(down_codes, down_scales, "down_codes", experts, k, n)
     out, op = _out(out, "out", torch.bfloat16, (tokens, k), codes.device, tokens * k, stream)
     if workspace is None:
-        have = _lib.mxfp8_moe_decode_workspace_bytes(tokens, topk, n, k)
+        have = _lib.mxfp8_moe_decode_workspace_bytes(tokens, topk, n)
         workspace = _new(have, torch.uint8, codes.device, stream, kept=False)
     else:
         have = workspace.numel() * workspace.element_size()
