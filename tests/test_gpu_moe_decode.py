@@ -4,9 +4,9 @@ Tolerances.  A product's sum over K runs in blocks of 32 products, each summed
 exactly or with a rounding of 2^-23 per product, and the K / 32 blocks one after
 the other or in any tree: (K / 32 + 72) * 2^-24 of the sum of absolute values.
 The activation carries 2^-20 relative and the derivative's share of g's error;
-h is held as four e4m3 terms, each of which leaves 2^-4 of what it rounds: 2^-16
-of a value, and of the largest in its block of 32 half of 2^-9 * 2^-12 / 2^7 =
-2^-29, where a value is small enough to be subnormal.  The outer sums add
+h is held as two f16 terms, each of which leaves 2^-11 of what it rounds: 2^-22
+of a value, and of the largest in its block of 32 half of 2^-24 / 2^14 = 2^-39,
+where a value is small enough to be subnormal.  The outer sums add
 (topk + N / 32 + 72) * 2^-24, the output its rounding."""
 import pytest
 import torch
@@ -66,7 +66,7 @@ def formula(s):
             h = g * sig * u
             # |silu'| <= 1.1 everywhere; g enters exp(-g) with |g| 2^-24
             eh = 1.1 * eg * (u.abs() + eu) + (g * sig).abs() * eu + h.abs() * (2.0 ** -20 + 4 * U * g.abs().clamp(max=100))
-            eh = eh + h.abs() * 2.0 ** -16 + h.abs().view(-1, 32).amax(1).repeat_interleave(32) * 2.0 ** -29
+            eh = eh + h.abs() * 2.0 ** -22 + h.abs().view(-1, 32).amax(1).repeat_interleave(32) * 2.0 ** -39
             p = float(s["p"][t, j])
             out[t] += p * (D @ h)
             tol[t] += abs(p) * (D.abs() @ (eh + c2 * h.abs()))

@@ -26,8 +26,8 @@ struct MdArgs {
     int tokens, topk, experts;
     int64_t n, k;
     const uint8_t *gate, *gate_scales, *up, *up_scales, *down, *down_scales;
-    uint8_t* h;                                     // [tokens * topk, 4, n], h's four terms
-    uint8_t* hs;                                    // [tokens * topk, hgroups * 4], the first one's scales
+    uint16_t* h;                                    // [tokens * topk, 2, n], h's two terms in f16
+    uint8_t* hs;                                    // [tokens * topk, hgroups * 4], their scales
     int hgroups;                                    // groups of four blocks of 32
     uint16_t* out;                                  // [tokens, k]
     int tiles;                                      // column tiles that a pass takes, at most kMdTiles
@@ -41,6 +41,18 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint2 a0, uint2 a1, uint
     asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0.x), "r"(a1.x), "r"(a0.y), "r"(a1.y), "r"(b.x), "r"(b.y), "f"(0.0f));
+}
+// The same for 16 columns of K and f16 operands: A's codes as f16, exactly.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t e4m3_f16(uint32_t two) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+    return r;
 }
 // Four E8M0 bytes -> 2^(byte - 127) each, NaN for 255.
 __device__ __forceinline__ void e8m0x4(uint32_t w, float (&f)[4]) {
@@ -65,12 +77,10 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
     return r;
 }
-// acc += (d * row) * column for a tile's sums over one block of 32: rows' scales a and b, columns' c0 and c1.
-__device__ __forceinline__ void scaled_add(float (&acc)[4], const float (&d)[4], float a, float b, float c0, float c1) {
-    acc[0] = __fmaf_rn(d[0] * a, c0, acc[0]);
-    acc[1] = __fmaf_rn(d[1] * a, c1, acc[1]);
-    acc[2] = __fmaf_rn(d[2] * b, c0, acc[2]);
-    acc[3] = __fmaf_rn(d[3] * b, c1, acc[3]);
+// acc += (d * row) * column for a tile's sums over one block of 32: rows' scales a and b, columns' c.
+__device__ __forceinline__ void scaled_add(uint64_t (&acc)[2], const float (&d)[4], float a, float b, uint64_t c) {
+    acc[0] = f2_fma(f2_mul(f2_pack(d[0], d[1]), f2_pack(a, a)), c, acc[0]);
+    acc[1] = f2_fma(f2_mul(f2_pack(d[2], d[3]), f2_pack(b, b)), c, acc[1]);
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t r;
@@ -191,34 +201,25 @@ __device__ __forceinline__ void copy_unit(uint32_t stage, const uint8_t* upper, 
     if (lane < 16) copy16(stage + kMdScales + lane * 16, line);
 }
 
-// A unit's products with one or two tiles of columns: x their bytes, w0 and w1
-// the scales of this lane's two columns.  `word`: the scale word of its rows.
-__device__ __forceinline__ void multiply_unit(float (&acc)[kMdTiles][4], uint32_t stage, uint32_t word, const uint2 (&x)[kMdTiles][4],
-                                              const uint32_t (&w0)[kMdTiles], const uint32_t (&w1)[kMdTiles], int nt, int nblocks) {
+// What this lane multiplies of a unit: its two rows' bytes of the four blocks,
+// and their scales.  `word`: the scale word of the unit's rows.  Scales of blocks
+// from `nblocks` on may be anything and become 0, as the codes there are.
+struct Weights {
+    uint2 u[4], l[4];
+    float su[4], sl[4];
+};
+__device__ __forceinline__ uint32_t only(uint32_t scales, int nblocks) {
+    return nblocks < 4 ? scales & ((1u << (8 * nblocks)) - 1u) : scales;
+}
+__device__ __forceinline__ void read_unit(Weights& w, uint32_t stage, uint32_t word, int nblocks) {
     const int lane = (int)(threadIdx.x & 31u), q = lane >> 2, t = lane & 3;
     const uint32_t scales = stage + kMdScales + q * 16 + word, row = stage + q * kMdRow + t * 8;
-    float su[4], sl[4];
-    e8m0x4(lds32(scales), su);
-    e8m0x4(lds32(scales + 128), sl);
-    uint2 wu[4], wl[4];
+    e8m0x4(only(lds32(scales), nblocks), w.su);
+    e8m0x4(only(lds32(scales + 128), nblocks), w.sl);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-        wu[b] = lds64(row + b * 32);
-        wl[b] = lds64(row + 8 * kMdRow + b * 32);
-    }
-#pragma unroll
-    for (int i = 0; i < kMdTiles; ++i) {
-        if (i >= nt) break;
-        float c0[4], c1[4];
-        e8m0x4(w0[i], c0);
-        e8m0x4(w1[i], c1);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            if (b >= nblocks) break;                    // scales of no block may be anything
-            float d[4];
-            mma_e4m3(d, wu[b], wl[b], x[i][b]);
-            scaled_add(acc[i], d, su[b], sl[b], c0[b], c1[b]);
-        }
+        w.u[b] = lds64(row + b * 32);
+        w.l[b] = lds64(row + 8 * kMdRow + b * 32);
     }
 }
 
@@ -318,11 +319,9 @@ template <int SPLIT> __global__ void __launch_bounds__(kUpThreads, 2) moe_decode
                 s0[i] = smem_addr(xscales + list.token[at + (rd < left ? rd : 0)] * groups + part);
                 s1[i] = smem_addr(xscales + list.token[at + (rd + 1 < left ? rd + 1 : 0)] * groups + part);
             }
-            float acc[kMdTiles][4];
+            uint64_t acc[kMdTiles][2];
 #pragma unroll
-            for (int i = 0; i < kMdTiles; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+            for (int i = 0; i < kMdTiles; ++i) acc[i][0] = acc[i][1] = 0;
             for (int b0 = part * 4; b0 < kb; b0 += 4 * SPLIT) {
                 uint2 x[kMdTiles][4];
                 uint32_t w0[kMdTiles], w1[kMdTiles];
@@ -346,15 +345,33 @@ template <int SPLIT> __global__ void __launch_bounds__(kUpThreads, 2) moe_decode
                 copy_wait<kUpDepth - 2>();
                 __syncwarp();
                 issue(stage == 0 ? (kUpDepth - 1) * kMdStage : stage - kMdStage);
-                multiply_unit(acc, ring + stage, (uint32_t)(block & 3) * 4, x, w0, w1, nt, kb - b0);
+                Weights w;
+                read_unit(w, ring + stage, (uint32_t)(block & 3) * 4, kb - b0);
+#pragma unroll
+                for (int i = 0; i < kMdTiles; ++i) {
+                    if (i >= nt) break;
+                    float c0[4], c1[4];
+                    e8m0x4(w0[i], c0);
+                    e8m0x4(w1[i], c1);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        float d[4];
+                        mma_e4m3(d, w.u[b], w.l[b], x[i][b]);
+                        scaled_add(acc[i], d, w.su[b], w.sl[b], f2_pack(c0[b], c1[b]));
+                    }
+                }
                 stage = stage + kMdStage < kUpDepth * kMdStage ? stage + kMdStage : 0;
             }
             float* p = red + (flip * kUpWarps + warp) * warp_words + lane;
 #pragma unroll
             for (int i = 0; i < kMdTiles; ++i)
-                if (i < nt)
+                if (i < nt) {
+                    float v[4];
+                    f2_unpack(acc[i][0], v[0], v[1]);
+                    f2_unpack(acc[i][1], v[2], v[3]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) p[(i * 4 + j) * 33] = acc[i][j];
+                    for (int j = 0; j < 4; ++j) p[(i * 4 + j) * 33] = v[j];
+                }
             team_sync<SPLIT>(team);
             // a warp takes a row, a lane a feature: the sums, the activation, and the terms of h
             for (int r = member; r < nt * 8 && r < left; r += kTeam) {
@@ -363,20 +380,17 @@ template <int SPLIT> __global__ void __launch_bounds__(kUpThreads, 2) moe_decode
                 float g = s[0], u = s[66];
                 if (SPLIT == 2) g += s[warp_words], u += s[warp_words + 66];
                 const float h = g / (1.0f + expf(-g)) * u;
-                // the block's largest value goes to [2^7, 2^8), and each term leaves at most 2^-4 of what it rounds
+                // the block's largest value goes to [2^14, 2^15): h = (hi + lo) * 2^(byte - 127)
                 uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu) >> 23;
-                top = top < 20u ? 20u : top > 254u ? 254u : top;
-                float v = h * __uint_as_float((261u - top) << 23);
-                if (isinf(v)) v = __uint_as_float(0x7FFFFFFFu);     // the codes have no infinity
+                top = top < 16u ? 16u : top > 254u ? 254u : top;
+                const float v = h * __uint_as_float((268u - top) << 23);
+                const __half hi = __float2half_rn(v);
+                const __half lo = __hisinf(hi) ? __half(0.0f) : __float2half_rn(v - __half2float(hi));
                 const int64_t choice = list.order[first + r0 + r];
-                uint8_t* out = a.h + choice * 4 * a.n + block * 32 + lane;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t code = cvt_fp8x2<kE4M3>(v, 0.0f) & 0xFFu;
-                    out[j * a.n] = (uint8_t)code;
-                    v = (v - decode_fp8x2<kE4M3>(code).x) * 16.0f;
-                }
-                if (lane == 0) a.hs[choice * a.hgroups * 4 + block] = (uint8_t)(top - 7u);
+                uint16_t* out = a.h + choice * 2 * a.n + block * 32 + lane;
+                out[0] = __half_as_ushort(hi);
+                out[a.n] = __half_as_ushort(lo);
+                if (lane == 0) a.hs[choice * a.hgroups * 4 + block] = (uint8_t)(top - 14u);
             }
             flip ^= 1;                                  // the other half is free: its readers have met the barrier above
         }
@@ -387,8 +401,8 @@ template <int SPLIT> __global__ void __launch_bounds__(kUpThreads, 2) moe_decode
 // -------------------------------------------- down product, sum over choices ----
 // A block, or a cluster of them where there are few, takes 16 output features
 // of all tokens.  The pairs of a chosen expert and a group of 128 columns of n
-// are cut evenly over its warps; the columns of a tensor-core tile are the four
-// terms of two rows of h.  A warp adds its products, times the choices' weights,
+// are cut evenly over its warps; the columns of a tensor-core tile are the two
+// terms of four rows of h.  A warp adds its products, times the choices' weights,
 // to sums of its own, which are joined over the warps and over the cluster's
 // blocks in a fixed order.  The first weights are on their way before h is
 // waited for.
@@ -419,12 +433,16 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_decode_down_kernel(const 
     const uint32_t ring = smem_addr(dyn) + warp * kDownDepth * kMdStage;
     const int q = lane >> 2, t = lane & 3;
 
-    int c_unit = lo, c_ai = lo / groups, c_g = lo % groups;         // where the copies are
+    int c_unit = lo, c_g = 0, c_end = 0, c_left_rows = 0;           // where the copies are: an expert's groups from c_unit on
     const int64_t four = 4 * a.n, matrix = (a.k + 127) / 128 * groups * 512;
     const uint8_t *upper = nullptr, *line = nullptr;
     auto aim = [&] {
         if (c_unit >= hi) return;
-        const int64_t e = list.expert[c_ai];
+        const int ai = c_unit / groups;
+        c_g = c_unit - ai * groups;
+        c_end = c_g + (hi - c_unit) < groups ? c_g + (hi - c_unit) : groups;
+        if (c_left_rows <= 0) c_left_rows = list.start[ai + 1] - list.start[ai];
+        const int64_t e = list.expert[ai];
         upper = a.down + (e * a.k + f0 + (lane >> 3)) * a.n + c_g * 128 + (lane & 7) * 16;
         line = scale_line(a.down_scales, f0 + (lane & 15), c_g, groups) + matrix * e;
     };
@@ -433,10 +451,9 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_decode_down_kernel(const 
             copy_unit(ring + at, upper, upper + 2 * four, four, line, (int)a.n - c_g * 128);
             upper += 128;
             line += 512;
-            ++c_unit;
-            if (++c_g == groups) {
-                c_g = 0;
-                ++c_ai;
+            if (++c_g == c_end) {
+                c_left_rows -= 4;
+                if (c_left_rows <= 0) c_unit += c_end - c_unit % groups;
                 aim();
             }
         }
@@ -452,66 +469,56 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_decode_down_kernel(const 
     allow_dependents();
 
     uint32_t stage = 0;
-    int ai = lo / groups, g = lo % groups;
-    float acc[kMdTiles][4] = {};                        // of an expert's first four rows, over its groups
-    for (int u = lo; u < hi; ++u) {
+    const uint32_t word = (uint32_t)(f0 >> 5 & 3) * 4;
+    for (int u = lo; u < hi;) {
+        // one expert's groups g0 .. g1 - 1, four rows at a time: this lane's column of B is term q % 2 of row q / 2, its
+        // sums' columns are both terms of row t
+        const int ai = u / groups, g0 = u - ai * groups, g1 = g0 + (hi - u) < groups ? g0 + (hi - u) : groups;
         const int first = list.start[ai], rows = list.start[ai + 1] - first;
-        const bool last = g == groups - 1 || u == hi - 1;
-        for (int r0 = 0; r0 < rows; r0 += 2 * kMdTiles) {
-            const int left = rows - r0, nt = left > 2 ? 2 : 1;
-            // this lane's column of B: term q % 4 of row q / 4; its sums' columns: terms 2 t and 2 t + 1 of a row
-            uint2 x[kMdTiles][4];
-            uint32_t w0[kMdTiles], w1[kMdTiles];
-            int choice[kMdTiles];                       // of this lane's sums, or -1
+        for (int r0 = 0; r0 < rows; r0 += 4) {
+            const int left = rows - r0, at = first + r0;
+            const int choice = list.order[at + (t < left ? t : 0)];
+            const uint16_t* hb = a.h + ((int64_t)list.order[at + ((q >> 1) < left ? q >> 1 : 0)] * 2 + (q & 1)) * a.n + g0 * 128 + t * 8;
+            const uint32_t* sb = reinterpret_cast<const uint32_t*>(a.hs) + (int64_t)choice * groups;
+            float upper_sum = 0.0f, lower_sum = 0.0f;
+            for (int g = g0; g < g1; ++g, hb += 128) {
+                uint4 x[4];
+                if (g * 4 + 4 <= nb) {
 #pragma unroll
-            for (int i = 0; i < kMdTiles; ++i) {
-                const int rb = i * 2 + (q >> 2), rd = i * 2 + (t >> 1), at = first + r0;
-                choice[i] = rd < left ? list.order[at + rd] : -1;
-                if (i >= nt) break;
-                const uint8_t* hb = a.h + ((int64_t)list.order[at + (rb < left ? rb : 0)] * 4 + (q & 3)) * a.n + g * 128 + t * 8;
+                    for (int b = 0; b < 4; ++b) x[b] = *reinterpret_cast<const uint4*>(hb + b * 32);
+                } else {
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    x[i][b] = g * 4 + b < nb ? *reinterpret_cast<const uint2*>(hb + b * 32) : make_uint2(0u, 0u);
-                // a term's scale is 2^-4 of the one's before it; the first is at least 2^(13 - 127)
-                w0[i] = reinterpret_cast<const uint32_t*>(a.hs)[(int64_t)list.order[at + (rd < left ? rd : 0)] * groups + g] -
-                        (t & 1) * 0x08080808u;
-                w1[i] = w0[i] - 0x04040404u;
-            }
-            if (r0 == 0) {
+                    for (int b = 0; b < 4; ++b)
+                        x[b] = g * 4 + b < nb ? *reinterpret_cast<const uint4*>(hb + b * 32) : make_uint4(0u, 0u, 0u, 0u);
+                }
+                float c[4];
+                e8m0x4(only(sb[g], nb - g * 4), c);
                 copy_wait<kDownDepth - 2>();
                 __syncwarp();
                 issue(stage == 0 ? (kDownDepth - 1) * kMdStage : stage - kMdStage);
-            } else {
+                Weights w;
+                read_unit(w, ring + stage, word, nb - g * 4);
 #pragma unroll
-                for (int i = 0; i < kMdTiles; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+                for (int b = 0; b < 4; ++b) {
+                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma_f16(d, e4m3_f16(w.u[b].x), e4m3_f16(w.l[b].x), e4m3_f16(w.u[b].x >> 16), e4m3_f16(w.l[b].x >> 16), x[b].x,
+                            x[b].y);
+                    mma_f16(d, e4m3_f16(w.u[b].y), e4m3_f16(w.l[b].y), e4m3_f16(w.u[b].y >> 16), e4m3_f16(w.l[b].y >> 16), x[b].z,
+                            x[b].w);
+                    upper_sum = __fmaf_rn((d[0] + d[1]) * w.su[b], c[b], upper_sum);
+                    lower_sum = __fmaf_rn((d[2] + d[3]) * w.sl[b], c[b], lower_sum);
+                }
+                stage = stage + kMdStage < kDownDepth * kMdStage ? stage + kMdStage : 0;
             }
-            multiply_unit(acc, ring + stage, (uint32_t)(f0 >> 5 & 3) * 4, x, w0, w1, nt, nb - g * 4);
-            // the first four rows' sums go on over the expert's groups, unless more rows need the registers
-            if (rows <= 2 * kMdTiles && !last) continue;
-#pragma unroll
-            for (int i = 0; i < kMdTiles; ++i) {
-                if (i >= nt) break;
-                const float p = choice[i] >= 0 ? __ldcg(a.weights + choice[i]) : 0.0f;
-                float v0 = acc[i][0] + acc[i][1], v1 = acc[i][2] + acc[i][3];
-                v0 += __shfl_xor_sync(0xFFFFFFFFu, v0, 1);
-                v1 += __shfl_xor_sync(0xFFFFFFFFu, v1, 1);
-                float* o = mine + (choice[i] >= 0 ? choice[i] / a.topk * 17 : 0) + q;
-                // a token that names an expert twice has both rows of a tile: the upper one adds after the lower one
-                if (t == 0 && choice[i] >= 0) o[0] = __fmaf_rn(p, v0, o[0]), o[8] = __fmaf_rn(p, v1, o[8]);
+            // one row after the other: a token that names an expert twice has two of them
+            const float p = __ldcg(a.weights + choice);
+            float* o = mine + choice / a.topk * 17 + q;
+            for (int turn = 0; turn < 4 && turn < left; ++turn) {
+                if (t == turn) o[0] = __fmaf_rn(p, upper_sum, o[0]), o[8] = __fmaf_rn(p, lower_sum, o[8]);
                 __syncwarp();
-                if (t == 2 && choice[i] >= 0) o[0] = __fmaf_rn(p, v0, o[0]), o[8] = __fmaf_rn(p, v1, o[8]);
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
             }
         }
-        stage = stage + kMdStage < kDownDepth * kMdStage ? stage + kMdStage : 0;
-        if (++g == groups) {
-            g = 0;
-            ++ai;
-        }
+        u += g1 - g0;
     }
     copy_wait<0>();
     __syncthreads();
@@ -542,7 +549,7 @@ using namespace fp8q;
 
 namespace {
 
-// The four terms of h and a byte for every 32 of its values, rows of them filled up to words.
+// The two terms of h and a byte for every 32 of its values, rows of them filled up to words.
 size_t workspace_of(int64_t tokens, int topk, int64_t n) {
     const size_t choices = (size_t)tokens * (size_t)topk;
     return choices * (size_t)n * 4 + choices * (size_t)((n + 127) / 128) * 4;
@@ -588,8 +595,8 @@ extern "C" fp8q_status_t mxfp8_moe_decode(const uint8_t* codes, const uint8_t* s
     MdArgs a = {codes, scales, ids, id_bytes == 8, weights, (int)tokens, topk, experts, n, k, gate_codes, gate_scales,
                 up_codes, up_scales, down_codes, down_scales};
     a.hgroups = (int)((n + 127) / 128);
-    a.h = static_cast<uint8_t*>(workspace);
-    a.hs = a.h + (size_t)choices * n * 4;
+    a.h = static_cast<uint16_t*>(workspace);
+    a.hs = reinterpret_cast<uint8_t*>(a.h + (size_t)choices * n * 2);
     a.out = static_cast<uint16_t*>(out_bf16);
     a.tiles = (choices + 7) / 8 < kMdTiles ? (choices + 7) / 8 : kMdTiles;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
