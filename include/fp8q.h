@@ -587,8 +587,8 @@ fp8q_status_t fp8q_token_logprobs_backward(const void* logits, int logit_bytes, 
  *     out_i   = RN(x_i * RN(scale * norm[1])), rounded to the output's type
  * `scale` is what the gradients are to be multiplied by anyway: 1 / ranks
  * where they are the ranks' sum (fp8q_dequant_reduce).  Squares are summed in
- * binary32 by 64 and in binary64 above, over any magnitude and in a fixed
- * order.  NaN and infinities are not looked for: a NaN anywhere makes the norm
+ * binary32 by 2048 (11 additions deep, then 5) and in binary64 above, over any
+ * magnitude and in a fixed order.  NaN and infinities are not looked for: a NaN anywhere makes the norm
  * and all clipped gradients NaN; an infinite norm makes norm[1] 0.
  *
  * fp8q_grad_plan (host only, no GPU) checks a list of tensors and lays it out

@@ -1,8 +1,9 @@
 """The global gradient norm and clipping against the formulas in 64 bits.
 
-Tolerances.  A thread sums up to 64 squares in binary32, in four chains of 16
-and two joins: 18 roundings of 2^-24, which the square root halves; then one of
-the result.  So 10 * 2^-24 for a norm, one more for the coefficient; a clipped
+Tolerances.  A thread sums 64 squares in binary32, in eight chains of 8 and three
+joins, and a warp its 32 sums in five more: 16 roundings of 2^-24, which the
+square root halves; then one of the result.  So 9 (taken as 10) * 2^-24 for a
+norm, one more for the coefficient; a clipped
 gradient carries the coefficient's, the factor's and the product's roundings and
 that of its type."""
 import math
@@ -141,6 +142,17 @@ def test_any_magnitude(kind, size):
     mixed[5] = size * 1e-6
     norm, _ = w.fp8q_grad_norm([mixed])
     check_norm(norm, None, [mixed], math.inf, 1.0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_zeros_among_the_gradients(kind):
+    """Rows that got no gradient: whole warps of zeros, lanes of zeros beside others, and one value alone."""
+    x = torch.zeros(200_000, dtype=kind, device="cuda")
+    x[70_000:90_000] = 1e-4
+    x[199_999] = -3.0
+    x[100_000:120_000:97] = 1e-12
+    norm, each = w.fp8q_grad_norm([x, x[:60_000], x[120_000:199_000]], want_each=True)
+    check_norm(norm, each, [x, x[:60_000], x[120_000:199_000]], math.inf, 1.0)
 
 
 def test_zero_and_nothing():

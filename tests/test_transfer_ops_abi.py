@@ -93,10 +93,12 @@ def test_grad_plan(L):
 
 
 def test_grad_workspace_grows_with_the_chunks(L):
-    """8 bytes for each chunk of 16,384 elements, of larger ones past 2^28 elements."""
+    """8 bytes for each chunk of 32 KB, of larger ones past 4096 of them."""
     sizes = [1, 16384, 16385, 0, 40000]
     assert plan_of(L, *[(P[i], None, n, 0, 0) for i, n in enumerate(sizes)])[2] == 8 * (1 + 1 + 2 + 0 + 3)
-    assert plan_of(L, (P[0], None, 3_500_000_000, 0, 0))[2] <= 8 * 16384
+    assert plan_of(L, *[(P[i], None, n, 1, 0) for i, n in enumerate([1, 8192, 8193])])[2] == 8 * (1 + 1 + 2)
+    assert plan_of(L, (P[0], None, 3_500_000_000, 0, 0))[2] == 8 * -(-7_000_000_000 // (1 << 21))
+    assert plan_of(L, (P[0], None, 1 << 42, 0, 0))[2] == 8 * 4096
 
 
 @pytest.mark.parametrize("name", ["fp8q_grad_norm", "fp8q_grad_clip"])

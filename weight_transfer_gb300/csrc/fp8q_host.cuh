@@ -78,6 +78,7 @@ unsigned unit_errors_mxfp8(bool clear);
 unsigned unit_errors_selftest(bool clear);
 unsigned unit_errors_tensorwise(bool clear);
 unsigned unit_errors_moe_product(bool clear);
+unsigned unit_errors_grad_norm(bool clear);
 
 // The driver's cuTensorMapEncodeTiled (PFN_cuTensorMapEncodeTiled_v12000), or
 // NULL where the driver has none.

@@ -2,16 +2,17 @@
 //
 //     norm = scale * sqrt(sum of x^2 over all tensors),  coefficient = min(1, max_norm / (norm + 1e-6))
 //     out = x * (scale * coefficient)
-// The tensors are cut into chunks of a fixed number of elements; a block sums
-// one chunk's squares into its place of the workspace, and a single block
-// joins the places in their order, so that the norm does not depend on timing.
+// The tensors are cut into chunks of a fixed number of bytes; a block sums one
+// chunk's squares into its place of the workspace, and a single block joins the
+// places in their order, so that the norm does not depend on timing.
 // The table of tensors travels in the kernel's parameters, kGradGroup at a
 // time: nothing is copied to the device ahead of the launch, and a captured
 // graph keeps the table with its node.
 //
-// A thread's squares are summed in binary32 (up to 64 of them) and everything
-// above in binary64.  Sums outside [2^-80, 2^100] would lose squares to the
-// range of binary32; their elements are summed again in binary64.
+// A thread sums 64 squares in binary32, in eight chains, a warp its threads'
+// sums, and everything above is binary64 (of which this GPU does two additions
+// a cycle and SM).  Sums outside [2^-80, 2^100] would lose squares to the range
+// of binary32; their elements are summed again in binary64.
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 
@@ -22,24 +23,27 @@
 namespace fp8q {
 
 constexpr int kGradGroup = 1024;            // tensors per launch
+constexpr int kGradFew = 64;                // a launch of no more has a smaller table
 constexpr int kGradThreads = 256;
-constexpr int64_t kGradChunk = 16384;       // elements of the smallest chunk
-constexpr int64_t kGradMaxChunks = 16384;   // larger chunks keep their number near this
+constexpr int kPiece = 32768;               // bytes of one copy
+constexpr int kStages = 5;
+constexpr uint64_t kGradMaxChunks = 4096;   // chunks grow from one piece so that there are not many more than this
 constexpr int kJoinThreads = 1024;
 
 // Element types and count share a word: count in the low 44 bits.
-struct GradTable {
-    const void* grad[kGradGroup];
-    void* out[kGradGroup];
-    uint64_t kind[kGradGroup];
-    uint32_t first[kGradGroup + 1];         // chunks of the group's earlier tensors
+template <int N> struct GradTableN {
+    const void* grad[N];
+    void* out[N];
+    uint64_t kind[N];
+    uint32_t first[N + 1];                  // chunks of the group's earlier tensors
     int count;
 };
+using GradTable = GradTableN<kGradGroup>;
 static_assert(sizeof(GradTable) + 64 <= 32764, "a kernel's parameters");
 constexpr uint64_t kCountMask = (1ull << 44) - 1;
 constexpr uint64_t kGradF32 = 1ull << 62, kOutF32 = 1ull << 63;
 
-__device__ __forceinline__ int tensor_of(const GradTable& t, uint32_t chunk) {
+template <int N> __device__ __forceinline__ int tensor_of(const GradTableN<N>& t, uint32_t chunk) {
     int lo = 0, hi = t.count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -48,89 +52,78 @@ __device__ __forceinline__ int tensor_of(const GradTable& t, uint32_t chunk) {
     return lo;
 }
 
-// The elements [lo, hi) of a tensor that a chunk holds, and the first of them
-// that lies on a 16-byte boundary.
-struct Chunk {
-    int64_t lo, hi, body;
-    int64_t vecs;
-};
-template <int BYTES> __device__ __forceinline__ Chunk cut_chunk(const void* p, int64_t n, int64_t index, int64_t size) {
-    Chunk c;
-    c.lo = index * size;
-    c.hi = c.lo + size < n ? c.lo + size : n;
-    const uint32_t off = (uint32_t)((reinterpret_cast<uintptr_t>(p) + (uintptr_t)c.lo * BYTES) & 15u);
-    const int64_t to = c.lo + (int64_t)((16u - off) & 15u) / BYTES;
-    c.body = to < c.hi ? to : c.hi;
-    c.vecs = (c.hi - c.body) / (16 / BYTES);
-    return c;
-}
-
 template <int BYTES> __device__ __forceinline__ float load_grad(const void* p, int64_t i) {
     return BYTES == 2 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16) : static_cast<const float*>(p)[i];
 }
 
-template <int BYTES, int N> __device__ __forceinline__ double squares(const uint4 (&v)[N]) {
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    uint32_t any = 0;
+// Sum of the squares of a thread's vectors tid, tid + kGradThreads, ... of a
+// piece, in eight chains of binary32 (up to 64 squares).
+template <int BYTES> __device__ __forceinline__ float squares(const uint4* piece, int vecs) {
+    constexpr int kLoads = kPiece / 16 / kGradThreads;
+    uint64_t s[4] = {0, 0, 0, 0};
+    uint4 v[kLoads];
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
+    for (int u = 0; u < kLoads; ++u) {
+        const int i = (int)threadIdx.x + u * kGradThreads;
+        v[u] = i < vecs ? piece[i] : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
         const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        if (BYTES == 2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (BYTES == 2) {
-                s[j & 1] = __fmaf_rn(bf16_lo(w[j]), bf16_lo(w[j]), s[j & 1]);
-                s[2 + (j & 1)] = __fmaf_rn(bf16_hi(w[j]), bf16_hi(w[j]), s[2 + (j & 1)]);
-            } else {
-                s[j] = __fmaf_rn(__uint_as_float(w[j]), __uint_as_float(w[j]), s[j]);
+            for (int j = 0; j < 4; ++j) {
+                const uint64_t x = f2_pack(bf16_lo(w[j]), bf16_hi(w[j]));
+                s[j] = f2_fma(x, x, s[j]);
             }
-            any |= w[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint64_t x = f2_pack(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+                s[(u & 1) * 2 + j] = f2_fma(x, x, s[(u & 1) * 2 + j]);
+            }
         }
     }
-    const float total = (s[0] + s[1]) + (s[2] + s[3]);
-    if (total >= 0x1p-80f && total <= 0x1p100f) return (double)total;
-    if (total == 0.0f && (any & (BYTES == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu)) == 0) return 0.0;
+    float a, b;
+    f2_unpack(f2_add(f2_add(s[0], s[1]), f2_add(s[2], s[3])), a, b);
+    return a + b;
+}
+
+// The same in binary64: squares whose sum left the range in which binary32
+// keeps them all.  Nothing but zeros needs no binary64.
+template <int BYTES> __device__ __noinline__ double exact_squares(const uint4* piece, int vecs) {
     double d = 0.0;
-#pragma unroll 1
-    for (int u = 0; u < N; ++u) {
-        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-        for (int j = 0; j < 4; ++j) {
-            if (BYTES == 2) {
-                const double a = (double)bf16_lo(w[j]), b = (double)bf16_hi(w[j]);
-                d += a * a + b * b;
-            } else {
-                const double a = (double)__uint_as_float(w[j]);
-                d += a * a;
-            }
+    uint32_t any = 0;
+    for (int i = (int)threadIdx.x; i < vecs; i += kGradThreads) any |= piece[i].x | piece[i].y | piece[i].z | piece[i].w;
+    if ((any & (BYTES == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu)) == 0) return 0.0;
+    for (int i = (int)threadIdx.x; i < vecs; i += kGradThreads)
+        for (int j = 0; j < 16 / BYTES; ++j) {
+            const double x = (double)load_grad<BYTES>(piece + i, j);
+            d += x * x;
         }
-    }
     return d;
 }
 
-template <int BYTES> __device__ __forceinline__ double chunk_squares(const void* p, int64_t n, int64_t index, int64_t size) {
-    constexpr int per = 16 / BYTES, U = 8;
-    const int tid = (int)threadIdx.x;
-    const Chunk c = cut_chunk<BYTES>(p, n, index, size);
-    double sum = 0.0;
-    if (c.lo + tid < c.body) {
-        const double x = (double)load_grad<BYTES>(p, c.lo + tid);
-        sum += x * x;
-    }
-    const int64_t tail = c.body + c.vecs * per + tid;
-    if (tail < c.hi) {
-        const double x = (double)load_grad<BYTES>(p, tail);
-        sum += x * x;
-    }
-    const unsigned char* body = static_cast<const unsigned char*>(p) + c.body * BYTES;
-    for (int64_t b = 0; b < c.vecs; b += (int64_t)kGradThreads * U) {
-        uint4 v[U];
+__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t i = b + u * kGradThreads + tid;
-            v[u] = i < c.vecs ? ld_stream(body + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// A warp's sum of its vectors' squares, in lane 0: over the lanes in binary32
+// where all their sums are within range.
+template <int BYTES> __device__ __forceinline__ double piece_squares(const uint4* piece, int vecs) {
+    float v = squares<BYTES>(piece, vecs);
+    if (__all_sync(0xFFFFFFFFu, v == 0.0f || (v >= 0x1p-80f && v <= 0x1p100f))) {
+        // a sum of 0 may be one of squares that vanished: then nothing larger than 2^-74 is among them, which counts
+        // only where the whole warp has no more
+        if (__any_sync(0xFFFFFFFFu, v != 0.0f)) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            return (double)v;
         }
-        sum += squares<BYTES>(v);
     }
-    return sum;
+    return warp_sum(exact_squares<BYTES>(piece, vecs));
 }
 
 // Sum of a value over the block, in thread 0.
@@ -146,18 +139,133 @@ template <int NT> __device__ __forceinline__ double block_sum(double v, double* 
     return v;
 }
 
-__global__ void __launch_bounds__(kGradThreads) grad_squares_kernel(const __grid_constant__ GradTable t, int64_t size,
-                                                                    double* partial) {
-    __shared__ double sh[kGradThreads / 32];
-    const int i = tensor_of(t, blockIdx.x);
-    const int64_t n = (int64_t)(t.kind[i] & kCountMask);
-    const int64_t index = blockIdx.x - t.first[i];
+// What the copying warp tells the summing ones about a stage.
+struct Piece {
+    const void* tensor;         // for the elements outside the vectors
+    int64_t tail;               // where those behind them start
+    int head, tails;            // how many there are in front and behind, in this piece's care
+    int vecs;                   // -1: no more pieces
+    int f32, last;              // last piece of its chunk
+};
+
+// One block per SM walks over the chunks.  A warp of its own copies them, 32 KB
+// at a time, into a ring of stages; eight warps sum.  A warp's sum of a chunk
+// waits in the chunk's last stage, where the copying warp joins the eight when
+// it takes the stage back.
+template <int N>
+__global__ void __launch_bounds__(kGradThreads + 32, 1) grad_squares_kernel(const __grid_constant__ GradTableN<N> t, uint32_t chunks,
+                                                                            int64_t chunk_bytes, double* partial) {
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ Piece info[kStages];
+    __shared__ double sums[kStages][kGradThreads / 32];
+    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kGradThreads / 32);
+        }
+        fence_barrier_init();
+    }
+    __syncthreads();
     dependency_wait();
     allow_dependents();
-    const double mine = (t.kind[i] & kGradF32) ? chunk_squares<4>(t.grad[i], n, index, size)
-                                               : chunk_squares<2>(t.grad[i], n, index, size);
-    const double sum = block_sum<kGradThreads>(mine, sh);
-    if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+    if (warp == kGradThreads / 32) {
+        if (lane != 0) return;
+        int64_t chunk_of[kStages];                      // chunk that a stage ends, or -1
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) chunk_of[s] = -1;
+        uint32_t round = 0;                             // of the ring
+        int s = 0;
+        // Takes a stage back from the summing warps and stores the sum of the chunk that it ended.
+        auto take = [&]() -> bool {
+            if (round == 0) return true;
+            if (!mbar_wait(&empty[s], (round - 1) & 1)) {
+                raise_error(kErrCopyTimeout);
+                return false;
+            }
+            int64_t done = -1;
+#pragma unroll
+            for (int i = 0; i < kStages; ++i)
+                if (i == s) done = chunk_of[i];
+            if (done >= 0) {
+                double v = 0.0;
+                for (int w = 0; w < kGradThreads / 32; ++w) v += sums[s][w];
+                partial[done] = v;
+            }
+            return true;
+        };
+        auto next = [&](int64_t ends) {
+#pragma unroll
+            for (int i = 0; i < kStages; ++i)
+                if (i == s) chunk_of[i] = ends;
+            if (++s == kStages) s = 0, ++round;
+        };
+        for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+            const int i = tensor_of(t, c);
+            const int f32 = (t.kind[i] & kGradF32) != 0, shift = f32 ? 2 : 1, per = 16 >> shift;
+            const int64_t n = (int64_t)(t.kind[i] & kCountMask), index = c - t.first[i];
+            const unsigned char* p = static_cast<const unsigned char*>(t.grad[i]);
+            const int64_t to = (int64_t)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) >> shift;
+            const int64_t head = to < n ? to : n, vecs = (n - head) / per, mine = index * (chunk_bytes / 16);
+            int64_t left = vecs - mine < chunk_bytes / 16 ? vecs - mine : chunk_bytes / 16;
+            if (left < 0) left = 0;                     // a last chunk of nothing but elements behind the vectors
+            const bool ends_tensor = c + 1 == t.first[i + 1];
+            const unsigned char* from = p + (head << shift) + mine * 16;
+            for (bool first = true; first || left > 0; first = false) {
+                const int v = (int)(left < kPiece / 16 ? left : kPiece / 16);
+                left -= v;
+                if (!take()) return;
+                Piece& m = info[s];
+                m.tensor = p;
+                m.head = first && index == 0 ? (int)head : 0;
+                m.tail = head + vecs * per;
+                m.tails = left == 0 && ends_tensor ? (int)(n - m.tail) : 0;
+                m.vecs = v;
+                m.f32 = f32;
+                m.last = left == 0;
+                mbar_arrive_expect_tx(&full[s], (uint32_t)v * 16);
+                if (v) bulk_g2s(ring + s * kPiece, from, (uint32_t)v * 16, &full[s]);
+                from += (int64_t)v * 16;
+                next(left == 0 ? (int64_t)c : -1);
+            }
+        }
+        if (!take()) return;
+        info[s].vecs = -1;
+        mbar_arrive_expect_tx(&full[s], 0);
+        for (int i = 1; i < kStages; ++i) {             // the stages still on their way
+            next(-1);
+            if (!take()) return;
+        }
+        return;
+    }
+    double sum = 0.0;                                   // lane 0: of the chunk so far
+    uint32_t parity = 0;
+    for (int s = 0;;) {
+        if (!mbar_wait(&full[s], parity)) {
+            if (lane == 0) raise_error(kErrCopyTimeout);
+            return;
+        }
+        const Piece m = info[s];
+        if (m.vecs < 0) return;
+        const uint4* piece = reinterpret_cast<const uint4*>(ring + s * kPiece);
+        sum += m.f32 ? piece_squares<4>(piece, m.vecs) : piece_squares<2>(piece, m.vecs);
+        if (warp == 0 && m.head + m.tails > 0) {        // up to 7 on either side, one for a lane
+            const int64_t at = lane < m.head ? lane : m.tail + (lane - m.head);
+            double d = 0.0;
+            if (lane < m.head + m.tails) d = (double)(m.f32 ? load_grad<4>(m.tensor, at) : load_grad<2>(m.tensor, at));
+            sum += warp_sum(d * d);
+        }
+        if (lane == 0) {
+            if (m.last) {
+                sums[s][warp] = sum;
+                sum = 0.0;
+            }
+            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[s])) : "memory");
+        }
+        __syncwarp();
+        if (++s == kStages) s = 0, parity ^= 1;
+    }
 }
 
 struct JoinArgs {
@@ -172,6 +280,7 @@ __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const JoinArgs 
     dependency_wait();
     allow_dependents();
     double v = 0.0;
+#pragma unroll 8
     for (uint64_t i = threadIdx.x; i < a.chunks; i += kJoinThreads) v += __ldcg(a.partial + i);
     const double sum = block_sum<kJoinThreads>(v, sh);
     if (threadIdx.x == 0) {
@@ -183,7 +292,8 @@ __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const JoinArgs 
 }
 
 // A warp joins one tensor's chunks.
-__global__ void __launch_bounds__(256) grad_each_kernel(const __grid_constant__ GradTable t, const double* partial, double scale,
+template <int N>
+__global__ void __launch_bounds__(256) grad_each_kernel(const __grid_constant__ GradTableN<N> t, const double* partial, double scale,
                                                         float* each) {
     const int lane = (int)(threadIdx.x & 31u);
     const int i = (int)(blockIdx.x * 8 + (threadIdx.x >> 5));
@@ -191,28 +301,98 @@ __global__ void __launch_bounds__(256) grad_each_kernel(const __grid_constant__ 
     allow_dependents();
     if (i >= t.count) return;
     double v = 0.0;
+#pragma unroll 8
     for (uint32_t c = t.first[i] + (uint32_t)lane; c < t.first[i + 1]; c += 32) v += __ldcg(partial + c);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     if (lane == 0) each[i] = (float)(sqrt(v) * scale);
 }
 
-template <int IN, int OUT>
-__device__ __forceinline__ void scale_chunk(const void* p, void* q, int64_t n, int64_t index, int64_t size, float f) {
-    const int64_t lo = index * size, hi = lo + size < n ? lo + size : n;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kGradThreads) {
-        const float x = load_grad<IN>(p, i) * f;
-        if (OUT == 2) static_cast<uint16_t*>(q)[i] = (uint16_t)pack_bf16x2(x, 0.0f);
-        else static_cast<float*>(q)[i] = x;
+template <int BYTES> __device__ __forceinline__ void store_grad(void* q, int64_t i, float x) {
+    if (BYTES == 2) static_cast<uint16_t*>(q)[i] = (uint16_t)pack_bf16x2(x, 0.0f);
+    else static_cast<float*>(q)[i] = x;
+}
+
+// Eight elements, in and out on 16-byte boundaries.
+template <int BYTES> __device__ __forceinline__ void load8(const unsigned char* p, float (&f)[8]) {
+    if (BYTES == 2) {
+        unpack8(ld_once(p), f);
+    } else {
+        const uint4 a = ld_once(p), b = ld_once(p + 16);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
+    }
+}
+template <int BYTES> __device__ __forceinline__ void store8(unsigned char* q, const float (&f)[8]) {
+    if (BYTES == 2) {
+        st_stream(q, make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+    } else {
+        st_stream(q, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+        st_stream(q + 16, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
     }
 }
 
-__global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const __grid_constant__ GradTable t, int64_t size, float scale,
-                                                                  const float* norm) {
-    const uint32_t chunk = gridDim.x - 1 - blockIdx.x;
+// One by one, sixteen on their way: where the input and the output lie
+// differently relative to 16-byte boundaries.
+template <int IN, int OUT>
+__device__ __forceinline__ void scale_each(const void* p, void* q, int64_t lo, int64_t hi, float f) {
+    constexpr int U = 16;
+    for (int64_t b = lo + threadIdx.x; b < hi; b += U * kGradThreads) {
+        float x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = b + u * kGradThreads < hi ? load_grad<IN>(p, b + u * kGradThreads) : 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (b + u * kGradThreads < hi) store_grad<OUT>(q, b + u * kGradThreads, x[u] * f);
+    }
+}
+
+template <int IN, int OUT>
+__device__ __forceinline__ void scale_chunk(const void* p, void* q, int64_t n, int64_t index, int64_t size, float f) {
+    const int64_t lo = index * size, hi = lo + size < n ? lo + size : n;
+    // elements to the first place where eight are whole vectors of both
+    constexpr int IV = IN == 2 ? 8 : 4, OV = OUT == 2 ? 8 : 4, V = IV > OV ? IV : OV;
+    const int in_off = (int)((reinterpret_cast<uintptr_t>(p) / IN + (uintptr_t)lo) % IV);
+    const int out_off = (int)((reinterpret_cast<uintptr_t>(q) / OUT + (uintptr_t)lo) % OV);
+    const int head = (V - (IV == V ? in_off : out_off)) % V;
+    if ((in_off + head) % IV != 0 || (out_off + head) % OV != 0 || hi - lo < head + 8) {
+        scale_each<IN, OUT>(p, q, lo, hi, f);
+        return;
+    }
+    const int tid = (int)threadIdx.x;
+    const int64_t body = lo + head;
+    const int eights = (int)((hi - body) / 8);
+    const unsigned char* pb = static_cast<const unsigned char*>(p) + body * IN;
+    unsigned char* qb = static_cast<unsigned char*>(q) + body * OUT;
+    constexpr int U = IN == 2 ? 4 : 2;
+    for (int b = tid; b < eights; b += U * kGradThreads) {
+        float x[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (b + u * kGradThreads < eights) load8<IN>(pb + (int64_t)(b + u * kGradThreads) * 8 * IN, x[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (b + u * kGradThreads >= eights) break;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[u][j] *= f;
+            store8<OUT>(qb + (int64_t)(b + u * kGradThreads) * 8 * OUT, x[u]);
+        }
+    }
+    if (tid < head) store_grad<OUT>(q, lo + tid, load_grad<IN>(p, lo + tid) * f);
+    const int64_t tail = body + (int64_t)eights * 8 + tid;
+    if (tail < hi) store_grad<OUT>(q, tail, load_grad<IN>(p, tail) * f);
+}
+
+// The chunks backwards: what the sums read last is still in the second-level cache.
+template <int N>
+__global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const __grid_constant__ GradTableN<N> t, uint32_t pieces,
+                                                                  float scale, const float* norm) {
+    // `pieces` blocks to a chunk
+    const uint32_t at = gridDim.x - 1 - blockIdx.x, chunk = at / pieces;
     const int i = tensor_of(t, chunk);
     const int64_t n = (int64_t)(t.kind[i] & kCountMask);
-    const int64_t index = chunk - t.first[i];
+    const int64_t index = (int64_t)(chunk - t.first[i]) * pieces + at % pieces;
     dependency_wait();
     allow_dependents();
     const float f = scale * __ldcg(norm + 1);
@@ -220,6 +400,8 @@ __global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const __grid_c
     void* q = t.out[i];
     const bool in4 = (t.kind[i] & kGradF32) != 0, out4 = (t.kind[i] & kOutF32) != 0;
     if (p == q && f == 1.0f) return;                        // in place and unchanged
+    const int64_t size = kPiece / (in4 ? 4 : 2);
+    if (index * size >= n) return;
     if (in4) {
         if (out4) scale_chunk<4, 4>(p, q, n, index, size, f);
         else scale_chunk<4, 2>(p, q, n, index, size, f);
@@ -228,6 +410,8 @@ __global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const __grid_c
         else scale_chunk<2, 2>(p, q, n, index, size, f);
     }
 }
+
+unsigned unit_errors_grad_norm(bool clear) { return read_unit_errors(clear); }
 
 }  // namespace fp8q
 
@@ -241,7 +425,7 @@ constexpr uint64_t kPlanMark = 0x66703871677264ull;
 struct Plan {
     uint64_t mark;
     int count, groups;
-    int64_t size;               // elements per chunk
+    int64_t chunk_bytes;
     uint64_t chunks;
     int aliased;                // an output overlaps what it may not
     int spans;                  // behind the tables, sorted
@@ -293,6 +477,21 @@ bool meets(const Span* s, int n, const Range& r) {
     return lo > 0 && s[lo - 1].hi > a;
 }
 
+// f on the table, or on a smaller one that holds it: the launch carries it along.
+template <class F> fp8q_status_t with_table(const GradTable& t, F f) {
+    if (t.count > kGradFew) return f(t);
+    GradTableN<kGradFew> few;
+    for (int i = 0; i < t.count; ++i) {
+        few.grad[i] = t.grad[i];
+        few.out[i] = t.out[i];
+        few.kind[i] = t.kind[i];
+        few.first[i] = t.first[i];
+    }
+    few.first[t.count] = t.first[t.count];
+    few.count = t.count;
+    return f(few);
+}
+
 fp8q_status_t grad_entry(const void* plan_memory, double scale, double max_norm, float* norm, float* each, void* workspace,
                          size_t workspace_bytes, bool clip, cudaStream_t stream) {
     if (!plan_memory || !norm) return FP8Q_ERR_NULL;
@@ -313,22 +512,38 @@ fp8q_status_t grad_entry(const void* plan_memory, double scale, double max_norm,
     uint64_t base = 0;
     for (int g = 0; g < plan.groups; ++g) {
         const GradTable& t = tables(plan_memory)[g];
-        const uint32_t chunks = t.first[t.count];
-        if (chunks) st = launch(grad_squares_kernel, chunks, kGradThreads, 0, stream, t, plan.size, partial + base);
-        if (st == FP8Q_OK && each)
-            st = launch(grad_each_kernel, (unsigned)(t.count + 7) / 8, 256, 0, stream, t, (const double*)(partial + base), scale,
-                        each + (size_t)g * kGradGroup);
+        st = with_table(t, [&](const auto& tab) {
+            constexpr int N = sizeof(tab.grad) / sizeof(void*);
+            const uint32_t chunks = tab.first[tab.count];
+            fp8q_status_t s = FP8Q_OK;
+            if (chunks) {
+                static KernelCache cache;
+                int resident = 0;
+                s = prepare_kernel(cache, grad_squares_kernel<N>, kGradThreads + 32, kStages * kPiece, kStages * kPiece, &resident);
+                if (s == FP8Q_OK)
+                    s = launch(grad_squares_kernel<N>, grid_for(chunks, 1), kGradThreads + 32, kStages * kPiece, stream, tab, chunks,
+                               plan.chunk_bytes, partial + base);
+            }
+            if (s == FP8Q_OK && each)
+                s = launch(grad_each_kernel<N>, (unsigned)(tab.count + 7) / 8, 256, 0, stream, tab, (const double*)(partial + base),
+                           scale, each + (size_t)g * kGradGroup);
+            return s;
+        });
         if (st != FP8Q_OK) return st;
-        base += chunks;
+        base += t.first[t.count];
     }
     const JoinArgs a = {partial, plan.chunks, scale, max_norm, norm};
     st = launch(grad_join_kernel, 1, kJoinThreads, 0, stream, a);
-    for (int g = plan.groups - 1; clip && st == FP8Q_OK && g >= 0; --g) {
-        const GradTable& t = tables(plan_memory)[g];
-        if (t.first[t.count])
-            st = launch(grad_scale_kernel, t.first[t.count], kGradThreads, 0, stream, t, plan.size, (float)scale,
-                        (const float*)norm);
-    }
+    for (int g = plan.groups - 1; clip && st == FP8Q_OK && g >= 0; --g)
+        st = with_table(tables(plan_memory)[g], [&](const auto& tab) {
+            constexpr int N = sizeof(tab.grad) / sizeof(void*);
+            const uint32_t chunks = tab.first[tab.count];
+            const uint32_t pieces = (uint32_t)(plan.chunk_bytes / kPiece);
+            if (chunks == 0) return FP8Q_OK;
+            if ((uint64_t)chunks * pieces > 0x7FFFFFFFull) return FP8Q_ERR_SIZE;
+            return launch(grad_scale_kernel<N>, chunks * pieces, kGradThreads, 0, stream, tab, pieces, (float)scale,
+                          (const float*)norm);
+        });
     return st;
 }
 
@@ -346,12 +561,12 @@ extern "C" fp8q_status_t fp8q_grad_plan(const fp8q_grad_t* grads, int count, voi
     if (bytes < plan_bytes(count)) return FP8Q_ERR_SIZE;
     Plan& plan = *static_cast<Plan*>(plan_memory);
     plan = {};
-    uint64_t total = 0;                                     // at most 2^14 * 2^42
+    uint64_t total = 0;                                     // bytes, at most 2^14 * 2^44
     for (int i = 0; i < count; ++i) {
         const fp8q_grad_t& g = grads[i];
         if (!valid_type(g.grad_type) || (g.out && !valid_type(g.out_type))) return FP8Q_ERR_FORMAT;
         if (g.n > FP8Q_MAX_ELEMENTS) return FP8Q_ERR_SIZE;
-        total += g.n;
+        total += g.n * type_bytes(g.grad_type);
         if (g.n == 0) continue;
         if (!g.grad) return FP8Q_ERR_NULL;
         if (reinterpret_cast<uintptr_t>(g.grad) % type_bytes(g.grad_type)) return FP8Q_ERR_ALIGN;
@@ -359,8 +574,8 @@ extern "C" fp8q_status_t fp8q_grad_plan(const fp8q_grad_t* grads, int count, voi
     }
     plan.count = count;
     plan.groups = groups_of(count);
-    plan.size = kGradChunk;
-    while (total / (uint64_t)plan.size > kGradMaxChunks) plan.size *= 2;
+    plan.chunk_bytes = kPiece;
+    while (total / (uint64_t)plan.chunk_bytes > kGradMaxChunks) plan.chunk_bytes *= 2;
     GradTable* tab = tables(plan_memory);
     Span* spans = reinterpret_cast<Span*>(tab + plan.groups);
     int n = 0;
@@ -377,7 +592,7 @@ extern "C" fp8q_status_t fp8q_grad_plan(const fp8q_grad_t* grads, int count, voi
             t.out[k] = s.out ? s.out : const_cast<void*>(s.grad);
             t.kind[k] = s.n | (s.grad_type == FP8Q_F32 ? kGradF32 : 0) | (out_type == FP8Q_F32 ? kOutF32 : 0);
             t.first[k] = chunks;
-            chunks += (uint32_t)((s.n + (uint64_t)plan.size - 1) / (uint64_t)plan.size);
+            chunks += (uint32_t)((s.n * type_bytes(s.grad_type) + (uint64_t)plan.chunk_bytes - 1) / (uint64_t)plan.chunk_bytes);
             if (s.n == 0) continue;
             spans[n++] = {out, out + s.n * type_bytes(out_type), 1};
             if (in != out || s.grad_type != out_type) spans[n++] = {in, in + s.n * type_bytes(s.grad_type), 0};
