@@ -19,6 +19,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace fp8q {
 
@@ -28,10 +29,11 @@ constexpr int kGradThreads = 256;
 constexpr int kPiece = 32768;               // bytes of one copy
 constexpr int kStages = 5;
 constexpr uint64_t kGradMaxChunks = 4096;   // chunks grow from one piece so that there are not many more than this
-constexpr int kJoinThreads = 1024;
+constexpr int kJoinThreads = 256;
 
 // Element types and count share a word: count in the low 44 bits.
 template <int N> struct GradTableN {
+    static constexpr int kSize = N;
     const void* grad[N];
     void* out[N];
     uint64_t kind[N];
@@ -126,17 +128,31 @@ template <int BYTES> __device__ __forceinline__ double piece_squares(const uint4
     return warp_sum(exact_squares<BYTES>(piece, vecs));
 }
 
-// Sum of a value over the block, in thread 0.
-template <int NT> __device__ __forceinline__ double block_sum(double v, double* sh) {
-    const int lane = (int)(threadIdx.x & 31u), warp = (int)(threadIdx.x >> 5);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if (lane == 0) sh[warp] = v;
-    __syncthreads();
-    v = 0.0;
-    if (threadIdx.x == 0)
-        for (int w = 0; w < NT / 32; ++w) v += sh[w];
-    return v;
+// Where a chunk lies: `vecs` whole vectors from `from` on, element `first` of
+// its tensor; `head` elements in front of the tensor's vectors and `tails`
+// behind them are in the care of its first and its last chunk.
+struct Place {
+    const unsigned char* from;
+    int64_t first, vecs;
+    int tensor, f32, head, tails;
+};
+template <int N> __device__ __forceinline__ Place locate(const GradTableN<N>& t, uint32_t chunk, int64_t chunk_bytes) {
+    Place r;
+    const int i = tensor_of(t, chunk);
+    r.tensor = i;
+    r.f32 = (t.kind[i] & kGradF32) != 0;
+    const int shift = r.f32 ? 2 : 1, per = 16 >> shift;
+    const int64_t n = (int64_t)(t.kind[i] & kCountMask), index = chunk - t.first[i], most = chunk_bytes / 16;
+    const unsigned char* p = static_cast<const unsigned char*>(t.grad[i]);
+    const int64_t to = (int64_t)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) >> shift;
+    const int64_t head = to < n ? to : n, all = (n - head) / per;
+    r.vecs = all - index * most < most ? all - index * most : most;
+    if (r.vecs < 0) r.vecs = 0;                         // a last chunk of nothing but elements behind the vectors
+    r.first = head + index * most * per;
+    r.from = p + (r.first << shift);
+    r.head = index == 0 ? (int)head : 0;
+    r.tails = chunk + 1 == t.first[i + 1] ? (int)(n - head - all * per) : 0;
+    return r;
 }
 
 // What the copying warp tells the summing ones about a stage.
@@ -202,27 +218,20 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_squares_kernel(cons
             if (++s == kStages) s = 0, ++round;
         };
         for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-            const int i = tensor_of(t, c);
-            const int f32 = (t.kind[i] & kGradF32) != 0, shift = f32 ? 2 : 1, per = 16 >> shift;
-            const int64_t n = (int64_t)(t.kind[i] & kCountMask), index = c - t.first[i];
-            const unsigned char* p = static_cast<const unsigned char*>(t.grad[i]);
-            const int64_t to = (int64_t)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) >> shift;
-            const int64_t head = to < n ? to : n, vecs = (n - head) / per, mine = index * (chunk_bytes / 16);
-            int64_t left = vecs - mine < chunk_bytes / 16 ? vecs - mine : chunk_bytes / 16;
-            if (left < 0) left = 0;                     // a last chunk of nothing but elements behind the vectors
-            const bool ends_tensor = c + 1 == t.first[i + 1];
-            const unsigned char* from = p + (head << shift) + mine * 16;
+            const Place at = locate(t, c, chunk_bytes);
+            int64_t left = at.vecs;
+            const unsigned char* from = at.from;
             for (bool first = true; first || left > 0; first = false) {
                 const int v = (int)(left < kPiece / 16 ? left : kPiece / 16);
                 left -= v;
                 if (!take()) return;
                 Piece& m = info[s];
-                m.tensor = p;
-                m.head = first && index == 0 ? (int)head : 0;
-                m.tail = head + vecs * per;
-                m.tails = left == 0 && ends_tensor ? (int)(n - m.tail) : 0;
+                m.tensor = t.grad[at.tensor];
+                m.head = first ? at.head : 0;
+                m.tails = left == 0 ? at.tails : 0;
+                m.tail = (int64_t)(t.kind[at.tensor] & kCountMask) - at.tails;
                 m.vecs = v;
-                m.f32 = f32;
+                m.f32 = at.f32;
                 m.last = left == 0;
                 mbar_arrive_expect_tx(&full[s], (uint32_t)v * 16);
                 if (v) bulk_g2s(ring + s * kPiece, from, (uint32_t)v * 16, &full[s]);
@@ -272,18 +281,37 @@ struct JoinArgs {
     const double* partial;      // all chunks
     uint64_t chunks;
     double scale, max_norm;
-    float* norm;                // [2]
+    float* norm;                // [2], or NULL: another launch joins them
+    const double* group;        // this group's chunks
+    float* each;                // of this group, or NULL
 };
 
-__global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const JoinArgs a) {
+// The first block joins all chunks, a warp of the others one tensor's.
+template <int N> __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const __grid_constant__ GradTableN<N> t, const JoinArgs a) {
     __shared__ double sh[kJoinThreads / 32];
+    const int lane = (int)(threadIdx.x & 31u), warp = (int)(threadIdx.x >> 5);
     dependency_wait();
     allow_dependents();
-    double v = 0.0;
+    if (blockIdx.x > 0) {
+        const int i = (int)(blockIdx.x - 1) * (kJoinThreads / 32) + warp;
+        if (i >= t.count) return;
+        double v = 0.0;
 #pragma unroll 8
+        for (uint32_t c = t.first[i] + (uint32_t)lane; c < t.first[i + 1]; c += 32) v += __ldcg(a.group + c);
+        v = warp_sum(v);
+        if (lane == 0) a.each[i] = (float)(sqrt(v) * a.scale);
+        return;
+    }
+    if (!a.norm) return;
+    double v = 0.0;
+#pragma unroll 16
     for (uint64_t i = threadIdx.x; i < a.chunks; i += kJoinThreads) v += __ldcg(a.partial + i);
-    const double sum = block_sum<kJoinThreads>(v, sh);
+    v = warp_sum(v);
+    if (lane == 0) sh[warp] = v;
+    __syncthreads();
     if (threadIdx.x == 0) {
+        double sum = 0.0;
+        for (int w = 0; w < kJoinThreads / 32; ++w) sum += sh[w];
         const double norm = sqrt(sum) * a.scale;
         const double ratio = a.max_norm / (norm + 1e-6);
         a.norm[0] = (float)norm;
@@ -291,123 +319,145 @@ __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const JoinArgs 
     }
 }
 
-// A warp joins one tensor's chunks.
-template <int N>
-__global__ void __launch_bounds__(256) grad_each_kernel(const __grid_constant__ GradTableN<N> t, const double* partial, double scale,
-                                                        float* each) {
-    const int lane = (int)(threadIdx.x & 31u);
-    const int i = (int)(blockIdx.x * 8 + (threadIdx.x >> 5));
-    dependency_wait();
-    allow_dependents();
-    if (i >= t.count) return;
-    double v = 0.0;
-#pragma unroll 8
-    for (uint32_t c = t.first[i] + (uint32_t)lane; c < t.first[i + 1]; c += 32) v += __ldcg(partial + c);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if (lane == 0) each[i] = (float)(sqrt(v) * scale);
-}
-
 template <int BYTES> __device__ __forceinline__ void store_grad(void* q, int64_t i, float x) {
     if (BYTES == 2) static_cast<uint16_t*>(q)[i] = (uint16_t)pack_bf16x2(x, 0.0f);
     else static_cast<float*>(q)[i] = x;
 }
 
-// Eight elements, in and out on 16-byte boundaries.
-template <int BYTES> __device__ __forceinline__ void load8(const unsigned char* p, float (&f)[8]) {
-    if (BYTES == 2) {
-        unpack8(ld_once(p), f);
-    } else {
-        const uint4 a = ld_once(p), b = ld_once(p + 16);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
-    }
-}
-template <int BYTES> __device__ __forceinline__ void store8(unsigned char* q, const float (&f)[8]) {
-    if (BYTES == 2) {
-        st_stream(q, make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
-    } else {
-        st_stream(q, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
-        st_stream(q + 16, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
-    }
-}
+// What the copying warp tells the scaling ones about a stage.
+struct ScalePiece {
+    const void* grad;           // for the elements outside the vectors
+    void* out;
+    int64_t first, tail;        // the first element of the vectors, and of those behind them
+    int head, tails;
+    int vecs;                   // -1: no more pieces
+    int kind;                   // 2 * f32 of the input + f32 of the output
+};
 
-// One by one, sixteen on their way: where the input and the output lie
-// differently relative to 16-byte boundaries.
-template <int IN, int OUT>
-__device__ __forceinline__ void scale_each(const void* p, void* q, int64_t lo, int64_t hi, float f) {
-    constexpr int U = 16;
-    for (int64_t b = lo + threadIdx.x; b < hi; b += U * kGradThreads) {
-        float x[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = b + u * kGradThreads < hi ? load_grad<IN>(p, b + u * kGradThreads) : 0.0f;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (b + u * kGradThreads < hi) store_grad<OUT>(q, b + u * kGradThreads, x[u] * f);
-    }
-}
-
-template <int IN, int OUT>
-__device__ __forceinline__ void scale_chunk(const void* p, void* q, int64_t n, int64_t index, int64_t size, float f) {
-    const int64_t lo = index * size, hi = lo + size < n ? lo + size : n;
-    // elements to the first place where eight are whole vectors of both
-    constexpr int IV = IN == 2 ? 8 : 4, OV = OUT == 2 ? 8 : 4, V = IV > OV ? IV : OV;
-    const int in_off = (int)((reinterpret_cast<uintptr_t>(p) / IN + (uintptr_t)lo) % IV);
-    const int out_off = (int)((reinterpret_cast<uintptr_t>(q) / OUT + (uintptr_t)lo) % OV);
-    const int head = (V - (IV == V ? in_off : out_off)) % V;
-    if ((in_off + head) % IV != 0 || (out_off + head) % OV != 0 || hi - lo < head + 8) {
-        scale_each<IN, OUT>(p, q, lo, hi, f);
-        return;
-    }
+// `count` elements from shared memory, times f, to out: whole vectors of the
+// output, single elements on either side of them.
+template <int IN, int OUT> __device__ __forceinline__ void scale_piece(const unsigned char* in, void* out, int64_t first, int count, float f) {
+    constexpr int OV = 16 / OUT;
     const int tid = (int)threadIdx.x;
-    const int64_t body = lo + head;
-    const int eights = (int)((hi - body) / 8);
-    const unsigned char* pb = static_cast<const unsigned char*>(p) + body * IN;
-    unsigned char* qb = static_cast<unsigned char*>(q) + body * OUT;
-    constexpr int U = IN == 2 ? 4 : 2;
-    for (int b = tid; b < eights; b += U * kGradThreads) {
-        float x[U][8];
+    unsigned char* q = static_cast<unsigned char*>(out) + first * OUT;
+    int head = (int)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(q) & 15u)) & 15u) / OUT;
+    if (head > count) head = count;
+    const int vecs = (count - head) / OV, tail = head + vecs * OV;
+    const unsigned char* body = in + head * IN;
+    const bool whole = (head * IN) % (OV * IN < 16 ? OV * IN : 16) == 0;    // the elements of a vector lie in vectors of the input
+#pragma unroll 4
+    for (int i = tid; i < vecs; i += kGradThreads) {
+        float x[OV];
+        const unsigned char* p = body + i * (OV * IN);
+        if (whole) {
+            if constexpr (OV * IN == 8) {
+                const uint2 v = *reinterpret_cast<const uint2*>(p);
+                x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
+            } else if constexpr (IN == 2) {
+                unpack8(*reinterpret_cast<const uint4*>(p), x);
+            } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (b + u * kGradThreads < eights) load8<IN>(pb + (int64_t)(b + u * kGradThreads) * 8 * IN, x[u]);
+                for (int j = 0; j < OV; j += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(p + j * 4);
+                    x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+                }
+            }
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (b + u * kGradThreads >= eights) break;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[u][j] *= f;
-            store8<OUT>(qb + (int64_t)(b + u * kGradThreads) * 8 * OUT, x[u]);
+            for (int j = 0; j < OV; ++j) x[j] = load_grad<IN>(p, j);
         }
+#pragma unroll
+        for (int j = 0; j < OV; ++j) x[j] *= f;
+        uint4 v;
+        if constexpr (OUT == 2)
+            v = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        else
+            v = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        st_stream(q + (int64_t)(head + i * OV) * OUT, v);
     }
-    if (tid < head) store_grad<OUT>(q, lo + tid, load_grad<IN>(p, lo + tid) * f);
-    const int64_t tail = body + (int64_t)eights * 8 + tid;
-    if (tail < hi) store_grad<OUT>(q, tail, load_grad<IN>(p, tail) * f);
+    if (tid < head) store_grad<OUT>(q, tid, load_grad<IN>(in, tid) * f);
+    if (tid < count - tail) store_grad<OUT>(q, tail + tid, load_grad<IN>(in, tail + tid) * f);
+}
+template <int IN, int OUT> __device__ __forceinline__ void scale_stage(const unsigned char* stage, const ScalePiece& m, float f) {
+    scale_piece<IN, OUT>(stage, m.out, m.first, m.vecs * (16 / IN), f);
+    const int lane = (int)threadIdx.x;                  // up to 7 elements on either side of the vectors
+    if (lane < m.head + m.tails) {
+        const int64_t at = lane < m.head ? lane : m.tail + (lane - m.head);
+        store_grad<OUT>(m.out, at, load_grad<IN>(m.grad, at) * f);
+    }
 }
 
-// The chunks backwards: what the sums read last is still in the second-level cache.
+// As the sums: one block per SM, a copying warp and eight that scale.  The
+// chunks backwards: what the sums read last is still in the second-level cache.
+// Reading through shared memory lets the output have its own alignment.
 template <int N>
-__global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const __grid_constant__ GradTableN<N> t, uint32_t pieces,
-                                                                  float scale, const float* norm) {
-    // `pieces` blocks to a chunk
-    const uint32_t at = gridDim.x - 1 - blockIdx.x, chunk = at / pieces;
-    const int i = tensor_of(t, chunk);
-    const int64_t n = (int64_t)(t.kind[i] & kCountMask);
-    const int64_t index = (int64_t)(chunk - t.first[i]) * pieces + at % pieces;
+__global__ void __launch_bounds__(kGradThreads + 32, 1) grad_scale_kernel(const __grid_constant__ GradTableN<N> t, uint32_t chunks,
+                                                                          int64_t chunk_bytes, float scale, const float* norm) {
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ ScalePiece info[kStages];
+    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kGradThreads / 32);
+        }
+        fence_barrier_init();
+    }
+    __syncthreads();
     dependency_wait();
     allow_dependents();
     const float f = scale * __ldcg(norm + 1);
-    const void* p = t.grad[i];
-    void* q = t.out[i];
-    const bool in4 = (t.kind[i] & kGradF32) != 0, out4 = (t.kind[i] & kOutF32) != 0;
-    if (p == q && f == 1.0f) return;                        // in place and unchanged
-    const int64_t size = kPiece / (in4 ? 4 : 2);
-    if (index * size >= n) return;
-    if (in4) {
-        if (out4) scale_chunk<4, 4>(p, q, n, index, size, f);
-        else scale_chunk<4, 2>(p, q, n, index, size, f);
-    } else {
-        if (out4) scale_chunk<2, 4>(p, q, n, index, size, f);
-        else scale_chunk<2, 2>(p, q, n, index, size, f);
+    if (warp == kGradThreads / 32) {
+        if (lane != 0) return;
+        uint32_t round = 0;                             // of the ring
+        int s = 0;
+        auto take = [&]() -> bool {
+            if (round == 0 || mbar_wait(&empty[s], (round - 1) & 1)) return true;
+            raise_error(kErrCopyTimeout);
+            return false;
+        };
+        for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+            const Place at = locate(t, chunks - 1 - c, chunk_bytes);
+            void* out = t.out[at.tensor];
+            const int out32 = (t.kind[at.tensor] & kOutF32) != 0;
+            if (f == 1.0f && out == t.grad[at.tensor]) continue;            // in place and unchanged
+            int64_t left = at.vecs, element = at.first;
+            const unsigned char* from = at.from;
+            for (bool first = true; first || left > 0; first = false) {
+                const int v = (int)(left < kPiece / 16 ? left : kPiece / 16);
+                left -= v;
+                if (!take()) return;
+                info[s] = {t.grad[at.tensor], out, element, (int64_t)(t.kind[at.tensor] & kCountMask) - at.tails,
+                           first ? at.head : 0, left == 0 ? at.tails : 0, v, 2 * at.f32 + out32};
+                mbar_arrive_expect_tx(&full[s], (uint32_t)v * 16);
+                if (v) bulk_g2s(ring + s * kPiece, from, (uint32_t)v * 16, &full[s]);
+                from += (int64_t)v * 16;
+                element += (int64_t)v * (at.f32 ? 4 : 8);
+                if (++s == kStages) s = 0, ++round;
+            }
+        }
+        if (!take()) return;
+        info[s].vecs = -1;
+        mbar_arrive_expect_tx(&full[s], 0);
+        return;
+    }
+    uint32_t parity = 0;
+    for (int s = 0;;) {
+        if (!mbar_wait(&full[s], parity)) {
+            if (lane == 0) raise_error(kErrCopyTimeout);
+            return;
+        }
+        const ScalePiece m = info[s];
+        if (m.vecs < 0) return;
+        const unsigned char* stage = ring + s * kPiece;
+        if (m.kind == 0) scale_stage<2, 2>(stage, m, f);
+        else if (m.kind == 1) scale_stage<2, 4>(stage, m, f);
+        else if (m.kind == 2) scale_stage<4, 2>(stage, m, f);
+        else scale_stage<4, 4>(stage, m, f);
+        __syncwarp();
+        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[s])) : "memory");
+        if (++s == kStages) s = 0, parity ^= 1;
     }
 }
 
@@ -438,7 +488,7 @@ struct Span {
     int written;
 };
 
-int groups_of(int count) { return (count + kGradGroup - 1) / kGradGroup; }
+int groups_of(int count) { return count > 0 ? (count + kGradGroup - 1) / kGradGroup : 1; }
 size_t plan_bytes(int count) {
     return sizeof(Plan) + (size_t)groups_of(count) * sizeof(GradTable) + 2 * (size_t)count * sizeof(Span);
 }
@@ -477,6 +527,14 @@ bool meets(const Span* s, int n, const Range& r) {
     return lo > 0 && s[lo - 1].hi > a;
 }
 
+// One block per SM, or per chunk where there are fewer.
+template <auto KERNEL, class... Args> fp8q_status_t launch_ring(uint32_t chunks, cudaStream_t stream, const Args&... args) {
+    static KernelCache cache;
+    int resident = 0;
+    const fp8q_status_t s = prepare_kernel(cache, KERNEL, kGradThreads + 32, kStages * kPiece, kStages * kPiece, &resident);
+    return s != FP8Q_OK ? s : launch(KERNEL, grid_for(chunks, 1), kGradThreads + 32, kStages * kPiece, stream, args...);
+}
+
 // f on the table, or on a smaller one that holds it: the launch carries it along.
 template <class F> fp8q_status_t with_table(const GradTable& t, F f) {
     if (t.count > kGradFew) return f(t);
@@ -510,39 +568,34 @@ fp8q_status_t grad_entry(const void* plan_memory, double scale, double max_norm,
     double* partial = static_cast<double*>(workspace);
     fp8q_status_t st = FP8Q_OK;
     uint64_t base = 0;
-    for (int g = 0; g < plan.groups; ++g) {
-        const GradTable& t = tables(plan_memory)[g];
-        st = with_table(t, [&](const auto& tab) {
-            constexpr int N = sizeof(tab.grad) / sizeof(void*);
-            const uint32_t chunks = tab.first[tab.count];
-            fp8q_status_t s = FP8Q_OK;
-            if (chunks) {
-                static KernelCache cache;
-                int resident = 0;
-                s = prepare_kernel(cache, grad_squares_kernel<N>, kGradThreads + 32, kStages * kPiece, kStages * kPiece, &resident);
-                if (s == FP8Q_OK)
-                    s = launch(grad_squares_kernel<N>, grid_for(chunks, 1), kGradThreads + 32, kStages * kPiece, stream, tab, chunks,
-                               plan.chunk_bytes, partial + base);
-            }
-            if (s == FP8Q_OK && each)
-                s = launch(grad_each_kernel<N>, (unsigned)(tab.count + 7) / 8, 256, 0, stream, tab, (const double*)(partial + base),
-                           scale, each + (size_t)g * kGradGroup);
+    for (int g = 0; g < plan.groups && st == FP8Q_OK; ++g)
+        st = with_table(tables(plan_memory)[g], [&](const auto& t) {
+            const uint32_t chunks = t.first[t.count];
+            constexpr int N = std::decay_t<decltype(t)>::kSize;
+            const fp8q_status_t s =
+                chunks ? launch_ring<grad_squares_kernel<N>>(chunks, stream, t, chunks, plan.chunk_bytes, partial + base) : FP8Q_OK;
+            base += chunks;
             return s;
         });
-        if (st != FP8Q_OK) return st;
-        base += t.first[t.count];
+    base = 0;
+    for (int g = 0; g < plan.groups && st == FP8Q_OK; ++g) {
+        const bool last = g == plan.groups - 1;
+        if (!each && !last) continue;
+        const JoinArgs a = {partial, plan.chunks, scale, max_norm, last ? norm : nullptr, partial + base,
+                            each ? each + (size_t)g * kGradGroup : nullptr};
+        st = with_table(tables(plan_memory)[g], [&](const auto& t) {
+            const unsigned blocks = 1 + (each ? (unsigned)(t.count + kJoinThreads / 32 - 1) / (kJoinThreads / 32) : 0);
+            base += t.first[t.count];
+            return launch(grad_join_kernel<std::decay_t<decltype(t)>::kSize>, blocks, kJoinThreads, 0, stream, t, a);
+        });
     }
-    const JoinArgs a = {partial, plan.chunks, scale, max_norm, norm};
-    st = launch(grad_join_kernel, 1, kJoinThreads, 0, stream, a);
     for (int g = plan.groups - 1; clip && st == FP8Q_OK && g >= 0; --g)
-        st = with_table(tables(plan_memory)[g], [&](const auto& tab) {
-            constexpr int N = sizeof(tab.grad) / sizeof(void*);
-            const uint32_t chunks = tab.first[tab.count];
-            const uint32_t pieces = (uint32_t)(plan.chunk_bytes / kPiece);
-            if (chunks == 0) return FP8Q_OK;
-            if ((uint64_t)chunks * pieces > 0x7FFFFFFFull) return FP8Q_ERR_SIZE;
-            return launch(grad_scale_kernel<N>, chunks * pieces, kGradThreads, 0, stream, tab, pieces, (float)scale,
-                          (const float*)norm);
+        st = with_table(tables(plan_memory)[g], [&](const auto& t) {
+            const uint32_t chunks = t.first[t.count];
+            constexpr int N = std::decay_t<decltype(t)>::kSize;
+            return chunks ? launch_ring<grad_scale_kernel<N>>(chunks, stream, t, chunks, plan.chunk_bytes, (float)scale,
+                                                              (const float*)norm)
+                          : FP8Q_OK;
         });
     return st;
 }
@@ -573,7 +626,7 @@ extern "C" fp8q_status_t fp8q_grad_plan(const fp8q_grad_t* grads, int count, voi
         if (g.out && reinterpret_cast<uintptr_t>(g.out) % type_bytes(g.out_type)) return FP8Q_ERR_ALIGN;
     }
     plan.count = count;
-    plan.groups = groups_of(count);
+    plan.groups = groups_of(count);                         // without tensors an empty one
     plan.chunk_bytes = kPiece;
     while (total / (uint64_t)plan.chunk_bytes > kGradMaxChunks) plan.chunk_bytes *= 2;
     GradTable* tab = tables(plan_memory);
