@@ -178,6 +178,34 @@ def test_large_values(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [2.0 ** -20, 1e-3, 0.01, 0.1, 30.0, 2.0 ** 20])
+def test_temperatures(T, dtype):
+    """From one at which only the largest logit counts to one at which all are alike."""
+    x, t = logits(6, 9001, TYPES[dtype], seed=12)
+    x[1] *= 100
+    x[2] *= 1e5
+    x[3] *= 1e-3
+    x[4, 4000:] = -math.inf
+    t[0] = x[0].argmax()
+    check(x, t, T, 6)
+    check_gradient(x, t, T)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("size", [30.0, 300.0, 3e3, 1e5, 2e5, 1e6])
+def test_logits_far_from_zero(size, dtype):
+    """Rows whose logits lie around +size and -size, close to one another in the type's own steps."""
+    g = torch.Generator(device="cuda").manual_seed(13)
+    step = size * (2.0 ** -7 if dtype == "bf16" else 2.0 ** -20)
+    x = (size + step * torch.randint(-20, 20, (4, 7003), generator=g, device="cuda")).to(TYPES[dtype])
+    x[2:] = -x[2:]
+    t = torch.randint(0, 7003, (4,), generator=g, device="cuda")
+    check(x, t, 1.0, 5)
+    check(x, t, 0.3, 0, entropy=False)
+    check_gradient(x, t)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("order", ["equal", "rising", "falling", "steps", "zeros", "late"])
 def test_alternatives_in_orders_that_overflow_the_candidates(order, dtype):
     """Equal, rising and stepped logits bring more candidates than there is room for."""

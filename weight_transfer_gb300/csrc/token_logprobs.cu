@@ -4,13 +4,12 @@
 // For a row x of logits and z = x / T, m = max x:
 //     S = sum of exp((x_j - m) / T),   log p_j = (x_j - m) / T - log S
 //     entropy = - sum of p_j log p_j = log S - (sum of e_j (x_j - m) / T) / S
-// One pass: every thread keeps the running maximum of what it has read, the
-// sum S relative to it and the sum E of 2^t * t with t = (x - m) * log2(e) / T,
-// so that a larger maximum m' turns them into
-//     S' = S * 2^d,   E' = 2^d * (E + d * S),   d = (m - m') * log2(e) / T
+// One pass: every thread keeps a running maximum m of what it has read, the
+// sum S relative to it and the sum E of 2^t * t with t = (x - m) c, c = log2(e) /
+// T, so that a larger maximum m' turns them into
+//     S' = S * 2^d,   E' = 2^d * (E + d * S),   d = (m - m') c
 // and the same step joins threads, warps and the blocks of a cluster, in a
-// fixed order.  The difference x - m is taken before the product with
-// log2(e) / T, so that rows of the type's lowest value stay finite.
+// fixed order.
 //
 // Gradient, from the statistics that the forward pass wrote:
 //     dx_j = ([j = t] g - p_j (g + dH (log p_j + entropy))) / T
@@ -22,7 +21,7 @@
 namespace fp8q {
 
 constexpr int kLpMaxTop = FP8Q_MAX_TOP;
-constexpr int kLpCap = 2048;            // candidates held in shared memory
+constexpr int kLpCap = 128;             // candidates that a warp holds in shared memory
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpUnroll = 4;            // 16-byte vectors per thread and step
 constexpr float kLog2e = 1.44269504088896341f;
@@ -52,6 +51,17 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
@@ -105,9 +115,10 @@ __device__ __forceinline__ int64_t load_id(const void* p, int id64, int64_t i) {
     return id64 ? (int64_t)static_cast<const long long*>(p)[i] : (int64_t)static_cast<const int*>(p)[i];
 }
 
-// The running maximum, sum and weighted sum of a set of logits.
+// Sums over a set of logits relative to one of them, m: s of 2^t and e of 2^t * t
+// with t = (x - m) c; and the set's largest logit.
 struct Soft {
-    float m, s, e;
+    float m, s, e, top;
 };
 __device__ __forceinline__ void raise(Soft& a, float m, float c) {
     const float d = fmaxf((a.m - m) * c, -1000.0f);         // a.m <= m; 2^-1000 is 0
@@ -120,7 +131,130 @@ __device__ __forceinline__ Soft join(Soft a, Soft b, float c) {
     const float m = fmaxf(a.m, b.m);
     raise(a, m, c);
     raise(b, m, c);
-    return {m, a.s + b.s, a.e + b.e};
+    return {m, a.s + b.s, a.e + b.e, fmaxf(a.top, b.top)};
+}
+
+// A thread's sums.  The reference m is raised only where a logit exceeds it by
+// 40 units of t, which binary32 holds as well, so that most steps raise nothing.
+// t is taken as x * c - mc with mc = RN(m * c), one instruction for two logits;
+// settle() and take() go between that reference and m itself.  Logits below
+// m - 4000 / c count as that, whose 2^t is 0, so that no 0 * -inf arises in e.
+// All that holds for |m| c below 2^18, where bf16 still tells m from that bound;
+// otherwise (no finite logit yet, the type's extremes, a temperature near 0)
+// logits are added one by one.
+constexpr float kSlack = 40.0f;
+constexpr float kBound = 4000.0f;
+__device__ __forceinline__ bool ordinary(float m, float c) { return fabsf(m) * c < 0x1p18f; }
+
+template <int BYTES, bool ENT> struct Sums {
+    float m, mc, top;
+    bool fast;                                               // ordinary(m, c)
+    uint32_t low;                                            // m - kBound / c: in binary32, or twice in bf16
+    uint64_t s[2], e[2];
+
+    __device__ __forceinline__ void reset() {
+        m = mc = kLowest;
+        top = -INFINITY;
+        fast = false;
+        low = 0;
+        s[0] = s[1] = e[0] = e[1] = 0;
+    }
+    __device__ __forceinline__ Soft settle(float c) const {
+        float a, b, x, y;
+        f2_unpack(f2_add(s[0], s[1]), a, b);
+        f2_unpack(f2_add(e[0], e[1]), x, y);
+        Soft r = {m, a + b, x + y, top};
+        if (fast) {                                          // 2^(x c - mc) = 2^t * 2^(m c - mc)
+            const float d = __fmaf_rn(m, c, -mc), f = ex2(-d);
+            r.e = f * (r.e - d * r.s);
+            r.s *= f;
+        }
+        return r;
+    }
+    __device__ __forceinline__ void take(const Soft& v, float c) {
+        m = v.m;
+        mc = m;
+        float d = 0.0f, f = 1.0f;
+        fast = ordinary(m, c);
+        if (fast) {
+            mc = m * c;
+            d = __fmaf_rn(m, c, -mc);
+            f = ex2(d);
+            const float l = m - __fdiv_rn(kBound, c);
+            low = BYTES == 2 ? pack_bf16x2(l, l) : __float_as_uint(l);
+        }
+        s[0] = f2_pack(v.s * f, 0.0f);
+        e[0] = f2_pack(f * (v.e + d * v.s), 0.0f);
+        s[1] = e[1] = 0;
+    }
+    // Before logits of which the largest is `most` are added.
+    __device__ __forceinline__ void meet(float most, float c) {
+        top = fmaxf(top, most);
+        if ((most - m) * c > kSlack) {
+            Soft v = settle(c);
+            raise(v, most, c);
+            take(v, c);
+        }
+    }
+    __device__ __forceinline__ void add_one(float x, float c) {
+        if (x == -INFINITY) return;
+        float d = fast ? __fmaf_rn(x, c, -mc) : (x - m) * c;
+        if (ENT) d = max_nan(d, -kBound);
+        const float p = ex2(d);
+        s[0] = f2_add(s[0], f2_pack(p, 0.0f));
+        if (ENT) e[0] = f2_fma(f2_pack(p, 0.0f), f2_pack(d, 0.0f), e[0]);
+    }
+    template <int V> __device__ __forceinline__ void add(const uint4 (&v)[V], float c) {
+        if (!fast) {
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                float f[16 / BYTES];
+                Logit<BYTES>::unpack(v[u], f);
+#pragma unroll
+                for (int j = 0; j < 16 / BYTES; ++j) add_one(f[j], c);
+            }
+            return;
+        }
+        const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-mc, -mc);
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int j = 0; j < 4; j += BYTES / 2) {
+                uint64_t x;
+                if (BYTES == 2) {
+                    const uint32_t y = ENT ? max_nan_bf16x2(w[j], low) : w[j];
+                    x = f2_pack(bf16_lo(y), bf16_hi(y));
+                } else {
+                    const float a = __uint_as_float(w[j]), b = __uint_as_float(w[j + 1]), l = __uint_as_float(low);
+                    x = ENT ? f2_pack(max_nan(a, l), max_nan(b, l)) : f2_pack(a, b);
+                }
+                const uint64_t d = f2_fma(x, c2, mc2);
+                float d0, d1;
+                f2_unpack(d, d0, d1);
+                const uint64_t p = f2_pack(ex2(d0), ex2(d1));
+                const int k = (j / (BYTES / 2)) & 1;
+                s[k] = f2_add(s[k], p);
+                if (ENT) e[k] = f2_fma(p, d, e[k]);
+            }
+        }
+    }
+};
+
+template <int BYTES, int V> __device__ __forceinline__ float largest(const uint4 (&v)[V]) {
+    if (BYTES == 2) {
+        uint32_t m = max_bf16x2(max_bf16x2(v[0].x, v[0].y), max_bf16x2(v[0].z, v[0].w));
+#pragma unroll
+        for (int u = 1; u < V; ++u) m = max_bf16x2(m, max_bf16x2(max_bf16x2(v[u].x, v[u].y), max_bf16x2(v[u].z, v[u].w)));
+        return fmaxf(bf16_lo(m), bf16_hi(m));
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        m = fmaxf(m, fmaxf(__uint_as_float(v[u].x), __uint_as_float(v[u].y)));
+        m = fmaxf(m, fmaxf(__uint_as_float(v[u].z), __uint_as_float(v[u].w)));
+    }
+    return m;
 }
 
 // Candidates are ordered by one 64-bit key, larger logits first and among
@@ -152,66 +286,72 @@ template <int NT> struct LpShared {
     Soft warp[NT / 32];
     Soft part[kLpMaxCluster];
 };
-struct LpTopShared {
+// A warp's candidates for the alternatives.
+struct WarpTop {
     uint64_t keys[kLpCap];
-    uint64_t sorted[kLpMaxTop];
-    uint64_t gather[kLpMaxCluster * kLpMaxTop];
     uint64_t best[kLpMaxTop];
-    uint64_t threshold;
+    int count, kept;
+};
+template <int NT> struct LpTopShared {
+    WarpTop warp[NT / 32];
+    uint64_t gather[kLpMaxCluster * kLpMaxTop];
+    uint64_t sorted[kLpMaxTop];
     float group[64];
-    int count, kept, sum[3];
+    float floor;
 };
 
-// Leaves the `top` largest of keys[0 .. n) and of the elements marked in
-// `open` as keys[0 .. top), and the smallest of them as the threshold: the
-// top-th largest key is found bit by bit.  Taken where the candidates do not
-// fit, which many equal logits or rising ones bring about.  n or open > top.
+// Leaves the `top` largest of the warp's keys and of the elements marked in
+// `open` as keys[0 .. top) and returns the smallest of them: it is found bit by
+// bit.  Taken where the candidates do not fit, which many equal logits or rising
+// ones bring about, and at the end.  More than `top` there have to be.
 template <int BYTES, int NT>
-__device__ __noinline__ void narrow(LpTopShared& t, int top, int n, uint64_t open, const uint4* v, float extra, int64_t at,
-                                    int64_t extra_at) {
+__device__ __noinline__ uint64_t narrow(WarpTop& t, int top, int n, uint64_t open, const uint4* v, float extra, int64_t at,
+                                        int64_t extra_at) {
     constexpr int per = 16 / BYTES;
-    const int tid = (int)threadIdx.x;
-    if (tid == 0) { t.sum[0] = 0; t.kept = 0; }
-    __syncthreads();
+    const int lane = (int)(threadIdx.x & 31u);
+    const bool any_open = __any_sync(0xFFFFFFFFu, open != 0);
     uint64_t lo = 0;
-    for (int i = 0; i < 64; ++i) {
-        const uint64_t mid = lo | (1ull << (63 - i));
+    for (int i = 63; i >= 0; --i) {
+        const uint64_t mid = lo | (1ull << i);
         int c = 0;
-        for (int j = tid; j < n; j += NT) c += t.keys[j] >= mid;
+        for (int j = lane; j < n; j += 32) c += t.keys[j] >= mid;
+        if (any_open) {
+            for (int u = 0; u < kLpUnroll; ++u) {
+                float f[per];
+                Logit<BYTES>::unpack(v[u], f);
+#pragma unroll
+                for (int j = 0; j < per; ++j)
+                    if (open >> (u * per + j) & 1) c += key_of(f[j], at + (int64_t)u * NT * per + j) >= mid;
+            }
+            if (open >> 63) c += key_of(extra, extra_at) >= mid;
+        }
+        if (__reduce_add_sync(0xFFFFFFFFu, c) >= top) lo = mid;
+    }
+    if (lane == 0) t.kept = 0;
+    __syncwarp();
+    for (int j = lane; j < n; j += 32)
+        if (t.keys[j] >= lo) t.best[atomicAdd(&t.kept, 1)] = t.keys[j];
+    if (any_open) {
         for (int u = 0; u < kLpUnroll; ++u) {
             float f[per];
             Logit<BYTES>::unpack(v[u], f);
 #pragma unroll
-            for (int j = 0; j < per; ++j)
-                if (open >> (u * per + j) & 1) c += key_of(f[j], at + (int64_t)u * NT * per + j) >= mid;
+            for (int j = 0; j < per; ++j) {
+                const uint64_t k = key_of(f[j], at + (int64_t)u * NT * per + j);
+                if ((open >> (u * per + j) & 1) && k >= lo) t.best[atomicAdd(&t.kept, 1)] = k;
+            }
         }
-        if (open >> 63) c += key_of(extra, extra_at) >= mid;
-        c = __reduce_add_sync(0xFFFFFFFFu, c);
-        if (tid == 0) t.sum[(i + 1) % 3] = 0;
-        if ((tid & 31) == 0 && c) atomicAdd(&t.sum[i % 3], c);
-        __syncthreads();
-        if (t.sum[i % 3] >= top) lo = mid;
+        if ((open >> 63) && key_of(extra, extra_at) >= lo) t.best[atomicAdd(&t.kept, 1)] = key_of(extra, extra_at);
     }
-    for (int j = tid; j < n; j += NT)
-        if (t.keys[j] >= lo) t.best[atomicAdd(&t.kept, 1)] = t.keys[j];
-    for (int u = 0; u < kLpUnroll; ++u) {
-        float f[per];
-        Logit<BYTES>::unpack(v[u], f);
-#pragma unroll
-        for (int j = 0; j < per; ++j) {
-            const uint64_t k = key_of(f[j], at + (int64_t)u * NT * per + j);
-            if ((open >> (u * per + j) & 1) && k >= lo) t.best[atomicAdd(&t.kept, 1)] = k;
-        }
-    }
-    if ((open >> 63) && key_of(extra, extra_at) >= lo) t.best[atomicAdd(&t.kept, 1)] = key_of(extra, extra_at);
-    __syncthreads();
-    if (tid < top) t.keys[tid] = t.best[tid];
-    if (tid == 0) { t.count = top; t.threshold = lo; }
-    __syncthreads();
+    __syncwarp();
+    if (lane < top) t.keys[lane] = t.best[lane];
+    if (lane == 0) t.count = top;
+    __syncwarp();
+    return lo;
 }
 
-// The top-th largest keys of keys[0 .. n) in falling order (keys are unique;
-// n of them where there are fewer), 0 behind.
+// The `top` largest keys of keys[0 .. n) in falling order (keys are unique, but
+// for 0, which is none), 0 behind.
 template <int NT> __device__ __forceinline__ void sort_top(const uint64_t* keys, int n, int top, uint64_t* sorted) {
     const int tid = (int)threadIdx.x;
     if (tid < top) sorted[tid] = 0;
@@ -232,8 +372,9 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
     constexpr int per = L::kPerVec;
     __shared__ LpShared<NT> sh;
     extern __shared__ __align__(16) unsigned char dyn[];
-    LpTopShared& t = *reinterpret_cast<LpTopShared*>(dyn);
+    LpTopShared<NT>& t = *reinterpret_cast<LpTopShared<NT>*>(dyn);
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    WarpTop& mine = t.warp[warp];
     uint32_t ranks;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
     const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
@@ -243,10 +384,19 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
     const int64_t v0 = cut.vecs * rank / ranks, v1 = cut.vecs * (rank + 1) / ranks;
     const unsigned char* body = x + (int64_t)cut.head * BYTES;
     if (ranks > 1) cluster_arrive();
-    if (TOP && tid == 0) t.count = 0;
+    if (TOP && lane == 0) mine.count = 0;
     dependency_wait();
     allow_dependents();
 
+    auto load = [&](uint4 (&v)[kLpUnroll], int64_t base) {
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) {
+            const int64_t i = base + u * NT + tid;
+            v[u] = i < v1 ? ld_stream(body + 16 * i) : make_uint4(L::kNothing, L::kNothing, L::kNothing, L::kNothing);
+        }
+    };
+    uint4 next[kLpUnroll];
+    load(next, v0);
     // the elements outside the row's vectors, one for a thread
     float extra = -INFINITY;
     int64_t extra_at = 0;
@@ -261,47 +411,22 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
         else target_logit = L::load(x, target);
     }
 
-    Soft acc = {kLowest, 0.0f, 0.0f};
-    float floor_value = -INFINITY;                   // candidates are not below it
+    Sums<BYTES, ENT> sums;
+    sums.reset();
+    float floor_value = -INFINITY;                   // candidates are not below it,
+    uint64_t floor_key = 0;                          // nor their keys below this one
     bool first = true;
     for (int64_t base = v0; base < v1 || first; base += (int64_t)NT * kLpUnroll) {
         uint4 v[kLpUnroll];
 #pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u) {
-            const int64_t i = base + u * NT + tid;
-            v[u] = i < v1 ? ld_stream(body + 16 * i) : make_uint4(L::kNothing, L::kNothing, L::kNothing, L::kNothing);
-        }
-        float most = first ? extra : -INFINITY;
-#pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u) {
-            float f[per];
-            L::unpack(v[u], f);
-#pragma unroll
-            for (int j = 0; j < per; ++j) most = fmaxf(most, f[j]);
-        }
-        if (most > acc.m) raise(acc, most, a.c);
-#pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u) {
-            float f[per];
-            L::unpack(v[u], f);
-#pragma unroll
-            for (int j = 0; j < per; ++j) {
-                float d = (f[j] - acc.m) * a.c;
-                if (ENT) d = max_nan(d, -126.0f);    // 2^-126 stands for 0, so that 0 * -inf does not arise
-                const float p = ex2(d);
-                acc.s += p;
-                if (ENT) acc.e = __fmaf_rn(p, d, acc.e);
-            }
-        }
-        if (first) {
-            float d = (extra - acc.m) * a.c;
-            if (ENT) d = max_nan(d, -126.0f);
-            const float p = ex2(d);
-            acc.s += p;
-            if (ENT) acc.e = __fmaf_rn(p, d, acc.e);
-        }
+        for (int u = 0; u < kLpUnroll; ++u) v[u] = next[u];
+        if (base + (int64_t)NT * kLpUnroll < v1) load(next, base + (int64_t)NT * kLpUnroll);
+        float most = largest<BYTES>(v);
+        if (first) most = fmaxf(most, extra);
+        sums.meet(most, a.c);
+        sums.add(v, a.c);
+        if (first && !(extra == -INFINITY)) sums.add_one(extra, a.c);
         if (TOP) {
-            const int64_t at = cut.head + (base + tid) * per;
             if (first) {
                 // the top-th largest of 64 groups' maxima: as many elements are not below it
                 float g = most;
@@ -310,69 +435,71 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
                 if (tid % (NT / 64) == 0) t.group[tid / (NT / 64)] = g;
                 __syncthreads();
                 if (tid < 64) {
-                    const float mine = t.group[tid];
+                    const float own = t.group[tid];
                     int above = 0;
                     for (int j = 0; j < 64; ++j) {
                         const float o = t.group[j];
-                        above += o > mine || (o == mine && j < tid);
+                        above += o > own || (o == own && j < tid);
                     }
-                    if (above == a.top - 1) t.threshold = key_of(mine, 0xFFFFFFFFll);
+                    if (above == a.top - 1) t.floor = own;
                 }
                 __syncthreads();
-                floor_value = key_value(t.threshold);
+                floor_value = t.floor;
             }
-            uint64_t open = 0;                       // candidates that found no place
-            if (most >= floor_value) {
-                const uint64_t threshold = t.threshold;
-                for (int u = 0; u < kLpUnroll; ++u) {
-                    float f[per];
-                    L::unpack(v[u], f);
+            if (__any_sync(0xFFFFFFFFu, most >= floor_value && most > -INFINITY)) {
+                const int64_t at = cut.head + (base + tid) * per;
+                uint64_t open = 0;                   // candidates that found no place
+                auto offer = [&](float f, int64_t i, int bit) {
+                    if (!(f > -INFINITY && f >= floor_value)) return;
+                    const uint64_t k = key_of(f, i);
+                    if (k < floor_key) return;
+                    const int pos = atomicAdd(&mine.count, 1);
+                    if (pos < kLpCap) mine.keys[pos] = k;
+                    else open |= 1ull << bit;
+                };
+                if (most >= floor_value) {
+                    for (int u = 0; u < kLpUnroll; ++u) {
+                        float f[per];
+                        L::unpack(v[u], f);
 #pragma unroll
-                    for (int j = 0; j < per; ++j) {
-                        if (f[j] > -INFINITY && f[j] >= floor_value) {
-                            const uint64_t k = key_of(f[j], at + (int64_t)u * NT * per + j);
-                            if (k >= threshold) {
-                                const int pos = atomicAdd(&t.count, 1);
-                                if (pos < kLpCap) t.keys[pos] = k;
-                                else open |= 1ull << (u * per + j);
-                            }
-                        }
+                        for (int j = 0; j < per; ++j) offer(f[j], at + (int64_t)u * NT * per + j, u * per + j);
                     }
+                    if (first) offer(extra, extra_at, 63);
                 }
-                if (first && extra > -INFINITY && extra >= floor_value) {
-                    const uint64_t k = key_of(extra, extra_at);
-                    const int pos = atomicAdd(&t.count, 1);
-                    if (pos < kLpCap) t.keys[pos] = k;
-                    else open |= 1ull << 63;
+                __syncwarp();
+                const int n = mine.count;
+                __syncwarp();
+                if (n > kLpCap - 32) {
+                    floor_key = narrow<BYTES, NT>(mine, a.top, n < kLpCap ? n : kLpCap, open, v, extra, at, extra_at);
+                    floor_value = fmaxf(floor_value, key_value(floor_key));
                 }
-            }
-            if (__syncthreads_or(open != 0)) {
-                narrow<BYTES, NT>(t, a.top, kLpCap, open, v, extra, at, extra_at);
-                floor_value = key_value(t.threshold);
             }
         }
         first = false;
     }
 
+    Soft acc = sums.settle(a.c);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         Soft b;
         b.m = __shfl_xor_sync(0xFFFFFFFFu, acc.m, o);
         b.s = __shfl_xor_sync(0xFFFFFFFFu, acc.s, o);
         b.e = __shfl_xor_sync(0xFFFFFFFFu, acc.e, o);
+        b.top = __shfl_xor_sync(0xFFFFFFFFu, acc.top, o);
         acc = (lane & o) ? join(b, acc, a.c) : join(acc, b, a.c);
     }
     if (lane == 0) sh.warp[warp] = acc;
     if (TOP) {
-        __syncthreads();
-        int n = t.count;
-        if (n > 256) {
+        // the warps' candidates, `top` each at most, side by side
+        int n = mine.count;
+        if (n > a.top) {
             const uint4 none[kLpUnroll] = {};
-            __syncthreads();
-            narrow<BYTES, NT>(t, a.top, n, 0, none, 0.0f, 0, 0);
+            narrow<BYTES, NT>(mine, a.top, n, 0, none, 0.0f, 0, 0);
             n = a.top;
         }
-        sort_top<NT>(t.keys, n, a.top, t.sorted);
+        if (lane < a.top) t.gather[warp * a.top + lane] = lane < n ? mine.keys[lane] : 0;
+        __syncthreads();
+        sort_top<NT>(t.gather, NT / 32 * a.top, a.top, t.sorted);
     } else {
         __syncthreads();
     }
@@ -382,11 +509,13 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
     }
     if (ranks > 1) {
         cluster_wait();                              // the first block has started
+        if (TOP) cluster_sync();                     // and no longer reads what it gathered from its warps
         if (tid == 0) {
             const uint32_t to = map_rank0(&sh.part[rank]);
             st_cluster_f32(to, acc.m);
             st_cluster_f32(to + 4, acc.s);
             st_cluster_f32(to + 8, acc.e);
+            st_cluster_f32(to + 12, acc.top);
         }
         if (TOP && tid < a.top) st_cluster_u64(map_rank0(&t.gather[rank * a.top + tid]), t.sorted[tid]);
         cluster_sync();
@@ -399,7 +528,8 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
     }
     if (tid == 0) {
         // a row of -inf alone has no distribution: its scores are -inf, its entropy 0
-        const bool none = acc.m == kLowest && acc.s < 0.5f;
+        raise(acc, acc.top == -INFINITY ? acc.m : acc.top, a.c);
+        const bool none = acc.top == -INFINITY && acc.s == 0.0f;
         const float log_s = none ? 0.0f : logf(acc.s);
         const float m = none ? -INFINITY : acc.m;
         if (a.logprobs)
@@ -410,7 +540,7 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
             a.stats[2 * row + 1] = log_s;
         }
         if (TOP) {
-            sh.part[0] = {m, log_s, none ? 1.0f : 0.0f};
+            sh.part[0] = {m, log_s, none ? 1.0f : 0.0f, 0.0f};
             // fewer candidates than asked for: the first logits that are -inf (or NaN) fill the list; fewer than `top`
             // are neither, so that they lie among the first 2 * top
             int n = 0;
@@ -437,7 +567,7 @@ struct LpGradArgs {
     const void* targets;
     int id64;
     int64_t rows, vocab, stride, dstride;
-    float temperature, c;
+    float inv_t, c;             // 1 / temperature, log2(e) / temperature
     const float* stats;
     const float* dlogprobs;     // or NULL
     const float* entropy;       // with dentropy
@@ -450,6 +580,10 @@ constexpr int kLpGradThreads = 256;
 
 // A block takes one part of one row.  VEC: the rows of logits and dlogits lie
 // alike relative to 16-byte boundaries.
+//   With t = (x - m) c - log2 S:  dx = 2^t (base + slope t), plus g at the
+// target, the last taken after the others.  Logits below m - 4000 / c count as
+// that, whose 2^t is 0, so that no 0 * -inf arises; where bf16 does not tell m
+// from that bound, logits go one by one.
 template <int BYTES, bool ENT, bool VEC>
 __global__ void __launch_bounds__(kLpGradThreads) token_logprobs_backward_kernel(const LpGradArgs a) {
     using L = Logit<BYTES>;
@@ -457,44 +591,49 @@ __global__ void __launch_bounds__(kLpGradThreads) token_logprobs_backward_kernel
     constexpr int NT = kLpGradThreads;
     const int tid = (int)threadIdx.x;
     const int64_t row = blockIdx.x / a.parts;
-    const unsigned part = blockIdx.x % a.parts;
+    const unsigned part = blockIdx.x - (unsigned)row * a.parts;
     const unsigned char* x = static_cast<const unsigned char*>(a.logits) + row * a.stride * BYTES;
     unsigned char* dx = static_cast<unsigned char*>(a.dlogits) + row * a.dstride * BYTES;
+    const RowCut cut = cut_row<BYTES>(x, a.vocab);
+    const int64_t v0 = cut.vecs * part / a.parts, v1 = cut.vecs * (part + 1) / a.parts;
+    const unsigned char* body = x + (int64_t)cut.head * BYTES;
+    unsigned char* dbody = dx + (int64_t)cut.head * BYTES;
     dependency_wait();
     allow_dependents();
     int64_t target = a.targets ? load_id(a.targets, a.id64, row) : -1;
     if (target < 0 || target >= a.vocab) target = -1;
     const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
-    const bool none = m == -INFINITY;
-    const float inv_t = __fdiv_rn(1.0f, a.temperature);
-    const float g = target >= 0 && a.dlogprobs ? a.dlogprobs[row] * inv_t : 0.0f;
-    const float dh = ENT ? a.dentropy[row] * inv_t : 0.0f;
-    const float base = ENT ? -(g + dh * a.entropy[row]) : -g;       // dx_j = p_j * (base + slope * log2 p_j)
+    const float g = target >= 0 && a.dlogprobs ? a.dlogprobs[row] * a.inv_t : 0.0f;
+    const float dh = ENT ? a.dentropy[row] * a.inv_t : 0.0f;
+    const float base = ENT ? -(g + dh * a.entropy[row]) : -g;
     const float slope = ENT ? -dh * kLn2 : 0.0f;
     const float shift = -log_s * kLog2e;
-    const bool zero = none || (g == 0.0f && dh == 0.0f);            // nothing reaches this row: zeros, whatever it holds
+    const bool zero = m == -INFINITY || (g == 0.0f && dh == 0.0f);  // nothing reaches this row: zeros, whatever it holds
+    const bool fast = ordinary(m, a.c);
     auto grad = [&](float v, int64_t i) {
         if (zero) return 0.0f;
         float d = __fmaf_rn(v - m, a.c, shift);
-        if (ENT) d = max_nan(d, -200.0f);            // 2^-200 is 0 here, and 0 * -inf does not arise
+        if (ENT) d = max_nan(d, -200.0f);            // 2^-200 is 0 here
         float r = ex2(d) * (ENT ? __fmaf_rn(slope, d, base) : base);
         if (i == target) r += g;
         return r;
     };
     if (!VEC) {
         const int64_t lo = a.vocab * part / a.parts, hi = a.vocab * (part + 1) / a.parts;
+#pragma unroll 8
         for (int64_t i = lo + tid; i < hi; i += NT) L::store(dx, i, grad(L::load(x, i), i));
         return;
     }
-    const RowCut cut = cut_row<BYTES>(x, a.vocab);
     if (part == 0 && tid < cut.head) L::store(dx, tid, grad(L::load(x, tid), tid));
     if (part == a.parts - 1 && tid < cut.tail) {
         const int64_t i = cut.head + cut.vecs * per + tid;
         L::store(dx, i, grad(L::load(x, i), i));
     }
-    const int64_t v0 = cut.vecs * part / a.parts, v1 = cut.vecs * (part + 1) / a.parts;
-    const unsigned char* body = x + (int64_t)cut.head * BYTES;
-    unsigned char* dbody = dx + (int64_t)cut.head * BYTES;
+    const int64_t target_vec = target >= cut.head ? (target - cut.head) / per : -1;
+    const float lowest = m - __fdiv_rn(kBound, a.c);
+    const uint32_t low = BYTES == 2 ? pack_bf16x2(lowest, lowest) : __float_as_uint(lowest);
+    const uint64_t c2 = f2_pack(a.c, a.c), m2 = f2_pack(-m, -m), shift2 = f2_pack(shift, shift);
+    const uint64_t base2 = f2_pack(base, base), slope2 = f2_pack(slope, slope);
     for (int64_t b = v0; b < v1; b += (int64_t)NT * kLpUnroll) {
         uint4 v[kLpUnroll];
 #pragma unroll
@@ -507,9 +646,39 @@ __global__ void __launch_bounds__(kLpGradThreads) token_logprobs_backward_kernel
             const int64_t i = b + u * NT + tid;
             if (i >= v1) break;
             float f[per];
-            L::unpack(v[u], f);
+            if (zero) {
+                st_stream(dbody + 16 * i, make_uint4(0u, 0u, 0u, 0u));
+                continue;
+            }
+            if (fast) {
+                const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
-            for (int j = 0; j < per; ++j) f[j] = grad(f[j], cut.head + i * per + j);
+                for (int j = 0; j < per; j += 2) {
+                    uint64_t y;
+                    if (BYTES == 2) {
+                        const uint32_t k = ENT ? max_nan_bf16x2(w[j / 2], low) : w[j / 2];
+                        y = f2_pack(bf16_lo(k), bf16_hi(k));
+                    } else {
+                        const float p = __uint_as_float(w[j & 3]), q = __uint_as_float(w[(j + 1) & 3]), l = __uint_as_float(low);
+                        y = ENT ? f2_pack(max_nan(p, l), max_nan(q, l)) : f2_pack(p, q);
+                    }
+                    const uint64_t d = f2_fma(f2_add(y, m2), c2, shift2);
+                    float d0, d1;
+                    f2_unpack(d, d0, d1);
+                    const uint64_t p = f2_pack(ex2(d0), ex2(d1));
+                    f2_unpack(f2_mul(p, ENT ? f2_fma(slope2, d, base2) : base2), f[j], f[j + 1]);
+                }
+                if (i == target_vec) {
+                    const int at = (int)(target - cut.head - i * per);
+#pragma unroll
+                    for (int j = 0; j < per; ++j)
+                        if (j == at) f[j] += g;
+                }
+            } else {
+                L::unpack(v[u], f);
+#pragma unroll
+                for (int j = 0; j < per; ++j) f[j] = grad(f[j], cut.head + i * per + j);
+            }
             st_stream(dbody + 16 * i, L::pack(f));
         }
     }
@@ -546,13 +715,13 @@ fp8q_status_t launch_logprobs(const LpArgs& a, int64_t rows, cudaStream_t stream
     const int64_t steps = (a.vocab * BYTES + NT * kLpUnroll * 16 - 1) / (NT * kLpUnroll * 16);
     while (ranks < kLpMaxCluster && rows * ranks * 2 <= 2 * sm_count() && (int64_t)ranks * 2 <= steps) ranks *= 2;
     return launch_clusters(token_logprobs_kernel<BYTES, TOP, ENT, NT>, (unsigned)rows * ranks, ranks, NT,
-                           TOP ? sizeof(LpTopShared) : 0, stream, a);
+                           TOP ? sizeof(LpTopShared<NT>) : 0, stream, a);
 }
 
 template <int BYTES, bool TOP, bool ENT>
 fp8q_status_t launch_logprobs_size(const LpArgs& a, int64_t rows, cudaStream_t stream) {
     return a.vocab * BYTES <= 16384 ? launch_logprobs<BYTES, TOP, ENT, 128>(a, rows, stream)
-                                    : launch_logprobs<BYTES, TOP, ENT, 512>(a, rows, stream);
+                                    : launch_logprobs<BYTES, TOP, ENT, 256>(a, rows, stream);
 }
 
 template <int BYTES> fp8q_status_t launch_logprobs_kind(const LpArgs& a, int64_t rows, cudaStream_t stream) {
@@ -628,7 +797,7 @@ extern "C" fp8q_status_t fp8q_token_logprobs_backward(const void* logits, int lo
     const Range ins[] = {{in_place ? nullptr : logits, span(rows, vocab, stride, logit_bytes)}, {targets, r * id_bytes},
                          {stats, 8 * r}, {dlogprobs, 4 * r}, {entropy, 4 * r}, {dentropy, 4 * r}};
     if (any_alias(out, 1, ins, 6)) return FP8Q_ERR_ALIAS;
-    const LpGradArgs a = {logits, targets, id_bytes == 8, rows, vocab, stride, dstride, temperature,
+    const LpGradArgs a = {logits, targets, id_bytes == 8, rows, vocab, stride, dstride, (float)(1.0 / (double)temperature),
                           (float)(1.44269504088896340736 / (double)temperature), stats, dlogprobs, entropy, dentropy, dlogits, 1};
     const uintptr_t apart = reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(dlogits);
     const bool vec = apart % 16 == 0 && (rows == 1 || (uint64_t)(stride - dstride) * (unsigned)logit_bytes % 16 == 0);
