@@ -223,6 +223,26 @@ def test_alternatives_in_orders_that_overflow_the_candidates(order, dtype):
     check(many, torch.zeros(700, dtype=torch.int64, device="cuda"), 1.0, 32)
 
 
+@pytest.mark.parametrize("vocab", [151936, 1_000_003, 6_000_001])
+def test_long_rows(vocab):
+    """Rows whose steps share places of the stored maxima."""
+    x, t = logits(2, vocab, torch.bfloat16, seed=14)
+    check(x, t, 1.0, 32)
+    x[0] = 2.0
+    x[1, 7:] = x[1, :-7].sort().values
+    check(x, t, 1.0, 32)
+
+
+def test_few_allowed_tokens():
+    """Rows of which a grammar leaves a handful of tokens, in any places."""
+    x = torch.full((40, 151669), -math.inf, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(15)
+    for r in range(40):
+        at = torch.randint(0, 151669, (r,), generator=g, device="cuda")
+        x[r, at] = torch.randn(r, generator=g, device="cuda").bfloat16()
+    check(x, torch.randint(0, 151669, (40,), generator=g, device="cuda"), 1.0, 20)
+
+
 def test_infinite_and_nan_rows_leave_the_others_alone():
     x, t = logits(6, 5000, torch.float32, seed=8)
     clean = [o.clone() for o in w.fp8q_token_logprobs(x, t, top=5, want_entropy=True, want_stats=True)]

@@ -23,6 +23,8 @@ namespace fp8q {
 constexpr int kLpMaxTop = FP8Q_MAX_TOP;
 constexpr int kLpCap = 128;             // candidates that a warp holds in shared memory
 constexpr int kLpMaxCluster = 8;
+constexpr int kLpBlocksPerSm = 4;
+constexpr int kLpPlaces = 48;            // of stored maxima a thread
 constexpr int kLpUnroll = 4;            // 16-byte vectors per thread and step
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
@@ -35,6 +37,7 @@ struct LpArgs {
     int64_t vocab, stride;
     float temperature, c;       // c = log2(e) / temperature
     int top;
+    int fold;                   // steps that share a place of the stored maxima
     float* logprobs;            // each NULL when not wanted
     float* entropy;
     float* top_logprobs;
@@ -286,88 +289,97 @@ template <int NT> struct LpShared {
     Soft warp[NT / 32];
     Soft part[kLpMaxCluster];
 };
-// A warp's candidates for the alternatives.
-struct WarpTop {
+// The alternatives.  Every thread stores the largest logit of each of its steps.
+// When the row is through, the top-th largest of 64 groups' maxima is a floor:
+// as many logits are not below it, and few more.  The steps that reach the
+// floor, a few dozen, are read again, one to a thread, and what is in them and
+// not below the floor is sorted.  Where that is too much (many equal logits),
+// the warps go through their steps one by one, each keeping its best.
+constexpr int kLpGather = kLpMaxCluster * kLpMaxTop;
+struct __align__(16) WarpTop {
     uint64_t keys[kLpCap];
-    uint64_t best[kLpMaxTop];
-    int count, kept;
+    int count;
 };
 template <int NT> struct LpTopShared {
     WarpTop warp[NT / 32];
-    uint64_t gather[kLpMaxCluster * kLpMaxTop];
+    uint64_t gather[kLpGather];
     uint64_t sorted[kLpMaxTop];
     float group[64];
+    int list[kLpGather];
     float floor;
+    int listed, gathered;
+    float most[1];              // [steps / fold][NT]
 };
 
-// Leaves the `top` largest of the warp's keys and of the elements marked in
-// `open` as keys[0 .. top) and returns the smallest of them: it is found bit by
-// bit.  Taken where the candidates do not fit, which many equal logits or rising
-// ones bring about, and at the end.  More than `top` there have to be.
-template <int BYTES, int NT>
-__device__ __noinline__ uint64_t narrow(WarpTop& t, int top, int n, uint64_t open, const uint4* v, float extra, int64_t at,
-                                        int64_t extra_at) {
-    constexpr int per = 16 / BYTES;
+// Leaves the `top` largest of the warp's n > top keys as keys[0 .. top) and
+// returns the smallest of them, which is found bit by bit.
+__device__ __noinline__ uint64_t narrow(WarpTop& t, int top, int n) {
     const int lane = (int)(threadIdx.x & 31u);
-    const bool any_open = __any_sync(0xFFFFFFFFu, open != 0);
+    uint64_t k[kLpCap / 32];
+#pragma unroll
+    for (int j = 0; j < kLpCap / 32; ++j) k[j] = lane + 32 * j < n ? t.keys[lane + 32 * j] : 0;
     uint64_t lo = 0;
+#pragma unroll 1
     for (int i = 63; i >= 0; --i) {
         const uint64_t mid = lo | (1ull << i);
         int c = 0;
-        for (int j = lane; j < n; j += 32) c += t.keys[j] >= mid;
-        if (any_open) {
-            for (int u = 0; u < kLpUnroll; ++u) {
-                float f[per];
-                Logit<BYTES>::unpack(v[u], f);
 #pragma unroll
-                for (int j = 0; j < per; ++j)
-                    if (open >> (u * per + j) & 1) c += key_of(f[j], at + (int64_t)u * NT * per + j) >= mid;
-            }
-            if (open >> 63) c += key_of(extra, extra_at) >= mid;
-        }
+        for (int j = 0; j < kLpCap / 32; ++j) c += k[j] >= mid;
         if (__reduce_add_sync(0xFFFFFFFFu, c) >= top) lo = mid;
     }
-    if (lane == 0) t.kept = 0;
+    int at = 0;
     __syncwarp();
-    for (int j = lane; j < n; j += 32)
-        if (t.keys[j] >= lo) t.best[atomicAdd(&t.kept, 1)] = t.keys[j];
-    if (any_open) {
-        for (int u = 0; u < kLpUnroll; ++u) {
-            float f[per];
-            Logit<BYTES>::unpack(v[u], f);
 #pragma unroll
-            for (int j = 0; j < per; ++j) {
-                const uint64_t k = key_of(f[j], at + (int64_t)u * NT * per + j);
-                if ((open >> (u * per + j) & 1) && k >= lo) t.best[atomicAdd(&t.kept, 1)] = k;
-            }
-        }
-        if ((open >> 63) && key_of(extra, extra_at) >= lo) t.best[atomicAdd(&t.kept, 1)] = key_of(extra, extra_at);
+    for (int j = 0; j < kLpCap / 32; ++j) {
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, k[j] >= lo);
+        if (k[j] >= lo) t.keys[at + __popc(m & ((1u << lane) - 1u))] = k[j];
+        at += __popc(m);
     }
-    __syncwarp();
-    if (lane < top) t.keys[lane] = t.best[lane];
     if (lane == 0) t.count = top;
     __syncwarp();
     return lo;
 }
 
 // The `top` largest keys of keys[0 .. n) in falling order (keys are unique, but
-// for 0, which is none), 0 behind.
-template <int NT> __device__ __forceinline__ void sort_top(const uint64_t* keys, int n, int top, uint64_t* sorted) {
-    const int tid = (int)threadIdx.x;
+// for 0, which is none), 0 behind.  n at most kLpGather; keys 16-byte aligned.
+template <int NT> __device__ __forceinline__ void sort_top(uint64_t* keys, int n, int top, uint64_t* sorted) {
+    const int tid = (int)threadIdx.x, padded = (n + 7) & ~7;
     if (tid < top) sorted[tid] = 0;
+    if (tid < padded - n) keys[n + tid] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += NT) {
         const uint64_t k = keys[i];
-        if (k == 0) continue;
         int above = 0;
-        for (int j = 0; j < n; ++j) above += keys[j] > k;
-        if (above < top) sorted[above] = k;
+        for (int j = 0; j < padded; j += 8) {
+            ulonglong2 o[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) o[u] = *reinterpret_cast<const ulonglong2*>(keys + j + 2 * u);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) above += (o[u].x > k) + (o[u].y > k);
+        }
+        if (k != 0 && above < top) sorted[above] = k;
     }
     __syncthreads();
 }
 
+// Joins n <= 8 partial results, in order of their place; for the whole first warp.
+__device__ __forceinline__ Soft join_parts(const Soft* parts, int n, float c) {
+    const int lane = (int)(threadIdx.x & 31u);
+    Soft v = lane < n ? parts[lane] : Soft{kLowest, 0.0f, 0.0f, -INFINITY};
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+        Soft b;
+        b.m = __shfl_down_sync(0xFFFFFFFFu, v.m, o);
+        b.s = __shfl_down_sync(0xFFFFFFFFu, v.s, o);
+        b.e = __shfl_down_sync(0xFFFFFFFFu, v.e, o);
+        b.top = __shfl_down_sync(0xFFFFFFFFu, v.top, o);
+        v = join(v, b, c);
+    }
+    return v;
+}
+
 template <int BYTES, bool TOP, bool ENT, int NT>
-__global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
+__global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(const LpArgs a) {
     using L = Logit<BYTES>;
     constexpr int per = L::kPerVec;
     __shared__ LpShared<NT> sh;
@@ -384,7 +396,7 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
     const int64_t v0 = cut.vecs * rank / ranks, v1 = cut.vecs * (rank + 1) / ranks;
     const unsigned char* body = x + (int64_t)cut.head * BYTES;
     if (ranks > 1) cluster_arrive();
-    if (TOP && lane == 0) mine.count = 0;
+    if (TOP && tid == 0) t.listed = t.gathered = 0;
     dependency_wait();
     allow_dependents();
 
@@ -413,69 +425,26 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
 
     Sums<BYTES, ENT> sums;
     sums.reset();
-    float floor_value = -INFINITY;                   // candidates are not below it,
-    uint64_t floor_key = 0;                          // nor their keys below this one
-    bool first = true;
-    for (int64_t base = v0; base < v1 || first; base += (int64_t)NT * kLpUnroll) {
+    int places = 0, sharing = 0;                     // places of stored maxima begun, and steps in the last of them
+    float held = -INFINITY;
+    for (int64_t base = v0; base < v1; base += (int64_t)NT * kLpUnroll) {
         uint4 v[kLpUnroll];
 #pragma unroll
         for (int u = 0; u < kLpUnroll; ++u) v[u] = next[u];
         if (base + (int64_t)NT * kLpUnroll < v1) load(next, base + (int64_t)NT * kLpUnroll);
-        float most = largest<BYTES>(v);
-        if (first) most = fmaxf(most, extra);
+        const float most = largest<BYTES>(v);
         sums.meet(most, a.c);
         sums.add(v, a.c);
-        if (first && !(extra == -INFINITY)) sums.add_one(extra, a.c);
         if (TOP) {
-            if (first) {
-                // the top-th largest of 64 groups' maxima: as many elements are not below it
-                float g = most;
-#pragma unroll
-                for (int o = 1; o < NT / 64; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
-                if (tid % (NT / 64) == 0) t.group[tid / (NT / 64)] = g;
-                __syncthreads();
-                if (tid < 64) {
-                    const float own = t.group[tid];
-                    int above = 0;
-                    for (int j = 0; j < 64; ++j) {
-                        const float o = t.group[j];
-                        above += o > own || (o == own && j < tid);
-                    }
-                    if (above == a.top - 1) t.floor = own;
-                }
-                __syncthreads();
-                floor_value = t.floor;
-            }
-            if (__any_sync(0xFFFFFFFFu, most >= floor_value && most > -INFINITY)) {
-                const int64_t at = cut.head + (base + tid) * per;
-                uint64_t open = 0;                   // candidates that found no place
-                auto offer = [&](float f, int64_t i, int bit) {
-                    if (!(f > -INFINITY && f >= floor_value)) return;
-                    const uint64_t k = key_of(f, i);
-                    if (k < floor_key) return;
-                    const int pos = atomicAdd(&mine.count, 1);
-                    if (pos < kLpCap) mine.keys[pos] = k;
-                    else open |= 1ull << bit;
-                };
-                if (most >= floor_value) {
-                    for (int u = 0; u < kLpUnroll; ++u) {
-                        float f[per];
-                        L::unpack(v[u], f);
-#pragma unroll
-                        for (int j = 0; j < per; ++j) offer(f[j], at + (int64_t)u * NT * per + j, u * per + j);
-                    }
-                    if (first) offer(extra, extra_at, 63);
-                }
-                __syncwarp();
-                const int n = mine.count;
-                __syncwarp();
-                if (n > kLpCap - 32) {
-                    floor_key = narrow<BYTES, NT>(mine, a.top, n < kLpCap ? n : kLpCap, open, v, extra, at, extra_at);
-                    floor_value = fmaxf(floor_value, key_value(floor_key));
-                }
-            }
+            if (sharing == 0) held = -INFINITY, ++places;
+            held = fmaxf(held, most);
+            t.most[(places - 1) * NT + tid] = held;
+            if (++sharing == a.fold) sharing = 0;
         }
-        first = false;
+    }
+    if (!(extra == -INFINITY)) {
+        sums.meet(extra, a.c);
+        sums.add_one(extra, a.c);
     }
 
     Soft acc = sums.settle(a.c);
@@ -490,23 +459,113 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
     }
     if (lane == 0) sh.warp[warp] = acc;
     if (TOP) {
-        // the warps' candidates, `top` each at most, side by side
-        int n = mine.count;
-        if (n > a.top) {
-            const uint4 none[kLpUnroll] = {};
-            narrow<BYTES, NT>(mine, a.top, n, 0, none, 0.0f, 0, 0);
-            n = a.top;
-        }
-        if (lane < a.top) t.gather[warp * a.top + lane] = lane < n ? mine.keys[lane] : 0;
+        float g = sums.top;
+#pragma unroll
+        for (int o = 1; o < NT / 64; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
+        if (tid % (NT / 64) == 0) t.group[tid / (NT / 64)] = g;
         __syncthreads();
-        sort_top<NT>(t.gather, NT / 32 * a.top, a.top, t.sorted);
+        if (tid < 64) {
+            const float own = t.group[tid];
+            int above = 0;
+#pragma unroll 16
+            for (int j = 0; j < 64; ++j) {
+                const float o = t.group[j];
+                above += o > own || (o == own && j < tid);
+            }
+            if (above == a.top - 1) t.floor = own;
+        }
+        __syncthreads();
+        const float floor_value = t.floor;
+        for (int i = 0; i < places; ++i) {
+            const float m = t.most[i * NT + tid];
+            if (m >= floor_value && m > -INFINITY) {
+                const int pos = atomicAdd(&t.listed, 1);
+                if (pos < kLpGather) t.list[pos] = i * NT + tid;
+            }
+        }
+        auto gather = [&](float f, int64_t i) {
+            if (!(f >= floor_value && f > -INFINITY)) return;
+            const int pos = atomicAdd(&t.gathered, 1);
+            if (pos < kLpGather) t.gather[pos] = key_of(f, i);
+        };
+        gather(extra, extra_at);
+        __syncthreads();
+        const int listed = t.listed;
+        if (listed <= kLpGather) {
+            for (int e = tid; e < listed; e += NT) {
+                const int place = t.list[e] / NT, owner = t.list[e] % NT;
+                for (int f = 0; f < a.fold; ++f) {
+                    const int64_t i0 = v0 + ((int64_t)(place * a.fold + f) * kLpUnroll) * NT + owner;
+                    uint4 v[kLpUnroll];
+#pragma unroll
+                    for (int u = 0; u < kLpUnroll; ++u)
+                        v[u] = i0 + u * NT < v1 ? ld_stream(body + 16 * (i0 + u * NT))
+                                                : make_uint4(L::kNothing, L::kNothing, L::kNothing, L::kNothing);
+#pragma unroll
+                    for (int u = 0; u < kLpUnroll; ++u) {
+                        float x8[per];
+                        L::unpack(v[u], x8);
+#pragma unroll
+                        for (int j = 0; j < per; ++j) gather(x8[j], cut.head + (i0 + u * NT) * per + j);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        int n = t.gathered;
+        if (listed > kLpGather || n > kLpGather) {
+            // too many: every warp goes through its steps again and keeps its best
+            if (lane == 0) mine.count = 0;
+            __syncwarp();
+            uint64_t floor_key = 0;
+            float floor_own = floor_value;
+            auto offer = [&](float f, int64_t i) {   // one logit of each lane
+                bool pending = f > -INFINITY && f >= floor_own && key_of(f, i) >= floor_key;
+                while (__any_sync(0xFFFFFFFFu, pending)) {
+                    if (pending) {
+                        const int pos = atomicAdd(&mine.count, 1);
+                        if (pos < kLpCap) mine.keys[pos] = key_of(f, i), pending = false;
+                    }
+                    __syncwarp();
+                    const int c = mine.count;
+                    __syncwarp();
+                    if (c > kLpCap - 32) {
+                        floor_key = narrow(mine, a.top, c < kLpCap ? c : kLpCap);
+                        floor_own = fmaxf(floor_own, key_value(floor_key));
+                        pending = pending && key_of(f, i) >= floor_key;
+                    }
+                }
+            };
+            offer(extra, extra_at);
+#pragma unroll 1
+            for (int s = 0; s < places; ++s) {
+                if (!__any_sync(0xFFFFFFFFu, t.most[s * NT + tid] >= floor_own)) continue;
+#pragma unroll 1
+                for (int u = 0; u < kLpUnroll * a.fold; ++u) {
+                    const int64_t i = v0 + ((int64_t)s * a.fold * kLpUnroll + u) * NT + tid;
+                    const uint4 v = i < v1 ? ld_stream(body + 16 * i) : make_uint4(L::kNothing, L::kNothing, L::kNothing, L::kNothing);
+                    float x8[per];
+                    L::unpack(v, x8);
+#pragma unroll
+                    for (int j = 0; j < per; ++j)
+                        if (__any_sync(0xFFFFFFFFu, x8[j] >= floor_own)) offer(x8[j], cut.head + i * per + j);
+                }
+            }
+            int own = mine.count;
+            if (own > a.top) {
+                narrow(mine, a.top, own);
+                own = a.top;
+            }
+            __syncthreads();                         // the gathered ones have been counted
+            if (lane < a.top) t.gather[warp * a.top + lane] = lane < own ? mine.keys[lane] : 0;
+            n = NT / 32 * a.top;
+            __syncthreads();
+        }
+        sort_top<NT>(t.gather, n, a.top, t.sorted);
     } else {
         __syncthreads();
     }
-    if (tid == 0) {
-        acc = sh.warp[0];
-        for (int w = 1; w < NT / 32; ++w) acc = join(acc, sh.warp[w], a.c);
-    }
+    if (warp == 0) acc = join_parts(sh.warp, NT / 32, a.c);
     if (ranks > 1) {
         cluster_wait();                              // the first block has started
         if (TOP) cluster_sync();                     // and no longer reads what it gathered from its warps
@@ -520,10 +579,7 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
         if (TOP && tid < a.top) st_cluster_u64(map_rank0(&t.gather[rank * a.top + tid]), t.sorted[tid]);
         cluster_sync();
         if (rank != 0) return;
-        if (tid == 0) {
-            acc = sh.part[0];
-            for (uint32_t r = 1; r < ranks; ++r) acc = join(acc, sh.part[r], a.c);
-        }
+        if (warp == 0) acc = join_parts(sh.part, (int)ranks, a.c);
         if (TOP) sort_top<NT>(t.gather, (int)ranks * a.top, a.top, t.sorted);
     }
     if (tid == 0) {
@@ -541,12 +597,14 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const LpArgs a) {
         }
         if (TOP) {
             sh.part[0] = {m, log_s, none ? 1.0f : 0.0f, 0.0f};
-            // fewer candidates than asked for: the first logits that are -inf (or NaN) fill the list; fewer than `top`
-            // are neither, so that they lie among the first 2 * top
-            int n = 0;
-            while (n < a.top && t.sorted[n] != 0) ++n;
-            for (int64_t i = 0; n < a.top; ++i)
-                if (!(L::load(x, i) > -INFINITY)) t.sorted[n++] = key_of(-INFINITY, i);
+            if (t.sorted[a.top - 1] == 0) {
+                // fewer candidates than asked for: the first logits that are -inf (or NaN) fill the list; fewer than
+                // `top` are neither, so that they lie among the first 2 * top
+                int n = 0;
+                while (t.sorted[n] != 0) ++n;
+                for (int64_t i = 0; n < a.top; ++i)
+                    if (!(L::load(x, i) > -INFINITY)) t.sorted[n++] = key_of(-INFINITY, i);
+            }
         }
     }
     if (TOP) {
@@ -709,13 +767,23 @@ fp8q_status_t check_logits(int64_t rows, int64_t vocab, int64_t stride, int logi
 }
 
 template <int BYTES, bool TOP, bool ENT, int NT>
-fp8q_status_t launch_logprobs(const LpArgs& a, int64_t rows, cudaStream_t stream) {
-    // blocks of a cluster share a row while there are fewer rows than SMs to fill twice
+fp8q_status_t launch_logprobs(LpArgs a, int64_t rows, cudaStream_t stream) {
+    // blocks of a cluster share a row while there are few rows
     unsigned ranks = 1;
     const int64_t steps = (a.vocab * BYTES + NT * kLpUnroll * 16 - 1) / (NT * kLpUnroll * 16);
-    while (ranks < kLpMaxCluster && rows * ranks * 2 <= 2 * sm_count() && (int64_t)ranks * 2 <= steps) ranks *= 2;
-    return launch_clusters(token_logprobs_kernel<BYTES, TOP, ENT, NT>, (unsigned)rows * ranks, ranks, NT,
-                           TOP ? sizeof(LpTopShared<NT>) : 0, stream, a);
+    while (ranks < kLpMaxCluster && rows * ranks * 2 <= kLpBlocksPerSm * sm_count() && (int64_t)ranks * 2 <= steps) ranks *= 2;
+    constexpr size_t kMax = TOP ? sizeof(LpTopShared<NT>) + (size_t)kLpPlaces * NT * 4 : 0;
+    size_t smem = 0;
+    if (TOP) {
+        const int64_t mine = steps / ranks + 1;      // of one block, at most
+        a.fold = (int)((mine + kLpPlaces - 1) / kLpPlaces);
+        smem = sizeof(LpTopShared<NT>) + (size_t)((mine + a.fold - 1) / a.fold) * NT * 4;
+    }
+    static KernelCache cache;
+    int resident = 0;
+    const fp8q_status_t st = prepare_kernel(cache, token_logprobs_kernel<BYTES, TOP, ENT, NT>, NT, smem, kMax, &resident);
+    if (st != FP8Q_OK) return st;
+    return launch_clusters(token_logprobs_kernel<BYTES, TOP, ENT, NT>, (unsigned)rows * ranks, ranks, NT, smem, stream, a);
 }
 
 template <int BYTES, bool TOP, bool ENT>
@@ -769,7 +837,7 @@ extern "C" fp8q_status_t fp8q_token_logprobs(const void* logits, int logit_bytes
     const Range ins[] = {{logits, span(rows, vocab, stride, logit_bytes)}, {targets, r * id_bytes}};
     if (any_alias(outs, 5, ins, 2)) return FP8Q_ERR_ALIAS;
     const LpArgs a = {logits, targets, id_bytes == 8, vocab, stride, temperature,
-                      (float)(1.44269504088896340736 / (double)temperature), top, logprobs, entropy, top_logprobs, top_ids, stats};
+                      (float)(1.44269504088896340736 / (double)temperature), top, 1, logprobs, entropy, top_logprobs, top_ids, stats};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return logit_bytes == 2 ? launch_logprobs_kind<2>(a, rows, s) : launch_logprobs_kind<4>(a, rows, s);
 }
