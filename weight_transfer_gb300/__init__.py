@@ -976,27 +976,62 @@ def mxfp8_moe_swiglu(codes: torch.Tensor, scales: torch.Tensor, gate_codes: torc
     return out_codes, out_scales
 
 
-def _one_device(tensors) -> None:
-    """Refuses tensors of different devices, or of another device than the current one, on which the call would run."""
-    at = None
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d < 0:
-                raise ValueError("every tensor must be a CUDA tensor")
-            if at is None:
-                at = d
-                if d != torch.cuda.current_device():
-                    raise ValueError(f"the tensors are on cuda:{d}, which is not the current device")
-            elif d != at:
-                raise ValueError(f"tensors on cuda:{at} and on cuda:{d} in one call")
+def _current_device() -> int:
+    # the index alone: torch.cuda.current_device() takes three times as long
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
 
 
-def _ids(t: torch.Tensor, what: str, shape) -> tuple:
+def _device_of(t: torch.Tensor, what: str) -> int:
+    """Index of a tensor's device, which has to be the current one, on which the call runs."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if d != torch._C._cuda_getDevice():      # the tensor is there, so that CUDA is initialized
+        raise ValueError(f"{what} is on cuda:{d}, which is not the current device")
+    return d
+
+
+def _ptr(t: torch.Tensor, what: str, dtype, shape, device: int) -> int:
+    """Pointer of a contiguous tensor of exactly this type, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be a CUDA tensor")
+        if t.get_device() != device:
+            raise ValueError(f"{what} is on cuda:{t.get_device()}, other tensors of the call on cuda:{device}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _held(t: Optional[torch.Tensor], what: str, dtype, numel: int, device: int) -> Optional[int]:
+    """Pointer of a contiguous tensor of this type and device with room for so many elements."""
+    if t is None:
+        return None
+    p = _dev(t, what, dtype, numel)
+    if t.get_device() != device:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, other tensors of the call on cuda:{device}")
+    return p
+
+
+def _made(t: Optional[torch.Tensor], what: str, dtype, shape, numel: int, like: torch.Tensor, device: int, stream):
+    """(tensor, pointer) of an output: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device) if stream is None else _new(shape, dtype, like.device, stream)
+        return t, t.data_ptr()
+    return t, _held(t, what, dtype, numel, device)
+
+
+def _ids(t: torch.Tensor, what: str, shape, device: int) -> tuple:
     """(pointer, bytes per element) of integers of exactly this shape."""
-    if t.dtype is not torch.int64 and t.dtype is not torch.int32:
-        raise ValueError(f"{what} must be int32 or int64, got {t.dtype}")
-    return _in(t, what, t.dtype, shape), 8 if t.dtype is torch.int64 else 4
+    dtype = t.dtype
+    if dtype is torch.int64:
+        return _ptr(t, what, dtype, shape, device), 8
+    if dtype is torch.int32:
+        return _ptr(t, what, dtype, shape, device), 4
+    raise ValueError(f"{what} must be int32 or int64, got {dtype}")
 
 
 def mxfp8_moe_decode_workspace_bytes(tokens: int, topk: int, n: int) -> int:
@@ -1014,23 +1049,33 @@ def mxfp8_moe_decode(codes: torch.Tensor, scales: torch.Tensor, ids: torch.Tenso
     swizzled scales -> bf16 [tokens, k]."""
     tokens, k = _rows_of(codes, "codes")
     topk = _rows_of(ids, "ids")[1]
-    experts, n = gate_codes.shape[0], gate_codes.shape[-2]
-    _one_device((codes, scales, ids, weights, gate_codes, gate_scales, up_codes, up_scales, down_codes, down_scales, out, workspace))
-    cp = _dev(codes, "codes", torch.uint8)
-    sp = _in(scales, "scales", torch.uint8, (tokens, k // MXFP8_BLOCK))
-    ip, id_bytes = _ids(ids, "ids", (tokens, topk))
-    wp = _in(weights, "weights", torch.float32, (tokens, topk))
-    gp, gsp = _expert_weights(gate_codes, gate_scales, "gate_codes", experts, n, k)
-    up, usp = _expert_weights(up_codes, up_scales, "up_codes", experts, n, k)
-    dp, dsp = _expert_weights(down_codes, down_scales, "down_codes", experts, k, n)
-    out, op = _out(out, "out", torch.bfloat16, (tokens, k), codes.device, tokens * k, stream)
+    if gate_codes.dim() != 3:
+        raise ValueError(f"gate_codes must be [experts, n, k], got {list(gate_codes.shape)}")
+    experts, n, _ = gate_codes.shape
+    d = _device_of(codes, "codes")
+    u8 = torch.uint8
+    inner, outer = (experts, n, k), (experts, k, n)
+    tiles_n, tiles_k = (n + 127) // 128, (k + 127) // 128
+    scale_bytes = experts * tiles_n * tiles_k * 512
+    cp = _ptr(codes, "codes", u8, (tokens, k), d)
+    sp = _ptr(scales, "scales", u8, (tokens, k // MXFP8_BLOCK), d)
+    ip, id_bytes = _ids(ids, "ids", (tokens, topk), d)
+    wp = _ptr(weights, "weights", torch.float32, (tokens, topk), d)
+    gp, up, dp = (_ptr(gate_codes, "gate_codes", u8, inner, d), _ptr(up_codes, "up_codes", u8, inner, d),
+                  _ptr(down_codes, "down_codes", u8, outer, d))
+    gsp, usp, dsp = (_held(gate_scales, "gate_scales", u8, scale_bytes, d), _held(up_scales, "up_scales", u8, scale_bytes, d),
+                     _held(down_scales, "down_scales", u8, scale_bytes, d))
+    out, op = _made(out, "out", torch.bfloat16, (tokens, k), tokens * k, codes, d, stream)
     if workspace is None:
         have = _lib.mxfp8_moe_decode_workspace_bytes(tokens, topk, n)
-        workspace = _new(have, torch.uint8, codes.device, stream, kept=False)
+        workspace = torch.empty(have, dtype=u8, device=codes.device) if stream is None else _new(have, u8, codes.device, stream,
+                                                                                                 kept=False)
+        bp = workspace.data_ptr()
     else:
         have = workspace.numel() * workspace.element_size()
-    st = _lib.mxfp8_moe_decode(cp, sp, ip, id_bytes, wp, tokens, topk, gp, gsp, up, usp, dp, dsp, experts, n, k, op,
-                               _dev(workspace, "workspace"), have, _stream(stream))
+        bp = _held(workspace, "workspace", None, 0, d)
+    st = _lib.mxfp8_moe_decode(cp, sp, ip, id_bytes, wp, tokens, topk, gp, gsp, up, usp, dp, dsp, experts, n, k, op, bp, have,
+                               _stream(stream))
     if st:
         _check("mxfp8_moe_decode", st)
     return out
@@ -1059,25 +1104,25 @@ def fp8q_token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = 
     [rows] or None, entropy float32 [rows] or None, top_logprobs float32 [rows,
     top] or None, top_ids int32 [rows, top] or None, stats float32 [rows, 2] or
     None), of softmax(logits / temperature).  stats is what the gradient reads."""
-    _one_device((logits, targets, logprobs, entropy, top_logprobs, top_ids, stats))
+    d = _device_of(logits, "logits")
     xp, size, rows, vocab, stride = _logits(logits, "logits")
-    dev = logits.device
+    f32 = torch.float32
     tp = lp = ep = vp = ip = sp = None
     id_bytes = 8
     if targets is not None:
-        tp, id_bytes = _ids(targets, "targets", (rows,))
-        logprobs, lp = _out(logprobs, "logprobs", torch.float32, (rows,), dev, rows, stream)
+        tp, id_bytes = _ids(targets, "targets", (rows,), d)
+        logprobs, lp = _made(logprobs, "logprobs", f32, (rows,), rows, logits, d, stream)
     elif logprobs is not None:
         raise ValueError("logprobs without targets")
     if want_entropy or entropy is not None:
-        entropy, ep = _out(entropy, "entropy", torch.float32, (rows,), dev, rows, stream)
+        entropy, ep = _made(entropy, "entropy", f32, (rows,), rows, logits, d, stream)
     if top > 0:
-        top_logprobs, vp = _out(top_logprobs, "top_logprobs", torch.float32, (rows, top), dev, rows * top, stream)
-        top_ids, ip = _out(top_ids, "top_ids", torch.int32, (rows, top), dev, rows * top, stream)
+        top_logprobs, vp = _made(top_logprobs, "top_logprobs", f32, (rows, top), rows * top, logits, d, stream)
+        top_ids, ip = _made(top_ids, "top_ids", torch.int32, (rows, top), rows * top, logits, d, stream)
     elif top_logprobs is not None or top_ids is not None:
         raise ValueError("top_logprobs or top_ids without top")
     if want_stats or stats is not None:
-        stats, sp = _out(stats, "stats", torch.float32, (rows, 2), dev, rows * 2, stream)
+        stats, sp = _made(stats, "stats", f32, (rows, 2), rows * 2, logits, d, stream)
     st = _lib.fp8q_token_logprobs(xp, size, rows, vocab, stride, tp, id_bytes, temperature, top, lp, ep, vp, ip, sp,
                                   _stream(stream))
     if st:
@@ -1092,6 +1137,8 @@ def _like_rows(logits: torch.Tensor, ptr: int, size: int, rows: int, vocab: int,
     per = 16 // size
     apart = vocab + (stride - vocab) % per
     shift = ptr % 16 // size
+    if shift == 0 and stream is None:
+        return torch.empty_strided((rows, vocab), (apart, 1), dtype=logits.dtype, device=logits.device)
     flat = _new(rows * apart + shift, logits.dtype, logits.device, stream)
     return flat[shift:].as_strided((rows, vocab), (apart, 1))
 
@@ -1103,21 +1150,27 @@ def fp8q_token_logprobs_backward(logits: torch.Tensor, targets: Optional[torch.T
     """Gradient of fp8q_token_logprobs' logprobs (dlogprobs float32 [rows], with
     the targets) and entropy (dentropy float32 [rows], with the entropy) ->
     dlogits of the logits' shape and type; may be `logits` (in place)."""
-    _one_device((logits, targets, stats, dlogprobs, entropy, dentropy, dlogits))
+    d = _device_of(logits, "logits")
     xp, size, rows, vocab, stride = _logits(logits, "logits")
-    sp = _in(stats, "stats", torch.float32, (rows, 2))
-    tp, id_bytes, gp = None, 8, None
+    f32 = torch.float32
+    sp = _ptr(stats, "stats", f32, (rows, 2), d)
+    tp, id_bytes, gp, ep, hp = None, 8, None, None, None
     if dlogprobs is not None:
         if targets is None:
             raise ValueError("dlogprobs without targets")
-        tp, id_bytes = _ids(targets, "targets", (rows,))
-        gp = _in(dlogprobs, "dlogprobs", torch.float32, (rows,))
-    ep = _in(entropy, "entropy", torch.float32, (rows,)) if dentropy is not None else None
-    hp = _in(dentropy, "dentropy", torch.float32, (rows,))
+        tp, id_bytes = _ids(targets, "targets", (rows,), d)
+        gp = _ptr(dlogprobs, "dlogprobs", f32, (rows,), d)
+    if dentropy is not None:
+        if entropy is None:
+            raise ValueError("dentropy without the entropy")
+        ep = _ptr(entropy, "entropy", f32, (rows,), d)
+        hp = _ptr(dentropy, "dentropy", f32, (rows,), d)
     if dlogits is None:
         dlogits = _like_rows(logits, xp, size, rows, vocab, stride, stream)
     elif dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
         raise ValueError(f"dlogits must be {logits.dtype} {list(logits.shape)}, got {dlogits.dtype} {list(dlogits.shape)}")
+    elif dlogits.get_device() != d:
+        raise ValueError(f"dlogits is on cuda:{dlogits.get_device()}, the logits on cuda:{d}")
     dp, _, _, _, dstride = _logits(dlogits, "dlogits")
     st = _lib.fp8q_token_logprobs_backward(xp, size, rows, vocab, stride, tp, id_bytes, temperature, sp, gp, ep, hp, dp, dstride,
                                            _stream(stream))
@@ -1141,15 +1194,17 @@ class fp8q_grad_list:
         outs = None if outs is None else list(outs)
         if outs is not None and len(outs) != len(grads):
             raise ValueError(f"{len(grads)} gradients and {len(outs)} outputs")
-        _one_device(grads + (outs or []))
         self.grads, self.outs, self.count = grads, outs, len(grads)
         self.device = grads[0].device if grads else torch.device("cuda")
         arr = (fp8q_grad_t * max(self.count, 1))()
+        d = _device_of(grads[0], "grads[0]") if grads else -1
         for i, g in enumerate(grads):
             o = g if outs is None else outs[i]
             for t, what in ((g, "grads"), (o, "outs")):
                 if t.dtype not in _GRAD_TYPES:
                     raise ValueError(f"{what}[{i}] must be bfloat16 or float32, got {t.dtype}")
+                if t.get_device() != d:
+                    raise ValueError(f"{what}[{i}] is on {t.device}, grads[0] on cuda:{d}")
             if o.numel() != g.numel():
                 raise ValueError(f"outs[{i}] holds {o.numel()} elements, grads[{i}] {g.numel()}")
             arr[i] = fp8q_grad_t(_dev(g, f"grads[{i}]"), _dev(o, f"outs[{i}]"), g.numel(), _GRAD_TYPES[g.dtype],
@@ -1163,17 +1218,31 @@ class fp8q_grad_list:
 
 
 def _grad_call(name: str, grads, max_norm, scale, want_each, norm, each, workspace, stream):
-    _one_device((norm, each, workspace) if not grads.grads else (grads.grads[0], norm, each, workspace))
-    norm, np_ = _out(norm, "norm", torch.float32, (2,), grads.device, 2, stream)
+    d = _current_device()
+    dev = torch.device("cuda", d)
+    if grads.count and grads.device != dev:
+        raise ValueError(f"the gradients are on {grads.device}, which is not the current device")
+    f32 = torch.float32
+    if norm is None:
+        norm = torch.empty(2, dtype=f32, device=dev) if stream is None else _new(2, f32, dev, stream)
+        np_ = norm.data_ptr()
+    else:
+        np_ = _held(norm, "norm", f32, 2, d)
     ep = None
-    if want_each or each is not None:
-        each, ep = _out(each, "each", torch.float32, (grads.count,), grads.device, grads.count, stream)
+    if each is not None:
+        ep = _held(each, "each", f32, grads.count, d)
+    elif want_each:
+        each = _new(grads.count, f32, dev, stream)
+        ep = each.data_ptr()
     have = grads.workspace_bytes
     if workspace is None:
-        workspace = _new(have, torch.uint8, grads.device, stream, kept=False)
+        workspace = torch.empty(have, dtype=torch.uint8, device=dev) if stream is None else _new(have, torch.uint8, dev, stream,
+                                                                                                 kept=False)
+        wp = workspace.data_ptr()
     else:
         have = workspace.numel() * workspace.element_size()
-    st = getattr(_lib, name)(grads.plan, scale, max_norm, np_, ep, _dev(workspace, "workspace"), have, _stream(stream))
+        wp = _held(workspace, "workspace", None, 0, d)
+    st = getattr(_lib, name)(grads.plan, scale, max_norm, np_, ep, wp, have, _stream(stream))
     if st:
         _check(name, st)
     return norm, each
