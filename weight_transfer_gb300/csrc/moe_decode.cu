@@ -106,63 +106,58 @@ struct MdList {                             // arrays in shared memory, list_str
 __host__ __device__ __forceinline__ int list_stride(int choices) { return (choices + 8) & ~7; }
 
 struct MdScratch {
-    int16_t key[kMdMaxChoices + 8], sorted[kMdMaxChoices + 1];
+    int key[kMdMaxChoices + 4], sorted[kMdMaxChoices + 1];
     int heads[kMdMaxChoices / 32];
+    int live;
 };
 
+// A choice's key is its expert and, below that, its own number, so that keys are
+// unique and its place is the number of smaller ones; dropped choices go last.
 // The ids are read past the first-level cache: the down products' kernel reads
 // them before its own dependency wait.
+constexpr int kMdDropped = 1024 << 10;
 template <int NT> __device__ __forceinline__ void sort_choices(const MdArgs& a, MdList& s, MdScratch& w) {
     const int tid = (int)threadIdx.x, lane = tid & 31;
-    const int choices = a.tokens * a.topk;
-    for (int i = tid; i < ((choices + 7) & ~7); i += NT) {
+    const int choices = a.tokens * a.topk, padded = (choices + 3) & ~3;
+    for (int i = tid; i < padded; i += NT) {
         int64_t id = -1;
         if (i < choices)
             id = a.id64 ? (int64_t)__ldcg(static_cast<const long long*>(a.ids) + i) : (int64_t)__ldcg(static_cast<const int*>(a.ids) + i);
-        w.key[i] = id >= 0 && id < a.experts ? (int16_t)id : (int16_t)0x7FFF;       // dropped choices go last
-    }
-    __syncthreads();
-    // a choice's place: those of lower experts, and the earlier ones of its own, counted eight at a time
-    for (int i = tid; i < choices; i += NT) {
-        const int key = w.key[i];
-        const uint32_t mine = (uint32_t)key * 0x10001u;
-        int place = 0;
-        for (int j = 0; j < choices; j += 8) {
-            const uint4 v = *reinterpret_cast<const uint4*>(&w.key[j]);
-            const uint32_t h[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                place += __popc(__vcmpltu2(h[m], mine)) / 16;
-                const uint32_t same = __vcmpeq2(h[m], mine);
-                place += (j + 2 * m < i && (same & 1u)) + (j + 2 * m + 1 < i && (same >> 31));
-            }
-        }
-        if (key == 0x7FFF) {
-            // the keys that fill the last eight stand behind all choices; a dropped choice has no place in the lists
-            continue;
-        }
-        w.sorted[place + 1] = (int16_t)key;
-        s.order[place] = (int16_t)i;
-        s.token[place] = (int16_t)(i / a.topk);
+        w.key[i] = id >= 0 && id < a.experts ? (int)id << 10 | i : kMdDropped | i;
     }
     if (tid == 0) w.sorted[0] = -1;
     __syncthreads();
-    int live = 0;                                       // choices that an expert takes
-    for (int i = tid; i < (choices + NT - 1) / NT * NT; i += NT) live += __syncthreads_count(i < choices && w.key[i] != 0x7FFF);
-    // an expert starts where the sorted keys change
-    for (int i = tid; i < ((live + 31) & ~31); i += NT) {
-        const unsigned m = __ballot_sync(0xFFFFFFFFu, i < live && w.sorted[i + 1] != w.sorted[i]);
-        if (lane == 0) w.heads[i >> 5] = (int)m;
+    for (int i = tid; i < choices; i += NT) {
+        const int key = w.key[i];
+        int place = 0;
+#pragma unroll 4
+        for (int j = 0; j < padded; j += 4) {
+            const int4 k = *reinterpret_cast<const int4*>(&w.key[j]);
+            place += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
+        }
+        w.sorted[place + 1] = key;
+        s.order[place] = (int16_t)i;
+        s.token[place] = (int16_t)(i / a.topk);
     }
     __syncthreads();
+    // an expert starts where the sorted keys' experts change
+    for (int i = tid; i < ((choices + 31) & ~31); i += NT) {
+        const int key = i < choices ? w.sorted[i + 1] : kMdDropped, before = i < choices ? w.sorted[i] : kMdDropped;
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, key < kMdDropped && key >> 10 != before >> 10);
+        if (lane == 0) w.heads[i >> 5] = (int)m;
+        if (i < choices && key >= kMdDropped && before < kMdDropped) w.live = i;
+        if (i == choices - 1 && key < kMdDropped) w.live = choices;
+    }
+    __syncthreads();
+    const int live = w.live;
     int active = 0;
-    for (int i = 0; i < (live + 31) >> 5; ++i) active += __popc(w.heads[i]);
-    for (int i = tid; i < live; i += NT) {
+    for (int i = 0; i < (choices + 31) >> 5; ++i) active += __popc(w.heads[i]);
+    for (int i = tid; i < choices; i += NT) {
         const int word = i >> 5;
         if (!(w.heads[word] >> lane & 1)) continue;
         int at = __popc(w.heads[word] & ((1u << lane) - 1u));
         for (int j = 0; j < word; ++j) at += __popc(w.heads[j]);
-        s.expert[at] = w.sorted[i + 1];
+        s.expert[at] = (int16_t)(w.sorted[i + 1] >> 10);
         s.start[at] = (int16_t)i;
     }
     if (tid == 0) s.start[active] = (int16_t)live;
