@@ -15,8 +15,6 @@
 namespace fp8q {
 
 constexpr int kMdMaxChoices = FP8Q_MOE_DECODE_MAX_TOKENS * FP8Q_MOE_MAX_TOPK;
-constexpr int kMdTiles = 2;                 // tiles of 8 columns that one pass over an expert's weights takes
-constexpr int kMdRow = 160;                 // bytes from row to row of a stage: 128, and 32 that keep rows off each other's banks
 
 struct MdArgs {
     const uint8_t *codes, *scales;                  // [tokens, k], [tokens, k / 32]
@@ -30,7 +28,6 @@ struct MdArgs {
     uint8_t* hs;                                    // [tokens * topk, hgroups * 4], their scales
     int hgroups;                                    // groups of four blocks of 32
     uint16_t* out;                                  // [tokens, k]
-    int tiles;                                      // column tiles that a pass takes, at most kMdTiles
 };
 
 // ------------------------------------------------------------ building blocks ----
@@ -170,6 +167,10 @@ template <int NT> __device__ __forceinline__ void sort_choices(const MdArgs& a, 
 // rows' scales.  A unit comes into a ring of a warp's own by asynchronous copies
 // that run DEPTH - 1 units ahead, across experts and tiles, so that no barrier
 // stops them.
+//   In a stage the four pieces of 32 bytes of a row lie in an order of their own,
+// piece b at b ^ (row % 4), so that the rows a warp reads at once keep off each
+// other's banks.
+constexpr int kMdRow = 128;
 constexpr int kMdScales = 16 * kMdRow;                  // where a stage's 16 scale lines lie
 constexpr int kMdStage = kMdScales + 16 * 16;
 
@@ -179,7 +180,7 @@ constexpr int kMdStage = kMdScales + 16 * 16;
 __device__ __forceinline__ void copy_unit(uint32_t stage, const uint8_t* upper, const uint8_t* lower, int64_t four, const uint8_t* line,
                                           int left) {
     const int lane = (int)(threadIdx.x & 31u), c = (lane & 7) * 16;
-    const uint32_t d = stage + (lane >> 3) * kMdRow + c;
+    const uint32_t d = stage + (lane >> 3) * kMdRow + (c ^ (lane >> 3) * 32);
     if (left >= 128) {
         copy16(d, upper);
         copy16(d + 4 * kMdRow, upper + four);
@@ -213,34 +214,31 @@ __device__ __forceinline__ void read_unit(Weights& w, uint32_t stage, uint32_t w
     e8m0x4(only(lds32(scales + 128), nblocks), w.sl);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-        w.u[b] = lds64(row + b * 32);
-        w.l[b] = lds64(row + 8 * kMdRow + b * 32);
+        const uint32_t at = row + ((b ^ (q & 3)) << 5);
+        w.u[b] = lds64(at);
+        w.l[b] = lds64(at + 8 * kMdRow);
     }
 }
 
 // ------------------------------------------------------ gate and up products ----
-// Four warps, or four pairs of warps that take turns at the groups of 128
-// columns (SPLIT), take 32 features of one expert: eight features' gate rows are
-// the upper and their up rows the lower half of a unit, so that a lane gets both
-// sums of a feature.  A tensor-core tile's columns are 8 rows of x; columns
+// A block takes 32 features of one expert, and a pair of its warps eight of
+// them: their gate rows are the upper and their up rows the lower half of a unit,
+// so that a lane gets both sums of a feature.  The two take turns at the groups
+// of 128 columns.  A tensor-core tile's columns are 8 rows of x; columns
 // without a row repeat the first one's data, and their sums are not read.
 constexpr int kUpThreads = 256;
 constexpr int kUpWarps = kUpThreads / 32;
-constexpr int kUpDepth = 4;
+constexpr int kUpDepth = 3;
 constexpr int kUpRing = kUpWarps * kUpDepth * kMdStage;
-constexpr int kUpSums = 2 * kUpWarps * 4 * 33 * 4;      // bytes of partial sums for each column tile
+constexpr int kUpWords = 4 * 33;                        // a warp's partial sums
+constexpr int kUpSums = 2 * kUpWarps * kUpWords * 4;
+constexpr int kUpBlocks = 2;                            // per SM
 
-template <int SPLIT> __device__ __forceinline__ void team_sync(int team) {
-    if (SPLIT == 2) __syncthreads();
-    else asm volatile("bar.sync %0, 128;" ::"r"(1 + team) : "memory");
-}
-
-template <int SPLIT> __global__ void __launch_bounds__(kUpThreads, 2) moe_decode_up_kernel(const MdArgs a) {
+__global__ void __launch_bounds__(kUpThreads, kUpBlocks) moe_decode_up_kernel(const MdArgs a) {
     extern __shared__ __align__(16) unsigned char dyn[];
-    constexpr int kTeam = 4 * SPLIT, kTeams = kUpWarps / kTeam;     // warps of a team, teams of a block
-    float* red = reinterpret_cast<float*>(dyn + kUpRing);           // [2][warps][tiles][4][33]
+    float* red = reinterpret_cast<float*>(dyn + kUpRing);           // [2][warps][4][33]
     const int stride = list_stride(a.tokens * a.topk);
-    int16_t* lists = reinterpret_cast<int16_t*>(dyn + kUpRing + a.tiles * kUpSums);
+    int16_t* lists = reinterpret_cast<int16_t*>(dyn + kUpRing + kUpSums);
     MdList list = {lists, lists + stride, lists + 2 * stride, lists + 3 * stride, 0};
     uint32_t* xscales = reinterpret_cast<uint32_t*>(lists + 4 * stride);                    // [tokens][groups]
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -250,11 +248,8 @@ template <int SPLIT> __global__ void __launch_bounds__(kUpThreads, 2) moe_decode
     sort_choices<kUpThreads>(a, list, *reinterpret_cast<MdScratch*>(dyn));
     const uint32_t ring = smem_addr(dyn) + warp * kUpDepth * kMdStage;
     const int q = lane >> 2, t = lane & 3;
-    const int team = warp / kTeam, member = warp % kTeam;
-    const int offset = member / SPLIT * 8, part = member % SPLIT;
-    const int warp_words = a.tiles * 4 * 33;
-    const int items = list.active * blocks, item0 = (int)blockIdx.x * kTeams + team, item_step = (int)gridDim.x * kTeams;
-    const int pass_rows = 8 * a.tiles;
+    const int offset = (warp >> 1) * 8, part = warp & 1;
+    const int items = list.active * blocks, item0 = (int)blockIdx.x, item_step = (int)gridDim.x;
 
     int c_item = item0, c_left_rows = 0, c_col = 0;     // where the copies are
     const uint8_t *upper = nullptr, *lower = nullptr, *line = nullptr;
@@ -273,12 +268,12 @@ template <int SPLIT> __global__ void __launch_bounds__(kUpThreads, 2) moe_decode
     auto issue = [&](uint32_t at) {
         if (c_item < items && part < groups) {
             copy_unit(ring + at, upper, lower, four, line, (int)a.k - c_col);
-            upper += 128 * SPLIT;
-            lower += 128 * SPLIT;
-            line += 512 * SPLIT;
-            c_col += 128 * SPLIT;
+            upper += 256;
+            lower += 256;
+            line += 1024;
+            c_col += 256;
             if (c_col >= (int)a.k) {
-                c_left_rows -= pass_rows;
+                c_left_rows -= 8;
                 if (c_left_rows <= 0) c_item += item_step;
                 aim();
             }
@@ -302,78 +297,54 @@ template <int SPLIT> __global__ void __launch_bounds__(kUpThreads, 2) moe_decode
     for (int item = item0; item < items; item += item_step) {
         const int ai = item / blocks, block = item - ai * blocks;
         const int first = list.start[ai], rows = list.start[ai + 1] - first;
-        for (int r0 = 0; r0 < rows; r0 += pass_rows) {
-            const int left = rows - r0, nt = left > 8 && a.tiles > 1 ? 2 : 1;
+        for (int r0 = 0; r0 < rows; r0 += 8) {
+            const int left = rows - r0, at = first + r0;
             // this lane's column of B, and the scales of its sums' two columns
-            const uint8_t* xb[kMdTiles];
-            uint32_t s0[kMdTiles], s1[kMdTiles];
+            const uint8_t* xb = a.codes + list.token[at + (q < left ? q : 0)] * a.k + part * 128 + t * 8;
+            uint32_t s0 = smem_addr(xscales + list.token[at + (2 * t < left ? 2 * t : 0)] * groups + part);
+            uint32_t s1 = smem_addr(xscales + list.token[at + (2 * t + 1 < left ? 2 * t + 1 : 0)] * groups + part);
+            uint64_t acc[2] = {0, 0};
+            for (int b0 = part * 4; b0 < kb; b0 += 8) {
+                uint2 x[4];
+                if (b0 + 4 <= kb) {
 #pragma unroll
-            for (int i = 0; i < kMdTiles; ++i) {
-                const int rb = i * 8 + q, rd = i * 8 + t * 2, at = first + r0;
-                xb[i] = a.codes + list.token[at + (rb < left ? rb : 0)] * a.k + part * 128 + t * 8;
-                s0[i] = smem_addr(xscales + list.token[at + (rd < left ? rd : 0)] * groups + part);
-                s1[i] = smem_addr(xscales + list.token[at + (rd + 1 < left ? rd + 1 : 0)] * groups + part);
-            }
-            uint64_t acc[kMdTiles][2];
+                    for (int b = 0; b < 4; ++b) x[b] = *reinterpret_cast<const uint2*>(xb + b * 32);
+                } else {
 #pragma unroll
-            for (int i = 0; i < kMdTiles; ++i) acc[i][0] = acc[i][1] = 0;
-            for (int b0 = part * 4; b0 < kb; b0 += 4 * SPLIT) {
-                uint2 x[kMdTiles][4];
-                uint32_t w0[kMdTiles], w1[kMdTiles];
-#pragma unroll
-                for (int i = 0; i < kMdTiles; ++i) {
-                    if (i >= nt) break;
-                    if (b0 + 4 <= kb) {
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) x[i][b] = *reinterpret_cast<const uint2*>(xb[i] + b * 32);
-                    } else {
-#pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            x[i][b] = b0 + b < kb ? *reinterpret_cast<const uint2*>(xb[i] + b * 32) : make_uint2(0u, 0u);
-                    }
-                    xb[i] += 128 * SPLIT;
-                    w0[i] = lds32(s0[i]);
-                    w1[i] = lds32(s1[i]);
-                    s0[i] += 4 * SPLIT;
-                    s1[i] += 4 * SPLIT;
+                    for (int b = 0; b < 4; ++b) x[b] = b0 + b < kb ? *reinterpret_cast<const uint2*>(xb + b * 32) : make_uint2(0u, 0u);
                 }
+                xb += 256;
+                const uint32_t w0 = lds32(s0), w1 = lds32(s1);
+                s0 += 8;
+                s1 += 8;
                 copy_wait<kUpDepth - 2>();
                 __syncwarp();
                 issue(stage == 0 ? (kUpDepth - 1) * kMdStage : stage - kMdStage);
                 Weights w;
                 read_unit(w, ring + stage, (uint32_t)(block & 3) * 4, kb - b0);
+                float c0[4], c1[4];
+                e8m0x4(w0, c0);
+                e8m0x4(w1, c1);
 #pragma unroll
-                for (int i = 0; i < kMdTiles; ++i) {
-                    if (i >= nt) break;
-                    float c0[4], c1[4];
-                    e8m0x4(w0[i], c0);
-                    e8m0x4(w1[i], c1);
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        float d[4];
-                        mma_e4m3(d, w.u[b], w.l[b], x[i][b]);
-                        scaled_add(acc[i], d, w.su[b], w.sl[b], f2_pack(c0[b], c1[b]));
-                    }
+                for (int b = 0; b < 4; ++b) {
+                    float d[4];
+                    mma_e4m3(d, w.u[b], w.l[b], x[b]);
+                    scaled_add(acc, d, w.su[b], w.sl[b], f2_pack(c0[b], c1[b]));
                 }
                 stage = stage + kMdStage < kUpDepth * kMdStage ? stage + kMdStage : 0;
             }
-            float* p = red + (flip * kUpWarps + warp) * warp_words + lane;
+            float v[4];
+            f2_unpack(acc[0], v[0], v[1]);
+            f2_unpack(acc[1], v[2], v[3]);
+            float* p = red + (flip * kUpWarps + warp) * kUpWords + lane;
 #pragma unroll
-            for (int i = 0; i < kMdTiles; ++i)
-                if (i < nt) {
-                    float v[4];
-                    f2_unpack(acc[i][0], v[0], v[1]);
-                    f2_unpack(acc[i][1], v[2], v[3]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) p[(i * 4 + j) * 33] = v[j];
-                }
-            team_sync<SPLIT>(team);
+            for (int j = 0; j < 4; ++j) p[j * 33] = v[j];
+            __syncthreads();
             // a warp takes a row, a lane a feature: the sums, the activation, and the terms of h
-            for (int r = member; r < nt * 8 && r < left; r += kTeam) {
-                const float* s = red + (flip * kUpWarps + team * kTeam + (lane >> 3) * SPLIT) * warp_words +
-                                 ((r >> 3) * 4 + (r & 1)) * 33 + (lane & 7) * 4 + ((r & 7) >> 1);
-                float g = s[0], u = s[66];
-                if (SPLIT == 2) g += s[warp_words], u += s[warp_words + 66];
+            if (warp < left) {
+                const float* s = red + (flip * kUpWarps + (lane >> 3) * 2) * kUpWords +
+                                 (warp & 1) * 33 + (lane & 7) * 4 + (warp >> 1);
+                const float g = s[0] + s[kUpWords], u = s[66] + s[kUpWords + 66];
                 const float h = g / (1.0f + expf(-g)) * u;
                 // the block's largest value goes to [2^14, 2^15): h = (hi + lo) * 2^(byte - 127)
                 uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu) >> 23;
@@ -381,7 +352,7 @@ template <int SPLIT> __global__ void __launch_bounds__(kUpThreads, 2) moe_decode
                 const float v = h * __uint_as_float((268u - top) << 23);
                 const __half hi = __float2half_rn(v);
                 const __half lo = __hisinf(hi) ? __half(0.0f) : __float2half_rn(v - __half2float(hi));
-                const int64_t choice = list.order[first + r0 + r];
+                const int64_t choice = list.order[at + warp];
                 uint16_t* out = a.h + choice * 2 * a.n + block * 32 + lane;
                 out[0] = __half_as_ushort(hi);
                 out[a.n] = __half_as_ushort(lo);
@@ -403,7 +374,7 @@ template <int SPLIT> __global__ void __launch_bounds__(kUpThreads, 2) moe_decode
 // waited for.
 constexpr int kDownThreads = 512;
 constexpr int kDownWarps = kDownThreads / 32;
-constexpr int kDownDepth = 4;
+constexpr int kDownDepth = 3;
 constexpr int kDownRing = kDownWarps * kDownDepth * kMdStage;
 constexpr int kDownMaxCluster = 8;
 
@@ -593,28 +564,21 @@ extern "C" fp8q_status_t mxfp8_moe_decode(const uint8_t* codes, const uint8_t* s
     a.h = static_cast<uint16_t*>(workspace);
     a.hs = reinterpret_cast<uint8_t*>(a.h + (size_t)choices * n * 2);
     a.out = static_cast<uint16_t*>(out_bf16);
-    a.tiles = (choices + 7) / 8 < kMdTiles ? (choices + 7) / 8 : kMdTiles;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     static_assert(kUpRing >= sizeof(MdScratch) && kDownRing >= sizeof(MdScratch), "the sort works where the rings lie");
     static_assert(kDownRing >= kDownMaxCluster * FP8Q_MOE_DECODE_MAX_TOKENS * 16 * sizeof(float), "and the cluster's sums too");
     constexpr size_t kMaxLists = 8 * (kMdMaxChoices + 8);
-    constexpr size_t kMaxUp = kUpRing + kMdTiles * kUpSums + kMaxLists +
+    constexpr size_t kMaxUp = kUpRing + kUpSums + kMaxLists +
                               FP8Q_MOE_DECODE_MAX_TOKENS * (FP8Q_MOE_DECODE_MAX_ROW / 128) * 4;
     constexpr size_t kMaxDown = kDownRing + kDownWarps * 17 * FP8Q_MOE_DECODE_MAX_TOKENS * sizeof(float) + kMaxLists;
     const size_t lists = 8 * (size_t)list_stride(choices);
-    const size_t up_smem = kUpRing + (size_t)a.tiles * kUpSums + lists + (size_t)tokens * (size_t)((k + 127) / 128) * 4;
-    static KernelCache up1_cache, up2_cache, down_cache;
+    const size_t up_smem = kUpRing + kUpSums + lists + (size_t)tokens * (size_t)((k + 127) / 128) * 4;
+    static KernelCache up_cache, down_cache;
     int resident = 0;
     const size_t most = (size_t)(choices < experts ? choices : experts);        // chosen experts
     const size_t items = most * (size_t)(n / 32);
-    fp8q_status_t st;
-    if (items >= 4 * (size_t)sm_count()) {
-        st = prepare_kernel(up1_cache, moe_decode_up_kernel<1>, kUpThreads, kMaxUp, kMaxUp, &resident);
-        if (st == FP8Q_OK) st = launch(moe_decode_up_kernel<1>, grid_for((items + 1) / 2, 2), kUpThreads, up_smem, s, a);
-    } else {
-        st = prepare_kernel(up2_cache, moe_decode_up_kernel<2>, kUpThreads, kMaxUp, kMaxUp, &resident);
-        if (st == FP8Q_OK) st = launch(moe_decode_up_kernel<2>, grid_for(items, 2), kUpThreads, up_smem, s, a);
-    }
+    fp8q_status_t st = prepare_kernel(up_cache, moe_decode_up_kernel, kUpThreads, kMaxUp, kMaxUp, &resident);
+    if (st == FP8Q_OK) st = launch(moe_decode_up_kernel, grid_for(items, kUpBlocks), kUpThreads, up_smem, s, a);
     if (st != FP8Q_OK) return st;
     unsigned ranks = 1;
     while (ranks < kDownMaxCluster && (int64_t)(k / 16) * ranks * 2 <= sm_count()) ranks *= 2;
