@@ -372,18 +372,17 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocks) moe_decode_up_kernel(co
 // to sums of its own, which are joined over the warps and over the cluster's
 // blocks in a fixed order.  The first weights are on their way before h is
 // waited for.
-constexpr int kDownThreads = 512;
-constexpr int kDownWarps = kDownThreads / 32;
 constexpr int kDownDepth = 3;
-constexpr int kDownRing = kDownWarps * kDownDepth * kMdStage;
+__host__ __device__ constexpr int down_ring(int threads) { return threads / 32 * kDownDepth * kMdStage; }
 constexpr int kDownMaxCluster = 8;
 
-__global__ void __launch_bounds__(kDownThreads, 1) moe_decode_down_kernel(const MdArgs a) {
+template <int NT> __global__ void __launch_bounds__(NT, 1) moe_decode_down_kernel(const MdArgs a) {
+    constexpr int kWarps = NT / 32;
     extern __shared__ __align__(16) unsigned char dyn[];
-    float* part = reinterpret_cast<float*>(dyn + kDownRing);        // [warps][tokens][17]
+    float* part = reinterpret_cast<float*>(dyn + down_ring(NT));        // [warps][tokens][17]
     float* gather = reinterpret_cast<float*>(dyn);      // [ranks][tokens][16], in the first block, where its rings were
     const int stride = list_stride(a.tokens * a.topk), sums = a.tokens * 17;
-    int16_t* lists = reinterpret_cast<int16_t*>(part + kDownWarps * sums);
+    int16_t* lists = reinterpret_cast<int16_t*>(part + kWarps * sums);
     MdList list = {lists, lists + stride, lists + 2 * stride, lists + 3 * stride, 0};
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t ranks;
@@ -391,10 +390,10 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_decode_down_kernel(const 
     const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
     // Ids and weights may be read at once: the blocks of the launch before this one let it start only when whatever
     // wrote them had completed.
-    sort_choices<kDownThreads>(a, list, *reinterpret_cast<MdScratch*>(dyn));
+    sort_choices<NT>(a, list, *reinterpret_cast<MdScratch*>(dyn));
     const int64_t f0 = (int64_t)(blockIdx.x / ranks) * 16;
     const int groups = a.hgroups, nb = (int)(a.n / 32);
-    const int units = list.active * groups, shares = (int)ranks * kDownWarps, share = (int)rank * kDownWarps + warp;
+    const int units = list.active * groups, shares = (int)ranks * kWarps, share = (int)rank * kWarps + warp;
     const int lo = (int)((int64_t)units * share / shares), hi = (int)((int64_t)units * (share + 1) / shares);
     const uint32_t ring = smem_addr(dyn) + warp * kDownDepth * kMdStage;
     const int q = lane >> 2, t = lane & 3;
@@ -491,18 +490,18 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_decode_down_kernel(const 
     if (ranks > 1) cluster_sync();                      // the first block's rings are free
     uint32_t to;
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_addr(gather + rank * a.tokens * 16)));
-    for (int i = tid; i < a.tokens * 16; i += kDownThreads) {
+    for (int i = tid; i < a.tokens * 16; i += NT) {
         const float* p = part + (i >> 4) * 17 + (i & 15);
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kDownWarps; ++w) v += p[w * sums];
+        for (int w = 0; w < kWarps; ++w) v += p[w * sums];
         if (ranks > 1) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * i), "f"(v) : "memory");
         else a.out[(int64_t)(i >> 4) * a.k + f0 + (i & 15)] = (uint16_t)pack_bf16x2(v, 0.0f);
     }
     if (ranks == 1) return;
     cluster_sync();
     if (rank != 0) return;
-    for (int i = tid; i < a.tokens * 16; i += kDownThreads) {
+    for (int i = tid; i < a.tokens * 16; i += NT) {
         float v = 0.0f;
         for (uint32_t r = 0; r < ranks; ++r) v += gather[r * a.tokens * 16 + i];
         a.out[(int64_t)(i >> 4) * a.k + f0 + (i & 15)] = (uint16_t)pack_bf16x2(v, 0.0f);
@@ -519,6 +518,20 @@ namespace {
 size_t workspace_of(int64_t tokens, int topk, int64_t n) {
     const size_t choices = (size_t)tokens * (size_t)topk;
     return choices * (size_t)n * 4 + choices * (size_t)((n + 127) / 128) * 4;
+}
+
+// Sixteen warps a block for one or two tokens, whose units last each of them a
+// few steps, twenty beyond (one token 14.8 and 15.6 us, eight 45.6 and 44.5, 32
+// 108.8 and 104.1; twenty-four 15.4, 45.1, 104.6).
+constexpr int64_t kDownFewTokens = 2;
+template <int NT> fp8q_status_t launch_down(const MdArgs& a, unsigned ranks, size_t lists, cudaStream_t stream) {
+    const auto bytes = [&](int tokens, size_t l) { return down_ring(NT) + (size_t)NT / 32 * 17 * tokens * sizeof(float) + l; };
+    static KernelCache cache;
+    int resident = 0;
+    const fp8q_status_t st = prepare_kernel(cache, moe_decode_down_kernel<NT>, NT, down_ring(NT),
+                                            bytes(FP8Q_MOE_DECODE_MAX_TOKENS, 8 * (kMdMaxChoices + 8)), &resident);
+    if (st != FP8Q_OK) return st;
+    return launch_clusters(moe_decode_down_kernel<NT>, (unsigned)(a.k / 16) * ranks, ranks, NT, bytes(a.tokens, lists), stream, a);
 }
 
 bool valid_row(int64_t k) { return k > 0 && k % MXFP8_BLOCK == 0 && k <= FP8Q_MOE_DECODE_MAX_ROW; }
@@ -565,15 +578,14 @@ extern "C" fp8q_status_t mxfp8_moe_decode(const uint8_t* codes, const uint8_t* s
     a.hs = reinterpret_cast<uint8_t*>(a.h + (size_t)choices * n * 2);
     a.out = static_cast<uint16_t*>(out_bf16);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    static_assert(kUpRing >= sizeof(MdScratch) && kDownRing >= sizeof(MdScratch), "the sort works where the rings lie");
-    static_assert(kDownRing >= kDownMaxCluster * FP8Q_MOE_DECODE_MAX_TOKENS * 16 * sizeof(float), "and the cluster's sums too");
+    static_assert(kUpRing >= sizeof(MdScratch) && down_ring(512) >= sizeof(MdScratch), "the sort works where the rings lie");
+    static_assert(down_ring(512) >= kDownMaxCluster * FP8Q_MOE_DECODE_MAX_TOKENS * 16 * sizeof(float), "and the cluster's sums too");
     constexpr size_t kMaxLists = 8 * (kMdMaxChoices + 8);
     constexpr size_t kMaxUp = kUpRing + kUpSums + kMaxLists +
                               FP8Q_MOE_DECODE_MAX_TOKENS * (FP8Q_MOE_DECODE_MAX_ROW / 128) * 4;
-    constexpr size_t kMaxDown = kDownRing + kDownWarps * 17 * FP8Q_MOE_DECODE_MAX_TOKENS * sizeof(float) + kMaxLists;
     const size_t lists = 8 * (size_t)list_stride(choices);
     const size_t up_smem = kUpRing + kUpSums + lists + (size_t)tokens * (size_t)((k + 127) / 128) * 4;
-    static KernelCache up_cache, down_cache;
+    static KernelCache up_cache;
     int resident = 0;
     const size_t most = (size_t)(choices < experts ? choices : experts);        // chosen experts
     const size_t items = most * (size_t)(n / 32);
@@ -582,8 +594,5 @@ extern "C" fp8q_status_t mxfp8_moe_decode(const uint8_t* codes, const uint8_t* s
     if (st != FP8Q_OK) return st;
     unsigned ranks = 1;
     while (ranks < kDownMaxCluster && (int64_t)(k / 16) * ranks * 2 <= sm_count()) ranks *= 2;
-    st = prepare_kernel(down_cache, moe_decode_down_kernel, kDownThreads, kMaxDown, kMaxDown, &resident);
-    if (st != FP8Q_OK) return st;
-    return launch_clusters(moe_decode_down_kernel, (unsigned)(k / 16) * ranks, ranks, kDownThreads,
-                           kDownRing + (size_t)kDownWarps * 17 * tokens * sizeof(float) + lists, s, a);
+    return tokens <= kDownFewTokens ? launch_down<512>(a, ranks, lists, s) : launch_down<640>(a, ranks, lists, s);
 }
