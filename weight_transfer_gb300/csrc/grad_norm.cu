@@ -13,6 +13,14 @@
 // sums, and everything above is binary64 (of which this GPU does two additions
 // a cycle and SM).  Sums outside [2^-80, 2^100] would lose squares to the range
 // of binary32; their elements are summed again in binary64.
+//
+// Both passes are bound by HBM.  A layer of 623 million bf16 gradients takes 182
+// us for its norm (6.85 TB/s; blocks of 256 threads that each read one chunk into
+// registers took 294 to 317).  Eight buckets of 13.1 million, averaged and
+// clipped into others, 97 us: the second reading finds some 40 MB in the
+// second-level cache.  A thousand ragged views into 32-bit buffers, 102 us, as
+// the copies into shared memory leave the output its own alignment (element by
+// element 188).  Fourteen small tensors: 5.4 us in two launches.
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 

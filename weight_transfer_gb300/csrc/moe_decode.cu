@@ -2,11 +2,30 @@
 //
 //     h[t, j] = silu(gate_e x_t) * (up_e x_t)  for token t's choice j, e = ids[t, j]
 //     out[t]  = sum over j of weights[t, j] * (down_e h[t, j])
-// x in MXFP8 rows, the weights as mxfp8_quantize_swizzled writes them; h stays
-// in binary32, and the sum over the choices is rounded once.
+// x in MXFP8 rows, the weights as mxfp8_quantize_swizzled writes them.  Two
+// launches: the gate and up products with the activation, and the down product
+// with the sum.  Between them h is held as two f16 terms with a scale for every
+// 32 of them, 22 bits of each value, which the tensor core multiplies exactly;
+// 16 bits of it in one term would show in the output, binary32 cannot enter the
+// products.  The sum over the choices is rounded once.
 //
-// Two launches: the gate and up products with the activation, and the down
-// product with the sum.
+// Every chosen expert's weights are read once, whatever number of tokens chose
+// it, which is what bounds the layer: 39 MB for one token and 8 of 128 experts of
+// 2048 x 768, 544 MB for 32 tokens.  The products themselves are tiles of 16 rows
+// of weights and 8 columns (mma.sync): with one to four rows of x per expert, the
+// 128 rows and 16 columns of a tcgen05 tile would leave a token's 8 experts to 48
+// of the 152 SMs, and their scales would have to be laid out for each expert.
+// This GPU has no e4m3 form of mma.sync, and converts the operands to f16 before
+// it (12 conversions and two products for each): the warps' own instructions are
+// the second bound, 280 for a unit of 2 KB of weights, issued in 0.65 of all
+// cycles at 32 tokens.
+//     one token 14.6 us, eight (15% of the choices dropped) 44.5 us, 5.6 TB/s,
+//     32 tokens 104 us, 5.2 TB/s; through sort, gather, swiglu, matmul and
+//     combine 22, 58 (none dropped) and 101 us
+// What did not gain: x or h fetched a unit ahead (32 tokens 135 us), x held in
+// shared memory (the same), three blocks per SM with 80 registers (111), partial
+// sums without a barrier (114 where 114), whole K to a warp (117), a lane's units
+// in registers instead of rings (261).
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 
