@@ -2,7 +2,8 @@
 
 Serving (``MoeBlock.forward``): the residual stream is normalized and quantized in one pass, the router picks experts
 from the bf16 rows, the MXFP8 rows travel to their experts, the gate/up and down products read the weights exactly as
-mxfp8_quantize_swizzled wrote them (what a refit ships), and the experts' rows are summed back with the router's weights.
+mxfp8_quantize_swizzled wrote them (what a refit ships), and the experts' rows are summed back with the router's weights.  A few tokens (``MoeBlock.decode``) go through their experts in one call, without
+sorting or carrying rows.
 
 Training (``norm``, ``gather`` and ``combine`` below): the same norm and routing with gradients, around whatever the
 experts compute in bf16.
@@ -38,6 +39,13 @@ class MoeBlock:
         h, h_scales = fp8q.mxfp8_moe_swiglu(rows, row_scales, *self.gate, *self.up, offsets)
         out = fp8q.mxfp8_moe_matmul(h, h_scales, *self.down, offsets)
         return fp8q.fp8q_moe_combine(out, slots, offsets, weights), stream
+
+
+    def decode(self, x: torch.Tensor, residual: torch.Tensor):
+        """forward() for a few tokens (at most FP8Q_MOE_DECODE_MAX_TOKENS): the experts in one call."""
+        codes, scales, stream, y, _ = fp8q.mxfp8_rmsnorm_quantize(x, self.norm, self.eps, residual=residual, want_bf16=True)
+        score, ids = torch.topk((y @ self.router.T).float(), self.topk, dim=1)
+        return fp8q.mxfp8_moe_decode(codes, scales, ids, torch.softmax(score, 1), *self.gate, *self.up, *self.down), stream
 
 
 class _Norm(torch.autograd.Function):
@@ -129,6 +137,10 @@ def main():
     err = (out.float() - ref.float()).norm() / ref.float().norm()
     print(f"{tokens} tokens, {experts} experts, top {topk}: MXFP8 block against bf16 experts: relative difference {err:.4f}")
     assert torch.equal(stream, ref_stream) and err < 0.1
+    few, few_stream = block.decode(x[:8], residual[:8])
+    err = (few.float() - out[:8].float()).norm() / out[:8].float().norm()
+    print(f"8 tokens in one call against the same through the sorted path: relative difference {err:.4f}")
+    assert torch.equal(few_stream, stream[:8]) and err < 0.05
     leaves = [t.clone().requires_grad_() for t in (x, residual, norm_w)]
     y, _ = train_block(*leaves, router, gate, up, down, topk)
     y.float().square().mean().backward()

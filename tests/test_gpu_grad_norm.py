@@ -239,6 +239,25 @@ def test_captured_on_another_stream_and_two_at_once():
         check_norm(nb, None, b, math.inf, 1.0)
 
 
+def test_a_long_list_captured():
+    """More tensors than the small table holds, and than one table holds: each node of the graph keeps its own."""
+    for count in (65, 1500):
+        sizes = [100 + i % 7 for i in range(count)]
+        g, flat = views(sizes, [torch.float32] * count, seed=count)
+        outs, oflat = views(sizes, [torch.bfloat16] * count, seed=1)
+        want, want_each = w.fp8q_grad_clip(g, 0.01, 0.5, outs=outs, want_each=True)
+        want_flat = oflat[torch.bfloat16].clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got, each = w.fp8q_grad_clip(w.fp8q_grad_list(g, outs), 0.01, 0.5, want_each=True)
+        w.fp8q_grad_norm(views([50] * 2000, [torch.float32] * 2000, seed=9)[0])      # another list in between
+        oflat[torch.bfloat16].zero_(), got.zero_(), each.zero_()
+        graph.replay()
+        assert torch.equal(got, want) and torch.equal(each, want_each)
+        n = sum(sizes)
+        assert torch.equal(oflat[torch.bfloat16][:n], want_flat[:n])
+
+
 def test_refusals_of_the_binding():
     a, b = torch.ones(10, device="cuda"), torch.ones(10, device="cuda", dtype=torch.float16)
     for bad in ([b], [a.view(2, 5).T]):

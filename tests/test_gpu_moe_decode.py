@@ -96,6 +96,12 @@ def test_shapes(n, k):
         check(layer(tokens, topk, experts, n, k, seed=n + k + tokens))
 
 
+@pytest.mark.parametrize("n,k", [(32, 16384), (16384, 32), (2560, 8192)])
+def test_long_rows(n, k):
+    for tokens in (1, 32):
+        check(layer(tokens, 2, 3, n, k, seed=n))
+
+
 @pytest.mark.parametrize("tokens", [1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 17, 31, 32])
 @pytest.mark.parametrize("topk,experts", [(1, 1), (2, 4), (6, 60)])
 def test_tokens(tokens, topk, experts):
