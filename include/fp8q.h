@@ -10,7 +10,7 @@
  *
  * Pointer rules common to all entry points:
  *  - data pointers are DEVICE pointers owned by the caller, 16-byte aligned
- *    (FP8Q_ERR_ALIGN otherwise);
+ *    (FP8Q_ERR_ALIGN otherwise) unless an entry point says so;
  *  - an output may not overlap an input or another output (FP8Q_ERR_ALIAS),
  *    except where an entry point says so;
  *  - bf16 arrays hold IEEE binary32 values truncated to their upper 16 bits
@@ -54,8 +54,9 @@ typedef enum {
     FP8Q_ERR_NULL = 1,   /* a required pointer is NULL                        */
     FP8Q_ERR_SIZE = 2,   /* a size is negative or beyond FP8Q_MAX_ELEMENTS    */
     FP8Q_ERR_ALIGN = 3,  /* a pointer is not 16-byte aligned                  */
-    FP8Q_ERR_FORMAT = 4, /* unknown fp8q_format_t, or expert ids of a width
-                            other than 4 or 8 bytes                           */
+    FP8Q_ERR_FORMAT = 4, /* unknown fp8q_format_t or fp8q_float_t, ids of a width
+                            other than 4 or 8 bytes, logits other than 2 or 4,
+                            or memory that holds no plan                      */
     FP8Q_ERR_K = 5,      /* a count outside its limits (shards, ranks, choices
                             per token), or a row length that is no positive
                             multiple of what the entry point asks for, or
@@ -510,7 +511,10 @@ fp8q_status_t mxfp8_moe_swiglu(const uint8_t* codes, const uint8_t* scales, int6
  *     h[t, j] = g / (1 + exp(-g)) * u,   g, u = the gate's and the up weights' products with x[t]
  *     out[t]  = RNE_bf16(sum over j of weights[t, j] * (down weights' product with h[t, j]))
  * x in MXFP8 rows as for the products above.  h is not quantized, so that the
- * result lies nearer to the formula than swiglu, matmul and combine together.
+ * result lies nearer to the formula than swiglu, matmul and combine together:
+ * it is held as two f16 terms under a scale per 32 values, 2^-22 of a value.
+ * The products are exact, their sums binary32; an infinite h gives NaN or
+ * infinities.
  * Choices whose id lies outside [0, experts) are left out; a token without any
  * gives zeros.  The same id may stand twice in a token.
  *   codes, scales : tokens * k codes, row-major [tokens, k / 32] E8M0 bytes
