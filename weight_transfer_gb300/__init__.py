@@ -976,6 +976,10 @@ def mxfp8_moe_swiglu(codes: torch.Tensor, scales: torch.Tensor, gate_codes: torc
     return out_codes, out_scales
 
 
+def _cuda(index: int) -> torch.device:
+    return torch.device("cuda", index)
+
+
 def _current_device() -> int:
     # the index alone: torch.cuda.current_device() takes three times as long
     return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
@@ -1018,10 +1022,9 @@ def _held(t: Optional[torch.Tensor], what: str, dtype, numel: int, device: int) 
 
 def _made(t: Optional[torch.Tensor], what: str, dtype, shape, numel: int, like: torch.Tensor, device: int, stream):
     """(tensor, pointer) of an output: the caller's, checked, or a new one."""
-    if t is None:
-        t = torch.empty(shape, dtype=dtype, device=like.device) if stream is None else _new(shape, dtype, like.device, stream)
-        return t, t.data_ptr()
-    return t, _held(t, what, dtype, numel, device)
+    if t is not None and t.get_device() != device:
+        raise ValueError(f"{what} is on {t.device}, other tensors of the call on cuda:{device}")
+    return _out(t, what, dtype, shape, like.device, numel, stream)
 
 
 def _ids(t: torch.Tensor, what: str, shape, device: int) -> tuple:
@@ -1068,8 +1071,7 @@ def mxfp8_moe_decode(codes: torch.Tensor, scales: torch.Tensor, ids: torch.Tenso
     out, op = _made(out, "out", torch.bfloat16, (tokens, k), tokens * k, codes, d, stream)
     if workspace is None:
         have = _lib.mxfp8_moe_decode_workspace_bytes(tokens, topk, n)
-        workspace = torch.empty(have, dtype=u8, device=codes.device) if stream is None else _new(have, u8, codes.device, stream,
-                                                                                                 kept=False)
+        workspace = _new(have, u8, codes.device, stream, kept=False)
         bp = workspace.data_ptr()
     else:
         have = workspace.numel() * workspace.element_size()
@@ -1137,10 +1139,9 @@ def _like_rows(logits: torch.Tensor, ptr: int, size: int, rows: int, vocab: int,
     per = 16 // size
     apart = vocab + (stride - vocab) % per
     shift = ptr % 16 // size
-    if shift == 0 and stream is None:
-        return torch.empty_strided((rows, vocab), (apart, 1), dtype=logits.dtype, device=logits.device)
-    flat = _new(rows * apart + shift, logits.dtype, logits.device, stream)
-    return flat[shift:].as_strided((rows, vocab), (apart, 1))
+    if apart == vocab and shift == 0:
+        return _new((rows, vocab), logits.dtype, logits.device, stream)
+    return _new(rows * apart + shift, logits.dtype, logits.device, stream).as_strided((rows, vocab), (apart, 1), shift)
 
 
 def fp8q_token_logprobs_backward(logits: torch.Tensor, targets: Optional[torch.Tensor], stats: torch.Tensor,
@@ -1219,25 +1220,22 @@ class fp8q_grad_list:
 
 def _grad_call(name: str, grads, max_norm, scale, want_each, norm, each, workspace, stream):
     d = _current_device()
-    dev = torch.device("cuda", d)
-    if grads.count and grads.device != dev:
-        raise ValueError(f"the gradients are on {grads.device}, which is not the current device")
+    dev = grads.device if grads.count else _cuda(d)
+    if dev.index != d:
+        raise ValueError(f"the gradients are on {dev}, which is not the current device")
     f32 = torch.float32
     if norm is None:
-        norm = torch.empty(2, dtype=f32, device=dev) if stream is None else _new(2, f32, dev, stream)
-        np_ = norm.data_ptr()
+        norm, np_ = _out(None, "norm", f32, (2,), dev, 2, stream)
     else:
         np_ = _held(norm, "norm", f32, 2, d)
     ep = None
     if each is not None:
         ep = _held(each, "each", f32, grads.count, d)
     elif want_each:
-        each = _new(grads.count, f32, dev, stream)
-        ep = each.data_ptr()
+        each, ep = _out(None, "each", f32, (grads.count,), dev, grads.count, stream)
     have = grads.workspace_bytes
     if workspace is None:
-        workspace = torch.empty(have, dtype=torch.uint8, device=dev) if stream is None else _new(have, torch.uint8, dev, stream,
-                                                                                                 kept=False)
+        workspace = _new(have, torch.uint8, dev, stream, kept=False)
         wp = workspace.data_ptr()
     else:
         have = workspace.numel() * workspace.element_size()
