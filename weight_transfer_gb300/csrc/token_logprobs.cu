@@ -18,7 +18,7 @@
 // with entropy (6.64 TB/s; scalar arithmetic on unpacked logits, 12 instructions
 // each instead of 5, took 261), 370 us for the gradient (6.72 TB/s; 400 with a
 // comparison with the target at every logit).  256 rows of 151,669 binary32
-// logits with five alternatives: 38 us, without them 27.  Four rows: 9.2 us, of
+// logits with five alternatives: 38 us, without them 27.  Four rows: 8.9 us, of
 // which the launch and the joins are most.
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
@@ -312,6 +312,7 @@ struct __align__(16) WarpTop {
 template <int NT> struct LpTopShared {
     WarpTop warp[NT / 32];
     uint64_t gather[kLpGather];
+    uint64_t parts[kLpGather];  // what the blocks of a cluster found, in the first of them
     uint64_t sorted[kLpMaxTop];
     float group[64];
     int list[kLpGather];
@@ -577,7 +578,6 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
     if (warp == 0) acc = join_parts(sh.warp, NT / 32, a.c);
     if (ranks > 1) {
         cluster_wait();                              // the first block has started
-        if (TOP) cluster_sync();                     // and no longer reads what it gathered from its warps
         if (tid == 0) {
             const uint32_t to = map_rank0(&sh.part[rank]);
             st_cluster_f32(to, acc.m);
@@ -585,11 +585,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
             st_cluster_f32(to + 8, acc.e);
             st_cluster_f32(to + 12, acc.top);
         }
-        if (TOP && tid < a.top) st_cluster_u64(map_rank0(&t.gather[rank * a.top + tid]), t.sorted[tid]);
+        if (TOP && tid < a.top) st_cluster_u64(map_rank0(&t.parts[rank * a.top + tid]), t.sorted[tid]);
         cluster_sync();
         if (rank != 0) return;
         if (warp == 0) acc = join_parts(sh.part, (int)ranks, a.c);
-        if (TOP) sort_top<NT>(t.gather, (int)ranks * a.top, a.top, t.sorted);
+        if (TOP) sort_top<NT>(t.parts, (int)ranks * a.top, a.top, t.sorted);
     }
     if (tid == 0) {
         // a row of -inf alone has no distribution: its scores are -inf, its entropy 0
@@ -643,7 +643,11 @@ struct LpGradArgs {
     unsigned parts;             // blocks per row
 };
 
-constexpr int kLpGradThreads = 256;
+// Blocks of 128 threads with four vectors each: a narrower window of memory on
+// its way than with 256 threads (score_grad_long 387.7 us where 392.5, 512
+// threads 443; two vectors 452, eight 395).
+constexpr int kLpGradThreads = 128;
+constexpr int kLpGradUnroll = 4;
 
 // A block takes one part of one row.  VEC: the rows of logits and dlogits lie
 // alike relative to 16-byte boundaries.
@@ -701,15 +705,15 @@ __global__ void __launch_bounds__(kLpGradThreads) token_logprobs_backward_kernel
     const uint32_t low = BYTES == 2 ? pack_bf16x2(lowest, lowest) : __float_as_uint(lowest);
     const uint64_t c2 = f2_pack(a.c, a.c), m2 = f2_pack(-m, -m), shift2 = f2_pack(shift, shift);
     const uint64_t base2 = f2_pack(base, base), slope2 = f2_pack(slope, slope);
-    for (int64_t b = v0; b < v1; b += (int64_t)NT * kLpUnroll) {
-        uint4 v[kLpUnroll];
+    for (int64_t b = v0; b < v1; b += (int64_t)NT * kLpGradUnroll) {
+        uint4 v[kLpGradUnroll];
 #pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u) {
+        for (int u = 0; u < kLpGradUnroll; ++u) {
             const int64_t i = b + u * NT + tid;
             if (i < v1 && !zero) v[u] = ld_once(body + 16 * i);     // dlogits may be the logits themselves
         }
 #pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u) {
+        for (int u = 0; u < kLpGradUnroll; ++u) {
             const int64_t i = b + u * NT + tid;
             if (i >= v1) break;
             float f[per];
@@ -809,7 +813,7 @@ template <int BYTES> fp8q_status_t launch_logprobs_kind(const LpArgs& a, int64_t
 }
 
 template <int BYTES> fp8q_status_t launch_backward(LpGradArgs a, bool vec, cudaStream_t stream) {
-    const int64_t per_block = (int64_t)kLpGradThreads * kLpUnroll * 16 / BYTES;
+    const int64_t per_block = (int64_t)kLpGradThreads * kLpGradUnroll * 16 / BYTES;
     int64_t parts = (a.vocab + per_block - 1) / per_block;
     const int64_t most = 0x7FFFFFFFll / a.rows;
     a.parts = (unsigned)(parts < most ? parts : most);
