@@ -592,8 +592,9 @@ fp8q_status_t fp8q_token_logprobs_backward(const void* logits, int logit_bytes, 
  * `scale` is what the gradients are to be multiplied by anyway: 1 / ranks
  * where they are the ranks' sum (fp8q_dequant_reduce).  Squares are summed in
  * binary32 by 2048 (11 additions deep, then 5) and in binary64 above, over any
- * magnitude and in a fixed order.  NaN and infinities are not looked for: a NaN anywhere makes the norm
- * and all clipped gradients NaN; an infinite norm makes norm[1] 0.
+ * magnitude and in a fixed order.  NaN and infinities are not looked for: a NaN
+ * anywhere makes the norm and all clipped gradients NaN; an infinite norm makes
+ * norm[1] 0, and NaN where max_norm is infinite as well.
  *
  * fp8q_grad_plan (host only, no GPU) checks a list of tensors and lays it out
  * for the calls below, in caller-owned HOST memory of fp8q_grad_plan_bytes(count)

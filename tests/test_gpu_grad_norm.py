@@ -271,3 +271,21 @@ def test_refusals_of_the_binding():
         w.fp8q_grad_clip([a], 0.0)
     with pytest.raises(ValueError, match="has its outputs"):
         w.fp8q_grad_clip(w.fp8q_grad_list([a]), 1.0, outs=[a])
+
+
+@pytest.mark.parametrize("scale,factor", [(1e300, 0.0), (1e-300, 0.0), (1.0 / 3.0, None)])
+def test_scale_beyond_binary32(scale, factor):
+    """The factor is RN(scale * coefficient) of a scale in binary64: the coefficient of 1e300 is 0, and so is the
+    factor; with 1e-300 the factor rounds to 0; with 1/3 it is rounded once."""
+    g, _ = views([1000], [torch.float32], seed=5)
+    before = g[0].clone()
+    norm, _ = w.fp8q_grad_clip(g, 1e30, scale)
+    want = torch.tensor(scale * float(norm[1]), dtype=torch.float64).float() if factor is None else torch.tensor(factor)
+    assert torch.equal(g[0], before * want.cuda())
+
+
+def test_infinite_norm_and_limit():
+    """inf / inf: the coefficient of an infinite norm is 0 for any finite limit and NaN without one."""
+    g = [torch.tensor([1.0, math.inf], device="cuda")]
+    assert float(w.fp8q_grad_norm(g, 2.0)[0][1]) == 0.0
+    assert math.isnan(float(w.fp8q_grad_norm(g)[0][1]))

@@ -192,6 +192,14 @@ struct Piece {
     int f32, last;              // last piece of its chunk
 };
 
+// Before the block's shared memory is given up: lets the copies of the ring
+// land that were issued before stage s of this round, but for those of stage
+// `taken`, which the summing warps have had.
+__device__ __noinline__ void land(uint64_t* full, uint32_t round, int s, int taken = -1) {
+    for (int i = 0; i < kStages; ++i)
+        if (i != taken && (i < s || round > 0)) mbar_wait(&full[i], (i < s ? round : round - 1) & 1);
+}
+
 // One block per SM walks over the chunks.  A warp of its own copies them, 32 KB
 // at a time, into a ring of stages; eight warps sum.  A warp's sum of a chunk
 // waits in the chunk's last stage, where the copying warp joins the eight when
@@ -253,7 +261,7 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_squares_kernel(cons
             for (bool first = true; first || left > 0; first = false) {
                 const int v = (int)(left < kPiece / 16 ? left : kPiece / 16);
                 left -= v;
-                if (!take()) return;
+                if (!take()) return land(full, round, s);
                 Piece& m = info[s];
                 m.tensor = t.grad[at.tensor];
                 m.head = first ? at.head : 0;
@@ -269,12 +277,14 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_squares_kernel(cons
                 next(left == 0 ? (int64_t)c : -1);
             }
         }
-        if (!take()) return;
+        if (!take()) return land(full, round, s);
         info[s].vecs = -1;
         mbar_arrive_expect_tx(&full[s], 0);
+        const uint32_t end_round = round;
+        const int end = s;
         for (int i = 1; i < kStages; ++i) {             // the stages still on their way
             next(-1);
-            if (!take()) return;
+            if (!take()) return land(full, end_round, end, end);
         }
         return;
     }
@@ -422,7 +432,7 @@ template <int IN, int OUT> __device__ __forceinline__ void scale_stage(const uns
 // Reading through shared memory lets the output have its own alignment.
 template <int N>
 __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_scale_kernel(const __grid_constant__ GradTableN<N> t, uint32_t chunks,
-                                                                          int64_t chunk_bytes, float scale, const float* norm) {
+                                                                          int64_t chunk_bytes, double scale, const float* norm) {
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ ScalePiece info[kStages];
@@ -437,7 +447,7 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_scale_kernel(const 
     __syncthreads();
     dependency_wait();
     allow_dependents();
-    const float f = scale * __ldcg(norm + 1);
+    const float f = (float)(scale * (double)__ldcg(norm + 1));
     if (warp == kGradThreads / 32) {
         if (lane != 0) return;
         const uint64_t drop = evict_first();
@@ -458,7 +468,7 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_scale_kernel(const 
             for (bool first = true; first || left > 0; first = false) {
                 const int v = (int)(left < kPiece / 16 ? left : kPiece / 16);
                 left -= v;
-                if (!take()) return;
+                if (!take()) return land(full, round, s);
                 info[s] = {t.grad[at.tensor], out, element, (int64_t)(t.kind[at.tensor] & kCountMask) - at.tails,
                            first ? at.head : 0, left == 0 ? at.tails : 0, v, 2 * at.f32 + out32};
                 mbar_arrive_expect_tx(&full[s], (uint32_t)v * 16);
@@ -468,10 +478,10 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_scale_kernel(const 
                 if (++s == kStages) s = 0, ++round;
             }
         }
-        if (!take()) return;
+        if (!take()) return land(full, round, s);
         info[s].vecs = -1;
         mbar_arrive_expect_tx(&full[s], 0);
-        return;
+        return land(full, round, s, s);
     }
     uint32_t parity = 0;
     for (int s = 0;;) {
@@ -635,7 +645,7 @@ fp8q_status_t grad_entry(const void* plan_memory, double scale, double max_norm,
         st = with_table(tables(plan_memory)[g], [&](const auto& t) {
             const uint32_t chunks = t.first[t.count];
             constexpr int N = std::decay_t<decltype(t)>::kSize;
-            return chunks ? launch_ring<grad_scale_kernel<N>>(chunks, stream, t, chunks, plan.chunk_bytes, (float)scale,
+            return chunks ? launch_ring<grad_scale_kernel<N>>(chunks, stream, t, chunks, plan.chunk_bytes, scale,
                                                               (const float*)norm)
                           : FP8Q_OK;
         });
