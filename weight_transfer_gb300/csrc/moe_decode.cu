@@ -30,6 +30,7 @@
 #include "fp8q_host.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace fp8q {
 
@@ -50,15 +51,7 @@ struct MdArgs {
 };
 
 // ------------------------------------------------------------ building blocks ----
-// D = A * B for 16 rows, 32 columns of K and 8 columns, e4m3 codes.  The order
-// of K is free as long as A and B share it: lane 4 r + t holds bytes 8 t .. 8 t
-// + 7 of the block of 32 for rows r and r + 8 of A and column r of B.
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint2 a0, uint2 a1, uint2 b) {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0.x), "r"(a1.x), "r"(a0.y), "r"(a1.y), "r"(b.x), "r"(b.y), "f"(0.0f));
-}
-// The same for 16 columns of K and f16 operands: A's codes as f16, exactly.
+// D += A * B for 16 rows, 16 columns of K and 8 columns, in f16.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -70,12 +63,29 @@ __device__ __forceinline__ uint32_t e4m3_f16(uint32_t two) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
     return r;
 }
-// Four E8M0 bytes -> 2^(byte - 127) each, NaN for 255.
-__device__ __forceinline__ void e8m0x4(uint32_t w, float (&f)[4]) {
-    uint32_t a, b;
-    asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(a) : "h"((uint16_t)w));
-    asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(w >> 16)));
-    f[0] = bf16_lo(a); f[1] = bf16_hi(a); f[2] = bf16_lo(b); f[3] = bf16_hi(b);
+// Products of 16 rows of weights with 8 columns over a block of 32, exact.  The
+// order of K is free as long as A and B share it: lane 4 r + t holds bytes 8 t ..
+// 8 t + 7 of the block for rows r and r + 8 of A and column r of B, the latter
+// as f16.
+__device__ __forceinline__ void mma_block(float (&d)[4], uint2 a0, uint2 a1, uint4 b) {
+    d[0] = d[1] = d[2] = d[3] = 0.0f;
+    mma_f16(d, e4m3_f16(a0.x), e4m3_f16(a1.x), e4m3_f16(a0.x >> 16), e4m3_f16(a1.x >> 16), b.x, b.y);
+    mma_f16(d, e4m3_f16(a0.y), e4m3_f16(a1.y), e4m3_f16(a0.y >> 16), e4m3_f16(a1.y >> 16), b.z, b.w);
+}
+// Byte i of each of two words of E8M0 scales -> 2^(byte - 127), NaN for 255.
+__device__ __forceinline__ void e8m0_of(uint32_t a, uint32_t b, int i, float& x, float& y) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"((uint16_t)__byte_perm(a, b, (uint32_t)(i | (i + 4) << 4))));
+    x = bf16_lo(r);
+    y = bf16_hi(r);
+}
+// v[i], i below P.
+template <int P> __device__ __forceinline__ float pick(const float (&v)[4], int i) {
+    if (P == 1) return v[0];
+    const float lo = i & 1 ? v[1] : v[0];
+    if (P == 2) return lo;
+    const float hi = i & 1 ? v[3] : v[2];
+    return i & 2 ? hi : lo;
 }
 // 16 bytes global -> shared, past the first-level cache.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -92,11 +102,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 r;
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
     return r;
-}
-// acc += (d * row) * column for a tile's sums over one block of 32: rows' scales a and b, columns' c.
-__device__ __forceinline__ void scaled_add(uint64_t (&acc)[2], const float (&d)[4], float a, float b, uint64_t c) {
-    acc[0] = f2_fma(f2_mul(f2_pack(d[0], d[1]), f2_pack(a, a)), c, acc[0]);
-    acc[1] = f2_fma(f2_mul(f2_pack(d[2], d[3]), f2_pack(b, b)), c, acc[1]);
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t r;
@@ -221,7 +226,7 @@ __device__ __forceinline__ void copy_unit(uint32_t stage, const uint8_t* upper, 
 // from `nblocks` on may be anything and become 0, as the codes there are.
 struct Weights {
     uint2 u[4], l[4];
-    float su[4], sl[4];
+    uint32_t su, sl;
 };
 __device__ __forceinline__ uint32_t only(uint32_t scales, int nblocks) {
     return nblocks < 4 ? scales & ((1u << (8 * nblocks)) - 1u) : scales;
@@ -229,8 +234,8 @@ __device__ __forceinline__ uint32_t only(uint32_t scales, int nblocks) {
 __device__ __forceinline__ void read_unit(Weights& w, uint32_t stage, uint32_t word, int nblocks) {
     const int lane = (int)(threadIdx.x & 31u), q = lane >> 2, t = lane & 3;
     const uint32_t scales = stage + kMdScales + q * 16 + word, row = stage + q * kMdRow + t * 8;
-    e8m0x4(only(lds32(scales), nblocks), w.su);
-    e8m0x4(only(lds32(scales + 128), nblocks), w.sl);
+    w.su = only(lds32(scales), nblocks);
+    w.sl = only(lds32(scales + 128), nblocks);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
         const uint32_t at = row + ((b ^ (q & 3)) << 5);
@@ -245,6 +250,10 @@ __device__ __forceinline__ void read_unit(Weights& w, uint32_t stage, uint32_t w
 // so that a lane gets both sums of a feature.  The two take turns at the groups
 // of 128 columns.  A tensor-core tile's columns are 8 rows of x; columns
 // without a row repeat the first one's data, and their sums are not read.
+//   Up to four or two rows leave room for P = 2 or 4 blocks of 32 in the columns:
+// those of block b are P-th parts of a tile, of which a product with the weights
+// of one block gives one part.  A lane takes its part from each product, and
+// scales and adds one sum instead of P.
 constexpr int kUpThreads = 256;
 constexpr int kUpWarps = kUpThreads / 32;
 constexpr int kUpDepth = 3;
@@ -318,40 +327,61 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocks) moe_decode_up_kernel(co
         const int first = list.start[ai], rows = list.start[ai + 1] - first;
         for (int r0 = 0; r0 < rows; r0 += 8) {
             const int left = rows - r0, at = first + r0;
-            // this lane's column of B, and the scales of its sums' two columns
-            const uint8_t* xb = a.codes + list.token[at + (q < left ? q : 0)] * a.k + part * 128 + t * 8;
-            uint32_t s0 = smem_addr(xscales + list.token[at + (2 * t < left ? 2 * t : 0)] * groups + part);
-            uint32_t s1 = smem_addr(xscales + list.token[at + (2 * t + 1 < left ? 2 * t + 1 : 0)] * groups + part);
             uint64_t acc[2] = {0, 0};
-            for (int b0 = part * 4; b0 < kb; b0 += 8) {
-                uint2 x[4];
-                if (b0 + 4 <= kb) {
+            auto multiply = [&](auto packed) {
+                constexpr int P = decltype(packed)::value, R = 8 / P;       // blocks in the columns, rows of x
+                // this lane's column of B, and its sums' two columns, whose rows are 2 t and 2 t + 1 modulo R
+                const int xr = q % R, r = 2 * t % R, xblock = q / R, sblock = t * P / 4;
+                const uint8_t* xb = a.codes + list.token[at + (xr < left ? xr : 0)] * a.k + (part * 4 + xblock) * 32 + t * 8;
+                uint32_t s0 = smem_addr(xscales + list.token[at + (r < left ? r : 0)] * groups + part);
+                uint32_t s1 = smem_addr(xscales + list.token[at + (r + 1 < left ? r + 1 : 0)] * groups + part);
+                for (int b0 = part * 4; b0 < kb; b0 += 8) {
+                    uint2 x[4 / P];
+                    if (b0 + 4 <= kb) {
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) x[b] = *reinterpret_cast<const uint2*>(xb + b * 32);
-                } else {
+                        for (int i = 0; i < 4 / P; ++i) x[i] = *reinterpret_cast<const uint2*>(xb + i * P * 32);
+                    } else {
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) x[b] = b0 + b < kb ? *reinterpret_cast<const uint2*>(xb + b * 32) : make_uint2(0u, 0u);
+                        for (int i = 0; i < 4 / P; ++i)
+                            x[i] = b0 + i * P + xblock < kb ? *reinterpret_cast<const uint2*>(xb + i * P * 32) : make_uint2(0u, 0u);
+                    }
+                    xb += 256;
+                    const uint32_t w0 = lds32(s0), w1 = lds32(s1);
+                    s0 += 8;
+                    s1 += 8;
+                    copy_wait<kUpDepth - 2>();
+                    __syncwarp();
+                    issue(stage == 0 ? (kUpDepth - 1) * kMdStage : stage - kMdStage);
+                    Weights w;
+                    read_unit(w, ring + stage, (uint32_t)(block & 3) * 4, kb - b0);
+#pragma unroll
+                    for (int i = 0; i < 4 / P; ++i) {
+                        const uint4 f = make_uint4(e4m3_f16(x[i].x), e4m3_f16(x[i].x >> 16), e4m3_f16(x[i].y), e4m3_f16(x[i].y >> 16));
+                        float d[4][4], su, sl, c0, c1;
+#pragma unroll
+                        for (int b = 0; b < P; ++b) {
+                            float v[4];
+                            mma_block(v, w.u[i * P + b], w.l[i * P + b], f);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) d[j][b] = v[j];
+                        }
+                        e8m0_of(w.su, w.sl, i * P + sblock, su, sl);
+                        e8m0_of(w0, w1, i * P + sblock, c0, c1);
+                        const uint64_t c = f2_pack(c0, c1), up = f2_pack(su, su), lo = f2_pack(sl, sl);
+                        acc[0] = f2_fma(f2_mul(f2_pack(pick<P>(d[0], sblock), pick<P>(d[1], sblock)), up), c, acc[0]);
+                        acc[1] = f2_fma(f2_mul(f2_pack(pick<P>(d[2], sblock), pick<P>(d[3], sblock)), lo), c, acc[1]);
+                    }
+                    stage = stage + kMdStage < kUpDepth * kMdStage ? stage + kMdStage : 0;
                 }
-                xb += 256;
-                const uint32_t w0 = lds32(s0), w1 = lds32(s1);
-                s0 += 8;
-                s1 += 8;
-                copy_wait<kUpDepth - 2>();
-                __syncwarp();
-                issue(stage == 0 ? (kUpDepth - 1) * kMdStage : stage - kMdStage);
-                Weights w;
-                read_unit(w, ring + stage, (uint32_t)(block & 3) * 4, kb - b0);
-                float c0[4], c1[4];
-                e8m0x4(w0, c0);
-                e8m0x4(w1, c1);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    float d[4];
-                    mma_e4m3(d, w.u[b], w.l[b], x[b]);
-                    scaled_add(acc, d, w.su[b], w.sl[b], f2_pack(c0[b], c1[b]));
+                for (int o = 4 / P; o < 4; o <<= 1) {
+                    acc[0] = f2_add(acc[0], __shfl_xor_sync(0xFFFFFFFFu, acc[0], o));
+                    acc[1] = f2_add(acc[1], __shfl_xor_sync(0xFFFFFFFFu, acc[1], o));
                 }
-                stage = stage + kMdStage < kUpDepth * kMdStage ? stage + kMdStage : 0;
-            }
+            };
+            if (left <= 2) multiply(std::integral_constant<int, 4>());
+            else if (left <= 4) multiply(std::integral_constant<int, 2>());
+            else multiply(std::integral_constant<int, 1>());
             float v[4];
             f2_unpack(acc[0], v[0], v[1]);
             f2_unpack(acc[1], v[2], v[3]);
@@ -461,39 +491,56 @@ template <int NT> __global__ void __launch_bounds__(NT, 1) moe_decode_down_kerne
         const int first = list.start[ai], rows = list.start[ai + 1] - first;
         for (int r0 = 0; r0 < rows; r0 += 4) {
             const int left = rows - r0, at = first + r0;
-            const int choice = list.order[at + (t < left ? t : 0)];
-            const uint16_t* hb = a.h + ((int64_t)list.order[at + ((q >> 1) < left ? q >> 1 : 0)] * 2 + (q & 1)) * a.n + g0 * 128 + t * 8;
-            const uint32_t* sb = reinterpret_cast<const uint32_t*>(a.hs) + (int64_t)choice * groups;
             float upper_sum = 0.0f, lower_sum = 0.0f;
-            for (int g = g0; g < g1; ++g, hb += 128) {
-                uint4 x[4];
-                if (g * 4 + 4 <= nb) {
+            int choice = 0;
+            auto multiply = [&](auto packed) {
+                constexpr int P = decltype(packed)::value, R = 4 / P;       // blocks in the columns, rows of h
+                const int hr = (q >> 1) % R, r = t % R, hblock = (q >> 1) / R, sblock = t / R;
+                choice = list.order[at + (r < left ? r : 0)];
+                const uint16_t* hb = a.h + ((int64_t)list.order[at + (hr < left ? hr : 0)] * 2 + (q & 1)) * a.n + g0 * 128 + hblock * 32 + t * 8;
+                const uint32_t* sb = reinterpret_cast<const uint32_t*>(a.hs) + (int64_t)choice * groups;
+                for (int g = g0; g < g1; ++g, hb += 128) {
+                    uint4 x[4 / P];
+                    if (g * 4 + 4 <= nb) {
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) x[b] = *reinterpret_cast<const uint4*>(hb + b * 32);
-                } else {
+                        for (int i = 0; i < 4 / P; ++i) x[i] = *reinterpret_cast<const uint4*>(hb + i * P * 32);
+                    } else {
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        x[b] = g * 4 + b < nb ? *reinterpret_cast<const uint4*>(hb + b * 32) : make_uint4(0u, 0u, 0u, 0u);
+                        for (int i = 0; i < 4 / P; ++i)
+                            x[i] = g * 4 + i * P + hblock < nb ? *reinterpret_cast<const uint4*>(hb + i * P * 32) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    const uint32_t c = only(sb[g], nb - g * 4);
+                    copy_wait<kDownDepth - 2>();
+                    __syncwarp();
+                    issue(stage == 0 ? (kDownDepth - 1) * kMdStage : stage - kMdStage);
+                    Weights w;
+                    read_unit(w, ring + stage, word, nb - g * 4);
+#pragma unroll
+                    for (int i = 0; i < 4 / P; ++i) {
+                        float upper[4], lower[4], su, sl, f, none;
+#pragma unroll
+                        for (int b = 0; b < P; ++b) {
+                            float d[4];
+                            mma_block(d, w.u[i * P + b], w.l[i * P + b], x[i]);
+                            upper[b] = d[0] + d[1];
+                            lower[b] = d[2] + d[3];
+                        }
+                        e8m0_of(w.su, w.sl, i * P + sblock, su, sl);
+                        e8m0_of(c, 0u, i * P + sblock, f, none);
+                        upper_sum = __fmaf_rn(pick<P>(upper, sblock) * su, f, upper_sum);
+                        lower_sum = __fmaf_rn(pick<P>(lower, sblock) * sl, f, lower_sum);
+                    }
+                    stage = stage + kMdStage < kDownDepth * kMdStage ? stage + kMdStage : 0;
                 }
-                float c[4];
-                e8m0x4(only(sb[g], nb - g * 4), c);
-                copy_wait<kDownDepth - 2>();
-                __syncwarp();
-                issue(stage == 0 ? (kDownDepth - 1) * kMdStage : stage - kMdStage);
-                Weights w;
-                read_unit(w, ring + stage, word, nb - g * 4);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma_f16(d, e4m3_f16(w.u[b].x), e4m3_f16(w.l[b].x), e4m3_f16(w.u[b].x >> 16), e4m3_f16(w.l[b].x >> 16), x[b].x,
-                            x[b].y);
-                    mma_f16(d, e4m3_f16(w.u[b].y), e4m3_f16(w.l[b].y), e4m3_f16(w.u[b].y >> 16), e4m3_f16(w.l[b].y >> 16), x[b].z,
-                            x[b].w);
-                    upper_sum = __fmaf_rn((d[0] + d[1]) * w.su[b], c[b], upper_sum);
-                    lower_sum = __fmaf_rn((d[2] + d[3]) * w.sl[b], c[b], lower_sum);
+                for (int o = R; o < 4; o <<= 1) {
+                    upper_sum += __shfl_xor_sync(0xFFFFFFFFu, upper_sum, o);
+                    lower_sum += __shfl_xor_sync(0xFFFFFFFFu, lower_sum, o);
                 }
-                stage = stage + kMdStage < kDownDepth * kMdStage ? stage + kMdStage : 0;
-            }
+            };
+            if (left == 1) multiply(std::integral_constant<int, 4>());
+            else if (left == 2) multiply(std::integral_constant<int, 2>());
+            else multiply(std::integral_constant<int, 1>());
             // one row after the other: a token that names an expert twice has two of them
             const float p = __ldcg(a.weights + choice);
             float* o = mine + choice / a.topk * 17 + q;
