@@ -116,19 +116,20 @@ __device__ __forceinline__ const uint8_t* scale_line(const uint8_t* s, int64_t r
 }
 
 // ------------------------------------------------------- choices by expert ----
-// Every block sorts the choices by expert for itself.
+// Every block sorts the choices by expert for itself, and cuts each expert's into
+// passes of no more rows than a tile of its products takes.
 struct MdList {                             // arrays in shared memory, list_stride(choices) long
-    int16_t* expert;                        // the experts that are chosen, rising
+    int16_t* expert;                        // the passes' experts, rising
     int16_t* start;                         // where their choices start in `order`
     int16_t* order;                         // choices by expert, and in their order
     int16_t* token;                         // their tokens
-    int active;
+    int passes;
 };
 __host__ __device__ __forceinline__ int list_stride(int choices) { return (choices + 8) & ~7; }
 
 struct MdScratch {
     int key[kMdMaxChoices + 4], sorted[kMdMaxChoices + 1];
-    int heads[kMdMaxChoices / 32];
+    int heads[kMdMaxChoices / 32], cuts[kMdMaxChoices / 32];        // where an expert starts, and where a pass does
     int live;
 };
 
@@ -137,7 +138,7 @@ struct MdScratch {
 // The ids are read past the first-level cache: the down products' kernel reads
 // them before its own dependency wait.
 constexpr int kMdDropped = 1024 << 10;
-template <int NT> __device__ __forceinline__ void sort_choices(const MdArgs& a, MdList& s, MdScratch& w) {
+template <int NT, int ROWS> __device__ __forceinline__ void sort_choices(const MdArgs& a, MdList& s, MdScratch& w) {
     const int tid = (int)threadIdx.x, lane = tid & 31;
     const int choices = a.tokens * a.topk, padded = (choices + 3) & ~3;
     for (int i = tid; i < padded; i += NT) {
@@ -171,18 +172,26 @@ template <int NT> __device__ __forceinline__ void sort_choices(const MdArgs& a, 
     }
     __syncthreads();
     const int live = w.live;
-    int active = 0;
-    for (int i = 0; i < (choices + 31) >> 5; ++i) active += __popc(w.heads[i]);
+    for (int i = tid; i < ((choices + 31) & ~31); i += NT) {
+        int word = i >> 5, heads = w.heads[word] & (int)((2u << lane) - 1u);
+        while (heads == 0 && word > 0) heads = w.heads[--word];
+        const int first = word * 32 + 31 - __clz(heads);                // where this choice's expert starts
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, i < live && (i - first) % ROWS == 0);
+        if (lane == 0) w.cuts[i >> 5] = (int)m;
+    }
+    __syncthreads();
+    int passes = 0;
+    for (int i = 0; i < (choices + 31) >> 5; ++i) passes += __popc(w.cuts[i]);
     for (int i = tid; i < choices; i += NT) {
         const int word = i >> 5;
-        if (!(w.heads[word] >> lane & 1)) continue;
-        int at = __popc(w.heads[word] & ((1u << lane) - 1u));
-        for (int j = 0; j < word; ++j) at += __popc(w.heads[j]);
+        if (!(w.cuts[word] >> lane & 1)) continue;
+        int at = __popc(w.cuts[word] & ((1u << lane) - 1u));
+        for (int j = 0; j < word; ++j) at += __popc(w.cuts[j]);
         s.expert[at] = (int16_t)(w.sorted[i + 1] >> 10);
         s.start[at] = (int16_t)i;
     }
-    if (tid == 0) s.start[active] = (int16_t)live;
-    s.active = active;
+    if (tid == 0) s.start[passes] = (int16_t)live;
+    s.passes = passes;
     __syncthreads();
 }
 
@@ -245,7 +254,7 @@ __device__ __forceinline__ void read_unit(Weights& w, uint32_t stage, uint32_t w
 }
 
 // ------------------------------------------------------ gate and up products ----
-// A block takes 32 features of one expert, and a pair of its warps eight of
+// A block takes 32 features of one pass, and a pair of its warps eight of
 // them: their gate rows are the upper and their up rows the lower half of a unit,
 // so that a lane gets both sums of a feature.  The two take turns at the groups
 // of 128 columns.  A tensor-core tile's columns are 8 rows of x; columns
@@ -255,6 +264,7 @@ __device__ __forceinline__ void read_unit(Weights& w, uint32_t stage, uint32_t w
 // of one block gives one part.  A lane takes its part from each product, and
 // scales and adds one sum instead of P.
 constexpr int kUpThreads = 256;
+constexpr int kUpRows = 8;                              // of a pass
 constexpr int kUpWarps = kUpThreads / 32;
 constexpr int kUpDepth = 3;
 constexpr int kUpRing = kUpWarps * kUpDepth * kMdStage;
@@ -273,13 +283,13 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocks) moe_decode_up_kernel(co
     const int kb = (int)(a.k / 32), groups = (kb + 3) / 4, blocks = (int)(a.n / 32);
     dependency_wait();
     allow_dependents();
-    sort_choices<kUpThreads>(a, list, *reinterpret_cast<MdScratch*>(dyn));
+    sort_choices<kUpThreads, kUpRows>(a, list, *reinterpret_cast<MdScratch*>(dyn));
     const uint32_t ring = smem_addr(dyn) + warp * kUpDepth * kMdStage;
     const int q = lane >> 2, t = lane & 3;
     const int offset = (warp >> 1) * 8, part = warp & 1;
-    const int items = list.active * blocks, item0 = (int)blockIdx.x, item_step = (int)gridDim.x;
+    const int items = list.passes * blocks, item0 = (int)blockIdx.x, item_step = (int)gridDim.x;
 
-    int c_item = item0, c_left_rows = 0, c_col = 0;     // where the copies are
+    int c_item = item0, c_col = 0;                      // where the copies are
     const uint8_t *upper = nullptr, *lower = nullptr, *line = nullptr;
     const int64_t four = 4 * a.k, matrix = (a.n + 127) / 128 * groups * 512;
     auto aim = [&] {
@@ -288,7 +298,6 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocks) moe_decode_up_kernel(co
         const int ai = c_item / blocks;
         const int64_t e = list.expert[ai], f = (int64_t)(c_item - ai * blocks) * 32 + offset;
         const int64_t at = (e * a.n + f + (lane >> 3)) * a.k + c_col + (lane & 7) * 16;
-        if (c_left_rows <= 0) c_left_rows = list.start[ai + 1] - list.start[ai];
         upper = a.gate + at;
         lower = a.up + at;
         line = scale_line(lane < 8 ? a.gate_scales : a.up_scales, f + (lane & 7), part, groups) + matrix * e;
@@ -301,8 +310,7 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocks) moe_decode_up_kernel(co
             line += 1024;
             c_col += 256;
             if (c_col >= (int)a.k) {
-                c_left_rows -= 8;
-                if (c_left_rows <= 0) c_item += item_step;
+                c_item += item_step;
                 aim();
             }
         }
@@ -324,104 +332,102 @@ __global__ void __launch_bounds__(kUpThreads, kUpBlocks) moe_decode_up_kernel(co
     int flip = 0;
     for (int item = item0; item < items; item += item_step) {
         const int ai = item / blocks, block = item - ai * blocks;
-        const int first = list.start[ai], rows = list.start[ai + 1] - first;
-        for (int r0 = 0; r0 < rows; r0 += 8) {
-            const int left = rows - r0, at = first + r0;
-            uint64_t acc[2] = {0, 0};
-            auto multiply = [&](auto packed) {
-                constexpr int P = decltype(packed)::value, R = 8 / P;       // blocks in the columns, rows of x
-                // this lane's column of B, and its sums' two columns, whose rows are 2 t and 2 t + 1 modulo R
-                const int xr = q % R, r = 2 * t % R, xblock = q / R, sblock = t * P / 4;
-                const uint8_t* xb = a.codes + list.token[at + (xr < left ? xr : 0)] * a.k + (part * 4 + xblock) * 32 + t * 8;
-                uint32_t s0 = smem_addr(xscales + list.token[at + (r < left ? r : 0)] * groups + part);
-                uint32_t s1 = smem_addr(xscales + list.token[at + (r + 1 < left ? r + 1 : 0)] * groups + part);
-                for (int b0 = part * 4; b0 < kb; b0 += 8) {
-                    uint2 x[4 / P];
-                    if (b0 + 4 <= kb) {
+        const int at = list.start[ai], left = list.start[ai + 1] - at;
+        uint64_t acc[2] = {0, 0};
+        auto multiply = [&](auto packed) {
+            constexpr int P = decltype(packed)::value, R = 8 / P;       // blocks in the columns, rows of x
+            // this lane's column of B, and its sums' two columns, whose rows are 2 t and 2 t + 1 modulo R
+            const int xr = q % R, r = 2 * t % R, xblock = q / R, sblock = t * P / 4;
+            const uint8_t* xb = a.codes + list.token[at + (xr < left ? xr : 0)] * a.k + (part * 4 + xblock) * 32 + t * 8;
+            uint32_t s0 = smem_addr(xscales + list.token[at + (r < left ? r : 0)] * groups + part);
+            uint32_t s1 = smem_addr(xscales + list.token[at + (r + 1 < left ? r + 1 : 0)] * groups + part);
+            for (int b0 = part * 4; b0 < kb; b0 += 8) {
+                uint2 x[4 / P];
+                if (b0 + 4 <= kb) {
 #pragma unroll
-                        for (int i = 0; i < 4 / P; ++i) x[i] = *reinterpret_cast<const uint2*>(xb + i * P * 32);
-                    } else {
+                    for (int i = 0; i < 4 / P; ++i) x[i] = *reinterpret_cast<const uint2*>(xb + i * P * 32);
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 4 / P; ++i)
-                            x[i] = b0 + i * P + xblock < kb ? *reinterpret_cast<const uint2*>(xb + i * P * 32) : make_uint2(0u, 0u);
-                    }
-                    xb += 256;
-                    const uint32_t w0 = lds32(s0), w1 = lds32(s1);
-                    s0 += 8;
-                    s1 += 8;
-                    copy_wait<kUpDepth - 2>();
-                    __syncwarp();
-                    issue(stage == 0 ? (kUpDepth - 1) * kMdStage : stage - kMdStage);
-                    Weights w;
-                    read_unit(w, ring + stage, (uint32_t)(block & 3) * 4, kb - b0);
-#pragma unroll
-                    for (int i = 0; i < 4 / P; ++i) {
-                        const uint4 f = make_uint4(e4m3_f16(x[i].x), e4m3_f16(x[i].x >> 16), e4m3_f16(x[i].y), e4m3_f16(x[i].y >> 16));
-                        float d[4][4], su, sl, c0, c1;
-#pragma unroll
-                        for (int b = 0; b < P; ++b) {
-                            float v[4];
-                            mma_block(v, w.u[i * P + b], w.l[i * P + b], f);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) d[j][b] = v[j];
-                        }
-                        e8m0_of(w.su, w.sl, i * P + sblock, su, sl);
-                        e8m0_of(w0, w1, i * P + sblock, c0, c1);
-                        const uint64_t c = f2_pack(c0, c1), up = f2_pack(su, su), lo = f2_pack(sl, sl);
-                        acc[0] = f2_fma(f2_mul(f2_pack(pick<P>(d[0], sblock), pick<P>(d[1], sblock)), up), c, acc[0]);
-                        acc[1] = f2_fma(f2_mul(f2_pack(pick<P>(d[2], sblock), pick<P>(d[3], sblock)), lo), c, acc[1]);
-                    }
-                    stage = stage + kMdStage < kUpDepth * kMdStage ? stage + kMdStage : 0;
+                    for (int i = 0; i < 4 / P; ++i)
+                        x[i] = b0 + i * P + xblock < kb ? *reinterpret_cast<const uint2*>(xb + i * P * 32) : make_uint2(0u, 0u);
                 }
+                xb += 256;
+                const uint32_t w0 = lds32(s0), w1 = lds32(s1);
+                s0 += 8;
+                s1 += 8;
+                copy_wait<kUpDepth - 2>();
+                __syncwarp();
+                issue(stage == 0 ? (kUpDepth - 1) * kMdStage : stage - kMdStage);
+                Weights w;
+                read_unit(w, ring + stage, (uint32_t)(block & 3) * 4, kb - b0);
 #pragma unroll
-                for (int o = 4 / P; o < 4; o <<= 1) {
-                    acc[0] = f2_add(acc[0], __shfl_xor_sync(0xFFFFFFFFu, acc[0], o));
-                    acc[1] = f2_add(acc[1], __shfl_xor_sync(0xFFFFFFFFu, acc[1], o));
+                for (int i = 0; i < 4 / P; ++i) {
+                    const uint4 f = make_uint4(e4m3_f16(x[i].x), e4m3_f16(x[i].x >> 16), e4m3_f16(x[i].y), e4m3_f16(x[i].y >> 16));
+                    float d[4][4], su, sl, c0, c1;
+#pragma unroll
+                    for (int b = 0; b < P; ++b) {
+                        float v[4];
+                        mma_block(v, w.u[i * P + b], w.l[i * P + b], f);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) d[j][b] = v[j];
+                    }
+                    e8m0_of(w.su, w.sl, i * P + sblock, su, sl);
+                    e8m0_of(w0, w1, i * P + sblock, c0, c1);
+                    const uint64_t c = f2_pack(c0, c1), up = f2_pack(su, su), lo = f2_pack(sl, sl);
+                    acc[0] = f2_fma(f2_mul(f2_pack(pick<P>(d[0], sblock), pick<P>(d[1], sblock)), up), c, acc[0]);
+                    acc[1] = f2_fma(f2_mul(f2_pack(pick<P>(d[2], sblock), pick<P>(d[3], sblock)), lo), c, acc[1]);
                 }
-            };
-            if (left <= 2) multiply(std::integral_constant<int, 4>());
-            else if (left <= 4) multiply(std::integral_constant<int, 2>());
-            else multiply(std::integral_constant<int, 1>());
-            float v[4];
-            f2_unpack(acc[0], v[0], v[1]);
-            f2_unpack(acc[1], v[2], v[3]);
-            float* p = red + (flip * kUpWarps + warp) * kUpWords + lane;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[j * 33] = v[j];
-            __syncthreads();
-            // a warp takes a row, a lane a feature: the sums, the activation, and the terms of h
-            if (warp < left) {
-                const float* s = red + (flip * kUpWarps + (lane >> 3) * 2) * kUpWords +
-                                 (warp & 1) * 33 + (lane & 7) * 4 + (warp >> 1);
-                const float g = s[0] + s[kUpWords], u = s[66] + s[kUpWords + 66];
-                const float h = g / (1.0f + expf(-g)) * u;
-                // the block's largest value goes to [2^14, 2^15): h = (hi + lo) * 2^(byte - 127)
-                uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu) >> 23;
-                top = top < 16u ? 16u : top > 254u ? 254u : top;
-                const float v = h * __uint_as_float((268u - top) << 23);
-                const __half hi = __float2half_rn(v);
-                const __half lo = __hisinf(hi) ? __half(0.0f) : __float2half_rn(v - __half2float(hi));
-                const int64_t choice = list.order[at + warp];
-                uint16_t* out = a.h + choice * 2 * a.n + block * 32 + lane;
-                out[0] = __half_as_ushort(hi);
-                out[a.n] = __half_as_ushort(lo);
-                if (lane == 0) a.hs[choice * a.hgroups * 4 + block] = (uint8_t)(top - 14u);
+                stage = stage + kMdStage < kUpDepth * kMdStage ? stage + kMdStage : 0;
             }
-            flip ^= 1;                                  // the other half is free: its readers have met the barrier above
+#pragma unroll
+            for (int o = 4 / P; o < 4; o <<= 1) {
+                acc[0] = f2_add(acc[0], __shfl_xor_sync(0xFFFFFFFFu, acc[0], o));
+                acc[1] = f2_add(acc[1], __shfl_xor_sync(0xFFFFFFFFu, acc[1], o));
+            }
+        };
+        if (left <= 2) multiply(std::integral_constant<int, 4>());
+        else if (left <= 4) multiply(std::integral_constant<int, 2>());
+        else multiply(std::integral_constant<int, 1>());
+        float v[4];
+        f2_unpack(acc[0], v[0], v[1]);
+        f2_unpack(acc[1], v[2], v[3]);
+        float* p = red + (flip * kUpWarps + warp) * kUpWords + lane;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j * 33] = v[j];
+        __syncthreads();
+        // a warp takes a row, a lane a feature: the sums, the activation, and the terms of h
+        if (warp < left) {
+            const float* s = red + (flip * kUpWarps + (lane >> 3) * 2) * kUpWords +
+                             (warp & 1) * 33 + (lane & 7) * 4 + (warp >> 1);
+            const float g = s[0] + s[kUpWords], u = s[66] + s[kUpWords + 66];
+            const float h = g / (1.0f + expf(-g)) * u;
+            // the block's largest value goes to [2^14, 2^15): h = (hi + lo) * 2^(byte - 127)
+            uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu) >> 23;
+            top = top < 16u ? 16u : top > 254u ? 254u : top;
+            const float v = h * __uint_as_float((268u - top) << 23);
+            const __half hi = __float2half_rn(v);
+            const __half lo = __hisinf(hi) ? __half(0.0f) : __float2half_rn(v - __half2float(hi));
+            const int64_t choice = list.order[at + warp];
+            uint16_t* out = a.h + choice * 2 * a.n + block * 32 + lane;
+            out[0] = __half_as_ushort(hi);
+            out[a.n] = __half_as_ushort(lo);
+            if (lane == 0) a.hs[choice * a.hgroups * 4 + block] = (uint8_t)(top - 14u);
         }
+        flip ^= 1;                                  // the other half is free: its readers have met the barrier above
     }
     copy_wait<0>();
 }
 
 // -------------------------------------------- down product, sum over choices ----
 // A block, or a cluster of them where there are few, takes 16 output features
-// of all tokens.  The pairs of a chosen expert and a group of 128 columns of n
-// are cut evenly over its warps; the columns of a tensor-core tile are the two
+// of all tokens.  The pairs of a pass and a group of 128 columns of n are cut
+// evenly over its warps; the columns of a tensor-core tile are the two
 // terms of four rows of h.  A warp adds its products, times the choices' weights,
 // to sums of its own, which are joined over the warps and over the cluster's
 // blocks in a fixed order.  The first weights are on their way before h is
 // waited for.
 constexpr int kDownDepth = 3;
+constexpr int kDownRows = 4;                            // of a pass
 __host__ __device__ constexpr int down_ring(int threads) { return threads / 32 * kDownDepth * kMdStage; }
 constexpr int kDownMaxCluster = 8;
 
@@ -439,23 +445,21 @@ template <int NT> __global__ void __launch_bounds__(NT, 1) moe_decode_down_kerne
     const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
     // Ids and weights may be read at once: the blocks of the launch before this one let it start only when whatever
     // wrote them had completed.
-    sort_choices<NT>(a, list, *reinterpret_cast<MdScratch*>(dyn));
+    sort_choices<NT, kDownRows>(a, list, *reinterpret_cast<MdScratch*>(dyn));
     const int64_t f0 = (int64_t)(blockIdx.x / ranks) * 16;
     const int groups = a.hgroups, nb = (int)(a.n / 32);
-    const int units = list.active * groups, shares = (int)ranks * kWarps, share = (int)rank * kWarps + warp;
+    const int units = list.passes * groups, shares = (int)ranks * kWarps, share = (int)rank * kWarps + warp;
     const int lo = (int)((int64_t)units * share / shares), hi = (int)((int64_t)units * (share + 1) / shares);
     const uint32_t ring = smem_addr(dyn) + warp * kDownDepth * kMdStage;
     const int q = lane >> 2, t = lane & 3;
 
-    int c_unit = lo, c_g = 0, c_end = 0, c_left_rows = 0;           // where the copies are: an expert's groups from c_unit on
+    int c_unit = lo, c_g = 0;                           // where the copies are
     const int64_t four = 4 * a.n, matrix = (a.k + 127) / 128 * groups * 512;
     const uint8_t *upper = nullptr, *line = nullptr;
     auto aim = [&] {
         if (c_unit >= hi) return;
         const int ai = c_unit / groups;
         c_g = c_unit - ai * groups;
-        c_end = c_g + (hi - c_unit) < groups ? c_g + (hi - c_unit) : groups;
-        if (c_left_rows <= 0) c_left_rows = list.start[ai + 1] - list.start[ai];
         const int64_t e = list.expert[ai];
         upper = a.down + (e * a.k + f0 + (lane >> 3)) * a.n + c_g * 128 + (lane & 7) * 16;
         line = scale_line(a.down_scales, f0 + (lane & 15), c_g, groups) + matrix * e;
@@ -465,11 +469,8 @@ template <int NT> __global__ void __launch_bounds__(NT, 1) moe_decode_down_kerne
             copy_unit(ring + at, upper, upper + 2 * four, four, line, (int)a.n - c_g * 128);
             upper += 128;
             line += 512;
-            if (++c_g == c_end) {
-                c_left_rows -= 4;
-                if (c_left_rows <= 0) c_unit += c_end - c_unit % groups;
-                aim();
-            }
+            ++c_unit;
+            if (++c_g == groups) aim();
         }
         copy_commit();
     };
@@ -485,69 +486,66 @@ template <int NT> __global__ void __launch_bounds__(NT, 1) moe_decode_down_kerne
     uint32_t stage = 0;
     const uint32_t word = (uint32_t)(f0 >> 5 & 3) * 4;
     for (int u = lo; u < hi;) {
-        // one expert's groups g0 .. g1 - 1, four rows at a time: this lane's column of B is term q % 2 of row q / 2, its
-        // sums' columns are both terms of row t
+        // one pass's groups g0 .. g1 - 1; the tile's columns are both terms of R rows in P blocks, and a lane's sums both
+        // terms of one row in one of the blocks
         const int ai = u / groups, g0 = u - ai * groups, g1 = g0 + (hi - u) < groups ? g0 + (hi - u) : groups;
-        const int first = list.start[ai], rows = list.start[ai + 1] - first;
-        for (int r0 = 0; r0 < rows; r0 += 4) {
-            const int left = rows - r0, at = first + r0;
-            float upper_sum = 0.0f, lower_sum = 0.0f;
-            int choice = 0;
-            auto multiply = [&](auto packed) {
-                constexpr int P = decltype(packed)::value, R = 4 / P;       // blocks in the columns, rows of h
-                const int hr = (q >> 1) % R, r = t % R, hblock = (q >> 1) / R, sblock = t / R;
-                choice = list.order[at + (r < left ? r : 0)];
-                const uint16_t* hb = a.h + ((int64_t)list.order[at + (hr < left ? hr : 0)] * 2 + (q & 1)) * a.n + g0 * 128 + hblock * 32 + t * 8;
-                const uint32_t* sb = reinterpret_cast<const uint32_t*>(a.hs) + (int64_t)choice * groups;
-                for (int g = g0; g < g1; ++g, hb += 128) {
-                    uint4 x[4 / P];
-                    if (g * 4 + 4 <= nb) {
+        const int at = list.start[ai], left = list.start[ai + 1] - at;
+        float upper_sum = 0.0f, lower_sum = 0.0f;
+        int choice = 0;
+        auto multiply = [&](auto packed) {
+            constexpr int P = decltype(packed)::value, R = 4 / P;       // blocks in the columns, rows of h
+            const int hr = (q >> 1) % R, r = t % R, hblock = (q >> 1) / R, sblock = t / R;
+            choice = list.order[at + (r < left ? r : 0)];
+            const uint16_t* hb = a.h + ((int64_t)list.order[at + (hr < left ? hr : 0)] * 2 + (q & 1)) * a.n + g0 * 128 + hblock * 32 + t * 8;
+            const uint32_t* sb = reinterpret_cast<const uint32_t*>(a.hs) + (int64_t)choice * groups;
+            for (int g = g0; g < g1; ++g, hb += 128) {
+                uint4 x[4 / P];
+                if (g * 4 + 4 <= nb) {
 #pragma unroll
-                        for (int i = 0; i < 4 / P; ++i) x[i] = *reinterpret_cast<const uint4*>(hb + i * P * 32);
-                    } else {
+                    for (int i = 0; i < 4 / P; ++i) x[i] = *reinterpret_cast<const uint4*>(hb + i * P * 32);
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 4 / P; ++i)
-                            x[i] = g * 4 + i * P + hblock < nb ? *reinterpret_cast<const uint4*>(hb + i * P * 32) : make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    const uint32_t c = only(sb[g], nb - g * 4);
-                    copy_wait<kDownDepth - 2>();
-                    __syncwarp();
-                    issue(stage == 0 ? (kDownDepth - 1) * kMdStage : stage - kMdStage);
-                    Weights w;
-                    read_unit(w, ring + stage, word, nb - g * 4);
-#pragma unroll
-                    for (int i = 0; i < 4 / P; ++i) {
-                        float upper[4], lower[4], su, sl, f, none;
-#pragma unroll
-                        for (int b = 0; b < P; ++b) {
-                            float d[4];
-                            mma_block(d, w.u[i * P + b], w.l[i * P + b], x[i]);
-                            upper[b] = d[0] + d[1];
-                            lower[b] = d[2] + d[3];
-                        }
-                        e8m0_of(w.su, w.sl, i * P + sblock, su, sl);
-                        e8m0_of(c, 0u, i * P + sblock, f, none);
-                        upper_sum = __fmaf_rn(pick<P>(upper, sblock) * su, f, upper_sum);
-                        lower_sum = __fmaf_rn(pick<P>(lower, sblock) * sl, f, lower_sum);
-                    }
-                    stage = stage + kMdStage < kDownDepth * kMdStage ? stage + kMdStage : 0;
+                    for (int i = 0; i < 4 / P; ++i)
+                        x[i] = g * 4 + i * P + hblock < nb ? *reinterpret_cast<const uint4*>(hb + i * P * 32) : make_uint4(0u, 0u, 0u, 0u);
                 }
-#pragma unroll
-                for (int o = R; o < 4; o <<= 1) {
-                    upper_sum += __shfl_xor_sync(0xFFFFFFFFu, upper_sum, o);
-                    lower_sum += __shfl_xor_sync(0xFFFFFFFFu, lower_sum, o);
-                }
-            };
-            if (left == 1) multiply(std::integral_constant<int, 4>());
-            else if (left == 2) multiply(std::integral_constant<int, 2>());
-            else multiply(std::integral_constant<int, 1>());
-            // one row after the other: a token that names an expert twice has two of them
-            const float p = __ldcg(a.weights + choice);
-            float* o = mine + choice / a.topk * 17 + q;
-            for (int turn = 0; turn < 4 && turn < left; ++turn) {
-                if (t == turn) o[0] = __fmaf_rn(p, upper_sum, o[0]), o[8] = __fmaf_rn(p, lower_sum, o[8]);
+                const uint32_t c = only(sb[g], nb - g * 4);
+                copy_wait<kDownDepth - 2>();
                 __syncwarp();
+                issue(stage == 0 ? (kDownDepth - 1) * kMdStage : stage - kMdStage);
+                Weights w;
+                read_unit(w, ring + stage, word, nb - g * 4);
+#pragma unroll
+                for (int i = 0; i < 4 / P; ++i) {
+                    float upper[4], lower[4], su, sl, f, none;
+#pragma unroll
+                    for (int b = 0; b < P; ++b) {
+                        float d[4];
+                        mma_block(d, w.u[i * P + b], w.l[i * P + b], x[i]);
+                        upper[b] = d[0] + d[1];
+                        lower[b] = d[2] + d[3];
+                    }
+                    e8m0_of(w.su, w.sl, i * P + sblock, su, sl);
+                    e8m0_of(c, 0u, i * P + sblock, f, none);
+                    upper_sum = __fmaf_rn(pick<P>(upper, sblock) * su, f, upper_sum);
+                    lower_sum = __fmaf_rn(pick<P>(lower, sblock) * sl, f, lower_sum);
+                }
+                stage = stage + kMdStage < kDownDepth * kMdStage ? stage + kMdStage : 0;
             }
+#pragma unroll
+            for (int o = R; o < 4; o <<= 1) {
+                upper_sum += __shfl_xor_sync(0xFFFFFFFFu, upper_sum, o);
+                lower_sum += __shfl_xor_sync(0xFFFFFFFFu, lower_sum, o);
+            }
+        };
+        if (left == 1) multiply(std::integral_constant<int, 4>());
+        else if (left == 2) multiply(std::integral_constant<int, 2>());
+        else multiply(std::integral_constant<int, 1>());
+        // one row after the other: a token that names an expert twice has two of them
+        const float p = __ldcg(a.weights + choice);
+        float* o = mine + choice / a.topk * 17 + q;
+        for (int turn = 0; turn < 4 && turn < left; ++turn) {
+            if (t == turn) o[0] = __fmaf_rn(p, upper_sum, o[0]), o[8] = __fmaf_rn(p, lower_sum, o[8]);
+            __syncwarp();
         }
         u += g1 - g0;
     }
@@ -653,7 +651,7 @@ extern "C" fp8q_status_t mxfp8_moe_decode(const uint8_t* codes, const uint8_t* s
     const size_t up_smem = kUpRing + kUpSums + lists + (size_t)tokens * (size_t)((k + 127) / 128) * 4;
     static KernelCache up_cache;
     int resident = 0;
-    const size_t most = (size_t)(choices < experts ? choices : experts);        // chosen experts
+    const size_t most = std::min((size_t)choices, (size_t)experts + (size_t)choices / kUpRows);     // passes
     const size_t items = most * (size_t)(n / 32);
     fp8q_status_t st = prepare_kernel(up_cache, moe_decode_up_kernel, kUpThreads, kMaxUp, kMaxUp, &resident);
     if (st == FP8Q_OK) st = launch(moe_decode_up_kernel, grid_for(items, kUpBlocks), kUpThreads, up_smem, s, a);
