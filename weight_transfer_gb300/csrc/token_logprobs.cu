@@ -31,7 +31,10 @@ constexpr int kLpMaxTop = FP8Q_MAX_TOP;
 constexpr int kLpCap = 128;             // candidates that a warp holds in shared memory
 constexpr int kLpMaxCluster = 8;
 constexpr int kLpBlocksPerSm = 4;           // up to which rows are divided: 256 rows 36.7 us, with 2 38.2, with 8 41.8
-constexpr int kLpPlaces = 48;            // of stored maxima a thread
+// Places of stored maxima a thread.  1024 rows of 151,669 binary32 logits with
+// five alternatives 112 us, 8 places 116; 48 139, as what a block then holds of
+// the shared memory leaves little first-level cache for loads on their way.
+constexpr int kLpPlaces = 24;
 constexpr int kLpUnroll = 4;            // 16-byte vectors per thread and step
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
@@ -781,10 +784,13 @@ fp8q_status_t check_logits(int64_t rows, int64_t vocab, int64_t stride, int logi
 
 template <int BYTES, bool TOP, bool ENT, int NT>
 fp8q_status_t launch_logprobs(LpArgs a, int64_t rows, cudaStream_t stream) {
-    // blocks of a cluster share a row while there are few rows
+    // blocks of a cluster share a row while there are few rows; clusters of four and eight do not fill every slot (72
+    // rows of 151,669 binary32 logits with five alternatives in clusters of eight 19.1 us, of four 15.2; 152 in clusters
+    // of four 31.4, of two 24.3)
     unsigned ranks = 1;
+    const int64_t slots = kLpBlocksPerSm * sm_count();
     const int64_t steps = (a.vocab * BYTES + NT * kLpUnroll * 16 - 1) / (NT * kLpUnroll * 16);
-    while (ranks < kLpMaxCluster && rows * ranks * 2 <= kLpBlocksPerSm * sm_count() && (int64_t)ranks * 2 <= steps) ranks *= 2;
+    while (ranks < kLpMaxCluster && rows * ranks * 2 <= (ranks > 1 ? slots - slots / 16 : slots) && (int64_t)ranks * 2 <= steps) ranks *= 2;
     constexpr size_t kMax = TOP ? sizeof(LpTopShared<NT>) + (size_t)kLpPlaces * NT * 4 : 0;
     size_t smem = 0;
     if (TOP) {
