@@ -15,17 +15,21 @@
 // of weights and 8 columns (mma.sync): with one to four rows of x per expert, the
 // 128 rows and 16 columns of a tcgen05 tile would leave a token's 8 experts to 48
 // of the 152 SMs, and their scales would have to be laid out for each expert.
-// This GPU has no e4m3 form of mma.sync, and converts the operands to f16 before
-// it (12 conversions and two products for each): the warps' own instructions are
-// the second bound, 280 for a unit of 2 KB of weights, issued in 0.65 of all
-// cycles at 32 tokens.
-//     one token 14.6 us, eight (15% of the choices dropped) 44.5 us, 5.6 TB/s,
-//     32 tokens 104 us, 5.2 TB/s; through sort, gather, swiglu, matmul and
-//     combine 22, 58 (none dropped) and 101 us
-// What did not gain: x or h fetched a unit ahead (32 tokens 135 us), x held in
-// shared memory (the same), three blocks per SM with 80 registers (111), partial
-// sums without a barrier (114 where 114), whole K to a warp (117), a lane's units
-// in registers instead of rings (261).
+// This GPU has no e4m3 form of mma.sync: the codes are converted to f16, exactly.
+// The warps' own instructions are the second bound, 220 (gate and up) and 260
+// (down) for a unit of 2 KB of weights, issued in 0.57 of all cycles at 32 tokens.
+//     one token 13.9 us, eight (15% of the choices dropped) 42.5 us, 5.9 TB/s,
+//     32 tokens 96 us, 5.7 TB/s; through sort, gather, swiglu, matmul and
+//     combine 22, 57.5 (none dropped) and 100.7 us
+// Columns without rows hold further blocks of K, so that a lane scales and adds
+// one sum for four: 14.6, 44.5 and 104 us without.
+// What did not gain: x or h fetched a unit ahead (the same), x held in shared
+// memory (the same), three blocks per SM with 80 registers (32 tokens 111 us where
+// 104), partial sums without a barrier (the same), whole K to a warp (117), a
+// lane's units in registers instead of rings (261).  Of the down products: tiles
+// of 32 features, which halve the reading of h (97.8 where 99.1, but 72.5 where
+// 71.6 for sixteen tokens); units cut evenly over all SMs with sums joined in
+// memory (104.4, one token 22.1).
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 
@@ -585,8 +589,8 @@ size_t workspace_of(int64_t tokens, int topk, int64_t n) {
 }
 
 // Sixteen warps a block for one or two tokens, whose units last each of them a
-// few steps, twenty beyond (one token 14.8 and 15.6 us, eight 45.6 and 44.5, 32
-// 108.8 and 104.1; twenty-four 15.4, 45.1, 104.6).
+// few steps (one token 13.9 us, with twenty 14.8), twenty-four beyond (32 tokens
+// 97.7 us, with twenty 98.9, sixteen 102.3; four tokens 32.5, 32.1 and 32.2).
 constexpr int64_t kDownFewTokens = 2;
 template <int NT> fp8q_status_t launch_down(const MdArgs& a, unsigned ranks, size_t lists, cudaStream_t stream) {
     const auto bytes = [&](int tokens, size_t l) { return down_ring(NT) + (size_t)NT / 32 * 17 * tokens * sizeof(float) + l; };
@@ -658,5 +662,5 @@ extern "C" fp8q_status_t mxfp8_moe_decode(const uint8_t* codes, const uint8_t* s
     if (st != FP8Q_OK) return st;
     unsigned ranks = 1;
     while (ranks < kDownMaxCluster && (int64_t)(k / 16) * ranks * 2 <= sm_count()) ranks *= 2;
-    return tokens <= kDownFewTokens ? launch_down<512>(a, ranks, lists, s) : launch_down<640>(a, ranks, lists, s);
+    return tokens <= kDownFewTokens ? launch_down<512>(a, ranks, lists, s) : launch_down<768>(a, ranks, lists, s);
 }
