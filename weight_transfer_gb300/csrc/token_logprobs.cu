@@ -18,7 +18,7 @@
 // with entropy (6.64 TB/s; scalar arithmetic on unpacked logits, 12 instructions
 // each instead of 5, took 261), 370 us for the gradient (6.72 TB/s; 400 with a
 // comparison with the target at every logit).  256 rows of 151,669 binary32
-// logits with five alternatives: 38 us, without them 27.  Four rows: 8.9 us, of
+// logits with five alternatives: 38 us, without them 27.  Four rows: 6.7 us, of
 // which the launch and the joins are most.
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
@@ -140,11 +140,20 @@ __device__ __forceinline__ void raise(Soft& a, float m, float c) {
     a.s *= f;
     a.m = m;
 }
-__device__ __forceinline__ Soft join(Soft a, Soft b, float c) {
-    const float m = fmaxf(a.m, b.m);
-    raise(a, m, c);
-    raise(b, m, c);
-    return {m, a.s + b.s, a.e + b.e, fmaxf(a.top, b.top)};
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+    return r;
+}
+// Joins the sums of a warp's lanes; the first LANES of them have the result.
+template <int LANES> __device__ __forceinline__ void join_lanes(Soft& a, float c) {
+    raise(a, warp_max(a.m), c);
+    a.top = warp_max(a.top);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+        a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, o);
+        a.e += __shfl_xor_sync(0xFFFFFFFFu, a.e, o);
+    }
 }
 
 // A thread's sums.  The reference m is raised only where a logit exceeds it by 4
@@ -379,15 +388,7 @@ template <int NT> __device__ __forceinline__ void sort_top(uint64_t* keys, int n
 __device__ __forceinline__ Soft join_parts(const Soft* parts, int n, float c) {
     const int lane = (int)(threadIdx.x & 31u);
     Soft v = lane < n ? parts[lane] : Soft{kLowest, 0.0f, 0.0f, -INFINITY};
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-        Soft b;
-        b.m = __shfl_down_sync(0xFFFFFFFFu, v.m, o);
-        b.s = __shfl_down_sync(0xFFFFFFFFu, v.s, o);
-        b.e = __shfl_down_sync(0xFFFFFFFFu, v.e, o);
-        b.top = __shfl_down_sync(0xFFFFFFFFu, v.top, o);
-        v = join(v, b, c);
-    }
+    join_lanes<8>(v, c);
     return v;
 }
 
@@ -461,15 +462,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
     }
 
     Soft acc = sums.settle(a.c);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Soft b;
-        b.m = __shfl_xor_sync(0xFFFFFFFFu, acc.m, o);
-        b.s = __shfl_xor_sync(0xFFFFFFFFu, acc.s, o);
-        b.e = __shfl_xor_sync(0xFFFFFFFFu, acc.e, o);
-        b.top = __shfl_xor_sync(0xFFFFFFFFu, acc.top, o);
-        acc = (lane & o) ? join(b, acc, a.c) : join(acc, b, a.c);
-    }
+    join_lanes<32>(acc, a.c);
     if (lane == 0) sh.warp[warp] = acc;
     if (TOP) {
         float g = sums.top;
@@ -480,15 +473,17 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
         if (tid < 64) {
             const float own = t.group[tid];
             int above = 0;
-#pragma unroll 16
-            for (int j = 0; j < 64; ++j) {
-                const float o = t.group[j];
-                above += o > own || (o == own && j < tid);
+#pragma unroll
+            for (int j = 0; j < 64; j += 4) {
+                const float4 o = *reinterpret_cast<const float4*>(&t.group[j]);
+                above += (o.x > own || (o.x == own && j < tid)) + (o.y > own || (o.y == own && j + 1 < tid)) +
+                         (o.z > own || (o.z == own && j + 2 < tid)) + (o.w > own || (o.w == own && j + 3 < tid));
             }
             if (above == a.top - 1) t.floor = own;
         }
         __syncthreads();
         const float floor_value = t.floor;
+#pragma unroll 4
         for (int i = 0; i < places; ++i) {
             const float m = t.most[i * NT + tid];
             if (m >= floor_value && m > -INFINITY) {
@@ -496,30 +491,30 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
                 if (pos < kLpGather) t.list[pos] = i * NT + tid;
             }
         }
-        auto gather = [&](float f, int64_t i) {
-            if (!(f >= floor_value && f > -INFINITY)) return;
+        if (extra >= floor_value && extra > -INFINITY) {
             const int pos = atomicAdd(&t.gathered, 1);
-            if (pos < kLpGather) t.gather[pos] = key_of(f, i);
-        };
-        gather(extra, extra_at);
+            if (pos < kLpGather) t.gather[pos] = key_of(extra, extra_at);
+        }
         __syncthreads();
         const int listed = t.listed;
         if (listed <= kLpGather) {
-            for (int e = tid; e < listed; e += NT) {
-                const int place = t.list[e] / NT, owner = t.list[e] % NT;
+            for (int e = tid; e < listed * kLpUnroll; e += NT) {        // one of a step's vectors to a thread
+                const int step = t.list[e / kLpUnroll], place = step / NT, owner = step % NT;
                 for (int f = 0; f < a.fold; ++f) {
-                    const int64_t i0 = v0 + ((int64_t)(place * a.fold + f) * kLpUnroll) * NT + owner;
-                    uint4 v[kLpUnroll];
+                    const int64_t i = v0 + ((int64_t)(place * a.fold + f) * kLpUnroll + e % kLpUnroll) * NT + owner;
+                    if (i >= v1) break;
+                    float x8[per];
+                    L::unpack(ld_stream(body + 16 * i), x8);
+                    unsigned hits = 0;
 #pragma unroll
-                    for (int u = 0; u < kLpUnroll; ++u)
-                        v[u] = i0 + u * NT < v1 ? ld_stream(body + 16 * (i0 + u * NT))
-                                                : make_uint4(L::kNothing, L::kNothing, L::kNothing, L::kNothing);
+                    for (int j = 0; j < per; ++j) hits |= (x8[j] >= floor_value && x8[j] > -INFINITY ? 1u : 0u) << j;
+                    if (hits == 0) continue;
+                    int pos = atomicAdd(&t.gathered, __popc(hits));
 #pragma unroll
-                    for (int u = 0; u < kLpUnroll; ++u) {
-                        float x8[per];
-                        L::unpack(v[u], x8);
-#pragma unroll
-                        for (int j = 0; j < per; ++j) gather(x8[j], cut.head + (i0 + u * NT) * per + j);
+                    for (int j = 0; j < per; ++j) {
+                        if (!(hits >> j & 1)) continue;
+                        if (pos < kLpGather) t.gather[pos] = key_of(x8[j], cut.head + i * per + j);
+                        ++pos;
                     }
                 }
             }
