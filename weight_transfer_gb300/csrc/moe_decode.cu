@@ -26,7 +26,8 @@
 // What did not gain: x or h fetched a unit ahead (the same), x held in shared
 // memory (the same), three blocks per SM with 80 registers (one token 15.2 us, two
 // 18.7 where 21.2, 32 the same), partial sums without a barrier (the same), whole
-// K to a warp (117 where 104), a lane's units in registers instead of rings (261).  Of the down products: tiles
+// K to a warp (117 where 104), a lane's units in registers instead of rings (261).
+// Of the down products: tiles
 // of 32 features, which halve the reading of h (97.8 where 99.1, but 72.5 where
 // 71.6 for sixteen tokens); units cut evenly over all SMs with sums joined in
 // memory (104.4, one token 22.1).

@@ -14,12 +14,13 @@
 // Gradient, from the statistics that the forward pass wrote:
 //     dx_j = ([j = t] g - p_j (g + dH (log p_j + entropy))) / T
 //
-// All of it is bound by HBM.  4096 rows of 151,936 bf16 logits: 187 us forward
-// with entropy (6.64 TB/s; scalar arithmetic on unpacked logits, 12 instructions
+// All of it is bound by HBM.  4096 rows of 151,936 bf16 logits: 184.7 us forward
+// with entropy (6.74 TB/s; scalar arithmetic on unpacked logits, 12 instructions
 // each instead of 5, took 261), 370 us for the gradient (6.72 TB/s; 400 with a
 // comparison with the target at every logit).  256 rows of 151,669 binary32
-// logits with five alternatives: 38 us, without them 27.  Four rows: 6.7 us, of
-// which the launch and the joins are most.
+// logits with five alternatives: 36.7 us, without them 27.  Four rows: 6.5 us, of
+// which the launch and the joins are most (8.8 where a warp's lanes join their
+// sums pair by pair and the joins wait for the sorting).
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 
@@ -309,6 +310,7 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t a, uint64_t v) {
 template <int NT> struct LpShared {
     Soft warp[NT / 32];
     Soft part[kLpMaxCluster];
+    float m, log_s;             // of the row; m = -inf without any logit
 };
 // The alternatives.  Every thread stores the largest logit of each of its steps.
 // When the row is through, the top-th largest of 64 groups' maxima is a floor:
@@ -325,7 +327,7 @@ template <int NT> struct LpTopShared {
     WarpTop warp[NT / 32];
     uint64_t gather[kLpGather];
     uint64_t parts[kLpGather];  // what the blocks of a cluster found, in the first of them
-    uint64_t sorted[kLpMaxTop];
+    uint64_t sorted[kLpMaxTop], best[kLpMaxTop];        // of gather, and of parts
     float group[64];
     int list[kLpGather];
     float floor;
@@ -362,17 +364,14 @@ __device__ __noinline__ uint64_t narrow(WarpTop& t, int top, int n) {
     return lo;
 }
 
-// The `top` largest keys of keys[0 .. n) in falling order (keys are unique, but
-// for 0, which is none), 0 behind.  n at most kLpGather; keys 16-byte aligned.
-template <int NT> __device__ __forceinline__ void sort_top(uint64_t* keys, int n, int top, uint64_t* sorted) {
-    const int tid = (int)threadIdx.x, padded = (n + 7) & ~7;
-    if (tid < top) sorted[tid] = 0;
-    if (tid < padded - n) keys[n + tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += NT) {
+// The `top` largest keys of keys[0 .. n) in falling order into sorted, which was
+// all 0 before.  Keys are unique, but for 0, which is none; n at most kLpGather,
+// keys behind n up to the next multiple of 8 are 0; keys 16-byte aligned.
+template <int NT> __device__ __forceinline__ void sort_top(const uint64_t* keys, int n, int top, uint64_t* sorted) {
+    for (int i = (int)threadIdx.x; i < n; i += NT) {
         const uint64_t k = keys[i];
         int above = 0;
-        for (int j = 0; j < padded; j += 8) {
+        for (int j = 0; j < n; j += 8) {
             ulonglong2 o[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) o[u] = *reinterpret_cast<const ulonglong2*>(keys + j + 2 * u);
@@ -384,7 +383,7 @@ template <int NT> __device__ __forceinline__ void sort_top(uint64_t* keys, int n
     __syncthreads();
 }
 
-// Joins n <= 8 partial results, in order of their place; for the whole first warp.
+// Joins n <= 8 partial results; for a whole warp, whose first lanes have the result.
 __device__ __forceinline__ Soft join_parts(const Soft* parts, int n, float c) {
     const int lane = (int)(threadIdx.x & 31u);
     Soft v = lane < n ? parts[lane] : Soft{kLowest, 0.0f, 0.0f, -INFINITY};
@@ -409,8 +408,12 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
     const RowCut cut = cut_row<BYTES>(x, a.vocab);
     const int64_t v0 = cut.vecs * rank / ranks, v1 = cut.vecs * (rank + 1) / ranks;
     const unsigned char* body = x + (int64_t)cut.head * BYTES;
+    if (TOP) {
+        if (tid == 0) t.listed = t.gathered = 0;
+        if (tid < kLpMaxTop) t.sorted[tid] = t.best[tid] = 0;
+        for (int i = tid; i < kLpGather; i += NT) t.gather[i] = t.parts[i] = 0;
+    }
     if (ranks > 1) cluster_arrive();
-    if (TOP && tid == 0) t.listed = t.gathered = 0;
     dependency_wait();
     allow_dependents();
 
@@ -429,9 +432,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
     if (rank == 0 && tid < cut.head) extra_at = tid, extra = L::load(x, extra_at);
     if (rank == ranks - 1 && tid >= 32 && tid - 32 < cut.tail)
         extra_at = cut.head + cut.vecs * per + (tid - 32), extra = L::load(x, extra_at);
+    // the lead joins the warps' sums while others sort; its first lane writes the row's scores
+    constexpr int kLead = TOP ? NT / 32 - 1 : 0;
     int64_t target = -1;
     float target_logit = 0.0f;
-    if (rank == 0 && tid == 0 && a.targets) {
+    if (rank == 0 && tid == kLead * 32 && a.targets) {
         target = load_id(a.targets, a.id64, row);
         if (target < 0 || target >= a.vocab) target = -1;
         else target_logit = L::load(x, target);
@@ -469,7 +474,38 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
 #pragma unroll
         for (int o = 1; o < NT / 64; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
         if (tid % (NT / 64) == 0) t.group[tid / (NT / 64)] = g;
-        __syncthreads();
+    }
+    __syncthreads();
+    auto finish = [&](Soft v) {
+        // a row of -inf alone has no distribution: its scores are -inf, its entropy 0
+        raise(v, v.top == -INFINITY ? v.m : v.top, a.c);
+        const bool none = v.top == -INFINITY && v.s == 0.0f;
+        const float log_s = none ? 0.0f : logf(v.s);
+        const float m = none ? -INFINITY : v.m;
+        if (a.logprobs)
+            a.logprobs[row] = target < 0 ? 0.0f : none ? -INFINITY : __fdiv_rn(target_logit - m, a.temperature) - log_s;
+        if (ENT) a.entropy[row] = none ? 0.0f : log_s - __fdiv_rn(v.e, v.s) * kLn2;
+        if (a.stats) {
+            a.stats[2 * row] = m;
+            a.stats[2 * row + 1] = log_s;
+        }
+        sh.m = m;
+        sh.log_s = log_s;
+    };
+    if (ranks > 1) cluster_wait();                   // the first block has started
+    if (warp == kLead) {
+        acc = join_parts(sh.warp, NT / 32, a.c);
+        if (lane == 0 && ranks > 1) {
+            const uint32_t to = map_rank0(&sh.part[rank]);
+            st_cluster_f32(to, acc.m);
+            st_cluster_f32(to + 4, acc.s);
+            st_cluster_f32(to + 8, acc.e);
+            st_cluster_f32(to + 12, acc.top);
+        } else if (lane == 0) {
+            finish(acc);
+        }
+    }
+    if (TOP) {
         if (tid < 64) {
             const float own = t.group[tid];
             int above = 0;
@@ -565,63 +601,43 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
                 own = a.top;
             }
             __syncthreads();                         // the gathered ones have been counted
-            if (lane < a.top) t.gather[warp * a.top + lane] = lane < own ? mine.keys[lane] : 0;
             n = NT / 32 * a.top;
+            if (lane < a.top) t.gather[warp * a.top + lane] = lane < own ? mine.keys[lane] : 0;
+            if (tid < 8 && n + tid < kLpGather) t.gather[n + tid] = 0;
             __syncthreads();
         }
         sort_top<NT>(t.gather, n, a.top, t.sorted);
-    } else {
-        __syncthreads();
     }
-    if (warp == 0) acc = join_parts(sh.warp, NT / 32, a.c);
     if (ranks > 1) {
-        cluster_wait();                              // the first block has started
-        if (tid == 0) {
-            const uint32_t to = map_rank0(&sh.part[rank]);
-            st_cluster_f32(to, acc.m);
-            st_cluster_f32(to + 4, acc.s);
-            st_cluster_f32(to + 8, acc.e);
-            st_cluster_f32(to + 12, acc.top);
-        }
         if (TOP && tid < a.top) st_cluster_u64(map_rank0(&t.parts[rank * a.top + tid]), t.sorted[tid]);
         cluster_sync();
         if (rank != 0) return;
-        if (warp == 0) acc = join_parts(sh.part, (int)ranks, a.c);
-        if (TOP) sort_top<NT>(t.parts, (int)ranks * a.top, a.top, t.sorted);
-    }
-    if (tid == 0) {
-        // a row of -inf alone has no distribution: its scores are -inf, its entropy 0
-        raise(acc, acc.top == -INFINITY ? acc.m : acc.top, a.c);
-        const bool none = acc.top == -INFINITY && acc.s == 0.0f;
-        const float log_s = none ? 0.0f : logf(acc.s);
-        const float m = none ? -INFINITY : acc.m;
-        if (a.logprobs)
-            a.logprobs[row] = target < 0 ? 0.0f : none ? -INFINITY : __fdiv_rn(target_logit - m, a.temperature) - log_s;
-        if (ENT) a.entropy[row] = none ? 0.0f : log_s - __fdiv_rn(acc.e, acc.s) * kLn2;
-        if (a.stats) {
-            a.stats[2 * row] = m;
-            a.stats[2 * row + 1] = log_s;
+        if (warp == kLead) {
+            acc = join_parts(sh.part, (int)ranks, a.c);
+            if (lane == 0) finish(acc);
         }
-        if (TOP) {
-            sh.part[0] = {m, log_s, none ? 1.0f : 0.0f, 0.0f};
-            if (t.sorted[a.top - 1] == 0) {
-                // fewer candidates than asked for: the first logits that are -inf (or NaN) fill the list; fewer than
-                // `top` are neither, so that they lie among the first 2 * top
-                int n = 0;
-                while (t.sorted[n] != 0) ++n;
-                for (int64_t i = 0; n < a.top; ++i)
-                    if (!(L::load(x, i) > -INFINITY)) t.sorted[n++] = key_of(-INFINITY, i);
-            }
-        }
+        if (TOP) sort_top<NT>(t.parts, (int)ranks * a.top, a.top, t.best);
     }
     if (TOP) {
-        __syncthreads();
+        uint64_t* list = ranks > 1 ? t.best : t.sorted;
+        if (list[a.top - 1] == 0) {
+            // fewer candidates than asked for: the first logits that are -inf (or NaN) fill the list; fewer than `top`
+            // are neither, so that they lie among the first 2 * top
+            __syncthreads();
+            if (tid == 0) {
+                int n = 0;
+                while (list[n] != 0) ++n;
+                for (int64_t i = 0; n < a.top; ++i)
+                    if (!(L::load(x, i) > -INFINITY)) list[n++] = key_of(-INFINITY, i);
+            }
+            __syncthreads();
+        }
         if (tid < a.top) {
-            const uint64_t k = t.sorted[tid];
-            const float value = key_value(k), m = sh.part[0].m, log_s = sh.part[0].s;
+            const uint64_t k = list[tid];
+            const float m = sh.m;
             a.top_ids[row * a.top + tid] = key_index(k);
             a.top_logprobs[row * a.top + tid] =
-                sh.part[0].e != 0.0f ? -INFINITY : __fdiv_rn(value - m, a.temperature) - log_s;
+                m == -INFINITY ? -INFINITY : __fdiv_rn(key_value(k) - m, a.temperature) - sh.log_s;
         }
     }
 }
