@@ -24,13 +24,11 @@
 // Columns without rows hold further blocks of K, so that a lane scales and adds
 // one sum for four: 14.6, 44.5 and 104 us without.
 // What did not gain: x or h fetched a unit ahead (the same), x held in shared
-// memory (the same), three blocks per SM with 80 registers (one token 15.2 us, two
-// 18.7 where 21.2, 32 the same), partial sums without a barrier (the same), whole
-// K to a warp (117 where 104), a lane's units in registers instead of rings (261).
-// Of the down products: tiles
-// of 32 features, which halve the reading of h (97.8 where 99.1, but 72.5 where
-// 71.6 for sixteen tokens); units cut evenly over all SMs with sums joined in
-// memory (104.4, one token 22.1).
+// memory (the same), partial sums without a barrier (the same), whole K to a warp
+// (117 where 104), a lane's units in registers instead of rings (261).  Of the
+// down products: tiles of 32 features, which halve the reading of h (97.8 where
+// 99.1, but 72.5 where 71.6 for sixteen tokens); units cut evenly over all SMs
+// with sums joined in memory (104.4, one token 22.1).
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 
@@ -275,9 +273,8 @@ constexpr int kUpDepth = 3;
 constexpr int kUpRing = kUpWarps * kUpDepth * kMdStage;
 constexpr int kUpWords = 4 * 33;                        // a warp's partial sums
 constexpr int kUpSums = 2 * kUpWarps * kUpWords * 4;
-constexpr int kUpBlocks = 2;                            // per SM
 
-__global__ void __launch_bounds__(kUpThreads, kUpBlocks) moe_decode_up_kernel(const MdArgs a) {
+template <int BLOCKS> __global__ void __launch_bounds__(kUpThreads, BLOCKS) moe_decode_up_kernel(const MdArgs a) {
     extern __shared__ __align__(16) unsigned char dyn[];
     float* red = reinterpret_cast<float*>(dyn + kUpRing);           // [2][warps][4][33]
     const int stride = list_stride(a.tokens * a.topk);
@@ -603,6 +600,16 @@ template <int NT> fp8q_status_t launch_down(const MdArgs& a, unsigned ranks, siz
     return launch_clusters(moe_decode_down_kernel<NT>, (unsigned)(a.k / 16) * ranks, ranks, NT, bytes(a.tokens, lists), stream, a);
 }
 
+// Two blocks per SM with 116 registers a thread, or three with 80 where that takes
+// all items at once and two would not (16 experts of 768 features: two tokens
+// 18.7 us, with two blocks 21.2; 8 experts 15.2 and 13.8, 81 experts 71.5 and 69.5).
+template <int BLOCKS> fp8q_status_t launch_up(const MdArgs& a, size_t items, size_t smem, size_t most, cudaStream_t stream) {
+    static KernelCache cache;
+    int resident = 0;
+    const fp8q_status_t st = prepare_kernel(cache, moe_decode_up_kernel<BLOCKS>, kUpThreads, most, most, &resident);
+    return st != FP8Q_OK ? st : launch(moe_decode_up_kernel<BLOCKS>, grid_for(items, BLOCKS), kUpThreads, smem, stream, a);
+}
+
 bool valid_row(int64_t k) { return k > 0 && k % MXFP8_BLOCK == 0 && k <= FP8Q_MOE_DECODE_MAX_ROW; }
 
 }  // namespace
@@ -654,12 +661,10 @@ extern "C" fp8q_status_t mxfp8_moe_decode(const uint8_t* codes, const uint8_t* s
                               FP8Q_MOE_DECODE_MAX_TOKENS * (FP8Q_MOE_DECODE_MAX_ROW / 128) * 4;
     const size_t lists = 8 * (size_t)list_stride(choices);
     const size_t up_smem = kUpRing + kUpSums + lists + (size_t)tokens * (size_t)((k + 127) / 128) * 4;
-    static KernelCache up_cache;
-    int resident = 0;
-    const size_t most = std::min((size_t)choices, (size_t)experts + (size_t)choices / kUpRows);     // passes
-    const size_t items = most * (size_t)(n / 32);
-    fp8q_status_t st = prepare_kernel(up_cache, moe_decode_up_kernel, kUpThreads, kMaxUp, kMaxUp, &resident);
-    if (st == FP8Q_OK) st = launch(moe_decode_up_kernel, grid_for(items, kUpBlocks), kUpThreads, up_smem, s, a);
+    const size_t passes = std::min((size_t)choices, (size_t)experts + (size_t)choices / kUpRows);      // at most
+    const size_t items = passes * (size_t)(n / 32), sms = (size_t)sm_count();
+    const fp8q_status_t st = items > 2 * sms && items <= 3 * sms ? launch_up<3>(a, items, up_smem, kMaxUp, s)
+                                                                 : launch_up<2>(a, items, up_smem, kMaxUp, s);
     if (st != FP8Q_OK) return st;
     unsigned ranks = 1;
     while (ranks < kDownMaxCluster && (int64_t)(k / 16) * ranks * 2 <= sm_count()) ranks *= 2;
