@@ -16,8 +16,9 @@
 // 128 rows and 16 columns of a tcgen05 tile would leave a token's 8 experts to 48
 // of the 152 SMs, and their scales would have to be laid out for each expert.
 // This GPU has no e4m3 form of mma.sync: the codes are converted to f16, exactly.
-// The warps' own instructions are the second bound, 220 (gate and up) and 260
-// (down) for a unit of 2 KB of weights, issued in 0.57 of all cycles at 32 tokens.
+// The warps' own instructions are the second bound, 218 (gate and up) and 280
+// (down) for a unit of 2 KB of weights, issued in 0.56 and 0.60 of all cycles at
+// 32 tokens.
 //     one token 13.9 us, eight (15% of the choices dropped) 42.5 us, 5.9 TB/s,
 //     32 tokens 96 us, 5.7 TB/s; through sort, gather, swiglu, matmul and
 //     combine 22, 57.5 (none dropped) and 100.7 us
