@@ -255,6 +255,34 @@ def test_weights_made_just_before():
     assert all(torch.equal(v, want[i % 2]) for i, v in enumerate(got))
 
 
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 6, 8, 9, 11, 20])
+def test_rows_of_one_expert(rows):
+    """Every number of rows that a tile's columns hold, with lengths that end inside a group of four blocks."""
+    for n, k in ((160, 736), (224, 96)):
+        check(layer(rows, 1, 1, n, k, seed=rows + n))
+
+
+@pytest.mark.parametrize("rows", [2, 3, 4, 7, 12])
+def test_nan_stays_with_its_row_of_an_expert(rows):
+    """A row without numbers beside others of the same expert, in the products' columns as in their sums."""
+    s = layer(rows, 1, 1, 96, 224, seed=rows)
+    clean = call(s)
+    for bad in (0, rows - 1):
+        r = dict(s, xc=s["xc"].clone())
+        r["xc"][bad] = 0x7F
+        got = call(r)
+        others = [i for i in range(rows) if i != bad]
+        assert got[bad].isnan().all() and torch.equal(got[others], clean[others])
+
+
+@pytest.mark.parametrize("tokens,topk,n", [(2, 8, 768), (3, 6, 640), (1, 13, 1120)])
+def test_items_between_two_and_three_per_multiprocessor(tokens, topk, n):
+    """Which on 152 of them run with three blocks on each."""
+    s = layer(tokens, topk, 40, n, 256, seed=n)
+    s["ids"] = torch.randperm(40, device="cuda")[:tokens * topk].view(tokens, topk)
+    check(s)
+
+
 def test_refusals_of_the_binding():
     s = layer(4, 2, 3, 64, 96, seed=13)
     with pytest.raises(ValueError, match="ids"):

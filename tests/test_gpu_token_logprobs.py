@@ -233,6 +233,24 @@ def test_long_rows(vocab):
     check(x, t, 1.0, 32)
 
 
+@pytest.mark.parametrize("rows", [70, 71, 72, 141, 142, 143, 304])
+@pytest.mark.parametrize("top", [0, 5])
+def test_rows_around_the_clusters_limits(rows, top):
+    x, t = logits(rows, 40009, torch.float32, seed=rows)
+    check(x, t, 0.8, top)
+
+
+def test_many_long_rows():
+    """So many rows that each is a block's own, with steps that share places: plain, equal, falling and masked ones."""
+    x, t = logits(310, 131075, torch.float32, seed=17)
+    x[1] = 3.0
+    x[2] = x[2].sort(descending=True).values
+    x[3, 5:] = -math.inf
+    x[4, ::2] = x[4].max()
+    x[5] = torch.arange(131075, device="cuda") // 1000
+    check(x, t, 1.0, 8)
+
+
 def test_few_allowed_tokens():
     """Rows of which a grammar leaves a handful of tokens, in any places."""
     x = torch.full((40, 151669), -math.inf, dtype=torch.bfloat16, device="cuda")
