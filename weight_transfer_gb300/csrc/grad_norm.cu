@@ -192,8 +192,8 @@ struct Piece {
     int f32, last;              // last piece of its chunk
 };
 
-// Before the block's shared memory is given up: lets the copies of the ring
-// land that were issued before stage s of this round, but for those of stage
+// Before the block's shared memory is given up: lets the copies land that were
+// issued before stage s in the ring's current turn, but for those of stage
 // `taken`, which the summing warps have had.
 __device__ __noinline__ void land(uint64_t* full, uint32_t round, int s, int taken = -1) {
     for (int i = 0; i < kStages; ++i)

@@ -424,11 +424,11 @@ template <int BLOCKS> __global__ void __launch_bounds__(kUpThreads, BLOCKS) moe_
 // -------------------------------------------- down product, sum over choices ----
 // A block, or a cluster of them where there are few, takes 16 output features
 // of all tokens.  The pairs of a pass and a group of 128 columns of n are cut
-// evenly over its warps; the columns of a tensor-core tile are the two
-// terms of four rows of h.  A warp adds its products, times the choices' weights,
-// to sums of its own, which are joined over the warps and over the cluster's
-// blocks in a fixed order.  The first weights are on their way before h is
-// waited for.
+// evenly over its warps; the columns of a tensor-core tile are the two terms of
+// four rows of h, or of fewer in P blocks of K, as above.  A warp adds its
+// products, times the choices' weights, to sums of its own, which are joined over
+// the warps and over the cluster's blocks in a fixed order.  The first weights are
+// on their way before h is waited for.
 constexpr int kDownDepth = 3;
 constexpr int kDownRows = 4;                            // of a pass
 __host__ __device__ constexpr int down_ring(int threads) { return threads / 32 * kDownDepth * kMdStage; }
