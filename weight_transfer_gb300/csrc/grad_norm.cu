@@ -18,9 +18,10 @@
 // us for its norm (6.85 TB/s; blocks of 256 threads that each read one chunk into
 // registers took 294 to 317).  Eight buckets of 13.1 million, averaged and
 // clipped into others, 97 us: the second reading finds some 40 MB in the
-// second-level cache.  A thousand ragged views into 32-bit buffers, 102 us, as
+// second-level cache.  A thousand ragged views into 32-bit buffers, 98 us, as
 // the copies into shared memory leave the output its own alignment (element by
-// element 188).  Fourteen small tensors: 5.4 us in two launches.
+// element 188).  Fourteen small tensors: 4.8 us in two launches (5.2 where the
+// first chunk is looked up behind the dependency wait).
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 
@@ -39,14 +40,23 @@ constexpr int kStages = 5;
 constexpr uint64_t kGradMaxChunks = 4096;   // chunks grow from one piece so that there are not many more than this
 constexpr int kJoinThreads = 256;
 constexpr uint32_t kNoPriority = ~0u;
+constexpr uint32_t kNear = 16;               // 8 and 32 take as long
 
 // Element types and count share a word: count in the low 44 bits.
+struct GradItem {
+    const void* grad;
+    void* out;
+    uint64_t kind;
+};
 template <int N> struct GradTableN {
     static constexpr int kSize = N;
-    const void* grad[N];
-    void* out[N];
-    uint64_t kind[N];
+    GradItem item[N];
     uint32_t first[N + 1];                  // chunks of the group's earlier tensors
+    // The tensor of every 16th chunk, and the last tensor, between which a look-up searches.  It reads the parameters
+    // one after the other, 300 cycles for each line that is not at hand: 2200 cycles a chunk among a thousand ragged
+    // views without these and with an item's members apart, 1400 as it is (clip_ragged 103 and 98.4 us).  A small
+    // table needs none.
+    uint16_t near[N > kGradFew ? (kGradMaxChunks + 1 + N) / kNear + 2 : 1];
     int count;
 };
 using GradTable = GradTableN<kGradGroup>;
@@ -56,6 +66,7 @@ constexpr uint64_t kGradF32 = 1ull << 62, kOutF32 = 1ull << 63;
 
 template <int N> __device__ __forceinline__ int tensor_of(const GradTableN<N>& t, uint32_t chunk) {
     int lo = 0, hi = t.count - 1;
+    if (N > kGradFew) lo = t.near[chunk / kNear], hi = t.near[chunk / kNear + 1];
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (t.first[mid] <= chunk) lo = mid; else hi = mid - 1;
@@ -158,20 +169,27 @@ __device__ __forceinline__ void bulk_g2s_hint(void* smem_dst, const void* gmem_s
 
 // Where a chunk lies: `vecs` whole vectors from `from` on, element `first` of
 // its tensor; `head` elements in front of the tensor's vectors and `tails`
-// behind them are in the care of its first and its last chunk.
+// behind them, from element `tail` on, are in the care of its first and its last
+// chunk.
 struct Place {
     const unsigned char* from;
-    int64_t first, vecs;
-    int tensor, f32, head, tails;
+    const void* grad;
+    void* out;
+    int64_t first, vecs, tail;
+    int f32, out32, head, tails;
 };
 template <int N> __device__ __forceinline__ Place locate(const GradTableN<N>& t, uint32_t chunk, int64_t chunk_bytes) {
     Place r;
     const int i = tensor_of(t, chunk);
-    r.tensor = i;
-    r.f32 = (t.kind[i] & kGradF32) != 0;
+    const uint64_t kind = t.item[i].kind;
+    const uint32_t begin = t.first[i], end = t.first[i + 1];
+    r.grad = t.item[i].grad;
+    r.out = t.item[i].out;
+    r.f32 = (kind & kGradF32) != 0;
+    r.out32 = (kind & kOutF32) != 0;
     const int shift = r.f32 ? 2 : 1, per = 16 >> shift;
-    const int64_t n = (int64_t)(t.kind[i] & kCountMask), index = chunk - t.first[i], most = chunk_bytes / 16;
-    const unsigned char* p = static_cast<const unsigned char*>(t.grad[i]);
+    const int64_t n = (int64_t)(kind & kCountMask), index = chunk - begin, most = chunk_bytes / 16;
+    const unsigned char* p = static_cast<const unsigned char*>(r.grad);
     const int64_t to = (int64_t)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) >> shift;
     const int64_t head = to < n ? to : n, all = (n - head) >> (4 - shift);
     r.vecs = all - index * most < most ? all - index * most : most;
@@ -179,7 +197,8 @@ template <int N> __device__ __forceinline__ Place locate(const GradTableN<N>& t,
     r.first = head + index * most * per;
     r.from = p + (r.first << shift);
     r.head = index == 0 ? (int)head : 0;
-    r.tails = chunk + 1 == t.first[i + 1] ? (int)(n - head - all * per) : 0;
+    r.tails = chunk + 1 == end ? (int)(n - head - all * per) : 0;
+    r.tail = n - r.tails;
     return r;
 }
 
@@ -220,6 +239,8 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_squares_kernel(cons
         fence_barrier_init();
     }
     __syncthreads();
+    Place at;
+    if (warp == kGradThreads / 32) at = locate(t, blockIdx.x, chunk_bytes);     // parameters need no wait
     dependency_wait();
     allow_dependents();
     if (warp == kGradThreads / 32) {
@@ -242,9 +263,13 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_squares_kernel(cons
             for (int i = 0; i < kStages; ++i)
                 if (i == s) done = chunk_of[i];
             if (done >= 0) {
-                double v = 0.0;
-                for (int w = 0; w < kGradThreads / 32; ++w) v += sums[s][w];
-                partial[done] = v;
+                double v[kGradThreads / 32];
+                for (int w = 0; w < kGradThreads / 32; ++w) v[w] = sums[s][w];
+#pragma unroll
+                for (int n = kGradThreads / 64; n > 0; n /= 2)
+#pragma unroll
+                    for (int w = 0; w < n; ++w) v[w] += v[w + n];
+                partial[done] = v[0];
             }
             return true;
         };
@@ -255,21 +280,14 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_squares_kernel(cons
             if (++s == kStages) s = 0, ++round;
         };
         for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-            const Place at = locate(t, c, chunk_bytes);
+            if (c != blockIdx.x) at = locate(t, c, chunk_bytes);
             int64_t left = at.vecs;
             const unsigned char* from = at.from;
             for (bool first = true; first || left > 0; first = false) {
                 const int v = (int)(left < kPiece / 16 ? left : kPiece / 16);
                 left -= v;
                 if (!take()) return land(full, round, s);
-                Piece& m = info[s];
-                m.tensor = t.grad[at.tensor];
-                m.head = first ? at.head : 0;
-                m.tails = left == 0 ? at.tails : 0;
-                m.tail = (int64_t)(t.kind[at.tensor] & kCountMask) - at.tails;
-                m.vecs = v;
-                m.f32 = at.f32;
-                m.last = left == 0;
+                info[s] = {at.grad, at.tail, first ? at.head : 0, left == 0 ? at.tails : 0, v, at.f32, left == 0};
                 mbar_arrive_expect_tx(&full[s], (uint32_t)v * 16);
                 if (v && kept == kNoPriority) bulk_g2s(ring + s * kPiece, from, (uint32_t)v * 16, &full[s]);
                 else if (v) bulk_g2s_hint(ring + s * kPiece, from, (uint32_t)v * 16, &full[s], c >= kept ? keep : drop);
@@ -445,6 +463,8 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_scale_kernel(const 
         fence_barrier_init();
     }
     __syncthreads();
+    Place at;
+    if (warp == kGradThreads / 32) at = locate(t, chunks - 1 - blockIdx.x, chunk_bytes);
     dependency_wait();
     allow_dependents();
     const float f = (float)(scale * (double)__ldcg(norm + 1));
@@ -459,18 +479,16 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_scale_kernel(const 
             return false;
         };
         for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-            const Place at = locate(t, chunks - 1 - c, chunk_bytes);
-            void* out = t.out[at.tensor];
-            const int out32 = (t.kind[at.tensor] & kOutF32) != 0;
-            if (f == 1.0f && out == t.grad[at.tensor]) continue;            // in place and unchanged
+            if (c != blockIdx.x) at = locate(t, chunks - 1 - c, chunk_bytes);
+            if (f == 1.0f && at.out == at.grad) continue;                   // in place and unchanged
             int64_t left = at.vecs, element = at.first;
             const unsigned char* from = at.from;
             for (bool first = true; first || left > 0; first = false) {
                 const int v = (int)(left < kPiece / 16 ? left : kPiece / 16);
                 left -= v;
                 if (!take()) return land(full, round, s);
-                info[s] = {t.grad[at.tensor], out, element, (int64_t)(t.kind[at.tensor] & kCountMask) - at.tails,
-                           first ? at.head : 0, left == 0 ? at.tails : 0, v, 2 * at.f32 + out32};
+                info[s] = {at.grad, at.out, element, at.tail, first ? at.head : 0, left == 0 ? at.tails : 0, v,
+                           2 * at.f32 + at.out32};
                 mbar_arrive_expect_tx(&full[s], (uint32_t)v * 16);
                 if (v) bulk_g2s_hint(ring + s * kPiece, from, (uint32_t)v * 16, &full[s], drop);
                 from += (int64_t)v * 16;
@@ -590,9 +608,9 @@ template <class F> fp8q_status_t with_table(const GradTable& t, F f) {
     if (t.count > kGradFew) return f(t);
     GradTableN<kGradFew> few;
     for (int i = 0; i < t.count; ++i) {
-        few.grad[i] = t.grad[i];
-        few.out[i] = t.out[i];
-        few.kind[i] = t.kind[i];
+        few.item[i].grad = t.item[i].grad;
+        few.item[i].out = t.item[i].out;
+        few.item[i].kind = t.item[i].kind;
         few.first[i] = t.first[i];
     }
     few.first[t.count] = t.first[t.count];
@@ -693,9 +711,9 @@ extern "C" fp8q_status_t fp8q_grad_plan(const fp8q_grad_t* grads, int count, voi
             const fp8q_grad_t& s = grads[lo + k];
             const int out_type = s.out ? s.out_type : s.grad_type;
             const uintptr_t in = reinterpret_cast<uintptr_t>(s.grad), out = s.out ? reinterpret_cast<uintptr_t>(s.out) : in;
-            t.grad[k] = s.grad;
-            t.out[k] = s.out ? s.out : const_cast<void*>(s.grad);
-            t.kind[k] = s.n | (s.grad_type == FP8Q_F32 ? kGradF32 : 0) | (out_type == FP8Q_F32 ? kOutF32 : 0);
+            t.item[k].grad = s.grad;
+            t.item[k].out = s.out ? s.out : const_cast<void*>(s.grad);
+            t.item[k].kind = s.n | (s.grad_type == FP8Q_F32 ? kGradF32 : 0) | (out_type == FP8Q_F32 ? kOutF32 : 0);
             t.first[k] = chunks;
             chunks += (uint32_t)((s.n * type_bytes(s.grad_type) + (uint64_t)plan.chunk_bytes - 1) / (uint64_t)plan.chunk_bytes);
             if (s.n == 0) continue;
@@ -703,6 +721,11 @@ extern "C" fp8q_status_t fp8q_grad_plan(const fp8q_grad_t* grads, int count, voi
             if (in != out || s.grad_type != out_type) spans[n++] = {in, in + s.n * type_bytes(s.grad_type), 0};
         }
         t.first[t.count] = chunks;
+        int at = 0;
+        for (uint32_t k = 0; k * kNear < chunks + kNear; ++k) {     // up to the first that lies behind the last chunk
+            while (at + 1 < t.count && t.first[at + 1] <= k * kNear) ++at;
+            t.near[k] = (uint16_t)at;
+        }
         plan.chunks += chunks;
     }
     plan.aliased = any_overlap(spans, n);
