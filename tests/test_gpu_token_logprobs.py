@@ -251,6 +251,32 @@ def test_many_long_rows():
     check(x, t, 1.0, 8)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("vocab,stride,offset", [(1, 1, 0), (5, 7, 1), (257, 257, 0), (1000, 1003, 3), (4001, 4001, 1), (12000, 12000, 0),
+                                                 (12289, 12296, 5)])
+def test_many_short_rows(vocab, stride, offset, dtype):
+    """More rows than blocks at once, on both sides of the length from which a row has a block: random, masked, equal and
+    infinite ones, padding's targets among them."""
+    rows = 1217 if vocab > 5000 else 5003
+    x, t = logits(rows, vocab, TYPES[dtype], seed=vocab, stride=stride, offset=offset)
+    x[1] = -math.inf
+    x[2] = torch.finfo(x.dtype).min
+    x[3, 1:] = -math.inf
+    x[4] = 7.0
+    t[5::7] = -1
+    t[6] = vocab
+    check(x, t, 1.0, 0)
+    y = x.clone()
+    y[9, vocab // 2] = math.nan
+    y[10, 0] = math.inf
+    got, want = [w.fp8q_token_logprobs(v, t, want_entropy=True, want_stats=True) for v in (y, x.clone())]
+    assert got[0][10].isnan() or t[10] < 0 or t[10] >= vocab
+    others = torch.ones(rows, dtype=torch.bool, device="cuda")
+    others[9:11] = False
+    for a, b in zip(got, want):
+        assert a is None or torch.equal(a[others].nan_to_num(2.0), b[others].nan_to_num(2.0))
+
+
 def test_few_allowed_tokens():
     """Rows of which a grammar leaves a handful of tokens, in any places."""
     x = torch.full((40, 151669), -math.inf, dtype=torch.bfloat16, device="cuda")
@@ -472,3 +498,18 @@ def test_offsets_past_32_bits():
     g = torch.ones(rows, device="cuda")
     d = w.fp8q_token_logprobs_backward(x, t, st, g, dlogits=x)
     assert torch.equal(d, w.fp8q_token_logprobs_backward(src, t, st, g)) and not flat[vocab:stride].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("vocab,stride,offset", [(1, 1, 0), (5, 7, 1), (257, 257, 0), (1000, 1003, 3), (1500, 1500, 0), (1501, 1504, 1),
+                                                 (3000, 3000, 0), (3001, 3011, 1)])
+def test_gradient_of_many_short_rows(vocab, stride, offset, dtype):
+    """On both sides of the length from which a row has a block of its own."""
+    x, t = logits(1217, vocab, TYPES[dtype], seed=vocab, stride=stride, offset=offset)
+    x[1] = -math.inf
+    x[3, 1:] = -math.inf
+    t[5::7] = -1
+    t[6] = vocab
+    check_gradient(x, t)
+    check_gradient(x, t, bonus=False)
+    check_gradient(x, t, 0.7, policy=False)

@@ -391,6 +391,82 @@ __device__ __forceinline__ Soft join_parts(const Soft* parts, int n, float c) {
     return v;
 }
 
+// A row's scores and statistics from its sums.
+template <bool ENT>
+__device__ __forceinline__ void write_row(const LpArgs& a, int64_t row, int64_t target, float target_logit, Soft v, float& m, float& log_s) {
+    // a row of -inf alone has no distribution: its scores are -inf, its entropy 0
+    raise(v, v.top == -INFINITY ? v.m : v.top, a.c);
+    const bool none = v.top == -INFINITY && v.s == 0.0f;
+    log_s = none ? 0.0f : logf(v.s);
+    m = none ? -INFINITY : v.m;
+    if (a.logprobs)
+        a.logprobs[row] = target < 0 ? 0.0f : none ? -INFINITY : __fdiv_rn(target_logit - m, a.temperature) - log_s;
+    if (ENT) a.entropy[row] = none ? 0.0f : log_s - __fdiv_rn(v.e, v.s) * kLn2;
+    if (a.stats) {
+        a.stats[2 * row] = m;
+        a.stats[2 * row + 1] = log_s;
+    }
+}
+
+// Many short rows: one for each warp, without a barrier.  From eight rows per SM
+// on, of up to 48 KB (9728 rows of 1 KB bf16 logits 7.2 us, of 16 KB 27.0, of 48
+// KB 71.3; with a block to each 32.6, 49.5 and 86.8.  1216 rows of 48 KB 10.8 and
+// 11.5, of 64 KB 18.0 and 14.1; 608 rows of 48 KB 8.6 and 6.6).
+constexpr int kLpRowThreads = 128;
+constexpr int64_t kLpRowBytes = 49152;
+constexpr int kLpRowsPerSm = 8;
+template <int BYTES, bool ENT>
+__global__ void __launch_bounds__(kLpRowThreads, 8) token_logprobs_rows_kernel(const LpArgs a, int64_t rows) {
+    using L = Logit<BYTES>;
+    const int lane = (int)(threadIdx.x & 31u);
+    const int64_t row = (int64_t)blockIdx.x * (kLpRowThreads / 32) + (threadIdx.x >> 5);
+    dependency_wait();
+    allow_dependents();
+    if (row >= rows) return;
+    const unsigned char* x = static_cast<const unsigned char*>(a.logits) + row * a.stride * BYTES;
+    const RowCut cut = cut_row<BYTES>(x, a.vocab);
+    const unsigned char* body = x + (int64_t)cut.head * BYTES;
+    const int vecs = (int)cut.vecs;
+    auto load = [&](uint4 (&v)[kLpUnroll], int base) {
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) {
+            const int i = base + u * 32 + lane;
+            v[u] = i < vecs ? ld_stream(body + 16 * (int64_t)i) : make_uint4(L::kNothing, L::kNothing, L::kNothing, L::kNothing);
+        }
+    };
+    uint4 next[kLpUnroll];
+    load(next, 0);
+    // the elements outside the row's vectors, up to 7 on either side, one for a lane
+    float extra = -INFINITY;
+    if (lane < cut.head) extra = L::load(x, lane);
+    if (lane >= 8 && lane - 8 < cut.tail) extra = L::load(x, cut.head + cut.vecs * L::kPerVec + (lane - 8));
+    int64_t target = -1;
+    float target_logit = 0.0f;
+    if (lane == 0 && a.targets) {
+        target = load_id(a.targets, a.id64, row);
+        if (target < 0 || target >= a.vocab) target = -1;
+        else target_logit = L::load(x, target);
+    }
+    Sums<BYTES, ENT> sums;
+    sums.reset();
+    for (int base = 0; base < vecs; base += 32 * kLpUnroll) {
+        uint4 v[kLpUnroll];
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) v[u] = next[u];
+        if (base + 32 * kLpUnroll < vecs) load(next, base + 32 * kLpUnroll);
+        sums.meet(largest<BYTES>(v), a.c);
+        sums.add(v, a.c);
+    }
+    if (!(extra == -INFINITY)) {
+        sums.meet(extra, a.c);
+        sums.add_one(extra, a.c);
+    }
+    Soft acc = sums.settle(a.c);
+    join_lanes<32>(acc, a.c);
+    float m, log_s;
+    if (lane == 0) write_row<ENT>(a, row, target, target_logit, acc, m, log_s);
+}
+
 template <int BYTES, bool TOP, bool ENT, int NT>
 __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(const LpArgs a) {
     using L = Logit<BYTES>;
@@ -476,22 +552,6 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
         if (tid % (NT / 64) == 0) t.group[tid / (NT / 64)] = g;
     }
     __syncthreads();
-    auto finish = [&](Soft v) {
-        // a row of -inf alone has no distribution: its scores are -inf, its entropy 0
-        raise(v, v.top == -INFINITY ? v.m : v.top, a.c);
-        const bool none = v.top == -INFINITY && v.s == 0.0f;
-        const float log_s = none ? 0.0f : logf(v.s);
-        const float m = none ? -INFINITY : v.m;
-        if (a.logprobs)
-            a.logprobs[row] = target < 0 ? 0.0f : none ? -INFINITY : __fdiv_rn(target_logit - m, a.temperature) - log_s;
-        if (ENT) a.entropy[row] = none ? 0.0f : log_s - __fdiv_rn(v.e, v.s) * kLn2;
-        if (a.stats) {
-            a.stats[2 * row] = m;
-            a.stats[2 * row + 1] = log_s;
-        }
-        sh.m = m;
-        sh.log_s = log_s;
-    };
     if (ranks > 1) cluster_wait();                   // the first block has started
     if (warp == kLead) {
         acc = join_parts(sh.warp, NT / 32, a.c);
@@ -502,7 +562,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
             st_cluster_f32(to + 8, acc.e);
             st_cluster_f32(to + 12, acc.top);
         } else if (lane == 0) {
-            finish(acc);
+            write_row<ENT>(a, row, target, target_logit, acc, sh.m, sh.log_s);
         }
     }
     if (TOP) {
@@ -614,7 +674,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
         if (rank != 0) return;
         if (warp == kLead) {
             acc = join_parts(sh.part, (int)ranks, a.c);
-            if (lane == 0) finish(acc);
+            if (lane == 0) write_row<ENT>(a, row, target, target_logit, acc, sh.m, sh.log_s);
         }
         if (TOP) sort_top<NT>(t.parts, (int)ranks * a.top, a.top, t.best);
     }
@@ -662,21 +722,26 @@ struct LpGradArgs {
 // threads 443; two vectors 452, eight 395).
 constexpr int kLpGradThreads = 128;
 constexpr int kLpGradUnroll = 4;
+// Many rows of up to 6 KB: one for each warp of a block (40,000 rows of 2 KB bf16
+// logits 26.4 us, of 6 KB 76.0; with a block to each 57.5 and 84.9, of 8 KB 97.6
+// and 95.6; 1216 rows of 2 KB 2.5 and 2.9, of 6 KB 4.5 and 3.9).
+constexpr int64_t kLpGradShort = 6000;
 
-// A block takes one part of one row.  VEC: the rows of logits and dlogits lie
+// NT threads take one part of one row, or all of it where a block has several rows.
+// VEC: the rows of logits and dlogits lie
 // alike relative to 16-byte boundaries.
 //   With t = (x - m) c - log2 S:  dx = 2^t (base + slope t), plus g at the
 // target, the last taken after the others.  Logits below m - 4000 / c count as
 // that, whose 2^t is 0, so that no 0 * -inf arises; where bf16 does not tell m
 // from that bound, logits go one by one.
-template <int BYTES, bool ENT, bool VEC>
+template <int BYTES, bool ENT, bool VEC, int NT>
 __global__ void __launch_bounds__(kLpGradThreads) token_logprobs_backward_kernel(const LpGradArgs a) {
     using L = Logit<BYTES>;
     constexpr int per = L::kPerVec;
-    constexpr int NT = kLpGradThreads;
-    const int tid = (int)threadIdx.x;
-    const int64_t row = blockIdx.x / a.parts;
-    const unsigned part = blockIdx.x - (unsigned)row * a.parts;
+    constexpr int kRows = kLpGradThreads / NT;
+    const int tid = (int)threadIdx.x % NT;
+    const int64_t row = kRows > 1 ? (int64_t)blockIdx.x * kRows + threadIdx.x / NT : blockIdx.x / a.parts;
+    const unsigned part = kRows > 1 ? 0u : blockIdx.x - (unsigned)row * a.parts;
     const unsigned char* x = static_cast<const unsigned char*>(a.logits) + row * a.stride * BYTES;
     unsigned char* dx = static_cast<unsigned char*>(a.dlogits) + row * a.dstride * BYTES;
     const RowCut cut = cut_row<BYTES>(x, a.vocab);
@@ -685,6 +750,7 @@ __global__ void __launch_bounds__(kLpGradThreads) token_logprobs_backward_kernel
     unsigned char* dbody = dx + (int64_t)cut.head * BYTES;
     dependency_wait();
     allow_dependents();
+    if (row >= a.rows) return;
     int64_t target = a.targets ? load_id(a.targets, a.id64, row) : -1;
     if (target < 0 || target >= a.vocab) target = -1;
     const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
@@ -818,6 +884,9 @@ fp8q_status_t launch_logprobs(LpArgs a, int64_t rows, cudaStream_t stream) {
 
 template <int BYTES, bool TOP, bool ENT>
 fp8q_status_t launch_logprobs_size(const LpArgs& a, int64_t rows, cudaStream_t stream) {
+    if (!TOP && a.vocab * BYTES <= kLpRowBytes && rows >= kLpRowsPerSm * sm_count())
+        return launch(token_logprobs_rows_kernel<BYTES, ENT>, (unsigned)((rows + kLpRowThreads / 32 - 1) / (kLpRowThreads / 32)),
+                      kLpRowThreads, 0, stream, a, rows);
     return a.vocab * BYTES <= 16384 ? launch_logprobs<BYTES, TOP, ENT, 128>(a, rows, stream)
                                     : launch_logprobs<BYTES, TOP, ENT, 256>(a, rows, stream);
 }
@@ -829,18 +898,23 @@ template <int BYTES> fp8q_status_t launch_logprobs_kind(const LpArgs& a, int64_t
                      : launch_logprobs_size<BYTES, false, false>(a, rows, stream);
 }
 
-template <int BYTES> fp8q_status_t launch_backward(LpGradArgs a, bool vec, cudaStream_t stream) {
-    const int64_t per_block = (int64_t)kLpGradThreads * kLpGradUnroll * 16 / BYTES;
-    int64_t parts = (a.vocab + per_block - 1) / per_block;
-    const int64_t most = 0x7FFFFFFFll / a.rows;
-    a.parts = (unsigned)(parts < most ? parts : most);
-    const unsigned grid = (unsigned)a.rows * a.parts;
+template <int BYTES, int NT> fp8q_status_t launch_backward_size(const LpGradArgs& a, bool vec, unsigned grid, cudaStream_t stream) {
     const bool ent = a.dentropy != nullptr;
     if (vec)
-        return ent ? launch(token_logprobs_backward_kernel<BYTES, true, true>, grid, kLpGradThreads, 0, stream, a)
-                   : launch(token_logprobs_backward_kernel<BYTES, false, true>, grid, kLpGradThreads, 0, stream, a);
-    return ent ? launch(token_logprobs_backward_kernel<BYTES, true, false>, grid, kLpGradThreads, 0, stream, a)
-               : launch(token_logprobs_backward_kernel<BYTES, false, false>, grid, kLpGradThreads, 0, stream, a);
+        return ent ? launch(token_logprobs_backward_kernel<BYTES, true, true, NT>, grid, kLpGradThreads, 0, stream, a)
+                   : launch(token_logprobs_backward_kernel<BYTES, false, true, NT>, grid, kLpGradThreads, 0, stream, a);
+    return ent ? launch(token_logprobs_backward_kernel<BYTES, true, false, NT>, grid, kLpGradThreads, 0, stream, a)
+               : launch(token_logprobs_backward_kernel<BYTES, false, false, NT>, grid, kLpGradThreads, 0, stream, a);
+}
+template <int BYTES> fp8q_status_t launch_backward(LpGradArgs a, bool vec, cudaStream_t stream) {
+    if (a.vocab * BYTES <= kLpGradShort && a.rows >= kLpRowsPerSm * sm_count()) {
+        a.parts = 1;
+        return launch_backward_size<BYTES, 32>(a, vec, (unsigned)((a.rows + kLpGradThreads / 32 - 1) / (kLpGradThreads / 32)), stream);
+    }
+    const int64_t per_block = (int64_t)kLpGradThreads * kLpGradUnroll * 16 / BYTES;
+    const int64_t parts = (a.vocab + per_block - 1) / per_block, most = 0x7FFFFFFFll / a.rows;
+    a.parts = (unsigned)(parts < most ? parts : most);
+    return launch_backward_size<BYTES, kLpGradThreads>(a, vec, (unsigned)a.rows * a.parts, stream);
 }
 
 }  // namespace
