@@ -515,6 +515,7 @@ fp8q_status_t mxfp8_moe_swiglu(const uint8_t* codes, const uint8_t* scales, int6
  * it is held as two f16 terms under a scale per 32 values, 2^-22 of a value.
  * The products are exact, their sums binary32; an infinite h gives NaN or
  * infinities.
+ * Faster than those calls up to about four tokens per chosen expert.
  * Choices whose id lies outside [0, experts) are left out; a token without any
  * gives zeros.  The same id may stand twice in a token.
  *   codes, scales : tokens * k codes, row-major [tokens, k / 32] E8M0 bytes
