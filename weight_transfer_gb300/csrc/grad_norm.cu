@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_squares_kernel(cons
             if (lane < m.head + m.tails) d = (double)(m.f32 ? load_grad<4>(m.tensor, at) : load_grad<2>(m.tensor, at));
             sum += warp_sum(d * d);
         }
+        __syncwarp();                                   // every lane is through with the stage
         if (lane == 0) {
             if (m.last) {
                 sums[s][warp] = sum;
@@ -330,7 +331,6 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_squares_kernel(cons
             }
             asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[s])) : "memory");
         }
-        __syncwarp();
         if (++s == kStages) s = 0, parity ^= 1;
     }
 }
