@@ -39,7 +39,6 @@ constexpr int kPiece = 32768;               // bytes of one copy
 constexpr int kStages = 5;
 constexpr uint64_t kGradMaxChunks = 4096;   // chunks grow from one piece so that there are not many more than this
 constexpr int kJoinThreads = 256;
-constexpr uint32_t kNoPriority = ~0u;
 constexpr uint32_t kNear = 16;               // 8 and 32 take as long
 
 // Element types and count share a word: count in the low 44 bits.
@@ -148,15 +147,11 @@ template <int BYTES> __device__ __forceinline__ double piece_squares(const uint4
     return warp_sum(exact_squares<BYTES>(piece, vecs));
 }
 
-// Eviction priorities in the second-level cache, and bulk_g2s with one.
+// The eviction priority in the second-level cache of what nothing reads again, and
+// bulk_g2s with one.
 __device__ __forceinline__ uint64_t evict_first() {
     uint64_t p;
     asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-__device__ __forceinline__ uint64_t evict_last() {
-    uint64_t p;
-    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
 __device__ __forceinline__ void bulk_g2s_hint(void* smem_dst, const void* gmem_src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
@@ -245,7 +240,7 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_squares_kernel(cons
     allow_dependents();
     if (warp == kGradThreads / 32) {
         if (lane != 0) return;
-        const uint64_t drop = evict_first(), keep = evict_last();
+        const uint64_t drop = evict_first();
         int64_t chunk_of[kStages];                      // chunk that a stage ends, or -1
 #pragma unroll
         for (int s = 0; s < kStages; ++s) chunk_of[s] = -1;
@@ -289,8 +284,8 @@ __global__ void __launch_bounds__(kGradThreads + 32, 1) grad_squares_kernel(cons
                 if (!take()) return land(full, round, s);
                 info[s] = {at.grad, at.tail, first ? at.head : 0, left == 0 ? at.tails : 0, v, at.f32, left == 0};
                 mbar_arrive_expect_tx(&full[s], (uint32_t)v * 16);
-                if (v && kept == kNoPriority) bulk_g2s(ring + s * kPiece, from, (uint32_t)v * 16, &full[s]);
-                else if (v) bulk_g2s_hint(ring + s * kPiece, from, (uint32_t)v * 16, &full[s], c >= kept ? keep : drop);
+                if (v && c >= kept) bulk_g2s(ring + s * kPiece, from, (uint32_t)v * 16, &full[s]);
+                else if (v) bulk_g2s_hint(ring + s * kPiece, from, (uint32_t)v * 16, &full[s], drop);
                 from += (int64_t)v * 16;
                 next(left == 0 ? (int64_t)c : -1);
             }
@@ -595,12 +590,14 @@ template <auto KERNEL, class... Args> fp8q_status_t launch_ring(uint32_t chunks,
 }
 
 // The first of the chunks that the sums leave in the second-level cache for the
-// clipping, which takes them first: 64 MB of the last launch's (clip_buckets
-// 97.3 us; with 32 MB 100.8, 96 MB 99.4, no priorities 101.5, forwards 108.7).
-uint32_t kept_from(const Plan& plan, uint32_t chunks, bool keep) {
-    if (!keep) return kNoPriority;
+// clipping, which takes them first: 64 MB of the last launch's.  What is read
+// before them is evicted first (clip_buckets 96.5 us; without priorities 101.7,
+// forwards 108.7).  None is given that would outlive the call: with evict_last
+// on the 64 MB, as fast, what ran next found them in its way (of 80 MB read a
+// second time 47 MB came from HBM after a step that clipped nothing, 4 MB now).
+uint32_t kept_from(const Plan& plan, uint32_t chunks, bool clips_next) {
     const uint64_t kept = (64ull << 20) / (uint64_t)plan.chunk_bytes;
-    return kept < chunks ? chunks - (uint32_t)kept : 0;
+    return clips_next && kept < chunks ? chunks - (uint32_t)kept : 0;
 }
 
 // f on the table, or on a smaller one that holds it: the launch carries it along.
