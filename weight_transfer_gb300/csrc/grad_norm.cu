@@ -11,8 +11,8 @@
 //
 // A thread sums 64 squares in binary32, in eight chains, a warp its threads'
 // sums, and everything above is binary64 (of which this GPU does two additions
-// a cycle and SM).  Sums outside [2^-80, 2^100] would lose squares to the range
-// of binary32; their elements are summed again in binary64.
+// a cycle and SM).  A warp's sum outside [2^-80, 2^100] would lose squares to the
+// range of binary32; its elements are squared again under a power of two.
 //
 // Both passes are bound by HBM.  A layer of 623 million bf16 gradients takes 182
 // us for its norm (6.85 TB/s; blocks of 256 threads that each read one chunk into
@@ -78,9 +78,11 @@ template <int BYTES> __device__ __forceinline__ float load_grad(const void* p, i
 }
 
 // Sum of the squares of a thread's vectors tid, tid + kGradThreads, ... of a
-// piece, in eight chains of binary32 (up to 64 squares).
-template <int BYTES> __device__ __forceinline__ float squares(const uint4* piece, int vecs) {
+// piece, in eight chains of binary32 (up to 64 squares); SCALED: of the elements
+// times `factor`, a power of two.
+template <int BYTES, bool SCALED = false> __device__ __forceinline__ float squares(const uint4* piece, int vecs, float factor = 1.0f) {
     constexpr int kLoads = kPiece / 16 / kGradThreads;
+    const uint64_t factors = f2_pack(factor, factor);
     uint64_t s[4] = {0, 0, 0, 0};
     uint4 v[kLoads];
 #pragma unroll
@@ -94,13 +96,15 @@ template <int BYTES> __device__ __forceinline__ float squares(const uint4* piece
         if (BYTES == 2) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint64_t x = f2_pack(bf16_lo(w[j]), bf16_hi(w[j]));
+                uint64_t x = f2_pack(bf16_lo(w[j]), bf16_hi(w[j]));
+                if (SCALED) x = f2_mul(x, factors);
                 s[j] = f2_fma(x, x, s[j]);
             }
         } else {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const uint64_t x = f2_pack(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+                uint64_t x = f2_pack(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+                if (SCALED) x = f2_mul(x, factors);
                 s[(u & 1) * 2 + j] = f2_fma(x, x, s[(u & 1) * 2 + j]);
             }
         }
@@ -110,41 +114,35 @@ template <int BYTES> __device__ __forceinline__ float squares(const uint4* piece
     return a + b;
 }
 
-// The same in binary64: squares whose sum left the range in which binary32
-// keeps them all.  Nothing but zeros needs no binary64.
-template <int BYTES> __device__ __noinline__ double exact_squares(const uint4* piece, int vecs) {
-    double d = 0.0;
-    uint32_t any = 0;
-    for (int i = (int)threadIdx.x; i < vecs; i += kGradThreads) any |= piece[i].x | piece[i].y | piece[i].z | piece[i].w;
-    if ((any & (BYTES == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu)) == 0) return 0.0;
-    for (int i = (int)threadIdx.x; i < vecs; i += kGradThreads)
-        for (int j = 0; j < 16 / BYTES; ++j) {
-            const double x = (double)load_grad<BYTES>(piece + i, j);
-            d += x * x;
-        }
-    return d;
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
 }
-
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
 
-// A warp's sum of its vectors' squares, in lane 0: over the lanes in binary32
-// where all their sums are within range.
+// A warp's sum of its vectors' squares, where binary32 loses some of them.
+// Below 2^-80 all elements are below 2^-40, and times 2^86 the smallest still
+// has a square of 2^-126; otherwise the elements go times 2^-70, where even 2048
+// of the largest stay below 2^127, and squares that vanish have no weight beside
+// one above 2^89.
+template <int BYTES> __device__ __noinline__ double scaled_squares(const uint4* piece, int vecs, bool small) {
+    const float v = warp_sum(squares<BYTES, true>(piece, vecs, small ? 0x1p86f : 0x1p-70f));
+    return (double)v * (small ? 0x1p-172 : 0x1p140);
+}
+
+// A warp's sum of its vectors' squares.  Up to 2048 squares that vanish, or keep
+// few bits, are off by 2^-150 each, which does not count beside 2^-80.  (64 Mi bf16
+// gradients of 1e-14: 35 us, of 1e-3 27; with binary64 squares 408.)
 template <int BYTES> __device__ __forceinline__ double piece_squares(const uint4* piece, int vecs) {
-    float v = squares<BYTES>(piece, vecs);
-    if (__all_sync(0xFFFFFFFFu, v == 0.0f || (v >= 0x1p-80f && v <= 0x1p100f))) {
-        // a sum of 0 may be one of squares that vanished: then nothing larger than 2^-74 is among them, which counts
-        // only where the whole warp has no more
-        if (__any_sync(0xFFFFFFFFu, v != 0.0f)) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            return (double)v;
-        }
-    }
-    return warp_sum(exact_squares<BYTES>(piece, vecs));
+    const float v = squares<BYTES>(piece, vecs);
+    const bool within = __all_sync(0xFFFFFFFFu, v <= 0x1p100f);     // a NaN is not
+    const float sum = warp_sum(v);
+    return within && sum >= 0x1p-80f ? (double)sum : scaled_squares<BYTES>(piece, vecs, within);
 }
 
 // The eviction priority in the second-level cache of what nothing reads again, and
