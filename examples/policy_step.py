@@ -54,8 +54,14 @@ class Trainer:
         self.clipped = [torch.empty(p.numel(), dtype=torch.bfloat16, device=p.device) for p in self.parameters]
         self.grads = fp8q.fp8q_grad_list([p.grad for p in self.parameters], self.clipped)
 
+    def zero_grad(self):
+        for p in self.parameters:
+            p.grad.zero_()
+
     def send(self):
         """The gradients (sums over the ranks) averaged, clipped and quantized -> (norm and coefficient, codes, scales)."""
+        if not self.grads.holds(p.grad for p in self.parameters):
+            raise RuntimeError("a gradient was replaced: use zero_grad(), which keeps the buffers")
         norm, _ = fp8q.fp8q_grad_clip(self.grads, self.max_norm, scale=1.0 / self.ranks)
         codes, scales = fp8q.fp8q_quantize_blockwise_group(self.clipped, self.fmt)
         return norm, codes, scales

@@ -16,7 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import Iterable, Optional, Sequence
 
 import torch
 
@@ -1188,7 +1188,12 @@ class fp8q_grad_list:
     """Gradient tensors (bf16 or float32, contiguous, any alignment), checked and
     laid out once for fp8q_grad_norm and fp8q_grad_clip, as a training loop with
     lasting gradient buffers keeps them.  `outs`: where the clipped gradients go
-    (bf16 or float32, the same number of elements each); in place without."""
+    (bf16 or float32, the same number of elements each); in place without.
+
+    The list holds these tensors and their memory, not the parameters: where a
+    gradient is replaced (torch's zero_grad() sets them to None, after which the
+    next backward pass makes new ones; zero_grad(set_to_none=False) does not),
+    the calls go on with the old one.  `holds` says whether that has happened."""
 
     def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
         grads = list(grads)
@@ -1216,6 +1221,15 @@ class fp8q_grad_list:
         workspace = _sz(0)
         _check("fp8q_grad_plan", _lib.fp8q_grad_plan(arr, self.count, self.plan, need, ctypes.byref(workspace)))
         self.workspace_bytes = int(workspace.value)
+        self._laid_out = arr
+
+    def holds(self, grads: Iterable[Optional[torch.Tensor]]) -> bool:
+        """Whether these are the list's gradients: as many, in the same memory,
+        of the same types and sizes."""
+        grads = list(grads)
+        return len(grads) == self.count and all(
+            g is not None and (g.data_ptr() or None, g.numel(), _GRAD_TYPES.get(g.dtype)) == (a.grad, a.n, a.grad_type)
+            for g, a in zip(grads, self._laid_out))
 
 
 def _grad_call(name: str, grads, max_norm, scale, want_each, norm, each, workspace, stream):
