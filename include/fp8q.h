@@ -569,6 +569,18 @@ fp8q_status_t fp8q_token_logprobs(const void* logits, int logit_bytes, int64_t r
                                   float* entropy, float* top_logprobs, int32_t* top_ids, float* stats,
                                   fp8q_stream_t stream);
 
+/* Flag of fp8q_token_logprobs_ex and fp8q_token_logprobs_backward_ex: the
+ * targets need only be aligned to id_bytes, and the arrays of 32-bit numbers per
+ * row to 4 bytes (parts of longer arrays, such as labels shifted by one).
+ * Results and time are the same.  Unknown flag bits give FP8Q_ERR_FLAGS. */
+#define FP8Q_ELEMENT_ALIGNED 2u
+
+/* fp8q_token_logprobs with flags (FP8Q_ELEMENT_ALIGNED). */
+fp8q_status_t fp8q_token_logprobs_ex(const void* logits, int logit_bytes, int64_t rows, int64_t vocab, int64_t stride,
+                                     const void* targets, int id_bytes, float temperature, int top, float* logprobs,
+                                     float* entropy, float* top_logprobs, int32_t* top_ids, float* stats,
+                                     unsigned int flags, fp8q_stream_t stream);
+
 /* Gradient of logprobs and entropy (the alternatives have none):
  *     dlogits[r, j] = ([j = target] g - p_j (g + dH (log p_j + entropy))) / T
  * with g = dlogprobs[r] (0 where the target lies outside [0, vocab)) and dH =
@@ -583,6 +595,12 @@ fp8q_status_t fp8q_token_logprobs_backward(const void* logits, int logit_bytes, 
                                            const void* targets, int id_bytes, float temperature, const float* stats,
                                            const float* dlogprobs, const float* entropy, const float* dentropy,
                                            void* dlogits, int64_t dstride, fp8q_stream_t stream);
+
+/* fp8q_token_logprobs_backward with flags (FP8Q_ELEMENT_ALIGNED). */
+fp8q_status_t fp8q_token_logprobs_backward_ex(const void* logits, int logit_bytes, int64_t rows, int64_t vocab, int64_t stride,
+                                              const void* targets, int id_bytes, float temperature, const float* stats,
+                                              const float* dlogprobs, const float* entropy, const float* dentropy,
+                                              void* dlogits, int64_t dstride, unsigned int flags, fp8q_stream_t stream);
 
 /* ------------------------------------------- norm and clipping of gradients ----
  * The global norm of many gradient tensors, and the gradients clipped by it:

@@ -78,6 +78,7 @@ FP8Q_MOE_DECODE_MAX_TOKENS = 32
 FP8Q_MOE_DECODE_MAX_ROW = 16384
 FP8Q_MAX_VOCAB = 1 << 30
 FP8Q_MAX_TOP = 32
+FP8Q_ELEMENT_ALIGNED = 2
 FP8Q_BF16 = 0
 FP8Q_F32 = 1
 FP8Q_MAX_GRADS = 16384
@@ -157,6 +158,10 @@ _SIGNATURES = {
                           _vp], _int),
     "fp8q_token_logprobs": ([_vp, _int, _i64, _i64, _i64, _vp, _int, _f32, _int, _vp, _vp, _vp, _vp, _vp, _vp], _int),
     "fp8q_token_logprobs_backward": ([_vp, _int, _i64, _i64, _i64, _vp, _int, _f32, _vp, _vp, _vp, _vp, _vp, _i64, _vp], _int),
+    "fp8q_token_logprobs_ex": ([_vp, _int, _i64, _i64, _i64, _vp, _int, _f32, _int, _vp, _vp, _vp, _vp, _vp, ctypes.c_uint, _vp],
+                               _int),
+    "fp8q_token_logprobs_backward_ex": ([_vp, _int, _i64, _i64, _i64, _vp, _int, _f32, _vp, _vp, _vp, _vp, _vp, _i64,
+                                         ctypes.c_uint, _vp], _int),
     "fp8q_grad_plan_bytes": ([_int], _sz),
     "fp8q_grad_plan": ([ctypes.POINTER(fp8q_grad_t), _int, _vp, _sz, ctypes.POINTER(_sz)], _int),
     "fp8q_grad_norm": ([_vp, _f64, _f64, _vp, _vp, _vp, _sz, _vp], _int),
@@ -1105,7 +1110,8 @@ def fp8q_token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = 
     int32 or int64 [rows] (one outside [0, vocab) scores 0) -> (logprobs float32
     [rows] or None, entropy float32 [rows] or None, top_logprobs float32 [rows,
     top] or None, top_ids int32 [rows, top] or None, stats float32 [rows, 2] or
-    None), of softmax(logits / temperature).  stats is what the gradient reads."""
+    None), of softmax(logits / temperature).  stats is what the gradient reads.
+    Contiguous parts of longer arrays (labels[1:], stats[a:b]) will do."""
     d = _device_of(logits, "logits")
     xp, size, rows, vocab, stride = _logits(logits, "logits")
     f32 = torch.float32
@@ -1125,8 +1131,8 @@ def fp8q_token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = 
         raise ValueError("top_logprobs or top_ids without top")
     if want_stats or stats is not None:
         stats, sp = _made(stats, "stats", f32, (rows, 2), rows * 2, logits, d, stream)
-    st = _lib.fp8q_token_logprobs(xp, size, rows, vocab, stride, tp, id_bytes, temperature, top, lp, ep, vp, ip, sp,
-                                  _stream(stream))
+    st = _lib.fp8q_token_logprobs_ex(xp, size, rows, vocab, stride, tp, id_bytes, temperature, top, lp, ep, vp, ip, sp,
+                                     FP8Q_ELEMENT_ALIGNED, _stream(stream))
     if st:
         _check("fp8q_token_logprobs", st)
     return logprobs, entropy, top_logprobs, top_ids, stats
@@ -1173,8 +1179,8 @@ def fp8q_token_logprobs_backward(logits: torch.Tensor, targets: Optional[torch.T
     elif dlogits.get_device() != d:
         raise ValueError(f"dlogits is on cuda:{dlogits.get_device()}, the logits on cuda:{d}")
     dp, _, _, _, dstride = _logits(dlogits, "dlogits")
-    st = _lib.fp8q_token_logprobs_backward(xp, size, rows, vocab, stride, tp, id_bytes, temperature, sp, gp, ep, hp, dp, dstride,
-                                           _stream(stream))
+    st = _lib.fp8q_token_logprobs_backward_ex(xp, size, rows, vocab, stride, tp, id_bytes, temperature, sp, gp, ep, hp, dp,
+                                              dstride, FP8Q_ELEMENT_ALIGNED, _stream(stream))
     if st:
         _check("fp8q_token_logprobs_backward", st)
     return dlogits

@@ -917,13 +917,15 @@ template <int BYTES> fp8q_status_t launch_backward(LpGradArgs a, bool vec, cudaS
     return launch_backward_size<BYTES, kLpGradThreads>(a, vec, (unsigned)a.rows * a.parts, stream);
 }
 
-}  // namespace
+// A row's ids and numbers are read and written one by one, so that their own size is all the alignment they need.
+bool aligned_for(const void* p, int bytes, unsigned flags) {
+    return reinterpret_cast<uintptr_t>(p) % (flags & FP8Q_ELEMENT_ALIGNED ? (unsigned)bytes : 16u) == 0;
+}
 
-extern "C" fp8q_status_t fp8q_token_logprobs(const void* logits, int logit_bytes, int64_t rows, int64_t vocab, int64_t stride,
-                                             const void* targets, int id_bytes, float temperature, int top,
-                                             float* logprobs, float* entropy, float* top_logprobs, int32_t* top_ids,
-                                             float* stats, fp8q_stream_t stream) {
-    FP8Q_NVTX_RANGE("fp8q_token_logprobs");
+fp8q_status_t logprobs_entry(const void* logits, int logit_bytes, int64_t rows, int64_t vocab, int64_t stride, const void* targets,
+                             int id_bytes, float temperature, int top, float* logprobs, float* entropy, float* top_logprobs,
+                             int32_t* top_ids, float* stats, unsigned flags, fp8q_stream_t stream) {
+    if (flags & ~FP8Q_ELEMENT_ALIGNED) return FP8Q_ERR_FLAGS;
     const fp8q_status_t st = check_logits(rows, vocab, stride, logit_bytes, id_bytes, temperature);
     if (st != FP8Q_OK) return st;
     if (top < 0 || top > FP8Q_MAX_TOP || top > vocab) return FP8Q_ERR_K;
@@ -932,9 +934,9 @@ extern "C" fp8q_status_t fp8q_token_logprobs(const void* logits, int logit_bytes
     if ((top > 0) != (top_logprobs != nullptr) || (top > 0) != (top_ids != nullptr)) return FP8Q_ERR_NULL;
     if (!logprobs && !entropy && !top && !stats) return FP8Q_ERR_NULL;
     if (reinterpret_cast<uintptr_t>(logits) % (unsigned)logit_bytes) return FP8Q_ERR_ALIGN;
-    if (!aligned16(targets) || !aligned16(logprobs) || !aligned16(entropy) || !aligned16(top_logprobs) ||
-        !aligned16(top_ids) || !aligned16(stats))
-        return FP8Q_ERR_ALIGN;
+    if (!aligned_for(targets, id_bytes, flags)) return FP8Q_ERR_ALIGN;
+    for (const void* p : {(const void*)logprobs, (const void*)entropy, (const void*)top_logprobs, (const void*)top_ids, (const void*)stats})
+        if (!aligned_for(p, 4, flags)) return FP8Q_ERR_ALIGN;
     const size_t r = (size_t)rows;
     const Range outs[] = {{logprobs, 4 * r}, {entropy, 4 * r}, {top_logprobs, 4 * r * top}, {top_ids, 4 * r * top},
                           {stats, 8 * r}};
@@ -946,12 +948,11 @@ extern "C" fp8q_status_t fp8q_token_logprobs(const void* logits, int logit_bytes
     return logit_bytes == 2 ? launch_logprobs_kind<2>(a, rows, s) : launch_logprobs_kind<4>(a, rows, s);
 }
 
-extern "C" fp8q_status_t fp8q_token_logprobs_backward(const void* logits, int logit_bytes, int64_t rows, int64_t vocab,
-                                                      int64_t stride, const void* targets, int id_bytes, float temperature,
-                                                      const float* stats, const float* dlogprobs, const float* entropy,
-                                                      const float* dentropy, void* dlogits, int64_t dstride,
-                                                      fp8q_stream_t stream) {
-    FP8Q_NVTX_RANGE("fp8q_token_logprobs_backward");
+fp8q_status_t logprobs_backward_entry(const void* logits, int logit_bytes, int64_t rows, int64_t vocab, int64_t stride,
+                                      const void* targets, int id_bytes, float temperature, const float* stats,
+                                      const float* dlogprobs, const float* entropy, const float* dentropy, void* dlogits,
+                                      int64_t dstride, unsigned flags, fp8q_stream_t stream) {
+    if (flags & ~FP8Q_ELEMENT_ALIGNED) return FP8Q_ERR_FLAGS;
     fp8q_status_t st = check_logits(rows, vocab, stride, logit_bytes, id_bytes, temperature);
     if (st == FP8Q_OK) st = check_logits(rows, vocab, dstride, logit_bytes, id_bytes, temperature);
     if (st != FP8Q_OK) return st;
@@ -961,8 +962,9 @@ extern "C" fp8q_status_t fp8q_token_logprobs_backward(const void* logits, int lo
     if (!dlogprobs && !dentropy) return FP8Q_ERR_NULL;
     if (reinterpret_cast<uintptr_t>(logits) % (unsigned)logit_bytes || reinterpret_cast<uintptr_t>(dlogits) % (unsigned)logit_bytes)
         return FP8Q_ERR_ALIGN;
-    if (!aligned16(targets) || !aligned16(stats) || !aligned16(dlogprobs) || !aligned16(entropy) || !aligned16(dentropy))
-        return FP8Q_ERR_ALIGN;
+    if (!aligned_for(targets, id_bytes, flags)) return FP8Q_ERR_ALIGN;
+    for (const float* p : {stats, dlogprobs, entropy, dentropy})
+        if (!aligned_for(p, 4, flags)) return FP8Q_ERR_ALIGN;
     const size_t r = (size_t)rows;
     const Range out[] = {{dlogits, span(rows, vocab, dstride, logit_bytes)}};
     const bool in_place = dlogits == logits && dstride == stride;
@@ -975,4 +977,44 @@ extern "C" fp8q_status_t fp8q_token_logprobs_backward(const void* logits, int lo
     const bool vec = apart % 16 == 0 && (rows == 1 || (uint64_t)(stride - dstride) * (unsigned)logit_bytes % 16 == 0);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return logit_bytes == 2 ? launch_backward<2>(a, vec, s) : launch_backward<4>(a, vec, s);
+}
+
+}  // namespace
+
+extern "C" fp8q_status_t fp8q_token_logprobs(const void* logits, int logit_bytes, int64_t rows, int64_t vocab, int64_t stride,
+                                             const void* targets, int id_bytes, float temperature, int top,
+                                             float* logprobs, float* entropy, float* top_logprobs, int32_t* top_ids,
+                                             float* stats, fp8q_stream_t stream) {
+    FP8Q_NVTX_RANGE("fp8q_token_logprobs");
+    return logprobs_entry(logits, logit_bytes, rows, vocab, stride, targets, id_bytes, temperature, top, logprobs, entropy,
+                          top_logprobs, top_ids, stats, 0, stream);
+}
+
+extern "C" fp8q_status_t fp8q_token_logprobs_ex(const void* logits, int logit_bytes, int64_t rows, int64_t vocab, int64_t stride,
+                                                const void* targets, int id_bytes, float temperature, int top,
+                                                float* logprobs, float* entropy, float* top_logprobs, int32_t* top_ids,
+                                                float* stats, unsigned int flags, fp8q_stream_t stream) {
+    FP8Q_NVTX_RANGE("fp8q_token_logprobs_ex");
+    return logprobs_entry(logits, logit_bytes, rows, vocab, stride, targets, id_bytes, temperature, top, logprobs, entropy,
+                          top_logprobs, top_ids, stats, flags, stream);
+}
+
+extern "C" fp8q_status_t fp8q_token_logprobs_backward(const void* logits, int logit_bytes, int64_t rows, int64_t vocab,
+                                                      int64_t stride, const void* targets, int id_bytes, float temperature,
+                                                      const float* stats, const float* dlogprobs, const float* entropy,
+                                                      const float* dentropy, void* dlogits, int64_t dstride,
+                                                      fp8q_stream_t stream) {
+    FP8Q_NVTX_RANGE("fp8q_token_logprobs_backward");
+    return logprobs_backward_entry(logits, logit_bytes, rows, vocab, stride, targets, id_bytes, temperature, stats, dlogprobs,
+                                   entropy, dentropy, dlogits, dstride, 0, stream);
+}
+
+extern "C" fp8q_status_t fp8q_token_logprobs_backward_ex(const void* logits, int logit_bytes, int64_t rows, int64_t vocab,
+                                                         int64_t stride, const void* targets, int id_bytes,
+                                                         float temperature, const float* stats, const float* dlogprobs,
+                                                         const float* entropy, const float* dentropy, void* dlogits,
+                                                         int64_t dstride, unsigned int flags, fp8q_stream_t stream) {
+    FP8Q_NVTX_RANGE("fp8q_token_logprobs_backward_ex");
+    return logprobs_backward_entry(logits, logit_bytes, rows, vocab, stride, targets, id_bytes, temperature, stats, dlogprobs,
+                                   entropy, dentropy, dlogits, dstride, flags, stream);
 }
