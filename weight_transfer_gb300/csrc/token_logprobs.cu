@@ -722,10 +722,13 @@ struct LpGradArgs {
 // threads 443; two vectors 452, eight 395).
 constexpr int kLpGradThreads = 128;
 constexpr int kLpGradUnroll = 4;
-// Many rows of up to 6 KB: one for each warp of a block (40,000 rows of 2 KB bf16
-// logits 26.4 us, of 6 KB 76.0; with a block to each 57.5 and 84.9, of 8 KB 97.6
-// and 95.6; 1216 rows of 2 KB 2.5 and 2.9, of 6 KB 4.5 and 3.9).
-constexpr int64_t kLpGradShort = 6000;
+// Many short rows go to a warp each: of up to 4 KB from eight rows per SM on (1216
+// rows of 2 KB bf16 logits 2.1 us, with a block to each 2.4, of 4 KB 2.8 and 2.8;
+// 608 rows of 2 KB 2.0 and 1.9), of up to 6 KB from twelve (1824 rows of 6 KB 3.8
+// and 4.1, 19,456 37.2 and 38.7; 1520 rows 3.7 and 3.4, 1216 3.4 and 3.2; of 8 KB
+// 40,000 rows 97.6 and 95.6).
+constexpr int64_t kLpGradShort = 4096, kLpGradMedium = 6000;
+constexpr int kLpGradShortRowsPerSm = 8, kLpGradMediumRowsPerSm = 12;
 
 // NT threads take one part of one row, or all of it where a block has several rows.
 // VEC: the rows of logits and dlogits lie
@@ -907,7 +910,8 @@ template <int BYTES, int NT> fp8q_status_t launch_backward_size(const LpGradArgs
                : launch(token_logprobs_backward_kernel<BYTES, false, false, NT>, grid, kLpGradThreads, 0, stream, a);
 }
 template <int BYTES> fp8q_status_t launch_backward(LpGradArgs a, bool vec, cudaStream_t stream) {
-    if (a.vocab * BYTES <= kLpGradShort && a.rows >= kLpRowsPerSm * sm_count()) {
+    const int64_t bytes = a.vocab * BYTES;
+    if (bytes <= kLpGradMedium && a.rows >= (bytes <= kLpGradShort ? kLpGradShortRowsPerSm : kLpGradMediumRowsPerSm) * sm_count()) {
         a.parts = 1;
         return launch_backward_size<BYTES, 32>(a, vec, (unsigned)((a.rows + kLpGradThreads / 32 - 1) / (kLpGradThreads / 32)), stream);
     }
