@@ -555,7 +555,9 @@ fp8q_status_t mxfp8_moe_decode(const uint8_t* codes, const uint8_t* scales, cons
  *   entropy, stats : rows and rows * 2 floats, or NULL
  *   top_logprobs, top_ids : rows * top, or NULL when top == 0
  * At least one output has to be asked for (FP8Q_ERR_NULL).  All arithmetic is
- * binary32; exponentials carry 2^-22 relative and are 0 below 2^-126.  A logit
+ * binary32; exponentials carry 2^-22 relative and are 0 below 2^-126.  At most 256
+ * terms are added one after another, whatever vocab: log S is within 2^-24 (320 +
+ * 3 E|z|), z = (x - m) / T, and the entropy within 1 + E|z| times that.  A logit
  * of -inf is a masked one; in a row of nothing else the scores are -inf, the
  * entropy 0 and stats (-inf, 0).  A row that holds +inf or NaN has NaN scores; among its
  * alternatives +inf counts as the largest, NaN as -inf.

@@ -49,6 +49,7 @@ struct LpArgs {
     float temperature, c;       // c = log2(e) / temperature
     int top;
     int fold;                   // steps that share a place of the stored maxima
+    int far;                    // where the far sums lie in the dynamic shared memory
     float* logprobs;            // each NULL when not wanted
     float* entropy;
     float* top_logprobs;
@@ -157,6 +158,38 @@ template <int LANES> __device__ __forceinline__ void join_lanes(Soft& a, float c
     }
 }
 
+// The far sums.  A thread's own chains take no more than 256 terms one after
+// another; then what they hold is added, with what that addition rounds off, to
+// sums in shared memory, so that a row's error does not grow with its length:
+// equal terms that are rounded the same way every time were off by 1e-4 at 200
+// million logits, 5e-7 at 151,936, and are 9e-7 at any length now.  They have an
+// instance of the kernel of their own (FAR): rows of which a block's share is
+// shorter would take 0.7% longer, four rows 3%.
+constexpr int kLpChain = 256;
+template <int BYTES> constexpr int kLpFarSteps = kLpChain * BYTES / 16;     // a step adds 8 bf16 or 4 binary32 terms to a chain
+template <int NT> struct LpFar {
+    float m[NT], s[NT], s_off[NT], e[NT], e_off[NT];
+};
+__device__ __forceinline__ void add_off(float& sum, float& off, float x) {  // sum + off += x, what is rounded off goes to off
+    const float t = sum + x, b = t - sum;
+    off += (sum - (t - b)) + (x - b);
+    sum = t;
+}
+// Brings a thread's far sums to the reference m, not below theirs, and adds s and e.
+template <int NT> __device__ __noinline__ void add_far(LpFar<NT>& far, float m, float s, float e, float c) {
+    const int i = (int)threadIdx.x;
+    const float d = fmaxf((far.m[i] - m) * c, -1000.0f), f = ex2(d);
+    float fe = f * (far.e[i] + d * far.s[i]), fe_off = f * (far.e_off[i] + d * far.s_off[i]);
+    float fs = f * far.s[i], fs_off = f * far.s_off[i];
+    add_off(fs, fs_off, s);
+    add_off(fe, fe_off, e);
+    far.m[i] = m;
+    far.s[i] = fs;
+    far.s_off[i] = fs_off;
+    far.e[i] = fe;
+    far.e_off[i] = fe_off;
+}
+
 // A thread's sums.  The reference m is raised only where a logit exceeds it by 4
 // units of t, so that most steps raise nothing (score_rollouts 187.4 us, 192.1
 // where every larger logit raises it); t is rounded by up to 4 * 2^-24 then, in
@@ -182,7 +215,7 @@ template <int BYTES, bool ENT> struct Sums {
         top = -INFINITY;
         fast = false;
         low = 0;
-        s[0] = s[1] = e[0] = e[1] = 0;
+        forget();
     }
     __device__ __forceinline__ Soft settle(float c) const {
         float a, b, x, y;
@@ -212,6 +245,7 @@ template <int BYTES, bool ENT> struct Sums {
         e[0] = f2_pack(f * (v.e + d * v.s), 0.0f);
         s[1] = e[1] = 0;
     }
+    __device__ __forceinline__ void forget() { s[0] = s[1] = e[0] = e[1] = 0; }    // what has been added elsewhere
     // Before logits of which the largest is `most` are added.
     __device__ __forceinline__ void meet(float most, float c) {
         top = fmaxf(top, most);
@@ -467,7 +501,7 @@ __global__ void __launch_bounds__(kLpRowThreads, 8) token_logprobs_rows_kernel(c
     if (lane == 0) write_row<ENT>(a, row, target, target_logit, acc, m, log_s);
 }
 
-template <int BYTES, bool TOP, bool ENT, int NT>
+template <int BYTES, bool TOP, bool ENT, int NT, bool FAR>
 __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(const LpArgs a) {
     using L = Logit<BYTES>;
     constexpr int per = L::kPerVec;
@@ -520,6 +554,12 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
 
     Sums<BYTES, ENT> sums;
     sums.reset();
+    LpFar<NT>& far = *reinterpret_cast<LpFar<NT>*>(dyn + a.far);
+    if (FAR) {
+        far.m[tid] = kLowest;
+        far.s[tid] = far.s_off[tid] = far.e[tid] = far.e_off[tid] = 0.0f;
+    }
+    int near = 0;                                    // steps in the threads' own sums
     int places = 0, sharing = 0;                     // places of stored maxima begun, and steps in the last of them
     float held = -INFINITY;
     for (int64_t base = v0; base < v1; base += (int64_t)NT * kLpUnroll) {
@@ -530,6 +570,12 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
         const float most = largest<BYTES>(v);
         sums.meet(most, a.c);
         sums.add(v, a.c);
+        if (FAR && ++near == kLpFarSteps<BYTES>) {
+            const Soft now = sums.settle(a.c);
+            add_far<NT>(far, now.m, now.s, now.e, a.c);
+            sums.forget();
+            near = 0;
+        }
         if (TOP) {
             if (sharing == 0) held = -INFINITY, ++places;
             held = fmaxf(held, most);
@@ -543,6 +589,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
     }
 
     Soft acc = sums.settle(a.c);
+    if (FAR) {
+        add_far<NT>(far, acc.m, acc.s, acc.e, a.c);
+        acc.s = far.s[tid] + far.s_off[tid];
+        acc.e = far.e[tid] + far.e_off[tid];
+    }
     join_lanes<32>(acc, a.c);
     if (lane == 0) sh.warp[warp] = acc;
     if (TOP) {
@@ -862,6 +913,16 @@ fp8q_status_t check_logits(int64_t rows, int64_t vocab, int64_t stride, int logi
     return FP8Q_OK;
 }
 
+template <int BYTES, bool TOP, bool ENT, int NT, bool FAR>
+fp8q_status_t launch_logprobs_kernel(const LpArgs& a, unsigned rows, unsigned ranks, size_t smem, cudaStream_t stream) {
+    constexpr size_t kMax = TOP ? sizeof(LpTopShared<NT>) + (size_t)kLpPlaces * NT * 4 + (FAR ? sizeof(LpFar<NT>) : 0) : 0;
+    static KernelCache cache;
+    int resident = 0;
+    const fp8q_status_t st = prepare_kernel(cache, token_logprobs_kernel<BYTES, TOP, ENT, NT, FAR>, NT, smem, kMax, &resident);
+    if (st != FP8Q_OK) return st;
+    return launch_clusters(token_logprobs_kernel<BYTES, TOP, ENT, NT, FAR>, rows * ranks, ranks, NT, smem, stream, a);
+}
+
 template <int BYTES, bool TOP, bool ENT, int NT>
 fp8q_status_t launch_logprobs(LpArgs a, int64_t rows, cudaStream_t stream) {
     // blocks of a cluster share a row while there are few rows; clusters of four and eight do not fill every slot (72
@@ -871,18 +932,19 @@ fp8q_status_t launch_logprobs(LpArgs a, int64_t rows, cudaStream_t stream) {
     const int64_t slots = kLpBlocksPerSm * sm_count();
     const int64_t steps = (a.vocab * BYTES + NT * kLpUnroll * 16 - 1) / (NT * kLpUnroll * 16);
     while (ranks < kLpMaxCluster && rows * ranks * 2 <= (ranks > 1 ? slots - slots / 16 : slots) && (int64_t)ranks * 2 <= steps) ranks *= 2;
-    constexpr size_t kMax = TOP ? sizeof(LpTopShared<NT>) + (size_t)kLpPlaces * NT * 4 : 0;
+    const int64_t mine = steps / ranks + 1;          // of one block, at most
     size_t smem = 0;
     if (TOP) {
-        const int64_t mine = steps / ranks + 1;      // of one block, at most
         a.fold = (int)((mine + kLpPlaces - 1) / kLpPlaces);
         smem = sizeof(LpTopShared<NT>) + (size_t)((mine + a.fold - 1) / a.fold) * NT * 4;
     }
-    static KernelCache cache;
-    int resident = 0;
-    const fp8q_status_t st = prepare_kernel(cache, token_logprobs_kernel<BYTES, TOP, ENT, NT>, NT, smem, kMax, &resident);
-    if (st != FP8Q_OK) return st;
-    return launch_clusters(token_logprobs_kernel<BYTES, TOP, ENT, NT>, (unsigned)rows * ranks, ranks, NT, smem, stream, a);
+    if constexpr (NT == 256) {                       // rows of so many steps
+        if (mine > kLpFarSteps<BYTES>) {
+            a.far = (int)smem;
+            return launch_logprobs_kernel<BYTES, TOP, ENT, NT, true>(a, (unsigned)rows, ranks, smem + sizeof(LpFar<NT>), stream);
+        }
+    }
+    return launch_logprobs_kernel<BYTES, TOP, ENT, NT, false>(a, (unsigned)rows, ranks, smem, stream);
 }
 
 template <int BYTES, bool TOP, bool ENT>
@@ -947,7 +1009,7 @@ fp8q_status_t logprobs_entry(const void* logits, int logit_bytes, int64_t rows, 
     const Range ins[] = {{logits, span(rows, vocab, stride, logit_bytes)}, {targets, r * id_bytes}};
     if (any_alias(outs, 5, ins, 2)) return FP8Q_ERR_ALIAS;
     const LpArgs a = {logits, targets, id_bytes == 8, vocab, stride, temperature,
-                      (float)(1.44269504088896340736 / (double)temperature), top, 1, logprobs, entropy, top_logprobs, top_ids, stats};
+                      (float)(1.44269504088896340736 / (double)temperature), top, 1, 0, logprobs, entropy, top_logprobs, top_ids, stats};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return logit_bytes == 2 ? launch_logprobs_kind<2>(a, rows, s) : launch_logprobs_kind<4>(a, rows, s);
 }
