@@ -5,7 +5,7 @@
 // x in MXFP8 rows, the weights as mxfp8_quantize_swizzled writes them.  Two
 // launches: the gate and up products with the activation, and the down product
 // with the sum.  Between them h is held as two f16 terms with a scale for every
-// 32 of them, 22 bits of each value, which the tensor core multiplies exactly;
+// 32 of them, 22 bits of each value, whose products with e4m3 codes are exact;
 // 16 bits of it in one term would show in the output, binary32 cannot enter the
 // products.  The sum over the choices is rounded once.
 //
@@ -67,10 +67,11 @@ __device__ __forceinline__ uint32_t e4m3_f16(uint32_t two) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
     return r;
 }
-// Products of 16 rows of weights with 8 columns over a block of 32, exact.  The
-// order of K is free as long as A and B share it: lane 4 r + t holds bytes 8 t ..
-// 8 t + 7 of the block for rows r and r + 8 of A and column r of B, the latter
-// as f16.
+// Products of 16 rows of weights with 8 columns over a block of 32.  Each is exact;
+// an instruction adds its 16 and the sum so far, cut off 25 bits below the largest
+// of them and then to 24 bits, towards zero.  The order of K is free as long as A
+// and B share it: lane 4 r + t holds bytes 8 t .. 8 t + 7 of the block for rows r
+// and r + 8 of A and column r of B, the latter as f16.
 __device__ __forceinline__ void mma_block(float (&d)[4], uint2 a0, uint2 a1, uint4 b) {
     d[0] = d[1] = d[2] = d[3] = 0.0f;
     mma_f16(d, e4m3_f16(a0.x), e4m3_f16(a1.x), e4m3_f16(a0.x >> 16), e4m3_f16(a1.x >> 16), b.x, b.y);
