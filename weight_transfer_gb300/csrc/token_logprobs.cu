@@ -82,7 +82,6 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
 
 template <int BYTES> struct Logit;
 template <> struct Logit<2> {
-    using type = uint16_t;
     static constexpr int kPerVec = 8;
     static constexpr uint32_t kNothing = 0xFF80FF80u;       // two -inf
     static __device__ __forceinline__ float load(const void* p, int64_t i) {
@@ -97,7 +96,6 @@ template <> struct Logit<2> {
     }
 };
 template <> struct Logit<4> {
-    using type = float;
     static constexpr int kPerVec = 4;
     static constexpr uint32_t kNothing = 0xFF800000u;
     static __device__ __forceinline__ float load(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
