@@ -160,9 +160,10 @@ template <int LANES> __device__ __forceinline__ void join_lanes(Soft& a, float c
 // another; then what they hold is added, with what that addition rounds off, to
 // sums in shared memory, so that a row's error does not grow with its length:
 // equal terms that are rounded the same way every time were off by 1e-4 at 200
-// million logits, 5e-7 at 151,936, and are 9e-7 at any length now.  They have an
-// instance of the kernel of their own (FAR): rows of which a block's share is
-// shorter would take 0.7% longer, four rows 3%.
+// million logits, 5e-7 at 151,936, and are 9e-7 at any length now (one row of 16
+// million bf16 logits 87.5 us, without them 84.8).  They have an instance of the
+// kernel of their own (FAR): rows of which a block's share is shorter would take
+// 0.7% longer, four rows 3%.
 constexpr int kLpChain = 256;
 template <int BYTES> constexpr int kLpFarSteps = kLpChain * BYTES / 16;     // a step adds 8 bf16 or 4 binary32 terms to a chain
 template <int NT> struct LpFar {
@@ -557,10 +558,9 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
         far.m[tid] = kLowest;
         far.s[tid] = far.s_off[tid] = far.e[tid] = far.e_off[tid] = 0.0f;
     }
-    int near = 0;                                    // steps in the threads' own sums
     int places = 0, sharing = 0;                     // places of stored maxima begun, and steps in the last of them
     float held = -INFINITY;
-    for (int64_t base = v0; base < v1; base += (int64_t)NT * kLpUnroll) {
+    auto step = [&](int64_t base) {
         uint4 v[kLpUnroll];
 #pragma unroll
         for (int u = 0; u < kLpUnroll; ++u) v[u] = next[u];
@@ -568,18 +568,26 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 4 : 1) token_logprobs_kernel(c
         const float most = largest<BYTES>(v);
         sums.meet(most, a.c);
         sums.add(v, a.c);
-        if (FAR && ++near == kLpFarSteps<BYTES>) {
-            const Soft now = sums.settle(a.c);
-            add_far<NT>(far, now.m, now.s, now.e, a.c);
-            sums.forget();
-            near = 0;
-        }
         if (TOP) {
             if (sharing == 0) held = -INFINITY, ++places;
             held = fmaxf(held, most);
             t.most[(places - 1) * NT + tid] = held;
             if (++sharing == a.fold) sharing = 0;
         }
+    };
+    if constexpr (FAR) {
+        constexpr int64_t kTurn = (int64_t)NT * kLpUnroll * kLpFarSteps<BYTES>;
+        for (int64_t turn = v0;; turn += kTurn) {
+            const int64_t end = turn + kTurn < v1 ? turn + kTurn : v1;
+#pragma unroll 1
+            for (int64_t base = turn; base < end; base += (int64_t)NT * kLpUnroll) step(base);
+            if (end == v1) break;
+            const Soft now = sums.settle(a.c);
+            add_far<NT>(far, now.m, now.s, now.e, a.c);
+            sums.forget();
+        }
+    } else {
+        for (int64_t base = v0; base < v1; base += (int64_t)NT * kLpUnroll) step(base);
     }
     if (!(extra == -INFINITY)) {
         sums.meet(extra, a.c);
