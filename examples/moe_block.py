@@ -2,8 +2,8 @@
 
 Serving (``MoeBlock.forward``): the residual stream is normalized and quantized in one pass, the router picks experts
 from the bf16 rows, the MXFP8 rows travel to their experts, the gate/up and down products read the weights exactly as
-mxfp8_quantize_swizzled wrote them (what a refit ships), and the experts' rows are summed back with the router's weights.  A few tokens (``MoeBlock.decode``) go through their experts in one call, without
-sorting or carrying rows.
+mxfp8_quantize_swizzled wrote them (what a refit ships), and the experts' rows are summed back with the router's weights.
+A few tokens (``MoeBlock.decode``) go through their experts in one call, without sorting or carrying rows.
 
 Training (``norm``, ``gather`` and ``combine`` below): the same norm and routing with gradients, around whatever the
 experts compute in bf16.

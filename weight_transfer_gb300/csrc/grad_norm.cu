@@ -14,14 +14,15 @@
 // a cycle and SM).  A warp's sum outside [2^-80, 2^100] would lose squares to the
 // range of binary32; its elements are squared again under a power of two.
 //
-// Both passes are bound by HBM.  A layer of 623 million bf16 gradients takes 182
-// us for its norm (6.85 TB/s; blocks of 256 threads that each read one chunk into
-// registers took 294 to 317).  Eight buckets of 13.1 million, averaged and
-// clipped into others, 97 us: the second reading finds some 40 MB in the
-// second-level cache.  A thousand ragged views into 32-bit buffers, 98 us, as
-// the copies into shared memory leave the output its own alignment (element by
-// element 188).  Fourteen small tensors: 4.8 us in two launches (5.2 where the
-// first chunk is looked up behind the dependency wait).
+// Both passes are bound by HBM.  A layer of 623 million bf16 gradients takes 179 to
+// 182 us for its norm (6.85 TB/s; blocks of 256 threads that each read one chunk
+// into registers took 294 to 317).  Eight buckets of 13.1 million, averaged and
+// clipped into others, 100 us in calls on other buffers than the last one's, 95.6
+// from a graph on the same ones: the second reading finds some 40 MB in the
+// second-level cache.  A thousand ragged views into 32-bit buffers, 99.6 and 97 us,
+// as the copies into shared memory leave the output its own alignment (element by
+// element 188).  Fourteen small tensors: 4.8 us in two launches of a graph (5.2
+// where the first chunk was looked up behind the dependency wait).
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 

@@ -19,17 +19,18 @@
 // The warps' own instructions are the second bound, 218 (gate and up) and 280
 // (down) for a unit of 2 KB of weights, issued in 0.56 and 0.60 of all cycles at
 // 32 tokens.
-//     one token 13.9 us, eight (15% of the choices dropped) 42.5 us, 5.9 TB/s,
-//     32 tokens 96 us, 5.7 TB/s; through sort, gather, swiglu, matmul and
-//     combine 22, 57.5 (none dropped) and 100.7 us
+//     one, two, four, eight, sixteen and 32 tokens 13.8, 18.6, 32.0, 47.2, 69.4
+//     and 96.0 us (5.7 TB/s) from a graph; through sort, gather, swiglu, matmul
+//     and combine 22.0, 26.8, 40.1, 56.3, 79.3 and 99.9
 // Columns without rows hold further blocks of K, so that a lane scales and adds
-// one sum for four: 14.6, 44.5 and 104 us without.
-// What did not gain: x or h fetched a unit ahead (the same), x held in shared
-// memory (the same), partial sums without a barrier (the same), whole K to a warp
-// (117 where 104), a lane's units in registers instead of rings (261).  Of the
-// down products: tiles of 32 features, which halve the reading of h (97.8 where
-// 99.1, but 72.5 where 71.6 for sixteen tokens); units cut evenly over all SMs
-// with sums joined in memory (104.4, one token 22.1).
+// one sum for four: without, one token took 1.06 times and 32 tokens 1.03 times as
+// long as with.
+// What did not gain, each against the kernel of its time: x or h fetched a unit
+// ahead (the same), x held in shared memory (the same), partial sums without a
+// barrier (the same), whole K to a warp (1.12 times as long), a lane's units in
+// registers instead of rings (2.5 times).  Of the down products: tiles of 32
+// features, which halve the reading of h (0.99, but 1.01 for sixteen tokens);
+// units cut evenly over all SMs with sums joined in memory (1.05, one token 1.6).
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 
@@ -589,8 +590,9 @@ size_t workspace_of(int64_t tokens, int topk, int64_t n) {
 }
 
 // Sixteen warps a block for one or two tokens, whose units last each of them a
-// few steps (one token 13.9 us, with twenty 14.8), twenty-four beyond (32 tokens
-// 97.7 us, with twenty 98.9, sixteen 102.3; four tokens 32.5, 32.1 and 32.2).
+// few steps (one token 13.8 us, with twenty 14.9, with twenty-four 14.8; two 18.6,
+// 19.2 and 19.4), twenty-four beyond (32 tokens 96.0 us, with twenty 97.1, with
+// sixteen 101.1; eight 47.2, 47.3 and 48.1; four 32.0, 31.6 and 31.6).
 constexpr int64_t kDownFewTokens = 2;
 template <int NT> fp8q_status_t launch_down(const MdArgs& a, unsigned ranks, size_t lists, cudaStream_t stream) {
     const auto bytes = [&](int tokens, size_t l) { return down_ring(NT) + (size_t)NT / 32 * 17 * tokens * sizeof(float) + l; };
@@ -604,7 +606,9 @@ template <int NT> fp8q_status_t launch_down(const MdArgs& a, unsigned ranks, siz
 
 // Two blocks per SM with 116 registers a thread, or three with 80 where that takes
 // all items at once and two would not (16 experts of 768 features: two tokens
-// 18.7 us, with two blocks 21.2; 8 experts 15.2 and 13.8, 81 experts 71.5 and 69.5).
+// 18.5 us, with two blocks 21.1; 8 experts 15.2 and 13.8, 81 experts 56.3 and 55.5,
+// sixteen and 32 tokens the same; but four and eight tokens 31.1 and 46.0 with
+// three, 32.0 and 47.2 with two).
 template <int BLOCKS> fp8q_status_t launch_up(const MdArgs& a, size_t items, size_t smem, size_t most, cudaStream_t stream) {
     static KernelCache cache;
     int resident = 0;

@@ -14,13 +14,15 @@
 // Gradient, from the statistics that the forward pass wrote:
 //     dx_j = ([j = t] g - p_j (g + dH (log p_j + entropy))) / T
 //
-// All of it is bound by HBM.  4096 rows of 151,936 bf16 logits: 184.7 us forward
-// with entropy (6.74 TB/s; scalar arithmetic on unpacked logits, 12 instructions
-// each instead of 5, took 261), 370 us for the gradient (6.72 TB/s; 400 with a
-// comparison with the target at every logit).  256 rows of 151,669 binary32
-// logits with five alternatives: 36.7 us, without them 27.  Four rows: 6.5 us, of
-// which the launch and the joins are most (8.8 where a warp's lanes join their
-// sums pair by pair and the joins wait for the sorting).
+// All of it is bound by HBM.  4096 rows of 151,936 bf16 logits: 180 to 185 us
+// forward with entropy (6.74 to 6.93 TB/s, from one GPU to another; scalar
+// arithmetic on unpacked logits, 12 instructions each instead of 5, took 261), 385
+// to 389 for the gradient in calls on other buffers than the last one's (6.4 TB/s)
+// and 360 to 380 from a graph on the same ones (a comparison with the target at
+// every logit cost 30 us more).  256 rows of 151,669 binary32 logits with five
+// alternatives: 36 to 37 us, without them 26.  Four rows: 6.5 us from a graph, of
+// which the launch and the joins are most (an earlier state, whose lanes joined
+// their sums pair by pair and whose joins waited for the sorting, took 8.8).
 #include "fp8q_device.cuh"
 #include "fp8q_host.cuh"
 
@@ -31,10 +33,12 @@ namespace fp8q {
 constexpr int kLpMaxTop = FP8Q_MAX_TOP;
 constexpr int kLpCap = 128;             // candidates that a warp holds in shared memory
 constexpr int kLpMaxCluster = 8;
-constexpr int kLpBlocksPerSm = 4;           // up to which rows are divided: 256 rows 36.7 us, with 2 38.2, with 8 41.8
-// Places of stored maxima a thread.  1024 rows of 151,669 binary32 logits with
-// five alternatives 112 us, 8 places 116; 48 139, as what a block then holds of
-// the shared memory leaves little first-level cache for loads on their way.
+// Blocks per SM up to which rows are divided: 256 rows of 151,669 normal binary32
+// logits with five alternatives 30.6 us, with 2 36.1, with 8 35.5.
+constexpr int kLpBlocksPerSm = 4;
+// Places of stored maxima a thread.  1024 such rows 106 us, 8 places 109; 48 137,
+// as what a block then holds of the shared memory leaves little first-level cache
+// for loads on their way.
 constexpr int kLpPlaces = 24;
 constexpr int kLpUnroll = 4;            // 16-byte vectors per thread and step
 constexpr float kLog2e = 1.44269504088896341f;
@@ -190,8 +194,8 @@ template <int NT> __device__ __noinline__ void add_far(LpFar<NT>& far, float m, 
 }
 
 // A thread's sums.  The reference m is raised only where a logit exceeds it by 4
-// units of t, so that most steps raise nothing (score_rollouts 187.4 us, 192.1
-// where every larger logit raises it); t is rounded by up to 4 * 2^-24 then, in
+// units of t, so that most steps raise nothing (score_rollouts 179.9 us, 183.0
+// where every larger logit raises it; 256 rows with alternatives 30.6 and 34.2); t is rounded by up to 4 * 2^-24 then, in
 // the terms that count, which a slack of 40 would make 40 * 2^-24.
 // t is taken as x * c - mc with mc = RN(m * c), one instruction for two logits;
 // settle() and take() go between that reference and m itself.  Logits below
@@ -442,9 +446,11 @@ __device__ __forceinline__ void write_row(const LpArgs& a, int64_t row, int64_t 
 }
 
 // Many short rows: one for each warp, without a barrier.  From eight rows per SM
-// on, of up to 48 KB (9728 rows of 1 KB bf16 logits 7.2 us, of 16 KB 27.0, of 48
-// KB 71.3; with a block to each 32.6, 49.5 and 86.8.  1216 rows of 48 KB 10.8 and
-// 11.5, of 64 KB 18.0 and 14.1; 608 rows of 48 KB 8.6 and 6.6).
+// on, of up to 48 KB (9728 rows of 1 KB bf16 logits 6.5 us, of 16 KB 25.9, of 48
+// KB 69.1; with a block to each 29.8, 44.9 and 84.3.  1216 rows of 48 KB 10.0 and
+// 10.7, 608 rows of 48 KB 7.9 and 6.0.  Of 64 KB 1216 rows take as long either way
+// and 9728 97.5 and 104, but a lane's chains are then as long as the error's bound
+// allows).
 constexpr int kLpRowThreads = 128;
 constexpr int64_t kLpRowBytes = 49152;
 constexpr int kLpRowsPerSm = 8;
@@ -775,8 +781,8 @@ struct LpGradArgs {
 };
 
 // Blocks of 128 threads with four vectors each: a narrower window of memory on
-// its way than with 256 threads (score_grad_long 387.7 us where 392.5, 512
-// threads 443; two vectors 452, eight 395).
+// its way than with 256 threads (score_grad_long in a row 385.8 us where 393.8, 512
+// threads 451; two vectors 463, eight 385).
 constexpr int kLpGradThreads = 128;
 constexpr int kLpGradUnroll = 4;
 // Many short rows go to a warp each: of up to 4 KB from eight rows per SM on (1216
@@ -932,8 +938,8 @@ fp8q_status_t launch_logprobs_kernel(const LpArgs& a, unsigned rows, unsigned ra
 template <int BYTES, bool TOP, bool ENT, int NT>
 fp8q_status_t launch_logprobs(LpArgs a, int64_t rows, cudaStream_t stream) {
     // blocks of a cluster share a row while there are few rows; clusters of four and eight do not fill every slot (72
-    // rows of 151,669 binary32 logits with five alternatives in clusters of eight 19.1 us, of four 15.2; 152 in clusters
-    // of four 31.4, of two 24.3)
+    // rows of 151,669 binary32 logits with five alternatives in clusters of eight took 1.25 times as long as of four, 152
+    // in clusters of four 1.29 times as long as of two; 10.9 and 19.1 us now)
     unsigned ranks = 1;
     const int64_t slots = kLpBlocksPerSm * sm_count();
     const int64_t steps = (a.vocab * BYTES + NT * kLpUnroll * 16 - 1) / (NT * kLpUnroll * 16);
